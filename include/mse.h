@@ -495,6 +495,109 @@ MSE_API mse_status mse_selftest_wait_timeout(uint64_t limit_ns, void *stream);
  * not overlap them. Process-wide; not meant for concurrent callers. */
 MSE_API void mse_set_phase_events(void *ev_begin, void *ev_mid, void *ev_end);
 
+/* ---------------------------------------------------------------------------
+ * The routed experts beside the shared expert: routing, products in 8 bits with a
+ * scale for each block of 128, and the experts' layer.  Inference only, like the
+ * rest of the library.
+ * ------------------------------------------------------------------------- */
+
+typedef enum { MSE_SCORE_SOFTMAX = 0, MSE_SCORE_SIGMOID = 1 } mse_score;
+
+/* Limits of moe_route: experts, groups, chosen experts per token. */
+#define MSE_ROUTE_MAX_EXPERTS 1024
+#define MSE_ROUTE_MAX_GROUPS 32
+#define MSE_ROUTE_MAX_TOP_K 32
+
+/* Routing of T tokens to E experts.
+ *
+ *   logits   [T x E]      bf16 or fp32 (logits_dtype), row pitch ld >= E elements
+ *   bias     [E]          fp32 for the choice alone, or null
+ *   ids      [T x top_k]  int32: the chosen experts, best first; -1 where no expert is left
+ *   weights  [T x top_k]  fp32, 0 where ids is -1; capacity >= T*top_k elements of each
+ *
+ * An expert is open to a token when its logit is above the lowest finite bf16 value; -inf,
+ * either type's lowest value and NaN close it.  In fp32:
+ *   score  = 1 / (1 + e^-l), or e^(l - max) / sum over the open experts (softmax; the sum
+ *            as if rounded once, so that no choice depends on an order of summation);
+ *   choice = score + bias;
+ *   groups: experts [g E / n_group, (g + 1) E / n_group); a group's value is the sum of its
+ *            group_top (1 or 2) best open choices (of fewer where fewer are open), and only
+ *            the topk_group best groups stay open;
+ *   ids    = the top_k best open choices; equal ones go to the lower index, groups too;
+ *   weight = score of the chosen (without the bias), divided by their sum if renormalise
+ *            (by nothing where that sum is 0), times scale.
+ * A token with no open expert gets ids -1 and weights 0.
+ * MSE_ERR_INVALID_ARG: null pointer, non-positive size, bad enum, ld < E, E, n_group or top_k
+ * beyond the limits, topk_group outside [1, n_group], top_k above the topk_group * E / n_group
+ * experts that stay, group_top not 1 or 2; MSE_ERR_NOT_DIVISIBLE: E by n_group;
+ * MSE_ERR_GEOMETRY: capacity. */
+MSE_API mse_status moe_route(const void *logits, mse_dtype logits_dtype, int64_t T, int64_t E, int64_t ld,
+                             const float *bias, mse_score scoring, int n_group, int topk_group, int group_top,
+                             int top_k, int renormalise, float scale, int32_t *ids, float *weights,
+                             int64_t capacity, void *stream);
+
+/* Rounding to 8 bits (e4m3: 4 exponent bits, 3 fraction bits, largest 448) with one scale for
+ * each block of block_rows x 128 (block_rows 1: activations; 128: weights):
+ *   a = max(max |B|, 2^-100),   scale = a / 448,   q = e4m3(448 B / a) to nearest, ties to even.
+ * A block that holds an infinity or a NaN stands for NaN throughout.
+ *   x       [rows x K]  bf16, row pitch ldx >= K
+ *   q       [rows x K]  row pitch ldq >= K bytes, q_capacity >= (rows - 1) * ldq + K
+ *   scales  [ceil(rows / block_rows) x ceil(K / 128)] fp32, scales_capacity elements */
+MSE_API mse_status fp8_block_quantise(const mse_bf16 *x, int64_t rows, int64_t K, int64_t ldx, int block_rows,
+                                      uint8_t *q, int64_t ldq, int64_t q_capacity, float *scales,
+                                      int64_t scales_capacity, void *stream);
+
+/* out [T x N] = sum over k-blocks b of xs[t, b] ws[n / 128, b] sum_{k in b} xq[t, k] wq[n, k].
+ *   xq [T x K] e4m3, row pitch ldx >= K bytes;  xs [T x ceil(K / 128)] fp32
+ *   wq [N x K] e4m3, row pitch ldw >= K bytes;  ws [ceil(N / 128) x ceil(K / 128)] fp32
+ *   out bf16 or fp32 (out_dtype), out_capacity >= T*N elements
+ * Each block's products are summed on the tensor cores and added, scaled, to an fp32 sum; out is
+ * rounded once.  The tensor-core kernels take row pitches that are multiples of 16 with 16-byte
+ * aligned operands; anything else takes the generic kernels. */
+MSE_API mse_status fp8_block_matmul(const uint8_t *xq, int64_t ldx, const float *xs, const uint8_t *wq, int64_t ldw,
+                                    const float *ws, int64_t T, int64_t N, int64_t K, void *out,
+                                    mse_dtype out_dtype, int64_t out_capacity, void *stream);
+
+/* Workspace of fp8_block_linear for every token count up to T (0 on invalid arguments):
+ * 256-byte aligned, need not be zeroed, holds x in 8 bits. */
+MSE_API size_t fp8_block_linear_workspace_bytes(int64_t T, int64_t N, int64_t K);
+
+/* fp8_block_quantise of x [T x K] bf16 (row pitch ldx) in blocks of 1 x 128, then
+ * fp8_block_matmul, in one call. */
+MSE_API mse_status fp8_block_linear(const mse_bf16 *x, int64_t ldx, const uint8_t *wq, int64_t ldw, const float *ws,
+                                    int64_t T, int64_t N, int64_t K, void *y, mse_dtype y_dtype, int64_t y_capacity,
+                                    void *workspace, size_t workspace_bytes, void *stream);
+
+/* Workspace of moe_experts_forward for every token count up to T with the same or smaller other
+ * sizes (0 on invalid arguments): 256-byte aligned, need not be zeroed. */
+MSE_API size_t moe_experts_workspace_bytes(int64_t T, int top_k, int64_t E, int64_t H, int64_t I);
+
+/* The routed experts of a rank that holds experts [first_expert, first_expert + E):
+ *
+ *   y[t] = shared[t] + sum_j weights[t, j] * W_down,e h,   e = ids[t, j] - first_expert,
+ *   [g; u] = W_gate_up,e x[t],   h = silu(g) * u,
+ *
+ * over the j whose e lies in [0, E) (others, -1 among them, belong to other ranks or to nobody).
+ * x and h are rounded to e4m3 in blocks of 1 x 128; products as in fp8_block_matmul; the sum over
+ * j runs in fp32, ascending, on top of shared, and is rounded once.
+ *
+ *   x         [T x H]         bf16
+ *   ids       [T x top_k]     int32;   weights [T x top_k] fp32
+ *   w_gate_up [E x 2I x H]    e4m3, row pitch ld_gate_up >= H; rows [0, I) gate, [I, 2I) up
+ *   s_gate_up [E x 2 ceil(I / 128) x ceil(H / 128)] fp32; gate's blocks, then up's, each half's
+ *                             blocks counted from its own first row
+ *   w_down    [E x H x I]     e4m3, row pitch ld_down >= I
+ *   s_down    [E x ceil(H / 128) x ceil(I / 128)] fp32
+ *   shared    [T x H]         bf16, or null for 0
+ *   y         [T x H]         bf16, y_capacity >= T*H elements (x or shared itself is allowed)
+ * top_k <= MSE_ROUTE_MAX_TOP_K, E <= MSE_ROUTE_MAX_EXPERTS; T * top_k <= 2^30. */
+MSE_API mse_status moe_experts_forward(const mse_bf16 *x, int64_t T, int64_t H, const int32_t *ids,
+                                       const float *weights, int top_k, const uint8_t *w_gate_up, int64_t ld_gate_up,
+                                       const float *s_gate_up, const uint8_t *w_down, int64_t ld_down,
+                                       const float *s_down, int64_t E, int64_t I, int64_t first_expert,
+                                       const mse_bf16 *shared, mse_bf16 *y, int64_t y_capacity, void *workspace,
+                                       size_t workspace_bytes, void *stream);
+
 /* Human-readable name of a status code (static string). */
 MSE_API const char *mse_status_string(mse_status s);
 

@@ -10,6 +10,8 @@ Functions carry the C-ABI names:
     merged_proj_forward, merged_proj_reorder, shard_sequence_parallel_mlp
 plus the workspace queries, the device-error poll and the settings, and
 ``sequence_parallel_mlp``, which takes the sharding decision and makes the matching call.
+The routed experts beside the shared expert are in ``routed.py`` (exported here too):
+    moe_route, fp8_block_quantise, fp8_block_matmul, fp8_block_linear, moe_experts_forward
 """
 from __future__ import annotations
 
@@ -26,6 +28,8 @@ __all__ = [
     "poll_device_error", "set_wait_limit_ns", "get_wait_limit_ns", "set_kernel_path", "selftest_wait_timeout",
     "set_phase_events", "set_prefill_kernel", "set_tuning", "BF16", "F32", "PATH_AUTO", "PATH_GENERIC", "PATH_TENSORCORE",
     "PREFILL_AUTO", "PREFILL_SINGLE", "PREFILL_PAIR", "STATUS",
+    "moe_route", "fp8_block_quantise", "fp8_block_matmul", "fp8_block_linear", "moe_experts_forward",
+    "fp8_linear_workspace_bytes", "new_fp8_linear_workspace", "moe_workspace_bytes", "new_moe_workspace",
 ]
 
 BF16, F32 = 0, 1
@@ -92,6 +96,14 @@ def lib() -> ctypes.CDLL:
                 "mse_merged_launch_plan": (ci, [i64, i64, i64, i64, ci, ci, P]),
                 "mse_selftest_wait_timeout": (ci, [u64, P]),
                 "mse_set_phase_events": (None, [P, P, P]),
+                "moe_route": (ci, [P, ci, i64, i64, i64, P, ci, ci, ci, ci, ci, ci, ctypes.c_float, P, P, i64, P]),
+                "fp8_block_quantise": (ci, [P, i64, i64, i64, ci, P, i64, i64, P, i64, P]),
+                "fp8_block_matmul": (ci, [P, i64, P, P, i64, P, i64, i64, i64, P, ci, i64, P]),
+                "fp8_block_linear_workspace_bytes": (sz, [i64, i64, i64]),
+                "fp8_block_linear": (ci, [P, i64, P, i64, P, i64, i64, i64, P, ci, i64, P, sz, P]),
+                "moe_experts_workspace_bytes": (sz, [i64, ci, i64, i64, i64]),
+                "moe_experts_forward": (ci, [P, i64, i64, P, P, ci, P, i64, P, P, i64, P, i64, i64, i64, P, P, i64,
+                                             P, sz, P]),
                 "mse_status_string": (ctypes.c_char_p, [ci]),
                 "mse_version": (ctypes.c_char_p, []),
             }
@@ -413,3 +425,8 @@ def selftest_wait_timeout(limit_ns: int, stream=None) -> None:
 def set_phase_events(ev_begin=None, ev_mid=None, ev_end=None) -> None:
     h = lambda e: None if e is None else e.cuda_event
     lib().mse_set_phase_events(h(ev_begin), h(ev_mid), h(ev_end))
+
+
+from .routed import (  # noqa: E402  (needs the names above)
+    fp8_block_linear, fp8_block_matmul, fp8_block_quantise, fp8_linear_workspace_bytes, moe_experts_forward,
+    moe_route, moe_workspace_bytes, new_fp8_linear_workspace, new_moe_workspace)

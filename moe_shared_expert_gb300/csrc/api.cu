@@ -6,6 +6,7 @@
 #include <unordered_map>
 
 #include "common.cuh"
+#include "device.h"
 #include "kernels.h"
 #include "tc.h"
 
@@ -206,6 +207,7 @@ struct MapKey {
     uint64_t strides[4];
     uint32_t box[5];
     int rank;
+    int type;
     bool operator==(const MapKey &o) const { return std::memcmp(this, &o, sizeof(MapKey)) == 0; }
 };
 struct MapKeyHash {
@@ -220,13 +222,14 @@ std::mutex g_map_mu;
 std::unordered_map<MapKey, CUtensorMap, MapKeyHash> g_map_cache;
 constexpr size_t kMapCacheMax = 4096;
 
-// bf16 tensor map with 128-byte swizzle; dims/strides innermost first, strides in bytes.
+// tensor map with 128-byte swizzle (bf16 unless told); dims/strides innermost first, strides in bytes.
 mse_status make_map(CUtensorMap *m, const void *base, int rank, const uint64_t *dims, const uint64_t *strides,
-                    const uint32_t *box) {
+                    const uint32_t *box, CUtensorMapDataType type = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16) {
     MapKey key;
     std::memset(&key, 0, sizeof key);
     key.base = reinterpret_cast<uint64_t>(base);
     key.rank = rank;
+    key.type = (int)type;
     for (int i = 0; i < rank; ++i) { key.dims[i] = dims[i]; key.box[i] = box[i]; }
     for (int i = 0; i < rank - 1; ++i) key.strides[i] = strides[i];
     {
@@ -245,7 +248,7 @@ mse_status make_map(CUtensorMap *m, const void *base, int rank, const uint64_t *
         e[i] = 1;
     }
     for (int i = 0; i < rank - 1; ++i) s[i] = strides[i];
-    CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank, const_cast<void *>(base), d, s, b, e,
+    CUresult r = fn(m, type, (cuuint32_t)rank, const_cast<void *>(base), d, s, b, e,
                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) return MSE_ERR_CUDA;
@@ -868,6 +871,31 @@ void record(std::atomic<void *> &ev, cudaStream_t s) {
 
 uint64_t wait_limit_ns() { return g_wait_limit_ns.load(); }
 
+bool pdl_enabled() { return use_pdl(); }
+
+mse_status device_view(DeviceView *out) {
+    DeviceInfo *d = nullptr;
+    const mse_status st = current_device(&d);
+    if (st != MSE_OK) return st;
+    out->sm_count = d->sm_count;
+    out->err = d->err;
+    return MSE_OK;
+}
+
+mse_status choose_tensorcore(bool tc_ok, bool *tensorcore) {
+    Path path = PATH_GENERIC;
+    const mse_status st = choose(tc_ok, &path);
+    *tensorcore = path == PATH_TC;
+    return st;
+}
+
+mse_status map_bytes(CUtensorMap *m, const void *base, int64_t rows, int64_t cols, int64_t ld, int box_rows) {
+    const uint64_t dims[2] = {(uint64_t)cols, (uint64_t)rows};
+    const uint64_t strides[1] = {(uint64_t)ld};
+    const uint32_t box[2] = {128u, (uint32_t)box_rows};
+    return make_map(m, base, 2, dims, strides, box, CU_TENSOR_MAP_DATA_TYPE_UINT8);
+}
+
 // Byte range of the sync words (tile counters, h flags, exit counts) inside an mlp
 // workspace of workspace_bytes (they must be zero before a call).
 void mlp_workspace_counter_range(int64_t T, int64_t H, int64_t I, size_t workspace_bytes, size_t *off,
@@ -969,6 +997,8 @@ void record_host_output(void *stream, uintptr_t lo, uintptr_t hi) {
     g_hostout[g_hostout_n++] = {stream, lo, hi};
 }
 }  // namespace
+
+void begin_untracked_call(void *stream) { forget_writes(stream); }
 }  // namespace mse
 
 // Workspace of mlp_swiglu_forward_host: the copy-count words of the two x buffers (fixed

@@ -1,0 +1,406 @@
+// Rounding to 8 bits, the dispatch of routed tokens, their weighted sum, and the generic
+// (CUDA-core) products that serve any size, pitch and alignment.
+#include "fp8.cuh"
+#include "launch.h"
+#include "routed.h"
+
+namespace mse {
+namespace routed {
+namespace {
+
+// ---------------------------------------------------------------------------
+// rounding to 8 bits
+// ---------------------------------------------------------------------------
+
+// One block of 128 values of a row, by 16 lanes with 8 values each.  Lane `l` of the 16 gets
+// values 8 l .. 8 l + 7 of block b (0 beyond K).
+__device__ __forceinline__ void load_block8(const uint16_t *row, int64_t K, int64_t b, int l, bool wide, float (&v)[8]) {
+    const int64_t k = b * kBlock + l * 8;
+    if (wide && k + 8 <= K) {
+        const uint4 w = *reinterpret_cast<const uint4 *>(row + k);
+        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[2 * i] = __uint_as_float(u[i] << 16);
+            v[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = k + i < K ? bf16_bits_to_f32(row[k + i]) : 0.f;
+    }
+}
+
+// amax over the 16 lanes, then the 8 rounded values of this lane
+__device__ __forceinline__ void round_block8(const float (&v)[8], uint32_t mask, float &a, uint8_t (&q)[8]) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = max(m, abs_bits(v[i]));
+#pragma unroll
+    for (int d = 8; d > 0; d >>= 1) m = max(m, __shfl_xor_sync(mask, m, d));
+    a = floored_amax(m);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) q[i] = e4m3_ratio(v[i], a);
+}
+
+__device__ __forceinline__ void store8(uint8_t *dst, int64_t left, bool wide, const uint8_t (&q)[8]) {
+    if (wide && left >= 8) {
+        uint2 w;
+        w.x = q[0] | (q[1] << 8) | (q[2] << 16) | ((uint32_t)q[3] << 24);
+        w.y = q[4] | (q[5] << 8) | (q[6] << 16) | ((uint32_t)q[7] << 24);
+        *reinterpret_cast<uint2 *>(dst) = w;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < left) dst[i] = q[i];
+    }
+}
+
+__global__ void __launch_bounds__(256) quantise_rows_kernel(const uint16_t *x, int64_t rows, int64_t K, int64_t ldx,
+                                                            int wide_in, uint8_t *q, int64_t ldq, int wide_out,
+                                                            float *scales) {
+    pdl_wait();
+    // (after the wait: what the next kernel reads early is complete before this kernel began)
+    pdl_launch_dependents();
+    const int64_t kb = (K + kBlock - 1) / kBlock, items = rows * kb;
+    const int l = threadIdx.x % 16;
+    const uint32_t mask = 0xFFFFu << (threadIdx.x & 16);
+    for (int64_t it = (int64_t)blockIdx.x * 16 + threadIdx.x / 16; it < items; it += (int64_t)gridDim.x * 16) {
+        const int64_t r = it / kb, b = it % kb;
+        float v[8], a;
+        uint8_t o[8];
+        load_block8(x + r * ldx, K, b, l, wide_in, v);
+        round_block8(v, mask, a, o);
+        const int64_t k = b * kBlock + l * 8;
+        store8(q + r * ldq + k, K - k, wide_out, o);
+        if (l == 0) scales[it] = block_scale(a);
+    }
+}
+
+// One 128 x 128 block per CTA.
+__global__ void __launch_bounds__(256) quantise_tiles_kernel(const uint16_t *x, int64_t rows, int64_t K, int64_t ldx,
+                                                             uint8_t *q, int64_t ldq, float *scales) {
+    __shared__ uint32_t part[8];
+    pdl_wait();
+    const int64_t r0 = (int64_t)blockIdx.y * kBlock, k0 = (int64_t)blockIdx.x * kBlock;
+    uint32_t m = 0;
+    for (int i = threadIdx.x; i < kBlock * kBlock; i += 256) {
+        const int64_t r = r0 + i / kBlock, k = k0 + i % kBlock;
+        if (r < rows && k < K) m = max(m, abs_bits(bf16_bits_to_f32(x[r * ldx + k])));
+    }
+    m = __reduce_max_sync(~0u, m);
+    if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = m;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < 8; ++w) m = max(m, part[w]);
+    const float a = floored_amax(m);
+    for (int i = threadIdx.x; i < kBlock * kBlock; i += 256) {
+        const int64_t r = r0 + i / kBlock, k = k0 + i % kBlock;
+        if (r < rows && k < K) q[r * ldq + k] = e4m3_ratio(bf16_bits_to_f32(x[r * ldx + k]), a);
+    }
+    if (threadIdx.x == 0) scales[blockIdx.y * (int64_t)gridDim.x + blockIdx.x] = block_scale(a);
+}
+
+// fp32 rows of the tiles of a dispatch, one warp per block of 128
+__global__ void __launch_bounds__(256) quantise_f32_kernel(const float *h, const int *n_tiles, const Tile *tiles,
+                                                           int64_t K, uint8_t *q, int64_t ldq, float *scales) {
+    pdl_wait();
+    if ((int)blockIdx.x >= *n_tiles) return;
+    const Tile t = tiles[blockIdx.x];
+    const int64_t kb = (K + kBlock - 1) / kBlock, items = t.rows * kb;
+    const int lane = threadIdx.x % 32;
+    for (int64_t it = (int64_t)blockIdx.y * 8 + threadIdx.x / 32; it < items; it += (int64_t)gridDim.y * 8) {
+        const int64_t r = t.row0 + it / kb, b = it % kb;
+        float v[4];
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int64_t k = b * kBlock + i * 32 + lane;
+            v[i] = k < K ? h[r * K + k] : 0.f;
+            m = max(m, abs_bits(v[i]));
+        }
+        const float a = floored_amax(__reduce_max_sync(~0u, m));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int64_t k = b * kBlock + i * 32 + lane;
+            if (k < K) q[r * ldq + k] = e4m3_ratio(v[i], a);
+        }
+        if (lane == 0) scales[r * kb + b] = block_scale(a);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// dispatch: pairs sorted by expert, their tokens in 8 bits at the sorted rows
+// ---------------------------------------------------------------------------
+
+// expert of pair i on this rank, or -1
+__device__ __forceinline__ int local_expert(const DispatchParams &p, int64_t i) {
+    const int64_t e = (int64_t)p.ids[i] - p.first_expert;
+    return e >= 0 && e < p.E ? (int)e : -1;
+}
+
+__global__ void __launch_bounds__(kDispatchThreads) count_kernel(const DispatchParams p) {
+    extern __shared__ int count_smem[];
+    pdl_wait();
+    pdl_launch_dependents();
+    for (int e = threadIdx.x; e < p.E; e += kDispatchThreads) count_smem[e] = 0;
+    __syncthreads();
+    const int64_t i0 = (int64_t)blockIdx.x * p.chunk * p.top_k;
+    const int64_t i1 = min(i0 + (int64_t)p.chunk * p.top_k, p.T * p.top_k);
+    for (int64_t i = i0 + threadIdx.x; i < i1; i += kDispatchThreads) {
+        const int e = local_expert(p, i);
+        if (e >= 0) atomicAdd(&count_smem[e], 1);
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < p.E; e += kDispatchThreads) p.hist[(int64_t)blockIdx.x * p.E + e] = count_smem[e];
+}
+
+// exclusive prefix sum of v[0 .. n) in shared memory by one warp; the total is returned
+__device__ __forceinline__ int warp_prefix(int *v, int n, int lane) {
+    int run = 0;
+    for (int c = 0; c < n; c += 32) {
+        const int mine = c + lane < n ? v[c + lane] : 0;
+        int s = mine;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int o = __shfl_up_sync(~0u, s, d);
+            if (lane >= d) s += o;
+        }
+        if (c + lane < n) v[c + lane] = run + s - mine;
+        run += __shfl_sync(~0u, s, 31);
+    }
+    return run;
+}
+
+// CTA (c, y): the sorted rows of token chunk c, and its k-blocks [y * per, (y + 1) * per) in 8 bits
+// at those rows.  A pair's row is its expert's first row plus the pairs of that expert before it,
+// counted, not drawn by atomics, so every CTA of a chunk finds the same rows.
+__global__ void __launch_bounds__(kDispatchThreads) dispatch_kernel(const DispatchParams p) {
+    extern __shared__ int dispatch_smem[];
+    int *total = dispatch_smem, *before = total + p.E, *tile_at = before + p.E;
+    __shared__ int pair_expert[kDispatchPairs], pair_row[kDispatchPairs];
+    const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+    pdl_wait();
+    pdl_launch_dependents();
+    for (int e = tid; e < p.E; e += kDispatchThreads) total[e] = before[e] = 0;
+    __syncthreads();
+    const int64_t pairs = p.T * p.top_k, i0 = (int64_t)blockIdx.x * p.chunk * p.top_k;
+    const int64_t t0 = (int64_t)blockIdx.x * p.chunk;
+    const int tokens = (int)min((int64_t)p.chunk, p.T - t0), mine = tokens * p.top_k;
+    if (p.hist) {
+        for (int e = tid; e < p.E; e += kDispatchThreads) {
+            int all = 0, bef = 0;
+            for (int c = 0; c < p.n_chunks; ++c) {
+                const int n = p.hist[(int64_t)c * p.E + e];
+                all += n;
+                if (c < (int)blockIdx.x) bef += n;
+            }
+            total[e] = all;
+            before[e] = bef;
+        }
+    } else {
+        for (int64_t i = tid; i < pairs; i += kDispatchThreads) {
+            const int e = local_expert(p, i);
+            if (e >= 0) {
+                atomicAdd(&total[e], 1);
+                if (i < i0) atomicAdd(&before[e], 1);
+            }
+        }
+    }
+    for (int i = tid; i < mine; i += kDispatchThreads) pair_expert[i] = local_expert(p, i0 + i);
+    __syncthreads();
+    const bool writes_tiles = blockIdx.x == 0 && blockIdx.y == 0;
+    if (writes_tiles) {
+        for (int e = tid; e < p.E; e += kDispatchThreads) tile_at[e] = (total[e] + p.tile_rows - 1) / p.tile_rows;
+        __syncthreads();
+        if (warp == 1) {
+            const int n = warp_prefix(tile_at, p.E, lane);
+            if (lane == 0) *p.n_tiles = n;
+        }
+        // (the counts are needed below: the tiles take a copy of them before they become rows)
+        __syncthreads();
+        for (int e = tid; e < p.E; e += kDispatchThreads) {
+            int row = 0;
+            for (int f = 0; f < e; ++f) row += total[f];
+            for (int k = 0; k * p.tile_rows < total[e]; ++k)
+                p.tiles[tile_at[e] + k] =
+                    Tile{row + k * p.tile_rows, min(p.tile_rows, total[e] - k * p.tile_rows), e, 0};
+        }
+        __syncthreads();
+    }
+    if (warp == 0) (void)warp_prefix(total, p.E, lane);   // now each expert's first row
+    __syncthreads();
+    for (int i = tid; i < mine; i += kDispatchThreads) {
+        const int e = pair_expert[i];
+        int row = -1;
+        if (e >= 0) {
+            row = total[e] + before[e];
+            for (int o = 0; o < i; ++o) row += pair_expert[o] == e ? 1 : 0;
+        }
+        pair_row[i] = row;
+        if (blockIdx.y == 0) p.pos[i0 + i] = row;
+    }
+    __syncthreads();
+    const int64_t kb = (p.H + kBlock - 1) / kBlock;
+    const int64_t per = (kb + gridDim.y - 1) / gridDim.y, b0 = blockIdx.y * per, nb = min(per, kb - b0);
+    if (nb <= 0) return;
+    const int l = tid % 16;
+    const uint32_t mask = 0xFFFFu << (tid & 16);
+    const bool wide = p.H % 8 == 0 && (reinterpret_cast<uintptr_t>(p.x) & 15u) == 0;
+    for (int64_t it = tid / 16; it < tokens * nb; it += kDispatchThreads / 16) {
+        const int t = (int)(it / nb);
+        const int64_t b = b0 + it % nb;
+        float v[8], a;
+        uint8_t q[8];
+        load_block8(p.x + (t0 + t) * p.H, p.H, b, l, wide, v);
+        round_block8(v, mask, a, q);
+        const float s = block_scale(a);
+        const int64_t k = b * kBlock + l * 8;
+        for (int j = 0; j < p.top_k; ++j) {
+            const int row = pair_row[t * p.top_k + j];
+            if (row < 0) continue;
+            store8(p.xq + (int64_t)row * p.ldq + k, p.H - k, true, q);
+            if (l == 0) p.xs[(int64_t)row * kb + b] = s;
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// y[t] = shared[t] + sum_j w o
+// ---------------------------------------------------------------------------
+template <int VEC>
+__global__ void __launch_bounds__(256) combine_kernel(const float *o, const int32_t *pos, const float *weights,
+                                                      int top_k, const uint16_t *shared, uint16_t *y, int64_t T,
+                                                      int64_t H) {
+    pdl_wait();
+    const int64_t per = H / VEC, items = T * per;
+    for (int64_t it = (int64_t)blockIdx.x * 256 + threadIdx.x; it < items; it += (int64_t)gridDim.x * 256) {
+        const int64_t t = it / per, c = it % per * VEC;
+        float acc[VEC];
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) acc[i] = shared ? bf16_bits_to_f32(shared[t * H + c + i]) : 0.f;
+        for (int j = 0; j < top_k; ++j) {
+            const int row = pos[t * top_k + j];
+            if (row < 0) continue;
+            const float w = weights[t * top_k + j];
+            const float *src = o + (int64_t)row * H + c;
+            if constexpr (VEC == 4) {
+                const float4 v = __ldcs(reinterpret_cast<const float4 *>(src));
+                acc[0] = fmaf(w, v.x, acc[0]);
+                acc[1] = fmaf(w, v.y, acc[1]);
+                acc[2] = fmaf(w, v.z, acc[2]);
+                acc[3] = fmaf(w, v.w, acc[3]);
+            } else {
+                acc[0] = fmaf(w, src[0], acc[0]);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) y[t * H + c + i] = f32_to_bf16_bits(acc[i]);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// generic product: 16 token rows x 16 weight rows per CTA, one thread per output
+// ---------------------------------------------------------------------------
+template <int EPI>
+__global__ void __launch_bounds__(256) block_simt_kernel(const BlockGemm g) {
+    constexpr int MATS = EPI == BLOCK_SWIGLU ? 2 : 1;
+    __shared__ float sx[kSimtTileRows][kBlock + 1], sw[MATS][16][kBlock + 1];
+    pdl_wait();
+    Tile t;
+    if (g.tiles) {
+        if ((int)blockIdx.x >= *g.n_tiles) return;
+        t = g.tiles[blockIdx.x];
+    } else {
+        t.row0 = blockIdx.x * kSimtTileRows;
+        t.rows = (int)min((int64_t)kSimtTileRows, g.T - t.row0);
+        t.expert = 0;
+    }
+    const int64_t n0 = (int64_t)blockIdx.y * 16, n = n0 + threadIdx.x % 16;
+    const int r = threadIdx.x / 16;
+    const uint8_t *w = g.wq + (int64_t)t.expert * g.w_group_rows * g.ldw;
+    const float *ws = g.ws + (int64_t)t.expert * g.ws_group;
+    float acc[MATS] = {};
+    for (int b = 0; b < g.kb; ++b) {
+        for (int i = threadIdx.x; i < 16 * kBlock; i += 256) {
+            const int rr = i / kBlock, kk = i % kBlock;
+            const int64_t k = (int64_t)b * kBlock + kk;
+            sx[rr][kk] = rr < t.rows && k < g.K ? e4m3_to_f32(g.xq[(int64_t)(t.row0 + rr) * g.ldx + k]) : 0.f;
+#pragma unroll
+            for (int m = 0; m < MATS; ++m)
+                sw[m][rr][kk] =
+                    n0 + rr < g.N && k < g.K ? e4m3_to_f32(w[(n0 + rr + m * g.up_rows) * g.ldw + k]) : 0.f;
+        }
+        __syncthreads();
+        if (r < t.rows && n < g.N) {
+            const float xs = g.xs[(int64_t)(t.row0 + r) * g.kb + b];
+#pragma unroll
+            for (int m = 0; m < MATS; ++m) {
+                float d = 0.f;
+                for (int kk = 0; kk < kBlock; ++kk) d = fmaf(sx[r][kk], sw[m][threadIdx.x % 16][kk], d);
+                acc[m] = fmaf(d, xs * ws[n / kBlock * g.kb + b + m * g.up_scales], acc[m]);
+            }
+        }
+        __syncthreads();
+    }
+    if (r >= t.rows || n >= g.N) return;
+    const int64_t at = (int64_t)(t.row0 + r) * g.ldo + n;
+    if constexpr (EPI == BLOCK_BF16) static_cast<uint16_t *>(g.out)[at] = f32_to_bf16_bits(acc[0]);
+    if constexpr (EPI == BLOCK_F32) static_cast<float *>(g.out)[at] = acc[0];
+    if constexpr (EPI == BLOCK_SWIGLU) static_cast<float *>(g.out)[at] = silu_f32(acc[0]) * acc[1];
+}
+
+}  // namespace
+
+cudaError_t launch_quantise_rows(const uint16_t *x, int64_t rows, int64_t K, int64_t ldx, uint8_t *q, int64_t ldq,
+                                 float *scales, int sm_count, bool pdl, cudaStream_t s) {
+    const int64_t items = rows * blocks_of(K);
+    const int blocks = (int)std::min<int64_t>((items + 15) / 16, (int64_t)sm_count * 8);
+    const int wide_in = ldx % 8 == 0 && (reinterpret_cast<uintptr_t>(x) & 15u) == 0;
+    const int wide_out = ldq % 8 == 0 && (reinterpret_cast<uintptr_t>(q) & 7u) == 0;
+    return launch_kernel(quantise_rows_kernel, dim3((unsigned)blocks), 256, 0, pdl, 1, s, x, rows, K, ldx, wide_in, q,
+                         ldq, wide_out, scales);
+}
+
+cudaError_t launch_quantise_tiles(const uint16_t *x, int64_t rows, int64_t K, int64_t ldx, uint8_t *q, int64_t ldq,
+                                  float *scales, bool pdl, cudaStream_t s) {
+    const dim3 grid((unsigned)blocks_of(K), (unsigned)blocks_of(rows));
+    return launch_kernel(quantise_tiles_kernel, grid, 256, 0, pdl, 1, s, x, rows, K, ldx, q, ldq, scales);
+}
+
+cudaError_t launch_quantise_f32(const float *h, const int *n_tiles, const Tile *tiles, int64_t max_tiles, int64_t K,
+                                uint8_t *q, int64_t ldq, float *scales, bool pdl, cudaStream_t s) {
+    const dim3 grid((unsigned)max_tiles, (unsigned)std::min<int64_t>((kSimtTileRows * blocks_of(K) + 7) / 8, 64));
+    return launch_kernel(quantise_f32_kernel, grid, 256, 0, pdl, 1, s, h, n_tiles, tiles, K, q, ldq, scales);
+}
+
+cudaError_t launch_dispatch(const DispatchParams &p, bool pdl, cudaStream_t s) {
+    if (p.hist) {
+        const cudaError_t e = launch_kernel(count_kernel, dim3((unsigned)p.n_chunks), kDispatchThreads,
+                                            (size_t)p.E * 4, pdl, 1, s, p);
+        if (e != cudaSuccess) return e;
+    }
+    return launch_kernel(dispatch_kernel, dim3((unsigned)p.n_chunks, (unsigned)p.splits), kDispatchThreads,
+                         (size_t)p.E * 12, pdl, 1, s, p);
+}
+
+cudaError_t launch_combine(const float *o, const int32_t *pos, const float *weights, int top_k, const uint16_t *shared,
+                           uint16_t *y, int64_t T, int64_t H, int sm_count, bool pdl, cudaStream_t s) {
+    const bool wide = H % 4 == 0;   // o lies in the workspace, 256-byte aligned
+    const int64_t items = wide ? T * (H / 4) : T * H;
+    const dim3 grid((unsigned)std::min<int64_t>((items + 255) / 256, (int64_t)sm_count * 16));
+    if (wide) return launch_kernel(combine_kernel<4>, grid, 256, 0, pdl, 1, s, o, pos, weights, top_k, shared, y, T, H);
+    return launch_kernel(combine_kernel<1>, grid, 256, 0, pdl, 1, s, o, pos, weights, top_k, shared, y, T, H);
+}
+
+cudaError_t launch_block_simt(const BlockGemm &g, bool pdl, cudaStream_t s) {
+    const dim3 grid((unsigned)(g.tiles ? g.max_tiles : (g.T + kSimtTileRows - 1) / kSimtTileRows),
+                    (unsigned)((g.N + 15) / 16));
+    switch (g.epi) {
+        case BLOCK_BF16: return launch_kernel(block_simt_kernel<BLOCK_BF16>, grid, 256, 0, pdl, 1, s, g);
+        case BLOCK_F32: return launch_kernel(block_simt_kernel<BLOCK_F32>, grid, 256, 0, pdl, 1, s, g);
+        default: return launch_kernel(block_simt_kernel<BLOCK_SWIGLU>, grid, 256, 0, pdl, 1, s, g);
+    }
+}
+
+}  // namespace routed
+}  // namespace mse

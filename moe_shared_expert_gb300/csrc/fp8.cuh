@@ -1,0 +1,33 @@
+// Rounding to e4m3 with one scale for each block, shared by the kernels that do it.
+#pragma once
+#include <cuda_fp8.h>
+
+#include "common.cuh"
+
+namespace mse {
+namespace routed {
+
+constexpr float kAmaxFloor = 7.888609052210118e-31f;   // 2^-100: scales stay normal numbers
+constexpr float kE4m3Max = 448.f;
+
+// |v| as an integer that orders like the number, infinities and NaN above every finite value, so
+// that a maximum over it keeps a NaN
+__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
+
+__device__ __forceinline__ float floored_amax(uint32_t bits) {
+    return __uint_as_float(max(bits, __float_as_uint(kAmaxFloor)));   // NaN orders above and stays
+}
+
+__device__ __forceinline__ float block_scale(float a) { return __fdiv_rn(a, kE4m3Max); }
+
+// e4m3(448 v / a): 448 / 512 first, so that nothing overflows; 512 is exact
+__device__ __forceinline__ uint8_t e4m3_ratio(float v, float a) {
+    return __nv_cvt_float_to_fp8(__fdiv_rn(v * 0.875f, a) * 512.f, __NV_SATFINITE, __NV_E4M3);
+}
+
+__device__ __forceinline__ float e4m3_to_f32(uint8_t q) {
+    return __half2float(__half(__nv_cvt_fp8_to_halfraw(q, __NV_E4M3)));
+}
+
+}  // namespace routed
+}  // namespace mse

@@ -1,0 +1,190 @@
+// Routing of tokens to experts: scores, groups, the best top_k, their weights.
+//
+// One warp per token; lane l holds experts l, l + 32, ... in registers.  Everything after the
+// one read of the logits stays in the warp.
+#include "common.cuh"
+#include "launch.h"
+#include "routed.h"
+
+namespace mse {
+namespace routed {
+namespace {
+
+constexpr int kRouteWarps = 8;
+// the lowest finite bf16: a logit at or below it (both types' lowest values, -inf) or NaN closes
+// its expert
+constexpr float kClosedFrom = -3.3895313892515355e38f;
+
+// Order-preserving map of a float to an unsigned integer; every finite float maps above 0.
+__device__ __forceinline__ uint32_t float_key(float f) {
+    const uint32_t u = __float_as_uint(f + 0.0f);   // -0 counts as 0
+    return (u >> 31) ? ~u : (u | 0x80000000u);
+}
+__device__ __forceinline__ float key_float(uint32_t k) {
+    return __uint_as_float((k >> 31) ? (k & 0x7FFFFFFFu) : ~k);
+}
+
+__device__ __forceinline__ float load_logit(const RouteParams &p, int64_t i) {
+    return p.bf16_logits ? bf16_bits_to_f32(static_cast<const uint16_t *>(p.logits)[i])
+                         : static_cast<const float *>(p.logits)[i];
+}
+
+// Keys of the experts whose group is not among the topk_group best become 0.  keys: this warp's
+// keys in shared memory, group g at g * (group_size + lanes) so that the lanes of neighbouring
+// groups read different banks.
+__device__ __forceinline__ uint32_t best_groups(const RouteParams &p, const uint32_t *keys, int pitch, int lanes,
+                                                int lane) {
+    const int g = lane / lanes, r = lane % lanes;
+    uint32_t k1 = 0, k2 = 0;   // the two best keys of the group
+    if (g < p.n_group) {
+        for (int i = r; i < p.group_size; i += lanes) {
+            const uint32_t k = keys[g * pitch + i];
+            k2 = max(k2, min(k, k1));
+            k1 = max(k1, k);
+        }
+    }
+    for (int d = 1; d < lanes; d <<= 1) {
+        const uint32_t o1 = __shfl_xor_sync(~0u, k1, d), o2 = __shfl_xor_sync(~0u, k2, d);
+        k2 = max(max(k2, o2), min(k1, o1));
+        k1 = max(k1, o1);
+    }
+    uint32_t value = k1;
+    if (p.group_top == 2 && k2 != 0) value = float_key(__fadd_rn(key_float(k1), key_float(k2)));
+    int better = 0;
+    for (int o = 0; o < p.n_group; ++o) {
+        const uint32_t v = __shfl_sync(~0u, value, o * lanes);
+        better += (v > value || (v == value && o < g)) ? 1 : 0;
+    }
+    const uint32_t kept = __ballot_sync(~0u, g < p.n_group && r == 0 && better < p.topk_group);
+    return kept;   // bit g * lanes: group g stays
+}
+
+template <int VPL>
+__global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RouteParams p) {
+    extern __shared__ uint32_t route_smem[];
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int64_t t = (int64_t)blockIdx.x * (blockDim.x / 32) + warp;
+    pdl_wait();
+    if (t >= p.T) return;
+    float score[VPL];
+    uint32_t key[VPL];
+    float top = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+        const int e = i * 32 + lane;
+        const float l = e < p.E ? load_logit(p, t * p.ld + e) : -INFINITY;
+        const bool open = l > kClosedFrom;
+        key[i] = open ? 1u : 0u;
+        score[i] = open ? l : -INFINITY;
+        top = fmaxf(top, score[i]);
+    }
+    if (p.sigmoid) {
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) score[i] = __fdiv_rn(1.0f, __fadd_rn(1.0f, expf(-score[i])));
+    } else {
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
+        // The sum as if rounded once, whatever the order: each term e <= 1 is split into a
+        // multiple of 2^-14 (at most 1024 of them add up exactly in 24 bits) and a remainder of
+        // at most 2^-15, whose sum's rounding errors lie 2^-13 below the last bit of the total.
+        float high = 0.f, low = 0.f;
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) {
+            score[i] = key[i] ? expf(__fsub_rn(score[i], top)) : 0.f;
+            const float h = __fsub_rn(__fadd_rn(score[i], 512.f), 512.f);
+            high += h;
+            low += __fsub_rn(score[i], h);
+        }
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) {
+            high += __shfl_xor_sync(~0u, high, d);
+            low += __shfl_xor_sync(~0u, low, d);
+        }
+        const float sum = fmaxf(__fadd_rn(high, low), 1e-30f);
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) score[i] = __fdiv_rn(score[i], sum);
+    }
+    float *my_score = reinterpret_cast<float *>(route_smem) + (size_t)warp * p.E;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+        const int e = i * 32 + lane;
+        if (e >= p.E) break;
+        my_score[e] = score[i];
+        if (key[i]) key[i] = float_key(p.bias ? __fadd_rn(score[i], p.bias[e]) : score[i]);
+    }
+    if (p.n_group > 1) {
+        const int lanes = p.n_group > 16 ? 1 : p.n_group > 8 ? 2 : p.n_group > 4 ? 4 : p.n_group > 2 ? 8 : 16;
+        const int pitch = p.group_size + lanes;
+        uint32_t *my_key = route_smem + (size_t)(blockDim.x / 32) * p.E + (size_t)warp * p.n_group * pitch;
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) {
+            const int e = i * 32 + lane;
+            if (e < p.E) my_key[e / p.group_size * pitch + e % p.group_size] = key[i];
+        }
+        __syncwarp();
+        const uint32_t kept = best_groups(p, my_key, pitch, lanes, lane);
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) {
+            const int e = i * 32 + lane;
+            if (e < p.E && !((kept >> (e / p.group_size * lanes)) & 1u)) key[i] = 0;
+        }
+    }
+    __syncwarp();
+    int id = -1;   // lane j: the j-th best
+    for (int j = 0; j < p.top_k; ++j) {
+        uint32_t best = 0;
+        int at = 0;
+#pragma unroll
+        for (int i = 0; i < VPL; ++i)
+            if (key[i] > best) { best = key[i]; at = i; }
+        const uint32_t m = __reduce_max_sync(~0u, best);
+        if (m == 0) break;
+        const uint32_t e = __reduce_min_sync(~0u, best == m ? (uint32_t)(at * 32 + lane) : ~0u);
+        if (lane == j) id = (int)e;
+#pragma unroll
+        for (int i = 0; i < VPL; ++i)
+            if ((uint32_t)(i * 32 + lane) == e) key[i] = 0;
+    }
+    float w = id >= 0 ? my_score[id] : 0.f;
+    if (p.renormalise) {
+        float total = w;
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) total += __shfl_xor_sync(~0u, total, d);
+        if (total > 0.f) w = __fdiv_rn(w, total);
+    }
+    if (lane < p.top_k) {
+        p.ids[t * p.top_k + lane] = id;
+        p.weights[t * p.top_k + lane] = w * p.scale;
+    }
+}
+
+template <int VPL>
+cudaError_t launch_vpl(const RouteParams &p, bool pdl, cudaStream_t s) {
+    // a few tokens: one warp per CTA, so that they run on as many SMs
+    const int warps = p.T >= 1024 ? kRouteWarps : 1;
+    const int lanes = p.n_group > 16 ? 1 : p.n_group > 8 ? 2 : p.n_group > 4 ? 4 : p.n_group > 2 ? 8 : 16;
+    const size_t words = (size_t)p.E + (p.n_group > 1 ? (size_t)p.n_group * (p.group_size + lanes) : 0);
+    const size_t smem = words * 4 * warps;
+    if (smem > 48 * 1024) {
+        const cudaError_t e =
+            cudaFuncSetAttribute(route_kernel<VPL>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+    }
+    return launch_kernel(route_kernel<VPL>, dim3((unsigned)((p.T + warps - 1) / warps)), warps * 32, smem, pdl, 1, s,
+                         p);
+}
+
+}  // namespace
+
+cudaError_t launch_route(const RouteParams &p, bool pdl, cudaStream_t s) {
+    const int vpl = (p.E + 31) / 32;
+    if (vpl <= 1) return launch_vpl<1>(p, pdl, s);
+    if (vpl <= 2) return launch_vpl<2>(p, pdl, s);
+    if (vpl <= 4) return launch_vpl<4>(p, pdl, s);
+    if (vpl <= 8) return launch_vpl<8>(p, pdl, s);
+    if (vpl <= 16) return launch_vpl<16>(p, pdl, s);
+    return launch_vpl<32>(p, pdl, s);
+}
+
+}  // namespace routed
+}  // namespace mse

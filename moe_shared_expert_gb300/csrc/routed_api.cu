@@ -1,0 +1,274 @@
+// C-ABI entry points of the routed-expert operators: argument validation (before any CUDA call),
+// workspace carving and kernel choice.
+#include <algorithm>
+#include <cstring>
+
+#include "device.h"
+#include "routed.h"
+
+using namespace mse;
+using namespace mse::routed;
+
+namespace {
+
+constexpr int64_t kMaxRows = (int64_t)1 << 30;     // rows and columns: indexes of tiles stay in 32 bits
+constexpr int64_t kMaxInner = (int64_t)1 << 24;
+constexpr int64_t kMaxPitch = (int64_t)1 << 32;
+
+size_t up256(size_t v) { return (v + 255) / 256 * 256; }
+bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned256(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 255u) == 0; }
+mse_status from_cuda(cudaError_t e) { return e == cudaSuccess ? MSE_OK : MSE_ERR_CUDA; }
+
+// x in 8 bits and its scales
+struct LinearWs {
+    size_t q_off, s_off, total;
+};
+LinearWs linear_ws(int64_t T, int64_t K) {
+    LinearWs w;
+    w.q_off = 0;
+    w.s_off = up256((size_t)T * (size_t)pad16(K));
+    w.total = w.s_off + up256((size_t)T * (size_t)blocks_of(K) * 4);
+    return w;
+}
+
+mse_status check_matmul(const void *xq, int64_t ldx, const void *xs, const void *wq, int64_t ldw, const void *ws,
+                        int64_t T, int64_t N, int64_t K, const void *out, mse_dtype dtype, int64_t capacity) {
+    if (!xq || !xs || !wq || !ws || !out || T <= 0 || N <= 0 || K <= 0 || ldx < K || ldw < K ||
+        ldx > kMaxPitch || ldw > kMaxPitch ||
+        (dtype != MSE_BF16 && dtype != MSE_F32) || T > kMaxRows || N > kMaxInner || K > kMaxInner)
+        return MSE_ERR_INVALID_ARG;
+    return capacity < T * N ? MSE_ERR_GEOMETRY : MSE_OK;
+}
+
+mse_status run_product(BlockGemm g, bool tensorcore, const DeviceView &d, cudaStream_t s) {
+    (void)tensorcore;
+    g.wait_limit_ns = wait_limit_ns();
+    g.err = d.err;
+    return from_cuda(launch_block_simt(g, pdl_enabled(), s));
+}
+
+BlockGemm plain_product(const uint8_t *xq, int64_t ldx, const float *xs, const uint8_t *wq, int64_t ldw,
+                        const float *ws, int64_t T, int64_t N, int64_t K, void *out, mse_dtype dtype) {
+    BlockGemm g;
+    std::memset(&g, 0, sizeof g);
+    g.T = T;
+    g.avg_rows = T;
+    g.xq = xq; g.ldx = ldx; g.xs = xs;
+    g.wq = wq; g.ldw = ldw; g.ws = ws;
+    g.N = N; g.K = K; g.kb = (int)blocks_of(K);
+    g.groups = 1;
+    g.w_group_rows = N;
+    g.epi = dtype == MSE_F32 ? BLOCK_F32 : BLOCK_BF16;
+    g.out = out; g.ldo = N;
+    return g;
+}
+
+bool tc_operands(const void *xq, int64_t ldx, const void *wq, int64_t ldw) {
+    return aligned16(xq) && aligned16(wq) && ldx % 16 == 0 && ldw % 16 == 0;
+}
+
+// ------------------------------------------------------------------ the experts' layer
+// Up to this many pairs every CTA of the dispatch counts all ids itself.
+constexpr int64_t kCountAllPairs = 4096;
+int chunk_max(int top_k) { return kDispatchPairs / top_k; }
+
+struct MoeWs {
+    size_t pos, tiles, n_tiles, hist, xq, xs, hq, hs, o, total;
+};
+MoeWs moe_ws(int64_t T, int top_k, int64_t E, int64_t H, int64_t I) {
+    const size_t P = (size_t)T * (size_t)top_k;
+    MoeWs w;
+    size_t off = 0;
+    auto take = [&](size_t bytes) { const size_t at = off; off += up256(bytes); return at; };
+    w.n_tiles = take(4);
+    w.pos = take(P * 4);
+    w.tiles = take((P / kSimtTileRows + std::min<size_t>(P, (size_t)E) + 1) * sizeof(Tile));
+    w.hist = take((size_t)((T + chunk_max(top_k) - 1) / chunk_max(top_k)) * (size_t)E * 4);
+    w.xq = take(P * (size_t)pad16(H));
+    w.xs = take(P * (size_t)blocks_of(H) * 4);
+    w.hq = take(P * (size_t)pad16(I));
+    w.hs = take(P * (size_t)blocks_of(I) * 4);
+    w.o = take(P * (size_t)std::max(H, I) * 4);   // the pairs' outputs (generic kernels: h before it)
+    w.total = off;
+    return w;
+}
+
+bool moe_sizes_ok(int64_t T, int top_k, int64_t E, int64_t H, int64_t I) {
+    return T > 0 && top_k > 0 && E > 0 && H > 0 && I > 0 && top_k <= MSE_ROUTE_MAX_TOP_K &&
+           E <= MSE_ROUTE_MAX_EXPERTS && T * top_k <= kMaxRows && T <= kMaxRows && H <= kMaxInner && I <= kMaxInner;
+}
+
+}  // namespace
+
+extern "C" {
+
+mse_status moe_route(const void *logits, mse_dtype logits_dtype, int64_t T, int64_t E, int64_t ld, const float *bias,
+                     mse_score scoring, int n_group, int topk_group, int group_top, int top_k, int renormalise,
+                     float scale, int32_t *ids, float *weights, int64_t capacity, void *stream) {
+    if (!logits || !ids || !weights || T <= 0 || E <= 0 || ld < E || E > MSE_ROUTE_MAX_EXPERTS || T > kMaxRows ||
+        ld > kMaxPitch ||
+        (logits_dtype != MSE_BF16 && logits_dtype != MSE_F32) ||
+        (scoring != MSE_SCORE_SOFTMAX && scoring != MSE_SCORE_SIGMOID) || n_group <= 0 ||
+        n_group > MSE_ROUTE_MAX_GROUPS || topk_group <= 0 || topk_group > n_group ||
+        (group_top != 1 && group_top != 2) || top_k <= 0 || top_k > MSE_ROUTE_MAX_TOP_K)
+        return MSE_ERR_INVALID_ARG;
+    if (E % n_group != 0) return MSE_ERR_NOT_DIVISIBLE;
+    if (top_k > topk_group * (E / n_group)) return MSE_ERR_INVALID_ARG;
+    if (capacity < T * top_k) return MSE_ERR_GEOMETRY;
+    DeviceView d;
+    const mse_status st = device_view(&d);
+    if (st != MSE_OK) return st;
+    begin_untracked_call(stream);
+    RouteParams p;
+    p.logits = logits; p.bf16_logits = logits_dtype == MSE_BF16;
+    p.T = T; p.ld = ld; p.E = (int)E; p.bias = bias;
+    p.sigmoid = scoring == MSE_SCORE_SIGMOID;
+    p.n_group = n_group; p.group_size = (int)(E / n_group); p.topk_group = topk_group; p.group_top = group_top;
+    p.top_k = top_k; p.renormalise = renormalise != 0; p.scale = scale;
+    p.ids = ids; p.weights = weights;
+    return from_cuda(launch_route(p, pdl_enabled(), static_cast<cudaStream_t>(stream)));
+}
+
+mse_status fp8_block_quantise(const mse_bf16 *x, int64_t rows, int64_t K, int64_t ldx, int block_rows, uint8_t *q,
+                              int64_t ldq, int64_t q_capacity, float *scales, int64_t scales_capacity, void *stream) {
+    if (!x || !q || !scales || rows <= 0 || K <= 0 || ldx < K || ldq < K || (block_rows != 1 && block_rows != kBlock) ||
+        rows > kMaxRows || K > kMaxInner || ldx > kMaxPitch || ldq > kMaxPitch)
+        return MSE_ERR_INVALID_ARG;
+    const int64_t scale_rows = block_rows == 1 ? rows : blocks_of(rows);
+    if (block_rows != 1 && scale_rows > 65535) return MSE_ERR_INVALID_ARG;
+    if (q_capacity < (rows - 1) * ldq + K || scales_capacity < scale_rows * blocks_of(K)) return MSE_ERR_GEOMETRY;
+    DeviceView d;
+    const mse_status st = device_view(&d);
+    if (st != MSE_OK) return st;
+    begin_untracked_call(stream);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (block_rows == 1)
+        return from_cuda(launch_quantise_rows(x, rows, K, ldx, q, ldq, scales, d.sm_count, pdl_enabled(), s));
+    return from_cuda(launch_quantise_tiles(x, rows, K, ldx, q, ldq, scales, pdl_enabled(), s));
+}
+
+mse_status fp8_block_matmul(const uint8_t *xq, int64_t ldx, const float *xs, const uint8_t *wq, int64_t ldw,
+                            const float *ws, int64_t T, int64_t N, int64_t K, void *out, mse_dtype out_dtype,
+                            int64_t out_capacity, void *stream) {
+    mse_status st = check_matmul(xq, ldx, xs, wq, ldw, ws, T, N, K, out, out_dtype, out_capacity);
+    if (st != MSE_OK) return st;
+    DeviceView d;
+    if ((st = device_view(&d)) != MSE_OK) return st;
+    bool tensorcore = false;
+    if ((st = choose_tensorcore(tc_operands(xq, ldx, wq, ldw), &tensorcore)) != MSE_OK) return st;
+    begin_untracked_call(stream);
+    return run_product(plain_product(xq, ldx, xs, wq, ldw, ws, T, N, K, out, out_dtype), tensorcore, d,
+                       static_cast<cudaStream_t>(stream));
+}
+
+size_t fp8_block_linear_workspace_bytes(int64_t T, int64_t N, int64_t K) {
+    if (T <= 0 || N <= 0 || K <= 0 || T > kMaxRows || N > kMaxInner || K > kMaxInner) return 0;
+    return linear_ws(T, K).total;
+}
+
+mse_status fp8_block_linear(const mse_bf16 *x, int64_t ldx, const uint8_t *wq, int64_t ldw, const float *ws, int64_t T,
+                            int64_t N, int64_t K, void *y, mse_dtype y_dtype, int64_t y_capacity, void *workspace,
+                            size_t workspace_bytes, void *stream) {
+    mse_status st = check_matmul(x, ldx, x, wq, ldw, ws, T, N, K, y, y_dtype, y_capacity);
+    if (st != MSE_OK) return st;
+    const LinearWs L = linear_ws(T, K);
+    if (!workspace || workspace_bytes < L.total || !aligned256(workspace)) return MSE_ERR_WORKSPACE;
+    DeviceView d;
+    if ((st = device_view(&d)) != MSE_OK) return st;
+    uint8_t *xq = static_cast<uint8_t *>(workspace) + L.q_off;
+    float *xs = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + L.s_off);
+    const int64_t ldq = pad16(K);
+    bool tensorcore = false;
+    if ((st = choose_tensorcore(tc_operands(xq, ldq, wq, ldw), &tensorcore)) != MSE_OK) return st;
+    begin_untracked_call(stream);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if ((st = from_cuda(launch_quantise_rows(x, T, K, ldx, xq, ldq, xs, d.sm_count, pdl_enabled(), s))) != MSE_OK)
+        return st;
+    BlockGemm g = plain_product(xq, ldq, xs, wq, ldw, ws, T, N, K, y, y_dtype);
+    g.weights_early = 1;
+    return run_product(g, tensorcore, d, s);
+}
+
+size_t moe_experts_workspace_bytes(int64_t T, int top_k, int64_t E, int64_t H, int64_t I) {
+    return moe_sizes_ok(T, top_k, E, H, I) ? moe_ws(T, top_k, E, H, I).total : 0;
+}
+
+mse_status moe_experts_forward(const mse_bf16 *x, int64_t T, int64_t H, const int32_t *ids, const float *weights,
+                               int top_k, const uint8_t *w_gate_up, int64_t ld_gate_up, const float *s_gate_up,
+                               const uint8_t *w_down, int64_t ld_down, const float *s_down, int64_t E, int64_t I,
+                               int64_t first_expert, const mse_bf16 *shared, mse_bf16 *y, int64_t y_capacity,
+                               void *workspace, size_t workspace_bytes, void *stream) {
+    if (!x || !ids || !weights || !w_gate_up || !s_gate_up || !w_down || !s_down || !y ||
+        !moe_sizes_ok(T, top_k, E, H, I) || ld_gate_up < H || ld_down < I || ld_gate_up > kMaxPitch ||
+        ld_down > kMaxPitch || first_expert < 0)
+        return MSE_ERR_INVALID_ARG;
+    if (y_capacity < T * H) return MSE_ERR_GEOMETRY;
+    const MoeWs L = moe_ws(T, top_k, E, H, I);
+    if (!workspace || workspace_bytes < L.total || !aligned256(workspace)) return MSE_ERR_WORKSPACE;
+    DeviceView d;
+    mse_status st = device_view(&d);
+    if (st != MSE_OK) return st;
+    bool tensorcore = false;
+    const bool tc_ok = aligned16(w_gate_up) && aligned16(w_down) && ld_gate_up % 16 == 0 && ld_down % 16 == 0;
+    if ((st = choose_tensorcore(tc_ok, &tensorcore)) != MSE_OK) return st;
+    begin_untracked_call(stream);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const bool pdl = pdl_enabled();
+    uint8_t *w = static_cast<uint8_t *>(workspace);
+    const int64_t pairs = T * top_k;
+
+    DispatchParams dp;
+    std::memset(&dp, 0, sizeof dp);
+    dp.x = x; dp.T = T; dp.H = H; dp.ids = ids; dp.top_k = top_k; dp.first_expert = first_expert; dp.E = (int)E;
+    // chunks of tokens on about as many CTAs as SMs, then the k-blocks of a chunk over several CTAs
+    dp.chunk = (int)std::min<int64_t>(chunk_max(top_k), std::max<int64_t>(1, T / d.sm_count));
+    if (pairs > kCountAllPairs) {   // the ids are counted once, by a kernel of their own
+        dp.chunk = chunk_max(top_k);
+        dp.hist = reinterpret_cast<int *>(w + L.hist);
+    }
+    dp.n_chunks = (int)((T + dp.chunk - 1) / dp.chunk);
+    dp.splits = (int)std::max<int64_t>(1, std::min<int64_t>(blocks_of(H) / 8, d.sm_count / dp.n_chunks));
+    dp.pos = reinterpret_cast<int32_t *>(w + L.pos);
+    dp.tiles = reinterpret_cast<Tile *>(w + L.tiles);
+    dp.n_tiles = reinterpret_cast<int *>(w + L.n_tiles);
+    dp.tile_rows = kSimtTileRows;
+    dp.xq = w + L.xq; dp.ldq = pad16(H);
+    dp.xs = reinterpret_cast<float *>(w + L.xs);
+    if ((st = from_cuda(launch_dispatch(dp, pdl, s))) != MSE_OK) return st;
+
+    float *o = reinterpret_cast<float *>(w + L.o);
+    BlockGemm g;
+    std::memset(&g, 0, sizeof g);
+    g.T = pairs;
+    g.tiles = dp.tiles; g.n_tiles = dp.n_tiles; g.tile_rows = dp.tile_rows;
+    g.max_tiles = (int)std::min<int64_t>(pairs, pairs / dp.tile_rows + std::min<int64_t>(E, pairs));
+    g.groups = (int)E;
+    g.weights_early = 1;
+    BlockGemm gu = g;
+    gu.xq = dp.xq; gu.ldx = dp.ldq; gu.xs = dp.xs;
+    gu.wq = w_gate_up; gu.ldw = ld_gate_up; gu.ws = s_gate_up;
+    gu.N = I; gu.K = H; gu.kb = (int)blocks_of(H);
+    gu.w_group_rows = 2 * I; gu.up_rows = I;
+    gu.up_scales = blocks_of(I) * blocks_of(H); gu.ws_group = 2 * gu.up_scales;
+    gu.epi = BLOCK_SWIGLU;
+    gu.out = o; gu.ldo = I;
+    gu.hq = w + L.hq; gu.ldh = pad16(I);
+    gu.hs = reinterpret_cast<float *>(w + L.hs); gu.hb = (int)blocks_of(I);
+    if ((st = run_product(gu, tensorcore, d, s)) != MSE_OK) return st;
+    if ((st = from_cuda(launch_quantise_f32(o, dp.n_tiles, dp.tiles, g.max_tiles, I, gu.hq, gu.ldh, gu.hs, pdl, s))) !=
+        MSE_OK)
+        return st;
+    BlockGemm dn = g;
+    dn.xq = gu.hq; dn.ldx = gu.ldh; dn.xs = gu.hs;
+    dn.wq = w_down; dn.ldw = ld_down; dn.ws = s_down;
+    dn.N = H; dn.K = I; dn.kb = gu.hb;
+    dn.w_group_rows = H;
+    dn.ws_group = blocks_of(H) * blocks_of(I);
+    dn.epi = BLOCK_F32;
+    dn.out = o; dn.ldo = H;
+    if ((st = run_product(dn, tensorcore, d, s)) != MSE_OK) return st;
+    return from_cuda(launch_combine(o, dp.pos, weights, top_k, shared, y, T, H, d.sm_count, pdl, s));
+}
+
+}  // extern "C"

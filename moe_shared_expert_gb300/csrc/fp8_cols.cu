@@ -1,0 +1,385 @@
+// Block-scaled 8-bit product for few token rows: weights fill the 128-row side of the MMA,
+// up to 128 tokens are its columns (swap-AB), so that a weight byte is read once and no MMA
+// row is padding.
+//
+// out[n, t] = sum_b ws[n / 128, b] xs[t, b] (sum_{k in b} w[n, k] x[t, k]).  A scale of one
+// k-block multiplies a sum over 128 products, so the tensor cores sum one k-block at a time
+// into a fresh TMEM buffer (2 or 4 of them in turn), and the promotion warps add it, scaled,
+// to fp32 sums in registers.  A CTA owns one 128-row weight tile (SWIGLU: gate and up tile)
+// and one token tile; the k-blocks may be split over a cluster, whose CTAs exchange their
+// sums through distributed shared memory and each finish a slice of the token columns, in
+// rank order.
+//
+// Warp 0 loads (TMA), warp 1 issues MMAs, the others promote.
+#include <atomic>
+
+#include "device.h"
+#include "fp8_tc.cuh"
+#include "launch.h"
+
+namespace mse {
+namespace routed {
+namespace {
+
+constexpr int kChunk = 32;       // k-blocks whose scales are in shared memory at a time
+constexpr int kMaxColsStages = 8;
+
+constexpr int pow2_up(int v) {
+    int p = 32;
+    while (p < v) p <<= 1;
+    return p;
+}
+
+struct ColsCtrl {
+    uint64_t full[kMaxColsStages], empty[kMaxColsStages], tfull[4], tempty[4], drain;
+    uint32_t tmem_base;
+    int abort_flag;
+};
+
+template <int BN_, int EPI_>
+struct Cols {
+    static constexpr int BN = BN_, EPI = EPI_;
+    static constexpr int MATS = EPI == BLOCK_SWIGLU ? 2 : 1;
+    static constexpr int WARPS = BN >= 64 ? 8 : 4;             // promotion warps
+    static constexpr int CPT = BN / (WARPS / 4);               // token columns per thread
+    static constexpr int THREADS = 64 + 32 * WARPS;
+    static constexpr int BUF = MATS * BN;                      // TMEM columns of one k-block's sums
+    static constexpr int NBUF = BUF * 4 <= 256 ? 4 : 2;
+    static constexpr int TMEM = pow2_up(NBUF * BUF);
+    static constexpr int CTAS = TMEM <= 256 ? 2 : 1;           // resident per SM
+    static constexpr uint32_t STAGE = MATS * kOperandTile + BN * 128;
+    static constexpr int XS_PITCH = BN + 4;                    // floats; 16-byte rows, 4-way conflicts at worst
+    static constexpr uint32_t SCALES = kChunk * XS_PITCH * 4 + MATS * kChunk * 4 + 4 * BN * 4;
+    static constexpr uint32_t FIXED = 1024 + SCALES + sizeof(ColsCtrl) + 64;
+    static constexpr uint32_t BUDGET = (CTAS == 2 ? 113 : 227) * 1024;
+    static constexpr int FIT = (int)((BUDGET - FIXED) / STAGE);
+    static constexpr int STAGES = FIT < kMaxColsStages ? FIT : kMaxColsStages;
+    static constexpr size_t SMEM = FIXED + (size_t)STAGES * STAGE;
+    static_assert(STAGES >= 2, "ring");
+    // the exchange of a split tile, at most BN + 7 columns of every mat, uses the ring and the tokens' scales
+    static_assert(MATS * (BN + 7) * 512 <= STAGES * STAGE + kChunk * XS_PITCH * 4, "exchange");
+};
+
+template <typename C>
+__global__ void __launch_bounds__(C::THREADS, C::CTAS)
+    cols_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX, const BlockGemm g,
+                const int stream_weights) {
+    constexpr int BN = C::BN, MATS = C::MATS, S = C::STAGES, CPT = C::CPT;
+    constexpr int kPromo = 32 * C::WARPS;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
+    uint8_t *ring = smem_raw + (base - raw);
+    float *xs_s = reinterpret_cast<float *>(ring + (size_t)S * C::STAGE);   // [kChunk][XS_PITCH]
+    float *ws_s = xs_s + kChunk * C::XS_PITCH;                              // [MATS][kChunk]
+    uint32_t *amax_s = reinterpret_cast<uint32_t *>(ws_s + MATS * kChunk);  // [4][BN]
+    ColsCtrl *ctl = reinterpret_cast<ColsCtrl *>(amax_s + 4 * BN);
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int part = blockIdx.x, parts = gridDim.x, m = blockIdx.z;
+    const int kb0 = (int)((int64_t)g.kb * part / parts), n = (int)((int64_t)g.kb * (part + 1) / parts) - kb0;
+    volatile int *abort_flag = &ctl->abort_flag;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < S; ++s) {
+            mbar_init(smem_u32(&ctl->full[s]), 1);
+            mbar_init(smem_u32(&ctl->empty[s]), 1);
+        }
+        for (int b = 0; b < C::NBUF; ++b) {
+            mbar_init(smem_u32(&ctl->tfull[b]), 1);
+            mbar_init(smem_u32(&ctl->tempty[b]), C::WARPS);
+        }
+        mbar_init(smem_u32(&ctl->drain), 1);
+        ctl->abort_flag = 0;
+        fence_barrier_init();
+        tma_prefetch_desc(&tmW);
+        tma_prefetch_desc(&tmX);
+    }
+    if (warp == 1) {
+        tmem_alloc(smem_u32(&ctl->tmem_base), C::TMEM);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem_base = ctl->tmem_base;
+    // weights_early: the tile table and the weights were complete before this launch could start, and only the
+    // tokens and their scales are the previous kernel's
+    if (!g.weights_early) pdl_wait();
+    Tile t;
+    const bool active = tile_of_slot(g, blockIdx.y, t);
+    // Only now may the next kernel of the layer start: what it reads before its own wait is complete.
+    // (A call's last kernel lets nothing start early: its outputs may be anything to the next one.)
+    if (g.tiles) pdl_launch_dependents();
+
+    const int w_row = active ? (int)(t.expert * g.w_group_rows) + m * kBlock : 0;
+    int issued = 0;
+    if (active && warp == 0) {
+        if (lane == 0) {
+            const uint64_t pol_w = stream_weights ? l2_policy_evict_first() : l2_policy_evict_last();
+            const uint64_t pol_x = l2_policy_evict_last();
+            auto weights = [&](int s, int kb) {
+                const uint32_t bar = smem_u32(&ctl->full[s]), dst = base + s * C::STAGE;
+                mbar_arrive_expect_tx(bar, C::STAGE);
+                tma_load_2d(dst, &tmW, bar, kb * kBlock, w_row, pol_w);
+                if constexpr (MATS == 2)
+                    tma_load_2d(dst + kOperandTile, &tmW, bar, kb * kBlock, w_row + (int)g.up_rows, pol_w);
+            };
+            auto tokens = [&](int s, int kb) {
+                tma_load_2d(base + s * C::STAGE + MATS * kOperandTile, &tmX, smem_u32(&ctl->full[s]), kb * kBlock,
+                            t.row0, pol_x);
+            };
+            const int pre = min(S, n);
+            for (int i = 0; i < pre; ++i) weights(i, kb0 + i);
+            if (g.weights_early) pdl_wait();
+            for (int i = 0; i < pre; ++i) tokens(i, kb0 + i);
+            issued = pre;
+            for (int i = pre; i < n; ++i, ++issued) {
+                const int s = i % S;
+                if (!mbar_wait_bounded(smem_u32(&ctl->empty[s]), (uint32_t)((i / S - 1) & 1), abort_flag,
+                                       g.wait_limit_ns, g.err))
+                    break;
+                weights(s, kb0 + i);
+                tokens(s, kb0 + i);
+            }
+        }
+        __syncwarp();
+    } else if (active && warp == 1) {
+        if (lane == 0) {
+            const uint32_t idesc = idesc_e4m3_f32(128, BN);
+            for (int i = 0; i < n; ++i) {
+                const int s = i % S, b = i % C::NBUF;
+                if (!mbar_wait_bounded(smem_u32(&ctl->tempty[b]), (uint32_t)((i / C::NBUF) & 1) ^ 1u, abort_flag,
+                                       g.wait_limit_ns, g.err) ||
+                    !mbar_wait_bounded(smem_u32(&ctl->full[s]), (uint32_t)((i / S) & 1), abort_flag, g.wait_limit_ns,
+                                       g.err))
+                    break;
+                tc_fence_after();
+                const uint32_t st = base + s * C::STAGE;
+                const uint64_t xd = smem_desc_sw128(st + MATS * kOperandTile);
+#pragma unroll
+                for (int a = 0; a < MATS; ++a) {
+                    const uint64_t wd = smem_desc_sw128(st + a * kOperandTile);
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        tc_mma_e4m3(tmem_base + (uint32_t)(b * C::BUF + a * BN), wd + (uint64_t)(kk * 2),
+                                    xd + (uint64_t)(kk * 2), idesc, kk > 0 ? 1u : 0u);
+                }
+                tc_commit(smem_u32(&ctl->empty[s]));
+                tc_commit(smem_u32(&ctl->tfull[b]));
+            }
+        }
+        __syncwarp();
+    }
+
+    float acc[MATS][CPT];
+    const int q = warp & 3, row = q * 32 + lane, col0 = warp >= 2 ? (warp - 2) / 4 * CPT : 0;
+    if (active && warp >= 2) {
+#pragma unroll
+        for (int a = 0; a < MATS; ++a)
+#pragma unroll
+            for (int c = 0; c < CPT; ++c) acc[a][c] = 0.f;
+        if (g.weights_early) pdl_wait();
+        const int pt = threadIdx.x - 64;
+        const float *ws = g.ws + (int64_t)t.expert * g.ws_group + (int64_t)m * g.kb;
+        bool ok = true;
+        for (int c0 = 0; c0 < n && ok; c0 += kChunk) {
+            if (c0 > 0) named_barrier_sync(1, kPromo);
+            for (int i = pt; i < kChunk * BN; i += kPromo) {
+                const int k = i % kChunk, j = i / kChunk;
+                if (j >= t.rows) break;
+                if (c0 + k < n)
+                    xs_s[k * C::XS_PITCH + j] = __ldcg(g.xs + (int64_t)(t.row0 + j) * g.kb + kb0 + c0 + k);
+            }
+            if (pt < MATS * kChunk && c0 + pt % kChunk < n)
+                ws_s[pt] = __ldg(ws + (pt / kChunk) * g.up_scales + kb0 + c0 + pt % kChunk);
+            named_barrier_sync(1, kPromo);
+            for (int k = 0; k < kChunk && c0 + k < n; ++k) {
+                const int i = c0 + k, b = i % C::NBUF;
+                ok = warp_wait(smem_u32(&ctl->tfull[b]), (uint32_t)((i / C::NBUF) & 1), abort_flag, g);
+                if (!ok) break;
+                tc_fence_after();
+                const float *x = xs_s + k * C::XS_PITCH + col0;
+                const uint32_t src = tmem_base + (uint32_t)(b * C::BUF + col0) + ((uint32_t)(q * 32) << 16);
+#pragma unroll
+                for (int c = 0; c < CPT; c += 16) {
+                    uint32_t d[MATS][16];
+#pragma unroll
+                    for (int a = 0; a < MATS; ++a) tmem_ld16(src + a * BN + c, d[a]);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int a = 0; a < MATS; ++a) {
+                        const float w = ws_s[a * kChunk + k];
+#pragma unroll
+                        for (int v = 0; v < 16; v += 4) {
+                            const float4 f = *reinterpret_cast<const float4 *>(x + c + v);
+                            acc[a][c + v] = fmaf(__uint_as_float(d[a][v]), f.x * w, acc[a][c + v]);
+                            acc[a][c + v + 1] = fmaf(__uint_as_float(d[a][v + 1]), f.y * w, acc[a][c + v + 1]);
+                            acc[a][c + v + 2] = fmaf(__uint_as_float(d[a][v + 2]), f.z * w, acc[a][c + v + 2]);
+                            acc[a][c + v + 3] = fmaf(__uint_as_float(d[a][v + 3]), f.w * w, acc[a][c + v + 3]);
+                        }
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&ctl->tempty[b]));
+            }
+        }
+        __syncwarp();
+    }
+
+    // ---- the cluster's sums: every CTA gets a slice of the token columns from all, [rank][mat][column][row]
+    float *red = reinterpret_cast<float *>(ring);
+    const int slice = (BN + parts - 1) / parts;
+    if (parts > 1) {
+        cluster_sync();   // every ring of the cluster is idle
+        if (active && warp >= 2) {
+#pragma unroll
+            for (int c = 0; c < CPT; ++c) {
+                const int col = col0 + c;
+                if (col < t.rows) {
+                    const int to = col / slice, at = col - to * slice;
+#pragma unroll
+                    for (int a = 0; a < MATS; ++a)
+                        st_cluster_f32(map_to_rank(smem_u32(red + ((size_t)(part * MATS + a) * slice + at) * 128 + row),
+                                                   (uint32_t)to),
+                                       acc[a][c]);
+                }
+            }
+        }
+        cluster_sync();
+    }
+    if (active && warp >= 2) {
+        const int64_t out_n = (int64_t)m * kBlock + row;
+        const bool valid = out_n < g.N;
+        auto summed = [&](int a, int at) {
+            float v = 0.f;
+            for (int r = 0; r < parts; ++r) v += red[((size_t)(r * MATS + a) * slice + at) * 128 + row];
+            return v;
+        };
+        const int first = part * slice;                          // parts > 1: this CTA's columns
+        const int mine = min(min(slice, BN - first), t.rows - first);
+        const int half = col0 / CPT;                             // and this warp's: half, half + 2, ..
+        if constexpr (C::EPI != BLOCK_SWIGLU) {
+            auto store = [&](int col, float v) {
+                const int64_t at = (int64_t)(t.row0 + col) * g.ldo + out_n;
+                if constexpr (C::EPI == BLOCK_BF16)
+                    static_cast<uint16_t *>(g.out)[at] = f32_to_bf16_bits(v);
+                else
+                    static_cast<float *>(g.out)[at] = v;
+            };
+            if (valid) {
+                if (parts == 1) {
+#pragma unroll
+                    for (int c = 0; c < CPT; ++c)
+                        if (col0 + c < t.rows) store(col0 + c, acc[0][c]);
+                } else {
+                    for (int at = half; at < mine; at += C::WARPS / 4) store(first + at, summed(0, at));
+                }
+            }
+        } else {
+            // h = silu(g) u; the largest |h| of a token over the tile's 128 rows is its block's scale
+            auto h_of = [&](float gate, float up) { return valid ? silu_f32(gate) * up : 0.f; };
+            auto note = [&](int col, float h) {
+                const uint32_t a = __reduce_max_sync(~0u, abs_bits(h));
+                if (lane == 0) amax_s[q * BN + col] = a;
+            };
+            auto write = [&](int col, float h) {
+                const float a = floored_amax(max(max(amax_s[col], amax_s[BN + col]),
+                                                 max(amax_s[2 * BN + col], amax_s[3 * BN + col])));
+                const int64_t r = t.row0 + col;
+                if (valid) g.hq[r * g.ldh + out_n] = e4m3_ratio(h, a);
+                if (row == 0) g.hs[r * g.hb + m] = block_scale(a);
+            };
+            if (parts == 1) {
+#pragma unroll
+                for (int c = 0; c < CPT; ++c)
+                    if (col0 + c < t.rows) {
+                        acc[0][c] = h_of(acc[0][c], acc[MATS - 1][c]);
+                        note(col0 + c, acc[0][c]);
+                    }
+                named_barrier_sync(1, kPromo);
+#pragma unroll
+                for (int c = 0; c < CPT; ++c)
+                    if (col0 + c < t.rows) write(col0 + c, acc[0][c]);
+            } else {
+                for (int at = half; at < mine; at += C::WARPS / 4) {
+                    const float h = h_of(summed(0, at), summed(MATS - 1, at));
+                    red[(size_t)at * 128 + row] = h;             // read again by this thread alone
+                    note(first + at, h);
+                }
+                named_barrier_sync(1, kPromo);
+                for (int at = half; at < mine; at += C::WARPS / 4) write(first + at, red[(size_t)at * 128 + row]);
+            }
+        }
+    }
+
+    // ---- teardown: nothing in flight (after an abort: bounded waits), then the TMEM goes back
+    if (warp == 0 && lane == 0) {
+        for (int i = max(0, issued - S); i < issued; ++i)
+            if (!mbar_wait_drain(smem_u32(&ctl->full[i % S]), (uint32_t)((i / S) & 1), drain_limit(g.wait_limit_ns)))
+                __nanosleep(200000);
+    }
+    if (warp == 1 && lane == 0) {
+        tc_commit(smem_u32(&ctl->drain));
+        (void)mbar_wait_drain(smem_u32(&ctl->drain), 0, drain_limit(g.wait_limit_ns));
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc(tmem_base, C::TMEM);
+}
+
+template <typename C>
+cudaError_t run(const CUtensorMap &tw, const CUtensorMap &tx, const BlockGemm &g, int parts, int slots, int row_tiles,
+                int stream_weights, bool pdl, cudaStream_t s) {
+    static std::atomic<uint64_t> done;   // bit per device
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (!(done.load(std::memory_order_acquire) >> (dev & 63) & 1)) {
+        e = cudaFuncSetAttribute(cols_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM);
+        if (e != cudaSuccess) return e;
+        done.fetch_or(1ull << (dev & 63), std::memory_order_acq_rel);
+    }
+    return launch_kernel(cols_kernel<C>, dim3((unsigned)parts, (unsigned)slots, (unsigned)row_tiles), C::THREADS,
+                         C::SMEM, pdl, parts, s, tw, tx, g, stream_weights);
+}
+
+template <int EPI>
+cudaError_t run_bn(const CUtensorMap &tw, const CUtensorMap &tx, const BlockGemm &g, int parts, int slots,
+                   int row_tiles, int stream_weights, bool pdl, cudaStream_t s) {
+    switch (g.tile_rows) {
+        case 16: return run<Cols<16, EPI>>(tw, tx, g, parts, slots, row_tiles, stream_weights, pdl, s);
+        case 32: return run<Cols<32, EPI>>(tw, tx, g, parts, slots, row_tiles, stream_weights, pdl, s);
+        case 64: return run<Cols<64, EPI>>(tw, tx, g, parts, slots, row_tiles, stream_weights, pdl, s);
+        default: return run<Cols<128, EPI>>(tw, tx, g, parts, slots, row_tiles, stream_weights, pdl, s);
+    }
+}
+
+}  // namespace
+
+// expected token tiles x weight tiles x parts fill the CTAs that can be resident
+mse_status launch_block_cols(const BlockGemm &g, int sm_count, bool pdl, cudaStream_t s) {
+    CUtensorMap tw, tx;
+    mse_status st = map_bytes(&tw, g.wq, g.groups * g.w_group_rows, g.K, g.ldw, kBlock);
+    if (st != MSE_OK) return st;
+    if ((st = map_bytes(&tx, g.xq, g.T, g.K, g.ldx, g.tile_rows)) != MSE_OK) return st;
+    const int64_t row_tiles = blocks_of(g.N);
+    const int64_t slots = g.tiles ? g.max_tiles : (g.T + g.tile_rows - 1) / g.tile_rows;
+    const int64_t expected = g.tiles ? std::min<int64_t>(slots, g.expected_tiles) : slots;
+    if (row_tiles > 65535 || slots > 65535) return MSE_ERR_UNSUPPORTED_SHAPE;
+    const int per_sm = (g.epi == BLOCK_SWIGLU && g.tile_rows == 128) ? 1 : 2;
+    const int64_t resident = (int64_t)sm_count * per_sm;
+    const int parts = (int)std::max<int64_t>(
+        1, std::min<int64_t>(std::min<int64_t>(8, g.kb / 4), resident / std::max<int64_t>(1, row_tiles * expected)));
+    const int stream_weights = g.tiles ? g.T <= (int64_t)g.tile_rows * g.groups : slots == 1;
+    cudaError_t e;
+    switch (g.epi) {
+        case BLOCK_BF16: e = run_bn<BLOCK_BF16>(tw, tx, g, parts, (int)slots, (int)row_tiles, stream_weights, pdl, s); break;
+        case BLOCK_F32: e = run_bn<BLOCK_F32>(tw, tx, g, parts, (int)slots, (int)row_tiles, stream_weights, pdl, s); break;
+        default: e = run_bn<BLOCK_SWIGLU>(tw, tx, g, parts, (int)slots, (int)row_tiles, stream_weights, pdl, s); break;
+    }
+    return e == cudaSuccess ? MSE_OK : MSE_ERR_CUDA;
+}
+
+}  // namespace routed
+}  // namespace mse

@@ -77,8 +77,8 @@ struct BlockGemm {
     const Tile *tiles;
     const int *n_tiles;
     int max_tiles;
+    int expected_tiles;            // as the host expects it (chooses grids, not results)
     int tile_rows;
-    int64_t avg_rows;              // expected rows of a tile (chooses nothing that changes results)
     const uint8_t *xq; int64_t ldx;
     const float *xs;               // [rows x kb]
     const uint8_t *wq; int64_t ldw;
@@ -97,6 +97,9 @@ struct BlockGemm {
     uint64_t wait_limit_ns;
     uint32_t *err;
 };
+
+// Tensor-core kernel for token tiles of 16, 32, 64 or 128 rows (weights on the 128-row side).
+mse_status launch_block_cols(const BlockGemm &g, int sm_count, bool pdl, cudaStream_t s);
 
 constexpr int kSimtTileRows = 16;
 cudaError_t launch_block_simt(const BlockGemm &g, bool pdl, cudaStream_t s);

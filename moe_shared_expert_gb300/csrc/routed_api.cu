@@ -12,7 +12,7 @@ using namespace mse::routed;
 namespace {
 
 constexpr int64_t kMaxRows = (int64_t)1 << 30;     // rows and columns: indexes of tiles stay in 32 bits
-constexpr int64_t kMaxInner = (int64_t)1 << 24;
+constexpr int64_t kMaxInner = (int64_t)1 << 22;
 constexpr int64_t kMaxPitch = (int64_t)1 << 32;
 
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
@@ -41,11 +41,14 @@ mse_status check_matmul(const void *xq, int64_t ldx, const void *xs, const void 
     return capacity < T * N ? MSE_ERR_GEOMETRY : MSE_OK;
 }
 
+// Token rows of a tile: the least power of two that holds the rows expected of a group.
+int cols_tile(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128; }
+
 mse_status run_product(BlockGemm g, bool tensorcore, const DeviceView &d, cudaStream_t s) {
-    (void)tensorcore;
     g.wait_limit_ns = wait_limit_ns();
     g.err = d.err;
-    return from_cuda(launch_block_simt(g, pdl_enabled(), s));
+    if (!tensorcore) return from_cuda(launch_block_simt(g, pdl_enabled(), s));
+    return launch_block_cols(g, d.sm_count, pdl_enabled(), s);
 }
 
 BlockGemm plain_product(const uint8_t *xq, int64_t ldx, const float *xs, const uint8_t *wq, int64_t ldw,
@@ -53,7 +56,7 @@ BlockGemm plain_product(const uint8_t *xq, int64_t ldx, const float *xs, const u
     BlockGemm g;
     std::memset(&g, 0, sizeof g);
     g.T = T;
-    g.avg_rows = T;
+    g.tile_rows = cols_tile(T);
     g.xq = xq; g.ldx = ldx; g.xs = xs;
     g.wq = wq; g.ldw = ldw; g.ws = ws;
     g.N = N; g.K = K; g.kb = (int)blocks_of(K);
@@ -210,7 +213,8 @@ mse_status moe_experts_forward(const mse_bf16 *x, int64_t T, int64_t H, const in
     mse_status st = device_view(&d);
     if (st != MSE_OK) return st;
     bool tensorcore = false;
-    const bool tc_ok = aligned16(w_gate_up) && aligned16(w_down) && ld_gate_up % 16 == 0 && ld_down % 16 == 0;
+    const bool tc_ok = aligned16(w_gate_up) && aligned16(w_down) && ld_gate_up % 16 == 0 && ld_down % 16 == 0 &&
+                       E * 2 * I <= kMaxRows && E * H <= kMaxRows;   // weight rows are 32-bit coordinates
     if ((st = choose_tensorcore(tc_ok, &tensorcore)) != MSE_OK) return st;
     begin_untracked_call(stream);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -232,7 +236,7 @@ mse_status moe_experts_forward(const mse_bf16 *x, int64_t T, int64_t H, const in
     dp.pos = reinterpret_cast<int32_t *>(w + L.pos);
     dp.tiles = reinterpret_cast<Tile *>(w + L.tiles);
     dp.n_tiles = reinterpret_cast<int *>(w + L.n_tiles);
-    dp.tile_rows = kSimtTileRows;
+    dp.tile_rows = tensorcore ? cols_tile(pairs / E) : kSimtTileRows;
     dp.xq = w + L.xq; dp.ldq = pad16(H);
     dp.xs = reinterpret_cast<float *>(w + L.xs);
     if ((st = from_cuda(launch_dispatch(dp, pdl, s))) != MSE_OK) return st;
@@ -243,8 +247,8 @@ mse_status moe_experts_forward(const mse_bf16 *x, int64_t T, int64_t H, const in
     g.T = pairs;
     g.tiles = dp.tiles; g.n_tiles = dp.n_tiles; g.tile_rows = dp.tile_rows;
     g.max_tiles = (int)std::min<int64_t>(pairs, pairs / dp.tile_rows + std::min<int64_t>(E, pairs));
+    g.expected_tiles = (int)std::min<int64_t>(g.max_tiles, pairs / dp.tile_rows / 2 + std::min<int64_t>(E, pairs));
     g.groups = (int)E;
-    g.weights_early = 1;
     BlockGemm gu = g;
     gu.xq = dp.xq; gu.ldx = dp.ldq; gu.xs = dp.xs;
     gu.wq = w_gate_up; gu.ldw = ld_gate_up; gu.ws = s_gate_up;
@@ -256,7 +260,7 @@ mse_status moe_experts_forward(const mse_bf16 *x, int64_t T, int64_t H, const in
     gu.hq = w + L.hq; gu.ldh = pad16(I);
     gu.hs = reinterpret_cast<float *>(w + L.hs); gu.hb = (int)blocks_of(I);
     if ((st = run_product(gu, tensorcore, d, s)) != MSE_OK) return st;
-    if ((st = from_cuda(launch_quantise_f32(o, dp.n_tiles, dp.tiles, g.max_tiles, I, gu.hq, gu.ldh, gu.hs, pdl, s))) !=
+    if (!tensorcore && (st = from_cuda(launch_quantise_f32(o, dp.n_tiles, dp.tiles, g.max_tiles, I, gu.hq, gu.ldh, gu.hs, pdl, s))) !=
         MSE_OK)
         return st;
     BlockGemm dn = g;
@@ -267,6 +271,7 @@ mse_status moe_experts_forward(const mse_bf16 *x, int64_t T, int64_t H, const in
     dn.ws_group = blocks_of(H) * blocks_of(I);
     dn.epi = BLOCK_F32;
     dn.out = o; dn.ldo = H;
+    dn.weights_early = 1;   // (and the tiles: the gate_up launch lets this one start after its own wait)
     if ((st = run_product(dn, tensorcore, d, s)) != MSE_OK) return st;
     return from_cuda(launch_combine(o, dp.pos, weights, top_k, shared, y, T, H, d.sm_count, pdl, s));
 }

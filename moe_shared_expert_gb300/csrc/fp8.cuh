@@ -25,6 +25,11 @@ __device__ __forceinline__ uint8_t e4m3_ratio(float v, float a) {
     return __nv_cvt_float_to_fp8(__fdiv_rn(v * 0.875f, a) * 512.f, __NV_SATFINITE, __NV_E4M3);
 }
 
+// two values, already in e4m3's range, in 16 bits
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
+    return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
+}
+
 __device__ __forceinline__ float e4m3_to_f32(uint8_t q) {
     return __half2float(__half(__nv_cvt_fp8_to_halfraw(q, __NV_E4M3)));
 }

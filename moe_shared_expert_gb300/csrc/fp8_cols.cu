@@ -181,8 +181,9 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
         const int pt = threadIdx.x - 64;
         const float *ws = g.ws + (int64_t)t.expert * g.ws_group + (int64_t)m * g.kb;
         bool ok = true;
-        for (int c0 = 0; c0 < n && ok; c0 += kChunk) {
-            if (c0 > 0) named_barrier_sync(1, kPromo);
+        for (int c0 = 0; c0 < n; c0 += kChunk) {
+            // (a warp whose wait ran out takes the others along: nobody is left at a barrier)
+            if (c0 > 0 && !named_barrier_and(1, kPromo, ok)) break;
             for (int i = pt; i < kChunk * BN; i += kPromo) {
                 const int k = i % kChunk, j = i / kChunk;
                 if (j >= t.rows) break;

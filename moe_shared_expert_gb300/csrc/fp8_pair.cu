@@ -1,0 +1,375 @@
+// Block-scaled 8-bit product for many token rows: a CTA pair (cta_group::2) owns 256 tokens x 256
+// weight rows (SWIGLU: 128 gate and the 128 up rows of the same columns of h).
+//
+// out[t, n] = sum_b xs[t, b] ws[n / 128, b] (sum_{k in b} x[t, k] w[n, k]).  The tensor cores sum one
+// k-block of 128 into one of two TMEM buffers (256 columns each); the eight promotion warps of
+// each CTA add it, times one factor per row and weight block, to fp32 sums in registers: 128
+// columns of one token per thread.  Tensor cores and promotion work on alternate buffers.  The
+// pair halves what each SM reads: 32 KB per k-block of 512 MMA cycles.
+//
+// Warp 0 loads (TMA), warp 1 of the leading CTA issues MMAs, warps 4-11 promote and store; the
+// first warpgroup hands registers to them.
+#include <atomic>
+
+#include "device.h"
+#include "fp8_tc.cuh"
+#include "launch.h"
+
+namespace mse {
+namespace routed {
+namespace {
+
+constexpr int kStages = 6;
+constexpr int kPromoWarps = 8;
+constexpr int kParts = kPromoWarps / 4;        // threads that share a token row
+constexpr int kRun = 128 / kParts;             // columns in each of a thread's two runs
+constexpr int kLoad = 64;                      // columns in flight from TMEM per thread
+constexpr int kThreads = 128 + 32 * kPromoWarps;
+// registers: 384 threads x 168 at launch = 128 x 56 + 256 x 224 afterwards
+constexpr int kLaunchRegs = 168;
+constexpr int kBand = 8;                       // token tiles whose weight tiles are taken in turn (L2 reuse)
+constexpr uint32_t kStage = 2 * kOperandTile;  // per CTA: 128 token rows, 128 weight rows
+
+struct PairCtrl {
+    uint64_t full[kStages], empty[kStages], tfull[2], tempty[2], drain;
+    uint32_t tmem_base;
+    int abort_flag;
+    uint32_t amax[kParts][128];
+};
+constexpr size_t kSmem = kStages * (size_t)kStage + 1024 + sizeof(PairCtrl) + 64;
+
+// Two neighbouring columns of fp32 sums in one 64-bit register pair.
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+    uint64_t v;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(lo), "f"(hi));
+    return v;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t v) {
+    float2 f;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
+    return f;
+}
+// acc += d * f, both columns
+__device__ __forceinline__ void fma2(uint64_t &acc, uint32_t d0, uint32_t d1, uint64_t f) {
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(d0), "r"(d1));
+    asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc) : "l"(d), "l"(f));
+}
+// 32 lanes x 32 consecutive columns
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t *r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr));
+}
+
+template <int EPI>
+__global__ void __launch_bounds__(kThreads, 1)
+    pair_block_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
+                      const BlockGemm g, const int n_tiles_n) {
+    constexpr bool GLU = EPI == BLOCK_SWIGLU;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
+    PairCtrl *ctl = reinterpret_cast<PairCtrl *>(smem_raw + (base - raw) + kStages * kStage);
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const uint32_t rank = cluster_ctarank();
+    const bool leader = rank == 0;
+    const int64_t cluster = blockIdx.x / 2, n_clusters = gridDim.x / 2;
+    volatile int *abort_flag = &ctl->abort_flag;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(smem_u32(&ctl->full[s]), 1);
+            mbar_init(smem_u32(&ctl->empty[s]), 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(smem_u32(&ctl->tfull[b]), 1);
+            mbar_init(smem_u32(&ctl->tempty[b]), 2 * kPromoWarps);   // of both CTAs, on the leader's
+        }
+        mbar_init(smem_u32(&ctl->drain), 1);
+        ctl->abort_flag = 0;
+        fence_barrier_init();
+        tma_prefetch_desc(&tmX);
+        tma_prefetch_desc(&tmW);
+    }
+    if (warp == 1) {
+        tmem_alloc_pair(smem_u32(&ctl->tmem_base), 512);
+        tmem_relinquish_pair();
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();   // the peer's barriers are initialised before any remote use
+    tc_fence_after();
+    const uint32_t tmem_base = ctl->tmem_base;
+    pdl_wait();
+    if (g.tiles) pdl_launch_dependents();
+
+    const int64_t slots = g.tiles ? *g.n_tiles : (g.T + 255) / 256;
+    const int64_t total = slots * n_tiles_n;
+    // tile id -> token tile z and weight tile n: bands of kBand token tiles, z fastest
+    auto place = [&](int64_t id, Tile &t, int &n) {
+        const int64_t per = (int64_t)kBand * n_tiles_n, band = id / per, in = id % per;
+        const int64_t wide = min((int64_t)kBand, slots - band * kBand);
+        (void)tile_of_slot(g, (int)(band * kBand + in % wide), t);
+        n = (int)(in / wide);
+    };
+
+    int64_t issued = 0;
+    if (warp < 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        if (warp == 0) {
+            if (lane == 0) {
+                bool ok = true;
+                int stage = 0;
+                uint32_t phase = 0;
+                for (int64_t id = cluster; ok && id < total; id += n_clusters) {
+                    Tile t;
+                    int n;
+                    place(id, t, n);
+                    const int x_row = t.row0 + (int)rank * 128;
+                    const int w_row = (int)(t.expert * g.w_group_rows) +
+                                      (GLU ? n * 128 + (int)(rank * g.up_rows) : n * 256 + (int)rank * 128);
+                    for (int kb = 0; kb < g.kb; ++kb) {
+                        if (!mbar_wait_bounded(smem_u32(&ctl->empty[stage]), phase ^ 1u, abort_flag, g.wait_limit_ns,
+                                               g.err)) {
+                            ok = false;
+                            break;
+                        }
+                        const uint32_t fb = map_to_rank(smem_u32(&ctl->full[stage]), 0), dst = base + stage * kStage;
+                        if (leader) mbar_arrive_expect_tx(smem_u32(&ctl->full[stage]), 2 * kStage);
+                        tma_load_2d_pair(dst, &tmX, fb, kb * kBlock, x_row);
+                        tma_load_2d_pair(dst + kOperandTile, &tmW, fb, kb * kBlock, w_row);
+                        ++issued;
+                        if (++stage == kStages) { stage = 0; phase ^= 1u; }
+                    }
+                }
+            }
+            __syncwarp();
+        } else if (warp == 1) {
+            if (lane == 0 && leader) {
+                const uint32_t idesc = idesc_e4m3_f32(256, 256);
+                bool ok = true;
+                int stage = 0;
+                uint32_t phase = 0, use = 0;   // use: k-blocks so far; buffer use & 1
+                for (int64_t id = cluster; ok && id < total; id += n_clusters) {
+                    for (int kb = 0; kb < g.kb; ++kb, ++use) {
+                        const uint32_t b = use & 1u;
+                        if (!mbar_wait_bounded(smem_u32(&ctl->tempty[b]), ((use >> 1) & 1u) ^ 1u, abort_flag,
+                                               g.wait_limit_ns, g.err) ||
+                            !mbar_wait_bounded(smem_u32(&ctl->full[stage]), phase, abort_flag, g.wait_limit_ns, g.err)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        const uint64_t xd = smem_desc_sw128(base + stage * kStage);
+                        const uint64_t wd = smem_desc_sw128(base + stage * kStage + kOperandTile);
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)
+                            tc_mma_e4m3_pair(tmem_base + b * 256u, xd + (uint64_t)(kk * 2), wd + (uint64_t)(kk * 2), idesc,
+                                             kk > 0 ? 1u : 0u);
+                        tc_commit_pair_multicast(smem_u32(&ctl->empty[stage]), (uint16_t)0x3);
+                        tc_commit_pair_multicast(smem_u32(&ctl->tfull[b]), (uint16_t)0x3);
+                        if (++stage == kStages) { stage = 0; phase ^= 1u; }
+                    }
+                }
+            }
+            __syncwarp();
+        }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+        const int q = warp & 3, row = q * 32 + lane, share = (warp - 4) / 4;
+        // this thread's columns: two runs (SWIGLU: of gate and of up)
+        const uint32_t at0 = GLU ? share * kRun : share * 2 * kRun, at1 = GLU ? 128 + share * kRun : share * 2 * kRun + kRun;
+        const uint32_t lanes = tmem_base + ((uint32_t)(q * 32) << 16);
+        const uint32_t empty0 = map_to_rank(smem_u32(&ctl->tempty[0]), 0);
+        const uint32_t empty1 = map_to_rank(smem_u32(&ctl->tempty[1]), 0);
+        uint32_t use = 0;
+        for (int64_t id = cluster; id < total; id += n_clusters) {
+            Tile t;
+            int n;
+            place(id, t, n);
+            const bool row_ok = row < t.rows - (int)rank * 128;
+            const int64_t r = t.row0 + (int)rank * 128 + row;
+            // factors of one k-block: xs (any valid row where this one is not), ws of the two runs
+            const float *xs = g.xs + (row_ok ? r : (int64_t)t.row0) * g.kb;
+            const int blk = GLU ? n : min(2 * n + share * 2 * kRun / 128, (int)((g.N + kBlock - 1) / kBlock) - 1);
+            const float *ws = g.ws + (int64_t)t.expert * g.ws_group + (int64_t)blk * g.kb;
+            uint64_t acc[kRun];
+#pragma unroll
+            for (int i = 0; i < kRun; ++i) acc[i] = 0;
+            // one k-block ahead: a row's factors of 8 k-blocks share one 32-byte sector
+            float xa = __ldg(xs), ga = __ldg(ws), ua = GLU ? __ldg(ws + g.up_scales) : 0.f;
+            bool ok = true;
+            for (int kb = 0; kb < g.kb; ++kb, ++use) {
+                const float f0 = xa * ga, f1 = GLU ? xa * ua : f0;
+                if (kb + 1 < g.kb) {
+                    xa = __ldg(xs + kb + 1);
+                    ga = __ldg(ws + kb + 1);
+                    if (GLU) ua = __ldg(ws + g.up_scales + kb + 1);
+                }
+                const uint32_t b = use & 1u;
+                ok = warp_wait(smem_u32(&ctl->tfull[b]), (use >> 1) & 1u, abort_flag, g);
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t src = lanes + b * 256u;
+                const uint64_t p0 = pack2(f0, f0), p1 = pack2(f1, f1);
+#pragma unroll
+                for (int c = 0; c < 2 * kRun; c += kLoad) {
+                    uint32_t d[kLoad];
+#pragma unroll
+                    for (int v = 0; v < kLoad; v += 32)
+                        tmem_ld32(src + (c + v < kRun ? at0 + c + v : at1 + c + v - kRun), d + v);
+                    tmem_ld_wait();
+                    if (c + kLoad == 2 * kRun) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive_cluster_relaxed(b ? empty1 : empty0);
+                    }
+#pragma unroll
+                    for (int v = 0; v < kLoad; v += 2)
+                        fma2(acc[(c + v) / 2], d[v], d[v + 1], c + v < kRun ? p0 : p1);
+                }
+            }
+            if (!named_barrier_and(1, 32 * kPromoWarps, ok)) break;
+            if constexpr (GLU) {
+                const int64_t j0 = (int64_t)n * kBlock + share * kRun;
+                uint32_t am = 0;
+#pragma unroll
+                for (int i = 0; i < kRun / 2; ++i) {
+                    const float2 gate = unpack2(acc[i]), up = unpack2(acc[kRun / 2 + i]);
+                    const float h0 = j0 + 2 * i < g.N ? silu_f32(gate.x) * up.x : 0.f;
+                    const float h1 = j0 + 2 * i + 1 < g.N ? silu_f32(gate.y) * up.y : 0.f;
+                    acc[i] = pack2(h0, h1);
+                    am = max(am, max(abs_bits(h0), abs_bits(h1)));
+                }
+                ctl->amax[share][row] = am;
+                named_barrier_sync(1, 32 * kPromoWarps);
+#pragma unroll
+                for (int i = 0; i < kParts; ++i) am = max(am, ctl->amax[i][row]);
+                const float a = floored_amax(am);
+                // (the barrier after the next tile's k-blocks keeps the next write of amax behind these reads)
+                if (row_ok) {
+                    const float inv = __fdiv_rn(kE4m3Max, a);
+                    uint8_t *dst = g.hq + r * g.ldh + j0;
+#pragma unroll
+                    for (int c = 0; c < kRun / 16; ++c) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float2 p = unpack2(acc[c * 8 + i * 2]), s = unpack2(acc[c * 8 + i * 2 + 1]);
+                            w[i] = e4m3x2(p.x * inv, p.y * inv) | (e4m3x2(s.x * inv, s.y * inv) << 16);
+                        }
+                        // rows have a pitch of 16 bytes: a run that starts inside a row may be written whole
+                        if (j0 + c * 16 < g.N) *reinterpret_cast<uint4 *>(dst + c * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                    if (share == 0) g.hs[r * g.hb + n] = block_scale(a);
+                }
+            } else if (row_ok) {
+                const int64_t c0 = (int64_t)n * 256 + share * 2 * kRun;
+                if constexpr (EPI == BLOCK_F32) {
+                    float *dst = static_cast<float *>(g.out) + r * g.ldo + c0;
+                    if (c0 + 2 * kRun <= g.N && (reinterpret_cast<uintptr_t>(dst) & 15u) == 0) {
+#pragma unroll
+                        for (int i = 0; i < kRun / 2; ++i) {
+                            const float2 p = unpack2(acc[2 * i]), s = unpack2(acc[2 * i + 1]);
+                            reinterpret_cast<float4 *>(dst)[i] = make_float4(p.x, p.y, s.x, s.y);
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < kRun; ++i) {
+                            const float2 p = unpack2(acc[i]);
+                            if (c0 + 2 * i < g.N) dst[2 * i] = p.x;
+                            if (c0 + 2 * i + 1 < g.N) dst[2 * i + 1] = p.y;
+                        }
+                    }
+                } else {
+                    uint16_t *dst = static_cast<uint16_t *>(g.out) + r * g.ldo + c0;
+                    if (c0 + 2 * kRun <= g.N && (reinterpret_cast<uintptr_t>(dst) & 15u) == 0) {
+#pragma unroll
+                        for (int i = 0; i < kRun / 4; ++i) {
+                            uint32_t w[4];
+#pragma unroll
+                            for (int v = 0; v < 4; ++v) {
+                                const float2 p = unpack2(acc[4 * i + v]);
+                                w[v] = (uint32_t)f32_to_bf16_bits(p.x) | ((uint32_t)f32_to_bf16_bits(p.y) << 16);
+                            }
+                            reinterpret_cast<uint4 *>(dst)[i] = make_uint4(w[0], w[1], w[2], w[3]);
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < kRun; ++i) {
+                            const float2 p = unpack2(acc[i]);
+                            if (c0 + 2 * i < g.N) dst[2 * i] = f32_to_bf16_bits(p.x);
+                            if (c0 + 2 * i + 1 < g.N) dst[2 * i + 1] = f32_to_bf16_bits(p.y);
+                        }
+                    }
+                }
+            }
+        }
+        __syncwarp();
+    }
+
+    // ---- teardown: every issued stage is released by the leader's MMA commit once its bytes (of both
+    // CTAs) have landed and been used; after an abort the waits are bounded
+    if (warp == 0 && lane == 0) {
+        for (int64_t i = issued > kStages ? issued - kStages : 0; i < issued; ++i)
+            if (!mbar_wait_drain(smem_u32(&ctl->empty[i % kStages]), (uint32_t)((i / kStages) & 1),
+                                 drain_limit(g.wait_limit_ns)))
+                __nanosleep(200000);
+    }
+    if (warp == 1 && lane == 0 && leader) {
+        tc_commit_pair_multicast(smem_u32(&ctl->drain), (uint16_t)0x1);
+        (void)mbar_wait_drain(smem_u32(&ctl->drain), 0, drain_limit(g.wait_limit_ns));
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc_pair(tmem_base, 512);
+}
+
+template <int EPI>
+cudaError_t run(const CUtensorMap &tx, const CUtensorMap &tw, const BlockGemm &g, int clusters, int n_tiles_n, bool pdl,
+                cudaStream_t s) {
+    static std::atomic<uint64_t> done;   // bit per device
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (!(done.load(std::memory_order_acquire) >> (dev & 63) & 1)) {
+        // the hand-over of registers needs the ones it was written for
+        cudaFuncAttributes at;
+        if ((e = cudaFuncGetAttributes(&at, pair_block_kernel<EPI>)) != cudaSuccess) return e;
+        if (at.numRegs < kLaunchRegs) return cudaErrorInvalidConfiguration;
+        e = cudaFuncSetAttribute(pair_block_kernel<EPI>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+        if (e != cudaSuccess) return e;
+        done.fetch_or(1ull << (dev & 63), std::memory_order_acq_rel);
+    }
+    return launch_kernel(pair_block_kernel<EPI>, dim3((unsigned)(2 * clusters)), kThreads, kSmem, pdl, 2, s, tx, tw, g,
+                         n_tiles_n);
+}
+
+}  // namespace
+
+mse_status launch_block_pair(const BlockGemm &g, int sm_count, bool pdl, cudaStream_t s) {
+    CUtensorMap tw, tx;
+    mse_status st = map_bytes(&tw, g.wq, g.groups * g.w_group_rows, g.K, g.ldw, 128);
+    if (st != MSE_OK) return st;
+    if ((st = map_bytes(&tx, g.xq, g.T, g.K, g.ldx, 128)) != MSE_OK) return st;
+    const int n_tiles_n = (int)((g.N + (g.epi == BLOCK_SWIGLU ? 127 : 255)) / (g.epi == BLOCK_SWIGLU ? 128 : 256));
+    const int64_t slots = g.tiles ? g.max_tiles : (g.T + 255) / 256;
+    const int clusters = (int)std::min<int64_t>(sm_count / 2, slots * n_tiles_n);
+    cudaError_t e;
+    switch (g.epi) {
+        case BLOCK_BF16: e = run<BLOCK_BF16>(tx, tw, g, clusters, n_tiles_n, pdl, s); break;
+        case BLOCK_F32: e = run<BLOCK_F32>(tx, tw, g, clusters, n_tiles_n, pdl, s); break;
+        default: e = run<BLOCK_SWIGLU>(tx, tw, g, clusters, n_tiles_n, pdl, s); break;
+    }
+    return e == cudaSuccess ? MSE_OK : MSE_ERR_CUDA;
+}
+
+}  // namespace routed
+}  // namespace mse

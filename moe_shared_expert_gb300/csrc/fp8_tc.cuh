@@ -33,6 +33,13 @@ __device__ __forceinline__ void tc_mma_e4m3_pair(uint32_t d_tmem, uint64_t a_des
         : "memory");
 }
 
+// Arrive on an mbarrier of a CTA of the cluster without ordering memory: what it announces is that
+// TMEM was read (tcgen05.wait::ld and a tcgen05 fence order that).  A release at cluster scope here
+// waits for the thread's outstanding global loads, once per k-block: 1.6 times the kernel's time.
+__device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t cluster_addr) {
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
 // The token tile of slot z: a dispatch's tile, or rows [z tile_rows, ..) of the one group.
 __device__ __forceinline__ bool tile_of_slot(const BlockGemm &g, int z, Tile &t) {
     if (g.tiles) {

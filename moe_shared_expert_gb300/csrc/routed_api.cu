@@ -41,13 +41,15 @@ mse_status check_matmul(const void *xq, int64_t ldx, const void *xs, const void 
     return capacity < T * N ? MSE_ERR_GEOMETRY : MSE_OK;
 }
 
-// Token rows of a tile: the least power of two that holds the rows expected of a group.
-int cols_tile(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128; }
+// Token rows of a tile, from the rows expected of a group: up to 128 the least power of two that
+// holds them (swap-AB kernel), above that 256 (CTA-pair kernel).
+int tile_rows_for(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : rows <= 256 ? 128 : 256; }
 
 mse_status run_product(BlockGemm g, bool tensorcore, const DeviceView &d, cudaStream_t s) {
     g.wait_limit_ns = wait_limit_ns();
     g.err = d.err;
     if (!tensorcore) return from_cuda(launch_block_simt(g, pdl_enabled(), s));
+    if (g.tile_rows == 256) return launch_block_pair(g, d.sm_count, pdl_enabled(), s);
     return launch_block_cols(g, d.sm_count, pdl_enabled(), s);
 }
 
@@ -56,7 +58,7 @@ BlockGemm plain_product(const uint8_t *xq, int64_t ldx, const float *xs, const u
     BlockGemm g;
     std::memset(&g, 0, sizeof g);
     g.T = T;
-    g.tile_rows = cols_tile(T);
+    g.tile_rows = tile_rows_for(T);
     g.xq = xq; g.ldx = ldx; g.xs = xs;
     g.wq = wq; g.ldw = ldw; g.ws = ws;
     g.N = N; g.K = K; g.kb = (int)blocks_of(K);
@@ -236,7 +238,7 @@ mse_status moe_experts_forward(const mse_bf16 *x, int64_t T, int64_t H, const in
     dp.pos = reinterpret_cast<int32_t *>(w + L.pos);
     dp.tiles = reinterpret_cast<Tile *>(w + L.tiles);
     dp.n_tiles = reinterpret_cast<int *>(w + L.n_tiles);
-    dp.tile_rows = tensorcore ? cols_tile(pairs / E) : kSimtTileRows;
+    dp.tile_rows = tensorcore ? tile_rows_for(pairs / E) : kSimtTileRows;
     dp.xq = w + L.xq; dp.ldq = pad16(H);
     dp.xs = reinterpret_cast<float *>(w + L.xs);
     if ((st = from_cuda(launch_dispatch(dp, pdl, s))) != MSE_OK) return st;

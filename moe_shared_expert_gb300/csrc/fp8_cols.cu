@@ -73,7 +73,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
     float *ws_s = xs_s + kChunk * C::XS_PITCH;                              // [MATS][kChunk]
     uint32_t *amax_s = reinterpret_cast<uint32_t *>(ws_s + MATS * kChunk);  // [4][BN]
     ColsCtrl *ctl = reinterpret_cast<ColsCtrl *>(amax_s + 4 * BN);
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int warp = __shfl_sync(~0u, (int)threadIdx.x / 32, 0), lane = threadIdx.x % 32;
     const int part = blockIdx.x, parts = gridDim.x, m = blockIdx.z;
     const int kb0 = (int)((int64_t)g.kb * part / parts), n = (int)((int64_t)g.kb * (part + 1) / parts) - kb0;
     volatile int *abort_flag = &ctl->abort_flag;
@@ -100,7 +100,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem_base = ctl->tmem_base;
+    const uint32_t tmem_base = __shfl_sync(~0u, ctl->tmem_base, 0);
     // weights_early: the tile table and the weights were complete before this launch could start, and only the
     // tokens and their scales are the previous kernel's
     if (!g.weights_early) pdl_wait();
@@ -113,48 +113,49 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
     const int w_row = active ? (int)(t.expert * g.w_group_rows) + m * kBlock : 0;
     int issued = 0;
     if (active && warp == 0) {
-        if (lane == 0) {
-            const uint64_t pol_w = stream_weights ? l2_policy_evict_first() : l2_policy_evict_last();
-            const uint64_t pol_x = l2_policy_evict_last();
-            auto weights = [&](int s, int kb) {
-                const uint32_t bar = smem_u32(&ctl->full[s]), dst = base + s * C::STAGE;
-                mbar_arrive_expect_tx(bar, C::STAGE);
-                tma_load_2d(dst, &tmW, bar, kb * kBlock, w_row, pol_w);
-                if constexpr (MATS == 2)
-                    tma_load_2d(dst + kOperandTile, &tmW, bar, kb * kBlock, w_row + (int)g.up_rows, pol_w);
-            };
-            auto tokens = [&](int s, int kb) {
-                tma_load_2d(base + s * C::STAGE + MATS * kOperandTile, &tmX, smem_u32(&ctl->full[s]), kb * kBlock,
-                            t.row0, pol_x);
-            };
-            const int pre = min(S, n);
-            for (int i = 0; i < pre; ++i) weights(i, kb0 + i);
-            if (g.weights_early) pdl_wait();
-            for (int i = 0; i < pre; ++i) tokens(i, kb0 + i);
-            issued = pre;
-            for (int i = pre; i < n; ++i, ++issued) {
-                const int s = i % S;
-                if (!mbar_wait_bounded(smem_u32(&ctl->empty[s]), (uint32_t)((i / S - 1) & 1), abort_flag,
-                                       g.wait_limit_ns, g.err))
-                    break;
+        const bool el = elect_lane();
+        const uint64_t pol_w = stream_weights ? l2_policy_evict_first() : l2_policy_evict_last();
+        const uint64_t pol_x = l2_policy_evict_last();
+        auto weights = [&](int s, int kb) {
+            const uint32_t bar = smem_u32(&ctl->full[s]), dst = base + s * C::STAGE;
+            mbar_arrive_expect_tx(bar, C::STAGE);
+            tma_load_2d(dst, &tmW, bar, kb * kBlock, w_row, pol_w);
+            if constexpr (MATS == 2)
+                tma_load_2d(dst + kOperandTile, &tmW, bar, kb * kBlock, w_row + (int)g.up_rows, pol_w);
+        };
+        auto tokens = [&](int s, int kb) {
+            tma_load_2d(base + s * C::STAGE + MATS * kOperandTile, &tmX, smem_u32(&ctl->full[s]), kb * kBlock, t.row0,
+                        pol_x);
+        };
+        const int pre = min(S, n);
+        for (int i = 0; i < pre; ++i)
+            if (el) weights(i, kb0 + i);
+        if (g.weights_early) pdl_wait();
+        for (int i = 0; i < pre; ++i)
+            if (el) tokens(i, kb0 + i);
+        __syncwarp();
+        issued = pre;
+        for (int i = pre; i < n; ++i, ++issued) {
+            const int s = i % S;
+            if (!warp_wait(smem_u32(&ctl->empty[s]), (uint32_t)((i / S - 1) & 1), abort_flag, g)) break;
+            if (el) {
                 weights(s, kb0 + i);
                 tokens(s, kb0 + i);
             }
+            __syncwarp();
         }
-        __syncwarp();
     } else if (active && warp == 1) {
-        if (lane == 0) {
-            const uint32_t idesc = idesc_e4m3_f32(128, BN);
-            for (int i = 0; i < n; ++i) {
-                const int s = i % S, b = i % C::NBUF;
-                if (!mbar_wait_bounded(smem_u32(&ctl->tempty[b]), (uint32_t)((i / C::NBUF) & 1) ^ 1u, abort_flag,
-                                       g.wait_limit_ns, g.err) ||
-                    !mbar_wait_bounded(smem_u32(&ctl->full[s]), (uint32_t)((i / S) & 1), abort_flag, g.wait_limit_ns,
-                                       g.err))
-                    break;
-                tc_fence_after();
-                const uint32_t st = base + s * C::STAGE;
-                const uint64_t xd = smem_desc_sw128(st + MATS * kOperandTile);
+        const bool el = elect_lane();
+        const uint32_t idesc = idesc_e4m3_f32(128, BN);
+        for (int i = 0; i < n; ++i) {
+            const int s = i % S, b = i % C::NBUF;
+            if (!warp_wait(smem_u32(&ctl->full[s]), (uint32_t)((i / S) & 1), abort_flag, g) ||
+                !warp_wait(smem_u32(&ctl->tempty[b]), (uint32_t)((i / C::NBUF) & 1) ^ 1u, abort_flag, g))
+                break;
+            tc_fence_after();
+            const uint32_t st = base + s * C::STAGE;
+            const uint64_t xd = smem_desc_sw128(st + MATS * kOperandTile);
+            if (el) {
 #pragma unroll
                 for (int a = 0; a < MATS; ++a) {
                     const uint64_t wd = smem_desc_sw128(st + a * kOperandTile);
@@ -163,11 +164,11 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
                         tc_mma_e4m3(tmem_base + (uint32_t)(b * C::BUF + a * BN), wd + (uint64_t)(kk * 2),
                                     xd + (uint64_t)(kk * 2), idesc, kk > 0 ? 1u : 0u);
                 }
-                tc_commit(smem_u32(&ctl->empty[s]));
                 tc_commit(smem_u32(&ctl->tfull[b]));
+                tc_commit(smem_u32(&ctl->empty[s]));
             }
+            __syncwarp();
         }
-        __syncwarp();
     }
 
     float acc[MATS][CPT];

@@ -23,7 +23,6 @@ constexpr int kStages = 6;
 constexpr int kPromoWarps = 8;
 constexpr int kParts = kPromoWarps / 4;        // threads that share a token row
 constexpr int kRun = 128 / kParts;             // columns in each of a thread's two runs
-constexpr int kLoad = 64;                      // columns in flight from TMEM per thread
 constexpr int kThreads = 128 + 32 * kPromoWarps;
 // registers: 384 threads x 168 at launch = 128 x 56 + 256 x 224 afterwards
 constexpr int kLaunchRegs = 168;
@@ -38,25 +37,8 @@ struct PairCtrl {
 };
 constexpr size_t kSmem = kStages * (size_t)kStage + 1024 + sizeof(PairCtrl) + 64;
 
-// Two neighbouring columns of fp32 sums in one 64-bit register pair.
-__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
-    uint64_t v;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(lo), "f"(hi));
-    return v;
-}
-__device__ __forceinline__ float2 unpack2(uint64_t v) {
-    float2 f;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
-    return f;
-}
-// acc += d * f, both columns
-__device__ __forceinline__ void fma2(uint64_t &acc, uint32_t d0, uint32_t d1, uint64_t f) {
-    uint64_t d;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(d0), "r"(d1));
-    asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc) : "l"(d), "l"(f));
-}
 // 32 lanes x 32 consecutive columns
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t *r) {
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
         "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
@@ -75,7 +57,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
     PairCtrl *ctl = reinterpret_cast<PairCtrl *>(smem_raw + (base - raw) + kStages * kStage);
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int warp = __shfl_sync(~0u, (int)threadIdx.x / 32, 0), lane = threadIdx.x % 32;
     const uint32_t rank = cluster_ctarank();
     const bool leader = rank == 0;
     const int64_t cluster = blockIdx.x / 2, n_clusters = gridDim.x / 2;
@@ -104,7 +86,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     cluster_sync();   // the peer's barriers are initialised before any remote use
     tc_fence_after();
-    const uint32_t tmem_base = ctl->tmem_base;
+    const uint32_t tmem_base = __shfl_sync(~0u, ctl->tmem_base, 0);
     pdl_wait();
     if (g.tiles) pdl_launch_dependents();
 
@@ -121,63 +103,58 @@ __global__ void __launch_bounds__(kThreads, 1)
     int64_t issued = 0;
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        const bool el = elect_lane();
         if (warp == 0) {
-            if (lane == 0) {
-                bool ok = true;
-                int stage = 0;
-                uint32_t phase = 0;
-                for (int64_t id = cluster; ok && id < total; id += n_clusters) {
-                    Tile t;
-                    int n;
-                    place(id, t, n);
-                    const int x_row = t.row0 + (int)rank * 128;
-                    const int w_row = (int)(t.expert * g.w_group_rows) +
-                                      (GLU ? n * 128 + (int)(rank * g.up_rows) : n * 256 + (int)rank * 128);
-                    for (int kb = 0; kb < g.kb; ++kb) {
-                        if (!mbar_wait_bounded(smem_u32(&ctl->empty[stage]), phase ^ 1u, abort_flag, g.wait_limit_ns,
-                                               g.err)) {
-                            ok = false;
-                            break;
-                        }
+            bool ok = true;
+            int stage = 0;
+            uint32_t phase = 0;
+            for (int64_t id = cluster; ok && id < total; id += n_clusters) {
+                Tile t;
+                int n;
+                place(id, t, n);
+                const int x_row = t.row0 + (int)rank * 128;
+                const int w_row = (int)(t.expert * g.w_group_rows) +
+                                  (GLU ? n * 128 + (int)(rank * g.up_rows) : n * 256 + (int)rank * 128);
+                for (int kb = 0; kb < g.kb; ++kb) {
+                    ok = warp_wait(smem_u32(&ctl->empty[stage]), phase ^ 1u, abort_flag, g);
+                    if (!ok) break;
+                    if (el) {
                         const uint32_t fb = map_to_rank(smem_u32(&ctl->full[stage]), 0), dst = base + stage * kStage;
                         if (leader) mbar_arrive_expect_tx(smem_u32(&ctl->full[stage]), 2 * kStage);
                         tma_load_2d_pair(dst, &tmX, fb, kb * kBlock, x_row);
                         tma_load_2d_pair(dst + kOperandTile, &tmW, fb, kb * kBlock, w_row);
-                        ++issued;
-                        if (++stage == kStages) { stage = 0; phase ^= 1u; }
                     }
+                    __syncwarp();
+                    ++issued;
+                    if (++stage == kStages) { stage = 0; phase ^= 1u; }
                 }
             }
-            __syncwarp();
-        } else if (warp == 1) {
-            if (lane == 0 && leader) {
-                const uint32_t idesc = idesc_e4m3_f32(256, 256);
-                bool ok = true;
-                int stage = 0;
-                uint32_t phase = 0, use = 0;   // use: k-blocks so far; buffer use & 1
-                for (int64_t id = cluster; ok && id < total; id += n_clusters) {
-                    for (int kb = 0; kb < g.kb; ++kb, ++use) {
-                        const uint32_t b = use & 1u;
-                        if (!mbar_wait_bounded(smem_u32(&ctl->tempty[b]), ((use >> 1) & 1u) ^ 1u, abort_flag,
-                                               g.wait_limit_ns, g.err) ||
-                            !mbar_wait_bounded(smem_u32(&ctl->full[stage]), phase, abort_flag, g.wait_limit_ns, g.err)) {
-                            ok = false;
-                            break;
-                        }
-                        tc_fence_after();
-                        const uint64_t xd = smem_desc_sw128(base + stage * kStage);
-                        const uint64_t wd = smem_desc_sw128(base + stage * kStage + kOperandTile);
+        } else if (warp == 1 && leader) {
+            const uint32_t idesc = idesc_e4m3_f32(256, 256);
+            bool ok = true;
+            int stage = 0;
+            uint32_t phase = 0, use = 0;   // use: k-blocks so far; buffer use & 1
+            for (int64_t id = cluster; ok && id < total; id += n_clusters) {
+                for (int kb = 0; kb < g.kb; ++kb, ++use) {
+                    const uint32_t b = use & 1u;
+                    ok = warp_wait(smem_u32(&ctl->full[stage]), phase, abort_flag, g) &&
+                         warp_wait(smem_u32(&ctl->tempty[b]), ((use >> 1) & 1u) ^ 1u, abort_flag, g);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint64_t xd = smem_desc_sw128(base + stage * kStage);
+                    const uint64_t wd = smem_desc_sw128(base + stage * kStage + kOperandTile);
+                    if (el) {
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk)
                             tc_mma_e4m3_pair(tmem_base + b * 256u, xd + (uint64_t)(kk * 2), wd + (uint64_t)(kk * 2), idesc,
                                              kk > 0 ? 1u : 0u);
-                        tc_commit_pair_multicast(smem_u32(&ctl->empty[stage]), (uint16_t)0x3);
                         tc_commit_pair_multicast(smem_u32(&ctl->tfull[b]), (uint16_t)0x3);
-                        if (++stage == kStages) { stage = 0; phase ^= 1u; }
+                        tc_commit_pair_multicast(smem_u32(&ctl->empty[stage]), (uint16_t)0x3);
                     }
+                    __syncwarp();
+                    if (++stage == kStages) { stage = 0; phase ^= 1u; }
                 }
             }
-            __syncwarp();
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
@@ -198,9 +175,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float *xs = g.xs + (row_ok ? r : (int64_t)t.row0) * g.kb;
             const int blk = GLU ? n : min(2 * n + share * 2 * kRun / 128, (int)((g.N + kBlock - 1) / kBlock) - 1);
             const float *ws = g.ws + (int64_t)t.expert * g.ws_group + (int64_t)blk * g.kb;
-            uint64_t acc[kRun];
+            float acc[2 * kRun];
 #pragma unroll
-            for (int i = 0; i < kRun; ++i) acc[i] = 0;
+            for (int i = 0; i < 2 * kRun; ++i) acc[i] = 0.f;
             // one k-block ahead: a row's factors of 8 k-blocks share one 32-byte sector
             float xa = __ldg(xs), ga = __ldg(ws), ua = GLU ? __ldg(ws + g.up_scales) : 0.f;
             bool ok = true;
@@ -216,22 +193,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!ok) break;
                 tc_fence_after();
                 const uint32_t src = lanes + b * 256u;
-                const uint64_t p0 = pack2(f0, f0), p1 = pack2(f1, f1);
+                // 32 columns are on their way from TMEM while the 32 before them are added
+                uint32_t d[2][32];
+                tmem_ld32(src + at0, d[0]);
 #pragma unroll
-                for (int c = 0; c < 2 * kRun; c += kLoad) {
-                    uint32_t d[kLoad];
-#pragma unroll
-                    for (int v = 0; v < kLoad; v += 32)
-                        tmem_ld32(src + (c + v < kRun ? at0 + c + v : at1 + c + v - kRun), d + v);
+                for (int c = 0; c < 2 * kRun; c += 32) {
+                    const int next = c + 32;
                     tmem_ld_wait();
-                    if (c + kLoad == 2 * kRun) {
+                    if (next < 2 * kRun) {
+                        tmem_ld32(src + (next < kRun ? at0 + next : at1 + next - kRun), d[next / 32 & 1]);
+                    } else {
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) mbar_arrive_cluster_relaxed(b ? empty1 : empty0);
                     }
 #pragma unroll
-                    for (int v = 0; v < kLoad; v += 2)
-                        fma2(acc[(c + v) / 2], d[v], d[v + 1], c + v < kRun ? p0 : p1);
+                    for (int v = 0; v < 32; ++v)
+                        acc[c + v] = fmaf(__uint_as_float(d[c / 32 & 1][v]), c < kRun ? f0 : f1, acc[c + v]);
                 }
             }
             if (!named_barrier_and(1, 32 * kPromoWarps, ok)) break;
@@ -239,32 +217,27 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int64_t j0 = (int64_t)n * kBlock + share * kRun;
                 uint32_t am = 0;
 #pragma unroll
-                for (int i = 0; i < kRun / 2; ++i) {
-                    const float2 gate = unpack2(acc[i]), up = unpack2(acc[kRun / 2 + i]);
-                    const float h0 = j0 + 2 * i < g.N ? silu_f32(gate.x) * up.x : 0.f;
-                    const float h1 = j0 + 2 * i + 1 < g.N ? silu_f32(gate.y) * up.y : 0.f;
-                    acc[i] = pack2(h0, h1);
-                    am = max(am, max(abs_bits(h0), abs_bits(h1)));
+                for (int i = 0; i < kRun; ++i) {
+                    acc[i] = j0 + i < g.N ? silu_f32(acc[i]) * acc[kRun + i] : 0.f;
+                    am = max(am, abs_bits(acc[i]));
                 }
                 ctl->amax[share][row] = am;
                 named_barrier_sync(1, 32 * kPromoWarps);
-#pragma unroll
-                for (int i = 0; i < kParts; ++i) am = max(am, ctl->amax[i][row]);
-                const float a = floored_amax(am);
-                // (the barrier after the next tile's k-blocks keeps the next write of amax behind these reads)
+                const float a = floored_amax(max(am, ctl->amax[share ^ 1][row]));
+                // (the barrier after the next tile's k-blocks keeps the next write of amax behind this read)
                 if (row_ok) {
                     const float inv = __fdiv_rn(kE4m3Max, a);
                     uint8_t *dst = g.hq + r * g.ldh + j0;
 #pragma unroll
-                    for (int c = 0; c < kRun / 16; ++c) {
+                    for (int c = 0; c < kRun; c += 16) {
                         uint32_t w[4];
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
-                            const float2 p = unpack2(acc[c * 8 + i * 2]), s = unpack2(acc[c * 8 + i * 2 + 1]);
-                            w[i] = e4m3x2(p.x * inv, p.y * inv) | (e4m3x2(s.x * inv, s.y * inv) << 16);
+                            const float *v = acc + c + 4 * i;
+                            w[i] = e4m3x2(v[0] * inv, v[1] * inv) | (e4m3x2(v[2] * inv, v[3] * inv) << 16);
                         }
                         // rows have a pitch of 16 bytes: a run that starts inside a row may be written whole
-                        if (j0 + c * 16 < g.N) *reinterpret_cast<uint4 *>(dst + c * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+                        if (j0 + c < g.N) *reinterpret_cast<uint4 *>(dst + c) = make_uint4(w[0], w[1], w[2], w[3]);
                     }
                     if (share == 0) g.hs[r * g.hb + n] = block_scale(a);
                 }
@@ -274,38 +247,30 @@ __global__ void __launch_bounds__(kThreads, 1)
                     float *dst = static_cast<float *>(g.out) + r * g.ldo + c0;
                     if (c0 + 2 * kRun <= g.N && (reinterpret_cast<uintptr_t>(dst) & 15u) == 0) {
 #pragma unroll
-                        for (int i = 0; i < kRun / 2; ++i) {
-                            const float2 p = unpack2(acc[2 * i]), s = unpack2(acc[2 * i + 1]);
-                            reinterpret_cast<float4 *>(dst)[i] = make_float4(p.x, p.y, s.x, s.y);
-                        }
+                        for (int i = 0; i < 2 * kRun; i += 4)
+                            *reinterpret_cast<float4 *>(dst + i) =
+                                make_float4(acc[i], acc[i + 1], acc[i + 2], acc[i + 3]);
                     } else {
 #pragma unroll
-                        for (int i = 0; i < kRun; ++i) {
-                            const float2 p = unpack2(acc[i]);
-                            if (c0 + 2 * i < g.N) dst[2 * i] = p.x;
-                            if (c0 + 2 * i + 1 < g.N) dst[2 * i + 1] = p.y;
-                        }
+                        for (int i = 0; i < 2 * kRun; ++i)
+                            if (c0 + i < g.N) dst[i] = acc[i];
                     }
                 } else {
                     uint16_t *dst = static_cast<uint16_t *>(g.out) + r * g.ldo + c0;
                     if (c0 + 2 * kRun <= g.N && (reinterpret_cast<uintptr_t>(dst) & 15u) == 0) {
 #pragma unroll
-                        for (int i = 0; i < kRun / 4; ++i) {
+                        for (int i = 0; i < 2 * kRun; i += 8) {
                             uint32_t w[4];
 #pragma unroll
-                            for (int v = 0; v < 4; ++v) {
-                                const float2 p = unpack2(acc[4 * i + v]);
-                                w[v] = (uint32_t)f32_to_bf16_bits(p.x) | ((uint32_t)f32_to_bf16_bits(p.y) << 16);
-                            }
-                            reinterpret_cast<uint4 *>(dst)[i] = make_uint4(w[0], w[1], w[2], w[3]);
+                            for (int v = 0; v < 4; ++v)
+                                w[v] = (uint32_t)f32_to_bf16_bits(acc[i + 2 * v]) |
+                                       ((uint32_t)f32_to_bf16_bits(acc[i + 2 * v + 1]) << 16);
+                            *reinterpret_cast<uint4 *>(dst + i) = make_uint4(w[0], w[1], w[2], w[3]);
                         }
                     } else {
 #pragma unroll
-                        for (int i = 0; i < kRun; ++i) {
-                            const float2 p = unpack2(acc[i]);
-                            if (c0 + 2 * i < g.N) dst[2 * i] = f32_to_bf16_bits(p.x);
-                            if (c0 + 2 * i + 1 < g.N) dst[2 * i + 1] = f32_to_bf16_bits(p.y);
-                        }
+                        for (int i = 0; i < 2 * kRun; ++i)
+                            if (c0 + i < g.N) dst[i] = f32_to_bf16_bits(acc[i]);
                     }
                 }
             }

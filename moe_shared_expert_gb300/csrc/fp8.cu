@@ -31,27 +31,27 @@ __device__ __forceinline__ void load_block8(const uint16_t *row, int64_t K, int6
 }
 
 // amax over the 16 lanes, then the 8 rounded values of this lane
-__device__ __forceinline__ void round_block8(const float (&v)[8], uint32_t mask, float &a, uint8_t (&q)[8]) {
+__device__ __forceinline__ void round_block8(const float (&v)[8], uint32_t mask, float &a, uint2 &q) {
     uint32_t m = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) m = max(m, abs_bits(v[i]));
 #pragma unroll
     for (int d = 8; d > 0; d >>= 1) m = max(m, __shfl_xor_sync(mask, m, d));
     a = floored_amax(m);
+    const float inv = __frcp_rn(a);
+    uint32_t w[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) q[i] = e4m3_ratio(v[i], a);
+    for (int i = 0; i < 4; ++i) w[i] = e4m3x2(e4m3_ratio(v[2 * i], a, inv), e4m3_ratio(v[2 * i + 1], a, inv));
+    q = make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
 }
 
-__device__ __forceinline__ void store8(uint8_t *dst, int64_t left, bool wide, const uint8_t (&q)[8]) {
+__device__ __forceinline__ void store8(uint8_t *dst, int64_t left, bool wide, uint2 q) {
     if (wide && left >= 8) {
-        uint2 w;
-        w.x = q[0] | (q[1] << 8) | (q[2] << 16) | ((uint32_t)q[3] << 24);
-        w.y = q[4] | (q[5] << 8) | (q[6] << 16) | ((uint32_t)q[7] << 24);
-        *reinterpret_cast<uint2 *>(dst) = w;
+        *reinterpret_cast<uint2 *>(dst) = q;
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            if (i < left) dst[i] = q[i];
+            if (i < left) dst[i] = (uint8_t)((i < 4 ? q.x : q.y) >> (i % 4 * 8));
     }
 }
 
@@ -67,7 +67,7 @@ __global__ void __launch_bounds__(256) quantise_rows_kernel(const uint16_t *x, i
     for (int64_t it = (int64_t)blockIdx.x * 16 + threadIdx.x / 16; it < items; it += (int64_t)gridDim.x * 16) {
         const int64_t r = it / kb, b = it % kb;
         float v[8], a;
-        uint8_t o[8];
+        uint2 o;
         load_block8(x + r * ldx, K, b, l, wide_in, v);
         round_block8(v, mask, a, o);
         const int64_t k = b * kBlock + l * 8;
@@ -92,10 +92,10 @@ __global__ void __launch_bounds__(256) quantise_tiles_kernel(const uint16_t *x, 
     __syncthreads();
 #pragma unroll
     for (int w = 0; w < 8; ++w) m = max(m, part[w]);
-    const float a = floored_amax(m);
+    const float a = floored_amax(m), inv = __frcp_rn(a);
     for (int i = threadIdx.x; i < kBlock * kBlock; i += 256) {
         const int64_t r = r0 + i / kBlock, k = k0 + i % kBlock;
-        if (r < rows && k < K) q[r * ldq + k] = e4m3_ratio(bf16_bits_to_f32(x[r * ldx + k]), a);
+        if (r < rows && k < K) q[r * ldq + k] = e4m3_of(bf16_bits_to_f32(x[r * ldx + k]), a, inv);
     }
     if (threadIdx.x == 0) scales[blockIdx.y * (int64_t)gridDim.x + blockIdx.x] = block_scale(a);
 }
@@ -118,11 +118,11 @@ __global__ void __launch_bounds__(256) quantise_f32_kernel(const float *h, const
             v[i] = k < K ? h[r * K + k] : 0.f;
             m = max(m, abs_bits(v[i]));
         }
-        const float a = floored_amax(__reduce_max_sync(~0u, m));
+        const float a = floored_amax(__reduce_max_sync(~0u, m)), inv = __frcp_rn(a);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int64_t k = b * kBlock + i * 32 + lane;
-            if (k < K) q[r * ldq + k] = e4m3_ratio(v[i], a);
+            if (k < K) q[r * ldq + k] = e4m3_of(v[i], a, inv);
         }
         if (lane == 0) scales[r * kb + b] = block_scale(a);
     }
@@ -187,15 +187,11 @@ __global__ void __launch_bounds__(kDispatchThreads) dispatch_kernel(const Dispat
     const int64_t t0 = (int64_t)blockIdx.x * p.chunk;
     const int tokens = (int)min((int64_t)p.chunk, p.T - t0), mine = tokens * p.top_k;
     if (p.hist) {
-        for (int e = tid; e < p.E; e += kDispatchThreads) {
-            int all = 0, bef = 0;
-            for (int c = 0; c < p.n_chunks; ++c) {
-                const int n = p.hist[(int64_t)c * p.E + e];
-                all += n;
-                if (c < (int)blockIdx.x) bef += n;
-            }
-            total[e] = all;
-            before[e] = bef;
+        for (int i = tid; i < p.n_chunks * p.E; i += kDispatchThreads) {
+            const int n = p.hist[i];
+            if (n == 0) continue;
+            atomicAdd(&total[i % p.E], n);
+            if (i / p.E < (int)blockIdx.x) atomicAdd(&before[i % p.E], n);
         }
     } else {
         for (int64_t i = tid; i < pairs; i += kDispatchThreads) {
@@ -250,7 +246,7 @@ __global__ void __launch_bounds__(kDispatchThreads) dispatch_kernel(const Dispat
         const int t = (int)(it / nb);
         const int64_t b = b0 + it % nb;
         float v[8], a;
-        uint8_t q[8];
+        uint2 q;
         load_block8(p.x + (t0 + t) * p.H, p.H, b, l, wide, v);
         round_block8(v, mask, a, q);
         const float s = block_scale(a);

@@ -20,9 +20,17 @@ __device__ __forceinline__ float floored_amax(uint32_t bits) {
 
 __device__ __forceinline__ float block_scale(float a) { return __fdiv_rn(a, kE4m3Max); }
 
-// e4m3(448 v / a): 448 / 512 first, so that nothing overflows; 512 is exact
-__device__ __forceinline__ uint8_t e4m3_ratio(float v, float a) {
-    return __nv_cvt_float_to_fp8(__fdiv_rn(v * 0.875f, a) * 512.f, __NV_SATFINITE, __NV_E4M3);
+// 448 v / a for an a of floored_amax(): (448 / 512) v first, so that nothing overflows; 512 is exact.
+// `inv` is 1 / a to nearest.  One residual step makes every quotient that 32 bits hold exact (q's
+// error is a few units in the last place, the residual is exact, and so the step's error lies far
+// below half a unit), ties of e4m3 among them; the others are nowhere near a tie when v and a are
+// bf16.  Infinite v or a: NaN, like the quotient's product with the scale.
+__device__ __forceinline__ float e4m3_ratio(float v, float a, float inv) {
+    const float t = v * 0.875f, q = t * inv;
+    return fmaf(fmaf(-a, q, t), inv, q) * 512.f;
+}
+__device__ __forceinline__ uint8_t e4m3_of(float v, float a, float inv) {
+    return __nv_cvt_float_to_fp8(e4m3_ratio(v, a, inv), __NV_SATFINITE, __NV_E4M3);
 }
 
 // two values, already in e4m3's range, in 16 bits

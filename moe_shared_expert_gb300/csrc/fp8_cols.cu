@@ -288,7 +288,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
                 const float a = floored_amax(max(max(amax_s[col], amax_s[BN + col]),
                                                  max(amax_s[2 * BN + col], amax_s[3 * BN + col])));
                 const int64_t r = t.row0 + col;
-                if (valid) g.hq[r * g.ldh + out_n] = e4m3_ratio(h, a);
+                if (valid) g.hq[r * g.ldh + out_n] = e4m3_of(h, a, __frcp_rn(a));
                 if (row == 0) g.hs[r * g.hb + m] = block_scale(a);
             };
             if (parts == 1) {

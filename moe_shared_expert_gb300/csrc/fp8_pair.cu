@@ -19,7 +19,7 @@ namespace mse {
 namespace routed {
 namespace {
 
-constexpr int kStages = 6;
+constexpr int kStages = 5;
 constexpr int kPromoWarps = 8;
 constexpr int kParts = kPromoWarps / 4;        // threads that share a token row
 constexpr int kRun = 128 / kParts;             // columns in each of a thread's two runs
@@ -35,7 +35,8 @@ struct PairCtrl {
     int abort_flag;
     uint32_t amax[kParts][128];
 };
-constexpr size_t kSmem = kStages * (size_t)kStage + 1024 + sizeof(PairCtrl) + 64;
+constexpr uint32_t kStaging = 32 * 128;        // per promotion warp: 32 rows of 128 bytes on their way out
+constexpr size_t kSmem = kStages * (size_t)kStage + kPromoWarps * kStaging + 1024 + sizeof(PairCtrl) + 64;
 
 // 32 lanes x 32 consecutive columns
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
@@ -49,6 +50,10 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
         : "r"(taddr));
 }
 
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
+    return (uint32_t)f32_to_bf16_bits(lo) | ((uint32_t)f32_to_bf16_bits(hi) << 16);
+}
+
 template <int EPI>
 __global__ void __launch_bounds__(kThreads, 1)
     pair_block_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
@@ -56,7 +61,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr bool GLU = EPI == BLOCK_SWIGLU;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
-    PairCtrl *ctl = reinterpret_cast<PairCtrl *>(smem_raw + (base - raw) + kStages * kStage);
+    uint8_t *staging = smem_raw + (base - raw) + kStages * kStage;
+    PairCtrl *ctl = reinterpret_cast<PairCtrl *>(staging + kPromoWarps * kStaging);
     const int warp = __shfl_sync(~0u, (int)threadIdx.x / 32, 0), lane = threadIdx.x % 32;
     const uint32_t rank = cluster_ctarank();
     const bool leader = rank == 0;
@@ -226,7 +232,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const float a = floored_amax(max(am, ctl->amax[share ^ 1][row]));
                 // (the barrier after the next tile's k-blocks keeps the next write of amax behind this read)
                 if (row_ok) {
-                    const float inv = __fdiv_rn(kE4m3Max, a);
+                    const float inv = __fdiv_rn(kE4m3Max, a);   // h is in 32 bits: no ties to keep
                     uint8_t *dst = g.hq + r * g.ldh + j0;
 #pragma unroll
                     for (int c = 0; c < kRun; c += 16) {
@@ -241,36 +247,54 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     if (share == 0) g.hs[r * g.hb + n] = block_scale(a);
                 }
-            } else if (row_ok) {
+            } else {
+                // 128 bytes of each of the warp's 32 rows at a time through shared memory, so that a store
+                // covers whole lines of four rows instead of 16 bytes of 32 (16-byte words of a row in
+                // an order of their own, row mod 8, against bank conflicts)
+                constexpr int kWord = EPI == BLOCK_F32 ? 4 : 8;      // columns in 16 bytes
+                constexpr int kSize = EPI == BLOCK_F32 ? 4 : 2;
                 const int64_t c0 = (int64_t)n * 256 + share * 2 * kRun;
-                if constexpr (EPI == BLOCK_F32) {
-                    float *dst = static_cast<float *>(g.out) + r * g.ldo + c0;
-                    if (c0 + 2 * kRun <= g.N && (reinterpret_cast<uintptr_t>(dst) & 15u) == 0) {
+                uint8_t *out = static_cast<uint8_t *>(g.out);
+                const bool wide = c0 + 2 * kRun <= g.N && ((reinterpret_cast<uintptr_t>(out) | (uint64_t)g.ldo * kSize) & 15u) == 0;
+                if (wide) {
+                    uint8_t *mine = staging + (warp - 4) * kStaging;
+                    const int64_t first = t.row0 + (int)rank * 128 + q * 32;
+                    const int left = t.rows - (int)rank * 128 - q * 32;   // valid rows of this warp
 #pragma unroll
-                        for (int i = 0; i < 2 * kRun; i += 4)
-                            *reinterpret_cast<float4 *>(dst + i) =
-                                make_float4(acc[i], acc[i + 1], acc[i + 2], acc[i + 3]);
-                    } else {
+                    for (int c = 0; c < 2 * kRun; c += 8 * kWord) {
 #pragma unroll
-                        for (int i = 0; i < 2 * kRun; ++i)
-                            if (c0 + i < g.N) dst[i] = acc[i];
-                    }
-                } else {
-                    uint16_t *dst = static_cast<uint16_t *>(g.out) + r * g.ldo + c0;
-                    if (c0 + 2 * kRun <= g.N && (reinterpret_cast<uintptr_t>(dst) & 15u) == 0) {
-#pragma unroll
-                        for (int i = 0; i < 2 * kRun; i += 8) {
-                            uint32_t w[4];
-#pragma unroll
-                            for (int v = 0; v < 4; ++v)
-                                w[v] = (uint32_t)f32_to_bf16_bits(acc[i + 2 * v]) |
-                                       ((uint32_t)f32_to_bf16_bits(acc[i + 2 * v + 1]) << 16);
-                            *reinterpret_cast<uint4 *>(dst + i) = make_uint4(w[0], w[1], w[2], w[3]);
+                        for (int i = 0; i < 8; ++i) {
+                            const float *v = acc + c + i * kWord;
+                            uint4 w;
+                            if constexpr (EPI == BLOCK_F32) {
+                                w = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
+                                               __float_as_uint(v[3]));
+                            } else {
+                                w = make_uint4(bf16x2(v[0], v[1]), bf16x2(v[2], v[3]), bf16x2(v[4], v[5]),
+                                               bf16x2(v[6], v[7]));
+                            }
+                            *reinterpret_cast<uint4 *>(mine + lane * 128 + (i ^ (lane & 7)) * 16) = w;
                         }
-                    } else {
+                        __syncwarp();
 #pragma unroll
-                        for (int i = 0; i < 2 * kRun; ++i)
-                            if (c0 + i < g.N) dst[i] = f32_to_bf16_bits(acc[i]);
+                        for (int i = 0; i < 8; ++i) {
+                            const int rr = i * 4 + lane / 8;
+                            const uint4 w =
+                                *reinterpret_cast<const uint4 *>(mine + rr * 128 + ((lane & 7) ^ (rr & 7)) * 16);
+                            if (rr < left)
+                                *reinterpret_cast<uint4 *>(
+                                    out + ((first + rr) * g.ldo + c0 + c + (lane & 7) * kWord) * kSize) = w;
+                        }
+                        __syncwarp();
+                    }
+                } else if (row_ok) {
+#pragma unroll
+                    for (int i = 0; i < 2 * kRun; ++i) {
+                        if (c0 + i >= g.N) continue;
+                        if constexpr (EPI == BLOCK_F32)
+                            static_cast<float *>(g.out)[r * g.ldo + c0 + i] = acc[i];
+                        else
+                            static_cast<uint16_t *>(g.out)[r * g.ldo + c0 + i] = f32_to_bf16_bits(acc[i]);
                     }
                 }
             }

@@ -227,14 +227,15 @@ mse_status moe_experts_forward(const mse_bf16 *x, int64_t T, int64_t H, const in
     DispatchParams dp;
     std::memset(&dp, 0, sizeof dp);
     dp.x = x; dp.T = T; dp.H = H; dp.ids = ids; dp.top_k = top_k; dp.first_expert = first_expert; dp.E = (int)E;
-    // chunks of tokens on about as many CTAs as SMs, then the k-blocks of a chunk over several CTAs
+    // chunks of tokens on about as many CTAs as SMs, then the k-blocks of a chunk over several CTAs, up
+    // to eight per SM (the rows are written by many warps at once: 4096 tokens x 8 in 60 us, 230 on 128 CTAs)
     dp.chunk = (int)std::min<int64_t>(chunk_max(top_k), std::max<int64_t>(1, T / d.sm_count));
     if (pairs > kCountAllPairs) {   // the ids are counted once, by a kernel of their own
         dp.chunk = chunk_max(top_k);
         dp.hist = reinterpret_cast<int *>(w + L.hist);
     }
     dp.n_chunks = (int)((T + dp.chunk - 1) / dp.chunk);
-    dp.splits = (int)std::max<int64_t>(1, std::min<int64_t>(blocks_of(H) / 8, d.sm_count / dp.n_chunks));
+    dp.splits = (int)std::max<int64_t>(1, std::min<int64_t>(blocks_of(H) / 4, 8 * d.sm_count / dp.n_chunks));
     dp.pos = reinterpret_cast<int32_t *>(w + L.pos);
     dp.tiles = reinterpret_cast<Tile *>(w + L.tiles);
     dp.n_tiles = reinterpret_cast<int *>(w + L.n_tiles);

@@ -185,11 +185,18 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
         for (int c0 = 0; c0 < n; c0 += kChunk) {
             // (a warp whose wait ran out takes the others along: nobody is left at a barrier)
             if (c0 > 0 && !named_barrier_and(1, kPromo, ok)) break;
-            for (int i = pt; i < kChunk * BN; i += kPromo) {
-                const int k = i % kChunk, j = i / kChunk;
-                if (j >= t.rows) break;
-                if (c0 + k < n)
-                    xs_s[k * C::XS_PITCH + j] = __ldcg(g.xs + (int64_t)(t.row0 + j) * g.kb + kb0 + c0 + k);
+            // (all loads before the first store: one trip to L2, not one for each)
+            constexpr int kPer = kChunk * BN / kPromo;
+            float v[kPer];
+#pragma unroll
+            for (int u = 0; u < kPer; ++u) {
+                const int i = pt + u * kPromo, k = i % kChunk, j = i / kChunk;
+                v[u] = j < t.rows && c0 + k < n ? __ldcg(g.xs + (int64_t)(t.row0 + j) * g.kb + kb0 + c0 + k) : 0.f;
+            }
+#pragma unroll
+            for (int u = 0; u < kPer; ++u) {
+                const int i = pt + u * kPromo;
+                xs_s[i % kChunk * C::XS_PITCH + i / kChunk] = v[u];
             }
             if (pt < MATS * kChunk && c0 + pt % kChunk < n)
                 ws_s[pt] = __ldg(ws + (pt / kChunk) * g.up_scales + kb0 + c0 + pt % kChunk);

@@ -1,5 +1,5 @@
 // Block-scaled 8-bit product for few token rows: weights fill the 128-row side of the MMA,
-// up to 128 tokens are its columns (swap-AB), so that a weight byte is read once and no MMA
+// up to 64 tokens are its columns (swap-AB), so that a weight byte is read once and no MMA
 // row is padding.
 //
 // out[n, t] = sum_b ws[n / 128, b] xs[t, b] (sum_{k in b} w[n, k] x[t, k]).  A scale of one
@@ -46,12 +46,13 @@ struct Cols {
     static constexpr int BUF = MATS * BN;                      // TMEM columns of one k-block's sums
     static constexpr int NBUF = BUF * 4 <= 256 ? 4 : 2;
     static constexpr int TMEM = pow2_up(NBUF * BUF);
-    static constexpr int CTAS = TMEM <= 256 ? 2 : 1;           // resident per SM
+    static constexpr int CTAS = 2;                             // resident per SM
+    static_assert(CTAS * TMEM <= 512, "TMEM");
     static constexpr uint32_t STAGE = MATS * kOperandTile + BN * 128;
     static constexpr int XS_PITCH = BN + 4;                    // floats; 16-byte rows, 4-way conflicts at worst
     static constexpr uint32_t SCALES = kChunk * XS_PITCH * 4 + MATS * kChunk * 4 + 4 * BN * 4;
     static constexpr uint32_t FIXED = 1024 + SCALES + sizeof(ColsCtrl) + 64;
-    static constexpr uint32_t BUDGET = (CTAS == 2 ? 113 : 227) * 1024;
+    static constexpr uint32_t BUDGET = 113 * 1024;
     static constexpr int FIT = (int)((BUDGET - FIXED) / STAGE);
     static constexpr int STAGES = FIT < kMaxColsStages ? FIT : kMaxColsStages;
     static constexpr size_t SMEM = FIXED + (size_t)STAGES * STAGE;
@@ -359,8 +360,7 @@ cudaError_t run_bn(const CUtensorMap &tw, const CUtensorMap &tx, const BlockGemm
     switch (g.tile_rows) {
         case 16: return run<Cols<16, EPI>>(tw, tx, g, parts, slots, row_tiles, stream_weights, pdl, s);
         case 32: return run<Cols<32, EPI>>(tw, tx, g, parts, slots, row_tiles, stream_weights, pdl, s);
-        case 64: return run<Cols<64, EPI>>(tw, tx, g, parts, slots, row_tiles, stream_weights, pdl, s);
-        default: return run<Cols<128, EPI>>(tw, tx, g, parts, slots, row_tiles, stream_weights, pdl, s);
+        default: return run<Cols<EPI == BLOCK_SWIGLU ? 32 : 64, EPI>>(tw, tx, g, parts, slots, row_tiles, stream_weights, pdl, s);
     }
 }
 
@@ -376,8 +376,7 @@ mse_status launch_block_cols(const BlockGemm &g, int sm_count, bool pdl, cudaStr
     const int64_t slots = g.tiles ? g.max_tiles : (g.T + g.tile_rows - 1) / g.tile_rows;
     const int64_t expected = g.tiles ? std::min<int64_t>(slots, g.expected_tiles) : slots;
     if (row_tiles > 65535 || slots > 65535) return MSE_ERR_UNSUPPORTED_SHAPE;
-    const int per_sm = (g.epi == BLOCK_SWIGLU && g.tile_rows == 128) ? 1 : 2;
-    const int64_t resident = (int64_t)sm_count * per_sm;
+    const int64_t resident = (int64_t)sm_count * 2;   // CTAs per SM
     const int parts = (int)std::max<int64_t>(
         1, std::min<int64_t>(std::min<int64_t>(8, g.kb / 4), resident / std::max<int64_t>(1, row_tiles * expected)));
     const int stream_weights = g.tiles ? g.T <= (int64_t)g.tile_rows * g.groups : slots == 1;

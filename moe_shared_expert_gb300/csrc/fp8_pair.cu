@@ -10,6 +10,7 @@
 // Warp 0 loads (TMA), warp 1 of the leading CTA issues MMAs, warps 4-11 promote and store; the
 // first warpgroup hands registers to them.
 #include <atomic>
+#include <type_traits>
 
 #include "device.h"
 #include "fp8_tc.cuh"
@@ -251,51 +252,49 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // 128 bytes of each of the warp's 32 rows at a time through shared memory, so that a store
                 // covers whole lines of four rows instead of 16 bytes of 32 (16-byte words of a row in
                 // an order of their own, row mod 8, against bank conflicts)
-                constexpr int kWord = EPI == BLOCK_F32 ? 4 : 8;      // columns in 16 bytes
-                constexpr int kSize = EPI == BLOCK_F32 ? 4 : 2;
+                using Out = typename std::conditional<EPI == BLOCK_F32, float, uint16_t>::type;
+                constexpr int kWord = 16 / sizeof(Out), kPass = 8 * kWord;   // columns in 16 and in 128 bytes
                 const int64_t c0 = (int64_t)n * 256 + share * 2 * kRun;
-                uint8_t *out = static_cast<uint8_t *>(g.out);
-                const bool wide = c0 + 2 * kRun <= g.N && ((reinterpret_cast<uintptr_t>(out) | (uint64_t)g.ldo * kSize) & 15u) == 0;
-                if (wide) {
-                    uint8_t *mine = staging + (warp - 4) * kStaging;
-                    const int64_t first = t.row0 + (int)rank * 128 + q * 32;
-                    const int left = t.rows - (int)rank * 128 - q * 32;   // valid rows of this warp
+                Out *out = static_cast<Out *>(g.out);
+                const bool aligned = ((reinterpret_cast<uintptr_t>(out) | (uint64_t)g.ldo * sizeof(Out)) & 15u) == 0;
+                uint8_t *mine = staging + (warp - 4) * kStaging;
+                const int64_t first = t.row0 + (int)rank * 128 + q * 32;
+                const int left = min(t.rows - (int)rank * 128 - q * 32, 32);   // valid rows of this warp
 #pragma unroll
-                    for (int c = 0; c < 2 * kRun; c += 8 * kWord) {
+                for (int c = 0; c < 2 * kRun; c += kPass) {
+                    if (c0 + c >= g.N) break;
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const float *v = acc + c + i * kWord;
-                            uint4 w;
-                            if constexpr (EPI == BLOCK_F32) {
-                                w = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
-                                               __float_as_uint(v[3]));
-                            } else {
-                                w = make_uint4(bf16x2(v[0], v[1]), bf16x2(v[2], v[3]), bf16x2(v[4], v[5]),
-                                               bf16x2(v[6], v[7]));
-                            }
-                            *reinterpret_cast<uint4 *>(mine + lane * 128 + (i ^ (lane & 7)) * 16) = w;
+                    for (int i = 0; i < 8; ++i) {
+                        const float *v = acc + c + i * kWord;
+                        uint4 w;
+                        if constexpr (EPI == BLOCK_F32) {
+                            w = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
+                                           __float_as_uint(v[3]));
+                        } else {
+                            w = make_uint4(bf16x2(v[0], v[1]), bf16x2(v[2], v[3]), bf16x2(v[4], v[5]),
+                                           bf16x2(v[6], v[7]));
                         }
-                        __syncwarp();
+                        *reinterpret_cast<uint4 *>(mine + lane * 128 + (i ^ (lane & 7)) * 16) = w;
+                    }
+                    __syncwarp();
+                    if (aligned && c0 + c + kPass <= g.N) {
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
                             const int rr = i * 4 + lane / 8;
                             const uint4 w =
                                 *reinterpret_cast<const uint4 *>(mine + rr * 128 + ((lane & 7) ^ (rr & 7)) * 16);
                             if (rr < left)
-                                *reinterpret_cast<uint4 *>(
-                                    out + ((first + rr) * g.ldo + c0 + c + (lane & 7) * kWord) * kSize) = w;
+                                *reinterpret_cast<uint4 *>(out + (first + rr) * g.ldo + c0 + c + (lane & 7) * kWord) = w;
                         }
-                        __syncwarp();
-                    }
-                } else if (row_ok) {
+                    } else {   // rows that start anywhere, or end inside: neighbouring columns by neighbouring lanes
+                        for (int rr = 0; rr < left; ++rr)
 #pragma unroll
-                    for (int i = 0; i < 2 * kRun; ++i) {
-                        if (c0 + i >= g.N) continue;
-                        if constexpr (EPI == BLOCK_F32)
-                            static_cast<float *>(g.out)[r * g.ldo + c0 + i] = acc[i];
-                        else
-                            static_cast<uint16_t *>(g.out)[r * g.ldo + c0 + i] = f32_to_bf16_bits(acc[i]);
+                            for (int j = lane; j < kPass; j += 32)
+                                if (c0 + c + j < g.N)
+                                    out[(first + rr) * g.ldo + c0 + c + j] = *reinterpret_cast<const Out *>(
+                                        mine + rr * 128 + ((j / kWord) ^ (rr & 7)) * 16 + j % kWord * sizeof(Out));
                     }
+                    __syncwarp();
                 }
             }
         }

@@ -98,7 +98,7 @@ struct BlockGemm {
     uint32_t *err;
 };
 
-// Tensor-core kernel for token tiles of 16, 32, 64 or 128 rows (weights on the 128-row side).
+// Tensor-core kernel for token tiles of 16, 32 or (not SWIGLU) 64 rows (weights on the 128-row side).
 mse_status launch_block_cols(const BlockGemm &g, int sm_count, bool pdl, cudaStream_t s);
 // Tensor-core kernel for token tiles of 256 rows (a CTA pair per 256 x 256 tile).
 mse_status launch_block_pair(const BlockGemm &g, int sm_count, bool pdl, cudaStream_t s);

@@ -41,9 +41,23 @@ mse_status check_matmul(const void *xq, int64_t ldx, const void *xs, const void 
     return capacity < T * N ? MSE_ERR_GEOMETRY : MSE_OK;
 }
 
-// Token rows of a tile, from the rows expected of a group: up to 128 the least power of two that
-// holds them (swap-AB kernel), above that 256 (CTA-pair kernel).
-int tile_rows_for(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : rows <= 256 ? 128 : 256; }
+// Token rows of a tile: 16, 32 and 64 take the swap-AB kernel, 256 the CTA-pair kernel.
+//
+// Plain product.  A CTA pair spends 0.41 us on a k-block of 256 x 256 and there are half as many pairs as
+// SMs; two swap-AB CTAs on an SM spend 0.54 us on a k-block of 128 x 64 each, and split tiles over
+// more CTAs when there are fewer tiles than SMs.  So the pair wins from two waves of swap-AB tiles
+// on, when its own waves are at most two thirds of theirs (us, pair and swap-AB: 256 x 7168 x 6144 23.2 and 26.3,
+// 128 x 12288 x 7168 26.6 and 29.7; 128 x 7168 x 6144 23.1 and 21.5, 512 x 2112 x 7168 25.7 and 23.5).
+int plain_tile_rows(int64_t T, int64_t N, int sm_count) {
+    if (T <= 32) return T <= 16 ? 16 : 32;
+    const int64_t cols = blocks_of(N) * ((T + 63) / 64), pairs = ((T + 255) / 256) * ((N + 255) / 256);
+    const int64_t cols_waves = (cols + sm_count - 1) / sm_count, pair_waves = (pairs + sm_count / 2 - 1) / (sm_count / 2);
+    return cols_waves >= 2 && 2 * cols_waves >= 3 * pair_waves ? 256 : 64;
+}
+// Experts, by the rows expected of each (32 experts of 7168 x 2048, us with tiles of 16, 32 and 256: 8 rows
+// 219, 232, 308; 16 rows 240, 250, 311; 32 rows 305, 278, 319; 48 rows 403, 351, 330; 64 rows 497, 417, 335;
+// tiles of 64 and 128 were never the fastest).
+int expert_tile_rows(int64_t rows) { return rows <= 16 ? 16 : rows <= 40 ? 32 : 256; }
 
 mse_status run_product(BlockGemm g, bool tensorcore, const DeviceView &d, cudaStream_t s) {
     g.wait_limit_ns = wait_limit_ns();
@@ -54,11 +68,11 @@ mse_status run_product(BlockGemm g, bool tensorcore, const DeviceView &d, cudaSt
 }
 
 BlockGemm plain_product(const uint8_t *xq, int64_t ldx, const float *xs, const uint8_t *wq, int64_t ldw,
-                        const float *ws, int64_t T, int64_t N, int64_t K, void *out, mse_dtype dtype) {
+                        const float *ws, int64_t T, int64_t N, int64_t K, void *out, mse_dtype dtype, int sm_count) {
     BlockGemm g;
     std::memset(&g, 0, sizeof g);
     g.T = T;
-    g.tile_rows = tile_rows_for(T);
+    g.tile_rows = plain_tile_rows(T, N, sm_count);
     g.xq = xq; g.ldx = ldx; g.xs = xs;
     g.wq = wq; g.ldw = ldw; g.ws = ws;
     g.N = N; g.K = K; g.kb = (int)blocks_of(K);
@@ -163,7 +177,7 @@ mse_status fp8_block_matmul(const uint8_t *xq, int64_t ldx, const float *xs, con
     bool tensorcore = false;
     if ((st = choose_tensorcore(tc_operands(xq, ldx, wq, ldw), &tensorcore)) != MSE_OK) return st;
     begin_untracked_call(stream);
-    return run_product(plain_product(xq, ldx, xs, wq, ldw, ws, T, N, K, out, out_dtype), tensorcore, d,
+    return run_product(plain_product(xq, ldx, xs, wq, ldw, ws, T, N, K, out, out_dtype, d.sm_count), tensorcore, d,
                        static_cast<cudaStream_t>(stream));
 }
 
@@ -190,7 +204,7 @@ mse_status fp8_block_linear(const mse_bf16 *x, int64_t ldx, const uint8_t *wq, i
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if ((st = from_cuda(launch_quantise_rows(x, T, K, ldx, xq, ldq, xs, d.sm_count, pdl_enabled(), s))) != MSE_OK)
         return st;
-    BlockGemm g = plain_product(xq, ldq, xs, wq, ldw, ws, T, N, K, y, y_dtype);
+    BlockGemm g = plain_product(xq, ldq, xs, wq, ldw, ws, T, N, K, y, y_dtype, d.sm_count);
     g.weights_early = 1;
     return run_product(g, tensorcore, d, s);
 }
@@ -239,7 +253,7 @@ mse_status moe_experts_forward(const mse_bf16 *x, int64_t T, int64_t H, const in
     dp.pos = reinterpret_cast<int32_t *>(w + L.pos);
     dp.tiles = reinterpret_cast<Tile *>(w + L.tiles);
     dp.n_tiles = reinterpret_cast<int *>(w + L.n_tiles);
-    dp.tile_rows = tensorcore ? tile_rows_for(pairs / E) : kSimtTileRows;
+    dp.tile_rows = tensorcore ? expert_tile_rows(pairs / E) : kSimtTileRows;
     dp.xq = w + L.xq; dp.ldq = pad16(H);
     dp.xs = reinterpret_cast<float *>(w + L.xs);
     if ((st = from_cuda(launch_dispatch(dp, pdl, s))) != MSE_OK) return st;

@@ -12,11 +12,20 @@ import moe_shared_expert_gb300 as _mse
 
 _BLOCK = 128
 _SCORING = {"softmax": 0, "sigmoid": 1}
+torch = None   # set by _load(); the package itself imports without it
 
 
-def _torch():
-    import torch
-    return torch
+def _load():
+    """torch, the library's functions and the dtypes, looked up once: a call's own Python is most of what a
+    single token's operators cost."""
+    global torch, _C, _BF16, _F32, _E4M3, _raw_stream
+    import torch as _torch
+    _C = _mse.lib()
+    _BF16, _F32, _E4M3 = _torch.bfloat16, _torch.float32, (_torch.float8_e4m3fn, _torch.uint8)
+    # the current stream's handle without making a Stream object, where this torch has it
+    _raw_stream = getattr(_torch._C, "_cuda_getCurrentRawStream", None) or (
+        lambda index: _torch.cuda.current_stream(index).cuda_stream)
+    torch = _torch
 
 
 def _blocks(n: int) -> int:
@@ -27,42 +36,43 @@ def _pad16(n: int) -> int:
     return -(-n // 16) * 16
 
 
+def _said(t):
+    return "None" if t is None else f"{t.dtype} {tuple(t.shape)}, strides {t.stride()}, on {t.device}"
+
+
 def _rows(t, name, dtypes, ndim):
-    """A CUDA tensor whose last dimension is contiguous, and whose leading ones make rows of one pitch."""
+    """The pitch of the rows of a CUDA tensor whose last dimension is contiguous and whose matrices follow one another."""
     if t is None or not t.is_cuda or t.dtype not in dtypes or t.dim() != ndim:
-        raise ValueError(f"{name}: need a {ndim}-d CUDA tensor of {dtypes}, got "
-                         + ("None" if t is None else f"{t.dtype} {tuple(t.shape)} on {t.device}"))
+        raise ValueError(f"{name}: need a {ndim}-d CUDA tensor of {dtypes}, got {_said(t)}")
     shape, stride = t.shape, t.stride()
-    if shape[-1] > 1 and stride[-1] != 1:
-        raise ValueError(f"{name}: the last dimension has to be contiguous, got strides {stride}")
-    ld = stride[-2] if shape[-2] > 1 else max(shape[-1], stride[-2])
-    if ld < shape[-1] or (ndim == 3 and shape[0] > 1 and stride[0] != shape[1] * ld):
-        raise ValueError(f"{name}: rows of one pitch are needed, got shape {tuple(shape)}, strides {stride}")
+    cols = shape[-1]
+    ld = stride[-2] if shape[-2] > 1 else max(cols, stride[-2])
+    if (cols > 1 and stride[-1] != 1) or ld < cols or (ndim == 3 and shape[0] > 1 and stride[0] != shape[1] * ld):
+        raise ValueError(f"{name}: contiguous rows of one pitch are needed, got {_said(t)}")
     return ld
 
 
 def _dense(t, name, dtype, shape):
-    if t is None or not t.is_cuda or t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
-        raise ValueError(f"{name}: need a contiguous CUDA tensor of {dtype} {tuple(shape)}, got "
-                         + ("None" if t is None else f"{t.dtype} {tuple(t.shape)} on {t.device}"))
-    return t
+    if t is None or t.dtype is not dtype or t.shape != shape or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name}: need a contiguous CUDA tensor of {dtype} {tuple(shape)}, got {_said(t)}")
 
 
-def _e4m3():
-    torch = _torch()
-    return (torch.float8_e4m3fn, torch.uint8)
+def _handle(stream, t):
+    """cudaStream_t of `stream`, or of the current stream of t's device."""
+    if stream is None:
+        return _raw_stream(t.device.index)
+    return stream if isinstance(stream, int) else stream.cuda_stream
 
 
 def _own_stream(t, stream):
     """Memory allocated here for a call on another stream than the current one stays taken until that call is done."""
     if stream is not None:
-        torch = _torch()
         t.record_stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
     return t
 
 
 def _empty(stream, shape, dtype, device):
-    return _own_stream(_torch().empty(shape, dtype=dtype, device=device), stream)
+    return _own_stream(torch.empty(shape, dtype=dtype, device=device), stream)
 
 
 # ---------------------------------------------------------------------------------------
@@ -75,23 +85,27 @@ def moe_route(logits, top_k, scoring="sigmoid", bias=None, n_group=1, topk_group
 
     Experts are chosen by score + bias, best first, ties to the lower index; -inf, a type's lowest value and NaN
     close an expert.  Slots for which no expert is left hold id -1 and weight 0."""
-    torch = _torch()
-    ld = _rows(logits, "logits", (torch.bfloat16, torch.float32), 2)
+    if torch is None:
+        _load()
+    ld = _rows(logits, "logits", (_BF16, _F32), 2)
     T, E = logits.shape
     if scoring not in _SCORING:
         raise ValueError(f"scoring must be one of {sorted(_SCORING)}, got {scoring!r}")
     if bias is not None:
-        _dense(bias, "bias", torch.float32, (E,))
+        _dense(bias, "bias", _F32, (E,))
     if ids is None:
         ids = _empty(stream, (T, max(top_k, 0)), torch.int32, logits.device)
+    else:
+        _dense(ids, "ids", torch.int32, (T, top_k))
     if weights is None:
-        weights = _empty(stream, (T, max(top_k, 0)), torch.float32, logits.device)
-    _dense(ids, "ids", torch.int32, (T, top_k))
-    _dense(weights, "weights", torch.float32, (T, top_k))
-    st = _mse.lib().moe_route(logits.data_ptr(), _mse._dtype_code(logits.dtype), T, E, ld, _mse._ptr(bias),
-                              _SCORING[scoring], n_group, topk_group, group_top, top_k, int(bool(renormalise)),
-                              scale, ids.data_ptr(), weights.data_ptr(), ids.numel(), _mse._stream(stream))
-    _mse._check("moe_route", st)
+        weights = _empty(stream, (T, max(top_k, 0)), _F32, logits.device)
+    else:
+        _dense(weights, "weights", _F32, (T, top_k))
+    st = _C.moe_route(logits.data_ptr(), int(logits.dtype is _F32), T, E, ld, None if bias is None else bias.data_ptr(),
+                      _SCORING[scoring], n_group, topk_group, group_top, top_k, 1 if renormalise else 0, scale,
+                      ids.data_ptr(), weights.data_ptr(), T * top_k, _handle(stream, logits))
+    if st:
+        _mse._check("moe_route", st)
     return ids, weights
 
 
@@ -104,38 +118,49 @@ def fp8_block_quantise(x, block_rows=1, stream=None):
 
     q has x's shape and rows of a pitch of 16 bytes; scales is [.., ceil(rows / block_rows), ceil(K / 128)] fp32.
     A merged gate_up weight [E, 2I, H] is rounded as its halves, [2E, I, H], so that each half has its own blocks."""
-    torch = _torch()
+    if torch is None:
+        _load()
     if x is None or x.dim() not in (2, 3):
-        raise ValueError("x: need a 2-d or 3-d tensor")
-    _rows(x, "x", (torch.bfloat16,), x.dim())
+        raise ValueError(f"x: need a 2-d or 3-d tensor, got {_said(x)}")
+    ld = _rows(x, "x", (_BF16,), x.dim())
     *lead, rows, K = x.shape
-    q = _empty(stream, (*lead, rows, _pad16(K)), torch.uint8, x.device)
-    scales = _empty(stream, (*lead, _blocks(rows) if block_rows != 1 else rows, _blocks(K)), torch.float32, x.device)
-    for xm, qm, sm in [(x, q, scales)] if x.dim() == 2 else zip(x, q, scales):
-        st = _mse.lib().fp8_block_quantise(xm.data_ptr(), rows, K, _rows(xm, "x", (torch.bfloat16,), 2), block_rows,
-                                           qm.data_ptr(), qm.stride(0), qm.numel(), sm.data_ptr(), sm.numel(),
-                                           _mse._stream(stream))
-        _mse._check("fp8_block_quantise", st)
+    pitch, srows, kb = _pad16(K), rows if block_rows == 1 else _blocks(rows), _blocks(K)
+    q = _empty(stream, (*lead, rows, pitch), torch.uint8, x.device)
+    scales = _empty(stream, (*lead, srows, kb), _F32, x.device)
+    for i in range(lead[0] if lead else 1):
+        st = _C.fp8_block_quantise(x.data_ptr() + 2 * i * rows * ld, rows, K, ld, block_rows,
+                                   q.data_ptr() + i * rows * pitch, pitch, rows * pitch,
+                                   scales.data_ptr() + 4 * i * srows * kb, srows * kb, _handle(stream, x))
+        if st:
+            _mse._check("fp8_block_quantise", st)
     return q.view(torch.float8_e4m3fn)[..., :K], scales
+
+
+def _out(out, dtype, name, shape, like, stream):
+    """The output tensor of a product and its type's code."""
+    code = _mse._dtype_code(dtype if dtype is not None else _BF16 if out is None else out.dtype)
+    dtype = _F32 if code else _BF16
+    if out is None:
+        return _empty(stream, shape, dtype, like.device), code
+    _dense(out, name, dtype, shape)
+    return out, code
 
 
 def fp8_block_matmul(xq, xs, wq, ws, out_dtype=None, out=None, stream=None):
     """out [T, N] = xq wq^T with block scales; xq [T, K], xs [T, K / 128], wq [N, K], ws [N / 128, K / 128]."""
-    torch = _torch()
-    ldx, ldw = _rows(xq, "xq", _e4m3(), 2), _rows(wq, "wq", _e4m3(), 2)
-    (T, K), N = xq.shape, wq.shape[0]
-    if wq.shape[1] != K:
-        raise ValueError(f"xq and wq differ in K: {K} and {wq.shape[1]}")
-    _dense(xs, "xs", torch.float32, (T, _blocks(K)))
-    _dense(ws, "ws", torch.float32, (_blocks(N), _blocks(K)))
-    code = _mse._dtype_code(out_dtype if out_dtype is not None else torch.bfloat16 if out is None else out.dtype)
-    dtype = torch.float32 if code == _mse.F32 else torch.bfloat16
-    if out is None:
-        out = _empty(stream, (T, N), dtype, xq.device)
-    _dense(out, "out", dtype, (T, N))
-    st = _mse.lib().fp8_block_matmul(xq.data_ptr(), ldx, xs.data_ptr(), wq.data_ptr(), ldw, ws.data_ptr(), T, N, K,
-                                     out.data_ptr(), code, out.numel(), _mse._stream(stream))
-    _mse._check("fp8_block_matmul", st)
+    if torch is None:
+        _load()
+    ldx, ldw = _rows(xq, "xq", _E4M3, 2), _rows(wq, "wq", _E4M3, 2)
+    (T, K), (N, Kw) = xq.shape, wq.shape
+    if K != Kw:
+        raise ValueError(f"xq and wq differ in K: {K} and {Kw}")
+    _dense(xs, "xs", _F32, (T, _blocks(K)))
+    _dense(ws, "ws", _F32, (_blocks(N), _blocks(K)))
+    out, code = _out(out, out_dtype, "out", (T, N), xq, stream)
+    st = _C.fp8_block_matmul(xq.data_ptr(), ldx, xs.data_ptr(), wq.data_ptr(), ldw, ws.data_ptr(), T, N, K,
+                             out.data_ptr(), code, T * N, _handle(stream, xq))
+    if st:
+        _mse._check("fp8_block_matmul", st)
     return out
 
 
@@ -143,30 +168,33 @@ def fp8_linear_workspace_bytes(T: int, N: int, K: int) -> int:
     return int(_mse.lib().fp8_block_linear_workspace_bytes(T, N, K))
 
 
+def _new_workspace(nbytes, device):
+    if torch is None:
+        _load()
+    return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
+
+
 def new_fp8_linear_workspace(T: int, N: int, K: int, device="cuda"):
     """A workspace for fp8_block_linear with up to T tokens."""
-    return _torch().empty(max(fp8_linear_workspace_bytes(T, N, K), 256), dtype=_torch().uint8, device=device)
+    return _new_workspace(fp8_linear_workspace_bytes(T, N, K), device)
 
 
 def fp8_block_linear(x, wq, ws, y_dtype=None, y=None, workspace=None, stream=None):
     """y [T, N] = x wq^T: x [T, K] bf16 is rounded to e4m3 in blocks of 1 x 128, wq and ws as in fp8_block_matmul."""
-    torch = _torch()
-    ldx, ldw = _rows(x, "x", (torch.bfloat16,), 2), _rows(wq, "wq", _e4m3(), 2)
-    (T, K), N = x.shape, wq.shape[0]
-    if wq.shape[1] != K:
-        raise ValueError(f"x and wq differ in K: {K} and {wq.shape[1]}")
-    _dense(ws, "ws", torch.float32, (_blocks(N), _blocks(K)))
-    code = _mse._dtype_code(y_dtype if y_dtype is not None else torch.bfloat16 if y is None else y.dtype)
-    dtype = torch.float32 if code == _mse.F32 else torch.bfloat16
-    if y is None:
-        y = _empty(stream, (T, N), dtype, x.device)
-    _dense(y, "y", dtype, (T, N))
+    if torch is None:
+        _load()
+    ldx, ldw = _rows(x, "x", (_BF16,), 2), _rows(wq, "wq", _E4M3, 2)
+    (T, K), (N, Kw) = x.shape, wq.shape
+    if K != Kw:
+        raise ValueError(f"x and wq differ in K: {K} and {Kw}")
+    _dense(ws, "ws", _F32, (_blocks(N), _blocks(K)))
+    y, code = _out(y, y_dtype, "y", (T, N), x, stream)
     if workspace is None:
         workspace = _own_stream(new_fp8_linear_workspace(T, N, K, x.device), stream)
-    st = _mse.lib().fp8_block_linear(x.data_ptr(), ldx, wq.data_ptr(), ldw, ws.data_ptr(), T, N, K, y.data_ptr(),
-                                     code, y.numel(), workspace.data_ptr(),
-                                     workspace.numel() * workspace.element_size(), _mse._stream(stream))
-    _mse._check("fp8_block_linear", st)
+    st = _C.fp8_block_linear(x.data_ptr(), ldx, wq.data_ptr(), ldw, ws.data_ptr(), T, N, K, y.data_ptr(), code, T * N,
+                             workspace.data_ptr(), workspace.nbytes, _handle(stream, x))
+    if st:
+        _mse._check("fp8_block_linear", st)
     return y
 
 
@@ -180,7 +208,7 @@ def moe_workspace_bytes(T: int, top_k: int, E: int, H: int, I: int) -> int:
 
 def new_moe_workspace(T: int, top_k: int, E: int, H: int, I: int, device="cuda"):
     """A workspace for moe_experts_forward with up to T tokens."""
-    return _torch().empty(max(moe_workspace_bytes(T, top_k, E, H, I), 256), dtype=_torch().uint8, device=device)
+    return _new_workspace(moe_workspace_bytes(T, top_k, E, H, I), device)
 
 
 def moe_experts_forward(x, ids, weights, w_gate_up, s_gate_up, w_down, s_down, first_expert=0, shared=None, y=None,
@@ -191,30 +219,33 @@ def moe_experts_forward(x, ids, weights, w_gate_up, s_gate_up, w_down, s_down, f
     e4m3 with s_gate_up [E, 2 ceil(I / 128), ceil(H / 128)] (gate's blocks, then up's) and s_down
     [E, ceil(H / 128), ceil(I / 128)].  The rank holds experts first_expert .. first_expert + E - 1; pairs of other
     experts, and ids of -1, add nothing."""
-    torch = _torch()
-    _dense(x, "x", torch.bfloat16, x.shape if x is not None and x.dim() == 2 else (-1, -1))
-    T, H = x.shape
-    ld_gu, ld_dn = _rows(w_gate_up, "w_gate_up", _e4m3(), 3), _rows(w_down, "w_down", _e4m3(), 3)
-    E, I = w_down.shape[0], w_down.shape[2]
-    if tuple(w_gate_up.shape) != (E, 2 * I, H) or w_down.shape[1] != H:
-        raise ValueError(f"w_gate_up {tuple(w_gate_up.shape)} and w_down {tuple(w_down.shape)} do not fit x "
-                         f"{tuple(x.shape)}")
-    _dense(s_gate_up, "s_gate_up", torch.float32, (E, 2 * _blocks(I), _blocks(H)))
-    _dense(s_down, "s_down", torch.float32, (E, _blocks(H), _blocks(I)))
-    k = ids.shape[1] if ids is not None and ids.dim() == 2 else -1
+    if torch is None:
+        _load()
+    ld_gu, ld_dn = _rows(w_gate_up, "w_gate_up", _E4M3, 3), _rows(w_down, "w_down", _E4M3, 3)
+    E, H, I = w_down.shape
+    if w_gate_up.shape != (E, 2 * I, H):
+        raise ValueError(f"w_gate_up {tuple(w_gate_up.shape)} does not fit w_down {tuple(w_down.shape)}")
+    if x is None or ids is None or x.dim() != 2 or ids.dim() != 2:
+        raise ValueError(f"x and ids: need 2-d tensors, got {_said(x)} and {_said(ids)}")
+    T, k = ids.shape
+    hb, ib = _blocks(H), _blocks(I)
+    _dense(x, "x", _BF16, (T, H))
     _dense(ids, "ids", torch.int32, (T, k))
-    _dense(weights, "weights", torch.float32, (T, k))
+    _dense(weights, "weights", _F32, (T, k))
+    _dense(s_gate_up, "s_gate_up", _F32, (E, 2 * ib, hb))
+    _dense(s_down, "s_down", _F32, (E, hb, ib))
     if shared is not None:
-        _dense(shared, "shared", torch.bfloat16, (T, H))
+        _dense(shared, "shared", _BF16, (T, H))
     if y is None:
-        y = _empty(stream, (T, H), torch.bfloat16, x.device)
-    _dense(y, "y", torch.bfloat16, (T, H))
+        y = _empty(stream, (T, H), _BF16, x.device)
+    else:
+        _dense(y, "y", _BF16, (T, H))
     if workspace is None:
         workspace = _own_stream(new_moe_workspace(T, k, E, H, I, x.device), stream)
-    st = _mse.lib().moe_experts_forward(x.data_ptr(), T, H, ids.data_ptr(), weights.data_ptr(), k,
-                                        w_gate_up.data_ptr(), ld_gu, s_gate_up.data_ptr(), w_down.data_ptr(), ld_dn,
-                                        s_down.data_ptr(), E, I, first_expert, _mse._ptr(shared), y.data_ptr(),
-                                        y.numel(), workspace.data_ptr(),
-                                        workspace.numel() * workspace.element_size(), _mse._stream(stream))
-    _mse._check("moe_experts_forward", st)
+    st = _C.moe_experts_forward(x.data_ptr(), T, H, ids.data_ptr(), weights.data_ptr(), k, w_gate_up.data_ptr(), ld_gu,
+                                s_gate_up.data_ptr(), w_down.data_ptr(), ld_dn, s_down.data_ptr(), E, I, first_expert,
+                                None if shared is None else shared.data_ptr(), y.data_ptr(), T * H,
+                                workspace.data_ptr(), workspace.nbytes, _handle(stream, x))
+    if st:
+        _mse._check("moe_experts_forward", st)
     return y

@@ -1,7 +1,10 @@
 // Routing of tokens to experts: scores, groups, the best top_k, their weights.
 //
 // One warp per token; lane l holds experts l, l + 32, ... in registers.  Everything after the
-// one read of the logits stays in the warp.
+// one read of the logits stays in the warp.  The top_k-th largest of the 32 lanes' best keys bounds
+// the top_k-th best key from below; the few keys that reach it are gathered, and each counts the
+// ones before it: its rank is its place.  (Only where more than 32 reach it, by ties, is the best
+// key drawn top_k times.)  What bounds it is the instructions of a warp, not the logits' bytes.
 #include "common.cuh"
 #include "launch.h"
 #include "routed.h"
@@ -34,7 +37,7 @@ __device__ __forceinline__ float load_logit(const RouteParams &p, int64_t i) {
 // groups read different banks.
 __device__ __forceinline__ uint32_t best_groups(const RouteParams &p, const uint32_t *keys, int pitch, int lanes,
                                                 int lane) {
-    const int g = lane / lanes, r = lane % lanes;
+    const int g = lane >> (31 - __clz(lanes)), r = lane & (lanes - 1);   // lanes: a power of two
     uint32_t k1 = 0, k2 = 0;   // the two best keys of the group
     if (g < p.n_group) {
         for (int i = r; i < p.group_size; i += lanes) {
@@ -59,11 +62,23 @@ __device__ __forceinline__ uint32_t best_groups(const RouteParams &p, const uint
     return kept;   // bit g * lanes: group g stays
 }
 
+// a / b to nearest, with inv = 1 / b to nearest: one residual step makes the product exact to the last
+// bit (Markstein); tiny quotients, whose residual could be cut off, take the division itself.
+__device__ __forceinline__ float quotient(float a, float b, float inv) {
+    if (a < 1e-30f) return __fdiv_rn(a, b);
+    const float q = __fmul_rn(a, inv);
+    return fmaf(fmaf(-b, q, a), inv, q);
+}
+
 template <int VPL>
 __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RouteParams p) {
     extern __shared__ uint32_t route_smem[];
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int64_t t = (int64_t)blockIdx.x * (blockDim.x / 32) + warp;
+    // keys and scores of up to 32 candidates, then (groups) the keys of all experts
+    uint32_t *mine = route_smem + (size_t)warp * p.smem_words;
+    uint32_t *cand_key = mine, *cand_id = mine + 32, *all_keys = mine + 96;
+    float *cand_score = reinterpret_cast<float *>(mine + 64);
     pdl_wait();
     if (t >= p.T) return;
     float score[VPL];
@@ -72,15 +87,18 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RoutePara
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
         const int e = i * 32 + lane;
-        const float l = e < p.E ? load_logit(p, t * p.ld + e) : -INFINITY;
-        const bool open = l > kClosedFrom;
+        score[i] = e < p.E ? load_logit(p, t * p.ld + e) : -INFINITY;
+    }
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+        const bool open = score[i] > kClosedFrom;
         key[i] = open ? 1u : 0u;
-        score[i] = open ? l : -INFINITY;
+        score[i] = open ? score[i] : -INFINITY;
         top = fmaxf(top, score[i]);
     }
     if (p.sigmoid) {
 #pragma unroll
-        for (int i = 0; i < VPL; ++i) score[i] = __fdiv_rn(1.0f, __fadd_rn(1.0f, expf(-score[i])));
+        for (int i = 0; i < VPL; ++i) score[i] = __frcp_rn(__fadd_rn(1.0f, expf(-score[i])));
     } else {
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
@@ -100,52 +118,97 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RoutePara
             high += __shfl_xor_sync(~0u, high, d);
             low += __shfl_xor_sync(~0u, low, d);
         }
-        const float sum = fmaxf(__fadd_rn(high, low), 1e-30f);
+        const float sum = fmaxf(__fadd_rn(high, low), 1e-30f), inv = __frcp_rn(sum);
 #pragma unroll
-        for (int i = 0; i < VPL; ++i) score[i] = __fdiv_rn(score[i], sum);
+        for (int i = 0; i < VPL; ++i) score[i] = quotient(score[i], sum, inv);
     }
-    float *my_score = reinterpret_cast<float *>(route_smem) + (size_t)warp * p.E;
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
         const int e = i * 32 + lane;
-        if (e >= p.E) break;
-        my_score[e] = score[i];
         if (key[i]) key[i] = float_key(p.bias ? __fadd_rn(score[i], p.bias[e]) : score[i]);
     }
     if (p.n_group > 1) {
-        const int lanes = p.n_group > 16 ? 1 : p.n_group > 8 ? 2 : p.n_group > 4 ? 4 : p.n_group > 2 ? 8 : 16;
-        const int pitch = p.group_size + lanes;
-        uint32_t *my_key = route_smem + (size_t)(blockDim.x / 32) * p.E + (size_t)warp * p.n_group * pitch;
+        const int lanes = p.group_lanes, pitch = p.group_size + lanes;
+        int bit[VPL];   // of the expert's group in `kept`
 #pragma unroll
         for (int i = 0; i < VPL; ++i) {
             const int e = i * 32 + lane;
-            if (e < p.E) my_key[e / p.group_size * pitch + e % p.group_size] = key[i];
+            const int g = (int)((uint32_t)e * (uint32_t)p.group_magic >> 20);   // e / group_size
+            bit[i] = g * lanes;
+            if (e < p.E) all_keys[g * lanes + e] = key[i];                      // g * pitch + e % group_size
         }
         __syncwarp();
-        const uint32_t kept = best_groups(p, my_key, pitch, lanes, lane);
+        const uint32_t kept = best_groups(p, all_keys, pitch, lanes, lane);
 #pragma unroll
-        for (int i = 0; i < VPL; ++i) {
-            const int e = i * 32 + lane;
-            if (e < p.E && !((kept >> (e / p.group_size * lanes)) & 1u)) key[i] = 0;
+        for (int i = 0; i < VPL; ++i)
+            if (!((kept >> (bit[i] & 31)) & 1u)) key[i] = 0;
+    }
+    // lower bound of the top_k-th best key: as many lanes hold one at least as large
+    uint32_t lane_best = 0;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) lane_best = max(lane_best, key[i]);
+    uint32_t bound = 0;
+    for (int j = 0; j < p.top_k; ++j) {
+        bound = __reduce_max_sync(~0u, lane_best);
+        if (bound == 0) break;
+        const uint32_t holders = __ballot_sync(~0u, lane_best == bound);
+        if (lane == __ffs(holders) - 1) lane_best = 0;
+    }
+    bound = max(bound, 1u);   // fewer lanes than top_k: every open key
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+        const bool in = key[i] >= bound;
+        const uint32_t who = __ballot_sync(~0u, in);
+        const int at = n + __popc(who & ((1u << lane) - 1u));
+        if (in && at < 32) {
+            cand_key[at] = key[i];
+            cand_id[at] = i * 32 + lane;
+            cand_score[at] = score[i];
         }
+        n += __popc(who);
     }
     __syncwarp();
     int id = -1;   // lane j: the j-th best
-    for (int j = 0; j < p.top_k; ++j) {
-        uint32_t best = 0;
-        int at = 0;
+    float w = 0.f;
+    if (n <= 32) {
+        const uint32_t k = lane < n ? cand_key[lane] : 0u;
+        const int e = lane < n ? (int)cand_id[lane] : 0;
+        const float sc = lane < n ? cand_score[lane] : 0.f;
+        int rank = 0;   // candidates lie in the order of their experts, chunk by chunk of 32
+        for (int j = 0; j < n; ++j) {
+            const uint32_t ko = __shfl_sync(~0u, k, j);
+            const int eo = __shfl_sync(~0u, e, j);
+            rank += (ko > k || (ko == k && eo < e)) ? 1 : 0;
+        }
+        __syncwarp();
+        if (lane < n) {   // every candidate to its place
+            cand_id[rank] = (uint32_t)e;
+            cand_score[rank] = sc;
+        }
+        __syncwarp();
+        if (lane < n && lane < p.top_k) {
+            id = (int)cand_id[lane];
+            w = cand_score[lane];
+        }
+    } else {
+        for (int j = 0; j < p.top_k; ++j) {
+            uint32_t best = 0;
+            int at = 0;
 #pragma unroll
-        for (int i = 0; i < VPL; ++i)
-            if (key[i] > best) { best = key[i]; at = i; }
-        const uint32_t m = __reduce_max_sync(~0u, best);
-        if (m == 0) break;
-        const uint32_t e = __reduce_min_sync(~0u, best == m ? (uint32_t)(at * 32 + lane) : ~0u);
-        if (lane == j) id = (int)e;
+            for (int i = 0; i < VPL; ++i)
+                if (key[i] > best) { best = key[i]; at = i; }
+            const uint32_t m = __reduce_max_sync(~0u, best);
+            if (m == 0) break;
+            const uint32_t e = __reduce_min_sync(~0u, best == m ? (uint32_t)(at * 32 + lane) : ~0u);
+            float sc = 0.f;
 #pragma unroll
-        for (int i = 0; i < VPL; ++i)
-            if ((uint32_t)(i * 32 + lane) == e) key[i] = 0;
+            for (int i = 0; i < VPL; ++i)
+                if ((uint32_t)(i * 32 + lane) == e) { key[i] = 0; sc = score[i]; }
+            sc = __shfl_sync(~0u, sc, e % 32);
+            if (lane == j) { id = (int)e; w = sc; }
+        }
     }
-    float w = id >= 0 ? my_score[id] : 0.f;
     if (p.renormalise) {
         float total = w;
 #pragma unroll
@@ -159,17 +222,13 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RoutePara
 }
 
 template <int VPL>
-cudaError_t launch_vpl(const RouteParams &p, bool pdl, cudaStream_t s) {
+cudaError_t launch_vpl(RouteParams p, bool pdl, cudaStream_t s) {
     // a few tokens: one warp per CTA, so that they run on as many SMs
     const int warps = p.T >= 1024 ? kRouteWarps : 1;
-    const int lanes = p.n_group > 16 ? 1 : p.n_group > 8 ? 2 : p.n_group > 4 ? 4 : p.n_group > 2 ? 8 : 16;
-    const size_t words = (size_t)p.E + (p.n_group > 1 ? (size_t)p.n_group * (p.group_size + lanes) : 0);
-    const size_t smem = words * 4 * warps;
-    if (smem > 48 * 1024) {
-        const cudaError_t e =
-            cudaFuncSetAttribute(route_kernel<VPL>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (e != cudaSuccess) return e;
-    }
+    p.group_lanes = p.n_group > 16 ? 1 : p.n_group > 8 ? 2 : p.n_group > 4 ? 4 : p.n_group > 2 ? 8 : 16;
+    p.group_magic = ((1 << 20) + p.group_size - 1) / p.group_size;   // exact for e < 1024
+    p.smem_words = 96 + (p.n_group > 1 ? p.n_group * (p.group_size + p.group_lanes) : 0);
+    const size_t smem = (size_t)p.smem_words * 4 * warps;
     return launch_kernel(route_kernel<VPL>, dim3((unsigned)((p.T + warps - 1) / warps)), warps * 32, smem, pdl, 1, s,
                          p);
 }
@@ -177,13 +236,19 @@ cudaError_t launch_vpl(const RouteParams &p, bool pdl, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_route(const RouteParams &p, bool pdl, cudaStream_t s) {
-    const int vpl = (p.E + 31) / 32;
-    if (vpl <= 1) return launch_vpl<1>(p, pdl, s);
-    if (vpl <= 2) return launch_vpl<2>(p, pdl, s);
-    if (vpl <= 4) return launch_vpl<4>(p, pdl, s);
-    if (vpl <= 8) return launch_vpl<8>(p, pdl, s);
-    if (vpl <= 16) return launch_vpl<16>(p, pdl, s);
-    return launch_vpl<32>(p, pdl, s);
+    switch ((p.E + 31) / 32) {
+        case 1: return launch_vpl<1>(p, pdl, s);
+        case 2: return launch_vpl<2>(p, pdl, s);
+        case 3: return launch_vpl<3>(p, pdl, s);
+        case 4: return launch_vpl<4>(p, pdl, s);
+        case 5: return launch_vpl<5>(p, pdl, s);
+        case 6: return launch_vpl<6>(p, pdl, s);
+        case 7: case 8: return launch_vpl<8>(p, pdl, s);
+        case 9: case 10: return launch_vpl<10>(p, pdl, s);
+        case 11: case 12: return launch_vpl<12>(p, pdl, s);
+        case 13: case 14: case 15: case 16: return launch_vpl<16>(p, pdl, s);
+        default: return launch_vpl<32>(p, pdl, s);
+    }
 }
 
 }  // namespace routed

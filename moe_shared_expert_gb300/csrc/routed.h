@@ -24,6 +24,7 @@ struct RouteParams {
     float scale;
     int32_t *ids;
     float *weights;
+    int group_lanes, group_magic, smem_words;   // filled in by launch_route
 };
 cudaError_t launch_route(const RouteParams &p, bool pdl, cudaStream_t s);
 

@@ -26,7 +26,7 @@ struct RouteParams {
     float *weights;
     int group_lanes, group_magic, smem_words;   // filled in by launch_route
 };
-cudaError_t launch_route(const RouteParams &p, bool pdl, cudaStream_t s);
+cudaError_t launch_route(const RouteParams &p, int sm_count, bool pdl, cudaStream_t s);
 
 // ------------------------------------------------------------------ rounding to 8 bits
 cudaError_t launch_quantise_rows(const uint16_t *x, int64_t rows, int64_t K, int64_t ldx, uint8_t *q, int64_t ldq,

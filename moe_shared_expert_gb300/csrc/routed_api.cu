@@ -146,7 +146,7 @@ mse_status moe_route(const void *logits, mse_dtype logits_dtype, int64_t T, int6
     p.n_group = n_group; p.group_size = (int)(E / n_group); p.topk_group = topk_group; p.group_top = group_top;
     p.top_k = top_k; p.renormalise = renormalise != 0; p.scale = scale;
     p.ids = ids; p.weights = weights;
-    return from_cuda(launch_route(p, pdl_enabled(), static_cast<cudaStream_t>(stream)));
+    return from_cuda(launch_route(p, d.sm_count, pdl_enabled(), static_cast<cudaStream_t>(stream)));
 }
 
 mse_status fp8_block_quantise(const mse_bf16 *x, int64_t rows, int64_t K, int64_t ldx, int block_rows, uint8_t *q,

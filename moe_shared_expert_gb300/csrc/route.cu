@@ -1,10 +1,15 @@
 // Routing of tokens to experts: scores, groups, the best top_k, their weights.
 //
 // One warp per token; lane l holds experts l, l + 32, ... in registers.  Everything after the
-// one read of the logits stays in the warp.  The top_k-th largest of the 32 lanes' best keys bounds
-// the top_k-th best key from below; the few keys that reach it are gathered, and each counts the
-// ones before it: its rank is its place.  (Only where more than 32 reach it, by ties, is the best
-// key drawn top_k times.)  What bounds it is the instructions of a warp, not the logits' bytes.
+// one read of the logits stays in the warp.  What bounds it is a warp's instructions, not the
+// logits' bytes, so the exact score (an accurate exponential and division) is computed for a few
+// experts only:
+//   - every expert gets its choice to about 2^-18 by the fast exponential and reciprocal;
+//   - the top_k-th largest of the 32 lanes' best ones bounds the top_k-th best from below, and
+//     the experts within twice the error of that bound, a few more than top_k, are gathered;
+//   - each of them gets its exact choice and counts the ones before it: its rank is its place.
+// Where more than 32 are that near, the exact choices of all are drawn from top_k times.  With
+// groups the groups' values need exact choices, so all are exact from the start.
 #include "common.cuh"
 #include "launch.h"
 #include "routed.h"
@@ -18,56 +23,13 @@ constexpr int kRouteWarps = 8;
 // its expert
 constexpr float kClosedFrom = -3.3895313892515355e38f;
 
-// Order-preserving map of a float to an unsigned integer; every finite float maps above 0.
-__device__ __forceinline__ uint32_t float_key(float f) {
-    const uint32_t u = __float_as_uint(f + 0.0f);   // -0 counts as 0
-    return (u >> 31) ? ~u : (u | 0x80000000u);
-}
-__device__ __forceinline__ float key_float(uint32_t k) {
-    return __uint_as_float((k >> 31) ? (k & 0x7FFFFFFFu) : ~k);
-}
-
 template <bool BF16>
 __device__ __forceinline__ float load_logit(const RouteParams &p, int64_t i) {
     return BF16 ? bf16_bits_to_f32(__ldg(static_cast<const uint16_t *>(p.logits) + i))
                 : __ldg(static_cast<const float *>(p.logits) + i);
 }
 
-// Bit g * lanes for each group g that stays: the topk_group largest values, equal ones to the lower group.
-// keys: this warp's in shared memory, group g's from g * pitch on (a pitch of `lanes` more than the group, so that
-// the lanes of neighbouring groups read different banks).
-__device__ __forceinline__ uint32_t best_groups(const RouteParams &p, const uint32_t *keys, int pitch, int lanes,
-                                                int lane) {
-    const int g = lane >> (31 - __clz(lanes)), r = lane & (lanes - 1);   // lanes: a power of two
-    uint32_t k1 = 0, k2 = 0;   // the two best keys of the group
-    if (g < p.n_group) {
-#pragma unroll 4
-        for (int i = r; i < p.group_size; i += lanes) {
-            const uint32_t k = keys[g * pitch + i];
-            k2 = max(k2, min(k, k1));
-            k1 = max(k1, k);
-        }
-    }
-    for (int d = 1; d < lanes; d <<= 1) {
-        const uint32_t o1 = __shfl_xor_sync(~0u, k1, d), o2 = __shfl_xor_sync(~0u, k2, d);
-        k2 = max(max(k2, o2), min(k1, o1));
-        k1 = max(k1, o1);
-    }
-    uint32_t value = k1;
-    if (p.group_top == 2 && k2 != 0) value = float_key(__fadd_rn(key_float(k1), key_float(k2)));
-    if (r != 0 || g >= p.n_group) value = 0;
-    uint32_t kept = 0;
-    for (int j = 0; j < p.topk_group; ++j) {
-        const uint32_t m = __reduce_max_sync(~0u, value);
-        if (m == 0) break;   // the others have no open expert
-        const uint32_t holders = __ballot_sync(~0u, value == m), first = holders & (0u - holders);
-        kept |= first;
-        if (first >> lane & 1u) value = 0;
-    }
-    return kept;
-}
-
-__device__ __forceinline__ float warp_fmax(float v) {   // no lane holds a NaN
+__device__ __forceinline__ float warp_fmax(float v) {
     float m;
     asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(v));
     return m;
@@ -81,15 +43,49 @@ __device__ __forceinline__ float quotient(float a, float b, float inv) {
     return fmaf(fmaf(-b, q, a), inv, q);
 }
 
-template <int VPL, bool BF16>
-__global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RouteParams p) {
-    extern __shared__ uint32_t route_smem[];
+// Bit g * lanes for each group g that stays: the topk_group largest values, equal ones to the lower group.
+// choices: this warp's in shared memory (-inf: closed), group g's from g * pitch on (a pitch of `lanes` more than
+// the group, so that the lanes of neighbouring groups read different banks).
+__device__ __forceinline__ uint32_t best_groups(const RouteParams &p, const float *choices, int pitch, int lanes,
+                                                int lane) {
+    const int g = lane >> (31 - __clz(lanes)), r = lane & (lanes - 1);   // lanes: a power of two
+    float c1 = -INFINITY, c2 = -INFINITY;                                // the group's two best
+    if (g < p.n_group) {
+#pragma unroll 4
+        for (int i = r; i < p.group_size; i += lanes) {
+            const float c = choices[g * pitch + i];
+            c2 = fmaxf(c2, fminf(c, c1));
+            c1 = fmaxf(c1, c);
+        }
+    }
+    for (int d = 1; d < lanes; d <<= 1) {
+        const float o1 = __shfl_xor_sync(~0u, c1, d), o2 = __shfl_xor_sync(~0u, c2, d);
+        c2 = fmaxf(fmaxf(c2, o2), fminf(c1, o1));
+        c1 = fmaxf(c1, o1);
+    }
+    float value = p.group_top == 2 && c2 > -INFINITY ? __fadd_rn(c1, c2) : c1;
+    if (r != 0 || g >= p.n_group) value = -INFINITY;
+    uint32_t kept = 0;
+    for (int j = 0; j < p.topk_group; ++j) {
+        const float m = warp_fmax(value);
+        if (m == -INFINITY) break;   // the others have no open expert
+        const uint32_t holders = __ballot_sync(~0u, value == m), first = holders & (0u - holders);
+        kept |= first;
+        if (first >> lane & 1u) value = -INFINITY;
+    }
+    return kept;
+}
+
+template <int VPL, bool BF16, bool GROUPS>
+__global__ void __launch_bounds__(kRouteWarps * 32, VPL <= 12 ? 4 : 1) route_kernel(const RouteParams p) {
+    extern __shared__ float route_smem[];
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, warps = blockDim.x / 32;
-    // keys, experts and scores of up to 32 candidates, then (groups) the keys of all experts
-    uint32_t *mine = route_smem + (size_t)warp * p.smem_words;
-    uint32_t *cand_key = mine, *cand_id = mine + 32, *all_keys = mine + 96;
-    float *cand_score = reinterpret_cast<float *>(mine + 64);
+    // up to 32 candidates, then (groups) the choices and the scores of all experts
+    float *cand_choice = route_smem + (size_t)warp * p.smem_words, *cand_score = cand_choice + 32;
+    int *cand_id = reinterpret_cast<int *>(cand_choice + 64);
+    float *all_choices = cand_choice + 96;
     const int lanes = p.group_lanes, pitch = p.group_size + lanes;
+    float *all_scores = all_choices + p.n_group * pitch;
     pdl_wait();
     float bias[VPL];
     int shift[VPL];   // g * lanes of the expert's group g: its bit among the kept ones
@@ -97,29 +93,27 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RoutePara
     for (int i = 0; i < VPL; ++i) {
         const int e = i * 32 + lane;
         bias[i] = p.bias && e < p.E ? __ldg(p.bias + e) : 0.f;
-        shift[i] = (int)((uint32_t)e * (uint32_t)p.group_magic >> 20) * lanes;   // e / group_size
+        shift[i] = GROUPS ? (int)((uint32_t)e * (uint32_t)p.group_magic >> 20) * lanes : 0;   // e / group_size
     }
     for (int64_t t = (int64_t)blockIdx.x * warps + warp; t < p.T; t += (int64_t)gridDim.x * warps) {
-        float score[VPL];
-        uint32_t key[VPL];   // 0: closed
-        float top = -INFINITY;
+        float v[VPL];        // logit (-inf: closed), then the softmax's term, then the choice
+        uint32_t open = 0;   // bit i
 #pragma unroll
         for (int i = 0; i < VPL; ++i) {
             const int e = i * 32 + lane;
-            score[i] = e < p.E ? load_logit<BF16>(p, t * p.ld + e) : -INFINITY;
+            v[i] = e < p.E ? load_logit<BF16>(p, t * p.ld + e) : -INFINITY;
         }
 #pragma unroll
         for (int i = 0; i < VPL; ++i) {
-            const bool open = score[i] > kClosedFrom;
-            key[i] = open ? 1u : 0u;
-            score[i] = open ? score[i] : -INFINITY;
-            top = fmaxf(top, score[i]);
+            v[i] = v[i] > kClosedFrom ? v[i] : -INFINITY;
+            open |= v[i] > -INFINITY ? 1u << i : 0u;
         }
-        if (p.sigmoid) {
+        float top = -INFINITY, sum = 1.f, inv = 1.f;
+        if (!p.sigmoid) {
 #pragma unroll
-            for (int i = 0; i < VPL; ++i) score[i] = __frcp_rn(__fadd_rn(1.0f, expf(-score[i])));
-        } else {
+            for (int i = 0; i < VPL; ++i) top = fmaxf(top, v[i]);
             top = warp_fmax(top);
+            if (top == -INFINITY) top = 0.f;
             // The sum as if rounded once, whatever the order: each term e <= 1 is split into a
             // multiple of 2^-14 (at most 1024 of them add up exactly, here and as integers) and a
             // remainder of at most 2^-15, summed per lane in fp32 and over the lanes in units of 2^-36:
@@ -127,66 +121,87 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RoutePara
             float high = 0.f, low = 0.f;
 #pragma unroll
             for (int i = 0; i < VPL; ++i) {
-                score[i] = key[i] ? expf(__fsub_rn(score[i], top)) : 0.f;
-                const float h = __fsub_rn(__fadd_rn(score[i], 512.f), 512.f);
+                v[i] = expf(__fsub_rn(v[i], top));   // closed: 0
+                const float h = __fsub_rn(__fadd_rn(v[i], 512.f), 512.f);
                 high += h;
-                low += __fsub_rn(score[i], h);
+                low += __fsub_rn(v[i], h);
             }
             const int hi = __reduce_add_sync(~0u, __float2int_rn(high * 0x1p14f));
             const int lo = __reduce_add_sync(~0u, __float2int_rn(low * 0x1p36f));
-            const float sum = fmaxf(fmaf((float)lo, 0x1p-36f, (float)hi * 0x1p-14f), 1e-30f), inv = __frcp_rn(sum);
-#pragma unroll
-            for (int i = 0; i < VPL; ++i) score[i] = quotient(score[i], sum, inv);
+            sum = fmaxf(fmaf((float)lo, 0x1p-36f, (float)hi * 0x1p-14f), 1e-30f);
+            inv = __frcp_rn(sum);
         }
-#pragma unroll
-        for (int i = 0; i < VPL; ++i)
-            if (key[i]) key[i] = float_key(__fadd_rn(score[i], bias[i]));   // (x + 0 is x)
-        if (p.n_group > 1) {
-#pragma unroll
-            for (int i = 0; i < VPL; ++i)
-                if (i * 32 + lane < p.E) all_keys[shift[i] + i * 32 + lane] = key[i];   // g * pitch + e % group_size
-            __syncwarp();
-            const uint32_t kept = best_groups(p, all_keys, pitch, lanes, lane);
-#pragma unroll
-            for (int i = 0; i < VPL; ++i)
-                if (!(kept >> (shift[i] & 31) & 1u)) key[i] = 0;
-        }
-        // lower bound of the top_k-th best key: as many lanes hold one at least as large
-        uint32_t lane_best = 0;
-#pragma unroll
-        for (int i = 0; i < VPL; ++i) lane_best = max(lane_best, key[i]);
-        uint32_t bound = 0;
-        for (int j = 0; j < p.top_k; ++j) {
-            bound = __reduce_max_sync(~0u, lane_best);
-            if (bound == 0) break;
-            const uint32_t holders = __ballot_sync(~0u, lane_best == bound);
-            if ((holders & (0u - holders)) >> lane & 1u) lane_best = 0;
-        }
-        bound = max(bound, 1u);   // fewer lanes than top_k: every open key
-        int n = 0;
+        auto score_of = [&](float logit) {   // exact
+            return p.sigmoid ? __frcp_rn(__fadd_rn(1.0f, expf(-logit)))
+                             : quotient(expf(__fsub_rn(logit, top)), sum, inv);
+        };
 #pragma unroll
         for (int i = 0; i < VPL; ++i) {
-            const bool in = key[i] >= bound;
-            const uint32_t who = __ballot_sync(~0u, in);
+            float c;
+            if constexpr (GROUPS) {
+                const float sc = p.sigmoid ? __frcp_rn(__fadd_rn(1.0f, expf(-v[i]))) : quotient(v[i], sum, inv);
+                if (i * 32 + lane < p.E) all_scores[i * 32 + lane] = sc;
+                c = __fadd_rn(sc, bias[i]);
+            } else
+                c = p.sigmoid ? __fdividef(1.0f, 1.0f + __expf(-v[i])) + bias[i] : fmaf(v[i], inv, bias[i]);
+            v[i] = open >> i & 1u ? c : -INFINITY;
+        }
+        if constexpr (GROUPS) {
+#pragma unroll
+            for (int i = 0; i < VPL; ++i)
+                if (i * 32 + lane < p.E) all_choices[shift[i] + i * 32 + lane] = v[i];   // g * pitch + e % group_size
+            __syncwarp();
+            const uint32_t kept = best_groups(p, all_choices, pitch, lanes, lane);
+#pragma unroll
+            for (int i = 0; i < VPL; ++i)
+                if (!(kept >> (shift[i] & 31) & 1u)) v[i] = -INFINITY;
+        }
+        // as many lanes as top_k hold a choice at least as large as the bound
+        float lane_best = -INFINITY, bound = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) lane_best = fmaxf(lane_best, v[i]);
+        for (int j = 0; j < p.top_k; ++j) {
+            bound = warp_fmax(lane_best);
+            if (bound == -INFINITY) break;
+            const uint32_t holders = __ballot_sync(~0u, lane_best == bound);
+            if ((holders & (0u - holders)) >> lane & 1u) lane_best = -INFINITY;
+        }
+        if constexpr (!GROUPS) {
+            // twice the error of a fast choice: 2^-18 of the score (an exponent of up to 88 costs the fast
+            // exponential 2^-18), the sum with the bias 2^-22 of the result
+            const float slack = fabsf(bound) * 0x1p-16f + (p.bias ? 0x1p-17f : 0.f);
+            bound = !p.bias && bound < 1e-30f ? kClosedFrom : bound - slack;   // (tiny scores: all of them)
+        }
+        bound = fmaxf(bound, kClosedFrom);   // fewer lanes than top_k: every open expert
+        uint32_t in = 0;                     // bit i: candidate
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) in |= v[i] >= bound ? 1u << i : 0u;
+        int n = 0;
+        for (;;) {
+            const uint32_t who = __ballot_sync(~0u, in != 0);
+            if (who == 0) break;
             const int at = n + __popc(who & ((1u << lane) - 1u));
-            if (in && at < 32) {
-                cand_key[at] = key[i];
-                cand_id[at] = i * 32 + lane;
-                cand_score[at] = score[i];
-            }
+            if (in != 0 && at < 32) cand_id[at] = (__ffs(in) - 1) * 32 + lane;
+            in &= in - 1u;
             n += __popc(who);
         }
         __syncwarp();
         int id = -1;   // lane j: the j-th best
         float w = 0.f;
         if (n <= 32) {
-            const uint32_t k = lane < n ? cand_key[lane] : 0u;
-            const uint32_t e = lane < n ? cand_id[lane] : 0u;
-            const float sc = lane < n ? cand_score[lane] : 0.f;
-            int rank = 0;   // candidates lie in the order of their experts: of equal keys the earlier is the better
+            int e = 0;
+            float sc = 0.f, c = -INFINITY;
+            if (lane < n) {
+                e = cand_id[lane];
+                sc = GROUPS ? all_scores[e] : score_of(load_logit<BF16>(p, t * p.ld + e));
+                c = p.bias ? __fadd_rn(sc, __ldg(p.bias + e)) : sc;
+                cand_choice[lane] = c;
+            }
+            __syncwarp();
+            int rank = 0;
             for (int j = 0; j < n; ++j) {
-                const uint32_t o = cand_key[j];
-                rank += o > k || (o == k && j < lane) ? 1 : 0;
+                const float o = cand_choice[j];
+                rank += o > c || (o == c && cand_id[j] < e) ? 1 : 0;
             }
             __syncwarp();
             if (lane < n) {   // every candidate to its place
@@ -195,27 +210,39 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RoutePara
             }
             __syncwarp();
             if (lane < n && lane < p.top_k) {
-                id = (int)cand_id[lane];
+                id = cand_id[lane];
                 w = cand_score[lane];
             }
             __syncwarp();   // the next token's candidates come after these reads
         } else {
+            if constexpr (!GROUPS) {
+#pragma unroll 1
+                for (int i = 0; i < VPL; ++i) {
+                    const int x = i * 32 + lane;
+                    float c = -INFINITY;
+                    if (open >> i & 1u)
+                        c = __fadd_rn(score_of(load_logit<BF16>(p, t * p.ld + x)), p.bias ? __ldg(p.bias + x) : 0.f);
+#pragma unroll
+                    for (int u = 0; u < VPL; ++u)
+                        if (u == i) v[u] = c;
+                }
+            }
             for (int j = 0; j < p.top_k; ++j) {
-                uint32_t best = 0;
+                float best = -INFINITY;
                 int at = 0;
 #pragma unroll
                 for (int i = 0; i < VPL; ++i)
-                    if (key[i] > best) { best = key[i]; at = i; }
-                const uint32_t m = __reduce_max_sync(~0u, best);
-                if (m == 0) break;
+                    if (v[i] > best) { best = v[i]; at = i; }
+                const float m = warp_fmax(best);
+                if (m == -INFINITY) break;
                 const uint32_t e = __reduce_min_sync(~0u, best == m ? (uint32_t)(at * 32 + lane) : ~0u);
-                float sc = 0.f;
 #pragma unroll
                 for (int i = 0; i < VPL; ++i)
-                    if ((uint32_t)(i * 32 + lane) == e) { key[i] = 0; sc = score[i]; }
-                sc = __shfl_sync(~0u, sc, e % 32);
-                if (lane == j) { id = (int)e; w = sc; }
+                    if ((uint32_t)(i * 32 + lane) == e) v[i] = -INFINITY;
+                if (lane == j) id = (int)e;
             }
+            if (id >= 0) w = score_of(load_logit<BF16>(p, t * p.ld + id));
+            __syncwarp();   // (groups: the next token's scores come after the reads of this one's)
         }
         if (p.renormalise) {
             float total = w;
@@ -227,40 +254,47 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RoutePara
             p.ids[t * p.top_k + lane] = id;
             p.weights[t * p.top_k + lane] = w * p.scale;
         }
-        }
     }
+}
 
-    template <int VPL>
-    cudaError_t launch_vpl(RouteParams p, int sm_count, bool pdl, cudaStream_t s) {
-        // a few tokens: one warp per CTA, so that they run on as many SMs
-        const int warps = p.T >= 1024 ? kRouteWarps : 1;
-        p.group_lanes = p.n_group > 16 ? 1 : p.n_group > 8 ? 2 : p.n_group > 4 ? 4 : p.n_group > 2 ? 8 : 16;
-        p.group_magic = ((1 << 20) + p.group_size - 1) / p.group_size;   // exact for e < 1024
-        p.smem_words = 96 + (p.n_group > 1 ? p.n_group * (p.group_size + p.group_lanes) : 0);
-        const size_t smem = (size_t)p.smem_words * 4 * warps;
-        // a warp keeps its experts' biases and groups from token to token
-        const dim3 grid((unsigned)std::min<int64_t>((p.T + warps - 1) / warps, (int64_t)sm_count * 8));
-        return p.bf16_logits ? launch_kernel(route_kernel<VPL, true>, grid, warps * 32, smem, pdl, 1, s, p)
-                             : launch_kernel(route_kernel<VPL, false>, grid, warps * 32, smem, pdl, 1, s, p);
+template <int VPL>
+cudaError_t launch_vpl(RouteParams p, int sm_count, bool pdl, cudaStream_t s) {
+    // a few tokens: one warp per CTA, so that they run on as many SMs
+    const int warps = p.T >= 1024 ? kRouteWarps : 1;
+    p.group_lanes = p.n_group > 16 ? 1 : p.n_group > 8 ? 2 : p.n_group > 4 ? 4 : p.n_group > 2 ? 8 : 16;
+    p.group_magic = ((1 << 20) + p.group_size - 1) / p.group_size;   // exact for e < 1024
+    p.smem_words = 96 + (p.n_group > 1 ? p.n_group * (p.group_size + p.group_lanes) + p.E : 0);
+    const size_t smem = (size_t)p.smem_words * 4 * warps;   // at most 70 KB
+    if (smem > 48 * 1024) {   // groups of over 700 experts
+        const cudaError_t e = p.bf16_logits ? cudaFuncSetAttribute(route_kernel<VPL, true, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)
+                                            : cudaFuncSetAttribute(route_kernel<VPL, false, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
     }
+    // a warp keeps its experts' biases and groups from token to token
+    const dim3 grid((unsigned)std::min<int64_t>((p.T + warps - 1) / warps, (int64_t)sm_count * 8));
+    const int threads = warps * 32;
+    if (p.n_group > 1)
+        return p.bf16_logits ? launch_kernel(route_kernel<VPL, true, true>, grid, threads, smem, pdl, 1, s, p)
+                             : launch_kernel(route_kernel<VPL, false, true>, grid, threads, smem, pdl, 1, s, p);
+    return p.bf16_logits ? launch_kernel(route_kernel<VPL, true, false>, grid, threads, smem, pdl, 1, s, p)
+                         : launch_kernel(route_kernel<VPL, false, false>, grid, threads, smem, pdl, 1, s, p);
+}
 
-    }  // namespace
+}  // namespace
 
-    cudaError_t launch_route(const RouteParams &p, int sm_count, bool pdl, cudaStream_t s) {
-        switch ((p.E + 31) / 32) {
-            case 1: return launch_vpl<1>(p, sm_count, pdl, s);
-            case 2: return launch_vpl<2>(p, sm_count, pdl, s);
-            case 3: return launch_vpl<3>(p, sm_count, pdl, s);
-            case 4: return launch_vpl<4>(p, sm_count, pdl, s);
-            case 5: return launch_vpl<5>(p, sm_count, pdl, s);
-            case 6: return launch_vpl<6>(p, sm_count, pdl, s);
-            case 7: case 8: return launch_vpl<8>(p, sm_count, pdl, s);
-            case 9: case 10: return launch_vpl<10>(p, sm_count, pdl, s);
-            case 11: case 12: return launch_vpl<12>(p, sm_count, pdl, s);
-            case 13: case 14: case 15: case 16: return launch_vpl<16>(p, sm_count, pdl, s);
-            default: return launch_vpl<32>(p, sm_count, pdl, s);
-        }
+cudaError_t launch_route(const RouteParams &p, int sm_count, bool pdl, cudaStream_t s) {
+    switch ((p.E + 31) / 32) {
+        case 1: return launch_vpl<1>(p, sm_count, pdl, s);
+        case 2: return launch_vpl<2>(p, sm_count, pdl, s);
+        case 3: case 4: return launch_vpl<4>(p, sm_count, pdl, s);
+        case 5: return launch_vpl<5>(p, sm_count, pdl, s);
+        case 6: return launch_vpl<6>(p, sm_count, pdl, s);
+        case 7: case 8: return launch_vpl<8>(p, sm_count, pdl, s);
+        case 9: case 10: case 11: case 12: return launch_vpl<12>(p, sm_count, pdl, s);
+        case 13: case 14: case 15: case 16: return launch_vpl<16>(p, sm_count, pdl, s);
+        default: return launch_vpl<32>(p, sm_count, pdl, s);
     }
+}
 
-    }  // namespace routed
-    }  // namespace mse
+}  // namespace routed
+}  // namespace mse

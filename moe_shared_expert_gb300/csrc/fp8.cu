@@ -17,7 +17,7 @@ namespace {
 __device__ __forceinline__ void load_block8(const uint16_t *row, int64_t K, int64_t b, int l, bool wide, float (&v)[8]) {
     const int64_t k = b * kBlock + l * 8;
     if (wide && k + 8 <= K) {
-        const uint4 w = *reinterpret_cast<const uint4 *>(row + k);
+        const uint4 w = __ldg(reinterpret_cast<const uint4 *>(row + k));
         const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -176,12 +176,13 @@ __device__ __forceinline__ int warp_prefix(int *v, int n, int lane) {
 // counted, not drawn by atomics, so every CTA of a chunk finds the same rows.
 __global__ void __launch_bounds__(kDispatchThreads) dispatch_kernel(const DispatchParams p) {
     extern __shared__ int dispatch_smem[];
-    int *total = dispatch_smem, *before = total + p.E, *tile_at = before + p.E;
-    __shared__ int pair_expert[kDispatchPairs], pair_row[kDispatchPairs];
+    int *total = dispatch_smem, *before = total + p.E, *tile_at = before + p.E, *of_warp = tile_at + p.E;
+    __shared__ int pair_row[kDispatchPairs];
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
     pdl_wait();
     pdl_launch_dependents();
     for (int e = tid; e < p.E; e += kDispatchThreads) total[e] = before[e] = 0;
+    for (int i = tid; i < kDispatchThreads / 32 * p.E; i += kDispatchThreads) of_warp[i] = 0;
     __syncthreads();
     const int64_t pairs = p.T * p.top_k, i0 = (int64_t)blockIdx.x * p.chunk * p.top_k;
     const int64_t t0 = (int64_t)blockIdx.x * p.chunk;
@@ -202,7 +203,12 @@ __global__ void __launch_bounds__(kDispatchThreads) dispatch_kernel(const Dispat
             }
         }
     }
-    for (int i = tid; i < mine; i += kDispatchThreads) pair_expert[i] = local_expert(p, i0 + i);
+    // pair `tid` of the chunk: the pairs of its expert before it in its warp, and per warp and expert
+    static_assert(kDispatchPairs <= kDispatchThreads, "one pair per thread");
+    const int expert = tid < mine ? local_expert(p, i0 + tid) : -1;
+    const uint32_t same = __match_any_sync(~0u, expert);
+    const int rank = __popc(same & ((1u << lane) - 1u));
+    if (expert >= 0 && rank == 0) of_warp[warp * p.E + expert] = __popc(same);
     __syncthreads();
     const bool writes_tiles = blockIdx.x == 0 && blockIdx.y == 0;
     if (writes_tiles) {
@@ -225,15 +231,14 @@ __global__ void __launch_bounds__(kDispatchThreads) dispatch_kernel(const Dispat
     }
     if (warp == 0) (void)warp_prefix(total, p.E, lane);   // now each expert's first row
     __syncthreads();
-    for (int i = tid; i < mine; i += kDispatchThreads) {
-        const int e = pair_expert[i];
+    if (tid < mine) {
         int row = -1;
-        if (e >= 0) {
-            row = total[e] + before[e];
-            for (int o = 0; o < i; ++o) row += pair_expert[o] == e ? 1 : 0;
+        if (expert >= 0) {
+            row = total[expert] + before[expert] + rank;
+            for (int w = 0; w < warp; ++w) row += of_warp[w * p.E + expert];
         }
-        pair_row[i] = row;
-        if (blockIdx.y == 0) p.pos[i0 + i] = row;
+        pair_row[tid] = row;
+        if (blockIdx.y == 0) p.pos[i0 + tid] = row;
     }
     __syncthreads();
     const int64_t kb = (p.H + kBlock - 1) / kBlock;
@@ -242,12 +247,20 @@ __global__ void __launch_bounds__(kDispatchThreads) dispatch_kernel(const Dispat
     const int l = tid % 16;
     const uint32_t mask = 0xFFFFu << (tid & 16);
     const bool wide = p.H % 8 == 0 && (reinterpret_cast<uintptr_t>(p.x) & 15u) == 0;
-    for (int64_t it = tid / 16; it < tokens * nb; it += kDispatchThreads / 16) {
-        const int t = (int)(it / nb);
-        const int64_t b = b0 + it % nb;
-        float v[8], a;
+    const int items = (int)(tokens * nb);
+    float v[8], next[8];
+    auto fetch = [&](int it, float (&to)[8]) {
+        load_block8(p.x + (t0 + it / (int)nb) * p.H, p.H, b0 + it % (int)nb, l, wide, to);
+    };
+    if (tid / 16 < items) fetch(tid / 16, next);
+    for (int it = tid / 16; it < items; it += kDispatchThreads / 16) {
+        const int t = it / (int)nb;
+        const int64_t b = b0 + it % (int)nb;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = next[i];
+        if (it + kDispatchThreads / 16 < items) fetch(it + kDispatchThreads / 16, next);   // while this one is rounded
+        float a;
         uint2 q;
-        load_block8(p.x + (t0 + t) * p.H, p.H, b, l, wide, v);
         round_block8(v, mask, a, q);
         const float s = block_scale(a);
         const int64_t k = b * kBlock + l * 8;
@@ -376,7 +389,7 @@ cudaError_t launch_dispatch(const DispatchParams &p, bool pdl, cudaStream_t s) {
         if (e != cudaSuccess) return e;
     }
     return launch_kernel(dispatch_kernel, dim3((unsigned)p.n_chunks, (unsigned)p.splits), kDispatchThreads,
-                         (size_t)p.E * 12, pdl, 1, s, p);
+                         (size_t)p.E * 4 * (3 + kDispatchThreads / 32), pdl, 1, s, p);
 }
 
 cudaError_t launch_combine(const float *o, const int32_t *pos, const float *weights, int top_k, const uint16_t *shared,

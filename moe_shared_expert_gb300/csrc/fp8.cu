@@ -64,14 +64,23 @@ __global__ void __launch_bounds__(256) quantise_rows_kernel(const uint16_t *x, i
     const int64_t kb = (K + kBlock - 1) / kBlock, items = rows * kb;
     const int l = threadIdx.x % 16;
     const uint32_t mask = 0xFFFFu << (threadIdx.x & 16);
-    for (int64_t it = (int64_t)blockIdx.x * 16 + threadIdx.x / 16; it < items; it += (int64_t)gridDim.x * 16) {
-        const int64_t r = it / kb, b = it % kb;
-        float v[8], a;
+    const int64_t stride = (int64_t)gridDim.x * 16, dr = stride / kb, db = stride % kb;
+    int64_t it = (int64_t)blockIdx.x * 16 + threadIdx.x / 16;
+    int64_t r = it / kb, b = it % kb;   // then advanced by (dr, db): no division per block
+    float v[8], next[8];
+    if (it < items) load_block8(x + r * ldx, K, b, l, wide_in, next);
+    for (; it < items; it += stride) {
+        const int64_t row = r, k = b * kBlock + l * 8;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = next[i];
+        r += dr;
+        b += db;
+        if (b >= kb) { b -= kb; ++r; }
+        if (it + stride < items) load_block8(x + r * ldx, K, b, l, wide_in, next);   // while this one is rounded
+        float a;
         uint2 o;
-        load_block8(x + r * ldx, K, b, l, wide_in, v);
         round_block8(v, mask, a, o);
-        const int64_t k = b * kBlock + l * 8;
-        store8(q + r * ldq + k, K - k, wide_out, o);
+        store8(q + row * ldq + k, K - k, wide_out, o);
         if (l == 0) scales[it] = block_scale(a);
     }
 }
@@ -178,6 +187,7 @@ __global__ void __launch_bounds__(kDispatchThreads) dispatch_kernel(const Dispat
     extern __shared__ int dispatch_smem[];
     int *total = dispatch_smem, *before = total + p.E, *tile_at = before + p.E, *of_warp = tile_at + p.E;
     __shared__ int pair_row[kDispatchPairs];
+    __shared__ int64_t pair_at[kDispatchPairs];   // byte offset of the row in xq, -1: none
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
     pdl_wait();
     pdl_launch_dependents();
@@ -238,6 +248,7 @@ __global__ void __launch_bounds__(kDispatchThreads) dispatch_kernel(const Dispat
             for (int w = 0; w < warp; ++w) row += of_warp[w * p.E + expert];
         }
         pair_row[tid] = row;
+        pair_at[tid] = row < 0 ? -1 : (int64_t)row * p.ldq;
         if (blockIdx.y == 0) p.pos[i0 + tid] = row;
     }
     __syncthreads();
@@ -247,28 +258,42 @@ __global__ void __launch_bounds__(kDispatchThreads) dispatch_kernel(const Dispat
     const int l = tid % 16;
     const uint32_t mask = 0xFFFFu << (tid & 16);
     const bool wide = p.H % 8 == 0 && (reinterpret_cast<uintptr_t>(p.x) & 15u) == 0;
-    const int items = (int)(tokens * nb);
-    float v[8], next[8];
-    auto fetch = [&](int it, float (&to)[8]) {
-        load_block8(p.x + (t0 + it / (int)nb) * p.H, p.H, b0 + it % (int)nb, l, wide, to);
-    };
-    if (tid / 16 < items) fetch(tid / 16, next);
-    for (int it = tid / 16; it < items; it += kDispatchThreads / 16) {
-        const int t = it / (int)nb;
-        const int64_t b = b0 + it % (int)nb;
+    // half-warp h: tokens h, h + 16, .. of the chunk, block after block; of fewer than 16 tokens, several share one
+    const int h = tid / 16, across = min(tokens, 16), stride = max(1, 16 / across);
+    if (h >= across * stride) return;
+    for (int t = h % across; t < tokens; t += 16) {
+        const uint16_t *row = p.x + (t0 + t) * p.H;
+        const int j0 = t * p.top_k;
+        const int mine_row = l < p.top_k ? pair_row[j0 + l] : -1;
+        float v[8], next[8];
+        int b = h / across;
+        if (b < nb) load_block8(row, p.H, b0 + b, l, wide, next);
+        for (; b < nb; b += stride) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = next[i];
-        if (it + kDispatchThreads / 16 < items) fetch(it + kDispatchThreads / 16, next);   // while this one is rounded
-        float a;
-        uint2 q;
-        round_block8(v, mask, a, q);
-        const float s = block_scale(a);
-        const int64_t k = b * kBlock + l * 8;
-        for (int j = 0; j < p.top_k; ++j) {
-            const int row = pair_row[t * p.top_k + j];
-            if (row < 0) continue;
-            store8(p.xq + (int64_t)row * p.ldq + k, p.H - k, true, q);
-            if (l == 0) p.xs[(int64_t)row * kb + b] = s;
+            for (int i = 0; i < 8; ++i) v[i] = next[i];
+            if (b + stride < nb) load_block8(row, p.H, b0 + b + stride, l, wide, next);   // while this one is rounded
+            float a;
+            uint2 q;
+            round_block8(v, mask, a, q);
+            const float s = block_scale(a);
+            const int64_t k = (b0 + b) * kBlock + l * 8;
+            if (k + 8 <= p.H) {
+                uint8_t *dst = p.xq + k;
+#pragma unroll 4
+                for (int j = 0; j < p.top_k; ++j) {
+                    const int64_t at = pair_at[j0 + j];
+                    if (at >= 0) *reinterpret_cast<uint2 *>(dst + at) = q;
+                }
+            } else {
+                for (int j = 0; j < p.top_k; ++j) {
+                    const int64_t at = pair_at[j0 + j];
+                    if (at >= 0) store8(p.xq + at + k, p.H - k, false, q);
+                }
+            }
+            // lane l writes the scale of the token's pair l (and l + 16)
+            if (mine_row >= 0) p.xs[(int64_t)mine_row * kb + b0 + b] = s;
+            if (l + 16 < p.top_k && pair_row[j0 + l + 16] >= 0)
+                p.xs[(int64_t)pair_row[j0 + l + 16] * kb + b0 + b] = s;
         }
     }
 }

@@ -22,7 +22,7 @@ namespace routed {
 namespace {
 
 constexpr int kChunk = 32;       // k-blocks whose scales are in shared memory at a time
-constexpr int kMaxColsStages = 8;
+constexpr int kMaxColsStages = 9;
 
 constexpr int pow2_up(int v) {
     int p = 32;
@@ -40,32 +40,40 @@ template <int BN_, int EPI_>
 struct Cols {
     static constexpr int BN = BN_, EPI = EPI_;
     static constexpr int MATS = EPI == BLOCK_SWIGLU ? 2 : 1;
-    static constexpr int WARPS = BN >= 64 ? 8 : 4;             // promotion warps
-    static constexpr int CPT = BN / (WARPS / 4);               // token columns per thread
+    static constexpr int WARPS = 8;                            // promotion warps: two groups of four
+    // Up to 32 columns the groups take k-blocks in turn and halve the columns at the end; with 64 columns
+    // each takes half of them throughout (us by k-blocks and by columns: 32 x 4096 x 2048 7.8 and 8.6,
+    // 16 x 12288 x 7168 18.9 and 19.6, 64 x 12288 x 7168 23.7 and 22.4).
+    static constexpr bool BY_K = BN < 64;
+    static constexpr int CPT = BN / 2;                         // token columns a thread finishes
+    static constexpr int ACC = BY_K ? BN : CPT;                // and sums
     static constexpr int THREADS = 64 + 32 * WARPS;
     static constexpr int BUF = MATS * BN;                      // TMEM columns of one k-block's sums
     static constexpr int NBUF = BUF * 4 <= 256 ? 4 : 2;
     static constexpr int TMEM = pow2_up(NBUF * BUF);
-    static constexpr int CTAS = 2;                             // resident per SM
+    static constexpr int CTAS = 2;                             // resident per SM (the ring may take a whole SM)
     static_assert(CTAS * TMEM <= 512, "TMEM");
     static constexpr uint32_t STAGE = MATS * kOperandTile + BN * 128;
     static constexpr int XS_PITCH = BN + 4;                    // floats; 16-byte rows, 4-way conflicts at worst
     static constexpr uint32_t SCALES = kChunk * XS_PITCH * 4 + MATS * kChunk * 4 + 4 * BN * 4;
     static constexpr uint32_t FIXED = 1024 + SCALES + sizeof(ColsCtrl) + 64;
-    static constexpr uint32_t BUDGET = 113 * 1024;
-    static constexpr int FIT = (int)((BUDGET - FIXED) / STAGE);
-    static constexpr int STAGES = FIT < kMaxColsStages ? FIT : kMaxColsStages;
-    static constexpr size_t SMEM = FIXED + (size_t)STAGES * STAGE;
-    static_assert(STAGES >= 2, "ring");
+    // stages of the ring with two CTAs on an SM, or one
+    static constexpr int fit(uint32_t budget) {
+        const int n = (int)((budget - FIXED) / STAGE);
+        return n < kMaxColsStages ? n : kMaxColsStages;
+    }
+    static constexpr int HALF = fit(113 * 1024), WHOLE = fit(227 * 1024);
+    static_assert(HALF >= 2, "ring");
     // the exchange of a split tile, at most BN + 7 columns of every mat, uses the ring and the tokens' scales
-    static_assert(MATS * (BN + 7) * 512 <= STAGES * STAGE + kChunk * XS_PITCH * 4, "exchange");
+    static_assert(MATS * BN * 512 <= HALF * STAGE, "halves");
+    static_assert(MATS * (BN + 7) * 512 <= HALF * STAGE + kChunk * XS_PITCH * 4, "exchange");
 };
 
 template <typename C>
 __global__ void __launch_bounds__(C::THREADS, C::CTAS)
     cols_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX, const BlockGemm g,
-                const int stream_weights) {
-    constexpr int BN = C::BN, MATS = C::MATS, S = C::STAGES, CPT = C::CPT;
+                const int stream_weights, const int S) {
+    constexpr int BN = C::BN, MATS = C::MATS, CPT = C::CPT;
     constexpr int kPromo = 32 * C::WARPS;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
@@ -86,7 +94,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
         }
         for (int b = 0; b < C::NBUF; ++b) {
             mbar_init(smem_u32(&ctl->tfull[b]), 1);
-            mbar_init(smem_u32(&ctl->tempty[b]), C::WARPS);
+            mbar_init(smem_u32(&ctl->tempty[b]), C::BY_K ? C::WARPS / 2 : C::WARPS);
         }
         mbar_init(smem_u32(&ctl->drain), 1);
         ctl->abort_flag = 0;
@@ -136,21 +144,23 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
             if (el) tokens(i, kb0 + i);
         __syncwarp();
         issued = pre;
-        for (int i = pre; i < n; ++i, ++issued) {
-            const int s = i % S;
-            if (!warp_wait(smem_u32(&ctl->empty[s]), (uint32_t)((i / S - 1) & 1), abort_flag, g)) break;
+        uint32_t phase = 0;
+        for (int i = pre, s = 0; i < n; ++i, ++issued) {
+            if (!warp_wait(smem_u32(&ctl->empty[s]), phase, abort_flag, g)) break;
             if (el) {
                 weights(s, kb0 + i);
                 tokens(s, kb0 + i);
             }
             __syncwarp();
+            if (++s == S) { s = 0; phase ^= 1u; }
         }
     } else if (active && warp == 1) {
         const bool el = elect_lane();
         const uint32_t idesc = idesc_e4m3_f32(128, BN);
-        for (int i = 0; i < n; ++i) {
-            const int s = i % S, b = i % C::NBUF;
-            if (!warp_wait(smem_u32(&ctl->full[s]), (uint32_t)((i / S) & 1), abort_flag, g) ||
+        uint32_t phase = 0;
+        for (int i = 0, s = 0; i < n; ++i) {
+            const int b = i % C::NBUF;
+            if (!warp_wait(smem_u32(&ctl->full[s]), phase, abort_flag, g) ||
                 !warp_wait(smem_u32(&ctl->tempty[b]), (uint32_t)((i / C::NBUF) & 1) ^ 1u, abort_flag, g))
                 break;
             tc_fence_after();
@@ -169,16 +179,18 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
                 tc_commit(smem_u32(&ctl->empty[s]));
             }
             __syncwarp();
+            if (++s == S) { s = 0; phase ^= 1u; }
         }
     }
 
     float acc[MATS][CPT];
-    const int q = warp & 3, row = q * 32 + lane, col0 = warp >= 2 ? (warp - 2) / 4 * CPT : 0;
+    const int q = warp & 3, row = q * 32 + lane, group = warp >= 2 ? (warp - 2) / 4 : 0, col0 = group * CPT;
     if (active && warp >= 2) {
+        float sum[MATS][C::ACC];
 #pragma unroll
         for (int a = 0; a < MATS; ++a)
 #pragma unroll
-            for (int c = 0; c < CPT; ++c) acc[a][c] = 0.f;
+            for (int c = 0; c < C::ACC; ++c) sum[a][c] = 0.f;
         if (g.weights_early) pdl_wait();
         const int pt = threadIdx.x - 64;
         const float *ws = g.ws + (int64_t)t.expert * g.ws_group + (int64_t)m * g.kb;
@@ -202,15 +214,15 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
             if (pt < MATS * kChunk && c0 + pt % kChunk < n)
                 ws_s[pt] = __ldg(ws + (pt / kChunk) * g.up_scales + kb0 + c0 + pt % kChunk);
             named_barrier_sync(1, kPromo);
-            for (int k = 0; k < kChunk && c0 + k < n; ++k) {
+            for (int k = C::BY_K ? group : 0; k < kChunk && c0 + k < n; k += C::BY_K ? 2 : 1) {   // kChunk is even
                 const int i = c0 + k, b = i % C::NBUF;
                 ok = warp_wait(smem_u32(&ctl->tfull[b]), (uint32_t)((i / C::NBUF) & 1), abort_flag, g);
                 if (!ok) break;
                 tc_fence_after();
-                const float *x = xs_s + k * C::XS_PITCH + col0;
-                const uint32_t src = tmem_base + (uint32_t)(b * C::BUF + col0) + ((uint32_t)(q * 32) << 16);
+                const float *x = xs_s + k * C::XS_PITCH + (C::BY_K ? 0 : col0);
+                const uint32_t src = tmem_base + (uint32_t)(b * C::BUF + (C::BY_K ? 0 : col0)) + ((uint32_t)(q * 32) << 16);
 #pragma unroll
-                for (int c = 0; c < CPT; c += 16) {
+                for (int c = 0; c < C::ACC; c += 16) {
                     uint32_t d[MATS][16];
 #pragma unroll
                     for (int a = 0; a < MATS; ++a) tmem_ld16(src + a * BN + c, d[a]);
@@ -221,10 +233,10 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
 #pragma unroll
                         for (int v = 0; v < 16; v += 4) {
                             const float4 f = *reinterpret_cast<const float4 *>(x + c + v);
-                            acc[a][c + v] = fmaf(__uint_as_float(d[a][v]), f.x * w, acc[a][c + v]);
-                            acc[a][c + v + 1] = fmaf(__uint_as_float(d[a][v + 1]), f.y * w, acc[a][c + v + 1]);
-                            acc[a][c + v + 2] = fmaf(__uint_as_float(d[a][v + 2]), f.z * w, acc[a][c + v + 2]);
-                            acc[a][c + v + 3] = fmaf(__uint_as_float(d[a][v + 3]), f.w * w, acc[a][c + v + 3]);
+                            sum[a][c + v] = fmaf(__uint_as_float(d[a][v]), f.x * w, sum[a][c + v]);
+                            sum[a][c + v + 1] = fmaf(__uint_as_float(d[a][v + 1]), f.y * w, sum[a][c + v + 1]);
+                            sum[a][c + v + 2] = fmaf(__uint_as_float(d[a][v + 2]), f.z * w, sum[a][c + v + 2]);
+                            sum[a][c + v + 3] = fmaf(__uint_as_float(d[a][v + 3]), f.w * w, sum[a][c + v + 3]);
                         }
                     }
                 }
@@ -234,6 +246,30 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
             }
         }
         __syncwarp();
+        if constexpr (C::BY_K) {
+            // every MMA is done: the ring takes the halves that the groups owe one another, [group][mat][column][row]
+            named_barrier_sync(1, kPromo);
+            float *owed = reinterpret_cast<float *>(ring);
+#pragma unroll
+            for (int a = 0; a < MATS; ++a)
+#pragma unroll
+                for (int c = 0; c < CPT; ++c)
+                    if (c + CPT - col0 < t.rows)
+                        owed[((group * MATS + a) * CPT + c) * 128 + row] = group == 0 ? sum[a][CPT + c] : sum[a][c];
+            named_barrier_sync(1, kPromo);
+#pragma unroll
+            for (int a = 0; a < MATS; ++a)
+#pragma unroll
+                for (int c = 0; c < CPT; ++c)   // group 0's sum first in either half
+                    acc[a][c] = col0 + c >= t.rows ? 0.f
+                                : group == 0       ? sum[a][c] + owed[((MATS + a) * CPT + c) * 128 + row]
+                                                   : owed[(a * CPT + c) * 128 + row] + sum[a][CPT + c];
+        } else {
+#pragma unroll
+            for (int a = 0; a < MATS; ++a)
+#pragma unroll
+                for (int c = 0; c < CPT; ++c) acc[a][c] = sum[a][c];
+        }
     }
 
     // ---- the cluster's sums: every CTA gets a slice of the token columns from all, [rank][mat][column][row]
@@ -267,7 +303,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
         };
         const int first = part * slice;                          // parts > 1: this CTA's columns
         const int mine = min(min(slice, BN - first), t.rows - first);
-        const int half = col0 / CPT;                             // and this warp's: half, half + 2, ..
+        // and this group's: every other one from `group` on
         if constexpr (C::EPI != BLOCK_SWIGLU) {
             auto store = [&](int col, float v) {
                 const int64_t at = (int64_t)(t.row0 + col) * g.ldo + out_n;
@@ -282,7 +318,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
                     for (int c = 0; c < CPT; ++c)
                         if (col0 + c < t.rows) store(col0 + c, acc[0][c]);
                 } else {
-                    for (int at = half; at < mine; at += C::WARPS / 4) store(first + at, summed(0, at));
+                    for (int at = group; at < mine; at += 2) store(first + at, summed(0, at));
                 }
             }
         } else {
@@ -311,13 +347,13 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
                 for (int c = 0; c < CPT; ++c)
                     if (col0 + c < t.rows) write(col0 + c, acc[0][c]);
             } else {
-                for (int at = half; at < mine; at += C::WARPS / 4) {
+                for (int at = group; at < mine; at += 2) {
                     const float h = h_of(summed(0, at), summed(MATS - 1, at));
                     red[(size_t)at * 128 + row] = h;             // read again by this thread alone
                     note(first + at, h);
                 }
                 named_barrier_sync(1, kPromo);
-                for (int at = half; at < mine; at += C::WARPS / 4) write(first + at, red[(size_t)at * 128 + row]);
+                for (int at = group; at < mine; at += 2) write(first + at, red[(size_t)at * 128 + row]);
             }
         }
     }
@@ -340,27 +376,28 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
 
 template <typename C>
 cudaError_t run(const CUtensorMap &tw, const CUtensorMap &tx, const BlockGemm &g, int parts, int slots, int row_tiles,
-                int stream_weights, bool pdl, cudaStream_t s) {
+                int stream_weights, bool whole, bool pdl, cudaStream_t s) {
     static std::atomic<uint64_t> done;   // bit per device
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (!(done.load(std::memory_order_acquire) >> (dev & 63) & 1)) {
-        e = cudaFuncSetAttribute(cols_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM);
+        e = cudaFuncSetAttribute(cols_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
         if (e != cudaSuccess) return e;
         done.fetch_or(1ull << (dev & 63), std::memory_order_acq_rel);
     }
+    const int stages = whole ? C::WHOLE : C::HALF;
     return launch_kernel(cols_kernel<C>, dim3((unsigned)parts, (unsigned)slots, (unsigned)row_tiles), C::THREADS,
-                         C::SMEM, pdl, parts, s, tw, tx, g, stream_weights);
+                         C::FIXED + (size_t)stages * C::STAGE, pdl, parts, s, tw, tx, g, stream_weights, stages);
 }
 
 template <int EPI>
 cudaError_t run_bn(const CUtensorMap &tw, const CUtensorMap &tx, const BlockGemm &g, int parts, int slots,
-                   int row_tiles, int stream_weights, bool pdl, cudaStream_t s) {
+                   int row_tiles, int stream_weights, bool whole, bool pdl, cudaStream_t s) {
     switch (g.tile_rows) {
-        case 16: return run<Cols<16, EPI>>(tw, tx, g, parts, slots, row_tiles, stream_weights, pdl, s);
-        case 32: return run<Cols<32, EPI>>(tw, tx, g, parts, slots, row_tiles, stream_weights, pdl, s);
-        default: return run<Cols<EPI == BLOCK_SWIGLU ? 32 : 64, EPI>>(tw, tx, g, parts, slots, row_tiles, stream_weights, pdl, s);
+        case 16: return run<Cols<16, EPI>>(tw, tx, g, parts, slots, row_tiles, stream_weights, whole, pdl, s);
+        case 32: return run<Cols<32, EPI>>(tw, tx, g, parts, slots, row_tiles, stream_weights, whole, pdl, s);
+        default: return run<Cols<EPI == BLOCK_SWIGLU ? 32 : 64, EPI>>(tw, tx, g, parts, slots, row_tiles, stream_weights, whole, pdl, s);
     }
 }
 
@@ -376,15 +413,20 @@ mse_status launch_block_cols(const BlockGemm &g, int sm_count, bool pdl, cudaStr
     const int64_t slots = g.tiles ? g.max_tiles : (g.T + g.tile_rows - 1) / g.tile_rows;
     const int64_t expected = g.tiles ? std::min<int64_t>(slots, g.expected_tiles) : slots;
     if (row_tiles > 65535 || slots > 65535) return MSE_ERR_UNSUPPORTED_SHAPE;
-    const int64_t resident = (int64_t)sm_count * 2;   // CTAs per SM
-    const int parts = (int)std::max<int64_t>(
-        1, std::min<int64_t>(std::min<int64_t>(8, g.kb / 4), resident / std::max<int64_t>(1, row_tiles * expected)));
+    // One SM's loads bring a k-block every 0.2 to 0.3 us; a cluster costs 2 to 3 us (its launch, two barriers and
+    // the exchange).  So tiles are split when at least four parts of at least four k-blocks fit on the SMs,
+    // two CTAs on each (us with 1, 2 and 4 parts: 64 x 7168 x 6144, 56 tiles, 18.1, 17.0, 15.6; 64 x 12288 x 7168, 96 tiles,
+    // 21.3, 24.1, 29.0; 128 x 1536 x 1536, 24 tiles of 12 k-blocks, 7.6, 10.1, 8.1; 1 x 2112 x 7168 15.7, 11.1, 8.2 and 7.5 with 6).
+    const int64_t most = std::min<int64_t>(g.kb / 4, 2 * (int64_t)sm_count / std::max<int64_t>(1, row_tiles * expected));
+    const int parts = most >= 4 ? (int)std::min<int64_t>(most, 8) : 1;
     const int stream_weights = g.tiles ? g.T <= (int64_t)g.tile_rows * g.groups : slots == 1;
+    // one CTA per SM: its ring gets all of it (not in clusters, of which fewer would fit)
+    const bool whole = parts == 1 && row_tiles * expected <= sm_count;
     cudaError_t e;
     switch (g.epi) {
-        case BLOCK_BF16: e = run_bn<BLOCK_BF16>(tw, tx, g, parts, (int)slots, (int)row_tiles, stream_weights, pdl, s); break;
-        case BLOCK_F32: e = run_bn<BLOCK_F32>(tw, tx, g, parts, (int)slots, (int)row_tiles, stream_weights, pdl, s); break;
-        default: e = run_bn<BLOCK_SWIGLU>(tw, tx, g, parts, (int)slots, (int)row_tiles, stream_weights, pdl, s); break;
+        case BLOCK_BF16: e = run_bn<BLOCK_BF16>(tw, tx, g, parts, (int)slots, (int)row_tiles, stream_weights, whole, pdl, s); break;
+        case BLOCK_F32: e = run_bn<BLOCK_F32>(tw, tx, g, parts, (int)slots, (int)row_tiles, stream_weights, whole, pdl, s); break;
+        default: e = run_bn<BLOCK_SWIGLU>(tw, tx, g, parts, (int)slots, (int)row_tiles, stream_weights, whole, pdl, s); break;
     }
     return e == cudaSuccess ? MSE_OK : MSE_ERR_CUDA;
 }

@@ -40,13 +40,15 @@ template <int BN_, int EPI_>
 struct Cols {
     static constexpr int BN = BN_, EPI = EPI_;
     static constexpr int MATS = EPI == BLOCK_SWIGLU ? 2 : 1;
-    static constexpr int WARPS = 8;                            // promotion warps: two groups of four
-    // Up to 32 columns the groups take k-blocks in turn and halve the columns at the end; with 64 columns
-    // each takes half of them throughout (us by k-blocks and by columns: 32 x 4096 x 2048 7.8 and 8.6,
-    // 16 x 12288 x 7168 18.9 and 19.6, 64 x 12288 x 7168 23.7 and 22.4).
-    static constexpr bool BY_K = BN < 64;
-    static constexpr int CPT = BN / 2;                         // token columns a thread finishes
+    // Promotion: two groups of four warps.  Up to 32 columns of one product they take k-blocks in turn and halve
+    // the columns at the end; with 64, or gate and up, each takes half of them throughout (us by k-blocks and by
+    // columns: 32 x 4096 x 2048 7.8 and 8.6, 16 x 12288 x 7168 18.9 and 19.6, 64 x 12288 x 7168 23.7 and 22.4; experts of 128 tokens
+    // 289 and 283).  Gate and up of 16 columns are one group's (two by k-blocks: a decode batch's experts 210 us, 202).
+    static constexpr bool BY_K = BN < 64 && MATS == 1;
+    static constexpr int GROUPS = BN * MATS == 32 && !BY_K ? 1 : 2, WARPS = 4 * GROUPS;
+    static constexpr int CPT = BN / GROUPS;                    // token columns a thread finishes
     static constexpr int ACC = BY_K ? BN : CPT;                // and sums
+    static_assert(ACC % 16 == 0, "TMEM loads of 16 columns");
     static constexpr int THREADS = 64 + 32 * WARPS;
     static constexpr int BUF = MATS * BN;                      // TMEM columns of one k-block's sums
     static constexpr int NBUF = BUF * 4 <= 256 ? 4 : 2;
@@ -68,6 +70,29 @@ struct Cols {
     static_assert(MATS * BN * 512 <= HALF * STAGE, "halves");
     static_assert(MATS * (BN + 7) * 512 <= HALF * STAGE + kChunk * XS_PITCH * 4, "exchange");
 };
+
+// The token tile of slot z of a dispatch of at most 32 pairs, from the ids themselves: experts ascending, tiles
+// of tile_rows rows.  Every warp finds it alone.
+__device__ __forceinline__ bool tile_of_ids(const BlockGemm &g, int z, int lane, Tile &t) {
+    const int64_t e64 = lane < g.pairs ? (int64_t)g.ids[lane] - g.first_expert : -1;
+    const int e = e64 >= 0 && e64 < g.groups ? (int)e64 : -1;
+    const uint32_t same = __match_any_sync(~0u, e);
+    const int count = e < 0 ? 0 : __popc(same), tiles = (count + g.tile_rows - 1) / g.tile_rows;
+    const bool head = e >= 0 && lane == __ffs(same) - 1;
+    int rows_before = 0, tiles_before = 0;
+    for (int j = 0; j < 32; ++j) {   // the experts before this one, each counted at its first pair
+        const int eo = __shfl_sync(~0u, head ? e : -1, j), co = __shfl_sync(~0u, count, j),
+                  to = __shfl_sync(~0u, tiles, j);
+        if (eo >= 0 && eo < e) { rows_before += co; tiles_before += to; }
+    }
+    const uint32_t owner = __ballot_sync(~0u, head && z >= tiles_before && z < tiles_before + tiles);
+    if (owner == 0) return false;
+    const int from = __ffs(owner) - 1, skip = (z - __shfl_sync(~0u, tiles_before, from)) * g.tile_rows;
+    t.row0 = __shfl_sync(~0u, rows_before, from) + skip;
+    t.rows = min(g.tile_rows, __shfl_sync(~0u, count, from) - skip);
+    t.expert = __shfl_sync(~0u, e, from);
+    return true;
+}
 
 template <typename C>
 __global__ void __launch_bounds__(C::THREADS, C::CTAS)
@@ -110,14 +135,16 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem_base = __shfl_sync(~0u, ctl->tmem_base, 0);
-    // weights_early: the tile table and the weights were complete before this launch could start, and only the
-    // tokens and their scales are the previous kernel's
+    // weights_early: the tile table (or the ids) and the weights were complete before this launch could start, and
+    // only the tokens and their scales are the previous kernel's
     if (!g.weights_early) pdl_wait();
     Tile t;
-    const bool active = tile_of_slot(g, blockIdx.y, t);
-    // Only now may the next kernel of the layer start: what it reads before its own wait is complete.
-    // (A call's last kernel lets nothing start early: its outputs may be anything to the next one.)
-    if (g.tiles) pdl_launch_dependents();
+    const bool active = g.ids ? tile_of_ids(g, blockIdx.y, lane, t) : tile_of_slot(g, blockIdx.y, t);
+    // Only now may the next kernel of the layer start: what it reads before its own wait is complete.  (With ids the
+    // table is not, until the wait is over.  A call's last kernel lets nothing start early: its outputs may be
+    // anything to the next one.)
+    if (g.tiles && !g.ids) pdl_launch_dependents();
+    if (g.ids && !active) pdl_wait();
 
     const int w_row = active ? (int)(t.expert * g.w_group_rows) + m * kBlock : 0;
     int issued = 0;
@@ -140,6 +167,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
         for (int i = 0; i < pre; ++i)
             if (el) weights(i, kb0 + i);
         if (g.weights_early) pdl_wait();
+        if (g.ids) pdl_launch_dependents();
         for (int i = 0; i < pre; ++i)
             if (el) tokens(i, kb0 + i);
         __syncwarp();
@@ -303,7 +331,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
         };
         const int first = part * slice;                          // parts > 1: this CTA's columns
         const int mine = min(min(slice, BN - first), t.rows - first);
-        // and this group's: every other one from `group` on
+        // (this group's: every GROUPS-th from `group` on)
         if constexpr (C::EPI != BLOCK_SWIGLU) {
             auto store = [&](int col, float v) {
                 const int64_t at = (int64_t)(t.row0 + col) * g.ldo + out_n;
@@ -318,7 +346,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
                     for (int c = 0; c < CPT; ++c)
                         if (col0 + c < t.rows) store(col0 + c, acc[0][c]);
                 } else {
-                    for (int at = group; at < mine; at += 2) store(first + at, summed(0, at));
+                    for (int at = group; at < mine; at += C::GROUPS) store(first + at, summed(0, at));
                 }
             }
         } else {
@@ -347,13 +375,13 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
                 for (int c = 0; c < CPT; ++c)
                     if (col0 + c < t.rows) write(col0 + c, acc[0][c]);
             } else {
-                for (int at = group; at < mine; at += 2) {
+                for (int at = group; at < mine; at += C::GROUPS) {
                     const float h = h_of(summed(0, at), summed(MATS - 1, at));
                     red[(size_t)at * 128 + row] = h;             // read again by this thread alone
                     note(first + at, h);
                 }
                 named_barrier_sync(1, kPromo);
-                for (int at = group; at < mine; at += 2) write(first + at, red[(size_t)at * 128 + row]);
+                for (int at = group; at < mine; at += C::GROUPS) write(first + at, red[(size_t)at * 128 + row]);
             }
         }
     }
@@ -418,7 +446,10 @@ mse_status launch_block_cols(const BlockGemm &g, int sm_count, bool pdl, cudaStr
     // two CTAs on each (us with 1, 2 and 4 parts: 64 x 7168 x 6144, 56 tiles, 18.1, 17.0, 15.6; 64 x 12288 x 7168, 96 tiles,
     // 21.3, 24.1, 29.0; 128 x 1536 x 1536, 24 tiles of 12 k-blocks, 7.6, 10.1, 8.1; 1 x 2112 x 7168 15.7, 11.1, 8.2 and 7.5 with 6).
     const int64_t most = std::min<int64_t>(g.kb / 4, 2 * (int64_t)sm_count / std::max<int64_t>(1, row_tiles * expected));
-    const int parts = most >= 4 ? (int)std::min<int64_t>(most, 8) : 1;
+    // Two or three parts where each keeps 40 operand tiles, so that the cluster costs little (the gate_up product of
+    // one token's eight experts of 2048 x 7168, 128 tiles: 39.4 us in two parts, 41.6 whole).
+    const int64_t mats = g.epi == BLOCK_SWIGLU ? 2 : 1;
+    const int parts = most >= 4 ? (int)std::min<int64_t>(most, 8) : most >= 2 && g.kb * mats >= 40 * most ? (int)most : 1;
     const int stream_weights = g.tiles ? g.T <= (int64_t)g.tile_rows * g.groups : slots == 1;
     // one CTA per SM: its ring gets all of it (not in clusters, of which fewer would fit)
     const bool whole = parts == 1 && row_tiles * expected <= sm_count;

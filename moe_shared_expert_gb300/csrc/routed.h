@@ -77,6 +77,9 @@ struct BlockGemm {
     int64_t T;
     const Tile *tiles;
     const int *n_tiles;
+    const int32_t *ids;            // at most 32 pairs: the tile of a slot is found from the ids, not the table
+    int pairs;
+    int64_t first_expert;
     int max_tiles;
     int expected_tiles;            // as the host expects it (chooses grids, not results)
     int tile_rows;

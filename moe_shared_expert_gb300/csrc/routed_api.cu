@@ -276,6 +276,12 @@ mse_status moe_experts_forward(const mse_bf16 *x, int64_t T, int64_t H, const in
     gu.out = o; gu.ldo = I;
     gu.hq = w + L.hq; gu.ldh = pad16(I);
     gu.hs = reinterpret_cast<float *>(w + L.hs); gu.hb = (int)blocks_of(I);
+    if (tensorcore && pairs <= 32 && pdl) {   // a token or a few: their weights are requested while they are dispatched
+        gu.ids = ids;
+        gu.pairs = (int)pairs;
+        gu.first_expert = first_expert;
+        gu.weights_early = 1;
+    }
     if ((st = run_product(gu, tensorcore, d, s)) != MSE_OK) return st;
     if (!tensorcore && (st = from_cuda(launch_quantise_f32(o, dp.n_tiles, dp.tiles, g.max_tiles, I, gu.hq, gu.ldh, gu.hs, pdl, s))) !=
         MSE_OK)

@@ -198,11 +198,11 @@ __global__ void __launch_bounds__(kDispatchThreads) dispatch_kernel(const Dispat
     const int64_t t0 = (int64_t)blockIdx.x * p.chunk;
     const int tokens = (int)min((int64_t)p.chunk, p.T - t0), mine = tokens * p.top_k;
     if (p.hist) {
-        for (int i = tid; i < p.n_chunks * p.E; i += kDispatchThreads) {
+        for (int64_t i = tid; i < (int64_t)p.n_chunks * p.E; i += kDispatchThreads) {
             const int n = p.hist[i];
             if (n == 0) continue;
             atomicAdd(&total[i % p.E], n);
-            if (i / p.E < (int)blockIdx.x) atomicAdd(&before[i % p.E], n);
+            if (i / p.E < blockIdx.x) atomicAdd(&before[i % p.E], n);
         }
     } else {
         for (int64_t i = tid; i < pairs; i += kDispatchThreads) {

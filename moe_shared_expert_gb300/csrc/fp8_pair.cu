@@ -27,7 +27,7 @@ constexpr int kRun = 128 / kParts;             // columns in each of a thread's 
 constexpr int kThreads = 128 + 32 * kPromoWarps;
 // registers: 384 threads x 168 at launch = 128 x 56 + 256 x 224 afterwards
 constexpr int kLaunchRegs = 168;
-constexpr int kBand = 8;                       // token tiles whose weight tiles are taken in turn (L2 reuse)
+constexpr int kBand = 16;                       // token tiles whose weight tiles are taken in turn (L2 reuse)
 constexpr uint32_t kStage = 2 * kOperandTile;  // per CTA: 128 token rows, 128 weight rows
 
 struct PairCtrl {
@@ -260,9 +260,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 uint8_t *mine = staging + (warp - 4) * kStaging;
                 const int64_t first = t.row0 + (int)rank * 128 + q * 32;
                 const int left = min(t.rows - (int)rank * 128 - q * 32, 32);   // valid rows of this warp
-#pragma unroll
-                for (int c = 0; c < 2 * kRun; c += kPass) {
-                    if (c0 + c >= g.N) break;
+                auto stage = [&](int c) {   // columns c .. c + kPass of the warp's rows
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
                         const float *v = acc + c + i * kWord;
@@ -277,7 +275,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                         *reinterpret_cast<uint4 *>(mine + lane * 128 + (i ^ (lane & 7)) * 16) = w;
                     }
                     __syncwarp();
-                    if (aligned && c0 + c + kPass <= g.N) {
+                };
+                if (aligned && c0 + 2 * kRun <= g.N) {
+#pragma unroll
+                    for (int c = 0; c < 2 * kRun; c += kPass) {
+                        stage(c);
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
                             const int rr = i * 4 + lane / 8;
@@ -286,15 +288,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                             if (rr < left)
                                 *reinterpret_cast<uint4 *>(out + (first + rr) * g.ldo + c0 + c + (lane & 7) * kWord) = w;
                         }
-                    } else {   // rows that start anywhere, or end inside: neighbouring columns by neighbouring lanes
+                        __syncwarp();
+                    }
+                } else {   // rows that start anywhere, or end inside: neighbouring columns by neighbouring lanes
+#pragma unroll
+                    for (int c = 0; c < 2 * kRun; c += kPass) {
+                        if (c0 + c >= g.N) break;
+                        stage(c);
                         for (int rr = 0; rr < left; ++rr)
 #pragma unroll
                             for (int j = lane; j < kPass; j += 32)
                                 if (c0 + c + j < g.N)
                                     out[(first + rr) * g.ldo + c0 + c + j] = *reinterpret_cast<const Out *>(
                                         mine + rr * 128 + ((j / kWord) ^ (rr & 7)) * 16 + j % kWord * sizeof(Out));
+                        __syncwarp();
                     }
-                    __syncwarp();
                 }
             }
         }

@@ -88,14 +88,17 @@ def experts(x, ids, weights, wgu, sgu, wd, sd, first=0, shared=None):
     I = wd.shape[2]
     nb = blocks(I)
     xr = spread_rows(*rounded(x.double()))
+    gate = [weight(wgu[e, :I], sgu[e, :nb]) for e in range(wd.shape[0])]
+    up = [weight(wgu[e, I:], sgu[e, nb:]) for e in range(wd.shape[0])]
+    down = [weight(wd[e], sd[e]) for e in range(wd.shape[0])]
     y = torch.zeros_like(xr) if shared is None else shared.double().clone()
     for t in range(x.shape[0]):
         for j in range(ids.shape[1]):
             e = int(ids[t, j]) - first
             if not 0 <= e < wd.shape[0]:
                 continue
-            g = weight(wgu[e, :I], sgu[e, :nb]) @ xr[t]
-            u = weight(wgu[e, I:], sgu[e, nb:]) @ xr[t]
+            g = gate[e] @ xr[t]
+            u = up[e] @ xr[t]
             h = spread_rows(*rounded(g / (1 + torch.exp(-g)) * u))
-            y[t] += weights[t, j].double() * (weight(wd[e], sd[e]) @ h)
+            y[t] += weights[t, j].double() * (down[e] @ h)
     return y

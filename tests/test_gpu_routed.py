@@ -114,6 +114,35 @@ def test_route_closed_experts(scoring, dtype):
     assert ids.cpu().tolist() == [[13, -1, -1]] and w.cpu()[0, 1:].tolist() == [0, 0]
 
 
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+def test_route_of_crowded_scores(scoring):
+    # more experts near the top_k-th best than are ranked at once: saturated, tiny and equal scores
+    E = 300
+    g = gen(41)
+    rows = [torch.full((E,), 30.0), torch.full((E,), -90.0), torch.zeros(E), torch.randn(E, generator=g) * 1e-4,
+            torch.cat([torch.full((150,), 20.0), torch.full((150,), -20.0)]), torch.randn(E, generator=g) * 30 - 200,
+            torch.cat([torch.tensor([50.0]), torch.zeros(E - 1)])]
+    logits = torch.stack(rows)
+    logits[3, 100:] = logits[3, 0]
+    for bias in (None, torch.linspace(0, 1e-3, E)):
+        ids, w = mse.moe_route(logits.cuda(), 8, scoring=scoring, bias=None if bias is None else bias.cuda())
+        l = logits                                         # in 32 bits, as the choices are defined
+        s = 1.0 / (1.0 + torch.exp(-l)) if scoring == "sigmoid" else torch.softmax(l.double(), 1).float()
+        c = s if bias is None else s + bias
+        ids, w = ids.cpu().long(), w.cpu()
+        for t in range(len(rows)):
+            best = c[t].sort(descending=True, stable=True)
+            # nothing left out is better than what was taken by more than 32-bit rounding
+            taken = c[t][ids[t]]
+            assert len(set(ids[t].tolist())) == 8 and torch.all(ids[t] >= 0)
+            assert torch.all((taken - best.values[:8]).abs() <= 8 * EPS32 * (best.values[:8].abs() + 1e-30) + 1e-42)
+            want = s[t][ids[t]].double()
+            if want.sum() > 0:
+                assert torch.allclose(w[t].double(), want / want.sum(), rtol=1e-5, atol=1e-6)
+    same, _ = mse.moe_route(logits[:3].cuda(), 8, scoring=scoring)
+    assert same.cpu().tolist() == [list(range(8))] * 3
+
+
 def test_route_of_a_pitched_view_and_extreme_logits():
     big = torch.randn(7, 100, generator=gen(4))
     big[1] = 80.0
@@ -180,7 +209,7 @@ def assert_product(got, x_values, w_values, roundings=2.0 ** -8):
 MATMULS = [
     (1, 1, 1), (1, 2112, 7168), (2, 128, 128), (3, 130, 257), (16, 256, 384), (17, 300, 1000), (64, 1000, 640),
     (65, 384, 2048), (100, 131, 4100), (129, 128, 520), (200, 700, 130), (257, 513, 1024), (333, 2111, 610),
-    (600, 256, 128), (1030, 260, 784),
+    (600, 256, 128), (1030, 260, 784), (2, 11000, 4500), (33, 9000, 300), (520, 5001, 300), (300, 4000, 5000),
 ]
 
 
@@ -204,6 +233,36 @@ def test_matmul_and_linear(T, N, K, path):
     ws_buf = mse.new_fp8_linear_workspace(T + 5, N, K)
     ws_buf.fill_(0xFF)
     assert torch.equal(mse.fp8_block_linear(x.cuda(), wq, ws, workspace=ws_buf), y)
+
+
+def test_forced_tensor_cores_refuse_what_they_cannot_serve():
+    T, N, K = 5, 130, 200
+    x = torch.randn(T, K, generator=gen(31)).to(torch.bfloat16).cuda()
+    wq, ws = mse.fp8_block_quantise(torch.randn(N, K, generator=gen(32)).to(torch.bfloat16).cuda(), block_rows=128)
+    odd = torch.zeros(N, K + 1, dtype=torch.uint8, device="cuda")[:, :K]
+    odd.copy_(wq.view(torch.uint8))
+    with kernel_path(mse.PATH_TENSORCORE):
+        y = mse.fp8_block_linear(x, wq, ws)
+        with pytest.raises(mse.MSEError, match="MSE_ERR_UNSUPPORTED_SHAPE"):
+            mse.fp8_block_linear(x, odd, ws)
+    assert_product(y, ref.spread_rows(*ref.rounded(x.cpu().double())), ref.weight(wq.cpu(), ws.cpu()))
+
+
+def test_bindings_refuse_on_the_gpu():
+    x = torch.zeros(4, 64, dtype=torch.bfloat16, device="cuda")
+    wq, ws = mse.fp8_block_quantise(torch.ones(8, 64, dtype=torch.bfloat16, device="cuda"), block_rows=128)
+    for bad in (dict(x=x.t()), dict(x=x.float()), dict(x=x[:, :60]), dict(wq=wq.t()), dict(ws=ws.double()),
+                dict(y=torch.empty(4, 9, device="cuda", dtype=torch.bfloat16)), dict(x=x[:0])):
+        a = dict(x=x, wq=wq, ws=ws, y=None)
+        a.update(bad)
+        with pytest.raises((ValueError, mse.MSEError)):
+            mse.fp8_block_linear(a["x"], a["wq"], a["ws"], y=a["y"])
+    with pytest.raises(ValueError):
+        mse.moe_route(x, 2, scoring="relu")
+    with pytest.raises(mse.MSEError):
+        mse.moe_route(x, 65)
+    with pytest.raises(ValueError):
+        mse.moe_route(x, 2, bias=torch.zeros(63, device="cuda"))
 
 
 def test_matmul_takes_any_pitch_and_alignment():
@@ -275,6 +334,11 @@ EXPERTS = [
     (70, 2, 2, 1, 256, 200, True),
     (150, 5, 10, 4, 384, 128, True),
     (530, 3, 4, 2, 256, 300, False),
+    (4, 5, 5, 5, 256, 128, True),          # up to 32 pairs: tiles from the ids
+    (1, 40, 64, 32, 128, 128, False),
+    (30, 300, 400, 9, 128, 60, True),      # more experts than pairs of any
+    (1100, 4, 5, 4, 128, 130, True),       # above 4096 pairs: counted apart
+    (700, 9, 9, 7, 200, 128, False),
 ]
 
 
@@ -303,6 +367,22 @@ def test_experts(case, path):
     else:
         mse.moe_experts_forward(*args, first_expert=first, shared=out, y=out, workspace=buf)
     assert torch.equal(out, y)
+
+
+def test_experts_of_a_few_tokens_with_repeated_ids(path):
+    # up to 32 pairs: repeated experts of one token, experts with more pairs than a tile has rows, holes
+    E, H, I = 7, 256, 128
+    weights = make_experts(E, H, I, 23)
+    cpu = [t.cpu().float() if i % 2 == 0 else t.cpu() for i, t in enumerate(weights)]
+    for T, k, fill in ((1, 32, "one"), (2, 16, "two"), (4, 8, "any"), (1, 1, "any"), (3, 7, "holes")):
+        g = gen(T + k)
+        x = torch.randn(T, H, generator=g).to(torch.bfloat16)
+        ids = {"one": torch.full((T, k), 5), "two": torch.arange(T * k).view(T, k) % 2 * 3 + 1,
+               "any": torch.randint(0, E, (T, k), generator=g),
+               "holes": torch.randint(-3, E + 3, (T, k), generator=g)}[fill].to(torch.int32)
+        w = torch.rand(T, k, generator=g)
+        y = mse.moe_experts_forward(x.cuda(), ids.cuda(), w.cuda(), *weights)
+        assert_experts(y, ref.experts(x, ids, w, *cpu))
 
 
 def test_experts_without_a_pair(path):

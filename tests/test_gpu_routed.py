@@ -469,3 +469,15 @@ def test_experts_beside_the_shared_expert():
     cpu = [t.cpu().float() if i % 2 == 0 else t.cpu() for i, t in enumerate(weights)]
     assert_experts(y, ref.experts(x.cpu(), ids.cpu(), w.cpu(), *cpu, shared=shared.cpu()))
     assert torch.equal(z, mse.mlp_swiglu_forward(y, wgu, wd))
+
+
+def test_example_layer():
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, os.path.join(root, "examples", "moe_layer.py"), "--tokens", "24", "--experts", "6",
+                        "--top-k", "2", "--hidden", "512", "--intermediate", "256", "--steps", "3", "--check"],
+                       capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stdout + r.stderr
+    assert "us a layer" in r.stdout

@@ -7,6 +7,7 @@ from __future__ import annotations
 
 import os
 import subprocess
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -15,6 +16,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmse.so")
+CALLS = os.path.join(PKG, "_calls.so")   # vectorcall entry of the routed-expert calls
 SOURCES = ["api.cu", "tc.cu", "simt.cu", "elementwise.cu", "static_scratch.cu", "route.cu", "fp8.cu", "fp8_cols.cu", "fp8_pair.cu",
            "routed_api.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -32,9 +34,25 @@ def _deps() -> list[str]:
     return deps
 
 
+def _build_calls() -> None:
+    """The Python entry in C.  Without Python's headers there is none, and the same calls go through ctypes."""
+    include = sysconfig.get_paths()["include"]
+    if not os.path.exists(os.path.join(include, "Python.h")):
+        return
+    tmp = CALLS + f".{os.getpid()}.tmp"
+    cmd = ["gcc", "-O2", "-std=gnu11", "-shared", "-fPIC", "-fvisibility=hidden", "-Wall", "-Wextra", "-I", include,
+           "-I", INCLUDE, os.path.join(CSRC, "calls.c"), "-o", tmp]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"gcc failed for calls.c:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, CALLS)
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     newest = max(os.path.getmtime(d) for d in _deps())
+    if force or not os.path.exists(CALLS) or os.path.getmtime(CALLS) < newest:
+        _build_calls()
     if not force and os.path.exists(LIB) and os.path.getmtime(LIB) >= newest:
         return LIB
     nvcc = _nvcc()

@@ -7,8 +7,12 @@ dimension is contiguous; their rows may have a pitch.  Rows whose pitch is a mul
 """
 from __future__ import annotations
 
+import ctypes
+import os
 
 import moe_shared_expert_gb300 as _mse
+
+from . import _build
 
 _BLOCK = 128
 _SCORING = {"softmax": 0, "sigmoid": 1}
@@ -18,9 +22,16 @@ torch = None   # set by _load(); the package itself imports without it
 def _load():
     """torch, the library's functions and the dtypes, looked up once: a call's own Python is most of what a
     single token's operators cost."""
-    global torch, _C, _BF16, _F32, _E4M3, _raw_stream
+    global torch, _C, _BF16, _F32, _E4M3, _raw_stream, _call_route, _call_linear, _call_matmul, _call_experts
     import torch as _torch
-    _C = _mse.lib()
+    _C = C = _mse.lib()
+    entries = C.moe_route, C.fp8_block_linear, C.fp8_block_matmul, C.moe_experts_forward
+    _call_route, _call_linear, _call_matmul, _call_experts = entries
+    if os.path.exists(_build.CALLS):   # the same functions without ctypes' conversions
+        from . import _calls
+        _calls.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in entries))
+        _call_route, _call_linear = _calls.moe_route, _calls.fp8_block_linear
+        _call_matmul, _call_experts = _calls.fp8_block_matmul, _calls.moe_experts_forward
     _BF16, _F32, _E4M3 = _torch.bfloat16, _torch.float32, (_torch.float8_e4m3fn, _torch.uint8)
     # the current stream's handle without making a Stream object, where this torch has it
     _raw_stream = getattr(_torch._C, "_cuda_getCurrentRawStream", None) or (
@@ -101,7 +112,7 @@ def moe_route(logits, top_k, scoring="sigmoid", bias=None, n_group=1, topk_group
         weights = _empty(stream, (T, max(top_k, 0)), _F32, logits.device)
     else:
         _dense(weights, "weights", _F32, (T, top_k))
-    st = _C.moe_route(logits.data_ptr(), int(logits.dtype is _F32), T, E, ld, None if bias is None else bias.data_ptr(),
+    st = _call_route(logits.data_ptr(), int(logits.dtype is _F32), T, E, ld, None if bias is None else bias.data_ptr(),
                       _SCORING[scoring], n_group, topk_group, group_top, top_k, 1 if renormalise else 0, scale,
                       ids.data_ptr(), weights.data_ptr(), T * top_k, _handle(stream, logits))
     if st:
@@ -157,7 +168,7 @@ def fp8_block_matmul(xq, xs, wq, ws, out_dtype=None, out=None, stream=None):
     _dense(xs, "xs", _F32, (T, _blocks(K)))
     _dense(ws, "ws", _F32, (_blocks(N), _blocks(K)))
     out, code = _out(out, out_dtype, "out", (T, N), xq, stream)
-    st = _C.fp8_block_matmul(xq.data_ptr(), ldx, xs.data_ptr(), wq.data_ptr(), ldw, ws.data_ptr(), T, N, K,
+    st = _call_matmul(xq.data_ptr(), ldx, xs.data_ptr(), wq.data_ptr(), ldw, ws.data_ptr(), T, N, K,
                              out.data_ptr(), code, T * N, _handle(stream, xq))
     if st:
         _mse._check("fp8_block_matmul", st)
@@ -191,7 +202,7 @@ def fp8_block_linear(x, wq, ws, y_dtype=None, y=None, workspace=None, stream=Non
     y, code = _out(y, y_dtype, "y", (T, N), x, stream)
     if workspace is None:
         workspace = _own_stream(new_fp8_linear_workspace(T, N, K, x.device), stream)
-    st = _C.fp8_block_linear(x.data_ptr(), ldx, wq.data_ptr(), ldw, ws.data_ptr(), T, N, K, y.data_ptr(), code, T * N,
+    st = _call_linear(x.data_ptr(), ldx, wq.data_ptr(), ldw, ws.data_ptr(), T, N, K, y.data_ptr(), code, T * N,
                              workspace.data_ptr(), workspace.nbytes, _handle(stream, x))
     if st:
         _mse._check("fp8_block_linear", st)
@@ -242,7 +253,7 @@ def moe_experts_forward(x, ids, weights, w_gate_up, s_gate_up, w_down, s_down, f
         _dense(y, "y", _BF16, (T, H))
     if workspace is None:
         workspace = _own_stream(new_moe_workspace(T, k, E, H, I, x.device), stream)
-    st = _C.moe_experts_forward(x.data_ptr(), T, H, ids.data_ptr(), weights.data_ptr(), k, w_gate_up.data_ptr(), ld_gu,
+    st = _call_experts(x.data_ptr(), T, H, ids.data_ptr(), weights.data_ptr(), k, w_gate_up.data_ptr(), ld_gu,
                                 s_gate_up.data_ptr(), w_down.data_ptr(), ld_dn, s_down.data_ptr(), E, I, first_expert,
                                 None if shared is None else shared.data_ptr(), y.data_ptr(), T * H,
                                 workspace.data_ptr(), workspace.nbytes, _handle(stream, x))

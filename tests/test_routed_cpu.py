@@ -117,3 +117,34 @@ def test_bindings_refuse():
         mse.fp8_block_linear(x, x, x)
     with pytest.raises(ValueError):
         mse.moe_experts_forward(None, None, None, None, None, None, None)
+
+
+def test_calls_in_c_take_the_arguments_of_the_library(L):
+    import ctypes
+    import os
+    import sysconfig
+    if not os.path.exists(os.path.join(sysconfig.get_paths()["include"], "Python.h")):
+        pytest.skip("no Python headers: calls go through ctypes")
+    from moe_shared_expert_gb300 import _calls
+    names = ("moe_route", "fp8_block_linear", "fp8_block_matmul", "moe_experts_forward")
+    _calls.bind(*(ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in names))
+    calls = {
+        "moe_route": [FAKE, mse.F32, 4, 64, 64, None, 1, 7, 4, 2, 8, 1, 1.0, FAKE, FAKE, 32, None],
+        "fp8_block_linear": [FAKE, 500, FAKE, 512, FAKE, 3, 7, 500, FAKE, 0, 20, FAKE, 1 << 21, None],
+        "fp8_block_matmul": [FAKE, 512, FAKE, FAKE, 512, FAKE, 3, 7, 500, FAKE, 0, 20, None],
+        "moe_experts_forward": [FAKE, 3, 256, FAKE, FAKE, 2, FAKE, 256, FAKE, FAKE, 128, FAKE, 4, 128, 0, None, FAKE,
+                                3 * 256 - 1, FAKE, 1 << 30, None],
+    }
+    want = {"moe_route": "MSE_ERR_NOT_DIVISIBLE"}
+    for name, a in calls.items():
+        f = getattr(_calls, name)
+        assert f(*a) == getattr(L, name)(*a) == code(want.get(name, "MSE_ERR_GEOMETRY")), name
+        # every pointer argument in turn: null is refused alike
+        for i, v in enumerate(a):
+            b = [*a[:i], None if v == FAKE else 0, *a[i + 1:]]
+            if v is not None and not isinstance(v, float):
+                assert f(*b) == getattr(L, name)(*b), (name, i)
+        with pytest.raises(TypeError):
+            f(*a[:-1])
+        with pytest.raises(TypeError):
+            f("x", *a[1:])

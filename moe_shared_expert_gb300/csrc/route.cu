@@ -36,12 +36,12 @@ __device__ __forceinline__ float warp_fmax(float v) {
 }
 
 // a / b to nearest, with inv = 1 / b to nearest: one residual step makes the product exact to the last
-// bit (Markstein); tiny quotients, whose residual could be cut off, take the division itself.
+// bit (Markstein), 0 included.  Not for tiny a, whose residual is cut off: they take the division itself.
 __device__ __forceinline__ float quotient(float a, float b, float inv) {
-    if (a < 1e-30f) return __fdiv_rn(a, b);
     const float q = __fmul_rn(a, inv);
     return fmaf(fmaf(-b, q, a), inv, q);
 }
+__device__ __forceinline__ bool is_tiny(float a) { return a < 1e-30f && a > 0.f; }
 
 // Bit g * lanes for each group g that stays: the topk_group largest values, equal ones to the lower group.
 // choices: this warp's in shared memory (-inf: closed), group g's from g * pitch on (a pitch of `lanes` more than
@@ -77,7 +77,7 @@ __device__ __forceinline__ uint32_t best_groups(const RouteParams &p, const floa
 }
 
 template <int VPL, bool BF16, bool GROUPS>
-__global__ void __launch_bounds__(kRouteWarps * 32, VPL <= 12 ? 4 : 1) route_kernel(const RouteParams p) {
+__global__ void __launch_bounds__(kRouteWarps * 32, VPL <= 8 ? 5 : VPL <= 16 ? 4 : 2) route_kernel(const RouteParams p) {
     extern __shared__ float route_smem[];
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, warps = blockDim.x / 32;
     // up to 32 candidates, then (groups) the choices and the scores of all experts
@@ -87,14 +87,22 @@ __global__ void __launch_bounds__(kRouteWarps * 32, VPL <= 12 ? 4 : 1) route_ker
     const int lanes = p.group_lanes, pitch = p.group_size + lanes;
     float *all_scores = all_choices + p.n_group * pitch;
     pdl_wait();
-    float bias[VPL];
-    int shift[VPL];   // g * lanes of the expert's group g: its bit among the kept ones
+    // Up to 384 experts a warp keeps their biases and groups from token to token; with more, warps on the SM
+    // are worth more than these registers (23405 x 448 in 8 groups 45 us, 98 with them).
+    constexpr bool KEEP = VPL <= 12;
+    float bias[KEEP ? VPL : 1] = {};
+    int shift[KEEP && GROUPS ? VPL : 1] = {};   // g * lanes of the expert's group g: its bit among the kept ones
+    auto load_bias = [&](int i) { return p.bias && i * 32 + lane < p.E ? __ldg(p.bias + i * 32 + lane) : 0.f; };
+    auto find_shift = [&](int i) { return (int)((uint32_t)(i * 32 + lane) * (uint32_t)p.group_magic >> 20) * lanes; };
+    if constexpr (KEEP) {
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-        const int e = i * 32 + lane;
-        bias[i] = p.bias && e < p.E ? __ldg(p.bias + e) : 0.f;
-        shift[i] = GROUPS ? (int)((uint32_t)e * (uint32_t)p.group_magic >> 20) * lanes : 0;   // e / group_size
+        for (int i = 0; i < VPL; ++i) {
+            bias[i] = load_bias(i);
+            if constexpr (GROUPS) shift[i] = find_shift(i);
+        }
     }
+    auto bias_of = [&](int i) { return KEEP ? bias[KEEP ? i : 0] : load_bias(i); };
+    auto shift_of = [&](int i) { return KEEP && GROUPS ? shift[KEEP && GROUPS ? i : 0] : find_shift(i); };
     for (int64_t t = (int64_t)blockIdx.x * warps + warp; t < p.T; t += (int64_t)gridDim.x * warps) {
         float v[VPL];        // logit (-inf: closed), then the softmax's term, then the choice
         uint32_t open = 0;   // bit i
@@ -131,30 +139,33 @@ __global__ void __launch_bounds__(kRouteWarps * 32, VPL <= 12 ? 4 : 1) route_ker
             sum = fmaxf(fmaf((float)lo, 0x1p-36f, (float)hi * 0x1p-14f), 1e-30f);
             inv = __frcp_rn(sum);
         }
+        auto divided = [&](float e) { return is_tiny(e) ? __fdiv_rn(e, sum) : quotient(e, sum, inv); };
         auto score_of = [&](float logit) {   // exact
             return p.sigmoid ? __frcp_rn(__fadd_rn(1.0f, expf(-logit)))
-                             : quotient(expf(__fsub_rn(logit, top)), sum, inv);
+                             : divided(expf(__fsub_rn(logit, top)));
         };
 #pragma unroll
         for (int i = 0; i < VPL; ++i) {
             float c;
             if constexpr (GROUPS) {
-                const float sc = p.sigmoid ? __frcp_rn(__fadd_rn(1.0f, expf(-v[i]))) : quotient(v[i], sum, inv);
+                const float sc = p.sigmoid ? __frcp_rn(__fadd_rn(1.0f, expf(-v[i]))) : divided(v[i]);
                 if (i * 32 + lane < p.E) all_scores[i * 32 + lane] = sc;
-                c = __fadd_rn(sc, bias[i]);
+                c = __fadd_rn(sc, bias_of(i));
             } else
-                c = p.sigmoid ? __fdividef(1.0f, 1.0f + __expf(-v[i])) + bias[i] : fmaf(v[i], inv, bias[i]);
+                c = p.sigmoid ? __fdividef(1.0f, 1.0f + __expf(-v[i])) + bias_of(i)
+                              : fmaf(v[i], inv, bias_of(i));
             v[i] = open >> i & 1u ? c : -INFINITY;
         }
         if constexpr (GROUPS) {
 #pragma unroll
             for (int i = 0; i < VPL; ++i)
-                if (i * 32 + lane < p.E) all_choices[shift[i] + i * 32 + lane] = v[i];   // g * pitch + e % group_size
+                if (i * 32 + lane < p.E)
+                    all_choices[shift_of(i) + i * 32 + lane] = v[i];   // g * pitch + e % group_size
             __syncwarp();
             const uint32_t kept = best_groups(p, all_choices, pitch, lanes, lane);
 #pragma unroll
             for (int i = 0; i < VPL; ++i)
-                if (!(kept >> (shift[i] & 31) & 1u)) v[i] = -INFINITY;
+                if (!(kept >> (shift_of(i) & 31) & 1u)) v[i] = -INFINITY;
         }
         // as many lanes as top_k hold a choice at least as large as the bound
         float lane_best = -INFINITY, bound = -INFINITY;
@@ -270,7 +281,7 @@ cudaError_t launch_vpl(RouteParams p, int sm_count, bool pdl, cudaStream_t s) {
                                             : cudaFuncSetAttribute(route_kernel<VPL, false, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return e;
     }
-    // a warp keeps its experts' biases and groups from token to token
+    // as many CTAs as can be resident, and then some
     const dim3 grid((unsigned)std::min<int64_t>((p.T + warps - 1) / warps, (int64_t)sm_count * 8));
     const int threads = warps * 32;
     if (p.n_group > 1)
@@ -291,7 +302,8 @@ cudaError_t launch_route(const RouteParams &p, int sm_count, bool pdl, cudaStrea
         case 6: return launch_vpl<6>(p, sm_count, pdl, s);
         case 7: case 8: return launch_vpl<8>(p, sm_count, pdl, s);
         case 9: case 10: case 11: case 12: return launch_vpl<12>(p, sm_count, pdl, s);
-        case 13: case 14: case 15: case 16: return launch_vpl<16>(p, sm_count, pdl, s);
+        case 13: case 14: return launch_vpl<14>(p, sm_count, pdl, s);
+        case 15: case 16: return launch_vpl<16>(p, sm_count, pdl, s);
         default: return launch_vpl<32>(p, sm_count, pdl, s);
     }
 }

@@ -143,7 +143,9 @@ mse_status moe_route(const void *logits, mse_dtype logits_dtype, int64_t T, int6
     p.logits = logits; p.bf16_logits = logits_dtype == MSE_BF16;
     p.T = T; p.ld = ld; p.E = (int)E; p.bias = bias;
     p.sigmoid = scoring == MSE_SCORE_SIGMOID;
-    p.n_group = n_group; p.group_size = (int)(E / n_group); p.topk_group = topk_group; p.group_top = group_top;
+    // where every group stays there are none to choose
+    p.n_group = topk_group == n_group ? 1 : n_group;
+    p.group_size = (int)(E / p.n_group); p.topk_group = topk_group; p.group_top = group_top;
     p.top_k = top_k; p.renormalise = renormalise != 0; p.scale = scale;
     p.ids = ids; p.weights = weights;
     return from_cuda(launch_route(p, d.sm_count, pdl_enabled(), static_cast<cudaStream_t>(stream)));

@@ -10,7 +10,7 @@
 // sums through distributed shared memory and each finish a slice of the token columns, in
 // rank order.
 //
-// Warp 0 loads (TMA), warp 1 issues MMAs, the others promote.
+// Warp 0 loads (TMA), warp 1 issues MMAs, the others promote (and, for a few tokens in bf16, round them).
 #include <atomic>
 
 #include "device.h"
@@ -23,6 +23,8 @@ namespace {
 
 constexpr int kChunk = 32;       // k-blocks whose scales are in shared memory at a time
 constexpr int kMaxColsStages = 9;
+constexpr int kXsRing = 16;      // k-blocks of token scales, where the kernel rounds the tokens itself
+constexpr int kRoundQuads = kRoundRows / 4;
 
 constexpr int pow2_up(int v) {
     int p = 32;
@@ -31,14 +33,22 @@ constexpr int pow2_up(int v) {
 }
 
 struct ColsCtrl {
-    uint64_t full[kMaxColsStages], empty[kMaxColsStages], tfull[4], tempty[4], drain;
+    uint64_t full[kMaxColsStages], empty[kMaxColsStages], tfull[4], tempty[4], xs_full[kXsRing], drain;
     uint32_t tmem_base;
     int abort_flag;
 };
 
-template <int BN_, int EPI_>
+// ROUND: the tokens come in bf16, and four more warps round them to 8 bits, each every fourth k-block, straight into
+// the ring: up to kRoundRows tokens of a plain product need no launch of their own for that.
+template <int BN_, int EPI_, bool ROUND_ = false>
 struct Cols {
     static constexpr int BN = BN_, EPI = EPI_;
+    static constexpr bool ROUND = ROUND_;
+    static constexpr int ROUND_WARPS = ROUND ? 4 : 0;
+    static_assert(!ROUND || (BN == 16 && EPI != BLOCK_SWIGLU), "a plain product of few tokens");
+    // slot i mod kXsRing is written again only when the promotion is past it: the ring and the TMEM buffers bound
+    // how far it lags
+    static_assert(!ROUND || kMaxColsStages + 4 < kXsRing, "scales");
     static constexpr int MATS = EPI == BLOCK_SWIGLU ? 2 : 1;
     // Promotion: two groups of four warps.  Up to 32 columns of one product they take k-blocks in turn and halve
     // the columns at the end; with 64, or gate and up, each takes half of them throughout (us by k-blocks and by
@@ -49,7 +59,7 @@ struct Cols {
     static constexpr int CPT = BN / GROUPS;                    // token columns a thread finishes
     static constexpr int ACC = BY_K ? BN : CPT;                // and sums
     static_assert(ACC % 16 == 0, "TMEM loads of 16 columns");
-    static constexpr int THREADS = 64 + 32 * WARPS;
+    static constexpr int THREADS = 64 + 32 * (WARPS + ROUND_WARPS);
     static constexpr int BUF = MATS * BN;                      // TMEM columns of one k-block's sums
     static constexpr int NBUF = BUF * 4 <= 256 ? 4 : 2;
     static constexpr int TMEM = pow2_up(NBUF * BUF);
@@ -114,9 +124,11 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
-            mbar_init(smem_u32(&ctl->full[s]), 1);
+            mbar_init(smem_u32(&ctl->full[s]), C::ROUND ? 2 : 1);
             mbar_init(smem_u32(&ctl->empty[s]), 1);
         }
+        if constexpr (C::ROUND)
+            for (int i = 0; i < kXsRing; ++i) mbar_init(smem_u32(&ctl->xs_full[i]), 1);
         for (int b = 0; b < C::NBUF; ++b) {
             mbar_init(smem_u32(&ctl->tfull[b]), 1);
             mbar_init(smem_u32(&ctl->tempty[b]), C::BY_K ? C::WARPS / 2 : C::WARPS);
@@ -154,13 +166,13 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
         const uint64_t pol_x = l2_policy_evict_last();
         auto weights = [&](int s, int kb) {
             const uint32_t bar = smem_u32(&ctl->full[s]), dst = base + s * C::STAGE;
-            mbar_arrive_expect_tx(bar, C::STAGE);
+            mbar_arrive_expect_tx(bar, C::ROUND ? MATS * kOperandTile : C::STAGE);
             tma_load_2d(dst, &tmW, bar, kb * kBlock, w_row, pol_w);
             if constexpr (MATS == 2)
                 tma_load_2d(dst + kOperandTile, &tmW, bar, kb * kBlock, w_row + (int)g.up_rows, pol_w);
         };
         auto tokens = [&](int s, int kb) {
-            tma_load_2d(base + s * C::STAGE + MATS * kOperandTile, &tmX, smem_u32(&ctl->full[s]), kb * kBlock, t.row0,
+            if constexpr (!C::ROUND) tma_load_2d(base + s * C::STAGE + MATS * kOperandTile, &tmX, smem_u32(&ctl->full[s]), kb * kBlock, t.row0,
                         pol_x);
         };
         const int pre = min(S, n);
@@ -211,9 +223,80 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
         }
     }
 
+    if constexpr (C::ROUND) {
+        if (active && warp >= 2 + C::WARPS) {
+            // Warp w of the four: k-blocks w, w + 4, ..; 8 lanes for a token, 16 values each, four tokens at a time.
+            // The values of its next k-block are on their way while this one's are rounded.
+            const int first = warp - 2 - C::WARPS, sub = lane % 8;
+            auto fetch = [&](int i, int quad, uint32_t (&to)[8]) {
+                const int token = quad * 4 + lane / 8;
+                const int64_t k = (int64_t)(kb0 + i) * kBlock + sub * 16;
+                const uint16_t *x = g.x + (int64_t)(t.row0 + token) * g.ldxb + k;
+#pragma unroll
+                for (int v = 0; v < 8; ++v) to[v] = 0;
+                if (i >= n || token >= t.rows) return;
+                if (g.x_wide && k + 16 <= g.K) {
+                    const uint4 lo = __ldg(reinterpret_cast<const uint4 *>(x));
+                    const uint4 hi = __ldg(reinterpret_cast<const uint4 *>(x) + 1);
+                    to[0] = lo.x; to[1] = lo.y; to[2] = lo.z; to[3] = lo.w;
+                    to[4] = hi.x; to[5] = hi.y; to[6] = hi.z; to[7] = hi.w;
+                } else {
+#pragma unroll
+                    for (int v = 0; v < 8; ++v) {
+                        const uint32_t a = k + 2 * v < g.K ? __ldg(x + 2 * v) : 0u;
+                        const uint32_t b = k + 2 * v + 1 < g.K ? __ldg(x + 2 * v + 1) : 0u;
+                        to[v] = a | (b << 16);
+                    }
+                }
+            };
+            uint32_t next[kRoundQuads][8];
+#pragma unroll
+            for (int quad = 0; quad < kRoundQuads; ++quad)
+                if (quad * 4 < t.rows) fetch(first, quad, next[quad]);
+            bool ok = true;
+            for (int i = first; i < n && ok; i += C::ROUND_WARPS) {
+                const int s = i % S, slot = i % kXsRing;
+                ok = warp_wait(smem_u32(&ctl->empty[s]), (uint32_t)((i / S) & 1) ^ 1u, abort_flag, g);
+                if (!ok) break;
+#pragma unroll
+                for (int quad = 0; quad < kRoundQuads; ++quad) {
+                    if (quad * 4 >= t.rows) break;
+                    uint32_t now[8], top = 0, w[4];
+#pragma unroll
+                    for (int v = 0; v < 8; ++v) now[v] = next[quad][v];
+                    fetch(i + C::ROUND_WARPS, quad, next[quad]);
+                    auto lo = [&](int v) { return __uint_as_float(now[v] << 16); };
+                    auto hi = [&](int v) { return __uint_as_float(now[v] & 0xFFFF0000u); };
+#pragma unroll
+                    for (int v = 0; v < 8; ++v) top = max(top, max(abs_bits(lo(v)), abs_bits(hi(v))));
+#pragma unroll
+                    for (int d = 4; d > 0; d >>= 1) top = max(top, __shfl_xor_sync(~0u, top, d));
+                    const float a = floored_amax(top), inv = __frcp_rn(a);
+#pragma unroll
+                    for (int v = 0; v < 4; ++v)
+                        w[v] = e4m3x2(e4m3_ratio(lo(2 * v), a, inv), e4m3_ratio(hi(2 * v), a, inv)) |
+                               (e4m3x2(e4m3_ratio(lo(2 * v + 1), a, inv), e4m3_ratio(hi(2 * v + 1), a, inv)) << 16);
+                    const int token = quad * 4 + lane / 8;
+                    // the 128-byte swizzle of the operand tiles: 16-byte word `sub` of a row at sub ^ (row mod 8)
+                    *reinterpret_cast<uint4 *>(ring + (size_t)s * C::STAGE + MATS * kOperandTile + token * 128 +
+                                               ((sub ^ (token & 7)) * 16)) = make_uint4(w[0], w[1], w[2], w[3]);
+                    if (sub == 0) xs_s[slot * C::XS_PITCH + token] = block_scale(a);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(smem_u32(&ctl->full[s]));
+                    mbar_arrive(smem_u32(&ctl->xs_full[slot]));
+                }
+            }
+            __syncwarp();
+        }
+    }
+
     float acc[MATS][CPT];
-    const int q = warp & 3, row = q * 32 + lane, group = warp >= 2 ? (warp - 2) / 4 : 0, col0 = group * CPT;
-    if (active && warp >= 2) {
+    const bool promo = warp >= 2 && warp < 2 + C::WARPS;
+    const int q = warp & 3, row = q * 32 + lane, group = promo ? (warp - 2) / 4 : 0, col0 = group * CPT;
+    if (active && promo) {
         float sum[MATS][C::ACC];
 #pragma unroll
         for (int a = 0; a < MATS; ++a)
@@ -226,18 +309,20 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
         for (int c0 = 0; c0 < n; c0 += kChunk) {
             // (a warp whose wait ran out takes the others along: nobody is left at a barrier)
             if (c0 > 0 && !named_barrier_and(1, kPromo, ok)) break;
-            // (all loads before the first store: one trip to L2, not one for each)
-            constexpr int kPer = kChunk * BN / kPromo;
-            float v[kPer];
+            if constexpr (!C::ROUND) {
+                // (all loads before the first store: one trip to L2, not one for each)
+                constexpr int kPer = kChunk * BN / kPromo;
+                float v[kPer];
 #pragma unroll
-            for (int u = 0; u < kPer; ++u) {
-                const int i = pt + u * kPromo, k = i % kChunk, j = i / kChunk;
-                v[u] = j < t.rows && c0 + k < n ? __ldcg(g.xs + (int64_t)(t.row0 + j) * g.kb + kb0 + c0 + k) : 0.f;
-            }
+                for (int u = 0; u < kPer; ++u) {
+                    const int i = pt + u * kPromo, k = i % kChunk, j = i / kChunk;
+                    v[u] = j < t.rows && c0 + k < n ? __ldcg(g.xs + (int64_t)(t.row0 + j) * g.kb + kb0 + c0 + k) : 0.f;
+                }
 #pragma unroll
-            for (int u = 0; u < kPer; ++u) {
-                const int i = pt + u * kPromo;
-                xs_s[i % kChunk * C::XS_PITCH + i / kChunk] = v[u];
+                for (int u = 0; u < kPer; ++u) {
+                    const int i = pt + u * kPromo;
+                    xs_s[i % kChunk * C::XS_PITCH + i / kChunk] = v[u];
+                }
             }
             if (pt < MATS * kChunk && c0 + pt % kChunk < n)
                 ws_s[pt] = __ldg(ws + (pt / kChunk) * g.up_scales + kb0 + c0 + pt % kChunk);
@@ -245,9 +330,11 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
             for (int k = C::BY_K ? group : 0; k < kChunk && c0 + k < n; k += C::BY_K ? 2 : 1) {   // kChunk is even
                 const int i = c0 + k, b = i % C::NBUF;
                 ok = warp_wait(smem_u32(&ctl->tfull[b]), (uint32_t)((i / C::NBUF) & 1), abort_flag, g);
+                if constexpr (C::ROUND)
+                    ok = ok && warp_wait(smem_u32(&ctl->xs_full[i % kXsRing]), (uint32_t)((i / kXsRing) & 1), abort_flag, g);
                 if (!ok) break;
                 tc_fence_after();
-                const float *x = xs_s + k * C::XS_PITCH + (C::BY_K ? 0 : col0);
+                const float *x = xs_s + (C::ROUND ? i % kXsRing : k) * C::XS_PITCH + (C::BY_K ? 0 : col0);
                 const uint32_t src = tmem_base + (uint32_t)(b * C::BUF + (C::BY_K ? 0 : col0)) + ((uint32_t)(q * 32) << 16);
 #pragma unroll
                 for (int c = 0; c < C::ACC; c += 16) {
@@ -305,7 +392,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
     const int slice = (BN + parts - 1) / parts;
     if (parts > 1) {
         cluster_sync();   // every ring of the cluster is idle
-        if (active && warp >= 2) {
+        if (active && promo) {
 #pragma unroll
             for (int c = 0; c < CPT; ++c) {
                 const int col = col0 + c;
@@ -321,7 +408,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
         }
         cluster_sync();
     }
-    if (active && warp >= 2) {
+    if (active && promo) {
         const int64_t out_n = (int64_t)m * kBlock + row;
         const bool valid = out_n < g.N;
         auto summed = [&](int a, int at) {
@@ -423,7 +510,11 @@ template <int EPI>
 cudaError_t run_bn(const CUtensorMap &tw, const CUtensorMap &tx, const BlockGemm &g, int parts, int slots,
                    int row_tiles, int stream_weights, bool whole, bool pdl, cudaStream_t s) {
     switch (g.tile_rows) {
-        case 16: return run<Cols<16, EPI>>(tw, tx, g, parts, slots, row_tiles, stream_weights, whole, pdl, s);
+        case 16:
+            if constexpr (EPI != BLOCK_SWIGLU)
+                if (g.x)
+                    return run<Cols<16, EPI, true>>(tw, tx, g, parts, slots, row_tiles, stream_weights, whole, pdl, s);
+            return run<Cols<16, EPI>>(tw, tx, g, parts, slots, row_tiles, stream_weights, whole, pdl, s);
         case 32: return run<Cols<32, EPI>>(tw, tx, g, parts, slots, row_tiles, stream_weights, whole, pdl, s);
         default: return run<Cols<EPI == BLOCK_SWIGLU ? 32 : 64, EPI>>(tw, tx, g, parts, slots, row_tiles, stream_weights, whole, pdl, s);
     }
@@ -436,7 +527,10 @@ mse_status launch_block_cols(const BlockGemm &g, int sm_count, bool pdl, cudaStr
     CUtensorMap tw, tx;
     mse_status st = map_bytes(&tw, g.wq, g.groups * g.w_group_rows, g.K, g.ldw, kBlock);
     if (st != MSE_OK) return st;
-    if ((st = map_bytes(&tx, g.xq, g.T, g.K, g.ldx, g.tile_rows)) != MSE_OK) return st;
+    if (g.x)
+        tx = tw;   // the kernel rounds x itself
+    else if ((st = map_bytes(&tx, g.xq, g.T, g.K, g.ldx, g.tile_rows)) != MSE_OK)
+        return st;
     const int64_t row_tiles = blocks_of(g.N);
     const int64_t slots = g.tiles ? g.max_tiles : (g.T + g.tile_rows - 1) / g.tile_rows;
     const int64_t expected = g.tiles ? std::min<int64_t>(slots, g.expected_tiles) : slots;

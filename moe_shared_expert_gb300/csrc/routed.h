@@ -66,6 +66,8 @@ cudaError_t launch_combine(const float *o, const int32_t *pos, const float *weig
                            uint16_t *y, int64_t T, int64_t H, int sm_count, bool pdl, cudaStream_t s);
 
 // ------------------------------------------------------------------ block-scaled products
+constexpr int kRoundRows = 8;
+
 enum BlockEpi : int {
     BLOCK_BF16 = 0,      // out bf16
     BLOCK_F32 = 1,       // out fp32
@@ -85,6 +87,8 @@ struct BlockGemm {
     int tile_rows;
     const uint8_t *xq; int64_t ldx;
     const float *xs;               // [rows x kb]
+    const uint16_t *x; int64_t ldxb;   // up to kRoundRows rows of a plain product in bf16, rounded by the product's kernel; or null
+    int x_wide;                    // x in 16-byte words
     const uint8_t *wq; int64_t ldw;
     const float *ws;               // [.. x kb] blocks
     int64_t N, K;                  // weight rows of one product (I for SWIGLU), inner size

@@ -204,9 +204,18 @@ mse_status fp8_block_linear(const mse_bf16 *x, int64_t ldx, const uint8_t *wq, i
     if ((st = choose_tensorcore(tc_operands(xq, ldq, wq, ldw), &tensorcore)) != MSE_OK) return st;
     begin_untracked_call(stream);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
+    BlockGemm g = plain_product(xq, ldq, xs, wq, ldw, ws, T, N, K, y, y_dtype, d.sm_count);
+    // One launch, whose kernel rounds the tokens itself, where the second one costs more than what every CTA
+    // spends on all tokens (us of GPU time with one launch and with two, the host's 5.8 and 7.8: 3 x 904 x 966 6.2, 6.6;
+    // 1 x 2112 x 7168 8.6, 8.2; 8 x 7168 x 6144 14.0, 13.7; 1 x 12288 x 7168 19.7, 18.2; 16 x 1024 x 4096 8.4, 6.9).
+    if (tensorcore && T <= kRoundRows && N * K <= (int64_t)1 << 24) {
+        g.x = x;
+        g.ldxb = ldx;
+        g.x_wide = ldx % 8 == 0 && aligned16(x);
+        return run_product(g, tensorcore, d, s);
+    }
     if ((st = from_cuda(launch_quantise_rows(x, T, K, ldx, xq, ldq, xs, d.sm_count, pdl_enabled(), s))) != MSE_OK)
         return st;
-    BlockGemm g = plain_product(xq, ldq, xs, wq, ldw, ws, T, N, K, y, y_dtype, d.sm_count);
     g.weights_early = 1;
     return run_product(g, tensorcore, d, s);
 }

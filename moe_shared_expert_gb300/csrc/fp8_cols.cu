@@ -76,9 +76,9 @@ struct Cols {
     }
     static constexpr int HALF = fit(113 * 1024), WHOLE = fit(227 * 1024);
     static_assert(HALF >= 2, "ring");
-    // the exchange of a split tile, at most BN + 7 columns of every mat, uses the ring and the tokens' scales
+    // the groups' halves, and the exchange of a split tile (at most BN / 4 + 7 groups of four columns), use the ring
     static_assert(MATS * BN * 512 <= HALF * STAGE, "halves");
-    static_assert(MATS * (BN + 7) * 512 <= HALF * STAGE + kChunk * XS_PITCH * 4, "exchange");
+    static_assert(MATS * (BN / 4 + 7) * 2048 <= HALF * STAGE, "exchange");
 };
 
 // The token tile of slot z of a dispatch of at most 32 pairs, from the ids themselves: experts ascending, tiles
@@ -387,22 +387,23 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
         }
     }
 
-    // ---- the cluster's sums: every CTA gets a slice of the token columns from all, [rank][mat][column][row]
-    float *red = reinterpret_cast<float *>(ring);
-    const int slice = (BN + parts - 1) / parts;
+    // ---- the cluster's sums: every CTA gets a slice of the token columns from all, in groups of four columns:
+    // [rank][mat][group][row] (16-byte stores: 4-byte ones made the exchange of 64 columns 4 us long)
+    float4 *red = reinterpret_cast<float4 *>(ring);
+    const int slice = (BN / 4 + parts - 1) / parts;
     if (parts > 1) {
         cluster_sync();   // every ring of the cluster is idle
         if (active && promo) {
 #pragma unroll
-            for (int c = 0; c < CPT; ++c) {
-                const int col = col0 + c;
-                if (col < t.rows) {
-                    const int to = col / slice, at = col - to * slice;
+            for (int c = 0; c < CPT; c += 4) {
+                const int quad = (col0 + c) / 4;
+                if (quad * 4 < t.rows) {
+                    const int to = quad / slice, at = quad - to * slice;
 #pragma unroll
                     for (int a = 0; a < MATS; ++a)
-                        st_cluster_f32(map_to_rank(smem_u32(red + ((size_t)(part * MATS + a) * slice + at) * 128 + row),
-                                                   (uint32_t)to),
-                                       acc[a][c]);
+                        st_cluster_f32x4(map_to_rank(smem_u32(red + (size_t)((part * MATS + a) * slice + at) * 128 + row),
+                                                     (uint32_t)to),
+                                         make_float4(acc[a][c], acc[a][c + 1], acc[a][c + 2], acc[a][c + 3]));
                 }
             }
         }
@@ -411,13 +412,16 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
     if (active && promo) {
         const int64_t out_n = (int64_t)m * kBlock + row;
         const bool valid = out_n < g.N;
-        auto summed = [&](int a, int at) {
-            float v = 0.f;
-            for (int r = 0; r < parts; ++r) v += red[((size_t)(r * MATS + a) * slice + at) * 128 + row];
+        auto summed = [&](int a, int at) {   // in rank order
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int r = 0; r < parts; ++r) {
+                const float4 o = red[(size_t)((r * MATS + a) * slice + at) * 128 + row];
+                v = make_float4(v.x + o.x, v.y + o.y, v.z + o.z, v.w + o.w);
+            }
             return v;
         };
-        const int first = part * slice;                          // parts > 1: this CTA's columns
-        const int mine = min(min(slice, BN - first), t.rows - first);
+        const int first = part * slice;                                              // parts > 1: this CTA's groups of
+        const int mine = min(min(slice, BN / 4 - first), (t.rows + 3) / 4 - first);  // columns
         // (this group's: every GROUPS-th from `group` on)
         if constexpr (C::EPI != BLOCK_SWIGLU) {
             auto store = [&](int col, float v) {
@@ -433,7 +437,13 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
                     for (int c = 0; c < CPT; ++c)
                         if (col0 + c < t.rows) store(col0 + c, acc[0][c]);
                 } else {
-                    for (int at = group; at < mine; at += C::GROUPS) store(first + at, summed(0, at));
+                    for (int at = group; at < mine; at += C::GROUPS) {
+                        const float4 v = summed(0, at);
+                        const float each[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            if ((first + at) * 4 + j < t.rows) store((first + at) * 4 + j, each[j]);
+                    }
                 }
             }
         } else {
@@ -463,12 +473,22 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
                     if (col0 + c < t.rows) write(col0 + c, acc[0][c]);
             } else {
                 for (int at = group; at < mine; at += C::GROUPS) {
-                    const float h = h_of(summed(0, at), summed(MATS - 1, at));
+                    const float4 gate = summed(0, at), up = summed(MATS - 1, at);
+                    const float4 h = make_float4(h_of(gate.x, up.x), h_of(gate.y, up.y), h_of(gate.z, up.z),
+                                                 h_of(gate.w, up.w));
                     red[(size_t)at * 128 + row] = h;             // read again by this thread alone
-                    note(first + at, h);
+                    const float each[4] = {h.x, h.y, h.z, h.w};
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) note((first + at) * 4 + j, each[j]);
                 }
                 named_barrier_sync(1, kPromo);
-                for (int at = group; at < mine; at += C::GROUPS) write(first + at, red[(size_t)at * 128 + row]);
+                for (int at = group; at < mine; at += C::GROUPS) {
+                    const float4 h = red[(size_t)at * 128 + row];
+                    const float each[4] = {h.x, h.y, h.z, h.w};
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if ((first + at) * 4 + j < t.rows) write((first + at) * 4 + j, each[j]);
+                }
             }
         }
     }
@@ -535,18 +555,22 @@ mse_status launch_block_cols(const BlockGemm &g, int sm_count, bool pdl, cudaStr
     const int64_t slots = g.tiles ? g.max_tiles : (g.T + g.tile_rows - 1) / g.tile_rows;
     const int64_t expected = g.tiles ? std::min<int64_t>(slots, g.expected_tiles) : slots;
     if (row_tiles > 65535 || slots > 65535) return MSE_ERR_UNSUPPORTED_SHAPE;
-    // One SM's loads bring a k-block every 0.2 to 0.3 us; a cluster costs 2 to 3 us (its launch, two barriers and
-    // the exchange).  So tiles are split when at least four parts of at least four k-blocks fit on the SMs,
-    // two CTAs on each (us with 1, 2 and 4 parts: 64 x 7168 x 6144, 56 tiles, 18.1, 17.0, 15.6; 64 x 12288 x 7168, 96 tiles,
-    // 21.3, 24.1, 29.0; 128 x 1536 x 1536, 24 tiles of 12 k-blocks, 7.6, 10.1, 8.1; 1 x 2112 x 7168 15.7, 11.1, 8.2 and 7.5 with 6).
-    const int64_t most = std::min<int64_t>(g.kb / 4, 2 * (int64_t)sm_count / std::max<int64_t>(1, row_tiles * expected));
-    // Two or three parts where each keeps 40 operand tiles, so that the cluster costs little (the gate_up product of
-    // one token's eight experts of 2048 x 7168, 128 tiles: 39.4 us in two parts, 41.6 whole).
-    const int64_t mats = g.epi == BLOCK_SWIGLU ? 2 : 1;
-    const int parts = most >= 4 ? (int)std::min<int64_t>(most, 8) : most >= 2 && g.kb * mats >= 40 * most ? (int)most : 1;
+    // One SM's loads bring a k-block every 0.2 to 0.3 us, so a tile's k-blocks are split over as many CTAs as find
+    // room, two on an SM (nearly: clusters do not fill every last place, and one that waits doubles the time), down to
+    // two k-blocks each: up to five parts (larger clusters find fewer places), eight
+    // where there are few tiles.  (us with 1, 3, 4, 5, 6 and 8 parts: 64 x 12288 x 7168, 96 tiles, 23.5, 19.2, 24.6, ..;
+    // 64 x 7168 x 6144, 56 tiles, 20.1, 14.3, 13.4, 13.6, 18.1, 19.8; 64 x 2048 x 2048, 16 tiles, 9.3, 7.0, 6.4, 6.5, 6.1, 7.5;
+    // 200 x 700 x 1200, 24 tiles, 8.3, 6.8, 6.4, 6.0, 6.8, 7.8; 16 x 1024 x 4096, 8 tiles, 10.7, 7.7, 7.1, 6.9, 6.7, 5.9;
+    // 64 x 7168 x 768, 56 tiles of six k-blocks, 5.9, 7.9.)
+    const int64_t tiles = row_tiles * expected;
+    const int64_t room = std::min<int64_t>(19 * (int64_t)sm_count / 10 / std::max<int64_t>(1, tiles), g.kb < 8 ? 1 : g.kb / 2);
+    int parts = (int)std::min<int64_t>(std::max<int64_t>(room, 1), 16 * tiles <= sm_count && g.kb >= 24 ? 8 : 5);
+    // 16 tokens take less time than the cluster where the tiles already fill most SMs (16 x 12288 x 7168 17.7 us whole,
+    // 18.5 in three parts); gate and up of 16 have two operand tiles for it.
+    if (parts < 4 && g.tile_rows == 16 && g.epi != BLOCK_SWIGLU) parts = 1;
     const int stream_weights = g.tiles ? g.T <= (int64_t)g.tile_rows * g.groups : slots == 1;
     // one CTA per SM: its ring gets all of it (not in clusters, of which fewer would fit)
-    const bool whole = parts == 1 && row_tiles * expected <= sm_count;
+    const bool whole = parts == 1 && tiles <= sm_count;
     cudaError_t e;
     switch (g.epi) {
         case BLOCK_BF16: e = run_bn<BLOCK_BF16>(tw, tx, g, parts, (int)slots, (int)row_tiles, stream_weights, whole, pdl, s); break;

@@ -40,6 +40,12 @@ __device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t cluster_add
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
+// 16 bytes to shared memory of a CTA of the cluster
+__device__ __forceinline__ void st_cluster_f32x4(uint32_t addr, float4 v) {
+    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
+                 : "memory");
+}
+
 // The token tile of slot z: a dispatch's tile, or rows [z tile_rows, ..) of the one group.
 __device__ __forceinline__ bool tile_of_slot(const BlockGemm &g, int z, Tile &t) {
     if (g.tiles) {

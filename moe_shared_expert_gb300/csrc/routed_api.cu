@@ -46,8 +46,8 @@ mse_status check_matmul(const void *xq, int64_t ldx, const void *xs, const void 
 // Plain product.  A CTA pair spends 0.41 us on a k-block of 256 x 256 and there are half as many pairs as
 // SMs; two swap-AB CTAs on an SM spend 0.54 us on a k-block of 128 x 64 each, and split tiles over
 // more CTAs when there are fewer tiles than SMs.  So the pair wins from two waves of swap-AB tiles
-// on, when its own waves are at most two thirds of theirs (us, pair and swap-AB: 256 x 7168 x 6144 23.2 and 26.3,
-// 128 x 12288 x 7168 26.6 and 29.7; 128 x 7168 x 6144 23.1 and 21.5, 512 x 2112 x 7168 25.7 and 23.5).
+// on, when its own waves are at most two thirds of theirs (us, pair and swap-AB: 256 x 7168 x 6144 23.2 and 26.6,
+// 128 x 12288 x 7168 26.9 and 30.0; 128 x 7168 x 6144 23.3 and 18.1, 512 x 2112 x 7168 25.5 and 19.8).
 int plain_tile_rows(int64_t T, int64_t N, int sm_count) {
     if (T <= 32) return T <= 16 ? 16 : 32;
     const int64_t cols = blocks_of(N) * ((T + 63) / 64), pairs = ((T + 255) / 256) * ((N + 255) / 256);

@@ -542,7 +542,22 @@ cudaError_t run_bn(const CUtensorMap &tw, const CUtensorMap &tx, const BlockGemm
 
 }  // namespace
 
-// expected token tiles x weight tiles x parts fill the CTAs that can be resident
+// CTAs that share a tile's k-blocks.
+// One SM's loads bring a k-block every 0.2 to 0.3 us, so a tile's k-blocks are split over as many CTAs as find
+// room, two on an SM (nearly: clusters do not fill every last place, and one that waits doubles the time), down to
+// two k-blocks each: up to five parts (larger clusters find fewer places), eight
+// where there are few tiles.  (us with 1, 3, 4, 5, 6 and 8 parts: 64 x 12288 x 7168, 96 tiles, 23.5, 19.2, 24.6, ..;
+// 64 x 7168 x 6144, 56 tiles, 20.1, 14.3, 13.4, 13.6, 18.1, 19.8; 64 x 2048 x 2048, 16 tiles, 9.3, 7.0, 6.4, 6.5, 6.1, 7.5;
+// 200 x 700 x 1200, 24 tiles, 8.3, 6.8, 6.4, 6.0, 6.8, 7.8; 16 x 1024 x 4096, 8 tiles, 10.7, 7.7, 7.1, 6.9, 6.7, 5.9;
+// 64 x 7168 x 768, 56 tiles of six k-blocks, 5.9, 7.9.)
+int cols_parts(int64_t tiles, int kb, int tile_rows, int epi, int sm_count) {
+    const int64_t room = std::min<int64_t>(19 * (int64_t)sm_count / 10 / std::max<int64_t>(1, tiles), kb < 8 ? 1 : kb / 2);
+    const int parts = (int)std::min<int64_t>(std::max<int64_t>(room, 1), 16 * tiles <= sm_count && kb >= 24 ? 8 : 5);
+    // 16 tokens take less time than the cluster where the tiles already fill most SMs (16 x 12288 x 7168 17.7 us whole,
+    // 18.5 in three parts); gate and up of 16 have two operand tiles for it.
+    return parts < 4 && tile_rows == 16 && epi != BLOCK_SWIGLU ? 1 : parts;
+}
+
 mse_status launch_block_cols(const BlockGemm &g, int sm_count, bool pdl, cudaStream_t s) {
     CUtensorMap tw, tx;
     mse_status st = map_bytes(&tw, g.wq, g.groups * g.w_group_rows, g.K, g.ldw, kBlock);
@@ -555,19 +570,8 @@ mse_status launch_block_cols(const BlockGemm &g, int sm_count, bool pdl, cudaStr
     const int64_t slots = g.tiles ? g.max_tiles : (g.T + g.tile_rows - 1) / g.tile_rows;
     const int64_t expected = g.tiles ? std::min<int64_t>(slots, g.expected_tiles) : slots;
     if (row_tiles > 65535 || slots > 65535) return MSE_ERR_UNSUPPORTED_SHAPE;
-    // One SM's loads bring a k-block every 0.2 to 0.3 us, so a tile's k-blocks are split over as many CTAs as find
-    // room, two on an SM (nearly: clusters do not fill every last place, and one that waits doubles the time), down to
-    // two k-blocks each: up to five parts (larger clusters find fewer places), eight
-    // where there are few tiles.  (us with 1, 3, 4, 5, 6 and 8 parts: 64 x 12288 x 7168, 96 tiles, 23.5, 19.2, 24.6, ..;
-    // 64 x 7168 x 6144, 56 tiles, 20.1, 14.3, 13.4, 13.6, 18.1, 19.8; 64 x 2048 x 2048, 16 tiles, 9.3, 7.0, 6.4, 6.5, 6.1, 7.5;
-    // 200 x 700 x 1200, 24 tiles, 8.3, 6.8, 6.4, 6.0, 6.8, 7.8; 16 x 1024 x 4096, 8 tiles, 10.7, 7.7, 7.1, 6.9, 6.7, 5.9;
-    // 64 x 7168 x 768, 56 tiles of six k-blocks, 5.9, 7.9.)
     const int64_t tiles = row_tiles * expected;
-    const int64_t room = std::min<int64_t>(19 * (int64_t)sm_count / 10 / std::max<int64_t>(1, tiles), g.kb < 8 ? 1 : g.kb / 2);
-    int parts = (int)std::min<int64_t>(std::max<int64_t>(room, 1), 16 * tiles <= sm_count && g.kb >= 24 ? 8 : 5);
-    // 16 tokens take less time than the cluster where the tiles already fill most SMs (16 x 12288 x 7168 17.7 us whole,
-    // 18.5 in three parts); gate and up of 16 have two operand tiles for it.
-    if (parts < 4 && g.tile_rows == 16 && g.epi != BLOCK_SWIGLU) parts = 1;
+    const int parts = cols_parts(tiles, g.kb, g.tile_rows, g.epi, sm_count);
     const int stream_weights = g.tiles ? g.T <= (int64_t)g.tile_rows * g.groups : slots == 1;
     // one CTA per SM: its ring gets all of it (not in clusters, of which fewer would fit)
     const bool whole = parts == 1 && tiles <= sm_count;

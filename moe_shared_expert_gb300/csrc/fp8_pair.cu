@@ -55,7 +55,7 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
     return (uint32_t)f32_to_bf16_bits(lo) | ((uint32_t)f32_to_bf16_bits(hi) << 16);
 }
 
-template <int EPI>
+template <int EPI, int PARTS>
 __global__ void __launch_bounds__(kThreads, 1)
     pair_block_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
                       const BlockGemm g, const int n_tiles_n) {
@@ -65,9 +65,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint8_t *staging = smem_raw + (base - raw) + kStages * kStage;
     PairCtrl *ctl = reinterpret_cast<PairCtrl *>(staging + kPromoWarps * kStaging);
     const int warp = __shfl_sync(~0u, (int)threadIdx.x / 32, 0), lane = threadIdx.x % 32;
-    const uint32_t rank = cluster_ctarank();
+    // PARTS > 1: a cluster of PARTS pairs has one tile, each pair its share of the k-blocks
+    const uint32_t in_cluster = cluster_ctarank(), rank = in_cluster & 1u, first_rank = in_cluster & ~1u;
+    const int part = (int)(in_cluster >> 1);
     const bool leader = rank == 0;
-    const int64_t cluster = blockIdx.x / 2, n_clusters = gridDim.x / 2;
+    const int64_t cluster = blockIdx.x / (2 * PARTS), n_clusters = gridDim.x / (2 * PARTS);
+    const int kb0 = (int)((int64_t)g.kb * part / PARTS), kb1 = (int)((int64_t)g.kb * (part + 1) / PARTS);
+    const uint16_t both = (uint16_t)(0x3u << first_rank);
     volatile int *abort_flag = &ctl->abort_flag;
 
     if (threadIdx.x == 0) {
@@ -122,11 +126,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int x_row = t.row0 + (int)rank * 128;
                 const int w_row = (int)(t.expert * g.w_group_rows) +
                                   (GLU ? n * 128 + (int)(rank * g.up_rows) : n * 256 + (int)rank * 128);
-                for (int kb = 0; kb < g.kb; ++kb) {
+                for (int kb = kb0; kb < kb1; ++kb) {
                     ok = warp_wait(smem_u32(&ctl->empty[stage]), phase ^ 1u, abort_flag, g);
                     if (!ok) break;
                     if (el) {
-                        const uint32_t fb = map_to_rank(smem_u32(&ctl->full[stage]), 0), dst = base + stage * kStage;
+                        const uint32_t fb = map_to_rank(smem_u32(&ctl->full[stage]), first_rank), dst = base + stage * kStage;
                         if (leader) mbar_arrive_expect_tx(smem_u32(&ctl->full[stage]), 2 * kStage);
                         tma_load_2d_pair(dst, &tmX, fb, kb * kBlock, x_row);
                         tma_load_2d_pair(dst + kOperandTile, &tmW, fb, kb * kBlock, w_row);
@@ -142,7 +146,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             int stage = 0;
             uint32_t phase = 0, use = 0;   // use: k-blocks so far; buffer use & 1
             for (int64_t id = cluster; ok && id < total; id += n_clusters) {
-                for (int kb = 0; kb < g.kb; ++kb, ++use) {
+                for (int kb = kb0; kb < kb1; ++kb, ++use) {
                     const uint32_t b = use & 1u;
                     ok = warp_wait(smem_u32(&ctl->full[stage]), phase, abort_flag, g) &&
                          warp_wait(smem_u32(&ctl->tempty[b]), ((use >> 1) & 1u) ^ 1u, abort_flag, g);
@@ -155,13 +159,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int kk = 0; kk < 4; ++kk)
                             tc_mma_e4m3_pair(tmem_base + b * 256u, xd + (uint64_t)(kk * 2), wd + (uint64_t)(kk * 2), idesc,
                                              kk > 0 ? 1u : 0u);
-                        tc_commit_pair_multicast(smem_u32(&ctl->tfull[b]), (uint16_t)0x3);
-                        tc_commit_pair_multicast(smem_u32(&ctl->empty[stage]), (uint16_t)0x3);
+                        tc_commit_pair_multicast(smem_u32(&ctl->tfull[b]), both);
+                        tc_commit_pair_multicast(smem_u32(&ctl->empty[stage]), both);
                     }
                     __syncwarp();
                     if (++stage == kStages) { stage = 0; phase ^= 1u; }
                 }
             }
+        }
+        if constexpr (PARTS > 1) {   // the promotion warps' exchange
+            __syncwarp();
+            cluster_sync();
+            cluster_sync();
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
@@ -169,8 +178,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         // this thread's columns: two runs (SWIGLU: of gate and of up)
         const uint32_t at0 = GLU ? share * kRun : share * 2 * kRun, at1 = GLU ? 128 + share * kRun : share * 2 * kRun + kRun;
         const uint32_t lanes = tmem_base + ((uint32_t)(q * 32) << 16);
-        const uint32_t empty0 = map_to_rank(smem_u32(&ctl->tempty[0]), 0);
-        const uint32_t empty1 = map_to_rank(smem_u32(&ctl->tempty[1]), 0);
+        const uint32_t empty0 = map_to_rank(smem_u32(&ctl->tempty[0]), first_rank);
+        const uint32_t empty1 = map_to_rank(smem_u32(&ctl->tempty[1]), first_rank);
         uint32_t use = 0;
         for (int64_t id = cluster; id < total; id += n_clusters) {
             Tile t;
@@ -186,11 +195,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int i = 0; i < 2 * kRun; ++i) acc[i] = 0.f;
             // one k-block ahead: a row's factors of 8 k-blocks share one 32-byte sector
-            float xa = __ldg(xs), ga = __ldg(ws), ua = GLU ? __ldg(ws + g.up_scales) : 0.f;
+            float xa = __ldg(xs + kb0), ga = __ldg(ws + kb0), ua = GLU ? __ldg(ws + g.up_scales + kb0) : 0.f;
             bool ok = true;
-            for (int kb = 0; kb < g.kb; ++kb, ++use) {
+            for (int kb = kb0; kb < kb1; ++kb, ++use) {
                 const float f0 = xa * ga, f1 = GLU ? xa * ua : f0;
-                if (kb + 1 < g.kb) {
+                if (kb + 1 < kb1) {
                     xa = __ldg(xs + kb + 1);
                     ga = __ldg(ws + kb + 1);
                     if (GLU) ua = __ldg(ws + g.up_scales + kb + 1);
@@ -219,7 +228,37 @@ __global__ void __launch_bounds__(kThreads, 1)
                         acc[c + v] = fmaf(__uint_as_float(d[c / 32 & 1][v]), c < kRun ? f0 : f1, acc[c + v]);
                 }
             }
-            if (!named_barrier_and(1, 32 * kPromoWarps, ok)) break;
+            ok = named_barrier_and(1, 32 * kPromoWarps, ok);
+            constexpr int cols = 2 * kRun / PARTS;   // of a thread's columns, those it finishes
+            if constexpr (PARTS > 1) {
+                // every pair gets a slice of the columns from all: [part][share][group of four columns][row]
+                float4 *red = reinterpret_cast<float4 *>(smem_raw + (base - raw));
+                constexpr int groups = cols / 4;
+                static_assert((size_t)PARTS * kParts * groups * 128 * 16 <= kStages * (size_t)kStage, "exchange");
+                cluster_sync();   // every ring of the cluster is idle
+                if (ok) {
+#pragma unroll
+                    for (int i = 0; i < 2 * kRun / 4; ++i)
+                        st_cluster_f32x4(map_to_rank(smem_u32(red + ((part * kParts + share) * groups + i % groups) * 128 + row),
+                                                     (uint32_t)(2 * (i / groups)) + rank),
+                                         make_float4(acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3]));
+                }
+                cluster_sync();
+#pragma unroll
+                for (int i = 0; i < groups; ++i) {
+                    float4 v = red[(share * groups + i) * 128 + row];
+#pragma unroll
+                    for (int o = 1; o < PARTS; ++o) {   // in the order of the parts
+                        const float4 w = red[((o * kParts + share) * groups + i) * 128 + row];
+                        v = make_float4(v.x + w.x, v.y + w.y, v.z + w.z, v.w + w.w);
+                    }
+                    acc[4 * i] = v.x;
+                    acc[4 * i + 1] = v.y;
+                    acc[4 * i + 2] = v.z;
+                    acc[4 * i + 3] = v.w;
+                }
+            }
+            if (!ok) break;
             if constexpr (GLU) {
                 const int64_t j0 = (int64_t)n * kBlock + share * kRun;
                 uint32_t am = 0;
@@ -254,7 +293,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // an order of their own, row mod 8, against bank conflicts)
                 using Out = typename std::conditional<EPI == BLOCK_F32, float, uint16_t>::type;
                 constexpr int kWord = 16 / sizeof(Out), kPass = 8 * kWord;   // columns in 16 and in 128 bytes
-                const int64_t c0 = (int64_t)n * 256 + share * 2 * kRun;
+                const int64_t c0 = (int64_t)n * 256 + share * 2 * kRun + part * cols;
                 Out *out = static_cast<Out *>(g.out);
                 const bool aligned = ((reinterpret_cast<uintptr_t>(out) | (uint64_t)g.ldo * sizeof(Out)) & 15u) == 0;
                 uint8_t *mine = staging + (warp - 4) * kStaging;
@@ -276,9 +315,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     __syncwarp();
                 };
-                if (aligned && c0 + 2 * kRun <= g.N) {
+                if (cols % kPass == 0 && aligned && c0 + cols <= g.N) {
 #pragma unroll
-                    for (int c = 0; c < 2 * kRun; c += kPass) {
+                    for (int c = 0; c < cols; c += kPass) {
                         stage(c);
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
@@ -292,13 +331,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 } else {   // rows that start anywhere, or end inside: neighbouring columns by neighbouring lanes
 #pragma unroll
-                    for (int c = 0; c < 2 * kRun; c += kPass) {
+                    for (int c = 0; c < cols; c += kPass) {
                         if (c0 + c >= g.N) break;
                         stage(c);
                         for (int rr = 0; rr < left; ++rr)
 #pragma unroll
                             for (int j = lane; j < kPass; j += 32)
-                                if (c0 + c + j < g.N)
+                                if (c + j < cols && c0 + c + j < g.N)
                                     out[(first + rr) * g.ldo + c0 + c + j] = *reinterpret_cast<const Out *>(
                                         mine + rr * 128 + ((j / kWord) ^ (rr & 7)) * 16 + j % kWord * sizeof(Out));
                         __syncwarp();
@@ -318,7 +357,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __nanosleep(200000);
     }
     if (warp == 1 && lane == 0 && leader) {
-        tc_commit_pair_multicast(smem_u32(&ctl->drain), (uint16_t)0x1);
+        tc_commit_pair_multicast(smem_u32(&ctl->drain), (uint16_t)(0x1u << first_rank));
         (void)mbar_wait_drain(smem_u32(&ctl->drain), 0, drain_limit(g.wait_limit_ns));
     }
     tc_fence_before();
@@ -328,27 +367,78 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 1) tmem_dealloc_pair(tmem_base, 512);
 }
 
-template <int EPI>
-cudaError_t run(const CUtensorMap &tx, const CUtensorMap &tw, const BlockGemm &g, int clusters, int n_tiles_n, bool pdl,
-                cudaStream_t s) {
+// Opts the kernel into its shared memory once per device.
+template <int EPI, int PARTS>
+cudaError_t prepare() {
     static std::atomic<uint64_t> done;   // bit per device
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess || (done.load(std::memory_order_acquire) >> (dev & 63) & 1)) return e;
+    // the hand-over of registers needs the ones it was written for
+    cudaFuncAttributes at;
+    if ((e = cudaFuncGetAttributes(&at, pair_block_kernel<EPI, PARTS>)) != cudaSuccess) return e;
+    if (at.numRegs < kLaunchRegs) return cudaErrorInvalidConfiguration;
+    e = cudaFuncSetAttribute(pair_block_kernel<EPI, PARTS>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+    if (e == cudaSuccess) done.fetch_or(1ull << (dev & 63), std::memory_order_acq_rel);
+    return e;
+}
+
+template <int EPI, int PARTS>
+cudaError_t run(const CUtensorMap &tx, const CUtensorMap &tw, const BlockGemm &g, int clusters, int n_tiles_n, bool pdl,
+                cudaStream_t s) {
+    const cudaError_t e = prepare<EPI, PARTS>();
     if (e != cudaSuccess) return e;
-    if (!(done.load(std::memory_order_acquire) >> (dev & 63) & 1)) {
-        // the hand-over of registers needs the ones it was written for
-        cudaFuncAttributes at;
-        if ((e = cudaFuncGetAttributes(&at, pair_block_kernel<EPI>)) != cudaSuccess) return e;
-        if (at.numRegs < kLaunchRegs) return cudaErrorInvalidConfiguration;
-        e = cudaFuncSetAttribute(pair_block_kernel<EPI>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
-        if (e != cudaSuccess) return e;
-        done.fetch_or(1ull << (dev & 63), std::memory_order_acq_rel);
+    return launch_kernel(pair_block_kernel<EPI, PARTS>, dim3((unsigned)(2 * PARTS * clusters)), kThreads, kSmem, pdl,
+                         2 * PARTS, s, tx, tw, g, n_tiles_n);
+}
+
+// Clusters of PARTS pairs that can be resident at once (0 on failure).
+template <int PARTS>
+int resident_clusters() {
+    static std::atomic<int> cache[64];
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+    if ((n = cache[dev & 63].load()) > 0) return n;
+    if (prepare<BLOCK_BF16, PARTS>() != cudaSuccess) return 0;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * PARTS);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2 * PARTS;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n, pair_block_kernel<BLOCK_BF16, PARTS>, &cfg) != cudaSuccess) {
+        cudaGetLastError();
+        return 0;
     }
-    return launch_kernel(pair_block_kernel<EPI>, dim3((unsigned)(2 * clusters)), kThreads, kSmem, pdl, 2, s, tx, tw, g,
-                         n_tiles_n);
+    cache[dev & 63].store(n);
+    return n;
+}
+
+template <int EPI>
+cudaError_t run_parts(int parts, const CUtensorMap &tx, const CUtensorMap &tw, const BlockGemm &g, int clusters,
+                      int n_tiles_n, bool pdl, cudaStream_t s) {
+    switch (parts) {
+        case 4: return run<EPI, 4>(tx, tw, g, clusters, n_tiles_n, pdl, s);
+        case 2: return run<EPI, 2>(tx, tw, g, clusters, n_tiles_n, pdl, s);
+        default: return run<EPI, 1>(tx, tw, g, clusters, n_tiles_n, pdl, s);
+    }
 }
 
 }  // namespace
+
+// Pairs that share a tile's k-blocks, where all tiles' clusters can be resident at once and the k-blocks saved
+// are worth the exchange, 4 us with two pairs and 6 with four (us with one pair and split: 1024 x 2112 x 7168, 36 tiles,
+// 26.1, 19.5; 256 x 7168 x 6144, 28 tiles, 23.2, 18.6; 512 x 4000 x 1000, 32 tiles of 8 k-blocks, 9.2, 10.4).
+int pair_parts(int64_t tiles, int kb) {
+    if (kb >= 24 && tiles <= resident_clusters<4>()) return 4;
+    if (kb >= 16 && tiles <= resident_clusters<2>()) return 2;
+    return 1;
+}
 
 mse_status launch_block_pair(const BlockGemm &g, int sm_count, bool pdl, cudaStream_t s) {
     CUtensorMap tw, tx;
@@ -356,13 +446,14 @@ mse_status launch_block_pair(const BlockGemm &g, int sm_count, bool pdl, cudaStr
     if (st != MSE_OK) return st;
     if ((st = map_bytes(&tx, g.xq, g.T, g.K, g.ldx, 128)) != MSE_OK) return st;
     const int n_tiles_n = (int)((g.N + (g.epi == BLOCK_SWIGLU ? 127 : 255)) / (g.epi == BLOCK_SWIGLU ? 128 : 256));
-    const int64_t slots = g.tiles ? g.max_tiles : (g.T + 255) / 256;
-    const int clusters = (int)std::min<int64_t>(sm_count / 2, slots * n_tiles_n);
+    const int64_t slots = g.tiles ? g.max_tiles : (g.T + 255) / 256, tiles = slots * n_tiles_n;
+    const int parts = g.tiles ? 1 : pair_parts(tiles, g.kb);
+    const int clusters = (int)std::min<int64_t>(parts > 1 ? tiles : sm_count / 2, tiles);
     cudaError_t e;
     switch (g.epi) {
-        case BLOCK_BF16: e = run<BLOCK_BF16>(tx, tw, g, clusters, n_tiles_n, pdl, s); break;
-        case BLOCK_F32: e = run<BLOCK_F32>(tx, tw, g, clusters, n_tiles_n, pdl, s); break;
-        default: e = run<BLOCK_SWIGLU>(tx, tw, g, clusters, n_tiles_n, pdl, s); break;
+        case BLOCK_BF16: e = run_parts<BLOCK_BF16>(parts, tx, tw, g, clusters, n_tiles_n, pdl, s); break;
+        case BLOCK_F32: e = run_parts<BLOCK_F32>(parts, tx, tw, g, clusters, n_tiles_n, pdl, s); break;
+        default: e = run<BLOCK_SWIGLU, 1>(tx, tw, g, clusters, n_tiles_n, pdl, s); break;
     }
     return e == cudaSuccess ? MSE_OK : MSE_ERR_CUDA;
 }

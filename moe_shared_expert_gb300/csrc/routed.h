@@ -108,8 +108,10 @@ struct BlockGemm {
 
 // Tensor-core kernel for token tiles of 16, 32 or (not SWIGLU) 64 rows (weights on the 128-row side).
 mse_status launch_block_cols(const BlockGemm &g, int sm_count, bool pdl, cudaStream_t s);
+int cols_parts(int64_t tiles, int kb, int tile_rows, int epi, int sm_count);
 // Tensor-core kernel for token tiles of 256 rows (a CTA pair per 256 x 256 tile).
 mse_status launch_block_pair(const BlockGemm &g, int sm_count, bool pdl, cudaStream_t s);
+int pair_parts(int64_t tiles, int kb);
 
 constexpr int kSimtTileRows = 16;
 cudaError_t launch_block_simt(const BlockGemm &g, bool pdl, cudaStream_t s);

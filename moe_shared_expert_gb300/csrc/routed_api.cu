@@ -43,16 +43,19 @@ mse_status check_matmul(const void *xq, int64_t ldx, const void *xs, const void 
 
 // Token rows of a tile: 16, 32 and 64 take the swap-AB kernel, 256 the CTA-pair kernel.
 //
-// Plain product.  A CTA pair spends 0.41 us on a k-block of 256 x 256 and there are half as many pairs as
-// SMs; two swap-AB CTAs on an SM spend 0.54 us on a k-block of 128 x 64 each, and split tiles over
-// more CTAs when there are fewer tiles than SMs.  So the pair wins from two waves of swap-AB tiles
-// on, when its own waves are at most two thirds of theirs (us, pair and swap-AB: 256 x 7168 x 6144 23.2 and 26.6,
-// 128 x 12288 x 7168 26.9 and 30.0; 128 x 7168 x 6144 23.3 and 18.1, 512 x 2112 x 7168 25.5 and 19.8).
-int plain_tile_rows(int64_t T, int64_t N, int sm_count) {
+// Plain product: the kernel that is expected to take less time, in units of 0.01 us.  A CTA pair (half as many as SMs)
+// spends 0.41 us on a k-block of 256 x 256, two swap-AB CTAs on an SM 0.54 us on one of 128 x 64 each; a split
+// tile's exchange takes 2.5 us in the swap-AB kernel, 4 or 6 in the pair's, which starts 1.3 us later (us, pair and swap-AB:
+// 256 x 7168 x 6144 18.6, 26.4; 128 x 12288 x 7168 27.1, 29.9; 512 x 2112 x 7168 17.8, 19.4; 320 x 2112 x 7168 17.7, 15.5;
+// 64 x 12288 x 7168 26.3, 19.3; 128 x 4000 x 1000 9.0, 8.0; 1024 x 700 x 3000 13.6, 11.4).
+int plain_tile_rows(int64_t T, int64_t N, int64_t K, int sm_count) {
     if (T <= 32) return T <= 16 ? 16 : 32;
-    const int64_t cols = blocks_of(N) * ((T + 63) / 64), pairs = ((T + 255) / 256) * ((N + 255) / 256);
-    const int64_t cols_waves = (cols + sm_count - 1) / sm_count, pair_waves = (pairs + sm_count / 2 - 1) / (sm_count / 2);
-    return cols_waves >= 2 && 2 * cols_waves >= 3 * pair_waves ? 256 : 64;
+    const int64_t kb = blocks_of(K), cols = blocks_of(N) * ((T + 63) / 64), pairs = ((T + 255) / 256) * ((N + 255) / 256);
+    const int64_t cp = cols_parts(cols, (int)kb, 64, BLOCK_BF16, sm_count), pp = pair_parts(pairs, (int)kb);
+    const int64_t cols_waves = (cols * cp + sm_count - 1) / sm_count, pair_waves = (pairs * pp + sm_count / 2 - 1) / (sm_count / 2);
+    const int64_t cols_time = cols_waves * kb * 27 / cp + (cp > 1 ? 250 : 0);
+    const int64_t pair_time = pair_waves * kb * 41 / pp + (pp == 4 ? 600 : pp == 2 ? 400 : 0) + 130;
+    return pair_time < cols_time ? 256 : 64;
 }
 // Experts, by the rows expected of each (32 experts of 7168 x 2048, us with tiles of 16, 32 and 256: 8 rows
 // 219, 232, 308; 16 rows 240, 250, 311; 32 rows 305, 278, 319; 48 rows 403, 351, 330; 64 rows 497, 417, 335;
@@ -72,7 +75,7 @@ BlockGemm plain_product(const uint8_t *xq, int64_t ldx, const float *xs, const u
     BlockGemm g;
     std::memset(&g, 0, sizeof g);
     g.T = T;
-    g.tile_rows = plain_tile_rows(T, N, sm_count);
+    g.tile_rows = plain_tile_rows(T, N, K, sm_count);
     g.xq = xq; g.ldx = ldx; g.xs = xs;
     g.wq = wq; g.ldw = ldw; g.ws = ws;
     g.N = N; g.K = K; g.kb = (int)blocks_of(K);

@@ -163,6 +163,39 @@ __global__ void __launch_bounds__(kDispatchThreads) count_kernel(const DispatchP
     for (int e = threadIdx.x; e < p.E; e += kDispatchThreads) p.hist[(int64_t)blockIdx.x * p.E + e] = count_smem[e];
 }
 
+// hist[c][e] becomes the pairs of expert e in the chunks before c; row n_chunks: in all of them.  Lane: an expert, warp: a
+// 32nd of the chunks, added up first and then run through.  (Each CTA of the dispatch adding up the whole table took
+// n_chunks^2: 32768 tokens with 8 of 256 experts 1112 us there, 157 now; 4096 tokens 81 and 21.)
+constexpr int kScanThreads = 1024;
+
+__global__ void __launch_bounds__(kScanThreads) scan_kernel(int *hist, int n_chunks, int E) {
+    __shared__ int sums[32][33];
+    pdl_wait();
+    pdl_launch_dependents();
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, e = (int)blockIdx.x * 32 + lane;
+    const int per = (n_chunks + 31) / 32, c0 = min(warp * per, n_chunks), c1 = min(c0 + per, n_chunks);
+    int sum = 0;
+    if (e < E)
+#pragma unroll 8
+        for (int c = c0; c < c1; ++c) sum += hist[(int64_t)c * E + e];
+    sums[warp][lane] = sum;
+    __syncthreads();
+    if (e >= E) return;
+    int run = 0;
+    for (int w = 0; w < warp; ++w) run += sums[w][lane];
+    for (int c = c0; c < c1; c += 8) {
+        int v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = c + i < c1 ? hist[(int64_t)(c + i) * E + e] : 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if (c + i < c1) hist[(int64_t)(c + i) * E + e] = run;
+            run += v[i];
+        }
+    }
+    if (warp == 31) hist[(int64_t)n_chunks * E + e] = run;
+}
+
 // exclusive prefix sum of v[0 .. n) in shared memory by one warp; the total is returned
 __device__ __forceinline__ int warp_prefix(int *v, int n, int lane) {
     int run = 0;
@@ -188,23 +221,23 @@ __global__ void __launch_bounds__(kDispatchThreads) dispatch_kernel(const Dispat
     int *total = dispatch_smem, *before = total + p.E, *tile_at = before + p.E, *of_warp = tile_at + p.E;
     __shared__ int pair_row[kDispatchPairs];
     __shared__ int64_t pair_at[kDispatchPairs];   // byte offset of the row in xq, -1: none
+    __shared__ int all;
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
     pdl_wait();
     pdl_launch_dependents();
-    for (int e = tid; e < p.E; e += kDispatchThreads) total[e] = before[e] = 0;
-    for (int i = tid; i < kDispatchThreads / 32 * p.E; i += kDispatchThreads) of_warp[i] = 0;
-    __syncthreads();
     const int64_t pairs = p.T * p.top_k, i0 = (int64_t)blockIdx.x * p.chunk * p.top_k;
     const int64_t t0 = (int64_t)blockIdx.x * p.chunk;
     const int tokens = (int)min((int64_t)p.chunk, p.T - t0), mine = tokens * p.top_k;
+    for (int i = tid; i < kDispatchThreads / 32 * p.E; i += kDispatchThreads) of_warp[i] = 0;
     if (p.hist) {
-        for (int64_t i = tid; i < (int64_t)p.n_chunks * p.E; i += kDispatchThreads) {
-            const int n = p.hist[i];
-            if (n == 0) continue;
-            atomicAdd(&total[i % p.E], n);
-            if (i / p.E < blockIdx.x) atomicAdd(&before[i % p.E], n);
+        for (int e = tid; e < p.E; e += kDispatchThreads) {
+            total[e] = p.hist[(int64_t)p.n_chunks * p.E + e];
+            before[e] = p.hist[(int64_t)blockIdx.x * p.E + e];
         }
+        __syncthreads();
     } else {
+        for (int e = tid; e < p.E; e += kDispatchThreads) total[e] = before[e] = 0;
+        __syncthreads();
         for (int64_t i = tid; i < pairs; i += kDispatchThreads) {
             const int e = local_expert(p, i);
             if (e >= 0) {
@@ -220,27 +253,26 @@ __global__ void __launch_bounds__(kDispatchThreads) dispatch_kernel(const Dispat
     const int rank = __popc(same & ((1u << lane) - 1u));
     if (expert >= 0 && rank == 0) of_warp[warp * p.E + expert] = __popc(same);
     __syncthreads();
-    const bool writes_tiles = blockIdx.x == 0 && blockIdx.y == 0;
-    if (writes_tiles) {
-        for (int e = tid; e < p.E; e += kDispatchThreads) tile_at[e] = (total[e] + p.tile_rows - 1) / p.tile_rows;
+    if (warp == 0) {   // each expert's first row
+        const int n = warp_prefix(total, p.E, lane);
+        if (lane == 0) all = n;
+    }
+    __syncthreads();
+    if (blockIdx.x == 0 && blockIdx.y == 0) {   // writes the tiles
+        for (int e = tid; e < p.E; e += kDispatchThreads)
+            tile_at[e] = ((e + 1 < p.E ? total[e + 1] : all) - total[e] + p.tile_rows - 1) / p.tile_rows;
         __syncthreads();
-        if (warp == 1) {
+        if (warp == 0) {
             const int n = warp_prefix(tile_at, p.E, lane);
             if (lane == 0) *p.n_tiles = n;
         }
-        // (the counts are needed below: the tiles take a copy of them before they become rows)
         __syncthreads();
         for (int e = tid; e < p.E; e += kDispatchThreads) {
-            int row = 0;
-            for (int f = 0; f < e; ++f) row += total[f];
-            for (int k = 0; k * p.tile_rows < total[e]; ++k)
-                p.tiles[tile_at[e] + k] =
-                    Tile{row + k * p.tile_rows, min(p.tile_rows, total[e] - k * p.tile_rows), e, 0};
+            const int row0 = total[e], rows = (e + 1 < p.E ? total[e + 1] : all) - row0;
+            for (int k = 0; k * p.tile_rows < rows; ++k)
+                p.tiles[tile_at[e] + k] = Tile{row0 + k * p.tile_rows, min(p.tile_rows, rows - k * p.tile_rows), e, 0};
         }
-        __syncthreads();
     }
-    if (warp == 0) (void)warp_prefix(total, p.E, lane);   // now each expert's first row
-    __syncthreads();
     if (tid < mine) {
         int row = -1;
         if (expert >= 0) {
@@ -437,8 +469,11 @@ cudaError_t launch_quantise_f32(const float *h, const int *n_tiles, const Tile *
 
 cudaError_t launch_dispatch(const DispatchParams &p, bool pdl, cudaStream_t s) {
     if (p.hist) {
-        const cudaError_t e = launch_kernel(count_kernel, dim3((unsigned)p.n_chunks), kDispatchThreads,
-                                            (size_t)p.E * 4, pdl, 1, s, p);
+        cudaError_t e = launch_kernel(count_kernel, dim3((unsigned)p.n_chunks), kDispatchThreads, (size_t)p.E * 4, pdl, 1,
+                                      s, p);
+        if (e == cudaSuccess)
+            e = launch_kernel(scan_kernel, dim3((unsigned)((p.E + 31) / 32)), kScanThreads, 0, pdl, 1, s, p.hist,
+                              p.n_chunks, p.E);
         if (e != cudaSuccess) return e;
     }
     return launch_kernel(dispatch_kernel, dim3((unsigned)p.n_chunks, (unsigned)p.splits), kDispatchThreads,

@@ -49,7 +49,7 @@ struct DispatchParams {
     int E;
     int chunk;             // tokens per CTA row (chunk * top_k <= kDispatchPairs)
     int n_chunks, splits;
-    int *hist;             // [n_chunks x E] pairs of each chunk and expert; null: every CTA counts all ids
+    int *hist;             // [n_chunks + 1 x E] pairs of each expert before each chunk; null: every CTA counts all ids
     int32_t *pos;          // [T x top_k] row of a pair among the sorted pairs, -1: not of this rank
     Tile *tiles;
     int *n_tiles;

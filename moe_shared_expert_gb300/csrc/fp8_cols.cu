@@ -265,17 +265,14 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
 #pragma unroll
                     for (int v = 0; v < 8; ++v) now[v] = next[quad][v];
                     fetch(i + C::ROUND_WARPS, quad, next[quad]);
-                    auto lo = [&](int v) { return __uint_as_float(now[v] << 16); };
-                    auto hi = [&](int v) { return __uint_as_float(now[v] & 0xFFFF0000u); };
 #pragma unroll
-                    for (int v = 0; v < 8; ++v) top = max(top, max(abs_bits(lo(v)), abs_bits(hi(v))));
+                    for (int v = 0; v < 8; ++v) top = abs_max2(top, now[v]);
 #pragma unroll
-                    for (int d = 4; d > 0; d >>= 1) top = max(top, __shfl_xor_sync(~0u, top, d));
-                    const float a = floored_amax(top), inv = __frcp_rn(a);
+                    for (int d = 4; d > 0; d >>= 1) top = __vmaxu2(top, __shfl_xor_sync(~0u, top, d));
+                    const float a = floored_amax(bits_of_max2(top));
+                    const E4m3Scale scale = e4m3_scale(a);
 #pragma unroll
-                    for (int v = 0; v < 4; ++v)
-                        w[v] = e4m3x2(e4m3_ratio(lo(2 * v), a, inv), e4m3_ratio(hi(2 * v), a, inv)) |
-                               (e4m3x2(e4m3_ratio(lo(2 * v + 1), a, inv), e4m3_ratio(hi(2 * v + 1), a, inv)) << 16);
+                    for (int v = 0; v < 4; ++v) w[v] = e4m3x4(now[2 * v], now[2 * v + 1], scale);
                     const int token = quad * 4 + lane / 8;
                     // the 128-byte swizzle of the operand tiles: 16-byte word `sub` of a row at sub ^ (row mod 8)
                     *reinterpret_cast<uint4 *>(ring + (size_t)s * C::STAGE + MATS * kOperandTile + token * 128 +

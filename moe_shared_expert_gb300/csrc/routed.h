@@ -43,6 +43,7 @@ struct Tile {
 struct DispatchParams {
     const uint16_t *x;
     int64_t T, H;
+    int align;             // of x's rows in bytes, 16 at most
     const int32_t *ids;
     int top_k;
     int64_t first_expert;
@@ -59,6 +60,7 @@ struct DispatchParams {
 };
 constexpr int kDispatchThreads = 256;
 constexpr int kDispatchPairs = 256;
+int align_of(const uint16_t *x, int64_t ld);   // of rows of pitch ld, in bytes, 16 at most
 cudaError_t launch_dispatch(const DispatchParams &p, bool pdl, cudaStream_t s);
 
 // y[t] = shared[t] + sum_j w[t, j] o[pos[t, j]]

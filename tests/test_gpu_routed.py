@@ -194,6 +194,20 @@ def test_quantise_of_extreme_blocks():
     assert float(q[2, 200]) == 448.0 and torch.isfinite(v[2]).all()
 
 
+@pytest.mark.parametrize("rows,K,pitch,offset", [(70, 200, 208, 8), (70, 200, 204, 4), (70, 136, 138, 2), (70, 300, 301, 0),
+                                                 (33, 128, 136, 3), (6000, 900, 900, 0)])
+def test_quantise_of_views(rows, K, pitch, offset):
+    # rows at multiples of 16, 8, 4 and 2 bytes, and more rows than are on their way at once
+    flat = torch.randn(rows * pitch + offset, generator=gen(K)).to(torch.bfloat16).cuda()
+    x = torch.as_strided(flat, (rows, K), (pitch, 1), offset)
+    rq, rs = ref.rounded(x.cpu().double())
+    q, s = mse.fp8_block_quantise(x)
+    assert torch.equal(q.cpu().double(), rq) and torch.all((s.cpu().double() - rs).abs() <= EPS32 * rs)
+    q, s = mse.fp8_block_quantise(x, block_rows=128)
+    q2, s2 = mse.fp8_block_quantise(x.clone(), block_rows=128)
+    assert torch.equal(q.cpu().float(), q2.cpu().float()) and torch.equal(s, s2)
+
+
 # ------------------------------------------------------------------------------------ products
 
 def assert_product(got, x_values, w_values, roundings=2.0 ** -8):
@@ -367,6 +381,25 @@ def test_experts(case, path):
     else:
         mse.moe_experts_forward(*args, first_expert=first, shared=out, y=out, workspace=buf)
     assert torch.equal(out, y)
+
+
+def test_experts_of_many_chunks_and_unaligned_rows(path):
+    # 277 chunks of tokens, 40 experts; x, shared and y that begin in the middle of a word
+    T, E, k, H, I = 17700, 40, 4, 36, 16
+    weights = make_experts(E, H, I, 31)
+    g = gen(32)
+    flat = torch.randn(2, T * H + 1, generator=g).to(torch.bfloat16).cuda()
+    x, shared = flat[0, 1:].view(T, H), flat[1, 1:].view(T, H)
+    ids = torch.randn(T, E, generator=g).topk(k, 1).indices.to(torch.int32)
+    w = torch.rand(T, k, generator=g)
+    y = torch.empty(T * H + 1, dtype=torch.bfloat16, device="cuda")[1:].view(T, H)
+    mse.moe_experts_forward(x, ids.cuda(), w.cuda(), *weights, shared=shared, y=y)
+    some = torch.cat([torch.arange(200), torch.arange(9000, 9200), torch.arange(T - 200, T)])
+    want = ref.experts(x.cpu()[some], ids[some], w[some],
+                       *[t.cpu().float() if i % 2 == 0 else t.cpu() for i, t in enumerate(weights)], shared=shared.cpu()[some])
+    assert_experts(y[some.cuda()], want)
+    aligned = mse.moe_experts_forward(x.clone(), ids.cuda(), w.cuda(), *weights, shared=shared.clone())
+    assert torch.equal(aligned, y)
 
 
 def test_experts_of_a_few_tokens_with_repeated_ids(path):

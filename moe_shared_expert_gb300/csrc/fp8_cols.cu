@@ -547,12 +547,18 @@ cudaError_t run_bn(const CUtensorMap &tw, const CUtensorMap &tx, const BlockGemm
 // 64 x 7168 x 6144, 56 tiles, 20.1, 14.3, 13.4, 13.6, 18.1, 19.8; 64 x 2048 x 2048, 16 tiles, 9.3, 7.0, 6.4, 6.5, 6.1, 7.5;
 // 200 x 700 x 1200, 24 tiles, 8.3, 6.8, 6.4, 6.0, 6.8, 7.8; 16 x 1024 x 4096, 8 tiles, 10.7, 7.7, 7.1, 6.9, 6.7, 5.9;
 // 64 x 7168 x 768, 56 tiles of six k-blocks, 5.9, 7.9.)
+// Gate and up have twice the k-block: four of them at least, and of 32 tokens three CTAs on two SMs.  (The experts' layer with 1, 2,
+// 3, 4 and 5 parts: 8 experts of 1024 x 896, 43 rows, 91 tiles of 8 k-blocks, 23.4, 22.0, 26.8, 26.9, 30.3; 4 of 4096 x 1024,
+// 25 rows, 56 tiles of 32 k-blocks, 34.4, 29.8, 27.4, 26.6, 30.9; 8 of 2048 x 1536, 32 rows, 144 tiles, 30.3, 34.7, ..; the
+// same with 16 rows 27.1, 26.1, 29.9; 8 of 1024 x 896, 15 rows, 77 tiles, 19.9, 18.7, 20.3.)
 int cols_parts(int64_t tiles, int kb, int tile_rows, int epi, int sm_count) {
-    const int64_t room = std::min<int64_t>(19 * (int64_t)sm_count / 10 / std::max<int64_t>(1, tiles), kb < 8 ? 1 : kb / 2);
+    const bool glu = epi == BLOCK_SWIGLU;
+    const int64_t ctas = (glu && tile_rows > 16 ? 15 : 19) * (int64_t)sm_count / 10;
+    const int64_t room = std::min<int64_t>(ctas / std::max<int64_t>(1, tiles), kb < 8 ? 1 : kb / (glu ? 4 : 2));
     const int parts = (int)std::min<int64_t>(std::max<int64_t>(room, 1), 16 * tiles <= sm_count && kb >= 24 ? 8 : 5);
     // 16 tokens take less time than the cluster where the tiles already fill most SMs (16 x 12288 x 7168 17.7 us whole,
     // 18.5 in three parts); gate and up of 16 have two operand tiles for it.
-    return parts < 4 && tile_rows == 16 && epi != BLOCK_SWIGLU ? 1 : parts;
+    return parts < 4 && tile_rows == 16 && !glu ? 1 : parts;
 }
 
 mse_status launch_block_cols(const BlockGemm &g, int sm_count, bool pdl, cudaStream_t s) {

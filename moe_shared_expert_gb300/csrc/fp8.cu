@@ -375,26 +375,32 @@ __global__ void __launch_bounds__(kDispatchThreads) dispatch_kernel(const Dispat
 // registers, and the 4096 tokens 17 us more.
 constexpr int kPairs = 4;
 
-template <int VEC>
-__global__ void __launch_bounds__(256) combine_kernel(const float *o, const int32_t *pos, const float *weights,
+// WIDE: H is a multiple of 4, and y and shared begin at multiples of 8 bytes.  o's rows always begin at 16.
+template <bool WIDE>
+__global__ void __launch_bounds__(256) combine_kernel(const float *o, int64_t ldo, const int32_t *pos, const float *weights,
                                                       int top_k, const uint16_t *shared, uint16_t *y, int64_t T,
                                                       int64_t H) {
     pdl_wait();
-    const int64_t per = H / VEC, items = T * per;
+    const int64_t per = (H + 3) / 4, items = T * per;
     for (int64_t it = (int64_t)blockIdx.x * 256 + threadIdx.x; it < items; it += (int64_t)gridDim.x * 256) {
-        const int64_t t = it / per, c = it % per * VEC;
-        float acc[VEC];
-        if constexpr (VEC == 4) {
-            const uint2 v = shared ? __ldcs(reinterpret_cast<const uint2 *>(shared + t * H + c)) : make_uint2(0, 0);
-            acc[0] = bf16_bits_to_f32((uint16_t)v.x), acc[1] = bf16_bits_to_f32((uint16_t)(v.x >> 16));
-            acc[2] = bf16_bits_to_f32((uint16_t)v.y), acc[3] = bf16_bits_to_f32((uint16_t)(v.y >> 16));
-        } else {
-            acc[0] = shared ? bf16_bits_to_f32(shared[t * H + c]) : 0.f;
+        const int64_t t = it / per, c = it % per * 4;
+        float acc[4] = {0.f, 0.f, 0.f, 0.f};
+        if (shared) {
+            const uint16_t *src = shared + t * H + c;
+            if constexpr (WIDE) {
+                const uint2 v = __ldcs(reinterpret_cast<const uint2 *>(src));
+                acc[0] = bf16_bits_to_f32((uint16_t)v.x), acc[1] = bf16_bits_to_f32((uint16_t)(v.x >> 16));
+                acc[2] = bf16_bits_to_f32((uint16_t)v.y), acc[3] = bf16_bits_to_f32((uint16_t)(v.y >> 16));
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[i] = c + i < H ? bf16_bits_to_f32(src[i]) : 0.f;
+            }
         }
         // kPairs at a time: their rows' numbers, then their values, all on their way before any is added
         for (int j0 = 0; j0 < top_k; j0 += kPairs) {
             int row[kPairs];
-            float w[kPairs], v[kPairs][VEC];
+            float w[kPairs];
+            float4 v[kPairs];
 #pragma unroll
             for (int j = 0; j < kPairs; ++j) {
                 const bool have = j0 + j < top_k;
@@ -402,29 +408,26 @@ __global__ void __launch_bounds__(256) combine_kernel(const float *o, const int3
                 w[j] = have ? weights[t * top_k + j0 + j] : 0.f;
             }
 #pragma unroll
-            for (int j = 0; j < kPairs; ++j) {
-                if (row[j] < 0) continue;
-                const float *src = o + (int64_t)row[j] * H + c;
-                if constexpr (VEC == 4) {
-                    const float4 f = __ldcs(reinterpret_cast<const float4 *>(src));
-                    v[j][0] = f.x; v[j][1] = f.y; v[j][2] = f.z; v[j][3] = f.w;
-                } else {
-                    v[j][0] = src[0];
-                }
-            }
+            for (int j = 0; j < kPairs; ++j)
+                if (row[j] >= 0) v[j] = __ldcs(reinterpret_cast<const float4 *>(o + row[j] * ldo + c));
 #pragma unroll
             for (int j = 0; j < kPairs; ++j)
-                if (row[j] >= 0)
-#pragma unroll
-                    for (int i = 0; i < VEC; ++i) acc[i] = fmaf(w[j], v[j][i], acc[i]);
+                if (row[j] >= 0) {
+                    acc[0] = fmaf(w[j], v[j].x, acc[0]);
+                    acc[1] = fmaf(w[j], v[j].y, acc[1]);
+                    acc[2] = fmaf(w[j], v[j].z, acc[2]);
+                    acc[3] = fmaf(w[j], v[j].w, acc[3]);
+                }
         }
-        uint16_t r[VEC];
+        uint16_t *dst = y + t * H + c, r[4];
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) r[i] = f32_to_bf16_bits(acc[i]);
-        if constexpr (VEC == 4) {
-            *reinterpret_cast<uint2 *>(y + t * H + c) = make_uint2(r[0] | (uint32_t)r[1] << 16, r[2] | (uint32_t)r[3] << 16);
+        for (int i = 0; i < 4; ++i) r[i] = f32_to_bf16_bits(acc[i]);
+        if constexpr (WIDE) {
+            *reinterpret_cast<uint2 *>(dst) = make_uint2(r[0] | (uint32_t)r[1] << 16, r[2] | (uint32_t)r[3] << 16);
         } else {
-            y[t * H + c] = r[0];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (c + i < H) dst[i] = r[i];
         }
     }
 }
@@ -524,14 +527,14 @@ cudaError_t launch_dispatch(const DispatchParams &p, bool pdl, cudaStream_t s) {
                          (size_t)p.E * 4 * (3 + kDispatchThreads / 32), pdl, 1, s, p);
 }
 
-cudaError_t launch_combine(const float *o, const int32_t *pos, const float *weights, int top_k, const uint16_t *shared,
-                           uint16_t *y, int64_t T, int64_t H, int sm_count, bool pdl, cudaStream_t s) {
-    // o lies in the workspace, 256-byte aligned
+cudaError_t launch_combine(const float *o, int64_t ldo, const int32_t *pos, const float *weights, int top_k,
+                           const uint16_t *shared, uint16_t *y, int64_t T, int64_t H, int sm_count, bool pdl,
+                           cudaStream_t s) {
     const bool wide = H % 4 == 0 && ((reinterpret_cast<uintptr_t>(y) | reinterpret_cast<uintptr_t>(shared)) & 7u) == 0;
-    const int64_t items = wide ? T * (H / 4) : T * H;
+    const int64_t items = T * ((H + 3) / 4);
     const dim3 grid((unsigned)std::min<int64_t>((items + 255) / 256, (int64_t)sm_count * 16));
-    if (wide) return launch_kernel(combine_kernel<4>, grid, 256, 0, pdl, 1, s, o, pos, weights, top_k, shared, y, T, H);
-    return launch_kernel(combine_kernel<1>, grid, 256, 0, pdl, 1, s, o, pos, weights, top_k, shared, y, T, H);
+    return launch_kernel(wide ? combine_kernel<true> : combine_kernel<false>, grid, 256, 0, pdl, 1, s, o, ldo, pos, weights,
+                         top_k, shared, y, T, H);
 }
 
 cudaError_t launch_block_simt(const BlockGemm &g, bool pdl, cudaStream_t s) {

@@ -315,21 +315,35 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     __syncwarp();
                 };
-                if (cols % kPass == 0 && aligned && c0 + cols <= g.N) {
+                if (cols % kPass == 0 && aligned) {
 #pragma unroll
                     for (int c = 0; c < cols; c += kPass) {
+                        if (c0 + c >= g.N) break;
                         stage(c);
+                        const int64_t col = c0 + c + (lane & 7) * kWord;
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
                             const int rr = i * 4 + lane / 8;
                             const uint4 w =
                                 *reinterpret_cast<const uint4 *>(mine + rr * 128 + ((lane & 7) ^ (rr & 7)) * 16);
-                            if (rr < left)
-                                *reinterpret_cast<uint4 *>(out + (first + rr) * g.ldo + c0 + c + (lane & 7) * kWord) = w;
+                            Out *dst = out + (first + rr) * g.ldo + col;
+                            if (rr < left && col + kWord <= g.N) {
+                                *reinterpret_cast<uint4 *>(dst) = w;
+                            } else if (rr < left) {   // the rows' last, incomplete word
+                                const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                                for (int e = 0; e < kWord; ++e)
+                                    if (col + e < g.N) {
+                                        if constexpr (EPI == BLOCK_F32)
+                                            dst[e] = __uint_as_float(u[e]);
+                                        else
+                                            dst[e] = (uint16_t)(u[e / 2] >> (e % 2 * 16));
+                                    }
+                            }
                         }
                         __syncwarp();
                     }
-                } else {   // rows that start anywhere, or end inside: neighbouring columns by neighbouring lanes
+                } else {   // rows that start anywhere: neighbouring columns by neighbouring lanes
 #pragma unroll
                     for (int c = 0; c < cols; c += kPass) {
                         if (c0 + c >= g.N) break;

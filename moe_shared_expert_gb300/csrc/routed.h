@@ -12,6 +12,7 @@ namespace routed {
 constexpr int kBlock = 128;              // rows or columns that share a scale
 inline int64_t blocks_of(int64_t n) { return (n + kBlock - 1) / kBlock; }
 inline int64_t pad16(int64_t n) { return (n + 15) / 16 * 16; }
+inline int64_t pad4(int64_t n) { return (n + 3) / 4 * 4; }
 
 // ------------------------------------------------------------------ routing
 struct RouteParams {
@@ -64,8 +65,9 @@ int align_of(const uint16_t *x, int64_t ld);   // of rows of pitch ld, in bytes,
 cudaError_t launch_dispatch(const DispatchParams &p, bool pdl, cudaStream_t s);
 
 // y[t] = shared[t] + sum_j w[t, j] o[pos[t, j]]
-cudaError_t launch_combine(const float *o, const int32_t *pos, const float *weights, int top_k, const uint16_t *shared,
-                           uint16_t *y, int64_t T, int64_t H, int sm_count, bool pdl, cudaStream_t s);
+cudaError_t launch_combine(const float *o, int64_t ldo, const int32_t *pos, const float *weights, int top_k,
+                           const uint16_t *shared, uint16_t *y, int64_t T, int64_t H, int sm_count, bool pdl,
+                           cudaStream_t s);
 
 // ------------------------------------------------------------------ block-scaled products
 constexpr int kRoundRows = 8;

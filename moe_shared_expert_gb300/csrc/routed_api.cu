@@ -94,7 +94,17 @@ bool tc_operands(const void *xq, int64_t ldx, const void *wq, int64_t ldw) {
 // ------------------------------------------------------------------ the experts' layer
 // Up to this many pairs every CTA of the dispatch counts all ids itself.
 constexpr int64_t kCountAllPairs = 4096;
-int chunk_max(int top_k) { return kDispatchPairs / top_k; }
+
+// Tokens of a CTA of the dispatch: about as many CTAs as SMs, as far as a CTA's pairs reach.
+constexpr int64_t kDispatchChunks = 152;
+int chunk_of(int64_t T, int top_k) {
+    return (int)std::min<int64_t>(kDispatchPairs / top_k, std::max<int64_t>(1, T / kDispatchChunks));
+}
+// no fewer than any number of tokens up to T has chunks
+size_t chunks_bound(int64_t T, int top_k) {
+    const int64_t most = kDispatchPairs / top_k;
+    return (size_t)std::max((T + most - 1) / most, std::min<int64_t>(T, 2 * kDispatchChunks));
+}
 
 struct MoeWs {
     size_t pos, tiles, n_tiles, hist, xq, xs, hq, hs, o, total;
@@ -107,12 +117,12 @@ MoeWs moe_ws(int64_t T, int top_k, int64_t E, int64_t H, int64_t I) {
     w.n_tiles = take(4);
     w.pos = take(P * 4);
     w.tiles = take((P / kSimtTileRows + std::min<size_t>(P, (size_t)E) + 1) * sizeof(Tile));
-    w.hist = take((size_t)((T + chunk_max(top_k) - 1) / chunk_max(top_k) + 1) * (size_t)E * 4);
+    w.hist = take((chunks_bound(T, top_k) + 1) * (size_t)E * 4);
     w.xq = take(P * (size_t)pad16(H));
     w.xs = take(P * (size_t)blocks_of(H) * 4);
     w.hq = take(P * (size_t)pad16(I));
     w.hs = take(P * (size_t)blocks_of(I) * 4);
-    w.o = take(P * (size_t)std::max(H, I) * 4);   // the pairs' outputs (generic kernels: h before it)
+    w.o = take(P * (size_t)std::max(pad4(H), I) * 4);   // the pairs' outputs (generic kernels: h before it)
     w.total = off;
     return w;
 }
@@ -256,14 +266,11 @@ mse_status moe_experts_forward(const mse_bf16 *x, int64_t T, int64_t H, const in
     DispatchParams dp;
     std::memset(&dp, 0, sizeof dp);
     dp.x = x; dp.T = T; dp.H = H; dp.align = align_of(x, H); dp.ids = ids; dp.top_k = top_k; dp.first_expert = first_expert; dp.E = (int)E;
-    // chunks of tokens on about as many CTAs as SMs, then the k-blocks of a chunk over several CTAs, up
-    // to eight per SM (the rows are written by many warps at once: 4096 tokens of 7168 x 8 in 60 us, 230 on 128 CTAs)
-    dp.chunk = (int)std::min<int64_t>(chunk_max(top_k), std::max<int64_t>(1, T / d.sm_count));
-    if (pairs > kCountAllPairs) {   // the ids are counted once, by two kernels of their own
-        dp.chunk = chunk_max(top_k);
-        dp.hist = reinterpret_cast<int *>(w + L.hist);
-    }
+    dp.chunk = chunk_of(T, top_k);
+    if (pairs > kCountAllPairs) dp.hist = reinterpret_cast<int *>(w + L.hist);   // the ids are counted once, by two kernels of their own
     dp.n_chunks = (int)((T + dp.chunk - 1) / dp.chunk);
+    // the k-blocks of a chunk over several CTAs, up to eight per SM (the rows are written by many warps at once: 4096 tokens of
+    // 7168 x 8 in 60 us, 230 on 128 CTAs)
     dp.splits = (int)std::max<int64_t>(1, std::min<int64_t>(blocks_of(H) / 4, 8 * d.sm_count / dp.n_chunks));
     dp.pos = reinterpret_cast<int32_t *>(w + L.pos);
     dp.tiles = reinterpret_cast<Tile *>(w + L.tiles);
@@ -308,10 +315,10 @@ mse_status moe_experts_forward(const mse_bf16 *x, int64_t T, int64_t H, const in
     dn.w_group_rows = H;
     dn.ws_group = blocks_of(H) * blocks_of(I);
     dn.epi = BLOCK_F32;
-    dn.out = o; dn.ldo = H;
+    dn.out = o; dn.ldo = pad4(H);
     dn.weights_early = 1;   // (and the tiles: the gate_up launch lets this one start after its own wait)
     if ((st = run_product(dn, tensorcore, d, s)) != MSE_OK) return st;
-    return from_cuda(launch_combine(o, dp.pos, weights, top_k, shared, y, T, H, d.sm_count, pdl, s));
+    return from_cuda(launch_combine(o, dn.ldo, dp.pos, weights, top_k, shared, y, T, H, d.sm_count, pdl, s));
 }
 
 }  // extern "C"

@@ -480,7 +480,7 @@ __global__ void __launch_bounds__(256) block_simt_kernel(const BlockGemm g) {
     const int64_t at = (int64_t)(t.row0 + r) * g.ldo + n;
     if constexpr (EPI == BLOCK_BF16) static_cast<uint16_t *>(g.out)[at] = f32_to_bf16_bits(acc[0]);
     if constexpr (EPI == BLOCK_F32) static_cast<float *>(g.out)[at] = acc[0];
-    if constexpr (EPI == BLOCK_SWIGLU) static_cast<float *>(g.out)[at] = silu_f32(acc[0]) * acc[1];
+    if constexpr (EPI == BLOCK_SWIGLU) static_cast<float *>(g.out)[at] = glu(acc[0], acc[1]);
 }
 
 }  // namespace

@@ -445,7 +445,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
             }
         } else {
             // h = silu(g) u; the largest |h| of a token over the tile's 128 rows is its block's scale
-            auto h_of = [&](float gate, float up) { return valid ? silu_f32(gate) * up : 0.f; };
+            auto h_of = [&](float gate, float up) { return valid ? glu(gate, up) : 0.f; };
             auto note = [&](int col, float h) {
                 const uint32_t a = __reduce_max_sync(~0u, abs_bits(h));
                 if (lane == 0) amax_s[q * BN + col] = a;

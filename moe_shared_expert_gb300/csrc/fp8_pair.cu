@@ -261,12 +261,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!ok) break;
             if constexpr (GLU) {
                 const int64_t j0 = (int64_t)n * kBlock + share * kRun;
-                uint32_t am = 0;
 #pragma unroll
-                for (int i = 0; i < kRun; ++i) {
-                    acc[i] = j0 + i < g.N ? silu_f32(acc[i]) * acc[kRun + i] : 0.f;
-                    am = max(am, abs_bits(acc[i]));
+                for (int i = 0; i < kRun; ++i) acc[i] = glu(acc[i], acc[kRun + i]);
+                if (j0 + kRun > g.N) {   // columns of another weight, or of none
+#pragma unroll
+                    for (int i = 0; i < kRun; ++i)
+                        if (j0 + i >= g.N) acc[i] = 0.f;
                 }
+                float most[2] = {0.f, 0.f};
+#pragma unroll
+                for (int i = 0; i < kRun; ++i) most[i & 1] = abs_max_nan(most[i & 1], acc[i]);
+                const uint32_t am = abs_bits(abs_max_nan(most[0], most[1]));
                 ctl->amax[share][row] = am;
                 named_barrier_sync(1, 32 * kPromoWarps);
                 const float a = floored_amax(max(am, ctl->amax[share ^ 1][row]));

@@ -181,21 +181,37 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t empty0 = map_to_rank(smem_u32(&ctl->tempty[0]), first_rank);
         const uint32_t empty1 = map_to_rank(smem_u32(&ctl->tempty[1]), first_rank);
         uint32_t use = 0;
-        for (int64_t id = cluster; id < total; id += n_clusters) {
+        // the next tile: its place and its first factors are on their way while this one's sums are written
+        struct {
             Tile t;
             int n;
-            place(id, t, n);
+            const float *xs, *ws;
+            float xa, ga, ua;
+        } next;
+        auto open = [&](int64_t id) {
+            if (id >= total) return;
+            place(id, next.t, next.n);
+            const bool have = row < next.t.rows - (int)rank * 128;
+            // factors of one k-block: xs (any valid row where this one is not), ws of the two runs
+            next.xs = g.xs + ((int64_t)next.t.row0 + (have ? (int)rank * 128 + row : 0)) * g.kb;
+            const int blk = GLU ? next.n : min(2 * next.n + share * 2 * kRun / 128, (int)((g.N + kBlock - 1) / kBlock) - 1);
+            next.ws = g.ws + (int64_t)next.t.expert * g.ws_group + (int64_t)blk * g.kb;
+            next.xa = __ldg(next.xs + kb0);
+            next.ga = __ldg(next.ws + kb0);
+            next.ua = GLU ? __ldg(next.ws + g.up_scales + kb0) : 0.f;
+        };
+        open(cluster);
+        for (int64_t id = cluster; id < total; id += n_clusters) {
+            const Tile t = next.t;
+            const int n = next.n;
             const bool row_ok = row < t.rows - (int)rank * 128;
             const int64_t r = t.row0 + (int)rank * 128 + row;
-            // factors of one k-block: xs (any valid row where this one is not), ws of the two runs
-            const float *xs = g.xs + (row_ok ? r : (int64_t)t.row0) * g.kb;
-            const int blk = GLU ? n : min(2 * n + share * 2 * kRun / 128, (int)((g.N + kBlock - 1) / kBlock) - 1);
-            const float *ws = g.ws + (int64_t)t.expert * g.ws_group + (int64_t)blk * g.kb;
+            const float *xs = next.xs, *ws = next.ws;
             float acc[2 * kRun];
 #pragma unroll
             for (int i = 0; i < 2 * kRun; ++i) acc[i] = 0.f;
             // one k-block ahead: a row's factors of 8 k-blocks share one 32-byte sector
-            float xa = __ldg(xs + kb0), ga = __ldg(ws + kb0), ua = GLU ? __ldg(ws + g.up_scales + kb0) : 0.f;
+            float xa = next.xa, ga = next.ga, ua = next.ua;
             bool ok = true;
             for (int kb = kb0; kb < kb1; ++kb, ++use) {
                 const float f0 = xa * ga, f1 = GLU ? xa * ua : f0;
@@ -214,10 +230,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tmem_ld32(src + at0, d[0]);
 #pragma unroll
                 for (int c = 0; c < 2 * kRun; c += 32) {
-                    const int next = c + 32;
+                    const int then = c + 32;
                     tmem_ld_wait();
-                    if (next < 2 * kRun) {
-                        tmem_ld32(src + (next < kRun ? at0 + next : at1 + next - kRun), d[next / 32 & 1]);
+                    if (then < 2 * kRun) {
+                        tmem_ld32(src + (then < kRun ? at0 + then : at1 + then - kRun), d[then / 32 & 1]);
                     } else {
                         tc_fence_before();
                         __syncwarp();
@@ -228,6 +244,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         acc[c + v] = fmaf(__uint_as_float(d[c / 32 & 1][v]), c < kRun ? f0 : f1, acc[c + v]);
                 }
             }
+            open(id + n_clusters);
             ok = named_barrier_and(1, 32 * kPromoWarps, ok);
             constexpr int cols = 2 * kRun / PARTS;   // of a thread's columns, those it finishes
             if constexpr (PARTS > 1) {

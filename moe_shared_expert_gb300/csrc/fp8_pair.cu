@@ -8,7 +8,10 @@
 // pair halves what each SM reads: 32 KB per k-block of 512 MMA cycles.
 //
 // Warp 0 loads (TMA), warp 1 of the leading CTA issues MMAs, warps 4-11 promote and store; the
-// first warpgroup hands registers to them.
+// first warpgroup hands registers to them.  A tile's sums are written while the MMAs of the next one's first two k-blocks run.
+//
+// Bound by the power limit and, with few k-blocks to a tile, by the sums' way out: 8192 x 12288 x 7168 486 us, 2.97 PFLOP/s;
+// gate and up of 4096 tokens x 8 experts (7168 x 2048) 764 us, down 508.
 #include <atomic>
 #include <type_traits>
 

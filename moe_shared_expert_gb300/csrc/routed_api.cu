@@ -58,9 +58,9 @@ int plain_tile_rows(int64_t T, int64_t N, int64_t K, int sm_count) {
     return pair_time < cols_time ? 256 : 64;
 }
 // Experts, by the rows expected of each, if all pairs were this rank's (us with tiles of 16, 32 and 256; 32 experts of
-// 7168 x 2048: 16 rows 240, 250, 311; 32 rows 305, 278, 319; 48 rows 403, 351, 330; 64 rows 497, 417, 335; 8 of 2048 x 1536:
-// 16 rows 27, 26, 42; 64 rows 55, 43, 47; 128 rows 82, 62, 49; half of 64 experts of 1000 x 500, 50 rows 36, 33, 41; tiles of 64
-// and 128 were never the fastest).
+// 7168 x 2048: 16 rows 247, 248, 313; 32 rows 311, 279, 322; 40 rows 371, 332, 327; 48 rows 407, 345, 332; 8 of 2048 x 1536:
+// 16 rows 26, 27, 41; 48 rows 48, 36, 45; 64 rows 54, 42, 46; 80 rows 60, 53, 46; half of 64 experts of 1000 x 500, 50 rows
+// 35, 32, 40; tiles of 64 and 128 were never the fastest).
 int expert_tile_rows(int64_t rows) { return rows <= 16 ? 16 : rows <= 56 ? 32 : 256; }
 
 mse_status run_product(BlockGemm g, bool tensorcore, const DeviceView &d, cudaStream_t s) {

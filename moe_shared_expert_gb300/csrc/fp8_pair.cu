@@ -10,8 +10,9 @@
 // Warp 0 loads (TMA), warp 1 of the leading CTA issues MMAs, warps 4-11 promote and store; the
 // first warpgroup hands registers to them.  A tile's sums are written while the MMAs of the next one's first two k-blocks run.
 //
-// Bound by the power limit and, with few k-blocks to a tile, by the sums' way out: 8192 x 12288 x 7168 486 us, 2.97 PFLOP/s;
-// gate and up of 4096 tokens x 8 experts (7168 x 2048) 764 us, down 508.
+// Bound by the power limit and, with few k-blocks to a tile, by the sums' way out: 8192 x 12288 x 7168 about 470 us,
+// 3.1 PFLOP/s (12 us more with the rows stored by the lanes); gate and up of 4096 tokens x 8 experts (7168 x 2048) 764 us,
+// down 508.
 #include <atomic>
 #include <type_traits>
 
@@ -39,7 +40,8 @@ struct PairCtrl {
     int abort_flag;
     uint32_t amax[kParts][128];
 };
-constexpr uint32_t kStaging = 32 * 128;        // per promotion warp: 32 rows of 128 bytes on their way out
+constexpr uint32_t kStaged = 32 * 128;         // 32 rows of 128 bytes on their way out
+constexpr uint32_t kStaging = 2 * kStaged;     // per promotion warp
 constexpr size_t kSmem = kStages * (size_t)kStage + kPromoWarps * kStaging + 1024 + sizeof(PairCtrl) + 64;
 
 // 32 lanes x 32 consecutive columns
@@ -58,10 +60,24 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
     return (uint32_t)f32_to_bf16_bits(lo) | ((uint32_t)f32_to_bf16_bits(hi) << 16);
 }
 
+// shared -> global, 32 rows of 128 bytes, clipped to the tensor; its group is the issuing thread's
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap *m, uint32_t src, int x, int y) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                     reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(src)
+                 : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+// all but the newest N stores of this thread have read their shared memory
+template <int N>
+__device__ __forceinline__ void tma_store_wait_read() {
+    asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void tma_store_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
 template <int EPI, int PARTS>
 __global__ void __launch_bounds__(kThreads, 1)
     pair_block_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
-                      const BlockGemm g, const int n_tiles_n) {
+                      const __grid_constant__ CUtensorMap tmOut, const BlockGemm g, const int n_tiles_n) {
     constexpr bool GLU = EPI == BLOCK_SWIGLU;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
@@ -183,7 +199,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t lanes = tmem_base + ((uint32_t)(q * 32) << 16);
         const uint32_t empty0 = map_to_rank(smem_u32(&ctl->tempty[0]), first_rank);
         const uint32_t empty1 = map_to_rank(smem_u32(&ctl->tempty[1]), first_rank);
-        uint32_t use = 0;
+        uint32_t use = 0, turn = 0;   // turn: of the two staging buffers
         // the next tile: its place and its first factors are on their way while this one's sums are written
         struct {
             Tile t;
@@ -324,7 +340,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 uint8_t *mine = staging + (warp - 4) * kStaging;
                 const int64_t first = t.row0 + (int)rank * 128 + q * 32;
                 const int left = min(t.rows - (int)rank * 128 - q * 32, 32);   // valid rows of this warp
-                auto stage = [&](int c) {   // columns c .. c + kPass of the warp's rows
+                auto stage = [&](int c, uint8_t *mine) {   // columns c .. c + kPass of the warp's rows
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
                         const float *v = acc + c + i * kWord;
@@ -340,50 +356,69 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     __syncwarp();
                 };
-                if (cols % kPass == 0 && aligned) {
+                if (cols % kPass == 0 && aligned && left == 32) {
+                    // whole rows of a warp leave by TMA, clipped at N, one buffer while the other is filled
 #pragma unroll
                     for (int c = 0; c < cols; c += kPass) {
                         if (c0 + c >= g.N) break;
-                        stage(c);
-                        const int64_t col = c0 + c + (lane & 7) * kWord;
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const int rr = i * 4 + lane / 8;
-                            const uint4 w =
-                                *reinterpret_cast<const uint4 *>(mine + rr * 128 + ((lane & 7) ^ (rr & 7)) * 16);
-                            Out *dst = out + (first + rr) * g.ldo + col;
-                            if (rr < left && col + kWord <= g.N) {
-                                *reinterpret_cast<uint4 *>(dst) = w;
-                            } else if (rr < left) {   // the rows' last, incomplete word
-                                const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                                for (int e = 0; e < kWord; ++e)
-                                    if (col + e < g.N) {
-                                        if constexpr (EPI == BLOCK_F32)
-                                            dst[e] = __uint_as_float(u[e]);
-                                        else
-                                            dst[e] = (uint16_t)(u[e / 2] >> (e % 2 * 16));
-                                    }
-                            }
-                        }
+                        uint8_t *buf = mine + (turn++ & 1u) * kStaged;
+                        if (lane == 0) tma_store_wait_read<1>();
                         __syncwarp();
+                        stage(c, buf);
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0)
+                            tma_store_2d(&tmOut, smem_u32(buf), (int)((c0 + c) * (int64_t)sizeof(Out)), (int)first);
                     }
-                } else {   // rows that start anywhere: neighbouring columns by neighbouring lanes
+                } else if (left > 0) {
+                    if (lane == 0) tma_store_wait_read<0>();
+                    __syncwarp();
+                    if (cols % kPass == 0 && aligned) {
 #pragma unroll
-                    for (int c = 0; c < cols; c += kPass) {
-                        if (c0 + c >= g.N) break;
-                        stage(c);
-                        for (int rr = 0; rr < left; ++rr)
+                        for (int c = 0; c < cols; c += kPass) {
+                            if (c0 + c >= g.N) break;
+                            stage(c, mine);
+                            const int64_t col = c0 + c + (lane & 7) * kWord;
 #pragma unroll
-                            for (int j = lane; j < kPass; j += 32)
-                                if (c + j < cols && c0 + c + j < g.N)
-                                    out[(first + rr) * g.ldo + c0 + c + j] = *reinterpret_cast<const Out *>(
-                                        mine + rr * 128 + ((j / kWord) ^ (rr & 7)) * 16 + j % kWord * sizeof(Out));
-                        __syncwarp();
+                            for (int i = 0; i < 8; ++i) {
+                                const int rr = i * 4 + lane / 8;
+                                const uint4 w =
+                                    *reinterpret_cast<const uint4 *>(mine + rr * 128 + ((lane & 7) ^ (rr & 7)) * 16);
+                                Out *dst = out + (first + rr) * g.ldo + col;
+                                if (rr < left && col + kWord <= g.N) {
+                                    *reinterpret_cast<uint4 *>(dst) = w;
+                                } else if (rr < left) {   // the rows' last, incomplete word
+                                    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                                    for (int e = 0; e < kWord; ++e)
+                                        if (col + e < g.N) {
+                                            if constexpr (EPI == BLOCK_F32)
+                                                dst[e] = __uint_as_float(u[e]);
+                                            else
+                                                dst[e] = (uint16_t)(u[e / 2] >> (e % 2 * 16));
+                                        }
+                                }
+                            }
+                            __syncwarp();
+                        }
+                    } else {   // rows that start anywhere: neighbouring columns by neighbouring lanes
+#pragma unroll
+                        for (int c = 0; c < cols; c += kPass) {
+                            if (c0 + c >= g.N) break;
+                            stage(c, mine);
+                            for (int rr = 0; rr < left; ++rr)
+#pragma unroll
+                                for (int j = lane; j < kPass; j += 32)
+                                    if (c + j < cols && c0 + c + j < g.N)
+                                        out[(first + rr) * g.ldo + c0 + c + j] = *reinterpret_cast<const Out *>(
+                                            mine + rr * 128 + ((j / kWord) ^ (rr & 7)) * 16 + j % kWord * sizeof(Out));
+                            __syncwarp();
+                        }
                     }
                 }
             }
         }
+        if (!GLU && lane == 0) tma_store_wait_all();
         __syncwarp();
     }
 
@@ -423,12 +458,12 @@ cudaError_t prepare() {
 }
 
 template <int EPI, int PARTS>
-cudaError_t run(const CUtensorMap &tx, const CUtensorMap &tw, const BlockGemm &g, int clusters, int n_tiles_n, bool pdl,
-                cudaStream_t s) {
+cudaError_t run(const CUtensorMap &tx, const CUtensorMap &tw, const CUtensorMap &to, const BlockGemm &g, int clusters,
+                int n_tiles_n, bool pdl, cudaStream_t s) {
     const cudaError_t e = prepare<EPI, PARTS>();
     if (e != cudaSuccess) return e;
     return launch_kernel(pair_block_kernel<EPI, PARTS>, dim3((unsigned)(2 * PARTS * clusters)), kThreads, kSmem, pdl,
-                         2 * PARTS, s, tx, tw, g, n_tiles_n);
+                         2 * PARTS, s, tx, tw, to, g, n_tiles_n);
 }
 
 // Clusters of PARTS pairs that can be resident at once (0 on failure).
@@ -459,12 +494,12 @@ int resident_clusters() {
 }
 
 template <int EPI>
-cudaError_t run_parts(int parts, const CUtensorMap &tx, const CUtensorMap &tw, const BlockGemm &g, int clusters,
-                      int n_tiles_n, bool pdl, cudaStream_t s) {
+cudaError_t run_parts(int parts, const CUtensorMap &tx, const CUtensorMap &tw, const CUtensorMap &to, const BlockGemm &g,
+                      int clusters, int n_tiles_n, bool pdl, cudaStream_t s) {
     switch (parts) {
-        case 4: return run<EPI, 4>(tx, tw, g, clusters, n_tiles_n, pdl, s);
-        case 2: return run<EPI, 2>(tx, tw, g, clusters, n_tiles_n, pdl, s);
-        default: return run<EPI, 1>(tx, tw, g, clusters, n_tiles_n, pdl, s);
+        case 4: return run<EPI, 4>(tx, tw, to, g, clusters, n_tiles_n, pdl, s);
+        case 2: return run<EPI, 2>(tx, tw, to, g, clusters, n_tiles_n, pdl, s);
+        default: return run<EPI, 1>(tx, tw, to, g, clusters, n_tiles_n, pdl, s);
     }
 }
 
@@ -484,15 +519,20 @@ mse_status launch_block_pair(const BlockGemm &g, int sm_count, bool pdl, cudaStr
     mse_status st = map_bytes(&tw, g.wq, g.groups * g.w_group_rows, g.K, g.ldw, 128);
     if (st != MSE_OK) return st;
     if ((st = map_bytes(&tx, g.xq, g.T, g.K, g.ldx, 128)) != MSE_OK) return st;
+    CUtensorMap to = tx;   // of rows at multiples of 16 bytes only
+    const int64_t size = g.epi == BLOCK_F32 ? 4 : 2;
+    if (g.epi != BLOCK_SWIGLU && ((reinterpret_cast<uintptr_t>(g.out) | (uint64_t)(g.ldo * size)) & 15u) == 0 &&
+        (st = map_bytes(&to, g.out, g.T, g.N * size, g.ldo * size, 32)) != MSE_OK)
+        return st;
     const int n_tiles_n = (int)((g.N + (g.epi == BLOCK_SWIGLU ? 127 : 255)) / (g.epi == BLOCK_SWIGLU ? 128 : 256));
     const int64_t slots = g.tiles ? g.max_tiles : (g.T + 255) / 256, tiles = slots * n_tiles_n;
     const int parts = g.tiles ? 1 : pair_parts(tiles, g.kb);
     const int clusters = (int)std::min<int64_t>(parts > 1 ? tiles : sm_count / 2, tiles);
     cudaError_t e;
     switch (g.epi) {
-        case BLOCK_BF16: e = run_parts<BLOCK_BF16>(parts, tx, tw, g, clusters, n_tiles_n, pdl, s); break;
-        case BLOCK_F32: e = run_parts<BLOCK_F32>(parts, tx, tw, g, clusters, n_tiles_n, pdl, s); break;
-        default: e = run<BLOCK_SWIGLU, 1>(tx, tw, g, clusters, n_tiles_n, pdl, s); break;
+        case BLOCK_BF16: e = run_parts<BLOCK_BF16>(parts, tx, tw, to, g, clusters, n_tiles_n, pdl, s); break;
+        case BLOCK_F32: e = run_parts<BLOCK_F32>(parts, tx, tw, to, g, clusters, n_tiles_n, pdl, s); break;
+        default: e = run<BLOCK_SWIGLU, 1>(tx, tw, tx, g, clusters, n_tiles_n, pdl, s); break;
     }
     return e == cudaSuccess ? MSE_OK : MSE_ERR_CUDA;
 }

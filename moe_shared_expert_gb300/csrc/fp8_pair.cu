@@ -10,9 +10,9 @@
 // Warp 0 loads (TMA), warp 1 of the leading CTA issues MMAs, warps 4-11 promote and store; the
 // first warpgroup hands registers to them.  A tile's sums are written while the MMAs of the next one's first two k-blocks run.
 //
-// Bound by the power limit and, with few k-blocks to a tile, by the sums' way out: 8192 x 12288 x 7168 about 470 us,
-// 3.1 PFLOP/s (12 us more with the rows stored by the lanes); gate and up of 4096 tokens x 8 experts (7168 x 2048) 764 us,
-// down 508.
+// Bound by the power limit and, with few k-blocks to a tile, by the sums' way out: 8192 x 12288 x 7168 475 us, 3.04 PFLOP/s
+// (486 with the rows stored by the lanes); gate and up of 4096 tokens x 8 experts (7168 x 2048) 764 to 780 us, down 464
+// (508).
 #include <atomic>
 #include <type_traits>
 

@@ -526,7 +526,9 @@ typedef enum { MSE_SCORE_SOFTMAX = 0, MSE_SCORE_SIGMOID = 1 } mse_score;
  *   ids    = the top_k best open choices; equal ones go to the lower index, groups too;
  *   weight = score of the chosen (without the bias), divided by their sum if renormalise
  *            (by nothing where that sum is 0), times scale.
- * A token with no open expert gets ids -1 and weights 0.
+ * A token with no open expert gets ids -1 and weights 0.  A logit of +inf makes every softmax score of
+ * its token NaN: equal choices, so the lowest open experts (of the lowest topk_group groups with one),
+ * with weights NaN.
  * MSE_ERR_INVALID_ARG: null pointer, non-positive size, bad enum, ld < E, E, n_group or top_k
  * beyond the limits, topk_group outside [1, n_group], top_k above the topk_group * E / n_group
  * experts that stay, group_top not 1 or 2; MSE_ERR_NOT_DIVISIBLE: E by n_group;

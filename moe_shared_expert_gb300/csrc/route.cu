@@ -76,6 +76,32 @@ __device__ __forceinline__ uint32_t best_groups(const RouteParams &p, const floa
     return kept;
 }
 
+// A token with an infinite logit under softmax: e^(l - max) / sum is NaN for every open expert.  Equal choices, so the lowest
+// open experts of the lowest groups with one, and weights of NaN: an overflow before the router shows in what follows.
+// Bit i of `open`: expert i * 32 + lane.
+__device__ __forceinline__ void undefined_scores(const RouteParams &p, int64_t t, uint32_t open, int per_lane, int lane) {
+    int id = -1, n = 0, groups = 0, group = -1;
+#pragma unroll 1
+    for (int i = 0; i < per_lane && n < p.top_k; ++i) {
+        for (uint32_t which = __ballot_sync(~0u, open >> i & 1u); which != 0 && n < p.top_k; which &= which - 1u) {
+            const int e = i * 32 + __ffs(which) - 1;
+            if (e / p.group_size != group) {
+                group = e / p.group_size;
+                if (++groups > p.topk_group) {
+                    n = p.top_k;   // no more groups
+                    break;
+                }
+            }
+            if (lane == n) id = e;
+            ++n;
+        }
+    }
+    if (lane < p.top_k) {
+        p.ids[t * p.top_k + lane] = id;
+        p.weights[t * p.top_k + lane] = id >= 0 ? __int_as_float(0x7FC00000) : 0.f;
+    }
+}
+
 template <int VPL, bool BF16, bool GROUPS>
 __global__ void __launch_bounds__(kRouteWarps * 32, VPL <= 8 ? 5 : VPL <= 16 ? 4 : 2) route_kernel(const RouteParams p) {
     extern __shared__ float route_smem[];
@@ -121,6 +147,10 @@ __global__ void __launch_bounds__(kRouteWarps * 32, VPL <= 8 ? 5 : VPL <= 16 ? 4
 #pragma unroll
             for (int i = 0; i < VPL; ++i) top = fmaxf(top, v[i]);
             top = warp_fmax(top);
+            if (top == INFINITY) {
+                undefined_scores(p, t, open, VPL, lane);
+                continue;
+            }
             if (top == -INFINITY) top = 0.f;
             // The sum as if rounded once, whatever the order: each term e <= 1 is split into a
             // multiple of 2^-14 (at most 1024 of them add up exactly, here and as integers) and a

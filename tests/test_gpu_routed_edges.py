@@ -1,0 +1,77 @@
+"""Routed-expert operators at the edges of their arguments: infinite and undefined logits."""
+import math
+
+import pytest
+
+from tests.test_gpu_routed import gen, make_experts
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+mse = pytest.importorskip("moe_shared_expert_gb300")
+
+# n_group, topk_group, group_top
+GROUPS = [(1, 1, 1), (4, 2, 2), (4, 2, 1), (8, 3, 2)]
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    from moe_shared_expert_gb300 import _build
+    _build.build()
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    mse.lib()
+    yield
+    torch.cuda.synchronize()
+    assert mse.poll_device_error() == 0
+
+
+# ------------------------------------------------------------------------------------ an infinite logit
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("with_bias", [False, True])
+@pytest.mark.parametrize("renormalise", [False, True])
+@pytest.mark.parametrize("groups", GROUPS, ids=str)
+@pytest.mark.parametrize("E", [40, 320, 1000])
+def test_softmax_of_an_infinite_logit_is_nan(E, groups, renormalise, with_bias, dtype):
+    # e^(l - max) / sum is NaN for every open expert: the choices are equal, the weights NaN
+    G, keep, top = groups
+    logits = torch.randn(5, E, generator=gen(E)).to(dtype)
+    logits[1, E // 2] = math.inf
+    logits[2, 0] = logits[2, E - 1] = math.inf
+    logits[3, ::2] = -math.inf
+    logits[3, 1] = math.inf
+    logits[4] = -math.inf
+    logits[4, E - 2] = math.inf
+    bias = torch.linspace(-1, 1, E) if with_bias else None
+    call = dict(scoring="softmax", bias=None if bias is None else bias.cuda(), n_group=G, topk_group=keep,
+                group_top=top, renormalise=renormalise)
+    ids, w = mse.moe_route(logits.cuda(), 6, **call)
+    ids, w = ids.cpu(), w.cpu()
+    size = E // G
+    for t in range(1, 5):
+        open_ = [e for e in range(E) if float(logits[t, e]) > -math.inf]
+        kept = sorted({e // size for e in open_})[:keep if G > 1 else None]
+        want = [e for e in open_ if e // size in kept][:6]
+        assert ids[t].tolist() == want + [-1] * (6 - len(want))
+        assert torch.isnan(w[t, :len(want)]).all() and not w[t, len(want):].any()
+    # the other tokens are as without it
+    alone, w0 = mse.moe_route(logits[:1].cuda(), 6, **call)
+    assert torch.equal(ids[:1], alone.cpu()) and torch.equal(w[:1], w0.cpu())
+
+
+def test_an_infinite_logit_reaches_the_layers_output():
+    E, H, I, T = 6, 256, 128, 4
+    weights = make_experts(E, H, I, 3)
+    x = torch.randn(T, H, generator=gen(4)).to(torch.bfloat16).cuda()
+    logits = torch.randn(T, E, generator=gen(5))
+    logits[2, 3] = math.inf
+    y = mse.moe_experts_forward(x, *mse.moe_route(logits.cuda(), 2, scoring="softmax"), *weights, shared=x)
+    assert torch.isnan(y[2]).all() and torch.isfinite(y[[0, 1, 3]]).all()
+
+
+def test_sigmoid_of_an_infinite_logit_is_one():
+    logits = torch.zeros(2, 50)
+    logits[0, 9] = logits[0, 33] = math.inf
+    ids, w = mse.moe_route(logits.cuda(), 3, scoring="sigmoid", renormalise=False)
+    assert ids.cpu().tolist() == [[9, 33, 0], [0, 1, 2]] and w.cpu().tolist() == [[1.0, 1.0, 0.5], [0.5] * 3]

@@ -519,7 +519,7 @@ typedef enum { MSE_SCORE_SOFTMAX = 0, MSE_SCORE_SIGMOID = 1 } mse_score;
  * either type's lowest value and NaN close it.  In fp32:
  *   score  = 1 / (1 + e^-l), or e^(l - max) / sum over the open experts (softmax; the sum
  *            as if rounded once, so that no choice depends on an order of summation);
- *   choice = score + bias;
+ *   choice = score + bias (an expert whose choice is NaN or -inf is not chosen, and counts for nothing in its group);
  *   groups: experts [g E / n_group, (g + 1) E / n_group); a group's value is the sum of its
  *            group_top (1 or 2) best open choices (of fewer where fewer are open), and only
  *            the topk_group best groups stay open;

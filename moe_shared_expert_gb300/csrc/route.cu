@@ -184,7 +184,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32, VPL <= 8 ? 5 : VPL <= 16 ? 4
             } else
                 c = p.sigmoid ? __fdividef(1.0f, 1.0f + __expf(-v[i])) + bias_of(i)
                               : fmaf(v[i], inv, bias_of(i));
-            v[i] = open >> i & 1u ? c : -INFINITY;
+            v[i] = (open >> i & 1u) && c >= -INFINITY ? c : -INFINITY;   // (a NaN of the bias is no choice)
         }
         if constexpr (GROUPS) {
 #pragma unroll

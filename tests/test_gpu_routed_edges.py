@@ -1,4 +1,4 @@
-"""Routed-expert operators at the edges of their arguments: infinite and undefined logits."""
+"""Routed-expert operators at the edges of their arguments: infinite and undefined logits and biases."""
 import math
 
 import pytest
@@ -75,3 +75,39 @@ def test_sigmoid_of_an_infinite_logit_is_one():
     logits[0, 9] = logits[0, 33] = math.inf
     ids, w = mse.moe_route(logits.cuda(), 3, scoring="sigmoid", renormalise=False)
     assert ids.cpu().tolist() == [[9, 33, 0], [0, 1, 2]] and w.cpu().tolist() == [[1.0, 1.0, 0.5], [0.5] * 3]
+
+
+# ------------------------------------------------------------------------------------ a bias that is NaN, infinite or lowest
+
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+def test_a_nan_bias_counts_for_nothing_in_its_group(scoring):
+    E, G = 64, 2
+    for nan_at in (19, 3, 35):
+        logits = torch.full((1, E), -8.0)
+        logits[0, 5], logits[0, 5 + 32], logits[0, 6 + 32] = 3.0, 2.5, 2.4     # one good expert against two
+        # lane r of a group's sixteen has experts r and r + 16: the best one, then the undefined one, and the other way
+        best = (nan_at + 16) % 32 + nan_at // 32 * 32
+        if nan_at < 32:
+            logits[0, 5], logits[0, best] = -8.0, 3.0
+        logits[0, nan_at] = 6.0
+        bias = torch.zeros(E)
+        bias[nan_at] = math.nan
+        ids, w = mse.moe_route(logits.cuda(), 2, scoring=scoring, bias=bias.cuda(), n_group=G, topk_group=1)
+        assert ids.cpu().tolist() == [[37, 38]], nan_at
+        assert torch.isfinite(w).all()
+        # without groups: the expert is never chosen
+        ids, _ = mse.moe_route(logits.cuda(), E, scoring=scoring, bias=bias.cuda()) if E <= 32 else \
+            mse.moe_route(logits.cuda(), 32, scoring=scoring, bias=bias.cuda())
+        assert nan_at not in ids.cpu()[0].tolist()
+
+
+@pytest.mark.parametrize("n_group", [1, 2])
+def test_an_infinite_bias(n_group):
+    # -inf: no choice is lower, the expert is never chosen; +inf: always, equal ones by index
+    E = 40
+    bias = torch.zeros(E)
+    bias[3:] = -math.inf
+    bias[[30, 10]] = math.inf
+    ids, w = mse.moe_route(torch.zeros(1, E).cuda(), 6, bias=bias.cuda(), n_group=n_group, topk_group=1 if n_group == 1 else 2)
+    assert ids.cpu().tolist() == [[10, 30, 0, 1, 2, -1]]
+    assert torch.allclose(w.cpu(), torch.tensor([[0.2] * 5 + [0.0]]))

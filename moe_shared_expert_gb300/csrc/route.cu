@@ -22,6 +22,7 @@ constexpr int kRouteWarps = 8;
 // the lowest finite bf16: a logit at or below it (both types' lowest values, -inf) or NaN closes
 // its expert
 constexpr float kClosedFrom = -3.3895313892515355e38f;
+constexpr float kLowest = -3.4028234663852886e38f;   // of fp32: a bias may bring a choice down to it
 
 template <bool BF16>
 __device__ __forceinline__ float load_logit(const RouteParams &p, int64_t i) {
@@ -63,7 +64,8 @@ __device__ __forceinline__ uint32_t best_groups(const RouteParams &p, const floa
         c2 = fmaxf(fmaxf(c2, o2), fminf(c1, o1));
         c1 = fmaxf(c1, o1);
     }
-    float value = p.group_top == 2 && c2 > -INFINITY ? __fadd_rn(c1, c2) : c1;
+    // (two lowest choices add up to -inf, but a group that has any comes before one that has none)
+    float value = p.group_top == 2 && c2 > -INFINITY ? fmaxf(__fadd_rn(c1, c2), kLowest) : c1;
     if (r != 0 || g >= p.n_group) value = -INFINITY;
     uint32_t kept = 0;
     for (int j = 0; j < p.topk_group; ++j) {
@@ -211,9 +213,9 @@ __global__ void __launch_bounds__(kRouteWarps * 32, VPL <= 8 ? 5 : VPL <= 16 ? 4
             // twice the error of a fast choice: 2^-18 of the score (an exponent of up to 88 costs the fast
             // exponential 2^-18), the sum with the bias 2^-22 of the result
             const float slack = fabsf(bound) * 0x1p-16f + (p.bias ? 0x1p-17f : 0.f);
-            bound = !p.bias && bound < 1e-30f ? kClosedFrom : bound - slack;   // (tiny scores: all of them)
+            bound = !p.bias && bound < 1e-30f ? kLowest : bound - slack;   // (tiny scores: all of them)
         }
-        bound = fmaxf(bound, kClosedFrom);   // fewer lanes than top_k: every open expert
+        bound = fmaxf(bound, kLowest);   // fewer lanes than top_k (or NaN: infinite choices): every open expert
         uint32_t in = 0;                     // bit i: candidate
 #pragma unroll
         for (int i = 0; i < VPL; ++i) in |= v[i] >= bound ? 1u << i : 0u;

@@ -10,6 +10,7 @@ pytestmark = pytest.mark.gpu
 
 mse = pytest.importorskip("moe_shared_expert_gb300")
 
+LOWEST = torch.finfo(torch.float32).min
 # n_group, topk_group, group_top
 GROUPS = [(1, 1, 1), (4, 2, 2), (4, 2, 1), (8, 3, 2)]
 
@@ -111,3 +112,35 @@ def test_an_infinite_bias(n_group):
     ids, w = mse.moe_route(torch.zeros(1, E).cuda(), 6, bias=bias.cuda(), n_group=n_group, topk_group=1 if n_group == 1 else 2)
     assert ids.cpu().tolist() == [[10, 30, 0, 1, 2, -1]]
     assert torch.allclose(w.cpu(), torch.tensor([[0.2] * 5 + [0.0]]))
+
+
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("low", [LOWEST, -3.3895313892515355e38, -1e38, -1e4])
+@pytest.mark.parametrize("E,k", [(8, 8), (40, 12), (500, 9)])
+def test_a_low_bias_puts_an_expert_last(E, k, low, scoring):
+    # the bias moves the choice; it is the logit that closes an expert
+    logits = torch.randn(3, E, generator=gen(E)) * 1e-3
+    bias = torch.zeros(E)
+    bias[2:E - 2] = low
+    ids, w = mse.moe_route(logits.cuda(), k, scoring=scoring, bias=bias.cuda(), renormalise=False)
+    score = torch.sigmoid(logits.double()) if scoring == "sigmoid" else torch.softmax(logits.double(), 1)
+    for t in range(3):
+        first = sorted((0, 1, E - 2, E - 1), key=lambda e: -float(logits[t, e]))
+        rest = list(range(2, E - 2))
+        if low == -1e4:   # its rounding leaves an order among the low ones
+            got = ids.cpu()[t].tolist()
+            assert got[:4] == first and set(got[4:]) <= set(rest) and len(set(got)) == k
+        else:
+            assert ids.cpu()[t].tolist() == (first + rest)[:k]
+        assert torch.allclose(w.cpu()[t].double(), score[t][ids.cpu()[t].long()], rtol=1e-6)
+
+
+@pytest.mark.parametrize("group_top", [1, 2])
+def test_a_low_bias_in_every_group(group_top):
+    E, G = 48, 4
+    logits = torch.zeros(2, E)
+    logits[1, :12] = -math.inf                     # the first group is closed to the second token
+    bias = torch.full((E,), LOWEST)
+    ids, w = mse.moe_route(logits.cuda(), 3, bias=bias.cuda(), n_group=G, topk_group=2, group_top=group_top)
+    assert ids.cpu().tolist() == [[0, 1, 2], [12, 13, 14]]
+    assert torch.allclose(w.cpu(), torch.full((2, 3), 1 / 3), rtol=1e-6)

@@ -295,7 +295,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32, VPL <= 8 ? 5 : VPL <= 16 ? 4
         }
         if (lane < p.top_k) {
             p.ids[t * p.top_k + lane] = id;
-            p.weights[t * p.top_k + lane] = w * p.scale;
+            p.weights[t * p.top_k + lane] = id >= 0 ? w * p.scale : 0.f;
         }
     }
 }

@@ -144,3 +144,13 @@ def test_a_low_bias_in_every_group(group_top):
     ids, w = mse.moe_route(logits.cuda(), 3, bias=bias.cuda(), n_group=G, topk_group=2, group_top=group_top)
     assert ids.cpu().tolist() == [[0, 1, 2], [12, 13, 14]]
     assert torch.allclose(w.cpu(), torch.full((2, 3), 1 / 3), rtol=1e-6)
+
+
+def test_empty_slots_have_weight_zero_whatever_the_scale():
+    logits = torch.full((2, 9), -math.inf)
+    logits[1, 4] = 0.0
+    for scale in (math.inf, -1.0, math.nan):
+        ids, w = mse.moe_route(logits.cuda(), 2, scale=scale)
+        assert ids.cpu().tolist() == [[-1, -1], [4, -1]]
+        w = w.cpu()
+        assert [math.copysign(1.0, v) * (v == 0) for v in (*w[0].tolist(), float(w[1, 1]))] == [1.0] * 3, scale

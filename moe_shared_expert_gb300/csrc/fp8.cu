@@ -449,38 +449,41 @@ __global__ void __launch_bounds__(256) block_simt_kernel(const BlockGemm g) {
         t.rows = (int)min((int64_t)kSimtTileRows, g.T - t.row0);
         t.expert = 0;
     }
-    const int64_t n0 = (int64_t)blockIdx.y * 16, n = n0 + threadIdx.x % 16;
     const int r = threadIdx.x / 16;
     const uint8_t *w = g.wq + (int64_t)t.expert * g.w_group_rows * g.ldw;
     const float *ws = g.ws + (int64_t)t.expert * g.ws_group;
-    float acc[MATS] = {};
-    for (int b = 0; b < g.kb; ++b) {
-        for (int i = threadIdx.x; i < 16 * kBlock; i += 256) {
-            const int rr = i / kBlock, kk = i % kBlock;
-            const int64_t k = (int64_t)b * kBlock + kk;
-            sx[rr][kk] = rr < t.rows && k < g.K ? e4m3_to_f32(g.xq[(int64_t)(t.row0 + rr) * g.ldx + k]) : 0.f;
+    // (one round of columns up to 1,048,560 of them: the grid's second dimension ends at 65,535)
+    for (int64_t n0 = (int64_t)blockIdx.y * 16; n0 < g.N; n0 += (int64_t)gridDim.y * 16) {
+        const int64_t n = n0 + threadIdx.x % 16;
+        float acc[MATS] = {};
+        for (int b = 0; b < g.kb; ++b) {
+            for (int i = threadIdx.x; i < 16 * kBlock; i += 256) {
+                const int rr = i / kBlock, kk = i % kBlock;
+                const int64_t k = (int64_t)b * kBlock + kk;
+                sx[rr][kk] = rr < t.rows && k < g.K ? e4m3_to_f32(g.xq[(int64_t)(t.row0 + rr) * g.ldx + k]) : 0.f;
 #pragma unroll
-            for (int m = 0; m < MATS; ++m)
-                sw[m][rr][kk] =
-                    n0 + rr < g.N && k < g.K ? e4m3_to_f32(w[(n0 + rr + m * g.up_rows) * g.ldw + k]) : 0.f;
-        }
-        __syncthreads();
-        if (r < t.rows && n < g.N) {
-            const float xs = g.xs[(int64_t)(t.row0 + r) * g.kb + b];
-#pragma unroll
-            for (int m = 0; m < MATS; ++m) {
-                float d = 0.f;
-                for (int kk = 0; kk < kBlock; ++kk) d = fmaf(sx[r][kk], sw[m][threadIdx.x % 16][kk], d);
-                acc[m] = fmaf(d, xs * ws[n / kBlock * g.kb + b + m * g.up_scales], acc[m]);
+                for (int m = 0; m < MATS; ++m)
+                    sw[m][rr][kk] =
+                        n0 + rr < g.N && k < g.K ? e4m3_to_f32(w[(n0 + rr + m * g.up_rows) * g.ldw + k]) : 0.f;
             }
+            __syncthreads();
+            if (r < t.rows && n < g.N) {
+                const float xs = g.xs[(int64_t)(t.row0 + r) * g.kb + b];
+#pragma unroll
+                for (int m = 0; m < MATS; ++m) {
+                    float d = 0.f;
+                    for (int kk = 0; kk < kBlock; ++kk) d = fmaf(sx[r][kk], sw[m][threadIdx.x % 16][kk], d);
+                    acc[m] = fmaf(d, xs * ws[n / kBlock * g.kb + b + m * g.up_scales], acc[m]);
+                }
+            }
+            __syncthreads();
         }
-        __syncthreads();
+        if (r >= t.rows || n >= g.N) continue;
+        const int64_t at = (int64_t)(t.row0 + r) * g.ldo + n;
+        if constexpr (EPI == BLOCK_BF16) static_cast<uint16_t *>(g.out)[at] = f32_to_bf16_bits(acc[0]);
+        if constexpr (EPI == BLOCK_F32) static_cast<float *>(g.out)[at] = acc[0];
+        if constexpr (EPI == BLOCK_SWIGLU) static_cast<float *>(g.out)[at] = glu(acc[0], acc[1]);
     }
-    if (r >= t.rows || n >= g.N) return;
-    const int64_t at = (int64_t)(t.row0 + r) * g.ldo + n;
-    if constexpr (EPI == BLOCK_BF16) static_cast<uint16_t *>(g.out)[at] = f32_to_bf16_bits(acc[0]);
-    if constexpr (EPI == BLOCK_F32) static_cast<float *>(g.out)[at] = acc[0];
-    if constexpr (EPI == BLOCK_SWIGLU) static_cast<float *>(g.out)[at] = glu(acc[0], acc[1]);
 }
 
 }  // namespace
@@ -539,7 +542,7 @@ cudaError_t launch_combine(const float *o, int64_t ldo, const int32_t *pos, cons
 
 cudaError_t launch_block_simt(const BlockGemm &g, bool pdl, cudaStream_t s) {
     const dim3 grid((unsigned)(g.tiles ? g.max_tiles : (g.T + kSimtTileRows - 1) / kSimtTileRows),
-                    (unsigned)((g.N + 15) / 16));
+                    (unsigned)std::min<int64_t>((g.N + 15) / 16, 65535));
     switch (g.epi) {
         case BLOCK_BF16: return launch_kernel(block_simt_kernel<BLOCK_BF16>, grid, 256, 0, pdl, 1, s, g);
         case BLOCK_F32: return launch_kernel(block_simt_kernel<BLOCK_F32>, grid, 256, 0, pdl, 1, s, g);

@@ -1,8 +1,10 @@
-"""Routed-expert operators at the edges of their arguments: infinite and undefined logits and biases."""
+"""Routed-expert operators at the edges of their arguments: infinite and undefined logits and biases, sizes beyond a
+grid's second dimension."""
 import math
 
 import pytest
 
+from tests.helpers import kernel_path
 from tests.test_gpu_routed import gen, make_experts
 
 torch = pytest.importorskip("torch")
@@ -154,3 +156,34 @@ def test_empty_slots_have_weight_zero_whatever_the_scale():
         assert ids.cpu().tolist() == [[-1, -1], [4, -1]]
         w = w.cpu()
         assert [math.copysign(1.0, v) * (v == 0) for v in (*w[0].tolist(), float(w[1, 1]))] == [1.0] * 3, scale
+
+
+# ------------------------------------------------------------------------------------ sizes beyond 65535 tiles
+
+@pytest.mark.parametrize("N", [1048560, 1048561, 1048700, 2100001])
+def test_generic_product_of_many_weight_rows(N):
+    T, K, pitch = 3, 20, 21                        # rows of an odd pitch: the generic kernel; whole numbers: no rounding
+    g = gen(N)
+    w = torch.randint(-8, 9, (N, K), generator=g).float()
+    x = torch.randint(-8, 9, (T, K), generator=g).float()
+    wq = torch.zeros(N, pitch, dtype=torch.uint8, device="cuda")[:, :K]
+    wq.copy_(w.to(torch.float8_e4m3fn).view(torch.uint8))
+    ws = torch.randint(1, 5, (-(-N // 128), 1), generator=g).float()
+    out = mse.fp8_block_matmul(x.to(torch.float8_e4m3fn).cuda(), torch.ones(T, 1, device="cuda"), wq, ws.cuda(),
+                               out_dtype=torch.float32)
+    want = (x @ w.t()) * ws.repeat_interleave(128, 0)[:N, 0]
+    assert torch.equal(out.cpu(), want)
+
+
+def test_generic_experts_of_a_long_row():
+    E, H, I, T = 1, 1048560 + 130, 16, 2
+    qgu, sgu, qd, sd = make_experts(E, H, I, 6)
+    x = torch.randn(T, H, generator=gen(7)).to(torch.bfloat16).cuda()
+    ids, w = torch.zeros(T, 1, dtype=torch.int32, device="cuda"), torch.ones(T, 1, device="cuda")
+    y = mse.moe_experts_forward(x, ids, w, qgu, sgu, qd, sd)
+    with kernel_path(mse.PATH_GENERIC):
+        z = mse.moe_experts_forward(x, ids, w, qgu, sgu, qd, sd)
+    # the same 8-bit operands and one h of 16 values a token: a value of h that falls on the other side of two e4m3
+    # numbers moves by 1/8 at most, and the results round to bf16
+    assert float((y.double() - z.double()).norm() / y.double().norm()) < 0.05
+    assert torch.isfinite(z).all()

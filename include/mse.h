@@ -499,6 +499,9 @@ MSE_API void mse_set_phase_events(void *ev_begin, void *ev_mid, void *ev_end);
  * The routed experts beside the shared expert: routing, products in 8 bits with a
  * scale for each block of 128, and the experts' layer.  Inference only, like the
  * rest of the library.
+ *
+ * Sizes beyond these are MSE_ERR_INVALID_ARG: token rows (T, rows; T * top_k of the experts) 2^30; weight rows and
+ * inner sizes (N, K, H, I) 2^22; row pitches 2^32 elements; blocks of 128 x 128 of one fp8_block_quantise 2^31 - 1.
  * ------------------------------------------------------------------------- */
 
 typedef enum { MSE_SCORE_SOFTMAX = 0, MSE_SCORE_SIGMOID = 1 } mse_score;

@@ -119,7 +119,8 @@ __global__ void __launch_bounds__(256) quantise_tiles_kernel(const uint16_t *x, 
     __shared__ uint32_t part[8];
     pdl_wait();
     const int l = threadIdx.x % 16, h = threadIdx.x / 16;
-    const int64_t r0 = (int64_t)blockIdx.y * kBlock + h, k = (int64_t)blockIdx.x * kBlock + l * 8;
+    const uint32_t kb = (uint32_t)((K + kBlock - 1) / kBlock);
+    const int64_t r0 = (int64_t)(blockIdx.x / kb) * kBlock + h, k = (int64_t)(blockIdx.x % kb) * kBlock + l * 8;
     uint4 raw[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -141,7 +142,7 @@ __global__ void __launch_bounds__(256) quantise_tiles_kernel(const uint16_t *x, 
         const int64_t r = r0 + i * 16;
         if (r < rows) store8(q + r * ldq + k, K - k, wide_out, e4m3x8(raw[i], scale));
     }
-    if (threadIdx.x == 0) scales[blockIdx.y * (int64_t)gridDim.x + blockIdx.x] = block_scale(a);
+    if (threadIdx.x == 0) scales[blockIdx.x] = block_scale(a);
 }
 
 // fp32 rows of the tiles of a dispatch, one warp per block of 128
@@ -505,7 +506,7 @@ cudaError_t launch_quantise_rows(const uint16_t *x, int64_t rows, int64_t K, int
 
 cudaError_t launch_quantise_tiles(const uint16_t *x, int64_t rows, int64_t K, int64_t ldx, uint8_t *q, int64_t ldq,
                                   float *scales, bool pdl, cudaStream_t s) {
-    const dim3 grid((unsigned)blocks_of(K), (unsigned)blocks_of(rows));
+    const dim3 grid((unsigned)(blocks_of(K) * blocks_of(rows)));   // block rows one after another
     const int wide_out = ldq % 8 == 0 && (reinterpret_cast<uintptr_t>(q) & 7u) == 0;
     return launch_kernel(quantise_tiles_kernel, grid, 256, 0, pdl, 1, s, x, rows, K, ldx, align_of(x, ldx), q, ldq, wide_out,
                          scales);

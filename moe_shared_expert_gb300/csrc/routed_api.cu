@@ -171,7 +171,7 @@ mse_status fp8_block_quantise(const mse_bf16 *x, int64_t rows, int64_t K, int64_
         rows > kMaxRows || K > kMaxInner || ldx > kMaxPitch || ldq > kMaxPitch)
         return MSE_ERR_INVALID_ARG;
     const int64_t scale_rows = block_rows == 1 ? rows : blocks_of(rows);
-    if (block_rows != 1 && scale_rows > 65535) return MSE_ERR_INVALID_ARG;
+    if (block_rows != 1 && scale_rows * blocks_of(K) > INT32_MAX) return MSE_ERR_INVALID_ARG;   // a CTA for each block
     if (q_capacity < (rows - 1) * ldq + K || scales_capacity < scale_rows * blocks_of(K)) return MSE_ERR_GEOMETRY;
     DeviceView d;
     const mse_status st = device_view(&d);

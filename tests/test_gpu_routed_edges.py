@@ -187,3 +187,13 @@ def test_generic_experts_of_a_long_row():
     # numbers moves by 1/8 at most, and the results round to bf16
     assert float((y.double() - z.double()).norm() / y.double().norm()) < 0.05
     assert torch.isfinite(z).all()
+
+
+def test_quantise_of_many_row_blocks():
+    rows, K = 65535 * 128 + 131, 3                 # 65,537 blocks of rows
+    x = torch.randn(rows, K, generator=gen(8)).to(torch.bfloat16).cuda()
+    q, s = mse.fp8_block_quantise(x, block_rows=128)
+    assert s.shape == (65537, 1)
+    for r0 in (0, 128 * 40000, 65535 * 128, 65536 * 128):
+        part, ps = mse.fp8_block_quantise(x[r0:r0 + 128].clone(), block_rows=128)
+        assert torch.equal(q[r0:r0 + 128].float(), part.float()) and torch.equal(s[r0 // 128:r0 // 128 + 1], ps)

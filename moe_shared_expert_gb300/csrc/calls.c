@@ -20,8 +20,6 @@ static int take(Py_ssize_t n, Py_ssize_t want, const char *name) {
     return 0;
 }
 
-static PyObject *done(mse_status st) { return PyErr_Occurred() ? NULL : PyLong_FromLong((long)st); }
-
 #define I(k) integer(a[k])
 #define P(k) address(a[k])
 #define READY(f, name)                                              \
@@ -30,7 +28,16 @@ static PyObject *done(mse_status st) { return PyErr_Occurred() ? NULL : PyLong_F
         return NULL;                                                \
     }
 
-/* Arguments are converted before the call, so that a bad one calls nothing. */
+/* Arguments are converted before the call, so that a bad one calls nothing.  The interpreter's lock is let go over the
+ * call, as ctypes does: a launch waits where the queue of launches is full, perhaps for a host function in Python. */
+#define CALL(expression)                  \
+    if (PyErr_Occurred()) return NULL;    \
+    mse_status status;                    \
+    Py_BEGIN_ALLOW_THREADS                \
+    status = (expression);                \
+    Py_END_ALLOW_THREADS                  \
+    return PyLong_FromLong((long)status);
+
 static PyObject *route(PyObject *self, PyObject *const *a, Py_ssize_t n) {
     (void)self;
     READY(f_route, "moe_route")
@@ -44,9 +51,8 @@ static PyObject *route(PyObject *self, PyObject *const *a, Py_ssize_t n) {
     float *weights = P(14);
     const long long cap = I(15);
     void *stream = P(16);
-    if (PyErr_Occurred()) return NULL;
-    return done(f_route(logits, (mse_dtype)dtype, T, E, ld, bias, (mse_score)scoring, (int)groups, (int)kept, (int)top,
-                        (int)k, (int)norm, (float)scale, ids, weights, cap, stream));
+    CALL(f_route(logits, (mse_dtype)dtype, T, E, ld, bias, (mse_score)scoring, (int)groups, (int)kept, (int)top,
+                 (int)k, (int)norm, (float)scale, ids, weights, cap, stream))
 }
 
 static PyObject *matmul(PyObject *self, PyObject *const *a, Py_ssize_t n) {
@@ -57,8 +63,7 @@ static PyObject *matmul(PyObject *self, PyObject *const *a, Py_ssize_t n) {
     const long long ldx = I(1), ldw = I(4), T = I(6), N = I(7), K = I(8), dtype = I(10), cap = I(11);
     const float *xs = P(2), *ws = P(5);
     void *out = P(9), *stream = P(12);
-    if (PyErr_Occurred()) return NULL;
-    return done(f_matmul(xq, ldx, xs, wq, ldw, ws, T, N, K, out, (mse_dtype)dtype, cap, stream));
+    CALL(f_matmul(xq, ldx, xs, wq, ldw, ws, T, N, K, out, (mse_dtype)dtype, cap, stream))
 }
 
 static PyObject *linear(PyObject *self, PyObject *const *a, Py_ssize_t n) {
@@ -70,8 +75,7 @@ static PyObject *linear(PyObject *self, PyObject *const *a, Py_ssize_t n) {
     const float *ws = P(4);
     const long long ldx = I(1), ldw = I(3), T = I(5), N = I(6), K = I(7), dtype = I(9), cap = I(10), bytes = I(12);
     void *y = P(8), *workspace = P(11), *stream = P(13);
-    if (PyErr_Occurred()) return NULL;
-    return done(f_linear(x, ldx, wq, ldw, ws, T, N, K, y, (mse_dtype)dtype, cap, workspace, (size_t)bytes, stream));
+    CALL(f_linear(x, ldx, wq, ldw, ws, T, N, K, y, (mse_dtype)dtype, cap, workspace, (size_t)bytes, stream))
 }
 
 static PyObject *experts(PyObject *self, PyObject *const *a, Py_ssize_t n) {
@@ -86,9 +90,8 @@ static PyObject *experts(PyObject *self, PyObject *const *a, Py_ssize_t n) {
     void *workspace = P(18), *stream = P(20);
     const long long T = I(1), H = I(2), k = I(5), ld_gate_up = I(7), ld_down = I(10), E = I(12), inter = I(13),
                     first = I(14), cap = I(17), bytes = I(19);
-    if (PyErr_Occurred()) return NULL;
-    return done(f_experts(x, T, H, ids, weights, (int)k, w_gate_up, ld_gate_up, s_gate_up, w_down, ld_down, s_down, E,
-                          inter, first, shared, y, cap, workspace, (size_t)bytes, stream));
+    CALL(f_experts(x, T, H, ids, weights, (int)k, w_gate_up, ld_gate_up, s_gate_up, w_down, ld_down, s_down, E,
+                   inter, first, shared, y, cap, workspace, (size_t)bytes, stream))
 }
 
 static PyObject *bind(PyObject *self, PyObject *const *a, Py_ssize_t n) {

@@ -52,3 +52,9 @@ def test_other_threads_run_during_a_call(calls, name):
     other.join()
     assert status == 0 and end - begin >= 0.4
     assert sum(begin < t < end for t in ticks) >= 10
+
+
+def test_the_entry_in_c_belongs_to_this_interpreter(calls):
+    # another Python, or another machine, finds no file of its own and takes ctypes
+    assert os.path.basename(_build.CALLS) == "_calls" + sysconfig.get_config_var("EXT_SUFFIX")
+    assert os.path.samefile(calls.__file__, _build.CALLS)

@@ -12,6 +12,11 @@ static __typeof__(&fp8_block_matmul) f_matmul;
 static __typeof__(&moe_experts_forward) f_experts;
 
 static long long integer(PyObject *o) { return o == Py_None ? 0 : PyLong_AsLongLong(o); }
+static int small(PyObject *o) {
+    const long long v = integer(o);
+    if (v != (int)v && !PyErr_Occurred()) PyErr_SetString(PyExc_OverflowError, "number beyond an int");
+    return (int)v;
+}
 static void *address(PyObject *o) { return o == Py_None ? NULL : PyLong_AsVoidPtr(o); }
 
 static int take(Py_ssize_t n, Py_ssize_t want, const char *name) {
@@ -21,6 +26,7 @@ static int take(Py_ssize_t n, Py_ssize_t want, const char *name) {
 }
 
 #define I(k) integer(a[k])
+#define S(k) small(a[k])
 #define P(k) address(a[k])
 #define READY(f, name)                                              \
     if (!(f)) {                                                     \
@@ -43,16 +49,17 @@ static PyObject *route(PyObject *self, PyObject *const *a, Py_ssize_t n) {
     READY(f_route, "moe_route")
     if (!take(n, 17, "moe_route")) return NULL;
     const void *logits = P(0);
-    const long long dtype = I(1), T = I(2), E = I(3), ld = I(4);
+    const int dtype = S(1);
+    const long long T = I(2), E = I(3), ld = I(4);
     const float *bias = P(5);
-    const long long scoring = I(6), groups = I(7), kept = I(8), top = I(9), k = I(10), norm = I(11);
+    const int scoring = S(6), groups = S(7), kept = S(8), top = S(9), k = S(10), norm = S(11);
     const double scale = PyFloat_AsDouble(a[12]);
     int32_t *ids = P(13);
     float *weights = P(14);
     const long long cap = I(15);
     void *stream = P(16);
-    CALL(f_route(logits, (mse_dtype)dtype, T, E, ld, bias, (mse_score)scoring, (int)groups, (int)kept, (int)top,
-                 (int)k, (int)norm, (float)scale, ids, weights, cap, stream))
+    CALL(f_route(logits, (mse_dtype)dtype, T, E, ld, bias, (mse_score)scoring, groups, kept, top, k, norm,
+                 (float)scale, ids, weights, cap, stream))
 }
 
 static PyObject *matmul(PyObject *self, PyObject *const *a, Py_ssize_t n) {
@@ -60,7 +67,8 @@ static PyObject *matmul(PyObject *self, PyObject *const *a, Py_ssize_t n) {
     READY(f_matmul, "fp8_block_matmul")
     if (!take(n, 13, "fp8_block_matmul")) return NULL;
     const uint8_t *xq = P(0), *wq = P(3);
-    const long long ldx = I(1), ldw = I(4), T = I(6), N = I(7), K = I(8), dtype = I(10), cap = I(11);
+    const long long ldx = I(1), ldw = I(4), T = I(6), N = I(7), K = I(8), cap = I(11);
+    const int dtype = S(10);
     const float *xs = P(2), *ws = P(5);
     void *out = P(9), *stream = P(12);
     CALL(f_matmul(xq, ldx, xs, wq, ldw, ws, T, N, K, out, (mse_dtype)dtype, cap, stream))
@@ -73,7 +81,8 @@ static PyObject *linear(PyObject *self, PyObject *const *a, Py_ssize_t n) {
     const mse_bf16 *x = P(0);
     const uint8_t *wq = P(2);
     const float *ws = P(4);
-    const long long ldx = I(1), ldw = I(3), T = I(5), N = I(6), K = I(7), dtype = I(9), cap = I(10), bytes = I(12);
+    const long long ldx = I(1), ldw = I(3), T = I(5), N = I(6), K = I(7), cap = I(10), bytes = I(12);
+    const int dtype = S(9);
     void *y = P(8), *workspace = P(11), *stream = P(13);
     CALL(f_linear(x, ldx, wq, ldw, ws, T, N, K, y, (mse_dtype)dtype, cap, workspace, (size_t)bytes, stream))
 }
@@ -88,9 +97,10 @@ static PyObject *experts(PyObject *self, PyObject *const *a, Py_ssize_t n) {
     const uint8_t *w_gate_up = P(6), *w_down = P(9);
     mse_bf16 *y = P(16);
     void *workspace = P(18), *stream = P(20);
-    const long long T = I(1), H = I(2), k = I(5), ld_gate_up = I(7), ld_down = I(10), E = I(12), inter = I(13),
+    const long long T = I(1), H = I(2), ld_gate_up = I(7), ld_down = I(10), E = I(12), inter = I(13),
                     first = I(14), cap = I(17), bytes = I(19);
-    CALL(f_experts(x, T, H, ids, weights, (int)k, w_gate_up, ld_gate_up, s_gate_up, w_down, ld_down, s_down, E,
+    const int k = S(5);
+    CALL(f_experts(x, T, H, ids, weights, k, w_gate_up, ld_gate_up, s_gate_up, w_down, ld_down, s_down, E,
                    inter, first, shared, y, cap, workspace, (size_t)bytes, stream))
 }
 

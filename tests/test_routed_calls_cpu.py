@@ -58,3 +58,19 @@ def test_the_entry_in_c_belongs_to_this_interpreter(calls):
     # another Python, or another machine, finds no file of its own and takes ctypes
     assert os.path.basename(_build.CALLS) == "_calls" + sysconfig.get_config_var("EXT_SUFFIX")
     assert os.path.samefile(calls.__file__, _build.CALLS)
+
+
+@pytest.mark.parametrize("name,at", [("moe_route", i) for i in (1, 6, 7, 8, 9, 10, 11)]
+                         + [("fp8_block_linear", 9), ("fp8_block_matmul", 10), ("moe_experts_forward", 5)])
+def test_numbers_beyond_an_int_are_refused(calls, name, at):
+    # 2^32 + 1 groups are not one group
+    def never(*_):
+        raise AssertionError("called")
+
+    made = ctypes.CFUNCTYPE(ctypes.c_int)(never)
+    calls.bind(*[ctypes.cast(made, ctypes.c_void_p).value] * 4)
+    for number in (2 ** 32 + 1, 2 ** 31, -2 ** 31 - 1):
+        a = numbers(name)
+        a[at] = number
+        with pytest.raises(OverflowError):
+            getattr(calls, name)(*a)

@@ -1,9 +1,9 @@
 """The routed experts beside the shared expert: routing, 8-bit block products, the experts' layer.
 
 Thin bindings like the rest of the package (torch tensors in, the library's functions by name); formulas, layouts
-and limits are in ``include/mse.h``.  8-bit tensors are ``torch.float8_e4m3fn`` (or ``uint8`` bit patterns) whose last
-dimension is contiguous; their rows may have a pitch.  Rows whose pitch is a multiple of 16 bytes, as
-``fp8_block_quantise`` makes them, take the tensor-core kernels.
+and limits are in ``include/mse.h``.  All tensors of a call are on the current device.  8-bit tensors are
+``torch.float8_e4m3fn`` (or ``uint8`` bit patterns) whose last dimension is contiguous; their rows may have a pitch.
+Rows whose pitch is a multiple of 16 bytes, as ``fp8_block_quantise`` makes them, take the tensor-core kernels.
 """
 from __future__ import annotations
 
@@ -22,7 +22,7 @@ torch = None   # set by _load(); the package itself imports without it
 def _load():
     """torch, the library's functions and the dtypes, looked up once: a call's own Python is most of what a
     single token's operators cost."""
-    global torch, _C, _BF16, _F32, _E4M3, _raw_stream, _call_route, _call_linear, _call_matmul, _call_experts
+    global torch, _C, _BF16, _F32, _E4M3, _raw_stream, _current, _call_route, _call_linear, _call_matmul, _call_experts
     import torch as _torch
     _C = C = _mse.lib()
     entries = C.moe_route, C.fp8_block_linear, C.fp8_block_matmul, C.moe_experts_forward
@@ -36,6 +36,7 @@ def _load():
     # the current stream's handle without making a Stream object, where this torch has it
     _raw_stream = getattr(_torch._C, "_cuda_getCurrentRawStream", None) or (
         lambda index: _torch.cuda.current_stream(index).cuda_stream)
+    _current = getattr(_torch._C, "_cuda_getDevice", None) or _torch.cuda.current_device
     torch = _torch
 
 
@@ -51,10 +52,21 @@ def _said(t):
     return "None" if t is None else f"{t.dtype} {tuple(t.shape)}, strides {t.stride()}, on {t.device}"
 
 
-def _rows(t, name, dtypes, ndim):
-    """The pitch of the rows of a CUDA tensor whose last dimension is contiguous and whose matrices follow one another."""
-    if t is None or not t.is_cuda or t.dtype not in dtypes or t.dim() != ndim:
-        raise ValueError(f"{name}: need a {ndim}-d CUDA tensor of {dtypes}, got {_said(t)}")
+def _device(t, name):
+    """The index of t's GPU, which has to be the current one: the library launches there."""
+    index = -1 if t is None else t.get_device()
+    if index < 0:
+        raise ValueError(f"{name}: need a CUDA tensor, got {_said(t)}")
+    current = _current()
+    if index != current:
+        raise ValueError(f"{name}: on cuda:{index}, and the current device is cuda:{current}")
+    return index
+
+
+def _rows(t, name, dtypes, ndim, device):
+    """The pitch of the rows of a tensor on `device` whose last dimension is contiguous and whose matrices follow one another."""
+    if t is None or t.get_device() != device or t.dtype not in dtypes or t.dim() != ndim:
+        raise ValueError(f"{name}: need a {ndim}-d tensor of {dtypes} on cuda:{device}, got {_said(t)}")
     shape, stride = t.shape, t.stride()
     cols = shape[-1]
     ld = stride[-2] if shape[-2] > 1 else max(cols, stride[-2])
@@ -63,15 +75,21 @@ def _rows(t, name, dtypes, ndim):
     return ld
 
 
-def _dense(t, name, dtype, shape):
-    if t is None or t.dtype is not dtype or t.shape != shape or not t.is_cuda or not t.is_contiguous():
-        raise ValueError(f"{name}: need a contiguous CUDA tensor of {dtype} {tuple(shape)}, got {_said(t)}")
+def _dense(t, name, dtype, shape, device):
+    if t is None or t.dtype is not dtype or t.shape != shape or t.get_device() != device or not t.is_contiguous():
+        raise ValueError(f"{name}: need a contiguous tensor of {dtype} {tuple(shape)} on cuda:{device}, got {_said(t)}")
 
 
-def _handle(stream, t):
-    """cudaStream_t of `stream`, or of the current stream of t's device."""
+def _taken(workspace, device):
+    """A caller's workspace: its bytes are what the call may write."""
+    if workspace.get_device() != device or not workspace.is_contiguous():
+        raise ValueError(f"workspace: need a contiguous tensor on cuda:{device}, got {_said(workspace)}")
+
+
+def _handle(stream, device):
+    """cudaStream_t of `stream`, or of the device's current stream."""
     if stream is None:
-        return _raw_stream(t.device.index)
+        return _raw_stream(device)
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
@@ -98,23 +116,24 @@ def moe_route(logits, top_k, scoring="sigmoid", bias=None, n_group=1, topk_group
     close an expert.  Slots for which no expert is left hold id -1 and weight 0."""
     if torch is None:
         _load()
-    ld = _rows(logits, "logits", (_BF16, _F32), 2)
+    device = _device(logits, "logits")
+    ld = _rows(logits, "logits", (_BF16, _F32), 2, device)
     T, E = logits.shape
     if scoring not in _SCORING:
         raise ValueError(f"scoring must be one of {sorted(_SCORING)}, got {scoring!r}")
     if bias is not None:
-        _dense(bias, "bias", _F32, (E,))
+        _dense(bias, "bias", _F32, (E,), device)
     if ids is None:
         ids = _empty(stream, (T, max(top_k, 0)), torch.int32, logits.device)
     else:
-        _dense(ids, "ids", torch.int32, (T, top_k))
+        _dense(ids, "ids", torch.int32, (T, top_k), device)
     if weights is None:
         weights = _empty(stream, (T, max(top_k, 0)), _F32, logits.device)
     else:
-        _dense(weights, "weights", _F32, (T, top_k))
+        _dense(weights, "weights", _F32, (T, top_k), device)
     st = _call_route(logits.data_ptr(), int(logits.dtype is _F32), T, E, ld, None if bias is None else bias.data_ptr(),
                       _SCORING[scoring], n_group, topk_group, group_top, top_k, 1 if renormalise else 0, scale,
-                      ids.data_ptr(), weights.data_ptr(), T * top_k, _handle(stream, logits))
+                      ids.data_ptr(), weights.data_ptr(), T * top_k, _handle(stream, device))
     if st:
         _mse._check("moe_route", st)
     return ids, weights
@@ -133,7 +152,8 @@ def fp8_block_quantise(x, block_rows=1, stream=None):
         _load()
     if x is None or x.dim() not in (2, 3):
         raise ValueError(f"x: need a 2-d or 3-d tensor, got {_said(x)}")
-    ld = _rows(x, "x", (_BF16,), x.dim())
+    device = _device(x, "x")
+    ld = _rows(x, "x", (_BF16,), x.dim(), device)
     *lead, rows, K = x.shape
     pitch, srows, kb = _pad16(K), rows if block_rows == 1 else _blocks(rows), _blocks(K)
     q = _empty(stream, (*lead, rows, pitch), torch.uint8, x.device)
@@ -141,7 +161,7 @@ def fp8_block_quantise(x, block_rows=1, stream=None):
     for i in range(lead[0] if lead else 1):
         st = _C.fp8_block_quantise(x.data_ptr() + 2 * i * rows * ld, rows, K, ld, block_rows,
                                    q.data_ptr() + i * rows * pitch, pitch, rows * pitch,
-                                   scales.data_ptr() + 4 * i * srows * kb, srows * kb, _handle(stream, x))
+                                   scales.data_ptr() + 4 * i * srows * kb, srows * kb, _handle(stream, device))
         if st:
             _mse._check("fp8_block_quantise", st)
     return q.view(torch.float8_e4m3fn)[..., :K], scales
@@ -153,7 +173,7 @@ def _out(out, dtype, name, shape, like, stream):
     dtype = _F32 if code else _BF16
     if out is None:
         return _empty(stream, shape, dtype, like.device), code
-    _dense(out, name, dtype, shape)
+    _dense(out, name, dtype, shape, like.get_device())
     return out, code
 
 
@@ -161,15 +181,16 @@ def fp8_block_matmul(xq, xs, wq, ws, out_dtype=None, out=None, stream=None):
     """out [T, N] = xq wq^T with block scales; xq [T, K], xs [T, K / 128], wq [N, K], ws [N / 128, K / 128]."""
     if torch is None:
         _load()
-    ldx, ldw = _rows(xq, "xq", _E4M3, 2), _rows(wq, "wq", _E4M3, 2)
+    device = _device(xq, "xq")
+    ldx, ldw = _rows(xq, "xq", _E4M3, 2, device), _rows(wq, "wq", _E4M3, 2, device)
     (T, K), (N, Kw) = xq.shape, wq.shape
     if K != Kw:
         raise ValueError(f"xq and wq differ in K: {K} and {Kw}")
-    _dense(xs, "xs", _F32, (T, _blocks(K)))
-    _dense(ws, "ws", _F32, (_blocks(N), _blocks(K)))
+    _dense(xs, "xs", _F32, (T, _blocks(K)), device)
+    _dense(ws, "ws", _F32, (_blocks(N), _blocks(K)), device)
     out, code = _out(out, out_dtype, "out", (T, N), xq, stream)
     st = _call_matmul(xq.data_ptr(), ldx, xs.data_ptr(), wq.data_ptr(), ldw, ws.data_ptr(), T, N, K,
-                             out.data_ptr(), code, T * N, _handle(stream, xq))
+                             out.data_ptr(), code, T * N, _handle(stream, device))
     if st:
         _mse._check("fp8_block_matmul", st)
     return out
@@ -194,16 +215,19 @@ def fp8_block_linear(x, wq, ws, y_dtype=None, y=None, workspace=None, stream=Non
     """y [T, N] = x wq^T: x [T, K] bf16 is rounded to e4m3 in blocks of 1 x 128, wq and ws as in fp8_block_matmul."""
     if torch is None:
         _load()
-    ldx, ldw = _rows(x, "x", (_BF16,), 2), _rows(wq, "wq", _E4M3, 2)
+    device = _device(x, "x")
+    ldx, ldw = _rows(x, "x", (_BF16,), 2, device), _rows(wq, "wq", _E4M3, 2, device)
     (T, K), (N, Kw) = x.shape, wq.shape
     if K != Kw:
         raise ValueError(f"x and wq differ in K: {K} and {Kw}")
-    _dense(ws, "ws", _F32, (_blocks(N), _blocks(K)))
+    _dense(ws, "ws", _F32, (_blocks(N), _blocks(K)), device)
     y, code = _out(y, y_dtype, "y", (T, N), x, stream)
     if workspace is None:
         workspace = _own_stream(new_fp8_linear_workspace(T, N, K, x.device), stream)
+    else:
+        _taken(workspace, device)
     st = _call_linear(x.data_ptr(), ldx, wq.data_ptr(), ldw, ws.data_ptr(), T, N, K, y.data_ptr(), code, T * N,
-                             workspace.data_ptr(), workspace.nbytes, _handle(stream, x))
+                             workspace.data_ptr(), workspace.nbytes, _handle(stream, device))
     if st:
         _mse._check("fp8_block_linear", st)
     return y
@@ -232,31 +256,34 @@ def moe_experts_forward(x, ids, weights, w_gate_up, s_gate_up, w_down, s_down, f
     experts, and ids of -1, add nothing."""
     if torch is None:
         _load()
-    ld_gu, ld_dn = _rows(w_gate_up, "w_gate_up", _E4M3, 3), _rows(w_down, "w_down", _E4M3, 3)
+    device = _device(x, "x")
+    ld_gu, ld_dn = _rows(w_gate_up, "w_gate_up", _E4M3, 3, device), _rows(w_down, "w_down", _E4M3, 3, device)
     E, H, I = w_down.shape
     if w_gate_up.shape != (E, 2 * I, H):
         raise ValueError(f"w_gate_up {tuple(w_gate_up.shape)} does not fit w_down {tuple(w_down.shape)}")
-    if x is None or ids is None or x.dim() != 2 or ids.dim() != 2:
+    if ids is None or x.dim() != 2 or ids.dim() != 2:
         raise ValueError(f"x and ids: need 2-d tensors, got {_said(x)} and {_said(ids)}")
     T, k = ids.shape
     hb, ib = _blocks(H), _blocks(I)
-    _dense(x, "x", _BF16, (T, H))
-    _dense(ids, "ids", torch.int32, (T, k))
-    _dense(weights, "weights", _F32, (T, k))
-    _dense(s_gate_up, "s_gate_up", _F32, (E, 2 * ib, hb))
-    _dense(s_down, "s_down", _F32, (E, hb, ib))
+    _dense(x, "x", _BF16, (T, H), device)
+    _dense(ids, "ids", torch.int32, (T, k), device)
+    _dense(weights, "weights", _F32, (T, k), device)
+    _dense(s_gate_up, "s_gate_up", _F32, (E, 2 * ib, hb), device)
+    _dense(s_down, "s_down", _F32, (E, hb, ib), device)
     if shared is not None:
-        _dense(shared, "shared", _BF16, (T, H))
+        _dense(shared, "shared", _BF16, (T, H), device)
     if y is None:
         y = _empty(stream, (T, H), _BF16, x.device)
     else:
-        _dense(y, "y", _BF16, (T, H))
+        _dense(y, "y", _BF16, (T, H), device)
     if workspace is None:
         workspace = _own_stream(new_moe_workspace(T, k, E, H, I, x.device), stream)
+    else:
+        _taken(workspace, device)
     st = _call_experts(x.data_ptr(), T, H, ids.data_ptr(), weights.data_ptr(), k, w_gate_up.data_ptr(), ld_gu,
                                 s_gate_up.data_ptr(), w_down.data_ptr(), ld_dn, s_down.data_ptr(), E, I, first_expert,
                                 None if shared is None else shared.data_ptr(), y.data_ptr(), T * H,
-                                workspace.data_ptr(), workspace.nbytes, _handle(stream, x))
+                                workspace.data_ptr(), workspace.nbytes, _handle(stream, device))
     if st:
         _mse._check("moe_experts_forward", st)
     return y

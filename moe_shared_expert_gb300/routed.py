@@ -93,15 +93,19 @@ def _handle(stream, device):
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
-def _own_stream(t, stream):
-    """Memory allocated here for a call on another stream than the current one stays taken until that call is done."""
-    if stream is not None:
-        t.record_stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
-    return t
-
-
 def _empty(stream, shape, dtype, device):
-    return _own_stream(torch.empty(shape, dtype=dtype, device=device), stream)
+    """New memory for a call on `stream`.
+
+    Another stream than the current one fills its own blocks: one that the current stream has let go may still be in
+    use by its kernels.  And what the caller drops is not taken again before the current stream, too, is done with it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if isinstance(stream, int):   # (0 is the default stream's handle, and would make a new stream)
+        stream = torch.cuda.ExternalStream(stream, device=device) if stream else torch.cuda.default_stream(device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream(device))
+    return t
 
 
 # ---------------------------------------------------------------------------------------
@@ -223,7 +227,7 @@ def fp8_block_linear(x, wq, ws, y_dtype=None, y=None, workspace=None, stream=Non
     _dense(ws, "ws", _F32, (_blocks(N), _blocks(K)), device)
     y, code = _out(y, y_dtype, "y", (T, N), x, stream)
     if workspace is None:
-        workspace = _own_stream(new_fp8_linear_workspace(T, N, K, x.device), stream)
+        workspace = _empty(stream, max(fp8_linear_workspace_bytes(T, N, K), 256), torch.uint8, x.device)
     else:
         _taken(workspace, device)
     st = _call_linear(x.data_ptr(), ldx, wq.data_ptr(), ldw, ws.data_ptr(), T, N, K, y.data_ptr(), code, T * N,
@@ -277,7 +281,7 @@ def moe_experts_forward(x, ids, weights, w_gate_up, s_gate_up, w_down, s_down, f
     else:
         _dense(y, "y", _BF16, (T, H), device)
     if workspace is None:
-        workspace = _own_stream(new_moe_workspace(T, k, E, H, I, x.device), stream)
+        workspace = _empty(stream, max(moe_workspace_bytes(T, k, E, H, I), 256), torch.uint8, x.device)
     else:
         _taken(workspace, device)
     st = _call_experts(x.data_ptr(), T, H, ids.data_ptr(), weights.data_ptr(), k, w_gate_up.data_ptr(), ld_gu,

@@ -102,3 +102,83 @@ def test_a_workspace_with_holes_is_refused(calls, op):
         with pytest.raises(ValueError, match="workspace"):
             f(**{**a, "workspace": On(wrong, 0)})
     assert calls == []
+
+
+class FakeCuda:
+    """torch.cuda of one device: streams, and which of them is current."""
+
+    class Stream:
+        def __init__(self, handle):
+            self.cuda_stream = handle
+
+    def __init__(self):
+        self.now = self.Stream(0)
+        self.default = self.now
+
+    def current_stream(self, device=None):
+        return self.now
+
+    def default_stream(self, device=None):
+        return self.default
+
+    def ExternalStream(self, handle, device=None):
+        assert handle != 0, "a handle of 0 makes a new stream"
+        return self.Stream(handle)
+
+    def stream(self, s):
+        import contextlib
+
+        @contextlib.contextmanager
+        def entered():
+            before, self.now = self.now, s
+            yield
+            self.now = before
+        return entered()
+
+
+@pytest.fixture
+def made(monkeypatch):
+    """(tensors, cuda): what the bindings allocate, with the stream that was current and the streams it was recorded on."""
+    routed._load()
+    cuda, tensors = FakeCuda(), []
+
+    class Made:
+        def __init__(self, shape):
+            self.shape, self.allocated_on, self.recorded = shape, cuda.now.cuda_stream, []
+            tensors.append(self)
+
+        def record_stream(self, s):
+            self.recorded.append(s.cuda_stream)
+
+    class Torch:
+        uint8 = torch.uint8
+        empty = staticmethod(lambda shape, dtype=None, device=None: Made(shape))
+
+    Torch.cuda = cuda
+    monkeypatch.setattr(routed, "torch", Torch)
+    return tensors, cuda
+
+
+@pytest.mark.parametrize("as_handle", [False, True])
+def test_memory_for_another_stream_is_that_streams(made, as_handle):
+    # a block that the current stream has let go may still be read and written by its kernels: what another stream
+    # fills comes from that stream's own blocks, and is not taken again before the current stream, too, is done with it
+    tensors, cuda = made
+    side = 77 if as_handle else cuda.Stream(77)
+    routed._empty(side, (3, 4), torch.bfloat16, "cuda:0")
+    assert tensors[-1].allocated_on == 77 and tensors[-1].recorded == [0] and cuda.now.cuda_stream == 0
+    cuda.now = cuda.Stream(5)
+    routed._empty(0 if as_handle else cuda.default, (3, 4), torch.bfloat16, "cuda:0")
+    assert tensors[-1].allocated_on == 0 and tensors[-1].recorded == [5]
+    routed._empty(None, (3, 4), torch.bfloat16, "cuda:0")
+    assert tensors[-1].allocated_on == 5 and tensors[-1].recorded == []
+
+
+@pytest.mark.parametrize("op", ["linear", "experts"])
+def test_a_workspace_for_another_stream_is_that_streams(calls, monkeypatch, op):
+    asked = []
+    monkeypatch.setattr(routed, "_empty", lambda stream, shape, dtype, device: asked.append((stream, shape, dtype)) or On(e4m3(shape), 0))
+    f, a = arguments(op)
+    f(**{**a, "workspace": None}, stream=77)
+    need = mse.fp8_linear_workspace_bytes(3, 5, 64) if op == "linear" else mse.moe_workspace_bytes(3, 2, 4, 64, 16)
+    assert asked == [(77, need, torch.uint8)] and calls == [op]

@@ -12,16 +12,17 @@ namespace {
 // rounding to 8 bits
 // ---------------------------------------------------------------------------
 
-// eight bf16 values at `src`, a multiple of `align` bytes, of which `left` are there (fewer than one: none; the others 0)
+// eight bf16 values at `src`, a multiple of `align` bytes, of which `left` are there (fewer than one: none; the others 0).  Not by
+// the read-only path: a grid begins while the kernel before it may still write what it reads after its wait.
 __device__ __forceinline__ uint4 load8(const uint16_t *src, int64_t left, int align) {
-    if (left >= 8 && align == 16) return __ldg(reinterpret_cast<const uint4 *>(src));
+    if (left >= 8 && align == 16) return *reinterpret_cast<const uint4 *>(src);
     if (left >= 8 && align == 8) {
-        const uint2 lo = __ldg(reinterpret_cast<const uint2 *>(src)), hi = __ldg(reinterpret_cast<const uint2 *>(src) + 1);
+        const uint2 lo = *reinterpret_cast<const uint2 *>(src), hi = reinterpret_cast<const uint2 *>(src)[1];
         return make_uint4(lo.x, lo.y, hi.x, hi.y);
     }
     if (left >= 8 && align == 4) {
         const uint32_t *w = reinterpret_cast<const uint32_t *>(src);
-        return make_uint4(__ldg(w), __ldg(w + 1), __ldg(w + 2), __ldg(w + 3));
+        return make_uint4(w[0], w[1], w[2], w[3]);
     }
     uint32_t u[4];
 #pragma unroll

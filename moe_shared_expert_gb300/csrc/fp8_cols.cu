@@ -236,15 +236,15 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
                 for (int v = 0; v < 8; ++v) to[v] = 0;
                 if (i >= n || token >= t.rows) return;
                 if (g.x_wide && k + 16 <= g.K) {
-                    const uint4 lo = __ldg(reinterpret_cast<const uint4 *>(x));
-                    const uint4 hi = __ldg(reinterpret_cast<const uint4 *>(x) + 1);
+                    const uint4 lo = *reinterpret_cast<const uint4 *>(x);
+                    const uint4 hi = reinterpret_cast<const uint4 *>(x)[1];
                     to[0] = lo.x; to[1] = lo.y; to[2] = lo.z; to[3] = lo.w;
                     to[4] = hi.x; to[5] = hi.y; to[6] = hi.z; to[7] = hi.w;
                 } else {
 #pragma unroll
                     for (int v = 0; v < 8; ++v) {
-                        const uint32_t a = k + 2 * v < g.K ? __ldg(x + 2 * v) : 0u;
-                        const uint32_t b = k + 2 * v + 1 < g.K ? __ldg(x + 2 * v + 1) : 0u;
+                        const uint32_t a = k + 2 * v < g.K ? x[2 * v] : 0u;
+                        const uint32_t b = k + 2 * v + 1 < g.K ? x[2 * v + 1] : 0u;
                         to[v] = a | (b << 16);
                     }
                 }
@@ -322,7 +322,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
                 }
             }
             if (pt < MATS * kChunk && c0 + pt % kChunk < n)
-                ws_s[pt] = __ldg(ws + (pt / kChunk) * g.up_scales + kb0 + c0 + pt % kChunk);
+                ws_s[pt] = ws[(pt / kChunk) * g.up_scales + kb0 + c0 + pt % kChunk];
             named_barrier_sync(1, kPromo);
             for (int k = C::BY_K ? group : 0; k < kChunk && c0 + k < n; k += C::BY_K ? 2 : 1) {   // kChunk is even
                 const int i = c0 + k, b = i % C::NBUF;

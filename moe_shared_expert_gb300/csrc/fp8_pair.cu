@@ -211,13 +211,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (id >= total) return;
             place(id, next.t, next.n);
             const bool have = row < next.t.rows - (int)rank * 128;
-            // factors of one k-block: xs (any valid row where this one is not), ws of the two runs
+            // factors of one k-block: xs (any valid row where this one is not), ws of the two runs (not by the read-only path:
+            // this grid began while the kernel before it wrote xs)
             next.xs = g.xs + ((int64_t)next.t.row0 + (have ? (int)rank * 128 + row : 0)) * g.kb;
             const int blk = GLU ? next.n : min(2 * next.n + share * 2 * kRun / 128, (int)((g.N + kBlock - 1) / kBlock) - 1);
             next.ws = g.ws + (int64_t)next.t.expert * g.ws_group + (int64_t)blk * g.kb;
-            next.xa = __ldg(next.xs + kb0);
-            next.ga = __ldg(next.ws + kb0);
-            next.ua = GLU ? __ldg(next.ws + g.up_scales + kb0) : 0.f;
+            next.xa = next.xs[kb0];
+            next.ga = next.ws[kb0];
+            next.ua = GLU ? next.ws[g.up_scales + kb0] : 0.f;
         };
         open(cluster);
         for (int64_t id = cluster; id < total; id += n_clusters) {
@@ -235,9 +236,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int kb = kb0; kb < kb1; ++kb, ++use) {
                 const float f0 = xa * ga, f1 = GLU ? xa * ua : f0;
                 if (kb + 1 < kb1) {
-                    xa = __ldg(xs + kb + 1);
-                    ga = __ldg(ws + kb + 1);
-                    if (GLU) ua = __ldg(ws + g.up_scales + kb + 1);
+                    xa = xs[kb + 1];
+                    ga = ws[kb + 1];
+                    if (GLU) ua = ws[g.up_scales + kb + 1];
                 }
                 const uint32_t b = use & 1u;
                 ok = warp_wait(smem_u32(&ctl->tfull[b]), (use >> 1) & 1u, abort_flag, g);

@@ -26,8 +26,8 @@ constexpr float kLowest = -3.4028234663852886e38f;   // of fp32: a bias may brin
 
 template <bool BF16>
 __device__ __forceinline__ float load_logit(const RouteParams &p, int64_t i) {
-    return BF16 ? bf16_bits_to_f32(__ldg(static_cast<const uint16_t *>(p.logits) + i))
-                : __ldg(static_cast<const float *>(p.logits) + i);
+    return BF16 ? bf16_bits_to_f32(static_cast<const uint16_t *>(p.logits)[i])
+                : static_cast<const float *>(p.logits)[i];
 }
 
 __device__ __forceinline__ float warp_fmax(float v) {
@@ -120,7 +120,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32, VPL <= 8 ? 5 : VPL <= 16 ? 4
     constexpr bool KEEP = VPL <= 12;
     float bias[KEEP ? VPL : 1] = {};
     int shift[KEEP && GROUPS ? VPL : 1] = {};   // g * lanes of the expert's group g: its bit among the kept ones
-    auto load_bias = [&](int i) { return p.bias && i * 32 + lane < p.E ? __ldg(p.bias + i * 32 + lane) : 0.f; };
+    auto load_bias = [&](int i) { return p.bias && i * 32 + lane < p.E ? p.bias[i * 32 + lane] : 0.f; };
     auto find_shift = [&](int i) { return (int)((uint32_t)(i * 32 + lane) * (uint32_t)p.group_magic >> 20) * lanes; };
     if constexpr (KEEP) {
 #pragma unroll
@@ -237,7 +237,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32, VPL <= 8 ? 5 : VPL <= 16 ? 4
             if (lane < n) {
                 e = cand_id[lane];
                 sc = GROUPS ? all_scores[e] : score_of(load_logit<BF16>(p, t * p.ld + e));
-                c = p.bias ? __fadd_rn(sc, __ldg(p.bias + e)) : sc;
+                c = p.bias ? __fadd_rn(sc, p.bias[e]) : sc;
                 cand_choice[lane] = c;
             }
             __syncwarp();
@@ -264,7 +264,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32, VPL <= 8 ? 5 : VPL <= 16 ? 4
                     const int x = i * 32 + lane;
                     float c = -INFINITY;
                     if (open >> i & 1u)
-                        c = __fadd_rn(score_of(load_logit<BF16>(p, t * p.ld + x)), p.bias ? __ldg(p.bias + x) : 0.f);
+                        c = __fadd_rn(score_of(load_logit<BF16>(p, t * p.ld + x)), p.bias ? p.bias[x] : 0.f);
 #pragma unroll
                     for (int u = 0; u < VPL; ++u)
                         if (u == i) v[u] = c;

@@ -1,0 +1,37 @@
+"""Calls in turn on one workspace, without a pause between them: each reads what its own kernels wrote."""
+import pytest
+
+from tests.test_gpu_routed import gen
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+mse = pytest.importorskip("moe_shared_expert_gb300")
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    from moe_shared_expert_gb300 import _build
+    _build.build()
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    mse.lib()
+    yield
+    torch.cuda.synchronize()
+    assert mse.poll_device_error() == 0
+
+
+@pytest.mark.parametrize("T,N,K", [(3, 500, 900), (64, 3000, 2000), (300, 4000, 5000), (1500, 2560, 512)])
+def test_linear_calls_in_turn(T, N, K):
+    wq, ws = mse.fp8_block_quantise(torch.randn(N, K, generator=gen(N)).to(torch.bfloat16).cuda(), block_rows=128)
+    # tokens whose scales differ by powers of two from call to call: a stale scale or value is far off
+    xs = [(torch.randn(T, K, generator=gen(i)) * 4.0 ** (i - 3)).to(torch.bfloat16).cuda() for i in range(6)]
+    want = [mse.fp8_block_linear(x, wq, ws) for x in xs]
+    torch.cuda.synchronize()
+    buf = mse.new_fp8_linear_workspace(T, N, K)
+    for _ in range(5):
+        got = [torch.empty_like(y) for y in want]
+        torch.cuda.synchronize()
+        for x, y in zip(xs, got):
+            mse.fp8_block_linear(x, wq, ws, y=y, workspace=buf)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))

@@ -156,7 +156,9 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
     // table is not, until the wait is over.  A call's last kernel lets nothing start early: its outputs may be
     // anything to the next one.)
     if (g.tiles && !g.ids) pdl_launch_dependents();
-    if (g.ids && !active) pdl_wait();
+    // A grid without a tile (slot 0 has none) waits too: it would else be over before the kernel before it, and the next call
+    // would write the tile table under that one's eyes.  With tiles, the CTAs that have one wait for all.
+    if (!active && (g.ids || (g.weights_early && blockIdx.y == 0))) pdl_wait();
 
     const int w_row = active ? (int)(t.expert * g.w_group_rows) + m * kBlock : 0;
     int issued = 0;

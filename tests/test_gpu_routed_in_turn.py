@@ -1,7 +1,7 @@
 """Calls in turn on one workspace, without a pause between them: each reads what its own kernels wrote."""
 import pytest
 
-from tests.test_gpu_routed import gen
+from tests.test_gpu_routed import gen, make_experts
 
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
@@ -34,4 +34,24 @@ def test_linear_calls_in_turn(T, N, K):
         torch.cuda.synchronize()
         for x, y in zip(xs, got):
             mse.fp8_block_linear(x, wq, ws, y=y, workspace=buf)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("T", [1, 9, 90, 900])
+def test_experts_calls_in_turn_with_and_without_pairs(T):
+    # calls of which the rank holds no pair between others on the same workspace
+    E, H, I, k = 5, 640, 256, 3
+    weights = make_experts(E, H, I, 9)
+    x = [(torch.randn(T, H, generator=gen(i)) * 4.0 ** (i % 3 - 1)).to(torch.bfloat16).cuda() for i in range(6)]
+    ids = [(torch.randint(0, E, (T, k), generator=gen(10 + i)) if i % 2 else torch.full((T, k), 77)).to(torch.int32).cuda()
+           for i in range(6)]
+    w = torch.rand(T, k, generator=gen(20)).cuda()
+    want = [mse.moe_experts_forward(a, i, w, *weights) for a, i in zip(x, ids)]
+    assert all(want[i].any() == (i % 2 == 1) for i in range(6))
+    buf = mse.new_moe_workspace(T, k, E, H, I)
+    for _ in range(5):
+        got = [torch.empty_like(y) for y in want]
+        torch.cuda.synchronize()
+        for a, i, y in zip(x, ids, got):
+            mse.moe_experts_forward(a, i, w, *weights, y=y, workspace=buf)
         assert all(torch.equal(a, b) for a, b in zip(got, want))

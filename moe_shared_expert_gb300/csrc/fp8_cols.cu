@@ -528,15 +528,14 @@ cudaError_t run(const CUtensorMap &tw, const CUtensorMap &tx, const BlockGemm &g
 template <int EPI>
 cudaError_t run_bn(const CUtensorMap &tw, const CUtensorMap &tx, const BlockGemm &g, int parts, int slots,
                    int row_tiles, int stream_weights, bool whole, bool pdl, cudaStream_t s) {
-    switch (g.tile_rows) {
-        case 16:
-            if constexpr (EPI != BLOCK_SWIGLU)
-                if (g.x)
-                    return run<Cols<16, EPI, true>>(tw, tx, g, parts, slots, row_tiles, stream_weights, whole, pdl, s);
-            return run<Cols<16, EPI>>(tw, tx, g, parts, slots, row_tiles, stream_weights, whole, pdl, s);
-        case 32: return run<Cols<32, EPI>>(tw, tx, g, parts, slots, row_tiles, stream_weights, whole, pdl, s);
-        default: return run<Cols<EPI == BLOCK_SWIGLU ? 32 : 64, EPI>>(tw, tx, g, parts, slots, row_tiles, stream_weights, whole, pdl, s);
+    auto with = [&](auto c) {
+        return run<decltype(c)>(tw, tx, g, parts, slots, row_tiles, stream_weights, whole, pdl, s);
+    };
+    if constexpr (EPI != BLOCK_SWIGLU) {
+        if (g.tile_rows == 64) return with(Cols<64, EPI>());
+        if (g.x) return with(Cols<16, EPI, true>());
     }
+    return g.tile_rows == 16 ? with(Cols<16, EPI>()) : with(Cols<32, EPI>());
 }
 
 }  // namespace

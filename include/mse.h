@@ -603,6 +603,18 @@ MSE_API mse_status moe_experts_forward(const mse_bf16 *x, int64_t T, int64_t H, 
                                        const mse_bf16 *shared, mse_bf16 *y, int64_t y_capacity, void *workspace,
                                        size_t workspace_bytes, void *stream);
 
+/* The kernels that fp8_block_matmul and fp8_block_linear would launch for operands with 16-byte rows, on the current
+ * device.  out[4] (host memory, written): [0] token rows of a tile, 16, 32 or 64 (weights on the MMA's 128-row side) or 256
+ * (CTA pairs), 0 when the generic kernels are forced (then [1..3] are 0); [1] CTAs, or pairs, that share a tile's
+ * k-blocks; [2] CTAs; [3] 1 when fp8_block_linear rounds its tokens inside the product's kernel.
+ * MSE_ERR_INVALID_ARG as the calls; MSE_ERR_UNSUPPORTED_DEVICE without a device. */
+MSE_API mse_status mse_fp8_launch_plan(int64_t T, int64_t N, int64_t K, int32_t *out);
+
+/* The same for moe_experts_forward: out[8]: [0] token rows of a tile, 16, 32 or 256 (0: generic kernels, then [1..5] are
+ * 0); [1] / [2] gate_up's CTAs to a tile's k-blocks and CTAs; [3] / [4] down's; [5] 1 when gate_up finds its tiles in the
+ * ids; [6] 1 when the ids are counted by kernels of their own; [7] 0. */
+MSE_API mse_status mse_moe_launch_plan(int64_t T, int top_k, int64_t E, int64_t H, int64_t I, int32_t *out);
+
 /* Human-readable name of a status code (static string). */
 MSE_API const char *mse_status_string(mse_status s);
 

@@ -30,6 +30,7 @@ __all__ = [
     "PREFILL_AUTO", "PREFILL_SINGLE", "PREFILL_PAIR", "STATUS",
     "moe_route", "fp8_block_quantise", "fp8_block_matmul", "fp8_block_linear", "moe_experts_forward",
     "fp8_linear_workspace_bytes", "new_fp8_linear_workspace", "moe_workspace_bytes", "new_moe_workspace",
+    "fp8_launch_plan", "moe_launch_plan",
 ]
 
 BF16, F32 = 0, 1
@@ -104,6 +105,8 @@ def lib() -> ctypes.CDLL:
                 "moe_experts_workspace_bytes": (sz, [i64, ci, i64, i64, i64]),
                 "moe_experts_forward": (ci, [P, i64, i64, P, P, ci, P, i64, P, P, i64, P, i64, i64, i64, P, P, i64,
                                              P, sz, P]),
+                "mse_fp8_launch_plan": (ci, [i64, i64, i64, P]),
+                "mse_moe_launch_plan": (ci, [i64, ci, i64, i64, i64, P]),
                 "mse_status_string": (ctypes.c_char_p, [ci]),
                 "mse_version": (ctypes.c_char_p, []),
             }
@@ -428,5 +431,5 @@ def set_phase_events(ev_begin=None, ev_mid=None, ev_end=None) -> None:
 
 
 from .routed import (  # noqa: E402  (needs the names above)
-    fp8_block_linear, fp8_block_matmul, fp8_block_quantise, fp8_linear_workspace_bytes, moe_experts_forward,
-    moe_route, moe_workspace_bytes, new_fp8_linear_workspace, new_moe_workspace)
+    fp8_block_linear, fp8_block_matmul, fp8_block_quantise, fp8_launch_plan, fp8_linear_workspace_bytes,
+    moe_experts_forward, moe_launch_plan, moe_route, moe_workspace_bytes, new_fp8_linear_workspace, new_moe_workspace)

@@ -562,6 +562,18 @@ int cols_parts(int64_t tiles, int kb, int tile_rows, int epi, int sm_count) {
     return parts < 4 && tile_rows == 16 && !glu ? 1 : parts;
 }
 
+namespace {
+int64_t cols_slots(const BlockGemm &g) { return g.tiles ? g.max_tiles : (g.T + g.tile_rows - 1) / g.tile_rows; }
+int64_t cols_expected(const BlockGemm &g) {   // tiles of the whole grid, as far as the host can tell
+    return blocks_of(g.N) * (g.tiles ? std::min<int64_t>(cols_slots(g), g.expected_tiles) : cols_slots(g));
+}
+}  // namespace
+
+Split cols_split(const BlockGemm &g, int sm_count) {
+    const int parts = cols_parts(cols_expected(g), g.kb, g.tile_rows, g.epi, sm_count);
+    return {parts * cols_slots(g) * blocks_of(g.N), parts};
+}
+
 mse_status launch_block_cols(const BlockGemm &g, int sm_count, bool pdl, cudaStream_t s) {
     CUtensorMap tw, tx;
     mse_status st = map_bytes(&tw, g.wq, g.groups * g.w_group_rows, g.K, g.ldw, kBlock);
@@ -570,15 +582,12 @@ mse_status launch_block_cols(const BlockGemm &g, int sm_count, bool pdl, cudaStr
         tx = tw;   // the kernel rounds x itself
     else if ((st = map_bytes(&tx, g.xq, g.T, g.K, g.ldx, g.tile_rows)) != MSE_OK)
         return st;
-    const int64_t row_tiles = blocks_of(g.N);
-    const int64_t slots = g.tiles ? g.max_tiles : (g.T + g.tile_rows - 1) / g.tile_rows;
-    const int64_t expected = g.tiles ? std::min<int64_t>(slots, g.expected_tiles) : slots;
+    const int64_t row_tiles = blocks_of(g.N), slots = cols_slots(g);
     if (row_tiles > 65535 || slots > 65535) return MSE_ERR_UNSUPPORTED_SHAPE;
-    const int64_t tiles = row_tiles * expected;
-    const int parts = cols_parts(tiles, g.kb, g.tile_rows, g.epi, sm_count);
+    const int parts = cols_split(g, sm_count).parts;
     const int stream_weights = g.tiles ? g.T <= (int64_t)g.tile_rows * g.groups : slots == 1;
     // one CTA per SM: its ring gets all of it (not in clusters, of which fewer would fit)
-    const bool whole = parts == 1 && tiles <= sm_count;
+    const bool whole = parts == 1 && cols_expected(g) <= sm_count;
     cudaError_t e;
     switch (g.epi) {
         case BLOCK_BF16: e = run_bn<BLOCK_BF16>(tw, tx, g, parts, (int)slots, (int)row_tiles, stream_weights, whole, pdl, s); break;

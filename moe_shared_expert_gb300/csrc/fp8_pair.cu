@@ -515,6 +515,19 @@ int pair_parts(int64_t tiles, int kb) {
     return 1;
 }
 
+namespace {
+int pair_columns(const BlockGemm &g) {   // tiles of weight rows
+    const int width = g.epi == BLOCK_SWIGLU ? 128 : 256;
+    return (int)((g.N + width - 1) / width);
+}
+}  // namespace
+
+Split pair_split(const BlockGemm &g, int sm_count) {
+    const int64_t tiles = (g.tiles ? g.max_tiles : (g.T + 255) / 256) * pair_columns(g);
+    const int parts = g.tiles ? 1 : pair_parts(tiles, g.kb);
+    return {2 * parts * std::min<int64_t>(parts > 1 ? tiles : sm_count / 2, tiles), parts};
+}
+
 mse_status launch_block_pair(const BlockGemm &g, int sm_count, bool pdl, cudaStream_t s) {
     CUtensorMap tw, tx;
     mse_status st = map_bytes(&tw, g.wq, g.groups * g.w_group_rows, g.K, g.ldw, 128);
@@ -525,10 +538,9 @@ mse_status launch_block_pair(const BlockGemm &g, int sm_count, bool pdl, cudaStr
     if (g.epi != BLOCK_SWIGLU && ((reinterpret_cast<uintptr_t>(g.out) | (uint64_t)(g.ldo * size)) & 15u) == 0 &&
         (st = map_bytes(&to, g.out, g.T, g.N * size, g.ldo * size, 32)) != MSE_OK)
         return st;
-    const int n_tiles_n = (int)((g.N + (g.epi == BLOCK_SWIGLU ? 127 : 255)) / (g.epi == BLOCK_SWIGLU ? 128 : 256));
-    const int64_t slots = g.tiles ? g.max_tiles : (g.T + 255) / 256, tiles = slots * n_tiles_n;
-    const int parts = g.tiles ? 1 : pair_parts(tiles, g.kb);
-    const int clusters = (int)std::min<int64_t>(parts > 1 ? tiles : sm_count / 2, tiles);
+    const int n_tiles_n = pair_columns(g);
+    const Split split = pair_split(g, sm_count);
+    const int parts = split.parts, clusters = (int)(split.ctas / (2 * parts));
     cudaError_t e;
     switch (g.epi) {
         case BLOCK_BF16: e = run_parts<BLOCK_BF16>(parts, tx, tw, to, g, clusters, n_tiles_n, pdl, s); break;

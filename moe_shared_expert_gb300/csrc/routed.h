@@ -110,12 +110,20 @@ struct BlockGemm {
     uint32_t *err;
 };
 
+// How a product's grid is split: CTAs, and the CTAs (CTA pairs) that share a tile's k-blocks.
+struct Split {
+    int64_t ctas;
+    int parts;
+};
+
 // Tensor-core kernel for token tiles of 16, 32 or (not SWIGLU) 64 rows (weights on the 128-row side).
 mse_status launch_block_cols(const BlockGemm &g, int sm_count, bool pdl, cudaStream_t s);
 int cols_parts(int64_t tiles, int kb, int tile_rows, int epi, int sm_count);
+Split cols_split(const BlockGemm &g, int sm_count);
 // Tensor-core kernel for token tiles of 256 rows (a CTA pair per 256 x 256 tile).
 mse_status launch_block_pair(const BlockGemm &g, int sm_count, bool pdl, cudaStream_t s);
 int pair_parts(int64_t tiles, int kb);
+Split pair_split(const BlockGemm &g, int sm_count);
 
 constexpr int kSimtTileRows = 16;
 cudaError_t launch_block_simt(const BlockGemm &g, bool pdl, cudaStream_t s);

@@ -87,6 +87,11 @@ BlockGemm plain_product(const uint8_t *xq, int64_t ldx, const float *xs, const u
     return g;
 }
 
+// One launch, whose kernel rounds the tokens itself, where the second one costs more than what every CTA
+// spends on all tokens (us of GPU time with one launch and with two, the host's 5.8 and 7.8: 3 x 904 x 966 6.2, 6.6;
+// 1 x 2112 x 7168 8.6, 8.2; 8 x 7168 x 6144 14.0, 13.7; 1 x 12288 x 7168 19.7, 18.2; 16 x 1024 x 4096 8.4, 6.9).
+bool rounds_itself(int64_t T, int64_t N, int64_t K) { return T <= kRoundRows && N * K <= (int64_t)1 << 24; }
+
 bool tc_operands(const void *xq, int64_t ldx, const void *wq, int64_t ldw) {
     return aligned16(xq) && aligned16(wq) && ldx % 16 == 0 && ldw % 16 == 0;
 }
@@ -127,10 +132,45 @@ MoeWs moe_ws(int64_t T, int top_k, int64_t E, int64_t H, int64_t I) {
     return w;
 }
 
+// The experts' two products, but for their operands.
+struct MoeProducts {
+    BlockGemm gate_up, down;
+};
+MoeProducts moe_products(int64_t T, int top_k, int64_t E, int64_t H, int64_t I, int tile_rows) {
+    const int64_t pairs = T * top_k;
+    BlockGemm g;
+    std::memset(&g, 0, sizeof g);
+    g.T = pairs;
+    g.tile_rows = tile_rows;
+    g.max_tiles = (int)std::min<int64_t>(pairs, pairs / tile_rows + std::min<int64_t>(E, pairs));
+    g.expected_tiles = (int)std::min<int64_t>(g.max_tiles, pairs / tile_rows / 2 + std::min<int64_t>(E, pairs));
+    g.groups = (int)E;
+    MoeProducts p = {g, g};
+    BlockGemm &gu = p.gate_up, &dn = p.down;
+    gu.N = I; gu.K = H; gu.kb = (int)blocks_of(H);
+    gu.w_group_rows = 2 * I; gu.up_rows = I;
+    gu.up_scales = blocks_of(I) * blocks_of(H); gu.ws_group = 2 * gu.up_scales;
+    gu.epi = BLOCK_SWIGLU;
+    gu.ldo = I;
+    gu.ldh = pad16(I);
+    gu.hb = (int)blocks_of(I);
+    dn.N = H; dn.K = I; dn.kb = gu.hb;
+    dn.w_group_rows = H;
+    dn.ws_group = blocks_of(H) * blocks_of(I);
+    dn.epi = BLOCK_F32;
+    dn.ldo = pad4(H);
+    return p;
+}
+// a token or a few: gate_up finds its tiles in the ids, and its weights are requested while the tokens are dispatched
+bool tiles_from_ids(int64_t pairs) { return pairs <= 32; }
+
 bool moe_sizes_ok(int64_t T, int top_k, int64_t E, int64_t H, int64_t I) {
     return T > 0 && top_k > 0 && E > 0 && H > 0 && I > 0 && top_k <= MSE_ROUTE_MAX_TOP_K &&
            E <= MSE_ROUTE_MAX_EXPERTS && T * top_k <= kMaxRows && T <= kMaxRows && H <= kMaxInner && I <= kMaxInner;
 }
+
+// weight rows are 32-bit coordinates
+bool moe_coordinates_ok(int64_t E, int64_t H, int64_t I) { return E * 2 * I <= kMaxRows && E * H <= kMaxRows; }
 
 }  // namespace
 
@@ -219,10 +259,7 @@ mse_status fp8_block_linear(const mse_bf16 *x, int64_t ldx, const uint8_t *wq, i
     begin_untracked_call(stream);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     BlockGemm g = plain_product(xq, ldq, xs, wq, ldw, ws, T, N, K, y, y_dtype, d.sm_count);
-    // One launch, whose kernel rounds the tokens itself, where the second one costs more than what every CTA
-    // spends on all tokens (us of GPU time with one launch and with two, the host's 5.8 and 7.8: 3 x 904 x 966 6.2, 6.6;
-    // 1 x 2112 x 7168 8.6, 8.2; 8 x 7168 x 6144 14.0, 13.7; 1 x 12288 x 7168 19.7, 18.2; 16 x 1024 x 4096 8.4, 6.9).
-    if (tensorcore && T <= kRoundRows && N * K <= (int64_t)1 << 24) {
+    if (tensorcore && rounds_itself(T, N, K)) {
         g.x = x;
         g.ldxb = ldx;
         g.x_wide = ldx % 8 == 0 && aligned16(x);
@@ -255,7 +292,7 @@ mse_status moe_experts_forward(const mse_bf16 *x, int64_t T, int64_t H, const in
     if (st != MSE_OK) return st;
     bool tensorcore = false;
     const bool tc_ok = aligned16(w_gate_up) && aligned16(w_down) && ld_gate_up % 16 == 0 && ld_down % 16 == 0 &&
-                       E * 2 * I <= kMaxRows && E * H <= kMaxRows;   // weight rows are 32-bit coordinates
+                       moe_coordinates_ok(E, H, I);
     if ((st = choose_tensorcore(tc_ok, &tensorcore)) != MSE_OK) return st;
     begin_untracked_call(stream);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -281,44 +318,72 @@ mse_status moe_experts_forward(const mse_bf16 *x, int64_t T, int64_t H, const in
     if ((st = from_cuda(launch_dispatch(dp, pdl, s))) != MSE_OK) return st;
 
     float *o = reinterpret_cast<float *>(w + L.o);
-    BlockGemm g;
-    std::memset(&g, 0, sizeof g);
-    g.T = pairs;
-    g.tiles = dp.tiles; g.n_tiles = dp.n_tiles; g.tile_rows = dp.tile_rows;
-    g.max_tiles = (int)std::min<int64_t>(pairs, pairs / dp.tile_rows + std::min<int64_t>(E, pairs));
-    g.expected_tiles = (int)std::min<int64_t>(g.max_tiles, pairs / dp.tile_rows / 2 + std::min<int64_t>(E, pairs));
-    g.groups = (int)E;
-    BlockGemm gu = g;
+    MoeProducts p = moe_products(T, top_k, E, H, I, dp.tile_rows);
+    BlockGemm &gu = p.gate_up, &dn = p.down;
+    gu.tiles = dn.tiles = dp.tiles;
+    gu.n_tiles = dn.n_tiles = dp.n_tiles;
     gu.xq = dp.xq; gu.ldx = dp.ldq; gu.xs = dp.xs;
     gu.wq = w_gate_up; gu.ldw = ld_gate_up; gu.ws = s_gate_up;
-    gu.N = I; gu.K = H; gu.kb = (int)blocks_of(H);
-    gu.w_group_rows = 2 * I; gu.up_rows = I;
-    gu.up_scales = blocks_of(I) * blocks_of(H); gu.ws_group = 2 * gu.up_scales;
-    gu.epi = BLOCK_SWIGLU;
-    gu.out = o; gu.ldo = I;
-    gu.hq = w + L.hq; gu.ldh = pad16(I);
-    gu.hs = reinterpret_cast<float *>(w + L.hs); gu.hb = (int)blocks_of(I);
-    if (tensorcore && pairs <= 32 && pdl) {   // a token or a few: their weights are requested while they are dispatched
+    gu.out = o;
+    gu.hq = w + L.hq;
+    gu.hs = reinterpret_cast<float *>(w + L.hs);
+    if (tensorcore && tiles_from_ids(pairs) && pdl) {
         gu.ids = ids;
         gu.pairs = (int)pairs;
         gu.first_expert = first_expert;
         gu.weights_early = 1;
     }
     if ((st = run_product(gu, tensorcore, d, s)) != MSE_OK) return st;
-    if (!tensorcore && (st = from_cuda(launch_quantise_f32(o, dp.n_tiles, dp.tiles, g.max_tiles, I, gu.hq, gu.ldh, gu.hs, pdl, s))) !=
+    if (!tensorcore && (st = from_cuda(launch_quantise_f32(o, dp.n_tiles, dp.tiles, gu.max_tiles, I, gu.hq, gu.ldh, gu.hs, pdl, s))) !=
         MSE_OK)
         return st;
-    BlockGemm dn = g;
     dn.xq = gu.hq; dn.ldx = gu.ldh; dn.xs = gu.hs;
     dn.wq = w_down; dn.ldw = ld_down; dn.ws = s_down;
-    dn.N = H; dn.K = I; dn.kb = gu.hb;
-    dn.w_group_rows = H;
-    dn.ws_group = blocks_of(H) * blocks_of(I);
-    dn.epi = BLOCK_F32;
-    dn.out = o; dn.ldo = pad4(H);
+    dn.out = o;
     dn.weights_early = 1;   // (and the tiles: the gate_up launch lets this one start after its own wait)
     if ((st = run_product(dn, tensorcore, d, s)) != MSE_OK) return st;
     return from_cuda(launch_combine(o, dn.ldo, dp.pos, weights, top_k, shared, y, T, H, d.sm_count, pdl, s));
+}
+
+mse_status mse_fp8_launch_plan(int64_t T, int64_t N, int64_t K, int32_t *out) {
+    if (!out || T <= 0 || N <= 0 || K <= 0 || T > kMaxRows || N > kMaxInner || K > kMaxInner) return MSE_ERR_INVALID_ARG;
+    for (int i = 0; i < 4; ++i) out[i] = 0;
+    DeviceView d;
+    mse_status st = device_view(&d);
+    if (st != MSE_OK) return st;
+    bool tensorcore = false;
+    if ((st = choose_tensorcore(true, &tensorcore)) != MSE_OK || !tensorcore) return st;
+    const BlockGemm g = plain_product(nullptr, pad16(K), nullptr, nullptr, pad16(K), nullptr, T, N, K, nullptr, MSE_BF16, d.sm_count);
+    const Split split = g.tile_rows == 256 ? pair_split(g, d.sm_count) : cols_split(g, d.sm_count);
+    out[0] = g.tile_rows;
+    out[1] = split.parts;
+    out[2] = (int32_t)std::min<int64_t>(split.ctas, INT32_MAX);
+    out[3] = rounds_itself(T, N, K);
+    return MSE_OK;
+}
+
+mse_status mse_moe_launch_plan(int64_t T, int top_k, int64_t E, int64_t H, int64_t I, int32_t *out) {
+    if (!out || !moe_sizes_ok(T, top_k, E, H, I)) return MSE_ERR_INVALID_ARG;
+    for (int i = 0; i < 8; ++i) out[i] = 0;
+    DeviceView d;
+    mse_status st = device_view(&d);
+    if (st != MSE_OK) return st;
+    bool tensorcore = false;
+    if ((st = choose_tensorcore(moe_coordinates_ok(E, H, I), &tensorcore)) != MSE_OK) return st;
+    out[6] = T * top_k > kCountAllPairs;
+    if (!tensorcore) return MSE_OK;
+    const MoeProducts p = moe_products(T, top_k, E, H, I, expert_tile_rows(T * top_k / E));
+    BlockGemm g[2] = {p.gate_up, p.down};
+    static const Tile some = {};   // a grouped product; its tiles are the call's
+    out[0] = g[0].tile_rows;
+    for (int i = 0; i < 2; ++i) {
+        g[i].tiles = &some;
+        const Split split = out[0] == 256 ? pair_split(g[i], d.sm_count) : cols_split(g[i], d.sm_count);
+        out[1 + 2 * i] = split.parts;
+        out[2 + 2 * i] = (int32_t)std::min<int64_t>(split.ctas, INT32_MAX);
+    }
+    out[5] = tiles_from_ids(T * top_k) && pdl_enabled();
+    return MSE_OK;
 }
 
 }  // extern "C"

@@ -291,3 +291,24 @@ def moe_experts_forward(x, ids, weights, w_gate_up, s_gate_up, w_down, s_down, f
     if st:
         _mse._check("moe_experts_forward", st)
     return y
+
+
+# ---------------------------------------------------------------------------------------
+# what a call would launch
+# ---------------------------------------------------------------------------------------
+
+def _plan(func, keys, *sizes):
+    out = (ctypes.c_int32 * 8)()
+    _mse._check(func, getattr(_mse.lib(), func)(*sizes, out))
+    return dict(zip(keys, map(int, out)))
+
+
+def fp8_launch_plan(T: int, N: int, K: int) -> dict:
+    """Kernel and split of a product on the current device: see mse_fp8_launch_plan in include/mse.h."""
+    return _plan("mse_fp8_launch_plan", ("tile_rows", "parts", "ctas", "one_launch"), T, N, K)
+
+
+def moe_launch_plan(T: int, top_k: int, E: int, H: int, I: int) -> dict:
+    """Kernels and splits of the experts' layer on the current device: see mse_moe_launch_plan in include/mse.h."""
+    return _plan("mse_moe_launch_plan", ("tile_rows", "gate_up_parts", "gate_up_ctas", "down_parts", "down_ctas",
+                                         "tiles_from_ids", "counted_apart"), T, top_k, E, H, I)

@@ -30,3 +30,14 @@ def test_products_refuse_sizes_beyond_their_limits(L, kw):
     a.update(kw)
     assert L.fp8_block_matmul(FAKE, a["ld"], FAKE, FAKE, a["ld"], FAKE, a["T"], a["N"], a["K"], FAKE, mse.F32, MANY, None) == \
         mse.STATUS_CODE["MSE_ERR_INVALID_ARG"]
+
+
+def test_launch_plans_refuse_what_the_calls_refuse(L):
+    import ctypes
+    out = (ctypes.c_int32 * 8)()
+    bad = mse.STATUS_CODE["MSE_ERR_INVALID_ARG"]
+    assert L.mse_fp8_launch_plan(3, 7, 500, None) == bad and L.mse_moe_launch_plan(3, 2, 4, 256, 128, None) == bad
+    for sizes in ((0, 7, 500), (3, 0, 500), (3, 7, -1), ((1 << 30) + 1, 7, 500), (3, (1 << 22) + 1, 500)):
+        assert L.mse_fp8_launch_plan(*sizes, out) == bad, sizes
+    for sizes in ((0, 2, 4, 256, 128), (3, 33, 4, 256, 128), (3, 2, 1025, 256, 128), (3, 2, 4, 0, 128), (1 << 29, 3, 4, 256, 128)):
+        assert L.mse_moe_launch_plan(*sizes, out) == bad, sizes

@@ -52,27 +52,20 @@ def _said(t):
     return "None" if t is None else f"{t.dtype} {tuple(t.shape)}, strides {t.stride()}, on {t.device}"
 
 
-def _device(t, name):
-    """The index of t's GPU, which has to be the current one: the library launches there."""
+def _rows(t, name, dtypes, ndim, device=None):
+    """(pitch of the rows, shape, index of the GPU) of a tensor whose last dimension is contiguous and whose matrices follow
+    one another.  It is on `device`; a call's first operand, without one, on the current device: the library launches there."""
     index = -1 if t is None else t.get_device()
-    if index < 0:
-        raise ValueError(f"{name}: need a CUDA tensor, got {_said(t)}")
-    current = _current()
-    if index != current:
-        raise ValueError(f"{name}: on cuda:{index}, and the current device is cuda:{current}")
-    return index
-
-
-def _rows(t, name, dtypes, ndim, device):
-    """The pitch of the rows of a tensor on `device` whose last dimension is contiguous and whose matrices follow one another."""
-    if t is None or t.get_device() != device or t.dtype not in dtypes or t.dim() != ndim:
-        raise ValueError(f"{name}: need a {ndim}-d tensor of {dtypes} on cuda:{device}, got {_said(t)}")
+    if index < 0 or t.dtype not in dtypes or t.dim() != ndim:
+        raise ValueError(f"{name}: need a {ndim}-d CUDA tensor of {dtypes}, got {_said(t)}")
+    if index != (_current() if device is None else device):
+        raise ValueError(f"{name}: on cuda:{index}, and not on the call's device, cuda:{_current() if device is None else device}")
     shape, stride = t.shape, t.stride()
     cols = shape[-1]
     ld = stride[-2] if shape[-2] > 1 else max(cols, stride[-2])
     if (cols > 1 and stride[-1] != 1) or ld < cols or (ndim == 3 and shape[0] > 1 and stride[0] != shape[1] * ld):
         raise ValueError(f"{name}: contiguous rows of one pitch are needed, got {_said(t)}")
-    return ld
+    return ld, shape, index
 
 
 def _dense(t, name, dtype, shape, device):
@@ -120,9 +113,7 @@ def moe_route(logits, top_k, scoring="sigmoid", bias=None, n_group=1, topk_group
     close an expert.  Slots for which no expert is left hold id -1 and weight 0."""
     if torch is None:
         _load()
-    device = _device(logits, "logits")
-    ld = _rows(logits, "logits", (_BF16, _F32), 2, device)
-    T, E = logits.shape
+    ld, (T, E), device = _rows(logits, "logits", (_BF16, _F32), 2)
     if scoring not in _SCORING:
         raise ValueError(f"scoring must be one of {sorted(_SCORING)}, got {scoring!r}")
     if bias is not None:
@@ -156,9 +147,7 @@ def fp8_block_quantise(x, block_rows=1, stream=None):
         _load()
     if x is None or x.dim() not in (2, 3):
         raise ValueError(f"x: need a 2-d or 3-d tensor, got {_said(x)}")
-    device = _device(x, "x")
-    ld = _rows(x, "x", (_BF16,), x.dim(), device)
-    *lead, rows, K = x.shape
+    ld, (*lead, rows, K), device = _rows(x, "x", (_BF16,), x.dim())
     pitch, srows, kb = _pad16(K), rows if block_rows == 1 else _blocks(rows), _blocks(K)
     q = _empty(stream, (*lead, rows, pitch), torch.uint8, x.device)
     scales = _empty(stream, (*lead, srows, kb), _F32, x.device)
@@ -185,9 +174,8 @@ def fp8_block_matmul(xq, xs, wq, ws, out_dtype=None, out=None, stream=None):
     """out [T, N] = xq wq^T with block scales; xq [T, K], xs [T, K / 128], wq [N, K], ws [N / 128, K / 128]."""
     if torch is None:
         _load()
-    device = _device(xq, "xq")
-    ldx, ldw = _rows(xq, "xq", _E4M3, 2, device), _rows(wq, "wq", _E4M3, 2, device)
-    (T, K), (N, Kw) = xq.shape, wq.shape
+    ldx, (T, K), device = _rows(xq, "xq", _E4M3, 2)
+    ldw, (N, Kw), _ = _rows(wq, "wq", _E4M3, 2, device)
     if K != Kw:
         raise ValueError(f"xq and wq differ in K: {K} and {Kw}")
     _dense(xs, "xs", _F32, (T, _blocks(K)), device)
@@ -219,9 +207,8 @@ def fp8_block_linear(x, wq, ws, y_dtype=None, y=None, workspace=None, stream=Non
     """y [T, N] = x wq^T: x [T, K] bf16 is rounded to e4m3 in blocks of 1 x 128, wq and ws as in fp8_block_matmul."""
     if torch is None:
         _load()
-    device = _device(x, "x")
-    ldx, ldw = _rows(x, "x", (_BF16,), 2, device), _rows(wq, "wq", _E4M3, 2, device)
-    (T, K), (N, Kw) = x.shape, wq.shape
+    ldx, (T, K), device = _rows(x, "x", (_BF16,), 2)
+    ldw, (N, Kw), _ = _rows(wq, "wq", _E4M3, 2, device)
     if K != Kw:
         raise ValueError(f"x and wq differ in K: {K} and {Kw}")
     _dense(ws, "ws", _F32, (_blocks(N), _blocks(K)), device)
@@ -260,12 +247,11 @@ def moe_experts_forward(x, ids, weights, w_gate_up, s_gate_up, w_down, s_down, f
     experts, and ids of -1, add nothing."""
     if torch is None:
         _load()
-    device = _device(x, "x")
-    ld_gu, ld_dn = _rows(w_gate_up, "w_gate_up", _E4M3, 3, device), _rows(w_down, "w_down", _E4M3, 3, device)
-    E, H, I = w_down.shape
-    if w_gate_up.shape != (E, 2 * I, H):
+    ld_gu, of_gate_up, device = _rows(w_gate_up, "w_gate_up", _E4M3, 3)
+    ld_dn, (E, H, I), _ = _rows(w_down, "w_down", _E4M3, 3, device)
+    if of_gate_up != (E, 2 * I, H):
         raise ValueError(f"w_gate_up {tuple(w_gate_up.shape)} does not fit w_down {tuple(w_down.shape)}")
-    if ids is None or x.dim() != 2 or ids.dim() != 2:
+    if x is None or ids is None or x.dim() != 2 or ids.dim() != 2:
         raise ValueError(f"x and ids: need 2-d tensors, got {_said(x)} and {_said(ids)}")
     T, k = ids.shape
     hb, ib = _blocks(H), _blocks(I)

@@ -568,7 +568,7 @@ MSE_API mse_status fp8_block_matmul(const uint8_t *xq, int64_t ldx, const float 
 MSE_API size_t fp8_block_linear_workspace_bytes(int64_t T, int64_t N, int64_t K);
 
 /* fp8_block_quantise of x [T x K] bf16 (row pitch ldx) in blocks of 1 x 128, then
- * fp8_block_matmul, in one call. */
+ * fp8_block_matmul, in one call.  y may lie over x. */
 MSE_API mse_status fp8_block_linear(const mse_bf16 *x, int64_t ldx, const uint8_t *wq, int64_t ldw, const float *ws,
                                     int64_t T, int64_t N, int64_t K, void *y, mse_dtype y_dtype, int64_t y_capacity,
                                     void *workspace, size_t workspace_bytes, void *stream);
@@ -606,7 +606,7 @@ MSE_API mse_status moe_experts_forward(const mse_bf16 *x, int64_t T, int64_t H, 
 /* The kernels that fp8_block_matmul and fp8_block_linear would launch for operands with 16-byte rows, on the current
  * device.  out[4] (host memory, written): [0] token rows of a tile, 16, 32 or 64 (weights on the MMA's 128-row side) or 256
  * (CTA pairs), 0 when the generic kernels are forced (then [1..3] are 0); [1] CTAs, or pairs, that share a tile's
- * k-blocks; [2] CTAs; [3] 1 when fp8_block_linear rounds its tokens inside the product's kernel.
+ * k-blocks; [2] CTAs; [3] 1 when fp8_block_linear rounds its tokens inside the product's kernel (y apart from x).
  * MSE_ERR_INVALID_ARG as the calls; MSE_ERR_UNSUPPORTED_DEVICE without a device. */
 MSE_API mse_status mse_fp8_launch_plan(int64_t T, int64_t N, int64_t K, int32_t *out);
 

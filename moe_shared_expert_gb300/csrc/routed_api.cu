@@ -18,6 +18,10 @@ constexpr int64_t kMaxPitch = (int64_t)1 << 32;
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool aligned256(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 255u) == 0; }
+bool disjoint(const void *a, int64_t a_bytes, const void *b, int64_t b_bytes) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x + (uintptr_t)a_bytes <= y || y + (uintptr_t)b_bytes <= x;
+}
 mse_status from_cuda(cudaError_t e) { return e == cudaSuccess ? MSE_OK : MSE_ERR_CUDA; }
 
 // x in 8 bits and its scales
@@ -259,7 +263,9 @@ mse_status fp8_block_linear(const mse_bf16 *x, int64_t ldx, const uint8_t *wq, i
     begin_untracked_call(stream);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     BlockGemm g = plain_product(xq, ldq, xs, wq, ldw, ws, T, N, K, y, y_dtype, d.sm_count);
-    if (tensorcore && rounds_itself(T, N, K)) {
+    // (y over x: the product's CTAs would write y while others still round x)
+    const bool apart = disjoint(x, ((T - 1) * ldx + K) * 2, y, T * N * (y_dtype == MSE_F32 ? 4 : 2));
+    if (tensorcore && apart && rounds_itself(T, N, K)) {
         g.x = x;
         g.ldxb = ldx;
         g.x_wide = ldx % 8 == 0 && aligned16(x);

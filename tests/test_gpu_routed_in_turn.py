@@ -55,3 +55,23 @@ def test_experts_calls_in_turn_with_and_without_pairs(T):
         for a, i, y in zip(x, ids, got):
             mse.moe_experts_forward(a, i, w, *weights, y=y, workspace=buf)
         assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("T", [1, 8, 9, 70, 600])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_linear_onto_its_own_tokens(T, dtype):
+    N, K = 512, 1024
+    wq, ws = mse.fp8_block_quantise(torch.randn(N, K, generator=gen(40)).to(torch.bfloat16).cuda(), block_rows=128)
+    x = torch.randn(T, K, generator=gen(41)).to(torch.bfloat16).cuda()
+    want = mse.fp8_block_linear(x, wq, ws, y_dtype=dtype)
+    for _ in range(5):
+        over = x.clone()
+        flat = over.view(-1).view(dtype)
+        y = flat[:T * N].view(T, N)                    # bf16: the first half of x; fp32: all of it
+        mse.fp8_block_linear(over, wq, ws, y=y)
+        assert torch.equal(y, want)
+        if dtype is torch.bfloat16:                    # and its second half
+            over = x.clone()
+            y = over.view(-1)[T * N:].view(T, N)
+            mse.fp8_block_linear(over, wq, ws, y=y)
+            assert torch.equal(y, want)

@@ -57,6 +57,42 @@ def test_experts_calls_in_turn_with_and_without_pairs(T):
         assert all(torch.equal(a, b) for a, b in zip(got, want))
 
 
+@pytest.mark.parametrize("T", [1, 3, 40])
+def test_a_decode_loop_on_kept_buffers(T):
+    # every step routes into the same ids and weights, and its experts read them at once
+    E, H, I, k = 12, 512, 256, 4
+    weights = make_experts(E, H, I, 30)
+    steps = 8
+    logits = torch.randn(steps, T, E, generator=gen(31)).cuda()
+    x = torch.randn(steps, T, H, generator=gen(32)).to(torch.bfloat16).cuda()
+    want = torch.empty_like(x)
+    for i in range(steps):
+        torch.cuda.synchronize()
+        want[i] = mse.moe_experts_forward(x[i], *mse.moe_route(logits[i], k), *weights)
+    torch.cuda.synchronize()
+    ids, w = torch.empty(T, k, dtype=torch.int32, device="cuda"), torch.empty(T, k, device="cuda")
+    buf = mse.new_moe_workspace(T, k, E, H, I)
+
+    def loop(y):
+        for i in range(steps):
+            mse.moe_route(logits[i], k, ids=ids, weights=w)
+            mse.moe_experts_forward(x[i], ids, w, *weights, y=y[i], workspace=buf)
+
+    for _ in range(5):
+        y = torch.empty_like(x)
+        torch.cuda.synchronize()
+        loop(y)
+        assert torch.equal(y, want)
+    y = torch.empty_like(x)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        loop(y)
+    for _ in range(3):
+        y.zero_()
+        graph.replay()
+        assert torch.equal(y, want)
+
+
 @pytest.mark.parametrize("T", [1, 8, 9, 70, 600])
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 def test_linear_onto_its_own_tokens(T, dtype):

@@ -24,7 +24,9 @@ __device__ __forceinline__ float block_scale(float a) { return __fdiv_rn(a, kE4m
 // `inv` is 1 / a to nearest.  One residual step makes every quotient that 32 bits hold exact (q's
 // error is a few units in the last place, the residual is exact, and so the step's error lies far
 // below half a unit), ties of e4m3 among them; the others are nowhere near a tie when v and a are
-// bf16.  Infinite v or a: NaN, like the quotient's product with the scale.
+// bf16.  Infinite v or a: NaN, like the quotient's product with the scale.  (h, which is in 32 bits, is rounded by this in the
+// swap-AB kernel and by one product with 448 / a in the CTA-pair kernel: the two differ, as their sums do, where h lies in the
+// last bits beside the middle of two e4m3 values.)
 __device__ __forceinline__ float e4m3_ratio(float v, float a, float inv) {
     const float t = v * 0.875f, q = t * inv;
     return fmaf(fmaf(-a, q, t), inv, q) * 512.f;
@@ -72,8 +74,9 @@ __device__ __forceinline__ uint32_t abs_max8(uint4 w) {
 __device__ __forceinline__ uint32_t bits_of_max2(uint32_t m) { return max(m << 16, m & 0xFFFF0000u); }
 
 // silu(g) u = g u / (1 + e^-g), without the care that the general exponential and quotient take of subnormal numbers:
-// e^-g below 2^-126 counts as 0 and 1 / (1 + e^-g) too, for g beyond 87 either way, where the result is g u or nothing.  Within
-// 2 ulp otherwise, like the general ones.  (64 of these a thread were a quarter of gate and up at K = 768; the layer of 1367 tokens with 8 of 32
+// e^-g below 2^-126 counts as 0 and 1 / (1 + e^-g) too, for g beyond 87 either way, where the result is g u or nothing.
+// Otherwise the rounding of g log2(e) makes e^-g wrong by up to 1.3 |g| 2^-24 of itself (2^-20.3 at g = -10, 2^-17.3 at
+// -80), and the two approximations by a few 2^-23 more: h keeps four bits of it.  (64 of these a thread were a quarter of gate and up at K = 768; the layer of 1367 tokens with 8 of 32
 // experts of 768 x 1792 takes 112 us, 140 with the general ones.)
 __device__ __forceinline__ float glu(float g, float u) {
     float e, r;

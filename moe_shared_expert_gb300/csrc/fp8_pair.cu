@@ -10,9 +10,11 @@
 // Warp 0 loads (TMA), warp 1 of the leading CTA issues MMAs, warps 4-11 promote and store; the
 // first warpgroup hands registers to them.  A tile's sums are written while the MMAs of the next one's first two k-blocks run.
 //
-// Bound by the power limit and, with few k-blocks to a tile, by the sums' way out: 8192 x 12288 x 7168 475 us, 3.04 PFLOP/s
-// (486 with the rows stored by the lanes); gate and up of 4096 tokens x 8 experts (7168 x 2048) 764 to 780 us, down 464
-// (508).
+// Bound by the hand-over of the two buffers and, with few k-blocks to a tile, by the sums' way out.  A k-block takes 790 cycles
+// (4096 x 4864 x 7168, four tiles to every pair): 512 of MMAs, and a buffer is the promotion's for about 1070 between two
+// turns of them; tensor pipe 66% busy, issue slots 57%.  8192 x 12288 x 7168 471 us alone, 3.06 PFLOP/s (486 with the rows
+// stored by the lanes), and 530 over seconds, when the power limit holds the clock at 1.66 of 2.07 GHz; fp32 492 and 555.
+// Gate and up of 4096 tokens x 8 experts (7168 x 2048) 764 to 780 us, down 464 (508).
 #include <atomic>
 #include <type_traits>
 

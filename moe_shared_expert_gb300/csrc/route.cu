@@ -325,6 +325,11 @@ cudaError_t launch_vpl(RouteParams p, int sm_count, bool pdl, cudaStream_t s) {
 
 }  // namespace
 
+// Experts a lane.  Beside the powers of two, classes for 129 to 192, 257 to 384 and 385 to 448 experts, whose unused registers and
+// steps cost most (us with them and with the next power of two: 65536 x 160 in 8 groups 57.2, 75.7; 65536 x 192 67.7, 80.5;
+// 32768 x 384 in 8 groups 51.8, 67.4; 23405 x 448 45.4, 49.3; 8192 x 160 without groups 6.8, 7.8; 192 8.0, 8.6; 384 9.9,
+// 10.7; 448 10.1, 10.6).  Other numbers take the next class (8192 x 320 9.6, 8192 x 96 6.4, like 128), from 513 on the
+// one of 1024.
 cudaError_t launch_route(const RouteParams &p, int sm_count, bool pdl, cudaStream_t s) {
     switch ((p.E + 31) / 32) {
         case 1: return launch_vpl<1>(p, sm_count, pdl, s);

@@ -105,7 +105,7 @@ struct BlockGemm {
     void *out; int64_t ldo;        // BF16 / F32 (and the generic kernels' SWIGLU, fp32)
     uint8_t *hq; int64_t ldh;      // SWIGLU: rounded h and its scales [rows x hb]
     float *hs; int hb;
-    int weights_early;             // the weights are complete before this launch can start
+    int weights_early;             // the weights are complete before this launch can start (swap-AB kernel)
     uint64_t wait_limit_ns;
     uint32_t *err;
 };

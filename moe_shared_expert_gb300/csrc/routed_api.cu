@@ -61,7 +61,10 @@ int plain_tile_rows(int64_t T, int64_t N, int64_t K, int sm_count) {
     const int64_t pair_time = pair_waves * kb * 41 / pp + (pp == 4 ? 600 : pp == 2 ? 400 : 0) + 130;
     return pair_time < cols_time ? 256 : 64;
 }
-// Experts, by the rows expected of each, if all pairs were this rank's (us with tiles of 16, 32 and 256; 32 experts of
+// Experts, by the rows expected of each, if all pairs were this rank's: the call does not know how many experts there are
+// in all, and a rank that holds some of them gets larger tiles than its rows ask for (32 of 128 experts of 7168 x 2048 with
+// 256 tokens, 16 rows each, 309 us, 280 with tiles of 16; 32 of 256, 8 rows, 306, 253; with 128 tokens 258, 230).  One bound
+// between 32 and 256 for all sizes lies between what small and large experts would have (us with tiles of 16, 32 and 256; 32 experts of
 // 7168 x 2048: 16 rows 247, 248, 313; 32 rows 311, 279, 322; 40 rows 371, 332, 327; 48 rows 407, 345, 332; 8 of 2048 x 1536:
 // 16 rows 26, 27, 41; 48 rows 48, 36, 45; 64 rows 54, 42, 46; 80 rows 60, 53, 46; half of 64 experts of 1000 x 500, 50 rows
 // 35, 32, 40; tiles of 64 and 128 were never the fastest).
@@ -91,9 +94,12 @@ BlockGemm plain_product(const uint8_t *xq, int64_t ldx, const float *xs, const u
     return g;
 }
 
-// One launch, whose kernel rounds the tokens itself, where the second one costs more than what every CTA
-// spends on all tokens (us of GPU time with one launch and with two, the host's 5.8 and 7.8: 3 x 904 x 966 6.2, 6.6;
-// 1 x 2112 x 7168 8.6, 8.2; 8 x 7168 x 6144 14.0, 13.7; 1 x 12288 x 7168 19.7, 18.2; 16 x 1024 x 4096 8.4, 6.9).
+// One launch, whose kernel rounds the tokens itself, up to 8 tokens of a small weight: called one after another it saves the
+// host a launch, and in a graph the two come to the same; every CTA rounds all tokens, which larger weights pay for.  (us with
+// one launch and with two, called in a row, and in a graph with the weights from memory: 3 x 904 x 966 6.3, 8.7 and 5.1, 5.2;
+// 8 x 1024 x 1024 6.1, 8.5 and 5.6, 5.4; 1 x 576 x 7168 7.3, 8.7 and 7.4, 7.6; 1 x 2112 x 7168 9.0, 9.2 and 8.9, 8.9;
+// 8 x 4096 x 4096 9.7, 10.0 and 9.9, 10.0; beyond the bound 8 x 7168 x 6144 13.3, 13.3 and 13.6, 13.3; 1 x 12288 x 7168 18.6,
+// 18.6 and 19.7, 19.3; 16 tokens of 1024 x 4096 8.4, 6.9.)
 bool rounds_itself(int64_t T, int64_t N, int64_t K) { return T <= kRoundRows && N * K <= (int64_t)1 << 24; }
 
 bool tc_operands(const void *xq, int64_t ldx, const void *wq, int64_t ldw) {
@@ -104,7 +110,8 @@ bool tc_operands(const void *xq, int64_t ldx, const void *wq, int64_t ldw) {
 // Up to this many pairs every CTA of the dispatch counts all ids itself.
 constexpr int64_t kCountAllPairs = 4096;
 
-// Tokens of a CTA of the dispatch: about as many CTAs as SMs, as far as a CTA's pairs reach.
+// Tokens of a CTA of the dispatch: about as many CTAs as SMs, as far as a CTA's pairs reach.  (A constant, because the
+// workspace's size, asked for without a device, follows from it; the GB300 has 152.)
 constexpr int64_t kDispatchChunks = 152;
 int chunk_of(int64_t T, int top_k) {
     return (int)std::min<int64_t>(kDispatchPairs / top_k, std::max<int64_t>(1, T / kDispatchChunks));
@@ -346,7 +353,8 @@ mse_status moe_experts_forward(const mse_bf16 *x, int64_t T, int64_t H, const in
     dn.xq = gu.hq; dn.ldx = gu.ldh; dn.xs = gu.hs;
     dn.wq = w_down; dn.ldw = ld_down; dn.ws = s_down;
     dn.out = o;
-    dn.weights_early = 1;   // (and the tiles: the gate_up launch lets this one start after its own wait)
+    dn.weights_early = 1;   // (and the tiles: the gate_up launch lets this one start after its own wait; the CTA-pair kernel
+                            // waits for all of it)
     if ((st = run_product(dn, tensorcore, d, s)) != MSE_OK) return st;
     return from_cuda(launch_combine(o, dn.ldo, dp.pos, weights, top_k, shared, y, T, H, d.sm_count, pdl, s));
 }

@@ -615,6 +615,106 @@ MSE_API mse_status mse_fp8_launch_plan(int64_t T, int64_t N, int64_t K, int32_t 
  * ids; [6] 1 when the ids are counted by kernels of their own; [7] 0. */
 MSE_API mse_status mse_moe_launch_plan(int64_t T, int top_k, int64_t E, int64_t H, int64_t I, int32_t *out);
 
+/* ---------------------------------------------------------------------------
+ * Tokens sorted by expert and back with their weights, with the gradients of both ways, for experts that the
+ * caller runs (any product over rows [offsets[e], offsets[e + 1])).
+ *
+ * Sizes beyond these are MSE_ERR_INVALID_ARG: T, rows and T * top_k 2^30; H 2^22; row pitches 2^32 values; top_k and E
+ * MSE_ROUTE_MAX_TOP_K and MSE_ROUTE_MAX_EXPERTS.  Outputs lie apart from the inputs, but for those named.
+ * ------------------------------------------------------------------------- */
+
+/* Workspace of moe_sort for every token count up to T (0 on invalid arguments): 256-byte aligned, need not be zeroed. */
+MSE_API size_t moe_sort_workspace_bytes(int64_t T, int top_k, int64_t E);
+
+/* The rows of a rank that holds experts [first_expert, first_expert + E), sorted by expert, in the order of t * top_k + j
+ * within each:
+ *
+ *   rows[place[t, j]] = x[t]  for every pair (t, j) with ids[t, j] - first_expert in [0, E); place is -1 for the others
+ *   offsets[e] = the first row of expert e; offsets[E] = the rows in all
+ *
+ *   x           [T x H]          values of value_bytes 1, 2 or 4 (copied as they are), row pitch ldx >= H
+ *   ids         [T x top_k]      int32, as moe_route gives them
+ *   scales      [T]              fp32 for each token, copied along to row_scales [T * top_k]; or null, both
+ *   rows        [T * top_k x H]  row pitch ldr >= H, rows_capacity >= (T * top_k - 1) * ldr + H; rows from offsets[E] on are
+ *                                left as they were, and the values between H and ldr too
+ *   place       [T x top_k]      int32;   offsets [E + 1] int32
+ * MSE_ERR_GEOMETRY: rows_capacity. */
+MSE_API mse_status moe_sort(const void *x, int value_bytes, int64_t T, int64_t H, int64_t ldx, const int32_t *ids, int top_k,
+                            int64_t E, int64_t first_expert, const float *scales, void *rows, int64_t ldr,
+                            int64_t rows_capacity, float *row_scales, int32_t *place, int32_t *offsets, void *workspace,
+                            size_t workspace_bytes, void *stream);
+
+/* y[t] = base[t] + sum_j weights[t, j] rows[place[t, j]], in fp32, ascending j, rounded once.  Pairs whose place is not in
+ * [0, n_rows) add nothing.
+ *   rows     [n_rows x H]  bf16 or fp32, row pitch ldr >= H;   place [T x top_k] int32
+ *   weights  [T x top_k]   fp32, or null for 1
+ *   base     [T x H]       of y's type (y itself is allowed), or null for 0
+ *   y        [T x H]       bf16 or fp32, y_capacity >= T*H elements
+ * With the gradient of sorted rows as rows and no weights: the gradient of moe_sort, dx[t] = sum_j drows[place[t, j]]. */
+MSE_API mse_status moe_unsort(const void *rows, mse_dtype rows_dtype, int64_t n_rows, int64_t ldr, const int32_t *place,
+                              const float *weights, int64_t T, int64_t H, int top_k, const void *base, void *y,
+                              mse_dtype y_dtype, int64_t y_capacity, void *stream);
+
+/* The gradients of moe_unsort from dy [T x H] (bf16 or fp32):
+ *   drows[place[t, j]] = weights[t, j] dy[t],    dweights[t, j] = <rows[place[t, j]], dy[t]> in fp32
+ * (base's is dy).  Pairs whose place is not in [0, n_rows) have dweights 0.
+ *   weights   [T x top_k]   fp32, or null for 1 (then dweights is null, and rows is not read)
+ *   rows      [n_rows x H]  as moe_unsort had them, row pitch ldr >= H
+ *   drows     [n_rows x H]  of rows' type (rows itself, with its pitch, is allowed), row pitch ldd >= H, drows_capacity >=
+ *                           (n_rows - 1) * ldd + H; rows that are no pair's place are left as they were
+ *   dweights  [T x top_k]   fp32
+ * place holds no row twice, as moe_sort gives it (else that row of drows is either pair's). */
+MSE_API mse_status moe_unsort_backward(const void *dy, mse_dtype dy_dtype, const int32_t *place, const float *weights,
+                                       const void *rows, mse_dtype rows_dtype, int64_t ldr, int64_t n_rows, int64_t T,
+                                       int64_t H, int top_k, void *drows, int64_t ldd, int64_t drows_capacity,
+                                       float *dweights, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * Products in 8-bit integers: a scale for each row of either operand (each token, each output channel).
+ *
+ * Sizes beyond these are MSE_ERR_INVALID_ARG: T, rows and groups * N 2^30; N 2^22; K 2^17 - 1 (so that a sum fits 32 bits;
+ * int8_quantise 2^22); groups MSE_ROUTE_MAX_EXPERTS; row pitches 2^32 values.
+ * ------------------------------------------------------------------------- */
+
+/* Rows rounded to 8-bit integers:  a = max(max |r|, 2^-100),  scale = a / 127,  q = rint(127 r / a), ties to even, of a
+ * quotient in fp32.  r = x, or with swiglu silu(x[.., :K]) * x[.., K:] in fp32.  A row with an infinity or a NaN stands for
+ * NaN throughout (scale NaN, q 0).
+ *   x       [rows x K], swiglu: [rows x 2K]  bf16 or fp32, row pitch ldx
+ *   last    null, or one int32 on the device: rows from *last on are left alone (offsets + E of moe_sort)
+ *   q       [rows x K]  int8, row pitch ldq >= K, q_capacity >= (rows - 1) * ldq + K, apart from x
+ *   scales  [rows] fp32 */
+MSE_API mse_status int8_quantise(const void *x, mse_dtype x_dtype, int64_t rows, int64_t K, int64_t ldx, int swiglu,
+                                 const int32_t *last, int8_t *q, int64_t ldq, int64_t q_capacity, float *scales,
+                                 void *stream);
+
+/* Workspace of the products for every token count up to T with the same or smaller other sizes (0 on invalid arguments):
+ * 256-byte aligned, need not be zeroed. */
+MSE_API size_t int8_workspace_bytes(int64_t T, int64_t N, int64_t K, int64_t groups);
+
+/* out[t, n] = (sum_k xq[t, k] wq[n, k]) xs[t] ws[n]: the sum is the integer itself, whatever the kernel; it is rounded to
+ * fp32, multiplied by xs[t], then by ws[n], and rounded to out's type.
+ *   xq [T x K] int8, row pitch ldx >= K;  xs [T] fp32
+ *   wq [N x K] int8, row pitch ldw >= K;  ws [N] fp32
+ *   out [T x N] bf16 or fp32, out_capacity >= T*N elements, apart from xq
+ * The tensor-core kernels take row pitches of wq that are multiples of 16 and a 16-byte aligned wq; anything else takes
+ * the generic kernels. */
+MSE_API mse_status int8_matmul(const int8_t *xq, int64_t ldx, const float *xs, const int8_t *wq, int64_t ldw, const float *ws,
+                               int64_t T, int64_t N, int64_t K, void *out, mse_dtype out_dtype, int64_t out_capacity,
+                               void *workspace, size_t workspace_bytes, void *stream);
+
+/* The same of sorted rows with their group's weights: rows [offsets[g], offsets[g + 1]) of xq with wq[g] [N x K] and ws[g]
+ * [N].  offsets [groups + 1] int32 ascends, as moe_sort gives it; rows of out outside them are left as they were.  T: rows of
+ * xq and out (offsets beyond count as T). */
+MSE_API mse_status int8_grouped_matmul(const int8_t *xq, int64_t ldx, const float *xs, const int32_t *offsets, int64_t groups,
+                                       const int8_t *wq, int64_t ldw, const float *ws, int64_t T, int64_t N, int64_t K,
+                                       void *out, mse_dtype out_dtype, int64_t out_capacity, void *workspace,
+                                       size_t workspace_bytes, void *stream);
+
+/* int8_quantise of x [T x K] (bf16 or fp32, row pitch ldx), then int8_matmul, in one call.  y may lie over x. */
+MSE_API mse_status int8_linear(const void *x, mse_dtype x_dtype, int64_t ldx, const int8_t *wq, int64_t ldw, const float *ws,
+                               int64_t T, int64_t N, int64_t K, void *y, mse_dtype y_dtype, int64_t y_capacity,
+                               void *workspace, size_t workspace_bytes, void *stream);
+
 /* Human-readable name of a status code (static string). */
 MSE_API const char *mse_status_string(mse_status s);
 

@@ -12,6 +12,10 @@ plus the workspace queries, the device-error poll and the settings, and
 ``sequence_parallel_mlp``, which takes the sharding decision and makes the matching call.
 The routed experts beside the shared expert are in ``routed.py`` (exported here too):
     moe_route, fp8_block_quantise, fp8_block_matmul, fp8_block_linear, moe_experts_forward
+tokens sorted by expert and back, with gradients, in ``rows.py``:
+    moe_sort, moe_unsort, moe_unsort_backward, moe_sort_backward
+and products in 8-bit integers in ``int8.py``:
+    int8_quantise, int8_matmul, int8_grouped_matmul, int8_linear
 """
 from __future__ import annotations
 
@@ -31,6 +35,8 @@ __all__ = [
     "moe_route", "fp8_block_quantise", "fp8_block_matmul", "fp8_block_linear", "moe_experts_forward",
     "fp8_linear_workspace_bytes", "new_fp8_linear_workspace", "moe_workspace_bytes", "new_moe_workspace",
     "fp8_launch_plan", "moe_launch_plan",
+    "moe_sort", "moe_sort_backward", "moe_unsort", "moe_unsort_backward", "moe_sort_workspace_bytes", "new_moe_sort_workspace",
+    "int8_quantise", "int8_matmul", "int8_grouped_matmul", "int8_linear", "int8_workspace_bytes", "new_int8_workspace",
 ]
 
 BF16, F32 = 0, 1
@@ -107,6 +113,15 @@ def lib() -> ctypes.CDLL:
                                              P, sz, P]),
                 "mse_fp8_launch_plan": (ci, [i64, i64, i64, P]),
                 "mse_moe_launch_plan": (ci, [i64, ci, i64, i64, i64, P]),
+                "moe_sort_workspace_bytes": (sz, [i64, ci, i64]),
+                "moe_sort": (ci, [P, ci, i64, i64, i64, P, ci, i64, i64, P, P, i64, i64, P, P, P, P, sz, P]),
+                "moe_unsort": (ci, [P, ci, i64, i64, P, P, i64, i64, ci, P, P, ci, i64, P]),
+                "moe_unsort_backward": (ci, [P, ci, P, P, P, ci, i64, i64, i64, i64, ci, P, i64, i64, P, P]),
+                "int8_quantise": (ci, [P, ci, i64, i64, i64, ci, P, P, i64, i64, P, P]),
+                "int8_workspace_bytes": (sz, [i64, i64, i64, i64]),
+                "int8_matmul": (ci, [P, i64, P, P, i64, P, i64, i64, i64, P, ci, i64, P, sz, P]),
+                "int8_grouped_matmul": (ci, [P, i64, P, P, i64, P, i64, P, i64, i64, i64, P, ci, i64, P, sz, P]),
+                "int8_linear": (ci, [P, ci, i64, P, i64, P, i64, i64, i64, P, ci, i64, P, sz, P]),
                 "mse_status_string": (ctypes.c_char_p, [ci]),
                 "mse_version": (ctypes.c_char_p, []),
             }
@@ -433,3 +448,7 @@ def set_phase_events(ev_begin=None, ev_mid=None, ev_end=None) -> None:
 from .routed import (  # noqa: E402  (needs the names above)
     fp8_block_linear, fp8_block_matmul, fp8_block_quantise, fp8_launch_plan, fp8_linear_workspace_bytes,
     moe_experts_forward, moe_launch_plan, moe_route, moe_workspace_bytes, new_fp8_linear_workspace, new_moe_workspace)
+from .rows import (  # noqa: E402
+    moe_sort, moe_sort_backward, moe_sort_workspace_bytes, moe_unsort, moe_unsort_backward, new_moe_sort_workspace)
+from .int8 import (  # noqa: E402
+    int8_grouped_matmul, int8_linear, int8_matmul, int8_quantise, int8_workspace_bytes, new_int8_workspace)

@@ -1,0 +1,382 @@
+// Tokens sorted by expert and back with weights, and the gradients of both ways.
+//
+// All of it moves rows: what bounds each kernel is the memory.  Nothing is drawn by atomics: a pair's place is counted, and
+// every sum has one order.
+#include "common.cuh"
+#include "launch.h"
+#include "sorted.h"
+
+namespace mse {
+namespace sorted {
+namespace {
+
+// ---------------------------------------------------------------------------
+// sort
+// ---------------------------------------------------------------------------
+
+// expert of pair i on this rank, or -1
+__device__ __forceinline__ int local_expert(const SortParams &p, int64_t i) {
+    const int64_t e = (int64_t)p.ids[i] - p.first_expert;
+    return e >= 0 && e < p.E ? (int)e : -1;
+}
+
+// hist[c][e] = pairs of expert e in chunk c
+__global__ void __launch_bounds__(kSortThreads) count_pairs_kernel(const SortParams p) {
+    extern __shared__ int count_smem[];
+    pdl_wait();
+    pdl_launch_dependents();
+    for (int e = threadIdx.x; e < p.E; e += kSortThreads) count_smem[e] = 0;
+    __syncthreads();
+    const int64_t i0 = (int64_t)blockIdx.x * p.chunk * p.top_k, i1 = min(i0 + (int64_t)p.chunk * p.top_k, p.T * p.top_k);
+    for (int64_t i = i0 + threadIdx.x; i < i1; i += kSortThreads) {
+        const int e = local_expert(p, i);
+        if (e >= 0) atomicAdd(&count_smem[e], 1);
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < p.E; e += kSortThreads) p.hist[(int64_t)blockIdx.x * p.E + e] = count_smem[e];
+}
+
+// hist[c][e] becomes the pairs of expert e in the chunks before c; row n_chunks: in all of them.  A warp has 32 experts' chunks
+// c = warp, warp + 32, .. summed first as 32 runs of neighbouring chunks.
+constexpr int kScanThreads = 1024;
+__global__ void __launch_bounds__(kScanThreads) scan_pairs_kernel(int *hist, int n_chunks, int E) {
+    __shared__ int sums[32][33];
+    pdl_wait();
+    pdl_launch_dependents();
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, e = (int)blockIdx.x * 32 + lane;
+    const int per = (n_chunks + 31) / 32, c0 = min(warp * per, n_chunks), c1 = min(c0 + per, n_chunks);
+    int sum = 0;
+    if (e < E)
+#pragma unroll 8
+        for (int c = c0; c < c1; ++c) sum += hist[(int64_t)c * E + e];
+    sums[warp][lane] = sum;
+    __syncthreads();
+    if (e >= E) return;
+    int run = 0;
+    for (int w = 0; w < warp; ++w) run += sums[w][lane];
+    for (int c = c0; c < c1; ++c) {
+        const int mine = hist[(int64_t)c * E + e];
+        hist[(int64_t)c * E + e] = run;
+        run += mine;
+    }
+    if (warp == 31) hist[(int64_t)n_chunks * E + e] = run;
+}
+
+// exclusive prefix sums of v[0 .. n) in shared memory by one warp; the total is returned
+__device__ __forceinline__ int warp_prefix(int *v, int n, int lane) {
+    int run = 0;
+    for (int c = 0; c < n; c += 32) {
+        const int mine = c + lane < n ? v[c + lane] : 0;
+        int s = mine;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int o = __shfl_up_sync(~0u, s, d);
+            if (lane >= d) s += o;
+        }
+        if (c + lane < n) v[c + lane] = run + s - mine;
+        run += __shfl_sync(~0u, s, 31);
+    }
+    return run;
+}
+
+// CTA (c, y): the places of chunk c's pairs, counted by every CTA of the chunk alike, and the y-th share of its rows' copies.
+// A pair's place is its expert's first row, the expert's pairs in the chunks before, and those before it in the chunk.
+template <typename W>
+__global__ void __launch_bounds__(kSortThreads) sort_kernel(const SortParams p) {
+    extern __shared__ int sort_smem[];
+    int *total = sort_smem, *before = total + p.E, *of_warp = before + p.E;   // of_warp: [warps x E]
+    __shared__ int pair_row[kSortThreads];
+    const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+    pdl_wait();
+    const int64_t t0 = (int64_t)blockIdx.x * p.chunk, i0 = t0 * p.top_k;
+    const int tokens = (int)min((int64_t)p.chunk, p.T - t0), mine = tokens * p.top_k;
+    for (int i = tid; i < kSortThreads / 32 * p.E; i += kSortThreads) of_warp[i] = 0;
+    if (p.hist) {
+        for (int e = tid; e < p.E; e += kSortThreads) {
+            total[e] = p.hist[(int64_t)p.n_chunks * p.E + e];
+            before[e] = p.hist[(int64_t)blockIdx.x * p.E + e];
+        }
+        __syncthreads();
+    } else {
+        for (int e = tid; e < p.E; e += kSortThreads) total[e] = before[e] = 0;
+        __syncthreads();
+        for (int64_t i = tid; i < p.T * p.top_k; i += kSortThreads) {
+            const int e = local_expert(p, i);
+            if (e >= 0) {
+                atomicAdd(&total[e], 1);
+                if (i < i0) atomicAdd(&before[e], 1);
+            }
+        }
+    }
+    // pair `tid` of the chunk: the pairs of its expert before it in its warp, and the warp's pairs of the expert
+    const int expert = tid < mine ? local_expert(p, i0 + tid) : -1;
+    const uint32_t same = __match_any_sync(~0u, expert);
+    const int rank = __popc(same & ((1u << lane) - 1u));
+    if (expert >= 0 && rank == 0) of_warp[warp * p.E + expert] = __popc(same);
+    __syncthreads();
+    if (warp == 0) {   // the experts' first rows
+        const int all = warp_prefix(total, p.E, lane);
+        __syncwarp();
+        if (blockIdx.x == 0 && blockIdx.y == 0) {
+            for (int e = lane; e < p.E; e += 32) p.offsets[e] = total[e];
+            if (lane == 0) p.offsets[p.E] = all;
+        }
+    }
+    __syncthreads();
+    if (tid < mine) {
+        int row = -1;
+        if (expert >= 0) {
+            row = total[expert] + before[expert] + rank;
+            for (int w = 0; w < warp; ++w) row += of_warp[w * p.E + expert];
+        }
+        pair_row[tid] = row;
+        if (blockIdx.y == 0) {
+            p.place[i0 + tid] = row;
+            if (p.scales && row >= 0) p.row_scales[row] = p.scales[t0 + tid / p.top_k];
+        }
+    }
+    __syncthreads();
+    // segments of kWords words a lane: (token, segment) by (token), warps of all the chunk's CTAs in turn
+    constexpr int kWords = 2;
+    const int64_t words = p.row_bytes / (int)sizeof(W);
+    const int segs = (int)((words + 32 * kWords - 1) / (32 * kWords));
+    const int64_t items = (int64_t)tokens * segs;
+    for (int64_t it = (int64_t)blockIdx.y * (kSortThreads / 32) + warp; it < items; it += (int64_t)p.splits * (kSortThreads / 32)) {
+        const int t = (int)(it / segs);
+        const int64_t at = (it - (int64_t)t * segs) * (32 * kWords) + lane;
+        const W *src = reinterpret_cast<const W *>(p.x + (t0 + t) * p.ldx) + at;
+        W v[kWords];
+#pragma unroll
+        for (int i = 0; i < kWords; ++i)
+            if (at + 32 * i < words) v[i] = src[32 * i];
+        for (int j = 0; j < p.top_k; ++j) {
+            const int row = pair_row[t * p.top_k + j];
+            if (row < 0) continue;
+            W *dst = reinterpret_cast<W *>(p.rows + row * p.ldr) + at;
+#pragma unroll
+            for (int i = 0; i < kWords; ++i)
+                if (at + 32 * i < words) dst[32 * i] = v[i];
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// values of 2 and 4 bytes, V at a time, in 32 bits
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ float value_of(uint16_t v) { return bf16_bits_to_f32(v); }
+__device__ __forceinline__ float value_of(float v) { return v; }
+__device__ __forceinline__ void put(uint16_t &o, float v) { o = f32_to_bf16_bits(v); }
+__device__ __forceinline__ void put(float &o, float v) { o = v; }
+
+// V values as they lie in memory, in words of up to 16 bytes
+template <typename T, int V>
+struct alignas(V * sizeof(T) > 16 ? 16 : V * sizeof(T)) Pack {
+    T v[V];
+};
+template <typename T, int V>
+__device__ __forceinline__ Pack<T, V> load_pack(const T *p) { return *reinterpret_cast<const Pack<T, V> *>(p); }
+template <typename T, int V>
+__device__ __forceinline__ void store_pack(T *p, const float (&f)[V]) {
+    Pack<T, V> o;
+#pragma unroll
+    for (int i = 0; i < V; ++i) put(o.v[i], f[i]);
+    *reinterpret_cast<Pack<T, V> *>(p) = o;
+}
+
+// ---------------------------------------------------------------------------
+// y[t] = base[t] + sum_j w[t, j] rows[place[t, j]], ascending j
+// ---------------------------------------------------------------------------
+constexpr int kPairs = 4;   // rows of a token on their way at once
+
+template <typename R, typename Y, int V>
+__global__ void __launch_bounds__(256) unsort_kernel(const UnsortParams p) {
+    pdl_wait();
+    const R *rows = static_cast<const R *>(p.rows);
+    const int64_t per = p.H / V, items = p.T * per;
+    for (int64_t it = (int64_t)blockIdx.x * 256 + threadIdx.x; it < items; it += (int64_t)gridDim.x * 256) {
+        const int64_t t = it / per, c = (it - t * per) * V;
+        float acc[V];
+        if (p.base) {
+            const Pack<Y, V> b = load_pack<Y, V>(static_cast<const Y *>(p.base) + t * p.H + c);
+#pragma unroll
+            for (int i = 0; i < V; ++i) acc[i] = value_of(b.v[i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; ++i) acc[i] = 0.f;
+        }
+        for (int j0 = 0; j0 < p.top_k; j0 += kPairs) {
+            int64_t row[kPairs];
+            float w[kPairs];
+            Pack<R, V> v[kPairs];
+#pragma unroll
+            for (int j = 0; j < kPairs; ++j) {
+                const bool have = j0 + j < p.top_k;
+                row[j] = have ? p.place[t * p.top_k + j0 + j] : -1;
+                w[j] = have && p.weights ? p.weights[t * p.top_k + j0 + j] : 1.f;
+                if (row[j] >= p.n_rows) row[j] = -1;
+            }
+#pragma unroll
+            for (int j = 0; j < kPairs; ++j)
+                if (row[j] >= 0) v[j] = load_pack<R, V>(rows + row[j] * p.ldr + c);
+#pragma unroll
+            for (int j = 0; j < kPairs; ++j)
+                if (row[j] >= 0)
+#pragma unroll
+                    for (int i = 0; i < V; ++i) acc[i] = fmaf(w[j], value_of(v[j].v[i]), acc[i]);
+        }
+        store_pack<Y, V>(static_cast<Y *>(p.y) + t * p.H + c, acc);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// drows[place[t, j]] = w[t, j] dy[t],  dweights[t, j] = <rows[place[t, j]], dy[t]>
+// ---------------------------------------------------------------------------
+// A CTA has one token at a time, kPairs of its pairs at once.
+constexpr int kBackThreads = 128;
+
+template <typename D, typename R, int V>
+__global__ void __launch_bounds__(kBackThreads) unsort_backward_kernel(const UnsortBackwardParams p) {
+    __shared__ float part[kBackThreads / 32][kPairs];
+    pdl_wait();
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    const D *dy = static_cast<const D *>(p.dy);
+    const R *rows = static_cast<const R *>(p.rows);
+    R *drows = static_cast<R *>(p.drows);
+    for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x) {
+        for (int j0 = 0; j0 < p.top_k; j0 += kPairs) {
+            int64_t row[kPairs];
+            float w[kPairs], dot[kPairs];
+            bool any = false;
+#pragma unroll
+            for (int j = 0; j < kPairs; ++j) {
+                const bool have = j0 + j < p.top_k;
+                row[j] = have ? p.place[t * p.top_k + j0 + j] : -1;
+                w[j] = have && p.weights ? p.weights[t * p.top_k + j0 + j] : 1.f;
+                if (row[j] >= p.n_rows) row[j] = -1;
+                any |= row[j] >= 0;
+                dot[j] = 0.f;
+            }
+            if (any)
+                for (int64_t c = (int64_t)threadIdx.x * V; c < p.H; c += kBackThreads * V) {
+                    const Pack<D, V> d = load_pack<D, V>(dy + t * p.H + c);
+                    Pack<R, V> v[kPairs];
+                    if (p.dweights)
+#pragma unroll
+                        for (int j = 0; j < kPairs; ++j)
+                            if (row[j] >= 0) v[j] = load_pack<R, V>(rows + row[j] * p.ldr + c);
+#pragma unroll
+                    for (int j = 0; j < kPairs; ++j)
+                        if (row[j] >= 0) {
+                            float o[V];
+#pragma unroll
+                            for (int i = 0; i < V; ++i) {
+                                const float g = value_of(d.v[i]);
+                                if (p.dweights) dot[j] = fmaf(value_of(v[j].v[i]), g, dot[j]);
+                                o[i] = w[j] * g;
+                            }
+                            store_pack<R, V>(drows + row[j] * p.ldd + c, o);
+                        }
+                }
+            if (!p.dweights) continue;
+#pragma unroll
+            for (int j = 0; j < kPairs; ++j) {
+#pragma unroll
+                for (int d = 16; d > 0; d >>= 1) dot[j] += __shfl_xor_sync(~0u, dot[j], d);
+                if (lane == 0) part[warp][j] = dot[j];
+            }
+            __syncthreads();
+            if (threadIdx.x < kPairs && j0 + threadIdx.x < p.top_k) {
+                float sum = 0.f;
+                for (int i = 0; i < kBackThreads / 32; ++i) sum += part[i][threadIdx.x];
+                p.dweights[t * p.top_k + j0 + threadIdx.x] = sum;
+            }
+            __syncthreads();
+        }
+    }
+}
+
+// the most values of a row, of 8, 4, 2 and 1, that one access of every tensor may take
+struct Width {
+    uint64_t bits = 0;   // byte addresses and pitches of words of `size`, brought to values
+    int64_t values = 0;
+    int limit = 8;
+    void tensor(const void *base, int64_t pitch, int size) {
+        if (!base) return;
+        values |= pitch;
+        while (limit > 1 && (reinterpret_cast<uintptr_t>(base) % (uintptr_t)std::min(limit * size, 16)) != 0) limit /= 2;
+    }
+    int width() const {
+        int v = limit;
+        while (v > 1 && values % v != 0) v /= 2;
+        return v;
+    }
+};
+
+}  // namespace
+
+cudaError_t launch_sort(const SortParams &p, bool pdl, cudaStream_t s) {
+    if (p.hist) {
+        cudaError_t e = launch_kernel(count_pairs_kernel, dim3((unsigned)p.n_chunks), kSortThreads, (size_t)p.E * 4, pdl, 1, s, p);
+        if (e == cudaSuccess)
+            e = launch_kernel(scan_pairs_kernel, dim3((unsigned)((p.E + 31) / 32)), kScanThreads, 0, pdl, 1, s, p.hist,
+                              p.n_chunks, p.E);
+        if (e != cudaSuccess) return e;
+    }
+    const dim3 grid((unsigned)p.n_chunks, (unsigned)p.splits);
+    const size_t smem = (size_t)p.E * 4 * (2 + kSortThreads / 32);
+    switch (p.unit) {
+        case 16: return launch_kernel(sort_kernel<uint4>, grid, kSortThreads, smem, pdl, 1, s, p);
+        case 8: return launch_kernel(sort_kernel<uint2>, grid, kSortThreads, smem, pdl, 1, s, p);
+        case 4: return launch_kernel(sort_kernel<uint32_t>, grid, kSortThreads, smem, pdl, 1, s, p);
+        case 2: return launch_kernel(sort_kernel<uint16_t>, grid, kSortThreads, smem, pdl, 1, s, p);
+        default: return launch_kernel(sort_kernel<uint8_t>, grid, kSortThreads, smem, pdl, 1, s, p);
+    }
+}
+
+namespace {
+template <typename R, typename Y>
+cudaError_t unsort_of(const UnsortParams &p, int v, dim3 grid, bool pdl, cudaStream_t s) {
+    switch (v) {
+        case 8: return launch_kernel(unsort_kernel<R, Y, 8>, grid, 256, 0, pdl, 1, s, p);
+        case 4: return launch_kernel(unsort_kernel<R, Y, 4>, grid, 256, 0, pdl, 1, s, p);
+        case 2: return launch_kernel(unsort_kernel<R, Y, 2>, grid, 256, 0, pdl, 1, s, p);
+        default: return launch_kernel(unsort_kernel<R, Y, 1>, grid, 256, 0, pdl, 1, s, p);
+    }
+}
+template <typename D, typename R>
+cudaError_t backward_of(const UnsortBackwardParams &p, int v, dim3 grid, bool pdl, cudaStream_t s) {
+    switch (v) {
+        case 8: return launch_kernel(unsort_backward_kernel<D, R, 8>, grid, kBackThreads, 0, pdl, 1, s, p);
+        case 4: return launch_kernel(unsort_backward_kernel<D, R, 4>, grid, kBackThreads, 0, pdl, 1, s, p);
+        case 2: return launch_kernel(unsort_backward_kernel<D, R, 2>, grid, kBackThreads, 0, pdl, 1, s, p);
+        default: return launch_kernel(unsort_backward_kernel<D, R, 1>, grid, kBackThreads, 0, pdl, 1, s, p);
+    }
+}
+}  // namespace
+
+cudaError_t launch_unsort(const UnsortParams &p, int sm_count, bool pdl, cudaStream_t s) {
+    Width w;
+    w.tensor(p.rows, p.ldr, p.rows_f32 ? 4 : 2);
+    w.tensor(p.base, p.H, p.y_f32 ? 4 : 2);
+    w.tensor(p.y, p.H, p.y_f32 ? 4 : 2);
+    const int v = w.width();
+    const dim3 grid((unsigned)std::min<int64_t>((p.T * (p.H / v) + 255) / 256, (int64_t)sm_count * 16));
+    if (p.rows_f32)
+        return p.y_f32 ? unsort_of<float, float>(p, v, grid, pdl, s) : unsort_of<float, uint16_t>(p, v, grid, pdl, s);
+    return p.y_f32 ? unsort_of<uint16_t, float>(p, v, grid, pdl, s) : unsort_of<uint16_t, uint16_t>(p, v, grid, pdl, s);
+}
+
+cudaError_t launch_unsort_backward(const UnsortBackwardParams &p, int sm_count, bool pdl, cudaStream_t s) {
+    Width w;
+    w.tensor(p.dy, p.H, p.dy_f32 ? 4 : 2);
+    w.tensor(p.rows, p.ldr, p.rows_f32 ? 4 : 2);
+    w.tensor(p.drows, p.ldd, p.rows_f32 ? 4 : 2);
+    const int v = w.width();
+    const dim3 grid((unsigned)std::min<int64_t>(p.T, (int64_t)sm_count * 16));
+    if (p.dy_f32)
+        return p.rows_f32 ? backward_of<float, float>(p, v, grid, pdl, s) : backward_of<float, uint16_t>(p, v, grid, pdl, s);
+    return p.rows_f32 ? backward_of<uint16_t, float>(p, v, grid, pdl, s) : backward_of<uint16_t, uint16_t>(p, v, grid, pdl, s);
+}
+
+}  // namespace sorted
+}  // namespace mse

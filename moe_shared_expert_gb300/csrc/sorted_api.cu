@@ -1,0 +1,266 @@
+// C-ABI entry points of the sorted rows and of the products in 8-bit integers: argument validation (before any CUDA
+// call), workspace carving and kernel choice.
+#include <algorithm>
+#include <cstring>
+
+#include "device.h"
+#include "sorted.h"
+
+using namespace mse;
+using namespace mse::sorted;
+
+namespace {
+
+size_t up256(size_t v) { return (v + 255) / 256 * 256; }
+bool aligned256(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 255u) == 0; }
+bool disjoint(const void *a, int64_t a_bytes, const void *b, int64_t b_bytes) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x + (uintptr_t)a_bytes <= y || y + (uintptr_t)b_bytes <= x;
+}
+mse_status from_cuda(cudaError_t e) { return e == cudaSuccess ? MSE_OK : MSE_ERR_CUDA; }
+bool dtype_ok(mse_dtype d) { return d == MSE_BF16 || d == MSE_F32; }
+int64_t size_of(mse_dtype d) { return d == MSE_F32 ? 4 : 2; }
+// bytes from the first to the last value of rows with a pitch
+int64_t span(int64_t rows, int64_t cols, int64_t ld, int64_t size) { return ((rows - 1) * ld + cols) * size; }
+
+// ------------------------------------------------------------------ sort
+// Up to this many pairs every CTA counts all ids itself.
+constexpr int64_t kCountAllPairs = 4096;
+// Tokens of a chunk: about as many chunks as the GB300 has SMs, as far as a chunk's pairs reach.  (A constant, because the
+// workspace's size, asked for without a device, follows from it.)
+constexpr int64_t kChunks = 152;
+int chunk_of(int64_t T, int top_k) {
+    return (int)std::min<int64_t>(kSortThreads / top_k, std::max<int64_t>(1, T / kChunks));
+}
+// no fewer than any number of tokens up to T has chunks
+size_t chunks_bound(int64_t T, int top_k) {
+    const int64_t most = kSortThreads / top_k;
+    return (size_t)std::max((T + most - 1) / most, std::min<int64_t>(T, 2 * kChunks));
+}
+bool sort_sizes_ok(int64_t T, int top_k, int64_t E) {
+    return T > 0 && top_k > 0 && E > 0 && top_k <= MSE_ROUTE_MAX_TOP_K && E <= MSE_ROUTE_MAX_EXPERTS && T <= kMaxRows &&
+           T * top_k <= kMaxRows;
+}
+size_t sort_ws(int64_t T, int top_k, int64_t E) {
+    return up256(T * top_k > kCountAllPairs ? (chunks_bound(T, top_k) + 1) * (size_t)E * 4 : 4);
+}
+
+// ------------------------------------------------------------------ 8-bit integers
+// tokens as the product's kernels take them, and their scales
+struct Int8Ws {
+    size_t q_off, s_off, total;
+};
+Int8Ws int8_ws(int64_t T, int64_t K) {
+    Int8Ws w;
+    w.q_off = 0;
+    w.s_off = up256((size_t)T * (size_t)((K + 63) / 64 * 64) * 2);
+    w.total = w.s_off + up256((size_t)T * 4);
+    return w;
+}
+bool int8_sizes_ok(int64_t T, int64_t N, int64_t K, int64_t groups) {
+    return T > 0 && N > 0 && K > 0 && groups > 0 && T <= kMaxRows && N <= kMaxInner && K <= kMaxInt8Inner &&
+           groups <= MSE_ROUTE_MAX_EXPERTS;
+}
+
+mse_status check_product(const void *x, int64_t ldx, const void *xs, const void *wq, int64_t ldw, const void *ws, int64_t T,
+                         int64_t N, int64_t K, int64_t groups, const void *out, mse_dtype dtype, int64_t capacity,
+                         const void *workspace, size_t bytes) {
+    if (!x || !xs || !wq || !ws || !out || !int8_sizes_ok(T, N, K, groups) || ldx < K || ldw < K || ldx > kMaxPitch ||
+        ldw > kMaxPitch || !dtype_ok(dtype) || groups * N > kMaxRows)
+        return MSE_ERR_INVALID_ARG;
+    if (capacity < T * N) return MSE_ERR_GEOMETRY;
+    if (!workspace || bytes < int8_ws(T, K).total || !aligned256(workspace)) return MSE_ERR_WORKSPACE;
+    return MSE_OK;
+}
+
+// the product reads all of a row of xq for every part of a row of out
+bool apart(const Int8Gemm &g) {
+    return disjoint(g.xq, span(g.T, g.K, g.ldx, 1), g.out, g.T * g.N * (g.out_f32 ? 4 : 2));
+}
+
+mse_status run_product(Int8Gemm g, const DeviceView &d, cudaStream_t s) {
+    g.wait_limit_ns = wait_limit_ns();
+    g.err = d.err;
+    return from_cuda(launch_int8_simt(g, pdl_enabled(), s));
+}
+
+Int8Gemm product(const int8_t *xq, int64_t ldx, const float *xs, const int32_t *offsets, int64_t groups, const int8_t *wq,
+                 int64_t ldw, const float *ws, int64_t T, int64_t N, int64_t K, void *out, mse_dtype dtype) {
+    Int8Gemm g;
+    std::memset(&g, 0, sizeof g);
+    g.T = T;
+    g.xq = xq; g.ldx = ldx; g.xs = xs;
+    g.offsets = offsets; g.groups = (int)groups;
+    g.wq = wq; g.ldw = ldw; g.ws = ws;
+    g.N = N; g.K = K;
+    g.out = out; g.out_f32 = dtype == MSE_F32;
+    return g;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t moe_sort_workspace_bytes(int64_t T, int top_k, int64_t E) { return sort_sizes_ok(T, top_k, E) ? sort_ws(T, top_k, E) : 0; }
+
+mse_status moe_sort(const void *x, int value_bytes, int64_t T, int64_t H, int64_t ldx, const int32_t *ids, int top_k, int64_t E,
+                    int64_t first_expert, const float *scales, void *rows, int64_t ldr, int64_t rows_capacity,
+                    float *row_scales, int32_t *place, int32_t *offsets, void *workspace, size_t workspace_bytes, void *stream) {
+    if (!x || !ids || !rows || !place || !offsets || (scales != nullptr) != (row_scales != nullptr) ||
+        (value_bytes != 1 && value_bytes != 2 && value_bytes != 4) || !sort_sizes_ok(T, top_k, E) || H <= 0 || H > kMaxInner ||
+        ldx < H || ldr < H || ldx > kMaxPitch || ldr > kMaxPitch || first_expert < 0)
+        return MSE_ERR_INVALID_ARG;
+    const int64_t pairs = T * top_k;
+    if (rows_capacity < (pairs - 1) * ldr + H) return MSE_ERR_GEOMETRY;
+    if (!disjoint(x, span(T, H, ldx, value_bytes), rows, span(pairs, H, ldr, value_bytes))) return MSE_ERR_INVALID_ARG;
+    if (!workspace || workspace_bytes < sort_ws(T, top_k, E) || !aligned256(workspace)) return MSE_ERR_WORKSPACE;
+    DeviceView d;
+    const mse_status st = device_view(&d);
+    if (st != MSE_OK) return st;
+    begin_untracked_call(stream);
+    SortParams p;
+    std::memset(&p, 0, sizeof p);
+    p.x = static_cast<const uint8_t *>(x); p.T = T; p.row_bytes = H * value_bytes; p.ldx = ldx * value_bytes;
+    p.ids = ids; p.top_k = top_k; p.first_expert = first_expert; p.E = (int)E;
+    p.scales = scales;
+    p.rows = static_cast<uint8_t *>(rows); p.ldr = ldr * value_bytes;
+    p.row_scales = row_scales;
+    p.place = place; p.offsets = offsets;
+    p.chunk = chunk_of(T, top_k);
+    p.n_chunks = (int)((T + p.chunk - 1) / p.chunk);
+    if (pairs > kCountAllPairs) p.hist = static_cast<int *>(workspace);
+    const uint64_t bits = reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(rows) | (uint64_t)p.ldx |
+                          (uint64_t)p.ldr | (uint64_t)p.row_bytes | 16u;
+    p.unit = (int)(bits & (~bits + 1));
+    // the copies of a chunk over several CTAs, up to eight an SM, of 1 KB for each warp at least
+    p.splits = (int)std::max<int64_t>(1, std::min<int64_t>((p.row_bytes * p.chunk + 8191) / 8192, 8 * d.sm_count / p.n_chunks));
+    return from_cuda(launch_sort(p, pdl_enabled(), static_cast<cudaStream_t>(stream)));
+}
+
+mse_status moe_unsort(const void *rows, mse_dtype rows_dtype, int64_t n_rows, int64_t ldr, const int32_t *place,
+                      const float *weights, int64_t T, int64_t H, int top_k, const void *base, void *y, mse_dtype y_dtype,
+                      int64_t y_capacity, void *stream) {
+    if (!rows || !place || !y || !dtype_ok(rows_dtype) || !dtype_ok(y_dtype) || T <= 0 || H <= 0 || top_k <= 0 ||
+        n_rows <= 0 || T > kMaxRows || n_rows > kMaxRows || H > kMaxInner || top_k > MSE_ROUTE_MAX_TOP_K || ldr < H ||
+        ldr > kMaxPitch)
+        return MSE_ERR_INVALID_ARG;
+    if (y_capacity < T * H) return MSE_ERR_GEOMETRY;
+    const int64_t y_bytes = T * H * size_of(y_dtype);
+    if (!disjoint(rows, span(n_rows, H, ldr, size_of(rows_dtype)), y, y_bytes) ||
+        (base && base != y && !disjoint(base, y_bytes, y, y_bytes)))
+        return MSE_ERR_INVALID_ARG;
+    DeviceView d;
+    const mse_status st = device_view(&d);
+    if (st != MSE_OK) return st;
+    begin_untracked_call(stream);
+    UnsortParams p;
+    p.rows = rows; p.n_rows = n_rows; p.ldr = ldr;
+    p.place = place; p.weights = weights; p.top_k = top_k;
+    p.base = base; p.y = y; p.T = T; p.H = H;
+    p.rows_f32 = rows_dtype == MSE_F32; p.y_f32 = y_dtype == MSE_F32;
+    return from_cuda(launch_unsort(p, d.sm_count, pdl_enabled(), static_cast<cudaStream_t>(stream)));
+}
+
+mse_status moe_unsort_backward(const void *dy, mse_dtype dy_dtype, const int32_t *place, const float *weights,
+                               const void *rows, mse_dtype rows_dtype, int64_t ldr, int64_t n_rows, int64_t T, int64_t H,
+                               int top_k, void *drows, int64_t ldd, int64_t drows_capacity, float *dweights, void *stream) {
+    if (!dy || !place || !drows || !dtype_ok(dy_dtype) || !dtype_ok(rows_dtype) || (weights != nullptr) != (dweights != nullptr) ||
+        (weights && (!rows || ldr < H || ldr > kMaxPitch)) || T <= 0 || H <= 0 || top_k <= 0 || n_rows <= 0 || T > kMaxRows ||
+        n_rows > kMaxRows || H > kMaxInner || top_k > MSE_ROUTE_MAX_TOP_K || ldd < H || ldd > kMaxPitch)
+        return MSE_ERR_INVALID_ARG;
+    if (drows_capacity < (n_rows - 1) * ldd + H) return MSE_ERR_GEOMETRY;
+    const int64_t size = size_of(rows_dtype), drows_bytes = span(n_rows, H, ldd, size);
+    if (!disjoint(dy, T * H * size_of(dy_dtype), drows, drows_bytes) ||
+        (weights && !(rows == drows && ldr == ldd) && !disjoint(rows, span(n_rows, H, ldr, size), drows, drows_bytes)))
+        return MSE_ERR_INVALID_ARG;
+    DeviceView d;
+    const mse_status st = device_view(&d);
+    if (st != MSE_OK) return st;
+    begin_untracked_call(stream);
+    UnsortBackwardParams p;
+    p.dy = dy; p.place = place; p.weights = weights;
+    p.rows = weights ? rows : nullptr; p.ldr = weights ? ldr : ldd;
+    p.top_k = top_k;
+    p.drows = drows; p.ldd = ldd; p.n_rows = n_rows;
+    p.dweights = dweights;
+    p.T = T; p.H = H;
+    p.dy_f32 = dy_dtype == MSE_F32; p.rows_f32 = rows_dtype == MSE_F32;
+    return from_cuda(launch_unsort_backward(p, d.sm_count, pdl_enabled(), static_cast<cudaStream_t>(stream)));
+}
+
+mse_status int8_quantise(const void *x, mse_dtype x_dtype, int64_t rows, int64_t K, int64_t ldx, int swiglu,
+                         const int32_t *last, int8_t *q, int64_t ldq, int64_t q_capacity, float *scales, void *stream) {
+    const int64_t width = swiglu ? 2 * K : K;
+    if (!x || !q || !scales || !dtype_ok(x_dtype) || rows <= 0 || K <= 0 || rows > kMaxRows || K > kMaxInner || ldx < width ||
+        ldq < K || ldx > kMaxPitch || ldq > kMaxPitch)
+        return MSE_ERR_INVALID_ARG;
+    if (q_capacity < (rows - 1) * ldq + K) return MSE_ERR_GEOMETRY;
+    if (!disjoint(x, span(rows, width, ldx, size_of(x_dtype)), q, span(rows, K, ldq, 1))) return MSE_ERR_INVALID_ARG;
+    DeviceView d;
+    const mse_status st = device_view(&d);
+    if (st != MSE_OK) return st;
+    begin_untracked_call(stream);
+    RoundParams p;
+    p.x = x; p.rows = rows; p.K = K; p.ldx = ldx;
+    p.f32 = x_dtype == MSE_F32; p.swiglu = swiglu != 0;
+    p.last = last;
+    p.q = q; p.ldq = ldq; p.half_out = 0; p.scales = scales;
+    return from_cuda(launch_int8_round(p, d.sm_count, pdl_enabled(), static_cast<cudaStream_t>(stream)));
+}
+
+size_t int8_workspace_bytes(int64_t T, int64_t N, int64_t K, int64_t groups) {
+    return int8_sizes_ok(T, N, K, groups) ? int8_ws(T, K).total : 0;
+}
+
+mse_status int8_matmul(const int8_t *xq, int64_t ldx, const float *xs, const int8_t *wq, int64_t ldw, const float *ws, int64_t T,
+                       int64_t N, int64_t K, void *out, mse_dtype out_dtype, int64_t out_capacity, void *workspace,
+                       size_t workspace_bytes, void *stream) {
+    mse_status st = check_product(xq, ldx, xs, wq, ldw, ws, T, N, K, 1, out, out_dtype, out_capacity, workspace, workspace_bytes);
+    if (st != MSE_OK) return st;
+    const Int8Gemm g = product(xq, ldx, xs, nullptr, 1, wq, ldw, ws, T, N, K, out, out_dtype);
+    if (!apart(g)) return MSE_ERR_INVALID_ARG;
+    DeviceView d;
+    if ((st = device_view(&d)) != MSE_OK) return st;
+    begin_untracked_call(stream);
+    return run_product(g, d, static_cast<cudaStream_t>(stream));
+}
+
+mse_status int8_grouped_matmul(const int8_t *xq, int64_t ldx, const float *xs, const int32_t *offsets, int64_t groups,
+                               const int8_t *wq, int64_t ldw, const float *ws, int64_t T, int64_t N, int64_t K, void *out,
+                               mse_dtype out_dtype, int64_t out_capacity, void *workspace, size_t workspace_bytes,
+                               void *stream) {
+    if (!offsets) return MSE_ERR_INVALID_ARG;
+    mse_status st =
+        check_product(xq, ldx, xs, wq, ldw, ws, T, N, K, groups, out, out_dtype, out_capacity, workspace, workspace_bytes);
+    if (st != MSE_OK) return st;
+    const Int8Gemm g = product(xq, ldx, xs, offsets, groups, wq, ldw, ws, T, N, K, out, out_dtype);
+    if (!apart(g)) return MSE_ERR_INVALID_ARG;
+    DeviceView d;
+    if ((st = device_view(&d)) != MSE_OK) return st;
+    begin_untracked_call(stream);
+    return run_product(g, d, static_cast<cudaStream_t>(stream));
+}
+
+mse_status int8_linear(const void *x, mse_dtype x_dtype, int64_t ldx, const int8_t *wq, int64_t ldw, const float *ws, int64_t T,
+                       int64_t N, int64_t K, void *y, mse_dtype y_dtype, int64_t y_capacity, void *workspace,
+                       size_t workspace_bytes, void *stream) {
+    if (!dtype_ok(x_dtype)) return MSE_ERR_INVALID_ARG;
+    mse_status st = check_product(x, ldx, ws, wq, ldw, ws, T, N, K, 1, y, y_dtype, y_capacity, workspace, workspace_bytes);
+    if (st != MSE_OK) return st;
+    DeviceView d;
+    if ((st = device_view(&d)) != MSE_OK) return st;
+    begin_untracked_call(stream);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const Int8Ws L = int8_ws(T, K);
+    int8_t *q = static_cast<int8_t *>(workspace) + L.q_off;
+    float *xs = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + L.s_off);
+    RoundParams p;
+    p.x = x; p.rows = T; p.K = K; p.ldx = ldx;
+    p.f32 = x_dtype == MSE_F32; p.swiglu = 0;
+    p.last = nullptr;
+    p.q = q; p.ldq = (K + 15) / 16 * 16; p.half_out = 0; p.scales = xs;
+    if ((st = from_cuda(launch_int8_round(p, d.sm_count, pdl_enabled(), s))) != MSE_OK) return st;
+    return run_product(product(q, p.ldq, xs, nullptr, 1, wq, ldw, ws, T, N, K, y, y_dtype), d, s);
+}
+
+}  // extern "C"

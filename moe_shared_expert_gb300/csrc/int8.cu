@@ -1,7 +1,7 @@
 // Rounding of rows to 8-bit integers, and the generic (CUDA-core) product that serves any size, pitch and alignment.
 #include <cuda_fp16.h>
 
-#include "int8.cuh"
+#include "int8_tc.cuh"
 #include "launch.h"
 #include "sorted.h"
 
@@ -55,6 +55,42 @@ __global__ void __launch_bounds__(kRoundThreads) round_rows_kernel(const RoundPa
 }
 
 // ---------------------------------------------------------------------------
+// int8 rows to the same integers in fp16, for the tensor-core kernels
+// ---------------------------------------------------------------------------
+// 16 values a thread; WIDE: rows begin at multiples of 16 bytes (out's always do)
+template <bool WIDE>
+__global__ void __launch_bounds__(256) expand_kernel(const int8_t *x, int64_t ldx, int64_t rows, int64_t K, const int32_t *last,
+                                                     uint16_t *out, int64_t ldo) {
+    pdl_wait();
+    pdl_launch_dependents();
+    if (last) rows = min((int64_t)max(*last, 0), rows);
+    const int64_t per = (K + 15) / 16, items = rows * per;
+    for (int64_t it = (int64_t)blockIdx.x * 256 + threadIdx.x; it < items; it += (int64_t)gridDim.x * 256) {
+        const int64_t r = it / per, k = (it - r * per) * 16;
+        const int8_t *src = x + r * ldx + k;
+        uint32_t w[4], h[8];
+        if (WIDE && k + 16 <= K) {
+            const uint4 v = *reinterpret_cast<const uint4 *>(src);
+            w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                w[i] = 0;
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (k + 4 * i + j < K) w[i] |= (uint32_t)(uint8_t)src[4 * i + j] << (8 * j);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) half_of_bytes(w[i], h[2 * i], h[2 * i + 1]);
+        // (out's pitch is a multiple of 64 values: a run that begins inside a row is written whole)
+        uint4 *dst = reinterpret_cast<uint4 *>(out + r * ldo + k);
+        dst[0] = make_uint4(h[0], h[1], h[2], h[3]);
+        dst[1] = make_uint4(h[4], h[5], h[6], h[7]);
+    }
+}
+
+// ---------------------------------------------------------------------------
 // generic product: 16 token rows x 16 weight rows per CTA, one thread per output
 // ---------------------------------------------------------------------------
 constexpr int kSimtRows = 16, kSimtInner = 64;
@@ -102,6 +138,13 @@ cudaError_t launch_int8_round(const RoundParams &p, int sm_count, bool pdl, cuda
     };
     if (p.f32) return p.swiglu ? with(std::true_type(), std::true_type()) : with(std::true_type(), std::false_type());
     return p.swiglu ? with(std::false_type(), std::true_type()) : with(std::false_type(), std::false_type());
+}
+
+cudaError_t launch_int8_expand(const int8_t *x, int64_t ldx, int64_t rows, int64_t K, const int32_t *last, uint16_t *out,
+                               int64_t ldo, int sm_count, bool pdl, cudaStream_t s) {
+    const dim3 grid((unsigned)std::min<int64_t>((rows * ((K + 15) / 16) + 255) / 256, (int64_t)sm_count * 8));
+    const bool wide = ((reinterpret_cast<uintptr_t>(x) | (uint64_t)ldx) & 15u) == 0;
+    return launch_kernel(wide ? expand_kernel<true> : expand_kernel<false>, grid, 256, 0, pdl, 1, s, x, ldx, rows, K, last, out, ldo);
 }
 
 cudaError_t launch_int8_simt(const Int8Gemm &g, bool pdl, cudaStream_t s) {

@@ -1,0 +1,323 @@
+// Product in 8-bit integers for few token rows: weights fill the 128-row side of the MMA, up to 128 tokens are its columns.
+//
+// A CTA owns one 128-row weight tile and one token tile; the k-blocks may be split over a cluster, whose CTAs exchange their
+// integer sums through distributed shared memory and each finish a slice of the token columns.
+//
+// Warp 0 loads (TMA), warp 1 issues MMAs, warps 2-5 convert weights (int8_tc.cuh), warps 6-9 add the chunks' sums.
+#include <atomic>
+
+#include "device.h"
+#include "int8_tc.cuh"
+#include "launch.h"
+
+namespace mse {
+namespace sorted {
+namespace {
+
+constexpr int kMaxStages = 10;
+constexpr int kColsThreads = 32 * 10;
+
+constexpr int pow2_at_least(int v) {
+    int p = 32;
+    while (p < v) p <<= 1;
+    return p;
+}
+
+struct ColsCtrl {
+    uint64_t full[kMaxStages], empty[kMaxStages], afull[4], aempty[4], dfull[2], dempty[2], drain;
+    uint32_t tmem_base;
+    int abort_flag;
+};
+
+template <int BN_>
+struct Cols {
+    static constexpr int BN = BN_;
+    static constexpr int CTAS = BN <= 64 ? 2 : 1;                        // resident per SM
+    static constexpr int NA = BN <= 32 ? 3 : BN == 64 ? 2 : 4;           // k-blocks of weights in TMEM
+    static constexpr int TMEM = pow2_at_least(2 * BN + NA * (int)kATmem);
+    static_assert(CTAS * TMEM <= 512, "TMEM");
+    static constexpr uint32_t TOKENS = BN * kInner * 2;                  // two tiles of 64 k
+    static constexpr uint32_t STAGE = kWeightTile + TOKENS;
+    static constexpr uint32_t FIXED = 1024 + sizeof(ColsCtrl) + 64;
+    static constexpr int fit(uint32_t budget) {
+        const int n = (int)((budget - FIXED) / STAGE);
+        return n < kMaxStages ? n : kMaxStages;
+    }
+    // stages of the ring with CTAS CTAs on an SM, or one
+    static constexpr int PART = fit((CTAS == 2 ? 113 : 227) * 1024), WHOLE = fit(227 * 1024);
+    // the exchange of a split tile uses the ring: at most BN / 4 + 7 groups of four columns
+    static_assert((BN / 4 + 7) * 2048 <= PART * STAGE, "exchange");
+};
+
+template <typename C>
+__global__ void __launch_bounds__(kColsThreads, C::CTAS)
+    int8_cols_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX, const Int8Gemm g,
+                     const int kb_total, const int stream_weights, const int S) {
+    constexpr int BN = C::BN;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
+    uint8_t *ring = smem_raw + (base - raw);
+    ColsCtrl *ctl = reinterpret_cast<ColsCtrl *>(ring + (size_t)S * C::STAGE);
+    const int warp = __shfl_sync(~0u, (int)threadIdx.x / 32, 0), lane = threadIdx.x % 32;
+    const int part = blockIdx.x, parts = gridDim.x, m = blockIdx.z;
+    const int kb0 = (int)((int64_t)kb_total * part / parts), n = (int)((int64_t)kb_total * (part + 1) / parts) - kb0;
+    volatile int *abort_flag = &ctl->abort_flag;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < S; ++s) {
+            mbar_init(smem_u32(&ctl->full[s]), 1);
+            mbar_init(smem_u32(&ctl->empty[s]), 1);
+        }
+        for (int a = 0; a < C::NA; ++a) {
+            mbar_init(smem_u32(&ctl->afull[a]), 4);
+            mbar_init(smem_u32(&ctl->aempty[a]), 1);
+        }
+        for (int d = 0; d < 2; ++d) {
+            mbar_init(smem_u32(&ctl->dfull[d]), 1);
+            mbar_init(smem_u32(&ctl->dempty[d]), 4);
+        }
+        mbar_init(smem_u32(&ctl->drain), 1);
+        ctl->abort_flag = 0;
+        fence_barrier_init();
+        tma_prefetch_desc(&tmW);
+        tma_prefetch_desc(&tmX);
+    }
+    if (warp == 1) {
+        tmem_alloc(smem_u32(&ctl->tmem_base), C::TMEM);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem_base = __shfl_sync(~0u, ctl->tmem_base, 0), tmem_a = tmem_base + 2 * BN;
+    // The kernel before this one, of the same call, let this one start after its own wait: weights and offsets are complete,
+    // and only the tokens are that kernel's.
+    RowTile t;
+    const bool active = row_tile(g.offsets, g.groups, g.T, BN, blockIdx.y, t);
+    if (!active || warp >= 2) pdl_wait();   // (a CTA without a tile too: the grid may not be over before the kernel before it)
+
+    int issued = 0;
+    if (active && warp == 0) {
+        const bool el = elected();
+        const int w_row = t.group * (int)g.N + m * 128;
+        const uint64_t pol_w = stream_weights ? l2_policy_evict_first() : l2_policy_evict_last();
+        const uint64_t pol_x = l2_policy_evict_last();
+        auto weights = [&](int s, int kb) {
+            const uint32_t bar = smem_u32(&ctl->full[s]);
+            mbar_arrive_expect_tx(bar, C::STAGE);
+            tma_load_2d(base + s * C::STAGE, &tmW, bar, kb * kInner, w_row, pol_w);
+        };
+        auto tokens = [&](int s, int kb) {
+            const uint32_t bar = smem_u32(&ctl->full[s]), dst = base + s * C::STAGE + kWeightTile;
+            tma_load_2d(dst, &tmX, bar, kb * 2 * kInner, t.row0, pol_x);   // coordinates in bytes
+            tma_load_2d(dst + C::TOKENS / 2, &tmX, bar, kb * 2 * kInner + kInner, t.row0, pol_x);
+        };
+        const int pre = min(S, n);
+        for (int i = 0; i < pre; ++i)
+            if (el) weights(i, kb0 + i);
+        pdl_wait();
+        for (int i = 0; i < pre; ++i)
+            if (el) tokens(i, kb0 + i);
+        __syncwarp();
+        issued = pre;
+        uint32_t phase = 0;
+        for (int i = pre, s = 0; i < n; ++i, ++issued) {
+            if (!wait_all(smem_u32(&ctl->empty[s]), phase, abort_flag, g)) break;
+            if (el) {
+                weights(s, kb0 + i);
+                tokens(s, kb0 + i);
+            }
+            __syncwarp();
+            if (++s == S) { s = 0; phase ^= 1u; }
+        }
+    } else if (active && warp == 1) {
+        const bool el = elected();
+        const uint32_t idesc = idesc_f16_f32(128, BN);
+        uint32_t phase = 0, aphase = 0;
+        for (int i = 0, s = 0, a = 0; i < n; ++i) {
+            const int chunk = i / kChunkBlocks, d = chunk & 1, in = i % kChunkBlocks;
+            if (!wait_all(smem_u32(&ctl->full[s]), phase, abort_flag, g) ||
+                !wait_all(smem_u32(&ctl->afull[a]), aphase, abort_flag, g) ||
+                (in == 0 && !wait_all(smem_u32(&ctl->dempty[d]), (uint32_t)((chunk >> 1) & 1) ^ 1u, abort_flag, g)))
+                break;
+            tc_fence_after();
+            const uint32_t x = base + s * C::STAGE + kWeightTile;
+            if (el) {
+#pragma unroll
+                for (int kk = 0; kk < kInner / 16; ++kk)
+                    tc_mma_f16_ts(tmem_base + (uint32_t)(d * BN), tmem_a + (uint32_t)(a * kATmem + kk * 8),
+                                  smem_desc_sw128(x + (kk / 4) * (C::TOKENS / 2)) + (uint64_t)(kk % 4 * 2), idesc,
+                                  in > 0 || kk > 0 ? 1u : 0u);
+                tc_commit(smem_u32(&ctl->empty[s]));
+                tc_commit(smem_u32(&ctl->aempty[a]));
+                if (in == kChunkBlocks - 1 || i == n - 1) tc_commit(smem_u32(&ctl->dfull[d]));
+            }
+            __syncwarp();
+            if (++s == S) { s = 0; phase ^= 1u; }
+            if (++a == C::NA) { a = 0; aphase ^= 1u; }
+        }
+    } else if (active && warp >= 2 && warp < 6) {
+        const int q = warp & 3, row = q * 32 + lane;
+        uint32_t phase = 0, aphase = 0;
+        for (int i = 0, s = 0, a = 0; i < n; ++i) {
+            if (!wait_all(smem_u32(&ctl->full[s]), phase, abort_flag, g) ||
+                !wait_all(smem_u32(&ctl->aempty[a]), aphase ^ 1u, abort_flag, g))
+                break;
+            tc_fence_after();
+            convert_rows(ring + (size_t)s * C::STAGE, row, tmem_a + (uint32_t)(a * kATmem) + ((uint32_t)(q * 32) << 16));
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&ctl->afull[a]));
+            if (++s == S) { s = 0; phase ^= 1u; }
+            if (++a == C::NA) { a = 0; aphase ^= 1u; }
+        }
+        __syncwarp();
+    }
+
+    int acc[BN];
+    const bool adds = warp >= 6;
+    const int q = warp & 3, row = q * 32 + lane;
+    if (active && adds) {
+#pragma unroll
+        for (int c = 0; c < BN; ++c) acc[c] = 0;
+        const int chunks = (n + kChunkBlocks - 1) / kChunkBlocks;
+        for (int i = 0; i < chunks; ++i) {
+            const int d = i & 1;
+            if (!wait_all(smem_u32(&ctl->dfull[d]), (uint32_t)((i >> 1) & 1), abort_flag, g)) break;
+            tc_fence_after();
+            const uint32_t src = tmem_base + (uint32_t)(d * BN) + ((uint32_t)(q * 32) << 16);
+#pragma unroll
+            for (int c = 0; c < BN; c += 16) {
+                uint32_t v[16];
+                tmem_ld16(src + c, v);
+                tmem_ld_wait();
+#pragma unroll
+                for (int j = 0; j < 16; ++j) acc[c + j] += __float2int_rn(__uint_as_float(v[j]));
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&ctl->dempty[d]));
+        }
+        __syncwarp();
+    }
+
+    // ---- the cluster's sums: every CTA gets a slice of the token columns from all, in groups of four: [part][group][row]
+    int4 *red = reinterpret_cast<int4 *>(ring);
+    const int slice = (BN / 4 + parts - 1) / parts;
+    if (parts > 1) {
+        cluster_sync();   // every ring of the cluster is idle
+        if (active && adds) {
+#pragma unroll
+            for (int c = 0; c < BN; c += 4)
+                if (c < t.rows) {
+                    const int to = c / 4 / slice, at = c / 4 - to * slice;
+                    st_cluster_s32x4(map_to_rank(smem_u32(red + (size_t)(part * slice + at) * 128 + row), (uint32_t)to),
+                                     make_int4(acc[c], acc[c + 1], acc[c + 2], acc[c + 3]));
+                }
+        }
+        cluster_sync();
+    }
+    if (active && adds) {
+        const int64_t out_n = (int64_t)m * 128 + row;
+        if (out_n < g.N) {
+            const float w = g.ws[(int64_t)t.group * g.N + out_n];
+            auto store = [&](int col, int sum) {
+                const float y = (float)sum * g.xs[t.row0 + col] * w;
+                const int64_t at = (int64_t)(t.row0 + col) * g.N + out_n;
+                if (g.out_f32)
+                    static_cast<float *>(g.out)[at] = y;
+                else
+                    static_cast<uint16_t *>(g.out)[at] = f32_to_bf16_bits(y);
+            };
+            if (parts == 1) {
+#pragma unroll
+                for (int c = 0; c < BN; ++c)
+                    if (c < t.rows) store(c, acc[c]);
+            } else {
+                const int first = part * slice, mine = min(min(slice, BN / 4 - first), (t.rows + 3) / 4 - first);
+                for (int at = 0; at < mine; ++at) {
+                    int4 v = make_int4(0, 0, 0, 0);
+                    for (int r = 0; r < parts; ++r) {
+                        const int4 o = red[(size_t)(r * slice + at) * 128 + row];
+                        v = make_int4(v.x + o.x, v.y + o.y, v.z + o.z, v.w + o.w);
+                    }
+                    const int col = (first + at) * 4, each[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (col + j < t.rows) store(col + j, each[j]);
+                }
+            }
+        }
+    }
+
+    // ---- teardown: nothing in flight (after an abort: bounded waits), then the TMEM goes back
+    if (warp == 0 && lane == 0) {
+        for (int i = max(0, issued - S); i < issued; ++i)
+            if (!mbar_wait_drain(smem_u32(&ctl->full[i % S]), (uint32_t)((i / S) & 1), drain_limit_of(g.wait_limit_ns)))
+                __nanosleep(200000);
+    }
+    if (warp == 1 && lane == 0) {
+        tc_commit(smem_u32(&ctl->drain));
+        (void)mbar_wait_drain(smem_u32(&ctl->drain), 0, drain_limit_of(g.wait_limit_ns));
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc(tmem_base, C::TMEM);
+}
+
+template <typename C>
+cudaError_t run(const CUtensorMap &tw, const CUtensorMap &tx, const Int8Gemm &g, int kb, int parts, int slots, int row_tiles,
+                int stream_weights, bool whole, bool pdl, cudaStream_t s) {
+    static std::atomic<uint64_t> done;   // bit per device
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (!(done.load(std::memory_order_acquire) >> (dev & 63) & 1)) {
+        e = cudaFuncSetAttribute(int8_cols_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+        if (e != cudaSuccess) return e;
+        done.fetch_or(1ull << (dev & 63), std::memory_order_acq_rel);
+    }
+    const int stages = whole ? C::WHOLE : C::PART;
+    return launch_kernel(int8_cols_kernel<C>, dim3((unsigned)parts, (unsigned)slots, (unsigned)row_tiles), kColsThreads,
+                         C::FIXED + (size_t)stages * C::STAGE, pdl, parts, s, tw, tx, g, kb, stream_weights, stages);
+}
+
+}  // namespace
+
+// CTAs that share a tile's k-blocks: as many as find room, two on an SM (one of 128 tokens), four k-blocks each at least.
+int int8_cols_parts(int64_t tiles, int kb, int tile_rows, int sm_count) {
+    const int64_t ctas = (tile_rows <= 64 ? 19 : 10) * (int64_t)sm_count / 10;
+    const int64_t room = std::min<int64_t>(ctas / std::max<int64_t>(1, tiles), kb / 4);
+    return (int)std::min<int64_t>(std::max<int64_t>(room, 1), 16 * tiles <= sm_count && kb >= 24 ? 8 : 5);
+}
+
+mse_status launch_int8_cols(const Int8Gemm &g, int tile_rows, int sm_count, bool pdl, cudaStream_t s) {
+    CUtensorMap tw, tx;
+    mse_status st = map_bytes(&tw, g.wq, g.groups * g.N, g.K, g.ldw, 128);
+    if (st != MSE_OK) return st;
+    if ((st = map_bytes(&tx, g.x16, g.T, g.K * 2, g.ldx16 * 2, tile_rows)) != MSE_OK) return st;
+    const int kb = (int)((g.K + kInner - 1) / kInner);
+    const int64_t row_tiles = (g.N + 127) / 128, per = (g.T + tile_rows - 1) / tile_rows;
+    // grouped: every group may begin a tile of its own; as many as there are rows at most
+    const int64_t slots = g.offsets ? std::min<int64_t>(g.T, g.T / tile_rows + std::min<int64_t>(g.groups, g.T)) : per;
+    if (row_tiles > 65535 || slots > 65535) return MSE_ERR_UNSUPPORTED_SHAPE;
+    const int parts = int8_cols_parts(row_tiles * slots, kb, tile_rows, sm_count);
+    const int stream_weights = slots == 1 || (g.offsets && g.T <= (int64_t)tile_rows * g.groups);
+    const bool whole = parts == 1 && row_tiles * slots <= sm_count;
+    cudaError_t e;
+    auto with = [&](auto c) {
+        return run<decltype(c)>(tw, tx, g, kb, parts, (int)slots, (int)row_tiles, stream_weights, whole, pdl, s);
+    };
+    switch (tile_rows) {
+        case 16: e = with(Cols<16>()); break;
+        case 32: e = with(Cols<32>()); break;
+        case 64: e = with(Cols<64>()); break;
+        default: e = with(Cols<128>()); break;
+    }
+    return e == cudaSuccess ? MSE_OK : MSE_ERR_CUDA;
+}
+
+}  // namespace sorted
+}  // namespace mse

@@ -73,7 +73,8 @@ cudaError_t launch_int8_round(const RoundParams &p, int sm_count, bool pdl, cuda
 
 struct Int8Gemm {
     int64_t T;                                     // token rows (grouped: at most)
-    const int8_t *xq; int64_t ldx;                 // int8 rows
+    const int8_t *xq; int64_t ldx;                 // int8 rows (generic kernels)
+    const uint16_t *x16; int64_t ldx16;            // the same integers in fp16 (tensor-core kernels)
     const float *xs;
     const int32_t *offsets;                        // grouped: [groups + 1], else null
     int groups;
@@ -86,6 +87,12 @@ struct Int8Gemm {
     uint32_t *err;
 };
 cudaError_t launch_int8_simt(const Int8Gemm &g, bool pdl, cudaStream_t s);
+// int8 rows to the same integers in fp16; rows from *last on are left out
+cudaError_t launch_int8_expand(const int8_t *x, int64_t ldx, int64_t rows, int64_t K, const int32_t *last, uint16_t *out,
+                               int64_t ldo, int sm_count, bool pdl, cudaStream_t s);
+// Tensor-core kernel for token tiles of 16, 32, 64 or 128 rows (weights on the 128-row side).
+mse_status launch_int8_cols(const Int8Gemm &g, int tile_rows, int sm_count, bool pdl, cudaStream_t s);
+int int8_cols_parts(int64_t tiles, int kb, int tile_rows, int sm_count);
 
 }  // namespace sorted
 }  // namespace mse

@@ -77,11 +77,35 @@ mse_status check_product(const void *x, int64_t ldx, const void *xs, const void 
 bool apart(const Int8Gemm &g) {
     return disjoint(g.xq, span(g.T, g.K, g.ldx, 1), g.out, g.T * g.N * (g.out_f32 ? 4 : 2));
 }
+int64_t pitch16(int64_t K) { return (K + 63) / 64 * 64; }   // of tokens in fp16
 
-mse_status run_product(Int8Gemm g, const DeviceView &d, cudaStream_t s) {
+// Token rows of a tensor-core tile, by the rows expected of a group.
+int tile_rows_of(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128; }
+
+bool tensorcore_ok(const Int8Gemm &g) {
+    return (reinterpret_cast<uintptr_t>(g.wq) & 15u) == 0 && g.ldw % 16 == 0 && (g.N + 127) / 128 <= 65535 &&
+           g.T / 128 + g.groups <= 65535;
+}
+
+mse_status run_tensorcore(Int8Gemm g, const DeviceView &d, cudaStream_t s) {
     g.wait_limit_ns = wait_limit_ns();
     g.err = d.err;
-    return from_cuda(launch_int8_simt(g, pdl_enabled(), s));
+    return launch_int8_cols(g, tile_rows_of(g.T / g.groups), d.sm_count, pdl_enabled(), s);
+}
+
+// int8 rows: expanded to fp16 in the workspace for the tensor cores
+mse_status run_product(Int8Gemm g, const DeviceView &d, void *workspace, cudaStream_t s) {
+    bool tensorcore = false;
+    mse_status st = choose_tensorcore(tensorcore_ok(g), &tensorcore);
+    if (st != MSE_OK) return st;
+    if (!tensorcore) return from_cuda(launch_int8_simt(g, pdl_enabled(), s));
+    g.ldx16 = pitch16(g.K);
+    uint16_t *x16 = static_cast<uint16_t *>(workspace);
+    st = from_cuda(launch_int8_expand(g.xq, g.ldx, g.T, g.K, g.offsets ? g.offsets + g.groups : nullptr, x16, g.ldx16, d.sm_count,
+                                      pdl_enabled(), s));
+    if (st != MSE_OK) return st;
+    g.x16 = x16;
+    return run_tensorcore(g, d, s);
 }
 
 Int8Gemm product(const int8_t *xq, int64_t ldx, const float *xs, const int32_t *offsets, int64_t groups, const int8_t *wq,
@@ -222,7 +246,7 @@ mse_status int8_matmul(const int8_t *xq, int64_t ldx, const float *xs, const int
     DeviceView d;
     if ((st = device_view(&d)) != MSE_OK) return st;
     begin_untracked_call(stream);
-    return run_product(g, d, static_cast<cudaStream_t>(stream));
+    return run_product(g, d, workspace, static_cast<cudaStream_t>(stream));
 }
 
 mse_status int8_grouped_matmul(const int8_t *xq, int64_t ldx, const float *xs, const int32_t *offsets, int64_t groups,
@@ -238,7 +262,7 @@ mse_status int8_grouped_matmul(const int8_t *xq, int64_t ldx, const float *xs, c
     DeviceView d;
     if ((st = device_view(&d)) != MSE_OK) return st;
     begin_untracked_call(stream);
-    return run_product(g, d, static_cast<cudaStream_t>(stream));
+    return run_product(g, d, workspace, static_cast<cudaStream_t>(stream));
 }
 
 mse_status int8_linear(const void *x, mse_dtype x_dtype, int64_t ldx, const int8_t *wq, int64_t ldw, const float *ws, int64_t T,
@@ -252,15 +276,22 @@ mse_status int8_linear(const void *x, mse_dtype x_dtype, int64_t ldx, const int8
     begin_untracked_call(stream);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const Int8Ws L = int8_ws(T, K);
-    int8_t *q = static_cast<int8_t *>(workspace) + L.q_off;
     float *xs = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + L.s_off);
+    Int8Gemm g = product(nullptr, 0, xs, nullptr, 1, wq, ldw, ws, T, N, K, y, y_dtype);
+    bool tensorcore = false;
+    if ((st = choose_tensorcore(tensorcore_ok(g), &tensorcore)) != MSE_OK) return st;
     RoundParams p;
     p.x = x; p.rows = T; p.K = K; p.ldx = ldx;
     p.f32 = x_dtype == MSE_F32; p.swiglu = 0;
     p.last = nullptr;
-    p.q = q; p.ldq = (K + 15) / 16 * 16; p.half_out = 0; p.scales = xs;
+    p.q = workspace; p.ldq = pitch16(K); p.half_out = tensorcore; p.scales = xs;
     if ((st = from_cuda(launch_int8_round(p, d.sm_count, pdl_enabled(), s))) != MSE_OK) return st;
-    return run_product(product(q, p.ldq, xs, nullptr, 1, wq, ldw, ws, T, N, K, y, y_dtype), d, s);
+    if (tensorcore) {
+        g.x16 = static_cast<const uint16_t *>(workspace); g.ldx16 = p.ldq;
+        return run_tensorcore(g, d, s);
+    }
+    g.xq = static_cast<const int8_t *>(workspace); g.ldx = p.ldq;
+    return from_cuda(launch_int8_simt(g, pdl_enabled(), s));
 }
 
 }  // extern "C"

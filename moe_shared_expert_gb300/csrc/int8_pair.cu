@@ -1,0 +1,359 @@
+// Product in 8-bit integers for many token rows: a CTA pair (cta_group::2) owns 256 weight rows x 256 tokens.
+//
+// Each CTA converts the 128 weight rows of its own (int8_tc.cuh) and loads half of the tokens, in fp16.  The sums have 256 TMEM
+// columns, the converted weights the other 256 (four k-blocks).  A tile's tokens are two halves with barriers of their own: at the end
+// of a chunk of k-blocks one half's sums are read while the MMAs of the other half run.
+//
+// Warp 0 loads (TMA), warp 1 of the leading CTA issues MMAs, warps 4-7 convert weights, warps 8-15 add the chunks' sums and store.
+#include <atomic>
+
+#include "device.h"
+#include "int8_tc.cuh"
+#include "launch.h"
+
+namespace mse {
+namespace sorted {
+namespace {
+
+constexpr int kStages = 4, kSlots = 4;               // k-blocks in shared memory, and of weights in TMEM
+constexpr int kThreads = 512, kAddWarps = 8;
+// registers: 512 threads x 128 at launch = 128 x (40 + 56 + 208 + 208) afterwards
+constexpr int kLaunchRegs = 128;
+constexpr int kTokens = 256, kHalf = kTokens / 2;
+constexpr int kBand = 16;                            // token tiles whose weight tiles are taken in turn (L2 reuse)
+constexpr uint32_t kTokenBox = kHalf / 2 * 128;      // 64 tokens x 64 k, per CTA
+constexpr uint32_t kTokenBytes = 4 * kTokenBox;
+constexpr uint32_t kStage = kWeightTile + kTokenBytes;
+constexpr int kMaxGroups = MSE_ROUTE_MAX_EXPERTS;
+
+struct PairCtrl {
+    uint64_t wfull[kStages], xfull[kStages], empty[kStages], afull[kSlots], aempty[kSlots], dfull[2], dempty[2], drain;
+    uint32_t tmem_base;
+    int abort_flag, slots;
+    float xs[kAddWarps][kHalf];
+    int first[kMaxGroups], row0[kMaxGroups + 1];     // a group's first token tile, and its rows
+    int end[kMaxGroups];
+};
+constexpr size_t kSmem = kStages * (size_t)kStage + 1024 + sizeof(PairCtrl) + 64;
+static_assert(kSmem <= 227 * 1024, "shared memory");
+
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr));
+}
+
+// as mbar_wait_bounded, for a barrier on which both CTAs' threads arrive
+__device__ __forceinline__ bool wait_cluster(uint32_t bar, uint32_t parity, volatile int *abort_flag, const Int8Gemm &g) {
+    bool ok = mbar_try_wait_acq_cluster(bar, parity);
+    if (!ok) {
+        const uint64_t t0 = global_timer_ns();
+        while (!(ok = mbar_try_wait_acq_cluster(bar, parity))) {
+            if (*abort_flag) break;
+            if (global_timer_ns() - t0 > g.wait_limit_ns) {
+                *abort_flag = 1;
+                raise_device_error(g.err, DEV_ERR_TIMEOUT);
+                break;
+            }
+        }
+    }
+    return __all_sync(~0u, ok);
+}
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    int8_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX, const Int8Gemm g,
+                     const int kb, const int n_tiles_n) {
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
+    uint8_t *ring = smem_raw + (base - raw);
+    PairCtrl *ctl = reinterpret_cast<PairCtrl *>(ring + kStages * (size_t)kStage);
+    const int warp = __shfl_sync(~0u, (int)threadIdx.x / 32, 0), lane = threadIdx.x % 32;
+    const uint32_t rank = cluster_ctarank();
+    const bool leader = rank == 0;
+    const int64_t pair = blockIdx.x / 2, n_pairs = gridDim.x / 2;
+    volatile int *abort_flag = &ctl->abort_flag;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(smem_u32(&ctl->wfull[s]), 1);
+            mbar_init(smem_u32(&ctl->xfull[s]), 1);
+            mbar_init(smem_u32(&ctl->empty[s]), 1);
+        }
+        for (int a = 0; a < kSlots; ++a) {
+            mbar_init(smem_u32(&ctl->afull[a]), 8);     // the converting warps of both CTAs, on the leader's
+            mbar_init(smem_u32(&ctl->aempty[a]), 1);
+        }
+        for (int h = 0; h < 2; ++h) {
+            mbar_init(smem_u32(&ctl->dfull[h]), 1);
+            mbar_init(smem_u32(&ctl->dempty[h]), 8);    // four adding warps of either CTA, on the leader's
+        }
+        mbar_init(smem_u32(&ctl->drain), 1);
+        ctl->abort_flag = 0;
+        fence_barrier_init();
+        tma_prefetch_desc(&tmW);
+        tma_prefetch_desc(&tmX);
+    }
+    if (warp == 1) {
+        tmem_alloc_pair(smem_u32(&ctl->tmem_base), 512);
+        tmem_relinquish_pair();
+    }
+    // The kernel before this one, of the same call, let this one start after its own wait: the offsets are complete.
+    if (warp == 2) {
+        int before = 0;
+        for (int g0 = 0; g.offsets && g0 < g.groups; g0 += 32) {
+            const int i = g0 + lane;
+            const int64_t a = i < g.groups ? min(max((int64_t)g.offsets[i], (int64_t)0), g.T) : 0;
+            const int64_t b = i < g.groups ? min(max((int64_t)g.offsets[i + 1], (int64_t)0), g.T) : 0;
+            const int tiles = b > a ? (int)((b - a + kTokens - 1) / kTokens) : 0;
+            int upto = tiles;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int o = __shfl_up_sync(~0u, upto, d);
+                if (lane >= d) upto += o;
+            }
+            if (i < g.groups) {
+                ctl->first[i] = before + upto - tiles;
+                ctl->row0[i] = (int)a;
+                ctl->end[i] = (int)b;
+            }
+            before += __shfl_sync(~0u, upto, 31);
+        }
+        if (lane == 0) ctl->slots = g.offsets ? before : (int)((g.T + kTokens - 1) / kTokens);
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();   // the peer's barriers are initialised before any remote use
+    tc_fence_after();
+    const uint32_t tmem_base = __shfl_sync(~0u, ctl->tmem_base, 0), tmem_a = tmem_base + kTokens;
+    pdl_wait();
+
+    const int64_t slots = ctl->slots, total = slots * n_tiles_n;
+    // tile id -> token tile and weight tile n: bands of kBand token tiles, the token tile fastest
+    auto place = [&](int64_t id, RowTile &t, int &n) {
+        const int64_t per = (int64_t)kBand * n_tiles_n, band = id / per, in = id % per;
+        const int64_t wide = min((int64_t)kBand, slots - band * kBand);
+        const int z = (int)(band * kBand + in % wide);
+        n = (int)(in / wide);
+        int lo = 0, skip = z;
+        if (g.offsets) {
+            for (int hi = g.groups; hi - lo > 1;) {   // the last group whose first tile is not behind z
+                const int mid = (lo + hi) / 2;
+                if (ctl->first[mid] <= z) lo = mid; else hi = mid;
+            }
+            skip = z - ctl->first[lo];
+        }
+        t.group = lo;
+        t.row0 = (g.offsets ? ctl->row0[lo] : 0) + skip * kTokens;
+        t.rows = (int)min((int64_t)kTokens, (g.offsets ? ctl->end[lo] : g.T) - t.row0);
+    };
+
+    int64_t issued = 0;
+    if (warp < 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+        const bool el = elected();
+        int stage = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        if (warp == 0) {
+            for (int64_t id = pair; ok && id < total; id += n_pairs) {
+                RowTile t;
+                int n;
+                place(id, t, n);
+                const int w_row = t.group * (int)g.N + n * 256 + (int)rank * 128;
+                const int x_row = t.row0 + (int)rank * (kHalf / 2);
+                for (int k = 0; k < kb; ++k) {
+                    ok = wait_all(smem_u32(&ctl->empty[stage]), phase ^ 1u, abort_flag, g);
+                    if (!ok) break;
+                    if (el) {
+                        const uint32_t dst = base + stage * kStage, wb = smem_u32(&ctl->wfull[stage]);
+                        const uint32_t xb = map_to_rank(smem_u32(&ctl->xfull[stage]), 0);
+                        mbar_arrive_expect_tx(wb, kWeightTile);
+                        tma_load_2d_nohint(dst, &tmW, wb, k * kInner, w_row);
+                        if (leader) mbar_arrive_expect_tx(smem_u32(&ctl->xfull[stage]), 2 * kTokenBytes);
+#pragma unroll
+                        for (int b = 0; b < 4; ++b)   // half b / 2, 64 k from b % 2; coordinates in bytes
+                            tma_load_2d_pair(dst + kWeightTile + b * kTokenBox, &tmX, xb, k * 2 * kInner + (b % 2) * 128,
+                                             x_row + b / 2 * kHalf);
+                    }
+                    __syncwarp();
+                    ++issued;
+                    if (++stage == kStages) { stage = 0; phase ^= 1u; }
+                }
+            }
+        } else if (warp == 1 && leader) {
+            const uint32_t idesc = idesc_f16_f32(256, kHalf);
+            uint32_t aphase = 0, use = 0;   // use: chunks so far
+            int a = 0;
+            for (int64_t id = pair; ok && id < total; id += n_pairs) {
+                for (int k = 0; k < kb; ++k) {
+                    const int in = k % kChunkBlocks;
+                    const bool last = in == kChunkBlocks - 1 || k == kb - 1;
+                    ok = wait_all(smem_u32(&ctl->xfull[stage]), phase, abort_flag, g) &&
+                         wait_cluster(smem_u32(&ctl->afull[a]), aphase, abort_flag, g);
+                    if (!ok) break;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        if (in == 0) {
+                            ok = wait_cluster(smem_u32(&ctl->dempty[h]), (use & 1u) ^ 1u, abort_flag, g);
+                            if (!ok) break;
+                        }
+                        tc_fence_after();
+                        const uint32_t x = base + stage * kStage + kWeightTile + h * 2 * kTokenBox;
+                        if (el) {
+#pragma unroll
+                            for (int kk = 0; kk < kInner / 16; ++kk)
+                                tc_mma_f16_ts_pair(tmem_base + h * kHalf, tmem_a + (uint32_t)(a * kATmem + kk * 8),
+                                                   smem_desc_sw128(x + (kk / 4) * kTokenBox) + (uint64_t)(kk % 4 * 2), idesc,
+                                                   in > 0 || kk > 0 ? 1u : 0u);
+                            if (last) tc_commit_pair_multicast(smem_u32(&ctl->dfull[h]), 3);
+                        }
+                        __syncwarp();
+                    }
+                    if (!ok) break;
+                    if (el) {
+                        tc_commit_pair_multicast(smem_u32(&ctl->empty[stage]), 3);
+                        tc_commit_pair_multicast(smem_u32(&ctl->aempty[a]), 3);
+                    }
+                    __syncwarp();
+                    if (last) ++use;
+                    if (++stage == kStages) { stage = 0; phase ^= 1u; }
+                    if (++a == kSlots) { a = 0; aphase ^= 1u; }
+                }
+            }
+        }
+    } else if (warp < 8) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        const int q = warp & 3, row = q * 32 + lane;
+        int stage = 0, a = 0;
+        uint32_t phase = 0, aphase = 0;
+        bool ok = true;
+        for (int64_t id = pair; ok && id < total; id += n_pairs)
+            for (int k = 0; k < kb; ++k) {
+                ok = wait_all(smem_u32(&ctl->wfull[stage]), phase, abort_flag, g) &&
+                     wait_all(smem_u32(&ctl->aempty[a]), aphase ^ 1u, abort_flag, g);
+                if (!ok) break;
+                tc_fence_after();
+                convert_rows(ring + (size_t)stage * kStage, row, tmem_a + (uint32_t)(a * kATmem) + ((uint32_t)(q * 32) << 16));
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(map_to_rank(smem_u32(&ctl->afull[a]), 0));
+                if (++stage == kStages) { stage = 0; phase ^= 1u; }
+                if (++a == kSlots) { a = 0; aphase ^= 1u; }
+            }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+        const int q = warp & 3, row = q * 32 + lane, h = (warp - 8) / 4;
+        const uint32_t src = tmem_base + (uint32_t)(h * kHalf) + ((uint32_t)(q * 32) << 16);
+        const uint32_t empty = map_to_rank(smem_u32(&ctl->dempty[h]), 0);
+        float *xs = ctl->xs[warp - 8];
+        const int chunks = (kb + kChunkBlocks - 1) / kChunkBlocks;
+        uint32_t use = 0;
+        bool ok = true;
+        for (int64_t id = pair; ok && id < total; id += n_pairs) {
+            RowTile t;
+            int n;
+            place(id, t, n);
+            const int left = min(t.rows - h * kHalf, kHalf);   // tokens of this half
+            const int64_t first = (int64_t)t.row0 + h * kHalf, out_n = (int64_t)n * 256 + rank * 128 + row;
+            const float w = out_n < g.N ? g.ws[(int64_t)t.group * g.N + out_n] : 0.f;
+#pragma unroll
+            for (int i = 0; i < kHalf; i += 32) xs[i + lane] = i + lane < left ? g.xs[first + i + lane] : 0.f;
+            __syncwarp();
+            int acc[kHalf];
+#pragma unroll
+            for (int i = 0; i < kHalf; ++i) acc[i] = 0;
+            for (int c = 0; c < chunks; ++c, ++use) {
+                ok = wait_all(smem_u32(&ctl->dfull[h]), use & 1u, abort_flag, g);
+                if (!ok) break;
+                tc_fence_after();
+#pragma unroll
+                for (int i = 0; i < kHalf; i += 32) {
+                    uint32_t v[32];
+                    tmem_ld32(src + i, v);
+                    tmem_ld_wait();
+                    if (i + 32 == kHalf) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) arrive_cluster_relaxed(empty);
+                    }
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) acc[i + j] += __float2int_rn(__uint_as_float(v[j]));
+                }
+            }
+            if (!ok) break;
+            if (out_n < g.N) {
+                if (g.out_f32) {
+                    float *out = static_cast<float *>(g.out) + first * g.N + out_n;
+#pragma unroll
+                    for (int i = 0; i < kHalf; ++i)
+                        if (i < left) out[i * g.N] = (float)acc[i] * xs[i] * w;
+                } else {
+                    uint16_t *out = static_cast<uint16_t *>(g.out) + first * g.N + out_n;
+#pragma unroll
+                    for (int i = 0; i < kHalf; ++i)
+                        if (i < left) out[i * g.N] = f32_to_bf16_bits((float)acc[i] * xs[i] * w);
+                }
+            }
+            __syncwarp();
+        }
+        __syncwarp();
+    }
+
+    // ---- teardown: every issued stage is released by the leader's MMA commit once its bytes (of both CTAs) have landed and been
+    // used; after an abort the waits are bounded
+    if (warp == 0 && lane == 0) {
+        for (int64_t i = issued > kStages ? issued - kStages : 0; i < issued; ++i)
+            if (!mbar_wait_drain(smem_u32(&ctl->empty[i % kStages]), (uint32_t)((i / kStages) & 1),
+                                 drain_limit_of(g.wait_limit_ns)))
+                __nanosleep(200000);
+    }
+    if (warp == 1 && lane == 0 && leader) {
+        tc_commit_pair_multicast(smem_u32(&ctl->drain), 1);
+        (void)mbar_wait_drain(smem_u32(&ctl->drain), 0, drain_limit_of(g.wait_limit_ns));
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc_pair(tmem_base, 512);
+}
+
+// Opts the kernel into its shared memory once per device.
+cudaError_t prepare() {
+    static std::atomic<uint64_t> done;   // bit per device
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess || (done.load(std::memory_order_acquire) >> (dev & 63) & 1)) return e;
+    // the hand-over of registers needs the ones it was written for
+    cudaFuncAttributes at;
+    if ((e = cudaFuncGetAttributes(&at, int8_pair_kernel)) != cudaSuccess) return e;
+    if (at.numRegs < kLaunchRegs) return cudaErrorInvalidConfiguration;
+    e = cudaFuncSetAttribute(int8_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+    if (e == cudaSuccess) done.fetch_or(1ull << (dev & 63), std::memory_order_acq_rel);
+    return e;
+}
+
+}  // namespace
+
+mse_status launch_int8_pair(const Int8Gemm &g, int sm_count, bool pdl, cudaStream_t s) {
+    CUtensorMap tw, tx;
+    mse_status st = map_bytes(&tw, g.wq, g.groups * g.N, g.K, g.ldw, 128);
+    if (st != MSE_OK) return st;
+    if ((st = map_bytes(&tx, g.x16, g.T, g.K * 2, g.ldx16 * 2, kHalf / 2)) != MSE_OK) return st;
+    if (prepare() != cudaSuccess) return MSE_ERR_CUDA;
+    const int kb = (int)((g.K + kInner - 1) / kInner), n_tiles_n = (int)((g.N + 255) / 256);
+    const int64_t slots = (g.T + kTokens - 1) / kTokens + (g.offsets ? std::min<int64_t>(g.groups, g.T) : 0);
+    const int64_t pairs = std::min<int64_t>(sm_count / 2, slots * n_tiles_n);
+    const cudaError_t e = launch_kernel(int8_pair_kernel, dim3((unsigned)(2 * pairs)), kThreads, kSmem, pdl, 1, s, tw, tx, g, kb,
+                                        n_tiles_n);
+    return e == cudaSuccess ? MSE_OK : MSE_ERR_CUDA;
+}
+
+}  // namespace sorted
+}  // namespace mse

@@ -98,6 +98,12 @@ __device__ __forceinline__ uint64_t drain_limit_of(uint64_t wait_limit_ns) {
     return wait_limit_ns > 100000000ull ? wait_limit_ns : 100000000ull;
 }
 
+// Arrive on an mbarrier of a CTA of the cluster without ordering memory: it announces that TMEM was read (tcgen05.wait::ld and a
+// tcgen05 fence order that).  A release at cluster scope would wait for the thread's stores of the tile before.
+__device__ __forceinline__ void arrive_cluster_relaxed(uint32_t cluster_addr) {
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
 // 16 bytes to shared memory of a CTA of the cluster
 __device__ __forceinline__ void st_cluster_s32x4(uint32_t addr, int4 v) {
     asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)

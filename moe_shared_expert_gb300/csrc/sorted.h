@@ -92,6 +92,8 @@ cudaError_t launch_int8_expand(const int8_t *x, int64_t ldx, int64_t rows, int64
                                int64_t ldo, int sm_count, bool pdl, cudaStream_t s);
 // Tensor-core kernel for token tiles of 16, 32, 64 or 128 rows (weights on the 128-row side).
 mse_status launch_int8_cols(const Int8Gemm &g, int tile_rows, int sm_count, bool pdl, cudaStream_t s);
+// Tensor-core kernel for token tiles of 256 rows (a CTA pair per 256 x 256 tile).
+mse_status launch_int8_pair(const Int8Gemm &g, int sm_count, bool pdl, cudaStream_t s);
 int int8_cols_parts(int64_t tiles, int kb, int tile_rows, int sm_count);
 
 }  // namespace sorted

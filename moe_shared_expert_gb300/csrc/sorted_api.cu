@@ -80,7 +80,7 @@ bool apart(const Int8Gemm &g) {
 int64_t pitch16(int64_t K) { return (K + 63) / 64 * 64; }   // of tokens in fp16
 
 // Token rows of a tensor-core tile, by the rows expected of a group.
-int tile_rows_of(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128; }
+int tile_rows_of(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : rows <= 128 ? 128 : 256; }
 
 bool tensorcore_ok(const Int8Gemm &g) {
     return (reinterpret_cast<uintptr_t>(g.wq) & 15u) == 0 && g.ldw % 16 == 0 && (g.N + 127) / 128 <= 65535 &&
@@ -90,6 +90,7 @@ bool tensorcore_ok(const Int8Gemm &g) {
 mse_status run_tensorcore(Int8Gemm g, const DeviceView &d, cudaStream_t s) {
     g.wait_limit_ns = wait_limit_ns();
     g.err = d.err;
+    if (tile_rows_of(g.T / g.groups) == 256) return launch_int8_pair(g, d.sm_count, pdl_enabled(), s);
     return launch_int8_cols(g, tile_rows_of(g.T / g.groups), d.sm_count, pdl_enabled(), s);
 }
 

@@ -4,7 +4,9 @@
 // columns, the converted weights the other 256 (four k-blocks).  A tile's tokens are two halves with barriers of their own: at the end
 // of a chunk of k-blocks one half's sums are read while the MMAs of the other half run.
 //
-// Warp 0 loads (TMA), warp 1 of the leading CTA issues MMAs, warps 4-7 convert weights, warps 8-15 add the chunks' sums and store.
+// Warp 0 loads (TMA), warp 1 of the leading CTA issues MMAs.  Warps 4-7 and 8-11 convert the weights of every other k-block each, and
+// each has one half's sums: it reads them when a chunk ends, which is when it would next wait for room to convert into, and stores
+// a tile while two to four converted k-blocks are left for the MMAs.
 #include <atomic>
 
 #include "device.h"
@@ -16,9 +18,9 @@ namespace sorted {
 namespace {
 
 constexpr int kStages = 4, kSlots = 4;               // k-blocks in shared memory, and of weights in TMEM
-constexpr int kThreads = 512, kAddWarps = 8;
-// registers: 512 threads x 128 at launch = 128 x (40 + 56 + 208 + 208) afterwards
-constexpr int kLaunchRegs = 128;
+constexpr int kWorkWarps = 8, kThreads = 128 + 32 * kWorkWarps;
+// registers: 384 threads x 168 at launch >= 128 x 56 + 256 x 224 afterwards
+constexpr int kLaunchRegs = 168;
 constexpr int kTokens = 256, kHalf = kTokens / 2;
 constexpr int kBand = 16;                            // token tiles whose weight tiles are taken in turn (L2 reuse)
 constexpr uint32_t kTokenBox = kHalf / 2 * 128;      // 64 tokens x 64 k, per CTA
@@ -30,7 +32,7 @@ struct PairCtrl {
     uint64_t wfull[kStages], xfull[kStages], empty[kStages], afull[kSlots], aempty[kSlots], dfull[2], dempty[2], drain;
     uint32_t tmem_base;
     int abort_flag, slots;
-    float xs[kAddWarps][kHalf];
+    float xs[kWorkWarps][kHalf];
     int first[kMaxGroups], row0[kMaxGroups + 1];     // a group's first token tile, and its rows
     int end[kMaxGroups];
 };
@@ -85,12 +87,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             mbar_init(smem_u32(&ctl->empty[s]), 1);
         }
         for (int a = 0; a < kSlots; ++a) {
-            mbar_init(smem_u32(&ctl->afull[a]), 8);     // the converting warps of both CTAs, on the leader's
+            mbar_init(smem_u32(&ctl->afull[a]), 8);     // four warps of both CTAs, on the leader's
             mbar_init(smem_u32(&ctl->aempty[a]), 1);
         }
         for (int h = 0; h < 2; ++h) {
             mbar_init(smem_u32(&ctl->dfull[h]), 1);
-            mbar_init(smem_u32(&ctl->dempty[h]), 8);    // four adding warps of either CTA, on the leader's
+            mbar_init(smem_u32(&ctl->dempty[h]), 8);    // four warps of either CTA, on the leader's
         }
         mbar_init(smem_u32(&ctl->drain), 1);
         ctl->abort_flag = 0;
@@ -154,7 +156,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
     int64_t issued = 0;
     if (warp < 4) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
         const bool el = elected();
         int stage = 0;
         uint32_t phase = 0;
@@ -226,81 +228,94 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 }
             }
         }
-    } else if (warp < 8) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-        const int q = warp & 3, row = q * 32 + lane;
-        int stage = 0, a = 0;
-        uint32_t phase = 0, aphase = 0;
-        bool ok = true;
-        for (int64_t id = pair; ok && id < total; id += n_pairs)
-            for (int k = 0; k < kb; ++k) {
-                ok = wait_all(smem_u32(&ctl->wfull[stage]), phase, abort_flag, g) &&
-                     wait_all(smem_u32(&ctl->aempty[a]), aphase ^ 1u, abort_flag, g);
-                if (!ok) break;
-                tc_fence_after();
-                convert_rows(ring + (size_t)stage * kStage, row, tmem_a + (uint32_t)(a * kATmem) + ((uint32_t)(q * 32) << 16));
-                tmem_st_wait();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(map_to_rank(smem_u32(&ctl->afull[a]), 0));
-                if (++stage == kStages) { stage = 0; phase ^= 1u; }
-                if (++a == kSlots) { a = 0; aphase ^= 1u; }
-            }
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
-        const int q = warp & 3, row = q * 32 + lane, h = (warp - 8) / 4;
-        const uint32_t src = tmem_base + (uint32_t)(h * kHalf) + ((uint32_t)(q * 32) << 16);
-        const uint32_t empty = map_to_rank(smem_u32(&ctl->dempty[h]), 0);
-        float *xs = ctl->xs[warp - 8];
-        const int chunks = (kb + kChunkBlocks - 1) / kChunkBlocks;
-        uint32_t use = 0;
-        bool ok = true;
-        for (int64_t id = pair; ok && id < total; id += n_pairs) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+        const int q = warp & 3, row = q * 32 + lane, h = (warp - 4) / 4;
+        const uint32_t lanes = (uint32_t)(q * 32) << 16, src = tmem_base + (uint32_t)(h * kHalf) + lanes;
+        const uint32_t dempty = map_to_rank(smem_u32(&ctl->dempty[h]), 0);
+        float *xs = ctl->xs[warp - 4];
+        const int64_t tiles = total > pair ? (total - pair + n_pairs - 1) / n_pairs : 0, blocks = tiles * kb;
+        // the tile whose sums come next: its place, and its factors on their way
+        int64_t first = 0, out_n = 0;
+        int left = 0;
+        float xa[kHalf / 32], w = 0.f;
+        auto open = [&](int64_t id) {
+            if (id >= total) return;
             RowTile t;
             int n;
             place(id, t, n);
-            const int left = min(t.rows - h * kHalf, kHalf);   // tokens of this half
-            const int64_t first = (int64_t)t.row0 + h * kHalf, out_n = (int64_t)n * 256 + rank * 128 + row;
-            const float w = out_n < g.N ? g.ws[(int64_t)t.group * g.N + out_n] : 0.f;
+            left = min(t.rows - h * kHalf, kHalf);   // tokens of this half
+            first = (int64_t)t.row0 + h * kHalf;
+            out_n = (int64_t)n * 256 + rank * 128 + row;
+            w = out_n < g.N ? g.ws[(int64_t)t.group * g.N + out_n] : 0.f;
 #pragma unroll
-            for (int i = 0; i < kHalf; i += 32) xs[i + lane] = i + lane < left ? g.xs[first + i + lane] : 0.f;
-            __syncwarp();
-            int acc[kHalf];
+            for (int i = 0; i < kHalf / 32; ++i) xa[i] = i * 32 + lane < left ? g.xs[first + i * 32 + lane] : 0.f;
+        };
+        int64_t id = pair, end = min(kb, kChunkBlocks);   // end: the k-block behind the next chunk, counted over all tiles
+        int done = 0;                                     // k-blocks of the tile in chunks that were added
+        uint32_t use = 0;
+        bool ok = true;
+        int acc[kHalf];
 #pragma unroll
-            for (int i = 0; i < kHalf; ++i) acc[i] = 0;
-            for (int c = 0; c < chunks; ++c, ++use) {
+        for (int i = 0; i < kHalf; ++i) acc[i] = 0;
+        open(id);
+        for (int64_t i = h; ok; i += 2) {
+            while (ok && id < total && (end + 2 <= i || i >= blocks)) {
                 ok = wait_all(smem_u32(&ctl->dfull[h]), use & 1u, abort_flag, g);
                 if (!ok) break;
+                ++use;
                 tc_fence_after();
 #pragma unroll
-                for (int i = 0; i < kHalf; i += 32) {
+                for (int c = 0; c < kHalf; c += 32) {
                     uint32_t v[32];
-                    tmem_ld32(src + i, v);
+                    tmem_ld32(src + c, v);
                     tmem_ld_wait();
-                    if (i + 32 == kHalf) {
+                    if (c + 32 == kHalf) {
                         tc_fence_before();
                         __syncwarp();
-                        if (lane == 0) arrive_cluster_relaxed(empty);
+                        if (lane == 0) arrive_cluster_relaxed(dempty);
                     }
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) acc[i + j] += __float2int_rn(__uint_as_float(v[j]));
+                    for (int j = 0; j < 32; ++j) acc[c + j] += __float2int_rn(__uint_as_float(v[j]));
                 }
+                done += min(kb - done, kChunkBlocks);
+                if (done == kb) {
+#pragma unroll
+                    for (int j = 0; j < kHalf / 32; ++j) xs[j * 32 + lane] = xa[j];
+                    __syncwarp();
+                    if (out_n < g.N) {
+                        if (g.out_f32) {
+                            float *out = static_cast<float *>(g.out) + first * g.N + out_n;
+#pragma unroll
+                            for (int j = 0; j < kHalf; ++j)
+                                if (j < left) out[j * g.N] = (float)acc[j] * xs[j] * w;
+                        } else {
+                            uint16_t *out = static_cast<uint16_t *>(g.out) + first * g.N + out_n;
+#pragma unroll
+                            for (int j = 0; j < kHalf; ++j)
+                                if (j < left) out[j * g.N] = f32_to_bf16_bits((float)acc[j] * xs[j] * w);
+                        }
+                    }
+                    __syncwarp();
+#pragma unroll
+                    for (int j = 0; j < kHalf; ++j) acc[j] = 0;
+                    done = 0;
+                    id += n_pairs;
+                    open(id);
+                }
+                end += min(kb - done, kChunkBlocks);
             }
+            if (!ok || i >= blocks) break;
+            const int stage = (int)(i % kStages), a = (int)(i % kSlots);
+            ok = wait_all(smem_u32(&ctl->wfull[stage]), (uint32_t)(i / kStages) & 1u, abort_flag, g) &&
+                 wait_all(smem_u32(&ctl->aempty[a]), ((uint32_t)(i / kSlots) & 1u) ^ 1u, abort_flag, g);
             if (!ok) break;
-            if (out_n < g.N) {
-                if (g.out_f32) {
-                    float *out = static_cast<float *>(g.out) + first * g.N + out_n;
-#pragma unroll
-                    for (int i = 0; i < kHalf; ++i)
-                        if (i < left) out[i * g.N] = (float)acc[i] * xs[i] * w;
-                } else {
-                    uint16_t *out = static_cast<uint16_t *>(g.out) + first * g.N + out_n;
-#pragma unroll
-                    for (int i = 0; i < kHalf; ++i)
-                        if (i < left) out[i * g.N] = f32_to_bf16_bits((float)acc[i] * xs[i] * w);
-                }
-            }
+            tc_fence_after();
+            convert_rows(ring + (size_t)stage * kStage, row, tmem_a + (uint32_t)(a * kATmem) + lanes);
+            tmem_st_wait();
+            tc_fence_before();
             __syncwarp();
+            if (lane == 0) arrive_cluster(map_to_rank(smem_u32(&ctl->afull[a]), 0));
         }
         __syncwarp();
     }

@@ -104,6 +104,12 @@ __device__ __forceinline__ void arrive_cluster_relaxed(uint32_t cluster_addr) {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
+// The same with the release that an arrival has by default, of the CTA's scope: for what went to TMEM (tcgen05.wait::st and a
+// tcgen05 fence order it; a release at cluster scope takes several hundred cycles for every k-block).
+__device__ __forceinline__ void arrive_cluster(uint32_t cluster_addr) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
 // 16 bytes to shared memory of a CTA of the cluster
 __device__ __forceinline__ void st_cluster_s32x4(uint32_t addr, int4 v) {
     asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)

@@ -1,6 +1,8 @@
 // Rounding of rows to 8-bit integers, and the generic (CUDA-core) product that serves any size, pitch and alignment.
 #include <cuda_fp16.h>
 
+#include <type_traits>
+
 #include "int8_tc.cuh"
 #include "launch.h"
 #include "sorted.h"
@@ -12,45 +14,162 @@ namespace {
 // ---------------------------------------------------------------------------
 // a = max(max |r|, 2^-100),  scale = a / 127,  q = rint(127 r / a);  r = x or silu(gate) up
 // ---------------------------------------------------------------------------
+// A row's values stay in the registers of a warp (up to 1024) or of a CTA (up to 8192) between its amax and its rounding; longer
+// rows are read again.  Eight values of a thread are one load, of as many bytes as the rows' alignment lets a load have.
 constexpr int kRoundThreads = 256;
 
+// eight values at `at` of which `left` are there (the others 0), as they lie in memory: 4 words of bf16 or 8 of fp32
 template <bool F32>
-__device__ __forceinline__ float value_at(const void *x, int64_t i) {
-    if constexpr (F32)
-        return static_cast<const float *>(x)[i];
-    else
-        return bf16_bits_to_f32(static_cast<const uint16_t *>(x)[i]);
+__device__ __forceinline__ void load8(const void *x, int64_t at, int64_t left, int align, uint32_t (&u)[F32 ? 8 : 4]) {
+    if constexpr (F32) {
+        const uint32_t *p = static_cast<const uint32_t *>(x) + at;
+        if (left >= 8 && align == 16) {
+            const uint4 a = reinterpret_cast<const uint4 *>(p)[0], b = reinterpret_cast<const uint4 *>(p)[1];
+            u[0] = a.x, u[1] = a.y, u[2] = a.z, u[3] = a.w, u[4] = b.x, u[5] = b.y, u[6] = b.z, u[7] = b.w;
+            return;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) u[i] = i < left ? p[i] : 0u;
+    } else {
+        const uint16_t *p = static_cast<const uint16_t *>(x) + at;
+        if (left >= 8 && align == 16) {
+            const uint4 w = *reinterpret_cast<const uint4 *>(p);
+            u[0] = w.x, u[1] = w.y, u[2] = w.z, u[3] = w.w;
+        } else if (left >= 8 && align == 8) {
+            const uint2 a = reinterpret_cast<const uint2 *>(p)[0], b = reinterpret_cast<const uint2 *>(p)[1];
+            u[0] = a.x, u[1] = a.y, u[2] = b.x, u[3] = b.y;
+        } else if (left >= 8 && align == 4) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) u[i] = reinterpret_cast<const uint32_t *>(p)[i];
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                u[i] = (2 * i < left ? p[2 * i] : 0u) | (2 * i + 1 < left ? (uint32_t)p[2 * i + 1] << 16 : 0u);
+        }
+    }
+}
+template <bool F32>
+__device__ __forceinline__ void numbers(const uint32_t (&u)[F32 ? 8 : 4], float (&v)[8]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[2 * i] = __uint_as_float(F32 ? u[F32 ? 2 * i : i] : u[i] << 16);
+        v[2 * i + 1] = __uint_as_float(F32 ? u[F32 ? 2 * i + 1 : i] : u[i] & 0xFFFF0000u);
+    }
 }
 
-// one row per CTA at a time, read twice
-template <bool F32, bool GLU, bool HALF>
-__global__ void __launch_bounds__(kRoundThreads) round_rows_kernel(const RoundParams p) {
-    __shared__ uint32_t part[kRoundThreads / 32];
+// eight rounded values, as bytes or in fp16, at `at` of a row of q; the fp16 rows' pitch is a multiple of 64
+template <bool HALF>
+__device__ __forceinline__ void store8(void *q, int64_t at, int64_t left, bool wide, const float (&v)[8], const RowScale &s) {
+    uint64_t m[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m[i] = int8x2_of(v[2 * i], v[2 * i + 1], s);
+    if constexpr (HALF) {
+        uint32_t h[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            asm("add.rn.f32x2 %0, %1, %2;" : "=l"(m[i]) : "l"(m[i]), "l"(twice(-12582912.f)));
+            const __half2 p = __floats2half2_rn(__uint_as_float((uint32_t)m[i]), __uint_as_float((uint32_t)(m[i] >> 32)));
+            h[i] = s.nan ? 0u : *reinterpret_cast<const uint32_t *>(&p);
+        }
+        *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(q) + at) = make_uint4(h[0], h[1], h[2], h[3]);
+    } else {
+        uint32_t b[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) b[i] = __byte_perm((uint32_t)m[i], (uint32_t)(m[i] >> 32), 0x0040);
+        const uint32_t lo = s.nan ? 0u : __byte_perm(b[0], b[1], 0x5410), hi = s.nan ? 0u : __byte_perm(b[2], b[3], 0x5410);
+        uint8_t *dst = static_cast<uint8_t *>(q) + at;
+        if (wide && left >= 8) {
+            *reinterpret_cast<uint2 *>(dst) = make_uint2(lo, hi);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (i < left) dst[i] = (uint8_t)((i < 4 ? lo : hi) >> (i % 4 * 8));
+        }
+    }
+}
+
+// LANES threads to a row (32 or 256), SLOTS times eight values of each kept (0: none, rows of any length)
+// What a thread keeps of eight values: bf16 as they lie in memory (half the registers, six CTAs on an SM), or 32 bits each.
+template <bool F32, bool GLU, bool HALF, int LANES, int SLOTS>
+__global__ void __launch_bounds__(kRoundThreads, F32 || GLU ? 4 : 6) round_rows_kernel(const RoundParams p, const int align,
+                                                                                       const int wide) {
+    constexpr bool kWide = F32 || GLU;
+    constexpr int kRows = kRoundThreads / LANES, kKeep = SLOTS > 0 ? SLOTS : 1;
+    __shared__ uint32_t part[2][kRoundThreads / 32];
     pdl_wait();
+    // (after the wait: what the next kernel reads early is complete before this kernel began)
     pdl_launch_dependents();
     const int64_t rows = p.last ? min((int64_t)max(*p.last, 0), p.rows) : p.rows;
-    for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
-        auto value = [&](int64_t k) {
-            const float v = value_at<F32>(p.x, r * p.ldx + k);
-            return GLU ? swiglu(v, value_at<F32>(p.x, r * p.ldx + p.K + k)) : v;
-        };
-        uint32_t top = 0;
-        for (int64_t k = threadIdx.x; k < p.K; k += kRoundThreads) top = max(top, magnitude(value(k)));
-        top = __reduce_max_sync(~0u, top);
-        if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = top;
-        __syncthreads();
+    const int l = threadIdx.x % LANES;
+    int turn = 0;
+    for (int64_t r = (int64_t)blockIdx.x * kRows + threadIdx.x / LANES; r < rows; r += (int64_t)gridDim.x * kRows, turn ^= 1) {
+        auto values = [&](int64_t k, uint32_t (&keep)[kWide ? 8 : 4]) {
+            if constexpr (GLU) {
+                uint32_t a[F32 ? 8 : 4], b[F32 ? 8 : 4];
+                float gate[8], up[8];
+                load8<F32>(p.x, r * p.ldx + k, p.K - k, align, a);
+                load8<F32>(p.x, r * p.ldx + p.K + k, p.K - k, align, b);
+                numbers<F32>(a, gate);
+                numbers<F32>(b, up);
 #pragma unroll
-        for (int w = 0; w < kRoundThreads / 32; ++w) top = max(top, part[w]);
-        const RowScale s = row_scale(top);
-        for (int64_t k = threadIdx.x; k < p.K; k += kRoundThreads) {
-            const int q = int8_of(value(k), s);
-            if constexpr (HALF)
-                static_cast<__half *>(p.q)[r * p.ldq + k] = __int2half_rn(q);
-            else
-                static_cast<int8_t *>(p.q)[r * p.ldq + k] = (int8_t)q;
+                for (int i = 0; i < 8; ++i) keep[i] = __float_as_uint(swiglu(gate[i], up[i]));
+            } else {
+                load8<F32>(p.x, r * p.ldx + k, p.K - k, align, keep);
+            }
+        };
+        auto largest = [&](const uint32_t (&keep)[kWide ? 8 : 4], uint32_t top) {
+            if constexpr (kWide) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) top = max(top, keep[j] & 0x7FFFFFFFu);
+            } else {   // each half is a maximum
+#pragma unroll
+                for (int j = 0; j < 4; ++j) top = __vmaxu2(top, keep[j] & 0x7FFF7FFFu);
+            }
+            return top;
+        };
+        auto rounded = [&](int64_t k, const uint32_t (&keep)[kWide ? 8 : 4], const RowScale &s) {
+            float v[8];
+            numbers<kWide>(keep, v);
+            store8<HALF>(p.q, r * p.ldq + k, p.K - k, wide, v, s);
+        };
+        uint32_t keep[kKeep][kWide ? 8 : 4], top = 0;
+        if constexpr (SLOTS > 0) {
+#pragma unroll
+            for (int i = 0; i < SLOTS; ++i) {
+                const int64_t k = (int64_t)(i * LANES + l) * 8;
+                if (k < p.K) values(k, keep[i]);
+            }
+#pragma unroll
+            for (int i = 0; i < SLOTS; ++i)
+                if ((int64_t)(i * LANES + l) * 8 < p.K) top = largest(keep[i], top);
+        } else {
+            for (int64_t k = (int64_t)l * 8; k < p.K; k += LANES * 8) {
+                values(k, keep[0]);
+                top = largest(keep[0], top);
+            }
         }
-        if (threadIdx.x == 0) p.scales[r] = s.scale;
-        __syncthreads();
+        if constexpr (!kWide) top = max(top << 16, top & 0xFFFF0000u);
+        top = __reduce_max_sync(~0u, top);
+        if constexpr (LANES > 32) {   // (rows in turn have buffers in turn: one barrier a row)
+            if (threadIdx.x % 32 == 0) part[turn][threadIdx.x / 32] = top;
+            __syncthreads();
+#pragma unroll
+            for (int w = 0; w < LANES / 32; ++w) top = max(top, part[turn][w]);
+        }
+        const RowScale s = row_scale(top);
+        if constexpr (SLOTS > 0) {
+#pragma unroll
+            for (int i = 0; i < SLOTS; ++i) {
+                const int64_t k = (int64_t)(i * LANES + l) * 8;
+                if (k < p.K) rounded(k, keep[i], s);
+            }
+        } else {
+            for (int64_t k = (int64_t)l * 8; k < p.K; k += LANES * 8) {
+                values(k, keep[0]);
+                rounded(k, keep[0], s);
+            }
+        }
+        if (l == 0) p.scales[r] = s.scale;
     }
 }
 
@@ -130,14 +249,33 @@ __global__ void __launch_bounds__(256) int8_simt_kernel(const Int8Gemm g) {
 
 }  // namespace
 
-cudaError_t launch_int8_round(const RoundParams &p, int sm_count, bool pdl, cudaStream_t s) {
-    const dim3 grid((unsigned)std::min<int64_t>(p.rows, (int64_t)sm_count * 8));
-    auto with = [&](auto f32, auto glu) {
-        if (p.half_out) return launch_kernel(round_rows_kernel<decltype(f32)::value, decltype(glu)::value, true>, grid, kRoundThreads, 0, pdl, 1, s, p);
-        return launch_kernel(round_rows_kernel<decltype(f32)::value, decltype(glu)::value, false>, grid, kRoundThreads, 0, pdl, 1, s, p);
+namespace {
+template <bool F32, bool GLU, bool HALF>
+cudaError_t round_of(const RoundParams &p, int sm_count, bool pdl, cudaStream_t s) {
+    // of every eight values: the largest power of two, 16 at most, that divides the address of each
+    const uintptr_t size = F32 ? 4 : 2;
+    const uintptr_t bits = reinterpret_cast<uintptr_t>(p.x) | (uintptr_t)p.ldx * size | (GLU ? (uintptr_t)p.K * size : 0) | 16u;
+    const int align = (int)(bits & (~bits + 1));
+    const int wide = ((reinterpret_cast<uintptr_t>(p.q) | (uintptr_t)p.ldq) & 7u) == 0;
+    auto with = [&](auto lanes, auto slots) {
+        constexpr int kRows = kRoundThreads / decltype(lanes)::value;
+        const dim3 grid((unsigned)std::min<int64_t>((p.rows + kRows - 1) / kRows, (int64_t)sm_count * 8));
+        return launch_kernel(round_rows_kernel<F32, GLU, HALF, decltype(lanes)::value, decltype(slots)::value>, grid, kRoundThreads, 0,
+                             pdl, 1, s, p, align, wide);
     };
-    if (p.f32) return p.swiglu ? with(std::true_type(), std::true_type()) : with(std::true_type(), std::false_type());
-    return p.swiglu ? with(std::false_type(), std::true_type()) : with(std::false_type(), std::false_type());
+    using std::integral_constant;
+    if (p.K <= 256) return with(integral_constant<int, 32>(), integral_constant<int, 1>());
+    if (p.K <= 1024) return with(integral_constant<int, 32>(), integral_constant<int, 4>());
+    if (p.K <= 4096) return with(integral_constant<int, 256>(), integral_constant<int, 2>());
+    if (p.K <= 8192) return with(integral_constant<int, 256>(), integral_constant<int, 4>());
+    return with(integral_constant<int, 256>(), integral_constant<int, 0>());
+}
+}  // namespace
+
+cudaError_t launch_int8_round(const RoundParams &p, int sm_count, bool pdl, cudaStream_t s) {
+    if (p.half_out) return p.f32 ? round_of<true, false, true>(p, sm_count, pdl, s) : round_of<false, false, true>(p, sm_count, pdl, s);
+    if (p.swiglu) return p.f32 ? round_of<true, true, false>(p, sm_count, pdl, s) : round_of<false, true, false>(p, sm_count, pdl, s);
+    return p.f32 ? round_of<true, false, false>(p, sm_count, pdl, s) : round_of<false, false, false>(p, sm_count, pdl, s);
 }
 
 cudaError_t launch_int8_expand(const int8_t *x, int64_t ldx, int64_t rows, int64_t K, const int32_t *last, uint16_t *out,

@@ -11,33 +11,39 @@ constexpr float kLevels = 127.f;
 // |v| as an integer that orders like the number, infinities and NaN above every finite value
 __device__ __forceinline__ uint32_t magnitude(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
 
-// A row's largest magnitude and what follows from it.
+// A row's largest magnitude and what follows from it: 512 / a and -a / 512, each twice, for the packed 32-bit instructions.
 struct RowScale {
-    float amax, inv, scale;   // inv = 127 / amax to within 2^-23
+    uint64_t inv, minus_a;
+    float scale;
+    bool nan;
 };
+__device__ __forceinline__ uint64_t twice(float v) {
+    const uint64_t u = __float_as_uint(v);
+    return u | u << 32;
+}
 __device__ __forceinline__ RowScale row_scale(uint32_t top) {
     RowScale r;
-    if (top >= 0x7F800000u) {   // infinity or NaN: the row stands for NaN
-        r.amax = 1.f;
-        r.inv = 0.f;
-        r.scale = __uint_as_float(0x7FC00000u);
-    } else {
-        r.amax = fmaxf(__uint_as_float(top), kInt8AmaxFloor);
-        r.inv = __fdiv_rn(kLevels, r.amax);
-        r.scale = __fdiv_rn(r.amax, kLevels);
-    }
+    r.nan = top >= 0x7F800000u;   // infinity or NaN: the row stands for NaN
+    const float a = r.nan ? 1.f : fmaxf(__uint_as_float(top), kInt8AmaxFloor);
+    const float b = a * 0.001953125f;   // and its reciprocal: normal numbers whatever a is
+    r.inv = twice(__frcp_rn(b));
+    r.minus_a = twice(-b);
+    r.scale = r.nan ? __uint_as_float(0x7FC00000u) : __fdiv_rn(a, kLevels);
     return r;
 }
 
-// rint(127 v / amax), ties to even, the quotient to nearest: 127 / 512 v first, so that nothing overflows; 512 is exact.
-// The product with 127 / amax is within 2^-22 of the quotient's value, 2^-15 in all, so only near the middle of two integers does
-// it take the division (every tie does; one value in a thousand of others).
-__device__ __forceinline__ int int8_of(float v, const RowScale &r) {
-    const float t = v * r.inv;
-    const float n = rintf(t);
-    if (fabsf(fabsf(t - n) - 0.5f) < 0.0009765625f && r.inv > 0.f)
-        return (int)rintf(__fdiv_rn(v * (kLevels / 512.f), r.amax) * 512.f);
-    return r.inv > 0.f ? (int)n : 0;
+// Twice rint(127 v / a), ties to even: the integers are in the low byte of each half of the result, which holds 1.5 * 2^23 more
+// than they are.  127 / 512 v first, so that nothing overflows.  One residual step (q's error is a few units in the last place, the
+// residual is exact, and so the step's error lies far below half a unit) makes every quotient that 32 bits hold exact, every one halfway
+// between two integers among them; with v and a in bf16 no other one is anywhere near that.
+__device__ __forceinline__ uint64_t int8x2_of(float lo, float hi, const RowScale &s) {
+    uint64_t t = (uint64_t)__float_as_uint(hi) << 32 | __float_as_uint(lo), q, r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(t) : "l"(t), "l"(twice(kLevels / 512.f)));
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(q) : "l"(t), "l"(s.inv));
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(s.minus_a), "l"(q), "l"(t));
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(q) : "l"(r), "l"(s.inv), "l"(q));
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(q) : "l"(q), "l"(twice(12582912.f)));
+    return q;
 }
 
 // silu(g) u

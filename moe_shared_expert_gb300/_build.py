@@ -19,7 +19,7 @@ LIB = os.path.join(PKG, "libmse.so")
 # vectorcall entry of the routed-expert calls, by this interpreter's name for its extensions
 CALLS = os.path.join(PKG, "_calls" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
 SOURCES = ["api.cu", "tc.cu", "simt.cu", "elementwise.cu", "static_scratch.cu", "route.cu", "fp8.cu", "fp8_cols.cu", "fp8_pair.cu",
-           "routed_api.cu", "sorted.cu", "int8.cu", "int8_cols.cu", "int8_pair.cu",
+           "routed_api.cu", "sorted.cu", "int8.cu", "int8_few.cu", "int8_cols.cu", "int8_pair.cu",
            "sorted_api.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

@@ -3,7 +3,8 @@
 // A CTA owns one 128-row weight tile and one token tile; the k-blocks may be split over a cluster, whose CTAs exchange their
 // integer sums through distributed shared memory and each finish a slice of the token columns.
 //
-// Warp 0 loads (TMA), warp 1 issues MMAs, warps 2-5 convert weights (int8_tc.cuh), warps 6-9 add the chunks' sums.
+// Warp 0 loads (TMA), warp 1 issues MMAs.  Warps 2-5 and 6-9 convert the weights of every other k-block each (int8_tc.cuh), and each
+// adds one half of the token columns when a chunk of k-blocks ends.
 #include <atomic>
 
 #include "device.h"
@@ -33,8 +34,10 @@ template <int BN_>
 struct Cols {
     static constexpr int BN = BN_;
     static constexpr int CTAS = BN <= 64 ? 2 : 1;                        // resident per SM
-    static constexpr int NA = BN <= 32 ? 3 : BN == 64 ? 2 : 4;           // k-blocks of weights in TMEM
-    static constexpr int TMEM = pow2_at_least(2 * BN + NA * (int)kATmem);
+    static constexpr int NA = BN <= 64 ? 3 : 4;                          // k-blocks of weights in TMEM
+    static constexpr int ND = BN == 64 ? 1 : 2;                          // chunks of sums there
+    static constexpr int CPT = BN / 2;                                   // token columns a thread adds
+    static constexpr int TMEM = pow2_at_least(ND * BN + NA * (int)kATmem);
     static_assert(CTAS * TMEM <= 512, "TMEM");
     static constexpr uint32_t TOKENS = BN * kInner * 2;                  // two tiles of 64 k
     static constexpr uint32_t STAGE = kWeightTile + TOKENS;
@@ -72,9 +75,9 @@ __global__ void __launch_bounds__(kColsThreads, C::CTAS)
             mbar_init(smem_u32(&ctl->afull[a]), 4);
             mbar_init(smem_u32(&ctl->aempty[a]), 1);
         }
-        for (int d = 0; d < 2; ++d) {
+        for (int d = 0; d < C::ND; ++d) {
             mbar_init(smem_u32(&ctl->dfull[d]), 1);
-            mbar_init(smem_u32(&ctl->dempty[d]), 4);
+            mbar_init(smem_u32(&ctl->dempty[d]), 8);
         }
         mbar_init(smem_u32(&ctl->drain), 1);
         ctl->abort_flag = 0;
@@ -89,7 +92,7 @@ __global__ void __launch_bounds__(kColsThreads, C::CTAS)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem_base = __shfl_sync(~0u, ctl->tmem_base, 0), tmem_a = tmem_base + 2 * BN;
+    const uint32_t tmem_base = __shfl_sync(~0u, ctl->tmem_base, 0), tmem_a = tmem_base + C::ND * BN;
     // The kernel before this one, of the same call, let this one start after its own wait: weights and offsets are complete,
     // and only the tokens are that kernel's.
     RowTile t;
@@ -135,10 +138,10 @@ __global__ void __launch_bounds__(kColsThreads, C::CTAS)
         const uint32_t idesc = idesc_f16_f32(128, BN);
         uint32_t phase = 0, aphase = 0;
         for (int i = 0, s = 0, a = 0; i < n; ++i) {
-            const int chunk = i / kChunkBlocks, d = chunk & 1, in = i % kChunkBlocks;
+            const int chunk = i / kChunkBlocks, d = chunk % C::ND, in = i % kChunkBlocks;
             if (!wait_all(smem_u32(&ctl->full[s]), phase, abort_flag, g) ||
                 !wait_all(smem_u32(&ctl->afull[a]), aphase, abort_flag, g) ||
-                (in == 0 && !wait_all(smem_u32(&ctl->dempty[d]), (uint32_t)((chunk >> 1) & 1) ^ 1u, abort_flag, g)))
+                (in == 0 && !wait_all(smem_u32(&ctl->dempty[d]), (uint32_t)((chunk / C::ND) & 1) ^ 1u, abort_flag, g)))
                 break;
             tc_fence_after();
             const uint32_t x = base + s * C::STAGE + kWeightTile;
@@ -156,48 +159,50 @@ __global__ void __launch_bounds__(kColsThreads, C::CTAS)
             if (++s == S) { s = 0; phase ^= 1u; }
             if (++a == C::NA) { a = 0; aphase ^= 1u; }
         }
-    } else if (active && warp >= 2 && warp < 6) {
-        const int q = warp & 3, row = q * 32 + lane;
-        uint32_t phase = 0, aphase = 0;
-        for (int i = 0, s = 0, a = 0; i < n; ++i) {
-            if (!wait_all(smem_u32(&ctl->full[s]), phase, abort_flag, g) ||
-                !wait_all(smem_u32(&ctl->aempty[a]), aphase ^ 1u, abort_flag, g))
-                break;
+    }
+
+    int acc[C::CPT];
+    const bool works = warp >= 2;
+    const int q = warp & 3, row = q * 32 + lane, h = works ? (warp - 2) / 4 : 0, col0 = h * C::CPT;
+    if (active && works) {
+        const uint32_t lanes = (uint32_t)(q * 32) << 16;
+        const int chunks = (n + kChunkBlocks - 1) / kChunkBlocks;
+#pragma unroll
+        for (int c = 0; c < C::CPT; ++c) acc[c] = 0;
+        bool ok = true;
+        // A chunk's sums are read before the second k-block behind it is converted: the MMAs of that one would wait for them.
+        for (int i = h, chunk = 0; ok; i += 2) {
+            while (ok && chunk < chunks && ((chunk + 1) * kChunkBlocks + 2 <= i || i >= n)) {
+                const int d = chunk % C::ND;
+                ok = wait_all(smem_u32(&ctl->dfull[d]), (uint32_t)((chunk / C::ND) & 1), abort_flag, g);
+                if (!ok) break;
+                ++chunk;
+                tc_fence_after();
+                const uint32_t src = tmem_base + (uint32_t)(d * BN + col0) + lanes;
+                constexpr int kLoad = C::CPT < 16 ? 8 : 16;
+#pragma unroll
+                for (int c = 0; c < C::CPT; c += kLoad) {
+                    uint32_t v[kLoad];
+                    if constexpr (kLoad == 8) tmem_ld8(src + c, v); else tmem_ld16(src + c, v);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int j = 0; j < kLoad; ++j) acc[c + j] += __float2int_rn(__uint_as_float(v[j]));
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&ctl->dempty[d]));
+            }
+            if (!ok || i >= n) break;
+            const int s = i % S, a = i % C::NA;
+            ok = wait_all(smem_u32(&ctl->full[s]), (uint32_t)((i / S) & 1), abort_flag, g) &&
+                 wait_all(smem_u32(&ctl->aempty[a]), (uint32_t)((i / C::NA) & 1) ^ 1u, abort_flag, g);
+            if (!ok) break;
             tc_fence_after();
-            convert_rows(ring + (size_t)s * C::STAGE, row, tmem_a + (uint32_t)(a * kATmem) + ((uint32_t)(q * 32) << 16));
+            convert_rows(ring + (size_t)s * C::STAGE, row, tmem_a + (uint32_t)(a * kATmem) + lanes);
             tmem_st_wait();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&ctl->afull[a]));
-            if (++s == S) { s = 0; phase ^= 1u; }
-            if (++a == C::NA) { a = 0; aphase ^= 1u; }
-        }
-        __syncwarp();
-    }
-
-    int acc[BN];
-    const bool adds = warp >= 6;
-    const int q = warp & 3, row = q * 32 + lane;
-    if (active && adds) {
-#pragma unroll
-        for (int c = 0; c < BN; ++c) acc[c] = 0;
-        const int chunks = (n + kChunkBlocks - 1) / kChunkBlocks;
-        for (int i = 0; i < chunks; ++i) {
-            const int d = i & 1;
-            if (!wait_all(smem_u32(&ctl->dfull[d]), (uint32_t)((i >> 1) & 1), abort_flag, g)) break;
-            tc_fence_after();
-            const uint32_t src = tmem_base + (uint32_t)(d * BN) + ((uint32_t)(q * 32) << 16);
-#pragma unroll
-            for (int c = 0; c < BN; c += 16) {
-                uint32_t v[16];
-                tmem_ld16(src + c, v);
-                tmem_ld_wait();
-#pragma unroll
-                for (int j = 0; j < 16; ++j) acc[c + j] += __float2int_rn(__uint_as_float(v[j]));
-            }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&ctl->dempty[d]));
         }
         __syncwarp();
     }
@@ -207,18 +212,18 @@ __global__ void __launch_bounds__(kColsThreads, C::CTAS)
     const int slice = (BN / 4 + parts - 1) / parts;
     if (parts > 1) {
         cluster_sync();   // every ring of the cluster is idle
-        if (active && adds) {
+        if (active && works) {
 #pragma unroll
-            for (int c = 0; c < BN; c += 4)
-                if (c < t.rows) {
-                    const int to = c / 4 / slice, at = c / 4 - to * slice;
+            for (int c = 0; c < C::CPT; c += 4)
+                if (col0 + c < t.rows) {
+                    const int quad = (col0 + c) / 4, to = quad / slice, at = quad - to * slice;
                     st_cluster_s32x4(map_to_rank(smem_u32(red + (size_t)(part * slice + at) * 128 + row), (uint32_t)to),
                                      make_int4(acc[c], acc[c + 1], acc[c + 2], acc[c + 3]));
                 }
         }
         cluster_sync();
     }
-    if (active && adds) {
+    if (active && works) {
         const int64_t out_n = (int64_t)m * 128 + row;
         if (out_n < g.N) {
             const float w = g.ws[(int64_t)t.group * g.N + out_n];
@@ -232,11 +237,11 @@ __global__ void __launch_bounds__(kColsThreads, C::CTAS)
             };
             if (parts == 1) {
 #pragma unroll
-                for (int c = 0; c < BN; ++c)
-                    if (c < t.rows) store(c, acc[c]);
+                for (int c = 0; c < C::CPT; ++c)
+                    if (col0 + c < t.rows) store(col0 + c, acc[c]);
             } else {
                 const int first = part * slice, mine = min(min(slice, BN / 4 - first), (t.rows + 3) / 4 - first);
-                for (int at = 0; at < mine; ++at) {
+                for (int at = h; at < mine; at += 2) {
                     int4 v = make_int4(0, 0, 0, 0);
                     for (int r = 0; r < parts; ++r) {
                         const int4 o = red[(size_t)(r * slice + at) * 128 + row];

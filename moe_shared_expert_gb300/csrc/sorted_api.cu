@@ -79,34 +79,45 @@ bool apart(const Int8Gemm &g) {
 }
 int64_t pitch16(int64_t K) { return (K + 63) / 64 * 64; }   // of tokens in fp16
 
-// Token rows of a tensor-core tile, by the rows expected of a group.
-int tile_rows_of(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : rows <= 128 ? 128 : 256; }
+// Token rows of a tile, by the rows expected of a group: 1 to 8 take the kernel for few, 16 to 128 the swap-AB kernel, 256 the
+// CTA-pair kernel.
+constexpr int kFewRows = 8;
+int tile_rows_of(int64_t rows, int64_t K) {
+    const int few = rows <= 1 ? 1 : rows <= 2 ? 2 : rows <= 4 ? 4 : 8;
+    if (rows <= kFewRows && int8_few_serves(few, K)) return few;
+    return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : rows <= 128 ? 128 : 256;
+}
+
+// One launch, whose kernel rounds the tokens itself: every CTA rounds all of them.
+bool rounds_itself(int tile_rows) { return tile_rows <= 2; }
 
 bool tensorcore_ok(const Int8Gemm &g) {
     return (reinterpret_cast<uintptr_t>(g.wq) & 15u) == 0 && g.ldw % 16 == 0 && (g.N + 127) / 128 <= 65535 &&
            g.T / 128 + g.groups <= 65535;
 }
 
-mse_status run_tensorcore(Int8Gemm g, const DeviceView &d, cudaStream_t s) {
-    g.wait_limit_ns = wait_limit_ns();
-    g.err = d.err;
-    if (tile_rows_of(g.T / g.groups) == 256) return launch_int8_pair(g, d.sm_count, pdl_enabled(), s);
-    return launch_int8_cols(g, tile_rows_of(g.T / g.groups), d.sm_count, pdl_enabled(), s);
+mse_status run_tensorcore(const Int8Gemm &g, int tile_rows, const DeviceView &d, cudaStream_t s) {
+    if (tile_rows == 256) return launch_int8_pair(g, d.sm_count, pdl_enabled(), s);
+    return launch_int8_cols(g, tile_rows, d.sm_count, pdl_enabled(), s);
 }
 
 // int8 rows: expanded to fp16 in the workspace for the tensor cores
 mse_status run_product(Int8Gemm g, const DeviceView &d, void *workspace, cudaStream_t s) {
-    bool tensorcore = false;
-    mse_status st = choose_tensorcore(tensorcore_ok(g), &tensorcore);
+    g.wait_limit_ns = wait_limit_ns();
+    g.err = d.err;
+    bool fast = false;
+    mse_status st = choose_tensorcore(tensorcore_ok(g), &fast);
     if (st != MSE_OK) return st;
-    if (!tensorcore) return from_cuda(launch_int8_simt(g, pdl_enabled(), s));
+    if (!fast) return from_cuda(launch_int8_simt(g, pdl_enabled(), s));
+    const int tile_rows = tile_rows_of(g.T / g.groups, g.K);
+    if (tile_rows <= 8) return from_cuda(launch_int8_few(g, tile_rows, nullptr, 0, 0, false, d.sm_count, pdl_enabled(), s));
     g.ldx16 = pitch16(g.K);
     uint16_t *x16 = static_cast<uint16_t *>(workspace);
     st = from_cuda(launch_int8_expand(g.xq, g.ldx, g.T, g.K, g.offsets ? g.offsets + g.groups : nullptr, x16, g.ldx16, d.sm_count,
                                       pdl_enabled(), s));
     if (st != MSE_OK) return st;
     g.x16 = x16;
-    return run_tensorcore(g, d, s);
+    return run_tensorcore(g, tile_rows, d, s);
 }
 
 Int8Gemm product(const int8_t *xq, int64_t ldx, const float *xs, const int32_t *offsets, int64_t groups, const int8_t *wq,
@@ -279,20 +290,26 @@ mse_status int8_linear(const void *x, mse_dtype x_dtype, int64_t ldx, const int8
     const Int8Ws L = int8_ws(T, K);
     float *xs = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + L.s_off);
     Int8Gemm g = product(nullptr, 0, xs, nullptr, 1, wq, ldw, ws, T, N, K, y, y_dtype);
-    bool tensorcore = false;
-    if ((st = choose_tensorcore(tensorcore_ok(g), &tensorcore)) != MSE_OK) return st;
+    g.wait_limit_ns = wait_limit_ns();
+    g.err = d.err;
+    bool fast = false;
+    if ((st = choose_tensorcore(tensorcore_ok(g), &fast)) != MSE_OK) return st;
+    const int tile_rows = fast ? tile_rows_of(T, K) : 0;
+    const int64_t x_size = size_of(x_dtype);
+    // (y over x: the product's CTAs would write y while others still round x)
+    if (fast && rounds_itself(tile_rows) && disjoint(x, span(T, K, ldx, x_size), y, T * N * size_of(y_dtype)))
+        return from_cuda(launch_int8_few(g, tile_rows, x, x_dtype == MSE_F32, ldx, false, d.sm_count, pdl_enabled(), s));
     RoundParams p;
     p.x = x; p.rows = T; p.K = K; p.ldx = ldx;
     p.f32 = x_dtype == MSE_F32; p.swiglu = 0;
     p.last = nullptr;
-    p.q = workspace; p.ldq = pitch16(K); p.half_out = tensorcore; p.scales = xs;
+    p.q = workspace; p.ldq = pitch16(K); p.half_out = fast && tile_rows > 8; p.scales = xs;
     if ((st = from_cuda(launch_int8_round(p, d.sm_count, pdl_enabled(), s))) != MSE_OK) return st;
-    if (tensorcore) {
-        g.x16 = static_cast<const uint16_t *>(workspace); g.ldx16 = p.ldq;
-        return run_tensorcore(g, d, s);
-    }
     g.xq = static_cast<const int8_t *>(workspace); g.ldx = p.ldq;
-    return from_cuda(launch_int8_simt(g, pdl_enabled(), s));
+    if (!fast) return from_cuda(launch_int8_simt(g, pdl_enabled(), s));
+    if (tile_rows <= 8) return from_cuda(launch_int8_few(g, tile_rows, nullptr, 0, 0, true, d.sm_count, pdl_enabled(), s));
+    g.x16 = static_cast<const uint16_t *>(workspace); g.ldx16 = p.ldq;
+    return run_tensorcore(g, tile_rows, d, s);
 }
 
 }  // extern "C"

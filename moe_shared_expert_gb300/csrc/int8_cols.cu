@@ -48,6 +48,7 @@ struct Cols {
     }
     // stages of the ring with CTAS CTAs on an SM, or one
     static constexpr int PART = fit((CTAS == 2 ? 113 : 227) * 1024), WHOLE = fit(227 * 1024);
+    static_assert(NA <= PART, "the order of waits before a conversion");
     // the exchange of a split tile uses the ring: at most BN / 4 + 7 groups of four columns
     static_assert((BN / 4 + 7) * 2048 <= PART * STAGE, "exchange");
 };
@@ -194,8 +195,10 @@ __global__ void __launch_bounds__(kColsThreads, C::CTAS)
             }
             if (!ok || i >= n) break;
             const int s = i % S, a = i % C::NA;
-            ok = wait_all(smem_u32(&ctl->full[s]), (uint32_t)((i / S) & 1), abort_flag, g) &&
-                 wait_all(smem_u32(&ctl->aempty[a]), (uint32_t)((i / C::NA) & 1) ^ 1u, abort_flag, g);
+            // In this order: the slot's wait says that the MMAs of k-block i - NA are done, and so that the stage's k-block before
+            // this one, which the other warps may have converted, has landed: else its parity could be taken for this one's.
+            ok = wait_all(smem_u32(&ctl->aempty[a]), (uint32_t)((i / C::NA) & 1) ^ 1u, abort_flag, g) &&
+                 wait_all(smem_u32(&ctl->full[s]), (uint32_t)((i / S) & 1), abort_flag, g);
             if (!ok) break;
             tc_fence_after();
             convert_rows(ring + (size_t)s * C::STAGE, row, tmem_a + (uint32_t)(a * kATmem) + lanes);

@@ -18,6 +18,7 @@ namespace sorted {
 namespace {
 
 constexpr int kStages = 4, kSlots = 4;               // k-blocks in shared memory, and of weights in TMEM
+static_assert(kSlots <= kStages, "the order of waits before a conversion");
 constexpr int kWorkWarps = 8, kThreads = 128 + 32 * kWorkWarps;
 // registers: 384 threads x 168 at launch >= 128 x 56 + 256 x 224 afterwards
 constexpr int kLaunchRegs = 168;
@@ -176,10 +177,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         const uint32_t xb = map_to_rank(smem_u32(&ctl->xfull[stage]), 0);
                         mbar_arrive_expect_tx(wb, kWeightTile);
                         tma_load_2d_nohint(dst, &tmW, wb, k * kInner, w_row);
-                        if (leader) mbar_arrive_expect_tx(smem_u32(&ctl->xfull[stage]), 2 * kTokenBytes);
+                        const bool both = t.rows > kHalf;
+                        if (leader) mbar_arrive_expect_tx(smem_u32(&ctl->xfull[stage]), both ? 2 * kTokenBytes : kTokenBytes);
 #pragma unroll
                         for (int b = 0; b < 4; ++b)   // half b / 2, 64 k from b % 2; coordinates in bytes
-                            tma_load_2d_pair(dst + kWeightTile + b * kTokenBox, &tmX, xb, k * 2 * kInner + (b % 2) * 128,
+                            if (b < 2 || both) tma_load_2d_pair(dst + kWeightTile + b * kTokenBox, &tmX, xb, k * 2 * kInner + (b % 2) * 128,
                                              x_row + b / 2 * kHalf);
                     }
                     __syncwarp();
@@ -189,9 +191,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
         } else if (warp == 1 && leader) {
             const uint32_t idesc = idesc_f16_f32(256, kHalf);
-            uint32_t aphase = 0, use = 0;   // use: chunks so far
+            uint32_t aphase = 0, use[2] = {0, 0};   // use: chunks of a half so far
             int a = 0;
             for (int64_t id = pair; ok && id < total; id += n_pairs) {
+                RowTile t;
+                int n;
+                place(id, t, n);
+                const int halves = t.rows > kHalf ? 2 : 1;
                 for (int k = 0; k < kb; ++k) {
                     const int in = k % kChunkBlocks;
                     const bool last = in == kChunkBlocks - 1 || k == kb - 1;
@@ -200,8 +206,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     if (!ok) break;
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
+                        if (h == halves) break;
                         if (in == 0) {
-                            ok = wait_cluster(smem_u32(&ctl->dempty[h]), (use & 1u) ^ 1u, abort_flag, g);
+                            ok = wait_cluster(smem_u32(&ctl->dempty[h]), (use[h] & 1u) ^ 1u, abort_flag, g);
                             if (!ok) break;
                         }
                         tc_fence_after();
@@ -215,6 +222,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                             if (last) tc_commit_pair_multicast(smem_u32(&ctl->dfull[h]), 3);
                         }
                         __syncwarp();
+                        if (last) ++use[h];
                     }
                     if (!ok) break;
                     if (el) {
@@ -222,7 +230,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         tc_commit_pair_multicast(smem_u32(&ctl->aempty[a]), 3);
                     }
                     __syncwarp();
-                    if (last) ++use;
                     if (++stage == kStages) { stage = 0; phase ^= 1u; }
                     if (++a == kSlots) { a = 0; aphase ^= 1u; }
                 }
@@ -261,29 +268,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         open(id);
         for (int64_t i = h; ok; i += 2) {
             while (ok && id < total && (end + 2 <= i || i >= blocks)) {
-                ok = wait_all(smem_u32(&ctl->dfull[h]), use & 1u, abort_flag, g);
-                if (!ok) break;
-                ++use;
-                tc_fence_after();
+                if (left > 0) {   // (a tile of up to kHalf tokens has no second half)
+                    ok = wait_all(smem_u32(&ctl->dfull[h]), use & 1u, abort_flag, g);
+                    if (!ok) break;
+                    ++use;
+                    tc_fence_after();
 #pragma unroll
-                for (int c = 0; c < kHalf; c += 32) {
-                    uint32_t v[32];
-                    tmem_ld32(src + c, v);
-                    tmem_ld_wait();
-                    if (c + 32 == kHalf) {
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) arrive_cluster_relaxed(dempty);
+                    for (int c = 0; c < kHalf; c += 32) {
+                        uint32_t v[32];
+                        tmem_ld32(src + c, v);
+                        tmem_ld_wait();
+                        if (c + 32 == kHalf) {
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) arrive_cluster_relaxed(dempty);
+                        }
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) acc[c + j] += __float2int_rn(__uint_as_float(v[j]));
                     }
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) acc[c + j] += __float2int_rn(__uint_as_float(v[j]));
                 }
                 done += min(kb - done, kChunkBlocks);
                 if (done == kb) {
 #pragma unroll
                     for (int j = 0; j < kHalf / 32; ++j) xs[j * 32 + lane] = xa[j];
                     __syncwarp();
-                    if (out_n < g.N) {
+                    if (out_n < g.N && left > 0) {
                         if (g.out_f32) {
                             float *out = static_cast<float *>(g.out) + first * g.N + out_n;
 #pragma unroll
@@ -307,8 +316,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
             if (!ok || i >= blocks) break;
             const int stage = (int)(i % kStages), a = (int)(i % kSlots);
-            ok = wait_all(smem_u32(&ctl->wfull[stage]), (uint32_t)(i / kStages) & 1u, abort_flag, g) &&
-                 wait_all(smem_u32(&ctl->aempty[a]), ((uint32_t)(i / kSlots) & 1u) ^ 1u, abort_flag, g);
+            // (in this order: the slot's wait says that the stage's k-block before this one has landed)
+            ok = wait_all(smem_u32(&ctl->aempty[a]), ((uint32_t)(i / kSlots) & 1u) ^ 1u, abort_flag, g) &&
+                 wait_all(smem_u32(&ctl->wfull[stage]), (uint32_t)(i / kStages) & 1u, abort_flag, g);
             if (!ok) break;
             tc_fence_after();
             convert_rows(ring + (size_t)stage * kStage, row, tmem_a + (uint32_t)(a * kATmem) + lanes);

@@ -70,7 +70,8 @@ __device__ __forceinline__ void half_of_bytes(uint32_t w, uint32_t &lo, uint32_t
     hi = *reinterpret_cast<const uint32_t *>(&y);
 }
 
-// One warp's 32 weight rows of a k-block (128 bytes each, 128-byte swizzle) from shared to tensor memory as fp16.
+// One warp's 32 weight rows of a k-block (128 bytes each, 128-byte swizzle) from shared to tensor memory as fp16.  (All of a
+// row's bytes first, and the next k-block's while these go to tensor memory, makes the products 5 to 15% slower.)
 __device__ __forceinline__ void convert_rows(const uint8_t *tile, int row, uint32_t taddr) {
     const uint8_t *mine = tile + row * kInner;
 #pragma unroll

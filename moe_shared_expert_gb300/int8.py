@@ -16,7 +16,7 @@ from __future__ import annotations
 import moe_shared_expert_gb300 as _mse
 
 from . import routed as _r
-from .rows import _floats, _ready
+from . import rows as _s
 
 
 def int8_workspace_bytes(T: int, N: int, K: int, groups: int = 1) -> int:
@@ -40,10 +40,10 @@ def int8_quantise(x, swiglu=False, offsets=None, q=None, scales=None, stream=Non
 
     With swiglu, x is [.., 2K] and silu(x[.., :K]) * x[.., K:] is rounded.  With offsets (as moe_sort gives them), rows from
     offsets[-1] on are left alone.  New q has rows of a pitch of 16 bytes."""
-    torch = _ready()
+    torch = _s._ready() if _s._C is None else _r.torch
     if x is None or x.dim() not in (2, 3):
         raise ValueError(f"x: need a 2-d or 3-d tensor, got {_r._said(x)}")
-    code, ld, (*lead, width), device = _floats(x, "x", x.dim())
+    code, ld, (*lead, width), device = _s._floats(x, "x", x.dim())
     if swiglu and width % 2:
         raise ValueError(f"x: gate and up need an even number of columns, got {_r._said(x)}")
     K = width // 2 if swiglu else width
@@ -58,14 +58,14 @@ def int8_quantise(x, swiglu=False, offsets=None, q=None, scales=None, stream=Non
         last = offsets.data_ptr() + 4 * (offsets.shape[0] - 1)
     if q is None:
         q = _r._empty(stream, (*lead, _r._pad16(K)), torch.int8, x.device)[..., :K]
-    ldq, shape, _ = _r._rows(q, "q", (torch.int8,), x.dim(), device)
+    ldq, shape, _ = _r._rows(q, "q", _s._I8, x.dim(), device)
     if tuple(shape) != (*lead, K):
         raise ValueError(f"q: need {(*lead, K)}, got {_r._said(q)}")
     if scales is None:
-        scales = _r._empty(stream, tuple(lead), torch.float32, x.device)
+        scales = _r._empty(stream, tuple(lead), _s._F32, x.device)
     else:
-        _r._dense(scales, "scales", torch.float32, tuple(lead), device)
-    st = _r._C.int8_quantise(x.data_ptr(), code, rows, K, ld, 1 if swiglu else 0, last, q.data_ptr(), ldq, (rows - 1) * ldq + K,
+        _r._dense(scales, "scales", _s._F32, tuple(lead), device)
+    st = _s._C.int8_quantise(x.data_ptr(), code, rows, K, ld, 1 if swiglu else 0, last, q.data_ptr(), ldq, (rows - 1) * ldq + K,
                              scales.data_ptr(), _r._handle(stream, device))
     if st:
         _mse._check("int8_quantise", st)
@@ -74,16 +74,17 @@ def int8_quantise(x, swiglu=False, offsets=None, q=None, scales=None, stream=Non
 
 def int8_matmul(xq, xs, wq, ws, out_dtype=None, out=None, workspace=None, stream=None):
     """out [T, N] (bf16 unless out_dtype or out says fp32) = (xq wq^T) xs ws; xq [T, K], xs [T], wq [N, K], ws [N]."""
-    torch = _ready()
-    ldx, (T, K), device = _r._rows(xq, "xq", (torch.int8,), 2)
-    ldw, (N, Kw), _ = _r._rows(wq, "wq", (torch.int8,), 2, device)
+    if _s._C is None:
+        _s._ready()
+    ldx, (T, K), device = _r._rows(xq, "xq", _s._I8, 2)
+    ldw, (N, Kw), _ = _r._rows(wq, "wq", _s._I8, 2, device)
     if K != Kw:
         raise ValueError(f"xq and wq differ in K: {K} and {Kw}")
-    _r._dense(xs, "xs", torch.float32, (T,), device)
-    _r._dense(ws, "ws", torch.float32, (N,), device)
+    _r._dense(xs, "xs", _s._F32, (T,), device)
+    _r._dense(ws, "ws", _s._F32, (N,), device)
     out, code = _r._out(out, out_dtype, "out", (T, N), xq, stream)
     space = _space(workspace, stream, xq, device, T, N, K)
-    st = _r._C.int8_matmul(xq.data_ptr(), ldx, xs.data_ptr(), wq.data_ptr(), ldw, ws.data_ptr(), T, N, K, out.data_ptr(), code,
+    st = _s._C.int8_matmul(xq.data_ptr(), ldx, xs.data_ptr(), wq.data_ptr(), ldw, ws.data_ptr(), T, N, K, out.data_ptr(), code,
                            T * N, space.data_ptr(), space.nbytes, _r._handle(stream, device))
     if st:
         _mse._check("int8_matmul", st)
@@ -94,17 +95,17 @@ def int8_grouped_matmul(xq, xs, offsets, wq, ws, out_dtype=None, out=None, works
     """out [T, N]: rows offsets[g] .. offsets[g + 1] of xq [T, K] times wq[g]^T; wq [G, N, K], ws [G, N], offsets [G + 1].
 
     Rows behind the last group's are left as they were."""
-    torch = _ready()
-    ldx, (T, K), device = _r._rows(xq, "xq", (torch.int8,), 2)
-    ldw, (G, N, Kw), _ = _r._rows(wq, "wq", (torch.int8,), 3, device)
+    torch = _s._ready() if _s._C is None else _r.torch
+    ldx, (T, K), device = _r._rows(xq, "xq", _s._I8, 2)
+    ldw, (G, N, Kw), _ = _r._rows(wq, "wq", _s._I8, 3, device)
     if K != Kw:
         raise ValueError(f"xq and wq differ in K: {K} and {Kw}")
-    _r._dense(xs, "xs", torch.float32, (T,), device)
-    _r._dense(ws, "ws", torch.float32, (G, N), device)
+    _r._dense(xs, "xs", _s._F32, (T,), device)
+    _r._dense(ws, "ws", _s._F32, (G, N), device)
     _r._dense(offsets, "offsets", torch.int32, (G + 1,), device)
     out, code = _r._out(out, out_dtype, "out", (T, N), xq, stream)
     space = _space(workspace, stream, xq, device, T, N, K, G)
-    st = _r._C.int8_grouped_matmul(xq.data_ptr(), ldx, xs.data_ptr(), offsets.data_ptr(), G, wq.data_ptr(), ldw, ws.data_ptr(),
+    st = _s._C.int8_grouped_matmul(xq.data_ptr(), ldx, xs.data_ptr(), offsets.data_ptr(), G, wq.data_ptr(), ldw, ws.data_ptr(),
                                    T, N, K, out.data_ptr(), code, T * N, space.data_ptr(), space.nbytes,
                                    _r._handle(stream, device))
     if st:
@@ -114,15 +115,16 @@ def int8_grouped_matmul(xq, xs, offsets, wq, ws, out_dtype=None, out=None, works
 
 def int8_linear(x, wq, ws, y_dtype=None, y=None, workspace=None, stream=None):
     """y [T, N] = x wq^T: x [T, K] (bf16 or fp32) is rounded to 8-bit integers by rows, wq and ws as in int8_matmul."""
-    torch = _ready()
-    x_code, ldx, (T, K), device = _floats(x, "x", 2)
-    ldw, (N, Kw), _ = _r._rows(wq, "wq", (torch.int8,), 2, device)
+    if _s._C is None:
+        _s._ready()
+    x_code, ldx, (T, K), device = _s._floats(x, "x", 2)
+    ldw, (N, Kw), _ = _r._rows(wq, "wq", _s._I8, 2, device)
     if K != Kw:
         raise ValueError(f"x and wq differ in K: {K} and {Kw}")
-    _r._dense(ws, "ws", torch.float32, (N,), device)
+    _r._dense(ws, "ws", _s._F32, (N,), device)
     y, code = _r._out(y, y_dtype, "y", (T, N), x, stream)
     space = _space(workspace, stream, x, device, T, N, K)
-    st = _r._C.int8_linear(x.data_ptr(), x_code, ldx, wq.data_ptr(), ldw, ws.data_ptr(), T, N, K, y.data_ptr(), code, T * N,
+    st = _s._C.int8_linear(x.data_ptr(), x_code, ldx, wq.data_ptr(), ldw, ws.data_ptr(), T, N, K, y.data_ptr(), code, T * N,
                            space.data_ptr(), space.nbytes, _r._handle(stream, device))
     if st:
         _mse._check("int8_linear", st)

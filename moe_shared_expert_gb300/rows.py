@@ -14,31 +14,40 @@ of their own, to be made from a program's backward pass:
 """
 from __future__ import annotations
 
+import ctypes
+import os
+import types
+
 import moe_shared_expert_gb300 as _mse
 
+from . import _build
 from . import routed as _r
+
+_NAMES = ("moe_sort", "moe_unsort", "moe_unsort_backward", "int8_quantise", "int8_matmul", "int8_grouped_matmul", "int8_linear")
+_C = None   # the library's functions of these names, set with torch and the dtypes by _ready()
 
 
 def _ready():
+    """torch; what a call needs besides is looked up once, since a call's own Python is most of what a single token costs."""
+    global _C, _BF16, _F32, _I8, _I32, _FLOATS
     if _r.torch is None:
         _r._load()
+    if _C is None:
+        _BF16, _F32, _I8, _I32 = _r.torch.bfloat16, _r.torch.float32, (_r.torch.int8,), _r.torch.int32
+        _FLOATS = (_BF16, _F32)
+        entries = {n: getattr(_mse.lib(), n) for n in _NAMES}
+        if os.path.exists(_build.CALLS):   # the same functions without ctypes' conversions
+            from . import _calls
+            _calls.bind_rows(*(ctypes.cast(f, ctypes.c_void_p).value for f in entries.values()))
+            entries = {n: getattr(_calls, n) for n in _NAMES}
+        _C = types.SimpleNamespace(**entries)
     return _r.torch
-
-
-def _code(t, name):
-    torch = _ready()
-    if t.dtype is torch.bfloat16:
-        return _mse.BF16
-    if t.dtype is torch.float32:
-        return _mse.F32
-    raise ValueError(f"{name}: need bfloat16 or float32, got {_r._said(t)}")
 
 
 def _floats(t, name, ndim, device=None):
     """(dtype code, row pitch, shape, device index) of rows in bf16 or fp32."""
-    torch = _ready()
-    ld, shape, index = _r._rows(t, name, (torch.bfloat16, torch.float32), ndim, device)
-    return _code(t, name), ld, shape, index
+    ld, shape, index = _r._rows(t, name, _FLOATS, ndim, device)
+    return 1 if t.dtype is _F32 else 0, ld, shape, index
 
 
 def moe_sort_workspace_bytes(T: int, top_k: int, num_experts: int) -> int:
@@ -58,7 +67,7 @@ def moe_sort(x, ids, num_experts, first_expert=0, scales=None, rows=None, row_sc
     [T * top_k] (else None).  ids [T, top_k] int32 as moe_route gives them; this rank's experts are first_expert ..
     first_expert + num_experts - 1, and place is -1 for pairs of others and for ids of -1.  New rows of 1-byte values have a
     pitch of 16 bytes."""
-    torch = _ready()
+    torch = _ready() if _C is None else _r.torch
     if x is None or x.dtype.itemsize not in (1, 2, 4):
         raise ValueError(f"x: need values of 1, 2 or 4 bytes, got {_r._said(x)}")
     size = x.dtype.itemsize
@@ -66,9 +75,9 @@ def moe_sort(x, ids, num_experts, first_expert=0, scales=None, rows=None, row_sc
     if ids is None or ids.dim() != 2:
         raise ValueError(f"ids: need a 2-d tensor, got {_r._said(ids)}")
     k = ids.shape[1]
-    _r._dense(ids, "ids", torch.int32, (T, k), device)
+    _r._dense(ids, "ids", _I32, (T, k), device)
     if scales is not None:
-        _r._dense(scales, "scales", torch.float32, (T,), device)
+        _r._dense(scales, "scales", _F32, (T,), device)
     elif row_scales is not None:
         raise ValueError("row_scales: there are no scales to sort")
     if rows is None:
@@ -78,22 +87,22 @@ def moe_sort(x, ids, num_experts, first_expert=0, scales=None, rows=None, row_sc
         raise ValueError(f"rows: need {(T * k, H)}, got {_r._said(rows)}")
     if scales is not None:
         if row_scales is None:
-            row_scales = _r._empty(stream, (T * k,), torch.float32, x.device)
+            row_scales = _r._empty(stream, (T * k,), _F32, x.device)
         else:
-            _r._dense(row_scales, "row_scales", torch.float32, (T * k,), device)
+            _r._dense(row_scales, "row_scales", _F32, (T * k,), device)
     if place is None:
-        place = _r._empty(stream, (T, k), torch.int32, x.device)
+        place = _r._empty(stream, (T, k), _I32, x.device)
     else:
-        _r._dense(place, "place", torch.int32, (T, k), device)
+        _r._dense(place, "place", _I32, (T, k), device)
     if offsets is None:
-        offsets = _r._empty(stream, (max(num_experts, 0) + 1,), torch.int32, x.device)
+        offsets = _r._empty(stream, (max(num_experts, 0) + 1,), _I32, x.device)
     else:
-        _r._dense(offsets, "offsets", torch.int32, (num_experts + 1,), device)
+        _r._dense(offsets, "offsets", _I32, (num_experts + 1,), device)
     if workspace is None:
         workspace = _r._empty(stream, max(moe_sort_workspace_bytes(T, k, num_experts), 256), torch.uint8, x.device)
     else:
         _r._taken(workspace, device)
-    st = _r._C.moe_sort(x.data_ptr(), size, T, H, ldx, ids.data_ptr(), k, num_experts, first_expert, _mse._ptr(scales),
+    st = _C.moe_sort(x.data_ptr(), size, T, H, ldx, ids.data_ptr(), k, num_experts, first_expert, _mse._ptr(scales),
                         rows.data_ptr(), ldr, (T * k - 1) * ldr + H, _mse._ptr(row_scales), place.data_ptr(),
                         offsets.data_ptr(), workspace.data_ptr(), workspace.nbytes, _r._handle(stream, device))
     if st:
@@ -106,18 +115,19 @@ def moe_unsort(rows, place, weights=None, base=None, y_dtype=None, y=None, strea
 
     rows [n, H] and y are bf16 or fp32 (y: rows' type unless y_dtype or y says otherwise), place [T, top_k] as moe_sort gives
     it, weights [T, top_k] fp32 (None: 1), base [T, H] of y's type (None: 0; y itself is allowed)."""
-    torch = _ready()
+    if _C is None:
+        _ready()
     code, ldr, (n, H), device = _floats(rows, "rows", 2)
     if place is None or place.dim() != 2:
         raise ValueError(f"place: need a 2-d tensor, got {_r._said(place)}")
     T, k = place.shape
-    _r._dense(place, "place", torch.int32, (T, k), device)
+    _r._dense(place, "place", _I32, (T, k), device)
     if weights is not None:
-        _r._dense(weights, "weights", torch.float32, (T, k), device)
+        _r._dense(weights, "weights", _F32, (T, k), device)
     y, y_code = _r._out(y, y_dtype if y_dtype is not None or y is not None else rows.dtype, "y", (T, H), rows, stream)
     if base is not None:
         _r._dense(base, "base", y.dtype, (T, H), device)
-    st = _r._C.moe_unsort(rows.data_ptr(), code, n, ldr, place.data_ptr(), _mse._ptr(weights), T, H, k, _mse._ptr(base),
+    st = _C.moe_unsort(rows.data_ptr(), code, n, ldr, place.data_ptr(), _mse._ptr(weights), T, H, k, _mse._ptr(base),
                           y.data_ptr(), y_code, T * H, _r._handle(stream, device))
     if st:
         _mse._check("moe_unsort", st)
@@ -130,21 +140,22 @@ def moe_unsort_backward(dy, place, rows=None, weights=None, drows=None, dweights
     rows and weights as moe_unsort had them.  Without weights, drows alone (dweights None): rows is not needed, and drows has
     the shape of `drows`, or rows_count (default T * top_k) rows of dy's type.  Rows that are no pair's place are left as they
     were.  drows may be rows."""
-    torch = _ready()
+    if _C is None:
+        _ready()
     dy_code, ld, (T, H), device = _floats(dy, "dy", 2)
     _r._dense(dy, "dy", dy.dtype, (T, H), device)
     if place is None or place.dim() != 2:
         raise ValueError(f"place: need a 2-d tensor, got {_r._said(place)}")
     k = place.shape[1]
-    _r._dense(place, "place", torch.int32, (T, k), device)
+    _r._dense(place, "place", _I32, (T, k), device)
     if weights is not None:
-        _r._dense(weights, "weights", torch.float32, (T, k), device)
+        _r._dense(weights, "weights", _F32, (T, k), device)
         if rows is None:
             raise ValueError("rows: needed for the weights' gradient")
         if dweights is None:
-            dweights = _r._empty(stream, (T, k), torch.float32, dy.device)
+            dweights = _r._empty(stream, (T, k), _F32, dy.device)
         else:
-            _r._dense(dweights, "dweights", torch.float32, (T, k), device)
+            _r._dense(dweights, "dweights", _F32, (T, k), device)
     elif dweights is not None:
         raise ValueError("dweights: there are no weights")
     code, ldr, n = None, 0, rows_count if rows_count is not None else T * k
@@ -157,7 +168,7 @@ def moe_unsort_backward(dy, place, rows=None, weights=None, drows=None, dweights
     d_code, ldd, (nd, Hd), _ = _floats(drows, "drows", 2, device)
     if Hd != H or (code is not None and (d_code != code or nd != n)) or (rows_count is not None and nd != n):
         raise ValueError(f"drows: need {(n, H)} like rows, got {_r._said(drows)}")
-    st = _r._C.moe_unsort_backward(dy.data_ptr(), dy_code, place.data_ptr(), _mse._ptr(weights), _mse._ptr(rows), d_code, ldr, nd,
+    st = _C.moe_unsort_backward(dy.data_ptr(), dy_code, place.data_ptr(), _mse._ptr(weights), _mse._ptr(rows), d_code, ldr, nd,
                                    T, H, k, drows.data_ptr(), ldd, (nd - 1) * ldd + H, _mse._ptr(dweights),
                                    _r._handle(stream, device))
     if st:

@@ -4,7 +4,7 @@ import pytest
 torch = pytest.importorskip("torch")
 
 import moe_shared_expert_gb300 as mse
-from moe_shared_expert_gb300 import _build, routed
+from moe_shared_expert_gb300 import _build, routed, rows
 from tests.test_routed_bindings_cpu import On
 
 FAKE, FAR = 1 << 20, 1 << 50   # never read: the calls fail before; FAR lies behind everything at FAKE
@@ -108,7 +108,7 @@ def test_workspaces_of_fewer_tokens_are_no_larger(L):
 @pytest.fixture
 def reached(monkeypatch):
     _build.build()
-    routed._load()
+    rows._ready()
     names = []
 
     class C:
@@ -116,7 +116,7 @@ def reached(monkeypatch):
 
     for n in CALLS:
         setattr(C, n, staticmethod(lambda *a, n=n: names.append(n) or 0))
-    monkeypatch.setattr(routed, "_C", C)
+    monkeypatch.setattr(rows, "_C", C)
     monkeypatch.setattr(routed, "_raw_stream", lambda index: 0)
     monkeypatch.setattr(routed, "_current", lambda: 0)
     return names
@@ -207,3 +207,47 @@ def test_bindings_refuse_what_does_not_go_together(reached):
     with pytest.raises(ValueError, match="even"):
         f(**{**a, "swiglu": True})
     assert reached == []
+
+
+# ------------------------------------------------------------------------------------ the entry in C
+
+ARGUMENTS = {n: len(c) for n, c in CALLS.items()}
+FLAGS = {"moe_sort": (1, 6), "moe_unsort": (1, 8, 11), "moe_unsort_backward": (1, 5, 10), "int8_quantise": (1, 5), "int8_matmul": (10,),
+         "int8_grouped_matmul": (12,), "int8_linear": (1, 10)}
+
+
+@pytest.fixture
+def entry():
+    import ctypes
+    import os
+    import sysconfig
+    if not os.path.exists(os.path.join(sysconfig.get_paths()["include"], "Python.h")):
+        pytest.skip("no Python headers: calls go through ctypes")
+    _build.build()
+    from moe_shared_expert_gb300 import _calls
+    seen = []
+    kinds = {n: list(getattr(mse.lib(), n).argtypes) for n in CALLS}
+    made = [ctypes.CFUNCTYPE(ctypes.c_int, *kinds[n])(lambda *a, n=n: seen.append((n, a)) or 5) for n in rows._NAMES]
+    _calls.bind_rows(*(ctypes.cast(f, ctypes.c_void_p).value for f in made))
+    yield _calls, seen
+    _calls.bind_rows(*(ctypes.cast(getattr(mse.lib(), n), ctypes.c_void_p).value for n in rows._NAMES))
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_the_entry_in_c_hands_on_every_argument(entry, name):
+    calls, seen = entry
+    a = list(range(1, ARGUMENTS[name] + 1))
+    assert getattr(calls, name)(*a) == 5 and seen == [(name, tuple(a))]
+    with pytest.raises(TypeError):
+        getattr(calls, name)(*a[:-1])
+
+
+@pytest.mark.parametrize("name,at", [(n, i) for n, flags in FLAGS.items() for i in flags])
+def test_the_entry_in_c_refuses_numbers_beyond_an_int(entry, name, at):
+    calls, seen = entry
+    for number in (2 ** 32 + 1, 2 ** 31, -2 ** 31 - 1):
+        a = [0] * ARGUMENTS[name]
+        a[at] = number
+        with pytest.raises(OverflowError):
+            getattr(calls, name)(*a)
+    assert seen == []

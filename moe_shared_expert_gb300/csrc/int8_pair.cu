@@ -241,6 +241,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const uint32_t lanes = (uint32_t)(q * 32) << 16, src = tmem_base + (uint32_t)(h * kHalf) + lanes;
         const uint32_t dempty = map_to_rank(smem_u32(&ctl->dempty[h]), 0);
         float *xs = ctl->xs[warp - 4];
+        const int chunks = (kb + kChunkBlocks - 1) / kChunkBlocks;
         const int64_t tiles = total > pair ? (total - pair + n_pairs - 1) / n_pairs : 0, blocks = tiles * kb;
         // the tile whose sums come next: its place, and its factors on their way
         int64_t first = 0, out_n = 0;
@@ -258,16 +259,49 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int i = 0; i < kHalf / 32; ++i) xa[i] = i * 32 + lane < left ? g.xs[first + i * 32 + lane] : 0.f;
         };
+        // Up to two chunks are added in fp32: a sum of two integers of 24 bits is rounded as the integer is at the end.
+        const bool floats = chunks <= 2;
         int64_t id = pair, end = min(kb, kChunkBlocks);   // end: the k-block behind the next chunk, counted over all tiles
+        int64_t tiles_left = tiles, owed_at = 0;
         int done = 0;                                     // k-blocks of the tile in chunks that were added
         uint32_t use = 0;
-        bool ok = true;
+        bool ok = true, owed = false;                     // owed: a tile's sums are in registers, not yet stored
         int acc[kHalf];
 #pragma unroll
         for (int i = 0; i < kHalf; ++i) acc[i] = 0;
         open(id);
         for (int64_t i = h; ok; i += 2) {
-            while (ok && id < total && (end + 2 <= i || i >= blocks)) {
+            while (ok) {
+                // A chunk's sums are read before the second k-block behind it is converted: its MMAs wait for that.  A tile is
+                // stored after one more, so that up to four converted k-blocks are left for the MMAs meanwhile.
+                const bool due = tiles_left > 0 && (end + 2 <= i || i >= blocks);
+                if (owed && (due || i >= owed_at || i >= blocks)) {
+                    owed = false;
+#pragma unroll
+                    for (int j = 0; j < kHalf / 32; ++j) xs[j * 32 + lane] = xa[j];
+                    __syncwarp();
+                    if (out_n < g.N && left > 0) {
+                        auto value = [&](int j) { return (floats ? __int_as_float(acc[j]) : (float)acc[j]) * xs[j] * w; };
+                        if (g.out_f32) {
+                            float *out = static_cast<float *>(g.out) + first * g.N + out_n;
+#pragma unroll
+                            for (int j = 0; j < kHalf; ++j, out += g.N)
+                                if (j < left) *out = value(j);
+                        } else {
+                            uint16_t *out = static_cast<uint16_t *>(g.out) + first * g.N + out_n;
+#pragma unroll
+                            for (int j = 0; j < kHalf; ++j, out += g.N)
+                                if (j < left) *out = f32_to_bf16_bits(value(j));
+                        }
+                    }
+                    __syncwarp();
+#pragma unroll
+                    for (int j = 0; j < kHalf; ++j) acc[j] = 0;
+                    id += n_pairs;
+                    open(id);
+                    continue;
+                }
+                if (!due) break;
                 if (left > 0) {   // (a tile of up to kHalf tokens has no second half)
                     ok = wait_all(smem_u32(&ctl->dfull[h]), use & 1u, abort_flag, g);
                     if (!ok) break;
@@ -283,34 +317,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                             __syncwarp();
                             if (lane == 0) arrive_cluster_relaxed(dempty);
                         }
+                        if (floats) {
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) acc[c + j] += __float2int_rn(__uint_as_float(v[j]));
+                            for (int j = 0; j < 32; ++j)
+                                acc[c + j] = __float_as_int(__int_as_float(acc[c + j]) + __uint_as_float(v[j]));
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) acc[c + j] += __float2int_rn(__uint_as_float(v[j]));
+                        }
                     }
                 }
                 done += min(kb - done, kChunkBlocks);
                 if (done == kb) {
-#pragma unroll
-                    for (int j = 0; j < kHalf / 32; ++j) xs[j * 32 + lane] = xa[j];
-                    __syncwarp();
-                    if (out_n < g.N && left > 0) {
-                        if (g.out_f32) {
-                            float *out = static_cast<float *>(g.out) + first * g.N + out_n;
-#pragma unroll
-                            for (int j = 0; j < kHalf; ++j)
-                                if (j < left) out[j * g.N] = (float)acc[j] * xs[j] * w;
-                        } else {
-                            uint16_t *out = static_cast<uint16_t *>(g.out) + first * g.N + out_n;
-#pragma unroll
-                            for (int j = 0; j < kHalf; ++j)
-                                if (j < left) out[j * g.N] = f32_to_bf16_bits((float)acc[j] * xs[j] * w);
-                        }
-                    }
-                    __syncwarp();
-#pragma unroll
-                    for (int j = 0; j < kHalf; ++j) acc[j] = 0;
+                    owed = true;
+                    owed_at = i + 2;
                     done = 0;
-                    id += n_pairs;
-                    open(id);
+                    --tiles_left;
                 }
                 end += min(kb - done, kChunkBlocks);
             }

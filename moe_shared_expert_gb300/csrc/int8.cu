@@ -89,9 +89,10 @@ __device__ __forceinline__ void store8(void *q, int64_t at, int64_t left, bool w
 }
 
 // LANES threads to a row (32 or 256), SLOTS times eight values of each kept (0: none, rows of any length)
-// What a thread keeps of eight values: bf16 as they lie in memory (half the registers, six CTAs on an SM), or 32 bits each.
+// What a thread keeps of eight values: bf16 as they lie in memory (half the registers, six CTAs on an SM), or 32 bits each.  Rows of
+// one load a thread have eight CTAs (silu(gate) up of 16384 x 2048 in bf16 32 us, 43 with four).
 template <bool F32, bool GLU, bool HALF, int LANES, int SLOTS>
-__global__ void __launch_bounds__(kRoundThreads, F32 || GLU ? 4 : 6) round_rows_kernel(const RoundParams p, const int align,
+__global__ void __launch_bounds__(kRoundThreads, SLOTS == 1 && LANES > 32 ? 8 : F32 || GLU ? 4 : 6) round_rows_kernel(const RoundParams p, const int align,
                                                                                        const int wide) {
     constexpr bool kWide = F32 || GLU;
     constexpr int kRows = kRoundThreads / LANES, kKeep = SLOTS > 0 ? SLOTS : 1;
@@ -259,13 +260,15 @@ cudaError_t round_of(const RoundParams &p, int sm_count, bool pdl, cudaStream_t 
     const int wide = ((reinterpret_cast<uintptr_t>(p.q) | (uintptr_t)p.ldq) & 7u) == 0;
     auto with = [&](auto lanes, auto slots) {
         constexpr int kRows = kRoundThreads / decltype(lanes)::value;
-        const dim3 grid((unsigned)std::min<int64_t>((p.rows + kRows - 1) / kRows, (int64_t)sm_count * 8));
+        // (more CTAs than are resident, where a row is one load: 8192 x 7168 30 us, 33 with eight an SM)
+        const dim3 grid((unsigned)std::min<int64_t>((p.rows + kRows - 1) / kRows, (int64_t)sm_count * (decltype(slots)::value > 0 ? 32 : 8)));
         return launch_kernel(round_rows_kernel<F32, GLU, HALF, decltype(lanes)::value, decltype(slots)::value>, grid, kRoundThreads, 0,
                              pdl, 1, s, p, align, wide);
     };
     using std::integral_constant;
     if (p.K <= 256) return with(integral_constant<int, 32>(), integral_constant<int, 1>());
     if (p.K <= 1024) return with(integral_constant<int, 32>(), integral_constant<int, 4>());
+    if (p.K <= 2048) return with(integral_constant<int, 256>(), integral_constant<int, 1>());
     if (p.K <= 4096) return with(integral_constant<int, 256>(), integral_constant<int, 2>());
     if (p.K <= 8192) return with(integral_constant<int, 256>(), integral_constant<int, 4>());
     return with(integral_constant<int, 256>(), integral_constant<int, 0>());

@@ -136,19 +136,30 @@ __global__ void __launch_bounds__(kSortThreads) sort_kernel(const SortParams p) 
         }
     }
     __syncthreads();
-    // segments of kWords words a lane: (token, segment) by (token), warps of all the chunk's CTAs in turn
-    constexpr int kWords = 2;
+    // segments of kWords words a lane: (token, segment) by (token), warps of all the chunk's CTAs in turn; the next one's words are
+    // on their way while this one's are stored
+    constexpr int kWords = 4;
     const int64_t words = p.row_bytes / (int)sizeof(W);
     const int segs = (int)((words + 32 * kWords - 1) / (32 * kWords));
-    const int64_t items = (int64_t)tokens * segs;
-    for (int64_t it = (int64_t)blockIdx.y * (kSortThreads / 32) + warp; it < items; it += (int64_t)p.splits * (kSortThreads / 32)) {
-        const int t = (int)(it / segs);
+    const int64_t items = (int64_t)tokens * segs, stride = (int64_t)p.splits * (kSortThreads / 32);
+    auto fetch = [&](int64_t it, W (&v)[kWords]) {
+        const int t = (int)((uint32_t)it / (uint32_t)segs);
         const int64_t at = (it - (int64_t)t * segs) * (32 * kWords) + lane;
         const W *src = reinterpret_cast<const W *>(p.x + (t0 + t) * p.ldx) + at;
-        W v[kWords];
 #pragma unroll
         for (int i = 0; i < kWords; ++i)
             if (at + 32 * i < words) v[i] = src[32 * i];
+    };
+    int64_t it = (int64_t)blockIdx.y * (kSortThreads / 32) + warp;
+    W next[kWords];
+    if (it < items) fetch(it, next);
+    for (; it < items; it += stride) {
+        W v[kWords];
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) v[i] = next[i];
+        if (it + stride < items) fetch(it + stride, next);
+        const int t = (int)((uint32_t)it / (uint32_t)segs);
+        const int64_t at = (it - (int64_t)t * segs) * (32 * kWords) + lane;
         for (int j = 0; j < p.top_k; ++j) {
             const int row = pair_row[t * p.top_k + j];
             if (row < 0) continue;
@@ -231,12 +242,13 @@ __global__ void __launch_bounds__(256) unsort_kernel(const UnsortParams p) {
 // ---------------------------------------------------------------------------
 // drows[place[t, j]] = w[t, j] dy[t],  dweights[t, j] = <rows[place[t, j]], dy[t]>
 // ---------------------------------------------------------------------------
-// A CTA has one token at a time, kPairs of its pairs at once.
-constexpr int kBackThreads = 128;
+// A CTA has one token at a time, kPairs of its pairs at once: of kManyThreads threads, or where there are too few tokens to fill the
+// SMs of kFewThreads, which take fewer steps one after another along a row (333 tokens of 1001 with 3 of 10 experts in fp32 ... us).
+constexpr int kManyThreads = 128, kFewThreads = 512;
 
-template <typename D, typename R, int V>
-__global__ void __launch_bounds__(kBackThreads) unsort_backward_kernel(const UnsortBackwardParams p) {
-    __shared__ float part[kBackThreads / 32][kPairs];
+template <typename D, typename R, int V, int THREADS>
+__global__ void __launch_bounds__(THREADS) unsort_backward_kernel(const UnsortBackwardParams p) {
+    __shared__ float part[THREADS / 32][kPairs];
     pdl_wait();
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     const D *dy = static_cast<const D *>(p.dy);
@@ -257,7 +269,7 @@ __global__ void __launch_bounds__(kBackThreads) unsort_backward_kernel(const Uns
                 dot[j] = 0.f;
             }
             if (any)
-                for (int64_t c = (int64_t)threadIdx.x * V; c < p.H; c += kBackThreads * V) {
+                for (int64_t c = (int64_t)threadIdx.x * V; c < p.H; c += THREADS * V) {
                     const Pack<D, V> d = load_pack<D, V>(dy + t * p.H + c);
                     Pack<R, V> v[kPairs];
                     if (p.dweights)
@@ -285,10 +297,12 @@ __global__ void __launch_bounds__(kBackThreads) unsort_backward_kernel(const Uns
                 if (lane == 0) part[warp][j] = dot[j];
             }
             __syncthreads();
-            if (threadIdx.x < kPairs && j0 + threadIdx.x < p.top_k) {
-                float sum = 0.f;
-                for (int i = 0; i < kBackThreads / 32; ++i) sum += part[i][threadIdx.x];
-                p.dweights[t * p.top_k + j0 + threadIdx.x] = sum;
+            if (warp < kPairs && j0 + warp < p.top_k) {   // a pair's sum by a warp
+                constexpr int kParts = THREADS / 32;
+                float sum = lane < kParts ? part[lane][warp] : 0.f;
+#pragma unroll
+                for (int d = kParts / 2; d > 0; d >>= 1) sum += __shfl_xor_sync(~0u, sum, d);
+                if (lane == 0) p.dweights[t * p.top_k + j0 + warp] = sum;
             }
             __syncthreads();
         }
@@ -343,14 +357,19 @@ cudaError_t unsort_of(const UnsortParams &p, int v, dim3 grid, bool pdl, cudaStr
         default: return launch_kernel(unsort_kernel<R, Y, 1>, grid, 256, 0, pdl, 1, s, p);
     }
 }
-template <typename D, typename R>
-cudaError_t backward_of(const UnsortBackwardParams &p, int v, dim3 grid, bool pdl, cudaStream_t s) {
+template <typename D, typename R, int THREADS>
+cudaError_t backward_by(const UnsortBackwardParams &p, int v, dim3 grid, bool pdl, cudaStream_t s) {
     switch (v) {
-        case 8: return launch_kernel(unsort_backward_kernel<D, R, 8>, grid, kBackThreads, 0, pdl, 1, s, p);
-        case 4: return launch_kernel(unsort_backward_kernel<D, R, 4>, grid, kBackThreads, 0, pdl, 1, s, p);
-        case 2: return launch_kernel(unsort_backward_kernel<D, R, 2>, grid, kBackThreads, 0, pdl, 1, s, p);
-        default: return launch_kernel(unsort_backward_kernel<D, R, 1>, grid, kBackThreads, 0, pdl, 1, s, p);
+        case 8: return launch_kernel(unsort_backward_kernel<D, R, 8, THREADS>, grid, THREADS, 0, pdl, 1, s, p);
+        case 4: return launch_kernel(unsort_backward_kernel<D, R, 4, THREADS>, grid, THREADS, 0, pdl, 1, s, p);
+        case 2: return launch_kernel(unsort_backward_kernel<D, R, 2, THREADS>, grid, THREADS, 0, pdl, 1, s, p);
+        default: return launch_kernel(unsort_backward_kernel<D, R, 1, THREADS>, grid, THREADS, 0, pdl, 1, s, p);
     }
+}
+template <typename D, typename R>
+cudaError_t backward_of(const UnsortBackwardParams &p, int v, int sm_count, bool pdl, cudaStream_t s) {
+    const dim3 grid((unsigned)std::min<int64_t>(p.T, (int64_t)sm_count * 16));
+    return p.T < sm_count * 4 ? backward_by<D, R, kFewThreads>(p, v, grid, pdl, s) : backward_by<D, R, kManyThreads>(p, v, grid, pdl, s);
 }
 }  // namespace
 
@@ -372,10 +391,9 @@ cudaError_t launch_unsort_backward(const UnsortBackwardParams &p, int sm_count, 
     w.tensor(p.rows, p.ldr, p.rows_f32 ? 4 : 2);
     w.tensor(p.drows, p.ldd, p.rows_f32 ? 4 : 2);
     const int v = w.width();
-    const dim3 grid((unsigned)std::min<int64_t>(p.T, (int64_t)sm_count * 16));
     if (p.dy_f32)
-        return p.rows_f32 ? backward_of<float, float>(p, v, grid, pdl, s) : backward_of<float, uint16_t>(p, v, grid, pdl, s);
-    return p.rows_f32 ? backward_of<uint16_t, float>(p, v, grid, pdl, s) : backward_of<uint16_t, uint16_t>(p, v, grid, pdl, s);
+        return p.rows_f32 ? backward_of<float, float>(p, v, sm_count, pdl, s) : backward_of<float, uint16_t>(p, v, sm_count, pdl, s);
+    return p.rows_f32 ? backward_of<uint16_t, float>(p, v, sm_count, pdl, s) : backward_of<uint16_t, uint16_t>(p, v, sm_count, pdl, s);
 }
 
 }  // namespace sorted

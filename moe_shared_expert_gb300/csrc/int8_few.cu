@@ -1,6 +1,6 @@
-// Product in 8-bit integers for up to eight token rows of a group: every weight byte goes from memory into a register once and
+// Product in 8-bit integers for up to four token rows of a group: every weight byte goes from memory into a register once and
 // meets all tokens there (four products an instruction).  Nothing but the launch stands before the weights' loads: no tensor
-// memory, no conversion, and of a plain product no second kernel for the rounding of its tokens.
+// memory, no conversion, and of one token's plain product no second kernel for its rounding.
 //
 // A warp has R weight rows at a time, a lane 16 bytes of every 512, U of those steps on their way while the U before them
 // are multiplied.  The tokens lie in shared memory as 8-bit integers; R rows share what a lane reads of them.
@@ -241,19 +241,20 @@ cudaError_t run(const FewParams &p, int slots, int sm_count, bool pdl, cudaStrea
     return launch_kernel(int8_few_kernel<TM, R, U, ROUND>, grid, kFewThreads, smem, pdl, 1, s, p);
 }
 
-template <bool ROUND>
+// One weight row at a time while the rows last for every warp of the grid once, two, which share what is read of the tokens, from
+// twice as many on.  (us with one and two: 4 x 2112 x 7168 7.4, 7.7; 4 x 12288 x 7168 23.3, 20.2; 2 x 7168 x 6144 10.9, 11.0.)
 cudaError_t run_rows(const FewParams &p, int tile_rows, int slots, int sm_count, bool pdl, cudaStream_t s) {
+    const bool two = p.g.N * slots >= 4 * (int64_t)sm_count * kWarps;
     switch (tile_rows) {
-        case 1: return run<1, 1, 8, ROUND>(p, slots, sm_count, pdl, s);
-        case 2: return run<2, 2, 4, ROUND>(p, slots, sm_count, pdl, s);
-        case 4: return run<4, 4, 2, ROUND>(p, slots, sm_count, pdl, s);
-        default: return run<8, 4, 2, ROUND>(p, slots, sm_count, pdl, s);
+        case 1: return p.x ? run<1, 1, 8, true>(p, slots, sm_count, pdl, s) : run<1, 1, 8, false>(p, slots, sm_count, pdl, s);
+        case 2: return two ? run<2, 2, 4, false>(p, slots, sm_count, pdl, s) : run<2, 1, 8, false>(p, slots, sm_count, pdl, s);
+        default: return two ? run<4, 2, 4, false>(p, slots, sm_count, pdl, s) : run<4, 1, 8, false>(p, slots, sm_count, pdl, s);
     }
 }
 
 }  // namespace
 
-bool int8_few_serves(int tile_rows, int64_t K) { return tile_rows <= 8 && tile_rows * ((K + kStep - 1) / kStep * kStep) <= kInt8FewBytes; }
+bool int8_few_serves(int tile_rows, int64_t K) { return tile_rows <= 4 && tile_rows * ((K + kStep - 1) / kStep * kStep) <= kInt8FewBytes; }
 
 cudaError_t launch_int8_few(const Int8Gemm &g, int tile_rows, const void *x, int f32, int64_t ldx, bool weights_early, int sm_count,
                             bool pdl, cudaStream_t s) {
@@ -266,7 +267,7 @@ cudaError_t launch_int8_few(const Int8Gemm &g, int tile_rows, const void *x, int
     p.weights_early = weights_early;
     const int64_t per = (g.T + tile_rows - 1) / tile_rows;
     const int slots = (int)(g.offsets ? std::min<int64_t>(g.T, g.T / tile_rows + std::min<int64_t>(g.groups, g.T)) : per);
-    return x ? run_rows<true>(p, tile_rows, slots, sm_count, pdl, s) : run_rows<false>(p, tile_rows, slots, sm_count, pdl, s);
+    return run_rows(p, tile_rows, slots, sm_count, pdl, s);
 }
 
 }  // namespace sorted

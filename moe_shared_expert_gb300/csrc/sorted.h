@@ -90,8 +90,8 @@ cudaError_t launch_int8_simt(const Int8Gemm &g, bool pdl, cudaStream_t s);
 // int8 rows to the same integers in fp16; rows from *last on are left out
 cudaError_t launch_int8_expand(const int8_t *x, int64_t ldx, int64_t rows, int64_t K, const int32_t *last, uint16_t *out,
                                int64_t ldo, int sm_count, bool pdl, cudaStream_t s);
-// Kernel for token tiles of 1, 2, 4 or 8 rows, whose tokens fit kInt8FewBytes of shared memory; with x (bf16 or fp32, of a plain
-// product) it rounds the tokens itself.
+// Kernel for token tiles of 1, 2 or 4 rows, whose tokens fit kInt8FewBytes of shared memory; with x (bf16 or fp32, of a plain
+// product of one row) it rounds the token itself.
 constexpr int kInt8FewBytes = 100 * 1024;
 bool int8_few_serves(int tile_rows, int64_t K);
 cudaError_t launch_int8_few(const Int8Gemm &g, int tile_rows, const void *x, int f32, int64_t ldx, bool weights_early, int sm_count,

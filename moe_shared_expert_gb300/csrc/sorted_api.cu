@@ -79,17 +79,24 @@ bool apart(const Int8Gemm &g) {
 }
 int64_t pitch16(int64_t K) { return (K + 63) / 64 * 64; }   // of tokens in fp16
 
-// Token rows of a tile, by the rows expected of a group: 1 to 8 take the kernel for few, 16 to 128 the swap-AB kernel, 256 the
-// CTA-pair kernel.
-constexpr int kFewRows = 8;
-int tile_rows_of(int64_t rows, int64_t K) {
-    const int few = rows <= 1 ? 1 : rows <= 2 ? 2 : rows <= 4 ? 4 : 8;
-    if (rows <= kFewRows && int8_few_serves(few, K)) return few;
+// Token rows of a tile: up to 4 the kernel for few, 16 to 128 the swap-AB kernel, 256 the CTA-pair kernel.
+//
+// A plain product by its rows.  (us with the kernel for few, of int8 rows, and the swap-AB kernel: 2 x 2112 x 7168 5.6, 9.8; 4 x
+// 2112 x 7168 7.4, 9.9; 4 x 12288 x 7168 20.2, 20.5; 8 x 2112 x 7168 10.7, 9.9; 8 x 12288 x 7168 28, 20.6.)  Grouped rows by those
+// expected of a group, but for a token's or two's rows, of which few groups have more than two.  (us with tiles of 2, 4 and 16, 8
+// experts a token: 1 token of 32 x 4096 x 7168 40.8, 46.1, 43.4, of 32 x 7168 x 2048 22.2, 22.5, 27.7; 2 tokens of 32 x 4096 x
+// 7168 69, 70, 76; 4 tokens 113, 119, 104; 16 tokens of 32 of 128 experts 233, 181, 94.)
+constexpr int64_t kFewRows = 4, kFewGroupedRows = 16;
+int tile_rows_of(const Int8Gemm &g) {
+    const int few = g.offsets ? (g.T <= kFewGroupedRows ? 2 : 0) : g.T <= kFewRows ? (g.T > 2 ? 4 : (int)g.T) : 0;
+    if (few > 0 && int8_few_serves(few, g.K)) return few;
+    const int64_t rows = g.T / g.groups;
     return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : rows <= 128 ? 128 : 256;
 }
 
-// One launch, whose kernel rounds the tokens itself: every CTA rounds all of them.
-bool rounds_itself(int tile_rows) { return tile_rows <= 2; }
+// One launch, whose kernel rounds the token itself: every CTA rounds it.  (us with one launch and two: 1 x 2112 x 7168 6.3, 7.6; two
+// tokens 8.3, 8.1.)
+bool rounds_itself(int tile_rows) { return tile_rows == 1; }
 
 bool tensorcore_ok(const Int8Gemm &g) {
     return (reinterpret_cast<uintptr_t>(g.wq) & 15u) == 0 && g.ldw % 16 == 0 && (g.N + 127) / 128 <= 65535 &&
@@ -109,8 +116,8 @@ mse_status run_product(Int8Gemm g, const DeviceView &d, void *workspace, cudaStr
     mse_status st = choose_tensorcore(tensorcore_ok(g), &fast);
     if (st != MSE_OK) return st;
     if (!fast) return from_cuda(launch_int8_simt(g, pdl_enabled(), s));
-    const int tile_rows = tile_rows_of(g.T / g.groups, g.K);
-    if (tile_rows <= 8) return from_cuda(launch_int8_few(g, tile_rows, nullptr, 0, 0, false, d.sm_count, pdl_enabled(), s));
+    const int tile_rows = tile_rows_of(g);
+    if (tile_rows <= 4) return from_cuda(launch_int8_few(g, tile_rows, nullptr, 0, 0, false, d.sm_count, pdl_enabled(), s));
     g.ldx16 = pitch16(g.K);
     uint16_t *x16 = static_cast<uint16_t *>(workspace);
     st = from_cuda(launch_int8_expand(g.xq, g.ldx, g.T, g.K, g.offsets ? g.offsets + g.groups : nullptr, x16, g.ldx16, d.sm_count,
@@ -295,7 +302,7 @@ mse_status int8_linear(const void *x, mse_dtype x_dtype, int64_t ldx, const int8
     g.err = d.err;
     bool fast = false;
     if ((st = choose_tensorcore(tensorcore_ok(g), &fast)) != MSE_OK) return st;
-    const int tile_rows = fast ? tile_rows_of(T, K) : 0;
+    const int tile_rows = fast ? tile_rows_of(g) : 0;
     const int64_t x_size = size_of(x_dtype);
     // (y over x: the product's CTAs would write y while others still round x)
     if (fast && rounds_itself(tile_rows) && disjoint(x, span(T, K, ldx, x_size), y, T * N * size_of(y_dtype)))
@@ -304,11 +311,11 @@ mse_status int8_linear(const void *x, mse_dtype x_dtype, int64_t ldx, const int8
     p.x = x; p.rows = T; p.K = K; p.ldx = ldx;
     p.f32 = x_dtype == MSE_F32; p.swiglu = 0;
     p.last = nullptr;
-    p.q = workspace; p.ldq = pitch16(K); p.half_out = fast && tile_rows > 8; p.scales = xs;
+    p.q = workspace; p.ldq = pitch16(K); p.half_out = fast && tile_rows > 4; p.scales = xs;
     if ((st = from_cuda(launch_int8_round(p, d.sm_count, pdl_enabled(), s))) != MSE_OK) return st;
     g.xq = static_cast<const int8_t *>(workspace); g.ldx = p.ldq;
     if (!fast) return from_cuda(launch_int8_simt(g, pdl_enabled(), s));
-    if (tile_rows <= 8) return from_cuda(launch_int8_few(g, tile_rows, nullptr, 0, 0, true, d.sm_count, pdl_enabled(), s));
+    if (tile_rows <= 4) return from_cuda(launch_int8_few(g, tile_rows, nullptr, 0, 0, true, d.sm_count, pdl_enabled(), s));
     g.x16 = static_cast<const uint16_t *>(workspace); g.ldx16 = p.ldq;
     return run_tensorcore(g, tile_rows, d, s);
 }

@@ -1,4 +1,4 @@
-// Product in 8-bit integers for few token rows: weights fill the 128-row side of the MMA, up to 128 tokens are its columns.
+// Product in 8-bit integers for few token rows: weights fill the 128-row side of the MMA, up to 64 tokens are its columns.
 //
 // A CTA owns one 128-row weight tile and one token tile; the k-blocks may be split over a cluster, whose CTAs exchange their
 // integer sums through distributed shared memory and each finish a slice of the token columns.
@@ -33,8 +33,8 @@ struct ColsCtrl {
 template <int BN_>
 struct Cols {
     static constexpr int BN = BN_;
-    static constexpr int CTAS = BN <= 64 ? 2 : 1;                        // resident per SM
-    static constexpr int NA = BN <= 64 ? 3 : 4;                          // k-blocks of weights in TMEM
+    static constexpr int CTAS = 2;                                       // resident per SM (the ring may take a whole SM)
+    static constexpr int NA = 3;                                         // k-blocks of weights in TMEM
     static constexpr int ND = BN == 64 ? 1 : 2;                          // chunks of sums there
     static constexpr int CPT = BN / 2;                                   // token columns a thread adds
     static constexpr int TMEM = pow2_at_least(ND * BN + NA * (int)kATmem);
@@ -46,8 +46,8 @@ struct Cols {
         const int n = (int)((budget - FIXED) / STAGE);
         return n < kMaxStages ? n : kMaxStages;
     }
-    // stages of the ring with CTAS CTAs on an SM, or one
-    static constexpr int PART = fit((CTAS == 2 ? 113 : 227) * 1024), WHOLE = fit(227 * 1024);
+    // stages of the ring with two CTAs on an SM, or one
+    static constexpr int PART = fit(113 * 1024), WHOLE = fit(227 * 1024);
     static_assert(NA <= PART, "the order of waits before a conversion");
     // the exchange of a split tile uses the ring: at most BN / 4 + 7 groups of four columns
     static_assert((BN / 4 + 7) * 2048 <= PART * STAGE, "exchange");
@@ -294,10 +294,11 @@ cudaError_t run(const CUtensorMap &tw, const CUtensorMap &tx, const Int8Gemm &g,
 
 }  // namespace
 
-// CTAs that share a tile's k-blocks: as many as find room, two on an SM (one of 128 tokens), four k-blocks each at least.
-int int8_cols_parts(int64_t tiles, int kb, int tile_rows, int sm_count) {
-    const int64_t ctas = (tile_rows <= 64 ? 19 : 10) * (int64_t)sm_count / 10;
-    const int64_t room = std::min<int64_t>(ctas / std::max<int64_t>(1, tiles), kb / 4);
+// CTAs that share a tile's k-blocks: as many as find room, two on an SM (nearly), four k-blocks each at least.  (us with 1, 2, 3 and
+// 4 parts: 16 x 12288 x 7168, 96 tiles, 24.6, 21.5, 21.1, 25.0; 64 x 12288 x 7168 28.7, 27.5, 26.1, 29.3; 16 x 2112 x 7168, 17 tiles,
+// 21.6, 14.2, .., 10.5, and with eight 9.9; 64 x 7168 x 6144, 56 tiles, 23.5, 19.6, .., 16.4.)
+int int8_cols_parts(int64_t tiles, int kb, int sm_count) {
+    const int64_t room = std::min<int64_t>(19 * (int64_t)sm_count / 10 / std::max<int64_t>(1, tiles), kb / 4);
     return (int)std::min<int64_t>(std::max<int64_t>(room, 1), 16 * tiles <= sm_count && kb >= 24 ? 8 : 5);
 }
 
@@ -311,7 +312,7 @@ mse_status launch_int8_cols(const Int8Gemm &g, int tile_rows, int sm_count, bool
     // grouped: every group may begin a tile of its own; as many as there are rows at most
     const int64_t slots = g.offsets ? std::min<int64_t>(g.T, g.T / tile_rows + std::min<int64_t>(g.groups, g.T)) : per;
     if (row_tiles > 65535 || slots > 65535) return MSE_ERR_UNSUPPORTED_SHAPE;
-    const int parts = int8_cols_parts(row_tiles * slots, kb, tile_rows, sm_count);
+    const int parts = int8_cols_parts(row_tiles * slots, kb, sm_count);
     const int stream_weights = slots == 1 || (g.offsets && g.T <= (int64_t)tile_rows * g.groups);
     const bool whole = parts == 1 && row_tiles * slots <= sm_count;
     cudaError_t e;
@@ -321,8 +322,7 @@ mse_status launch_int8_cols(const Int8Gemm &g, int tile_rows, int sm_count, bool
     switch (tile_rows) {
         case 16: e = with(Cols<16>()); break;
         case 32: e = with(Cols<32>()); break;
-        case 64: e = with(Cols<64>()); break;
-        default: e = with(Cols<128>()); break;
+        default: e = with(Cols<64>()); break;
     }
     return e == cudaSuccess ? MSE_OK : MSE_ERR_CUDA;
 }

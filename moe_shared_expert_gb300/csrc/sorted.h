@@ -96,11 +96,11 @@ constexpr int kInt8FewBytes = 100 * 1024;
 bool int8_few_serves(int tile_rows, int64_t K);
 cudaError_t launch_int8_few(const Int8Gemm &g, int tile_rows, const void *x, int f32, int64_t ldx, bool weights_early, int sm_count,
                             bool pdl, cudaStream_t s);
-// Tensor-core kernel for token tiles of 16, 32, 64 or 128 rows (weights on the 128-row side).
+// Tensor-core kernel for token tiles of 16, 32 or 64 rows (weights on the 128-row side).
 mse_status launch_int8_cols(const Int8Gemm &g, int tile_rows, int sm_count, bool pdl, cudaStream_t s);
 // Tensor-core kernel for token tiles of 256 rows (a CTA pair per 256 x 256 tile).
 mse_status launch_int8_pair(const Int8Gemm &g, int sm_count, bool pdl, cudaStream_t s);
-int int8_cols_parts(int64_t tiles, int kb, int tile_rows, int sm_count);
+int int8_cols_parts(int64_t tiles, int kb, int sm_count);
 
 }  // namespace sorted
 }  // namespace mse

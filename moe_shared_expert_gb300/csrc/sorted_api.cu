@@ -79,19 +79,34 @@ bool apart(const Int8Gemm &g) {
 }
 int64_t pitch16(int64_t K) { return (K + 63) / 64 * 64; }   // of tokens in fp16
 
-// Token rows of a tile: up to 4 the kernel for few, 16 to 128 the swap-AB kernel, 256 the CTA-pair kernel.
+// Token rows of a tile: up to 4 the kernel for few, 16 to 64 the swap-AB kernel, 256 the CTA-pair kernel.
 //
 // A plain product by its rows.  (us with the kernel for few, of int8 rows, and the swap-AB kernel: 2 x 2112 x 7168 5.6, 9.8; 4 x
 // 2112 x 7168 7.4, 9.9; 4 x 12288 x 7168 20.2, 20.5; 8 x 2112 x 7168 10.7, 9.9; 8 x 12288 x 7168 28, 20.6.)  Grouped rows by those
 // expected of a group, but for a token's or two's rows, of which few groups have more than two.  (us with tiles of 2, 4 and 16, 8
 // experts a token: 1 token of 32 x 4096 x 7168 40.8, 46.1, 43.4, of 32 x 7168 x 2048 22.2, 22.5, 27.7; 2 tokens of 32 x 4096 x
 // 7168 69, 70, 76; 4 tokens 113, 119, 104; 16 tokens of 32 of 128 experts 233, 181, 94.)
+//
+// More rows take tiles of 64 on the swap-AB kernel or the CTA pairs, whichever is expected to be done first, in units of 10 ns: two
+// swap-AB CTAs on an SM take 0.6 us for a k-block each and 4 us for a tile besides, 2.5 more where its k-blocks are split; a CTA pair
+// 0.75 us for a k-block and 5 us in all.  (us with tiles of 64 and 256: 512 x 2112 x 7168 24.7, 45.2; 1024 x 2112 x 7168 37.8, 47.2;
+// 160 x 12288 x 7168 38.1, 46.6; 320 x 12288 x 7168 69, 83; 400 x 4096 x 2048 15.0, 17.1; 800 x 4096 x 2048 24.8, 17.9; 32 experts of
+// 4096 x 2048 with 32, 64, 128 and 192 rows each 61, 82; 79, 83; 127, 92; 172, 116.  Tiles of 128 were never the fastest by more
+// than a few per cent.)
 constexpr int64_t kFewRows = 4, kFewGroupedRows = 16;
-int tile_rows_of(const Int8Gemm &g) {
+int tile_rows_of(const Int8Gemm &g, int sm_count) {
     const int few = g.offsets ? (g.T <= kFewGroupedRows ? 2 : 0) : g.T <= kFewRows ? (g.T > 2 ? 4 : (int)g.T) : 0;
     if (few > 0 && int8_few_serves(few, g.K)) return few;
     const int64_t rows = g.T / g.groups;
-    return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : rows <= 128 ? 128 : 256;
+    if (rows <= (g.offsets ? 8 : 16)) return 16;
+    if (rows <= (g.offsets ? 24 : 32)) return 32;
+    // a group's last tile is half full on the average; a pair's tile of up to 128 rows counts half
+    const int64_t kb = (g.K + 127) / 128, part = g.offsets ? g.groups / 2 : 0;
+    const int64_t cols = ((g.T + 63) / 64 + part) * ((g.N + 127) / 128), halves = ((g.T + 127) / 128 + part) * ((g.N + 255) / 256);
+    const int64_t parts = int8_cols_parts(cols, (int)kb, sm_count);
+    const int64_t waves = (cols * parts + 2 * sm_count - 1) / (2 * sm_count), rounds = ((halves + 1) / 2 + sm_count / 2 - 1) / (sm_count / 2);
+    const int64_t cols_time = waves * (kb * 60 / parts + 400 + (parts > 1 ? 250 : 0)), pair_time = rounds * kb * 75 + 500;
+    return pair_time < cols_time ? 256 : 64;
 }
 
 // One launch, whose kernel rounds the token itself: every CTA rounds it.  (us with one launch and two: 1 x 2112 x 7168 6.3, 7.6; two
@@ -116,7 +131,7 @@ mse_status run_product(Int8Gemm g, const DeviceView &d, void *workspace, cudaStr
     mse_status st = choose_tensorcore(tensorcore_ok(g), &fast);
     if (st != MSE_OK) return st;
     if (!fast) return from_cuda(launch_int8_simt(g, pdl_enabled(), s));
-    const int tile_rows = tile_rows_of(g);
+    const int tile_rows = tile_rows_of(g, d.sm_count);
     if (tile_rows <= 4) return from_cuda(launch_int8_few(g, tile_rows, nullptr, 0, 0, false, d.sm_count, pdl_enabled(), s));
     g.ldx16 = pitch16(g.K);
     uint16_t *x16 = static_cast<uint16_t *>(workspace);
@@ -302,7 +317,7 @@ mse_status int8_linear(const void *x, mse_dtype x_dtype, int64_t ldx, const int8
     g.err = d.err;
     bool fast = false;
     if ((st = choose_tensorcore(tensorcore_ok(g), &fast)) != MSE_OK) return st;
-    const int tile_rows = fast ? tile_rows_of(g) : 0;
+    const int tile_rows = fast ? tile_rows_of(g, d.sm_count) : 0;
     const int64_t x_size = size_of(x_dtype);
     // (y over x: the product's CTAs would write y while others still round x)
     if (fast && rounds_itself(tile_rows) && disjoint(x, span(T, K, ldx, x_size), y, T * N * size_of(y_dtype)))

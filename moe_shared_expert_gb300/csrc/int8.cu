@@ -177,36 +177,50 @@ __global__ void __launch_bounds__(kRoundThreads, SLOTS == 1 && LANES > 32 ? 8 : 
 // ---------------------------------------------------------------------------
 // int8 rows to the same integers in fp16, for the tensor-core kernels
 // ---------------------------------------------------------------------------
-// 16 values a thread; WIDE: rows begin at multiples of 16 bytes (out's always do)
+// 16 values a thread, two such runs on their way at once; WIDE: rows begin at multiples of 16 bytes (out's always do).
+constexpr int kExpandRuns = 2;
+
 template <bool WIDE>
 __global__ void __launch_bounds__(256) expand_kernel(const int8_t *x, int64_t ldx, int64_t rows, int64_t K, const int32_t *last,
                                                      uint16_t *out, int64_t ldo) {
     pdl_wait();
     pdl_launch_dependents();
     if (last) rows = min((int64_t)max(*last, 0), rows);
-    const int64_t per = (K + 15) / 16, items = rows * per;
-    for (int64_t it = (int64_t)blockIdx.x * 256 + threadIdx.x; it < items; it += (int64_t)gridDim.x * 256) {
-        const int64_t r = it / per, k = (it - r * per) * 16;
-        const int8_t *src = x + r * ldx + k;
-        uint32_t w[4], h[8];
-        if (WIDE && k + 16 <= K) {
-            const uint4 v = *reinterpret_cast<const uint4 *>(src);
-            w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
-        } else {
+    const uint32_t per = (uint32_t)((K + 15) / 16);   // (K below 2^17)
+    const int64_t items = rows * per, stride = (int64_t)gridDim.x * 256;
+    for (int64_t it = (int64_t)blockIdx.x * 256 + threadIdx.x; it < items; it += stride * kExpandRuns) {
+        uint32_t w[kExpandRuns][4];
+        int64_t to[kExpandRuns];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                w[i] = 0;
+        for (int u = 0; u < kExpandRuns; ++u) {
+            const int64_t i = it + u * stride;
+            if (i >= items) break;
+            const int64_t r = items >> 32 ? i / per : (uint32_t)i / per;
+            const int64_t k = (i - r * per) * 16;
+            const int8_t *src = x + r * ldx + k;
+            to[u] = r * ldo + k;
+            if (WIDE && k + 16 <= K) {
+                const uint4 v = *reinterpret_cast<const uint4 *>(src);
+                w[u][0] = v.x, w[u][1] = v.y, w[u][2] = v.z, w[u][3] = v.w;
+            } else {
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    if (k + 4 * i + j < K) w[i] |= (uint32_t)(uint8_t)src[4 * i + j] << (8 * j);
+                for (int j = 0; j < 16; ++j) {
+                    if (j % 4 == 0) w[u][j / 4] = 0;
+                    if (k + j < K) w[u][j / 4] |= (uint32_t)(uint8_t)src[j] << (j % 4 * 8);
+                }
             }
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) half_of_bytes(w[i], h[2 * i], h[2 * i + 1]);
-        // (out's pitch is a multiple of 64 values: a run that begins inside a row is written whole)
-        uint4 *dst = reinterpret_cast<uint4 *>(out + r * ldo + k);
-        dst[0] = make_uint4(h[0], h[1], h[2], h[3]);
-        dst[1] = make_uint4(h[4], h[5], h[6], h[7]);
+        for (int u = 0; u < kExpandRuns; ++u) {
+            if (it + u * stride >= items) break;
+            uint32_t h[8];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) half_of_bytes(w[u][j], h[2 * j], h[2 * j + 1]);
+            // (out's pitch is a multiple of 64 values: a run that begins inside a row is written whole)
+            uint4 *dst = reinterpret_cast<uint4 *>(out + to[u]);
+            dst[0] = make_uint4(h[0], h[1], h[2], h[3]);
+            dst[1] = make_uint4(h[4], h[5], h[6], h[7]);
+        }
     }
 }
 
@@ -283,7 +297,7 @@ cudaError_t launch_int8_round(const RoundParams &p, int sm_count, bool pdl, cuda
 
 cudaError_t launch_int8_expand(const int8_t *x, int64_t ldx, int64_t rows, int64_t K, const int32_t *last, uint16_t *out,
                                int64_t ldo, int sm_count, bool pdl, cudaStream_t s) {
-    const dim3 grid((unsigned)std::min<int64_t>((rows * ((K + 15) / 16) + 255) / 256, (int64_t)sm_count * 8));
+    const dim3 grid((unsigned)std::min<int64_t>((rows * ((K + 15) / 16) + 255) / 256, (int64_t)sm_count * 16));
     const bool wide = ((reinterpret_cast<uintptr_t>(x) | (uint64_t)ldx) & 15u) == 0;
     return launch_kernel(wide ? expand_kernel<true> : expand_kernel<false>, grid, 256, 0, pdl, 1, s, x, ldx, rows, K, last, out, ldo);
 }

@@ -87,9 +87,28 @@ __global__ void __launch_bounds__(kSortThreads) sort_kernel(const SortParams p) 
     int *total = sort_smem, *before = total + p.E, *of_warp = before + p.E;   // of_warp: [warps x E]
     __shared__ int pair_row[kSortThreads];
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
-    pdl_wait();
+    if (!p.hist) pdl_wait();
     const int64_t t0 = (int64_t)blockIdx.x * p.chunk, i0 = t0 * p.top_k;
     const int tokens = (int)min((int64_t)p.chunk, p.T - t0), mine = tokens * p.top_k;
+    // The rows go by segments of kWords words a lane: (token, segment) by (token), warps of all the chunk's CTAs in turn; the next
+    // one's words are on their way while one's are stored, and the first one's while places are counted.  (Behind the kernels that
+    // count, which began after everything before the call was complete, x may be read before the wait.)
+    constexpr int kWords = 4;
+    const int64_t words = p.row_bytes / (int)sizeof(W);
+    const int segs = (int)((words + 32 * kWords - 1) / (32 * kWords));
+    const int64_t items = (int64_t)tokens * segs, stride = (int64_t)p.splits * (kSortThreads / 32);
+    auto fetch = [&](int64_t it, W (&v)[kWords]) {
+        const int t = (int)((uint32_t)it / (uint32_t)segs);
+        const int64_t at = (it - (int64_t)t * segs) * (32 * kWords) + lane;
+        const W *src = reinterpret_cast<const W *>(p.x + (t0 + t) * p.ldx) + at;
+#pragma unroll
+        for (int i = 0; i < kWords; ++i)
+            if (at + 32 * i < words) v[i] = src[32 * i];
+    };
+    int64_t it = (int64_t)blockIdx.y * (kSortThreads / 32) + warp;
+    W next[kWords];
+    if (it < items) fetch(it, next);
+    if (p.hist) pdl_wait();
     for (int i = tid; i < kSortThreads / 32 * p.E; i += kSortThreads) of_warp[i] = 0;
     if (p.hist) {
         for (int e = tid; e < p.E; e += kSortThreads) {
@@ -136,23 +155,6 @@ __global__ void __launch_bounds__(kSortThreads) sort_kernel(const SortParams p) 
         }
     }
     __syncthreads();
-    // segments of kWords words a lane: (token, segment) by (token), warps of all the chunk's CTAs in turn; the next one's words are
-    // on their way while this one's are stored
-    constexpr int kWords = 4;
-    const int64_t words = p.row_bytes / (int)sizeof(W);
-    const int segs = (int)((words + 32 * kWords - 1) / (32 * kWords));
-    const int64_t items = (int64_t)tokens * segs, stride = (int64_t)p.splits * (kSortThreads / 32);
-    auto fetch = [&](int64_t it, W (&v)[kWords]) {
-        const int t = (int)((uint32_t)it / (uint32_t)segs);
-        const int64_t at = (it - (int64_t)t * segs) * (32 * kWords) + lane;
-        const W *src = reinterpret_cast<const W *>(p.x + (t0 + t) * p.ldx) + at;
-#pragma unroll
-        for (int i = 0; i < kWords; ++i)
-            if (at + 32 * i < words) v[i] = src[32 * i];
-    };
-    int64_t it = (int64_t)blockIdx.y * (kSortThreads / 32) + warp;
-    W next[kWords];
-    if (it < items) fetch(it, next);
     for (; it < items; it += stride) {
         W v[kWords];
 #pragma unroll

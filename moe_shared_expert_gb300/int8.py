@@ -82,7 +82,7 @@ def int8_matmul(xq, xs, wq, ws, out_dtype=None, out=None, workspace=None, stream
         raise ValueError(f"xq and wq differ in K: {K} and {Kw}")
     _r._dense(xs, "xs", _s._F32, (T,), device)
     _r._dense(ws, "ws", _s._F32, (N,), device)
-    out, code = _r._out(out, out_dtype, "out", (T, N), xq, stream)
+    out, code = _s._out(out, out_dtype if out is not None or out_dtype is not None else _s._BF16, "out", (T, N), xq, stream, device)
     space = _space(workspace, stream, xq, device, T, N, K)
     st = _s._C.int8_matmul(xq.data_ptr(), ldx, xs.data_ptr(), wq.data_ptr(), ldw, ws.data_ptr(), T, N, K, out.data_ptr(), code,
                            T * N, space.data_ptr(), space.nbytes, _r._handle(stream, device))
@@ -103,7 +103,7 @@ def int8_grouped_matmul(xq, xs, offsets, wq, ws, out_dtype=None, out=None, works
     _r._dense(xs, "xs", _s._F32, (T,), device)
     _r._dense(ws, "ws", _s._F32, (G, N), device)
     _r._dense(offsets, "offsets", torch.int32, (G + 1,), device)
-    out, code = _r._out(out, out_dtype, "out", (T, N), xq, stream)
+    out, code = _s._out(out, out_dtype if out is not None or out_dtype is not None else _s._BF16, "out", (T, N), xq, stream, device)
     space = _space(workspace, stream, xq, device, T, N, K, G)
     st = _s._C.int8_grouped_matmul(xq.data_ptr(), ldx, xs.data_ptr(), offsets.data_ptr(), G, wq.data_ptr(), ldw, ws.data_ptr(),
                                    T, N, K, out.data_ptr(), code, T * N, space.data_ptr(), space.nbytes,
@@ -122,7 +122,7 @@ def int8_linear(x, wq, ws, y_dtype=None, y=None, workspace=None, stream=None):
     if K != Kw:
         raise ValueError(f"x and wq differ in K: {K} and {Kw}")
     _r._dense(ws, "ws", _s._F32, (N,), device)
-    y, code = _r._out(y, y_dtype, "y", (T, N), x, stream)
+    y, code = _s._out(y, y_dtype if y is not None or y_dtype is not None else _s._BF16, "y", (T, N), x, stream, device)
     space = _space(workspace, stream, x, device, T, N, K)
     st = _s._C.int8_linear(x.data_ptr(), x_code, ldx, wq.data_ptr(), ldw, ws.data_ptr(), T, N, K, y.data_ptr(), code, T * N,
                            space.data_ptr(), space.nbytes, _r._handle(stream, device))

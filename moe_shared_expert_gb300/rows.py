@@ -50,6 +50,19 @@ def _floats(t, name, ndim, device=None):
     return 1 if t.dtype is _F32 else 0, ld, shape, index
 
 
+def _out(out, dtype, name, shape, like, stream, device):
+    """The output tensor of a call, bf16 or fp32 (`dtype`, where there is no tensor yet), and its type's code."""
+    if out is None:
+        if dtype is not _BF16 and dtype is not _F32:
+            raise ValueError(f"{name}: need bfloat16 or float32, got {dtype}")
+        return _r._empty(stream, shape, dtype, like.device), 1 if dtype is _F32 else 0
+    of = out.dtype
+    if of is not _BF16 and of is not _F32 or dtype is not None and dtype is not of:
+        raise ValueError(f"{name}: need a contiguous tensor of {dtype or _FLOATS} {tuple(shape)}, got {_r._said(out)}")
+    _r._dense(out, name, of, shape, device)
+    return out, 1 if of is _F32 else 0
+
+
 def moe_sort_workspace_bytes(T: int, top_k: int, num_experts: int) -> int:
     return int(_mse.lib().moe_sort_workspace_bytes(T, top_k, num_experts))
 
@@ -102,8 +115,8 @@ def moe_sort(x, ids, num_experts, first_expert=0, scales=None, rows=None, row_sc
         workspace = _r._empty(stream, max(moe_sort_workspace_bytes(T, k, num_experts), 256), torch.uint8, x.device)
     else:
         _r._taken(workspace, device)
-    st = _C.moe_sort(x.data_ptr(), size, T, H, ldx, ids.data_ptr(), k, num_experts, first_expert, _mse._ptr(scales),
-                        rows.data_ptr(), ldr, (T * k - 1) * ldr + H, _mse._ptr(row_scales), place.data_ptr(),
+    st = _C.moe_sort(x.data_ptr(), size, T, H, ldx, ids.data_ptr(), k, num_experts, first_expert, None if scales is None else scales.data_ptr(),
+                        rows.data_ptr(), ldr, (T * k - 1) * ldr + H, None if row_scales is None else row_scales.data_ptr(), place.data_ptr(),
                         offsets.data_ptr(), workspace.data_ptr(), workspace.nbytes, _r._handle(stream, device))
     if st:
         _mse._check("moe_sort", st)
@@ -124,10 +137,10 @@ def moe_unsort(rows, place, weights=None, base=None, y_dtype=None, y=None, strea
     _r._dense(place, "place", _I32, (T, k), device)
     if weights is not None:
         _r._dense(weights, "weights", _F32, (T, k), device)
-    y, y_code = _r._out(y, y_dtype if y_dtype is not None or y is not None else rows.dtype, "y", (T, H), rows, stream)
+    y, y_code = _out(y, y_dtype if y_dtype is not None or y is not None else rows.dtype, "y", (T, H), rows, stream, device)
     if base is not None:
         _r._dense(base, "base", y.dtype, (T, H), device)
-    st = _C.moe_unsort(rows.data_ptr(), code, n, ldr, place.data_ptr(), _mse._ptr(weights), T, H, k, _mse._ptr(base),
+    st = _C.moe_unsort(rows.data_ptr(), code, n, ldr, place.data_ptr(), None if weights is None else weights.data_ptr(), T, H, k, None if base is None else base.data_ptr(),
                           y.data_ptr(), y_code, T * H, _r._handle(stream, device))
     if st:
         _mse._check("moe_unsort", st)
@@ -143,7 +156,8 @@ def moe_unsort_backward(dy, place, rows=None, weights=None, drows=None, dweights
     if _C is None:
         _ready()
     dy_code, ld, (T, H), device = _floats(dy, "dy", 2)
-    _r._dense(dy, "dy", dy.dtype, (T, H), device)
+    if ld != H and T > 1:
+        raise ValueError(f"dy: need a contiguous tensor, got {_r._said(dy)}")
     if place is None or place.dim() != 2:
         raise ValueError(f"place: need a 2-d tensor, got {_r._said(place)}")
     k = place.shape[1]
@@ -168,8 +182,8 @@ def moe_unsort_backward(dy, place, rows=None, weights=None, drows=None, dweights
     d_code, ldd, (nd, Hd), _ = _floats(drows, "drows", 2, device)
     if Hd != H or (code is not None and (d_code != code or nd != n)) or (rows_count is not None and nd != n):
         raise ValueError(f"drows: need {(n, H)} like rows, got {_r._said(drows)}")
-    st = _C.moe_unsort_backward(dy.data_ptr(), dy_code, place.data_ptr(), _mse._ptr(weights), _mse._ptr(rows), d_code, ldr, nd,
-                                   T, H, k, drows.data_ptr(), ldd, (nd - 1) * ldd + H, _mse._ptr(dweights),
+    st = _C.moe_unsort_backward(dy.data_ptr(), dy_code, place.data_ptr(), None if weights is None else weights.data_ptr(), None if rows is None else rows.data_ptr(), d_code, ldr, nd,
+                                   T, H, k, drows.data_ptr(), ldd, (nd - 1) * ldd + H, None if dweights is None else dweights.data_ptr(),
                                    _r._handle(stream, device))
     if st:
         _mse._check("moe_unsort_backward", st)

@@ -710,6 +710,13 @@ MSE_API mse_status int8_grouped_matmul(const int8_t *xq, int64_t ldx, const floa
                                        void *out, mse_dtype out_dtype, int64_t out_capacity, void *workspace,
                                        size_t workspace_bytes, void *stream);
 
+/* The kernels that int8_matmul and int8_linear (groups 0), or int8_grouped_matmul, would launch for weights with 16-byte rows, on
+ * the current device.  out[4] (host memory, written): [0] token rows of a tile: 1, 2 or 4 (CUDA cores), 16, 32 or 64 (tensor
+ * cores, weights on the MMA's 128-row side) or 256 (CTA pairs), 0 when the generic kernels are forced (then [1] and [2] are 0);
+ * [1] CTAs, or pairs, that share a tile's k-blocks; [2] 1 when int8_linear rounds its token inside the product's kernel (y apart
+ * from x); [3] 0.  MSE_ERR_INVALID_ARG as the calls; MSE_ERR_UNSUPPORTED_DEVICE without a device. */
+MSE_API mse_status mse_int8_launch_plan(int64_t T, int64_t N, int64_t K, int64_t groups, int32_t *out);
+
 /* int8_quantise of x [T x K] (bf16 or fp32, row pitch ldx), then int8_matmul, in one call.  y may lie over x. */
 MSE_API mse_status int8_linear(const void *x, mse_dtype x_dtype, int64_t ldx, const int8_t *wq, int64_t ldw, const float *ws,
                                int64_t T, int64_t N, int64_t K, void *y, mse_dtype y_dtype, int64_t y_capacity,

@@ -37,6 +37,7 @@ __all__ = [
     "fp8_launch_plan", "moe_launch_plan",
     "moe_sort", "moe_sort_backward", "moe_unsort", "moe_unsort_backward", "moe_sort_workspace_bytes", "new_moe_sort_workspace",
     "int8_quantise", "int8_matmul", "int8_grouped_matmul", "int8_linear", "int8_workspace_bytes", "new_int8_workspace",
+    "int8_launch_plan",
 ]
 
 BF16, F32 = 0, 1
@@ -119,6 +120,7 @@ def lib() -> ctypes.CDLL:
                 "moe_unsort_backward": (ci, [P, ci, P, P, P, ci, i64, i64, i64, i64, ci, P, i64, i64, P, P]),
                 "int8_quantise": (ci, [P, ci, i64, i64, i64, ci, P, P, i64, i64, P, P]),
                 "int8_workspace_bytes": (sz, [i64, i64, i64, i64]),
+                "mse_int8_launch_plan": (ci, [i64, i64, i64, i64, P]),
                 "int8_matmul": (ci, [P, i64, P, P, i64, P, i64, i64, i64, P, ci, i64, P, sz, P]),
                 "int8_grouped_matmul": (ci, [P, i64, P, P, i64, P, i64, P, i64, i64, i64, P, ci, i64, P, sz, P]),
                 "int8_linear": (ci, [P, ci, i64, P, i64, P, i64, i64, i64, P, ci, i64, P, sz, P]),
@@ -451,4 +453,4 @@ from .routed import (  # noqa: E402  (needs the names above)
 from .rows import (  # noqa: E402
     moe_sort, moe_sort_backward, moe_sort_workspace_bytes, moe_unsort, moe_unsort_backward, new_moe_sort_workspace)
 from .int8 import (  # noqa: E402
-    int8_grouped_matmul, int8_linear, int8_matmul, int8_quantise, int8_workspace_bytes, new_int8_workspace)
+    int8_grouped_matmul, int8_launch_plan, int8_linear, int8_matmul, int8_quantise, int8_workspace_bytes, new_int8_workspace)

@@ -302,15 +302,18 @@ int int8_cols_parts(int64_t tiles, int kb, int sm_count) {
     return (int)std::min<int64_t>(std::max<int64_t>(room, 1), 16 * tiles <= sm_count && kb >= 24 ? 8 : 5);
 }
 
+// grouped: every group may begin a tile of its own; as many as there are rows at most
+int64_t int8_cols_slots(const Int8Gemm &g, int tile_rows) {
+    return g.offsets ? std::min<int64_t>(g.T, g.T / tile_rows + std::min<int64_t>(g.groups, g.T)) : (g.T + tile_rows - 1) / tile_rows;
+}
+
 mse_status launch_int8_cols(const Int8Gemm &g, int tile_rows, int sm_count, bool pdl, cudaStream_t s) {
     CUtensorMap tw, tx;
     mse_status st = map_bytes(&tw, g.wq, g.groups * g.N, g.K, g.ldw, 128);
     if (st != MSE_OK) return st;
     if ((st = map_bytes(&tx, g.x16, g.T, g.K * 2, g.ldx16 * 2, tile_rows)) != MSE_OK) return st;
     const int kb = (int)((g.K + kInner - 1) / kInner);
-    const int64_t row_tiles = (g.N + 127) / 128, per = (g.T + tile_rows - 1) / tile_rows;
-    // grouped: every group may begin a tile of its own; as many as there are rows at most
-    const int64_t slots = g.offsets ? std::min<int64_t>(g.T, g.T / tile_rows + std::min<int64_t>(g.groups, g.T)) : per;
+    const int64_t row_tiles = (g.N + 127) / 128, slots = int8_cols_slots(g, tile_rows);
     if (row_tiles > 65535 || slots > 65535) return MSE_ERR_UNSUPPORTED_SHAPE;
     const int parts = int8_cols_parts(row_tiles * slots, kb, sm_count);
     const int stream_weights = slots == 1 || (g.offsets && g.T <= (int64_t)tile_rows * g.groups);

@@ -68,17 +68,22 @@ __device__ __forceinline__ bool wait_cluster(uint32_t bar, uint32_t parity, vola
     return __all_sync(~0u, ok);
 }
 
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+// PARTS 2: a cluster of two pairs has one tile, each pair half of its k-blocks and, at the end, half of its tokens.
+template <int PARTS>
+__global__ void __launch_bounds__(kThreads, 1)
     int8_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX, const Int8Gemm g,
-                     const int kb, const int n_tiles_n) {
+                     const int kb_total, const int n_tiles_n) {
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
     uint8_t *ring = smem_raw + (base - raw);
     PairCtrl *ctl = reinterpret_cast<PairCtrl *>(ring + kStages * (size_t)kStage);
     const int warp = __shfl_sync(~0u, (int)threadIdx.x / 32, 0), lane = threadIdx.x % 32;
-    const uint32_t rank = cluster_ctarank();
+    const uint32_t in_cluster = cluster_ctarank(), rank = in_cluster & 1u, first_rank = in_cluster & ~1u;
     const bool leader = rank == 0;
-    const int64_t pair = blockIdx.x / 2, n_pairs = gridDim.x / 2;
+    const uint16_t both = (uint16_t)(3u << first_rank);
+    const int part = (int)(in_cluster >> 1);
+    const int64_t pair = blockIdx.x / (2 * PARTS), n_pairs = gridDim.x / (2 * PARTS);   // (pairs that have tiles of their own)
+    const int kb0 = kb_total * part / PARTS, kb = kb_total * (part + 1) / PARTS - kb0;
     volatile int *abort_flag = &ctl->abort_flag;
 
     if (threadIdx.x == 0) {
@@ -135,7 +140,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const uint32_t tmem_base = __shfl_sync(~0u, ctl->tmem_base, 0), tmem_a = tmem_base + kTokens;
     pdl_wait();
 
-    const int64_t slots = ctl->slots, total = slots * n_tiles_n;
+    // (PARTS 2: a cluster has one tile at most, whatever the offsets say)
+    const int64_t slots = ctl->slots, total = PARTS > 1 ? min(slots * n_tiles_n, n_pairs) : slots * n_tiles_n;
     // tile id -> token tile and weight tile n: bands of kBand token tiles, the token tile fastest
     auto place = [&](int64_t id, RowTile &t, int &n) {
         const int64_t per = (int64_t)kBand * n_tiles_n, band = id / per, in = id % per;
@@ -174,14 +180,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     if (!ok) break;
                     if (el) {
                         const uint32_t dst = base + stage * kStage, wb = smem_u32(&ctl->wfull[stage]);
-                        const uint32_t xb = map_to_rank(smem_u32(&ctl->xfull[stage]), 0);
+                        const uint32_t xb = map_to_rank(smem_u32(&ctl->xfull[stage]), first_rank);
                         mbar_arrive_expect_tx(wb, kWeightTile);
-                        tma_load_2d_nohint(dst, &tmW, wb, k * kInner, w_row);
+                        tma_load_2d_nohint(dst, &tmW, wb, (kb0 + k) * kInner, w_row);
                         const bool both = t.rows > kHalf;
                         if (leader) mbar_arrive_expect_tx(smem_u32(&ctl->xfull[stage]), both ? 2 * kTokenBytes : kTokenBytes);
 #pragma unroll
                         for (int b = 0; b < 4; ++b)   // half b / 2, 64 k from b % 2; coordinates in bytes
-                            if (b < 2 || both) tma_load_2d_pair(dst + kWeightTile + b * kTokenBox, &tmX, xb, k * 2 * kInner + (b % 2) * 128,
+                            if (b < 2 || both) tma_load_2d_pair(dst + kWeightTile + b * kTokenBox, &tmX, xb, (kb0 + k) * 2 * kInner + (b % 2) * 128,
                                              x_row + b / 2 * kHalf);
                     }
                     __syncwarp();
@@ -219,15 +225,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                                 tc_mma_f16_ts_pair(tmem_base + h * kHalf, tmem_a + (uint32_t)(a * kATmem + kk * 8),
                                                    smem_desc_sw128(x + (kk / 4) * kTokenBox) + (uint64_t)(kk % 4 * 2), idesc,
                                                    in > 0 || kk > 0 ? 1u : 0u);
-                            if (last) tc_commit_pair_multicast(smem_u32(&ctl->dfull[h]), 3);
+                            if (last) tc_commit_pair_multicast(smem_u32(&ctl->dfull[h]), both);
                         }
                         __syncwarp();
                         if (last) ++use[h];
                     }
                     if (!ok) break;
                     if (el) {
-                        tc_commit_pair_multicast(smem_u32(&ctl->empty[stage]), 3);
-                        tc_commit_pair_multicast(smem_u32(&ctl->aempty[a]), 3);
+                        tc_commit_pair_multicast(smem_u32(&ctl->empty[stage]), both);
+                        tc_commit_pair_multicast(smem_u32(&ctl->aempty[a]), both);
                     }
                     __syncwarp();
                     if (++stage == kStages) { stage = 0; phase ^= 1u; }
@@ -235,11 +241,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 }
             }
         }
+        if constexpr (PARTS > 1) {   // the other warps' exchange
+            __syncwarp();
+            cluster_sync();
+            cluster_sync();
+        }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
         const int q = warp & 3, row = q * 32 + lane, h = (warp - 4) / 4;
         const uint32_t lanes = (uint32_t)(q * 32) << 16, src = tmem_base + (uint32_t)(h * kHalf) + lanes;
-        const uint32_t dempty = map_to_rank(smem_u32(&ctl->dempty[h]), 0);
+        const uint32_t dempty = map_to_rank(smem_u32(&ctl->dempty[h]), first_rank);
         float *xs = ctl->xs[warp - 4];
         const int chunks = (kb + kChunkBlocks - 1) / kChunkBlocks;
         const int64_t tiles = total > pair ? (total - pair + n_pairs - 1) / n_pairs : 0, blocks = tiles * kb;
@@ -260,7 +271,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             for (int i = 0; i < kHalf / 32; ++i) xa[i] = i * 32 + lane < left ? g.xs[first + i * 32 + lane] : 0.f;
         };
         // Up to two chunks are added in fp32: a sum of two integers of 24 bits is rounded as the integer is at the end.
-        const bool floats = chunks <= 2;
+        const bool floats = PARTS == 1 && chunks <= 2;
         int64_t id = pair, end = min(kb, kChunkBlocks);   // end: the k-block behind the next chunk, counted over all tiles
         int64_t tiles_left = tiles, owed_at = 0;
         int done = 0;                                     // k-blocks of the tile in chunks that were added
@@ -275,7 +286,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 // A chunk's sums are read before the second k-block behind it is converted: its MMAs wait for that.  A tile is
                 // stored after one more, so that up to four converted k-blocks are left for the MMAs meanwhile.
                 const bool due = tiles_left > 0 && (end + 2 <= i || i >= blocks);
-                if (owed && (due || i >= owed_at || i >= blocks)) {
+                if (PARTS == 1 && owed && (due || i >= owed_at || i >= blocks)) {
                     owed = false;
 #pragma unroll
                     for (int j = 0; j < kHalf / 32; ++j) xs[j * 32 + lane] = xa[j];
@@ -347,9 +358,49 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             tmem_st_wait();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) arrive_cluster(map_to_rank(smem_u32(&ctl->afull[a]), 0));
+            if (lane == 0) arrive_cluster(map_to_rank(smem_u32(&ctl->afull[a]), first_rank));
         }
         __syncwarp();
+        if constexpr (PARTS > 1) {
+            // Either pair finishes half of the token columns of either half: it sends its sums of the others to the CTA with the
+            // same weight rows, [half][group of four columns][row], in the rings.
+            constexpr int kMine = kHalf / 2;
+            int4 *red = reinterpret_cast<int4 *>(ring);
+            static_assert(2 * (kMine / 4) * 128 * 16 <= kStages * kStage, "exchange");
+            cluster_sync();   // every ring of the cluster is idle
+#pragma unroll
+            for (int c = 0; c < kMine; c += 4) {
+                const int4 v = part == 0 ? make_int4(acc[kMine + c], acc[kMine + c + 1], acc[kMine + c + 2], acc[kMine + c + 3])
+                                         : make_int4(acc[c], acc[c + 1], acc[c + 2], acc[c + 3]);
+                st_cluster_s32x4(map_to_rank(smem_u32(red + (h * (kMine / 4) + c / 4) * 128 + row), in_cluster ^ 2u), v);
+            }
+#pragma unroll
+            for (int j = 0; j < kHalf / 32; ++j) xs[j * 32 + lane] = xa[j];
+            cluster_sync();
+            if (ok && tiles > 0 && out_n < g.N) {
+                const int from = part * kMine;
+                const int64_t at = (first + from) * g.N + out_n;
+                float *out = static_cast<float *>(g.out) + at;
+                uint16_t *out16 = static_cast<uint16_t *>(g.out) + at;
+#pragma unroll
+                for (int c = 0; c < kMine; c += 4) {
+                    const int4 v = red[(h * (kMine / 4) + c / 4) * 128 + row];
+                    const int sum[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                    for (int j = 0; j < 4; ++j, out += g.N, out16 += g.N) {
+                        const int mine = part == 0 ? acc[c + j] : acc[kMine + c + j];
+                        if (from + c + j < left) {
+                            const float y = (float)(mine + sum[j]) * xs[from + c + j] * w;
+                            if (g.out_f32)
+                                *out = y;
+                            else
+                                *out16 = f32_to_bf16_bits(y);
+                        }
+                    }
+                }
+            }
+            __syncwarp();
+        }
     }
 
     // ---- teardown: every issued stage is released by the leader's MMA commit once its bytes (of both CTAs) have landed and been
@@ -361,7 +412,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 __nanosleep(200000);
     }
     if (warp == 1 && lane == 0 && leader) {
-        tc_commit_pair_multicast(smem_u32(&ctl->drain), 1);
+        tc_commit_pair_multicast(smem_u32(&ctl->drain), (uint16_t)(1u << first_rank));
         (void)mbar_wait_drain(smem_u32(&ctl->drain), 0, drain_limit_of(g.wait_limit_ns));
     }
     tc_fence_before();
@@ -372,6 +423,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 }
 
 // Opts the kernel into its shared memory once per device.
+template <int PARTS>
 cudaError_t prepare() {
     static std::atomic<uint64_t> done;   // bit per device
     int dev = 0;
@@ -379,26 +431,68 @@ cudaError_t prepare() {
     if (e != cudaSuccess || (done.load(std::memory_order_acquire) >> (dev & 63) & 1)) return e;
     // the hand-over of registers needs the ones it was written for
     cudaFuncAttributes at;
-    if ((e = cudaFuncGetAttributes(&at, int8_pair_kernel)) != cudaSuccess) return e;
+    if ((e = cudaFuncGetAttributes(&at, int8_pair_kernel<PARTS>)) != cudaSuccess) return e;
     if (at.numRegs < kLaunchRegs) return cudaErrorInvalidConfiguration;
-    e = cudaFuncSetAttribute(int8_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+    e = cudaFuncSetAttribute(int8_pair_kernel<PARTS>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
     if (e == cudaSuccess) done.fetch_or(1ull << (dev & 63), std::memory_order_acq_rel);
     return e;
 }
 
+// Clusters of two pairs that can be resident at once (0 on failure).
+int resident_clusters() {
+    static std::atomic<int> cache[64];
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+    if ((n = cache[dev & 63].load()) > 0) return n;
+    if (prepare<2>() != cudaSuccess) return 0;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(4);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 4;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n, int8_pair_kernel<2>, &cfg) != cudaSuccess) {
+        cudaGetLastError();
+        return 0;
+    }
+    cache[dev & 63].store(n);
+    return n;
+}
+
+template <int PARTS>
+cudaError_t run(const CUtensorMap &tw, const CUtensorMap &tx, const Int8Gemm &g, int kb, int n_tiles_n, int64_t clusters, bool pdl,
+                cudaStream_t s) {
+    const cudaError_t e = prepare<PARTS>();
+    if (e != cudaSuccess) return e;
+    return launch_kernel(int8_pair_kernel<PARTS>, dim3((unsigned)(2 * PARTS * clusters)), kThreads, kSmem, pdl, 2 * PARTS, s, tw, tx, g,
+                         kb, n_tiles_n);
+}
+
 }  // namespace
+
+// Pairs that share a tile's k-blocks: two where every tile has a cluster of its own.  (us with one pair and two: 1024 x 2112 x 7168,
+// 36 tiles, 47.2, 32.4; the swap-AB kernel takes 37.8.)
+int int8_pair_parts(int64_t tiles, int kb) { return kb >= 8 && tiles <= resident_clusters() ? 2 : 1; }
+
+int64_t int8_pair_tiles(const Int8Gemm &g) {
+    return ((g.T + kTokens - 1) / kTokens + (g.offsets ? std::min<int64_t>(g.groups, g.T) : 0)) * ((g.N + 255) / 256);
+}
 
 mse_status launch_int8_pair(const Int8Gemm &g, int sm_count, bool pdl, cudaStream_t s) {
     CUtensorMap tw, tx;
     mse_status st = map_bytes(&tw, g.wq, g.groups * g.N, g.K, g.ldw, 128);
     if (st != MSE_OK) return st;
     if ((st = map_bytes(&tx, g.x16, g.T, g.K * 2, g.ldx16 * 2, kHalf / 2)) != MSE_OK) return st;
-    if (prepare() != cudaSuccess) return MSE_ERR_CUDA;
     const int kb = (int)((g.K + kInner - 1) / kInner), n_tiles_n = (int)((g.N + 255) / 256);
-    const int64_t slots = (g.T + kTokens - 1) / kTokens + (g.offsets ? std::min<int64_t>(g.groups, g.T) : 0);
-    const int64_t pairs = std::min<int64_t>(sm_count / 2, slots * n_tiles_n);
-    const cudaError_t e = launch_kernel(int8_pair_kernel, dim3((unsigned)(2 * pairs)), kThreads, kSmem, pdl, 1, s, tw, tx, g, kb,
-                                        n_tiles_n);
+    const int64_t tiles = int8_pair_tiles(g);
+    const cudaError_t e = int8_pair_parts(tiles, kb) == 2
+                              ? run<2>(tw, tx, g, kb, n_tiles_n, tiles, pdl, s)
+                              : run<1>(tw, tx, g, kb, n_tiles_n, std::min<int64_t>(sm_count / 2, tiles), pdl, s);
     return e == cudaSuccess ? MSE_OK : MSE_ERR_CUDA;
 }
 

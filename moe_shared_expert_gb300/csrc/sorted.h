@@ -100,7 +100,10 @@ cudaError_t launch_int8_few(const Int8Gemm &g, int tile_rows, const void *x, int
 mse_status launch_int8_cols(const Int8Gemm &g, int tile_rows, int sm_count, bool pdl, cudaStream_t s);
 // Tensor-core kernel for token tiles of 256 rows (a CTA pair per 256 x 256 tile).
 mse_status launch_int8_pair(const Int8Gemm &g, int sm_count, bool pdl, cudaStream_t s);
+int int8_pair_parts(int64_t tiles, int kb);
+int64_t int8_pair_tiles(const Int8Gemm &g);                  // tiles at most
 int int8_cols_parts(int64_t tiles, int kb, int sm_count);
+int64_t int8_cols_slots(const Int8Gemm &g, int tile_rows);   // token tiles at most
 
 }  // namespace sorted
 }  // namespace mse

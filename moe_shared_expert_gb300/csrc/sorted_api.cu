@@ -89,7 +89,7 @@ int64_t pitch16(int64_t K) { return (K + 63) / 64 * 64; }   // of tokens in fp16
 //
 // More rows take tiles of 64 on the swap-AB kernel or the CTA pairs, whichever is expected to be done first, in units of 10 ns: two
 // swap-AB CTAs on an SM take 0.6 us for a k-block each and 4 us for a tile besides, 2.5 more where its k-blocks are split; a CTA pair
-// 0.75 us for a k-block and 5 us in all.  (us with tiles of 64 and 256: 512 x 2112 x 7168 24.7, 45.2; 1024 x 2112 x 7168 37.8, 47.2;
+// 0.75 us for a k-block and 5 us in all, 3 more where two share a tile's.  (us with tiles of 64 and 256: 512 x 2112 x 7168 24.7, 45.2; 1024 x 2112 x 7168 37.8, 47.2;
 // 160 x 12288 x 7168 38.1, 46.6; 320 x 12288 x 7168 69, 83; 400 x 4096 x 2048 15.0, 17.1; 800 x 4096 x 2048 24.8, 17.9; 32 experts of
 // 4096 x 2048 with 32, 64, 128 and 192 rows each 61, 82; 79, 83; 127, 92; 172, 116.  Tiles of 128 were never the fastest by more
 // than a few per cent.)
@@ -103,20 +103,18 @@ int tile_rows_of(const Int8Gemm &g, int sm_count) {
     // a group's last tile is half full on the average; a pair's tile of up to 128 rows counts half
     const int64_t kb = (g.K + 127) / 128, part = g.offsets ? g.groups / 2 : 0;
     const int64_t cols = ((g.T + 63) / 64 + part) * ((g.N + 127) / 128), halves = ((g.T + 127) / 128 + part) * ((g.N + 255) / 256);
-    const int64_t parts = int8_cols_parts(cols, (int)kb, sm_count);
-    const int64_t waves = (cols * parts + 2 * sm_count - 1) / (2 * sm_count), rounds = ((halves + 1) / 2 + sm_count / 2 - 1) / (sm_count / 2);
-    const int64_t cols_time = waves * (kb * 60 / parts + 400 + (parts > 1 ? 250 : 0)), pair_time = rounds * kb * 75 + 500;
-    return pair_time < cols_time ? 256 : 64;
+    const int64_t cp = int8_cols_parts(cols, (int)kb, sm_count), pp = int8_pair_parts(int8_pair_tiles(g), (int)kb);
+    const int64_t waves = (cols * cp + 2 * sm_count - 1) / (2 * sm_count), rounds = ((halves + 1) / 2 * pp + sm_count / 2 - 1) / (sm_count / 2);
+    const int64_t cols_time = waves * (kb * 60 / cp + 400 + (cp > 1 ? 250 : 0)), pair_time = rounds * kb * 75 / pp + 500 + (pp > 1 ? 300 : 0);
+    // (a swap-AB grid has at most 65,535 token tiles)
+    return pair_time < cols_time || int8_cols_slots(g, 64) > 65535 ? 256 : 64;
 }
 
 // One launch, whose kernel rounds the token itself: every CTA rounds it.  (us with one launch and two: 1 x 2112 x 7168 6.3, 7.6; two
 // tokens 8.3, 8.1.)
 bool rounds_itself(int tile_rows) { return tile_rows == 1; }
 
-bool tensorcore_ok(const Int8Gemm &g) {
-    return (reinterpret_cast<uintptr_t>(g.wq) & 15u) == 0 && g.ldw % 16 == 0 && (g.N + 127) / 128 <= 65535 &&
-           g.T / 128 + g.groups <= 65535;
-}
+bool tensorcore_ok(const Int8Gemm &g) { return (reinterpret_cast<uintptr_t>(g.wq) & 15u) == 0 && g.ldw % 16 == 0; }
 
 mse_status run_tensorcore(const Int8Gemm &g, int tile_rows, const DeviceView &d, cudaStream_t s) {
     if (tile_rows == 256) return launch_int8_pair(g, d.sm_count, pdl_enabled(), s);
@@ -265,6 +263,27 @@ mse_status int8_quantise(const void *x, mse_dtype x_dtype, int64_t rows, int64_t
     p.last = last;
     p.q = q; p.ldq = ldq; p.half_out = 0; p.scales = scales;
     return from_cuda(launch_int8_round(p, d.sm_count, pdl_enabled(), static_cast<cudaStream_t>(stream)));
+}
+
+mse_status mse_int8_launch_plan(int64_t T, int64_t N, int64_t K, int64_t groups, int32_t *out) {
+    if (!out || !int8_sizes_ok(T, N, K, groups > 0 ? groups : 1) || groups < 0 || std::max<int64_t>(groups, 1) * N > kMaxRows)
+        return MSE_ERR_INVALID_ARG;
+    for (int i = 0; i < 4; ++i) out[i] = 0;
+    DeviceView d;
+    mse_status st = device_view(&d);
+    if (st != MSE_OK) return st;
+    static const int32_t some = 0;   // a grouped product; its offsets are the call's
+    const Int8Gemm g = product(nullptr, 0, nullptr, groups > 0 ? &some : nullptr, std::max<int64_t>(groups, 1), nullptr,
+                               (K + 15) / 16 * 16, nullptr, T, N, K, nullptr, MSE_BF16);
+    bool fast = false;
+    if ((st = choose_tensorcore(tensorcore_ok(g), &fast)) != MSE_OK || !fast) return st;
+    out[0] = tile_rows_of(g, d.sm_count);
+    out[1] = out[0] <= 4 ? 1
+             : out[0] == 256
+                 ? int8_pair_parts(int8_pair_tiles(g), (int)((K + 127) / 128))
+                 : int8_cols_parts(int8_cols_slots(g, out[0]) * ((N + 127) / 128), (int)((K + 127) / 128), d.sm_count);
+    out[2] = groups == 0 && rounds_itself(out[0]);
+    return MSE_OK;
 }
 
 size_t int8_workspace_bytes(int64_t T, int64_t N, int64_t K, int64_t groups) {

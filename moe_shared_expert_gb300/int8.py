@@ -13,6 +13,8 @@ The sum over k is the integer itself, so results do not depend on which kernel r
 """
 from __future__ import annotations
 
+import ctypes
+
 import moe_shared_expert_gb300 as _mse
 
 from . import routed as _r
@@ -129,3 +131,10 @@ def int8_linear(x, wq, ws, y_dtype=None, y=None, workspace=None, stream=None):
     if st:
         _mse._check("int8_linear", st)
     return y
+
+
+def int8_launch_plan(T: int, N: int, K: int, groups: int = 0) -> dict:
+    """Kernel and split of a product (groups 0: plain) on the current device: see mse_int8_launch_plan in include/mse.h."""
+    out = (ctypes.c_int32 * 4)()
+    _mse._check("mse_int8_launch_plan", _mse.lib().mse_int8_launch_plan(T, N, K, groups, out))
+    return dict(zip(("tile_rows", "parts", "one_launch"), map(int, out)))

@@ -253,6 +253,45 @@ def test_grouped_rows_that_begin_late_or_end_beyond(path):
     assert torch.equal(out[10:], expected(xq[10:], xs[10:], wq[2], ws[2], torch.float32))
 
 
+# Every kernel and split that the rules choose, each with its launch plan.
+PLANS = [
+    # T, N, K, counts of the groups or None, tile rows, parts
+    (1, 300, 700, None, 1, 1), (2, 300, 700, None, 2, 1), (2, 5000, 260, None, 2, 1), (3, 300, 700, None, 4, 1), (4, 5000, 260, None, 4, 1),
+    (2, 130, 60000, None, 16, 8), (5, 300, 700, None, 16, 1), (16, 1300, 1100, None, 16, 2), (9, 140, 3300, None, 16, 6),
+    (13, 2112, 7168, None, 16, 5), (16, 12288, 1600, None, 16, 3), (16, 2500, 2100, None, 16, 4), (32, 300, 5000, None, 32, 8),
+    (24, 7168, 2600, None, 32, 5), (33, 900, 900, None, 64, 2), (64, 2500, 3300, None, 64, 5), (64, 12288, 700, None, 64, 1), (100, 130, 9000, None, 64, 8),
+    (257, 12288, 1100, None, 256, 1), (2300, 1024, 4000, None, 256, 2), (2250, 1000, 3990, None, 256, 2), (2177, 1025, 1200, None, 256, 1), (5000, 1500, 1000, None, 256, 1),
+    (9, 500, 900, [1, 0, 3, 0, 0, 4], 2, 1), (60, 500, 900, [9, 11, 2, 0, 17, 9, 3, 8], 16, 2), (60, 500, 4100, [9, 31, 20], 32, 5),
+    (300, 500, 900, [90, 31, 0, 150, 3], 64, 2), (40, 40, 60, [40], 64, 1), (2000, 3000, 1100, [700, 129, 128, 1, 1000], 256, 1), (1600, 700, 8100, [1400, 150], 256, 2),
+    (16, 700, 900, [5, 5, 6], 2, 1),
+]
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=str)
+@pytest.mark.parametrize("T,N,K,counts,tile,parts", PLANS)
+def test_every_kernel_and_split(T, N, K, counts, tile, parts, dtype):
+    G = len(counts) if counts else 0
+    plan = mse.int8_launch_plan(T, N, K, G)
+    assert (plan["tile_rows"], plan["parts"]) == (tile, parts) and plan["one_launch"] == (tile == 1 and not counts)
+    # magnitudes that need all of 32 bits in the longest sums
+    pitch = -(-K // 16) * 16
+    xq, wq = integers(T, K, seed=1, top=128).abs().clamp_max(127).to(torch.int8), integers(max(G, 1), N, K, seed=2, top=128)
+    xs, ws = scales(T, seed=3), scales(max(G, 1), N, seed=4)
+    out = torch.full((T, N), 77.0, dtype=dtype, device="cuda")
+    w = rows_with_pitch(wq, pitch, 0x7F)
+    if counts:
+        offsets = torch.tensor([0] + counts).cumsum(0).to(torch.int32)
+        mse.int8_grouped_matmul(rows_with_pitch(xq, pitch, 0x7F), xs.cuda(), offsets.cuda(), w, ws.cuda(), out=out)
+        end = offsets.tolist()
+    else:
+        mse.int8_matmul(rows_with_pitch(xq, pitch, 0x7F), xs.cuda(), w[0], ws[0].cuda(), out=out)
+        end = [0, T]
+    for g, (a, b) in enumerate(zip(end, end[1:])):
+        if a < b:
+            assert torch.equal(out[a:b], expected(xq[a:b], xs[a:b], wq[g], ws[g], dtype)), g
+    assert bool((out[end[-1]:] == 77).all())
+
+
 # ------------------------------------------------------------------------------------ together
 
 def layer(x, ids, weights, E, first, wgu, wd, shared, stages=None):

@@ -3,9 +3,13 @@
     python examples/moe_layer.py                      # a decode batch of 64 tokens
     python examples/moe_layer.py --tokens 4096        # a prompt
     python examples/moe_layer.py --tokens 8 --experts 4 --top-k 2 --hidden 512 --intermediate 256 --check
+    python examples/moe_layer.py --int8               # routed experts in 8-bit integers
 
 The shared expert is bf16 (``mlp_swiglu_forward``); the routed experts are rounded once to e4m3 with a scale for each
-block of 128 x 128 (``fp8_block_quantise``), as a program does when it loads a model.  Weights and tokens are random.
+block of 128 x 128 (``fp8_block_quantise``), as a program does when it loads a model.  With --int8 they are 8-bit integers with a
+scale for each output channel (``int8_quantise``): the tokens are rounded and sorted by expert (``moe_sort``), go through
+grouped products (``int8_grouped_matmul``) and the activation, and come back weighted on top of the shared expert's output
+(``moe_unsort``).  Weights and tokens are random.
 """
 import argparse
 import math
@@ -40,18 +44,29 @@ class MoELayer:
         self.shared_workspace = mse.new_mlp_workspace(max_tokens, H, shared_intermediate)
         self.workspace = mse.new_moe_workspace(max_tokens, top_k, E, H, I)
 
+    def route(self, x):
+        return mse.moe_route(x @ self.router.t(), self.top_k, scoring="sigmoid", bias=self.bias)
+
+    def shared(self, x):
+        return mse.mlp_swiglu_forward(x, self.shared_gate_up, self.shared_down, workspace=self.shared_workspace)
+
     def __call__(self, x):
-        logits = x @ self.router.t()
-        ids, weights = mse.moe_route(logits, self.top_k, scoring="sigmoid", bias=self.bias)
-        y = mse.mlp_swiglu_forward(x, self.shared_gate_up, self.shared_down, workspace=self.shared_workspace)
+        ids, weights = self.route(x)
+        y = self.shared(x)
         return mse.moe_experts_forward(x, ids, weights, self.w_gate_up, self.s_gate_up, self.w_down, self.s_down,
                                        shared=y, y=y, workspace=self.workspace)
 
-    def plain(self, x):
-        """The layer in elementary torch operations (8-bit weights as they are, activations not rounded)."""
+    def experts(self):
+        """The routed experts' weights [E, 2I, H] and [E, H, I] as the values they stand for."""
         def values(q, s):
             return q.float() * s.repeat_interleave(128, -2)[..., :q.shape[-2], :].repeat_interleave(128, -1)[..., :q.shape[-1]]
 
+        E, _, H = self.w_gate_up.shape
+        halves = self.w_gate_up.float().view(2 * E, -1, H), self.s_gate_up.view(2 * E, -1, self.s_gate_up.shape[-1])
+        return values(*halves).view(E, -1, H), values(self.w_down, self.s_down)
+
+    def plain(self, x):
+        """The layer in elementary torch operations (8-bit weights as they are, activations not rounded)."""
         def swiglu(x, gate_up, down):
             g, u = (x @ gate_up.transpose(-1, -2)).chunk(2, -1)
             return (g / (1 + torch.exp(-g)) * u) @ down.transpose(-1, -2)
@@ -61,10 +76,34 @@ class MoELayer:
         ids = (score + self.bias).topk(self.top_k, 1).indices
         w = score.gather(1, ids)
         w = torch.zeros_like(score).scatter(1, ids, w / w.sum(1, keepdim=True))
-        E, _, H = self.w_gate_up.shape
-        halves = self.w_gate_up.float().view(2 * E, -1, H), self.s_gate_up.view(2 * E, -1, self.s_gate_up.shape[-1])
-        routed = swiglu(x, values(*halves).view(E, -1, H), values(self.w_down, self.s_down))
+        routed = swiglu(x, *self.experts())
         return swiglu(x, self.shared_gate_up.float(), self.shared_down.float()) + torch.einsum("te,eth->th", w, routed)
+
+
+class Int8MoELayer(MoELayer):
+    """The same layer with routed experts in 8-bit integers."""
+
+    def __init__(self, hidden, intermediate, shared_intermediate, experts, top_k, max_tokens, seed=0):
+        super().__init__(hidden, intermediate, shared_intermediate, experts, top_k, max_tokens, seed)
+        gate_up, down = MoELayer.experts(self)
+        self.gate_up, self.down = mse.int8_quantise(gate_up), mse.int8_quantise(down)
+        del self.w_gate_up, self.s_gate_up, self.w_down, self.s_down, self.workspace
+        pairs = max_tokens * top_k
+        self.sort_workspace = mse.new_moe_sort_workspace(max_tokens, top_k, experts)
+        self.workspaces = [mse.new_int8_workspace(pairs, w.shape[1], w.shape[2], experts) for w, _ in (self.gate_up, self.down)]
+
+    def __call__(self, x):
+        ids, weights = self.route(x)
+        y = self.shared(x)
+        q, scales = mse.int8_quantise(x)
+        rows, place, offsets, scales = mse.moe_sort(q, ids, len(self.down[1]), scales=scales, workspace=self.sort_workspace)
+        h = mse.int8_grouped_matmul(rows, scales, offsets, *self.gate_up, workspace=self.workspaces[0])
+        h, scales = mse.int8_quantise(h, swiglu=True, offsets=offsets)
+        o = mse.int8_grouped_matmul(h, scales, offsets, *self.down, workspace=self.workspaces[1])
+        return mse.moe_unsort(o, place, weights, base=y, y=y)
+
+    def experts(self):
+        return [q.float() * s[..., None] for q, s in (self.gate_up, self.down)]
 
 
 def main():
@@ -76,18 +115,20 @@ def main():
     ap.add_argument("--experts", type=int, default=32)
     ap.add_argument("--top-k", type=int, default=8)
     ap.add_argument("--steps", type=int, default=50)
+    ap.add_argument("--int8", action="store_true", help="routed experts in 8-bit integers")
     ap.add_argument("--check", action="store_true", help="compare with the layer in elementary operations")
     a = ap.parse_args()
     __graft_entry__.build()
     shared = a.shared_intermediate or (6144 if a.hidden == 7168 else 2 * a.intermediate)
-    layer = MoELayer(a.hidden, a.intermediate, shared, a.experts, a.top_k, a.tokens)
+    layer = (Int8MoELayer if a.int8 else MoELayer)(a.hidden, a.intermediate, shared, a.experts, a.top_k, a.tokens)
     x = torch.randn(a.tokens, a.hidden, device="cuda").to(torch.bfloat16)
     y = layer(x)
     if a.check:
         want = layer.plain(x)
         off = float((y.float() - want).norm() / want.norm())
         print(f"relative error against elementary operations: {off:.4f}")
-        if not off < 0.06:   # x and h keep 3 fraction bits: about 2^-5 each in the mean square
+        # x and h keep 3 fraction bits, about 2^-5 each in the mean square; 8-bit integers of a normal row more
+        if not off < 0.06:
             raise SystemExit("the layer is off")
     for _ in range(3):
         layer(x)

@@ -392,3 +392,68 @@ def test_calls_in_turn_share_a_workspace():
             mse.int8_linear(x, wq, ws, y=y, workspace=space)
     for y, w in zip(ys, want):
         assert torch.equal(y, w)
+
+
+def test_a_decode_loop_on_kept_buffers():
+    # every call writes what the next one reads, and the next round writes it again
+    steps = [layer_inputs(T, 512, 256, 8, 16, 4, seed) for seed, T in enumerate((24, 3, 24, 1, 40, 24))]
+    weights = steps[0][5:7]
+    steps = [(x, ids, w, E, first, *weights, shared) for x, ids, w, E, first, _, _, shared in steps]
+    want = [layer(*s) for s in steps]
+    T, k, E, H, I = 40, 4, 8, 512, 256
+    P = T * k
+    keep = dict(q=torch.empty(T, H, dtype=torch.int8, device="cuda"), s=torch.empty(T, device="cuda"), rows=torch.empty(P, H, dtype=torch.int8, device="cuda"),
+                rs=torch.empty(P, device="cuda"), place=torch.empty(T, k, dtype=torch.int32, device="cuda"), off=torch.empty(E + 1, dtype=torch.int32, device="cuda"),
+                gu=torch.empty(P, 2 * I, device="cuda"), h=torch.empty(P, I, dtype=torch.int8, device="cuda"), hs=torch.empty(P, device="cuda"),
+                o=torch.empty(P, H, device="cuda"), space=mse.new_int8_workspace(P, 2 * I, H, E), sort=mse.new_moe_sort_workspace(T, k, E))
+
+    def run(x, ids, w, E, first, wgu, wd, shared):
+        t, p, b = x.shape[0], x.shape[0] * k, keep
+        q, s = mse.int8_quantise(x, q=b["q"][:t], scales=b["s"][:t])
+        rows, place, off, rs = mse.moe_sort(q, ids, E, first_expert=first, scales=s, rows=b["rows"][:p], row_scales=b["rs"][:p], place=b["place"][:t],
+                                            offsets=b["off"], workspace=b["sort"])
+        gu = mse.int8_grouped_matmul(rows, rs, off, *wgu, out=b["gu"][:p], workspace=b["space"])
+        h, hs = mse.int8_quantise(gu, swiglu=True, offsets=off, q=b["h"][:p], scales=b["hs"][:p])
+        o = mse.int8_grouped_matmul(h, hs, off, *wd, out=b["o"][:p], workspace=b["space"])
+        return mse.moe_unsort(o, place, w, base=shared, y_dtype=torch.bfloat16)
+
+    got = [run(*s) for _ in range(30) for s in steps]
+    torch.cuda.synchronize()
+    for i, y in enumerate(got):
+        assert torch.equal(y, want[i % len(steps)]), i
+
+
+def test_two_streams_with_workspaces_of_their_own():
+    args = [layer_inputs(T, 512, 256, 8, 8, 4, T) for T in (33, 40)]
+    want = [layer(*a) for a in args]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in args]
+    got = [[], []]
+    for _ in range(20):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(layer(*args[i]))
+    torch.cuda.synchronize()
+    for ys, w in zip(got, want):
+        assert all(torch.equal(y, w) for y in ys)
+
+
+def test_outputs_beyond_32_bits():
+    T, N, K = 300_007, 7168, 48
+    xq, wq = integers(T, K, seed=1).cuda(), integers(N, K, seed=2).cuda()
+    xs, ws = scales(T, seed=3).cuda(), scales(N, seed=4).cuda()
+    y = mse.int8_matmul(xq, xs, wq, ws)
+    for rows in (slice(0, 9), slice(299_520, 299_700), slice(T - 300, T)):
+        assert torch.equal(y[rows], expected(xq[rows], xs[rows], wq, ws, torch.bfloat16))
+
+
+@pytest.mark.parametrize("tokens", ["24", "300"])
+def test_the_example_runs(tokens):
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, os.path.join(root, "examples", "moe_layer.py"), "--int8", "--tokens", tokens, "--experts", "6", "--top-k", "3",
+                        "--hidden", "512", "--intermediate", "256", "--steps", "2", "--check"], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stdout + r.stderr
+    assert "relative error" in r.stdout

@@ -259,3 +259,102 @@ def test_gradients_are_the_differences():
         step[t, 3] = 4.0
         # a sum of copies: x + 4 is rounded once, dx by k sums
         assert abs((r(x + step) - at) - 4.0 * float(dx[t, 3])) <= 4 * (k + 2) * EPS32 * 8 * k * float(g.abs().max())
+
+
+def test_rows_beyond_32_bits():
+    # 37,500 tokens of 7168 to eight experts each: more values than 31 bits count
+    T, k, E, H = 37_500, 8, 16, 7168
+    ids = torch.rand(T, E, generator=gen(1)).topk(k, 1).indices.to(torch.int32).cuda()
+    x = torch.arange(T, device="cuda").to(torch.float32)[:, None].expand(T, H).contiguous().to(torch.bfloat16)
+    x[:, 0] = (torch.arange(T, device="cuda") % 128).to(torch.bfloat16)
+    x[:, 1] = torch.div(torch.arange(T, device="cuda"), 128, rounding_mode="floor").to(torch.bfloat16)
+    rows, place, offsets, _ = mse.moe_sort(x, ids, E)
+    assert int(offsets[-1]) == T * k and torch.equal(place.flatten().sort().values.long(), torch.arange(T * k, device="cuda"))
+    for t in (0, 1, T // 2, T - 1):
+        for j in (0, k - 1):
+            assert torch.equal(rows[int(place[t, j])], x[t])
+    last = int(offsets[-1]) - 1
+    t = int((place == last).nonzero()[0, 0])
+    assert torch.equal(rows[last], x[t])
+    y = mse.moe_unsort(rows, place, torch.full((T, k), 0.125, device="cuda"))
+    assert torch.equal(y, x)                                  # eight eighths of the same value
+    drows, dw = mse.moe_unsort_backward(x, place, rows, torch.full((T, k), 2.0, device="cuda"))
+    assert torch.equal(drows[last], 2 * x[t])
+    want = (x[t].double() ** 2).sum()
+    assert abs(float(dw[t].double().max() - want)) <= (H / 128 + 17) * EPS32 * float(want)
+
+
+def test_a_captured_round_trip_follows_its_inputs():
+    T, k, E, H = 60, 4, 9, 264
+    w = torch.rand(T, k, generator=gen(2)).cuda()
+    x, ids = torch.empty(T, H, device="cuda"), torch.empty(T, k, dtype=torch.int32, device="cuda")
+
+    def step():
+        rows, place, _, _ = mse.moe_sort(x, ids, E, rows=torch.zeros(T * k, H, device="cuda"))
+        y = mse.moe_unsort(rows, place, w, base=x)
+        drows, dw = mse.moe_unsort_backward(y, place, rows, w, drows=torch.zeros_like(rows))
+        return y, drows, dw, mse.moe_sort_backward(drows, place)
+
+    def fill(seed):
+        x.copy_(torch.randn(T, H, generator=gen(seed)))
+        ids.copy_(some_ids(T, k, E, seed))
+
+    fill(1)
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured = step()
+    for seed in (5, 6, 7):
+        fill(seed)
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(captured, step()):
+            assert torch.equal(a, b)
+
+
+def test_a_program_s_backward_pass():
+    """The calls within an autograd function, experts of one matrix each in torch: gradients as autograd finds them for the plain layer."""
+    T, k, E, H = 30, 3, 5, 72
+
+    class Sort(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, x, ids):
+            rows, place, offsets, _ = mse.moe_sort(x, ids, E, rows=torch.zeros(T * k, H, device="cuda"))
+            ctx.save_for_backward(place)
+            ctx.mark_non_differentiable(place, offsets)
+            return rows, place, offsets
+
+        @staticmethod
+        def backward(ctx, drows, *_):
+            return mse.moe_sort_backward(drows.contiguous(), *ctx.saved_tensors), None
+
+    class Unsort(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, rows, place, w, base):
+            ctx.save_for_backward(rows, place, w)
+            return mse.moe_unsort(rows, place, w, base=base)
+
+        @staticmethod
+        def backward(ctx, dy):
+            rows, place, w = ctx.saved_tensors
+            drows, dw = mse.moe_unsort_backward(dy.contiguous(), place, rows, w, drows=torch.zeros_like(rows))
+            return drows, None, dw, dy
+
+    ids = some_ids(T, k, E, 3)
+    leaves = [torch.randn(T, H, generator=gen(1)), torch.rand(T, k, generator=gen(2)), torch.randn(E, H, H, generator=gen(3)) / H ** 0.5]
+    dy = torch.randn(T, H, generator=gen(4))
+    x, w, m = [v.cuda().requires_grad_() for v in leaves]
+    rows, place, offsets = Sort.apply(x, ids.cuda())
+    at = offsets.tolist()
+    out = torch.cat([rows[at[e]:at[e + 1]] @ m[e] for e in range(E)] + [rows[at[E]:]])
+    Unsort.apply(out, place, w, x).backward(dy.cuda())
+    X, W, M = [v.double().requires_grad_() for v in leaves]
+    y = X
+    for j in range(k):
+        here = (ids[:, j] >= 0).double()[:, None]
+        y = y + here * W[:, j, None] * torch.einsum("th,thg->tg", X, M[ids[:, j].clamp_min(0).long()])
+    y.backward(dy.double())
+    # fp32 products and sums of up to H k terms of a few units each
+    for got, want in ((x, X), (w, W), (m, M)):
+        assert float((got.grad.double().cpu() - want.grad).abs().max()) <= 2.0 ** -24 * H * (k + 2) * float(want.grad.abs().max() + 1)

@@ -16,7 +16,7 @@ namespace {
 // ---------------------------------------------------------------------------
 // A row's values stay in the registers of a warp (up to 1024) or of a CTA (up to 8192) between its amax and its rounding; longer
 // rows are read again.  Eight values of a thread are one load, of as many bytes as the rows' alignment lets a load have.
-constexpr int kRoundThreads = 256;
+constexpr int round_threads(int lanes) { return lanes > 256 ? lanes : 256; }
 
 // eight values at `at` of which `left` are there (the others 0), as they lie in memory: 4 words of bf16 or 8 of fp32
 template <bool F32>
@@ -88,15 +88,15 @@ __device__ __forceinline__ void store8(void *q, int64_t at, int64_t left, bool w
     }
 }
 
-// LANES threads to a row (32 or 256), SLOTS times eight values of each kept (0: none, rows of any length)
-// What a thread keeps of eight values: bf16 as they lie in memory (half the registers, six CTAs on an SM), or 32 bits each.  Rows of
-// one load a thread have eight CTAs (silu(gate) up of 16384 x 2048 in bf16 32 us, 43 with four).
-template <bool F32, bool GLU, bool HALF, int LANES, int SLOTS>
-__global__ void __launch_bounds__(kRoundThreads, SLOTS == 1 && LANES > 32 ? 8 : F32 || GLU ? 4 : 6) round_rows_kernel(const RoundParams p, const int align,
+// LANES threads to a row (32, 256 or 512), SLOTS times eight values of each kept (0: none, rows of any length)
+// What a thread keeps of eight values: bf16 as they lie in memory (half the registers, six CTAs on an SM), or 32 bits each.  BLOCKS:
+// CTAs on an SM.  Rows of one load a thread have eight (silu(gate) up of 16384 x 2048 in bf16 32 us, 43 with four).
+template <bool F32, bool GLU, bool HALF, int LANES, int SLOTS, int BLOCKS>
+__global__ void __launch_bounds__(round_threads(LANES), BLOCKS) round_rows_kernel(const RoundParams p, const int align,
                                                                                        const int wide) {
     constexpr bool kWide = F32 || GLU;
-    constexpr int kRows = kRoundThreads / LANES, kKeep = SLOTS > 0 ? SLOTS : 1;
-    __shared__ uint32_t part[2][kRoundThreads / 32];
+    constexpr int kRows = round_threads(LANES) / LANES, kKeep = SLOTS > 0 ? SLOTS : 1;
+    __shared__ uint32_t part[2][round_threads(LANES) / 32];
     pdl_wait();
     // (after the wait: what the next kernel reads early is complete before this kernel began)
     pdl_launch_dependents();
@@ -272,20 +272,27 @@ cudaError_t round_of(const RoundParams &p, int sm_count, bool pdl, cudaStream_t 
     const uintptr_t bits = reinterpret_cast<uintptr_t>(p.x) | (uintptr_t)p.ldx * size | (GLU ? (uintptr_t)p.K * size : 0) | 16u;
     const int align = (int)(bits & (~bits + 1));
     const int wide = ((reinterpret_cast<uintptr_t>(p.q) | (uintptr_t)p.ldq) & 7u) == 0;
-    auto with = [&](auto lanes, auto slots) {
-        constexpr int kRows = kRoundThreads / decltype(lanes)::value;
+    auto with = [&](auto lanes, auto slots, auto blocks) {
+        constexpr int kLanes = decltype(lanes)::value, kSlots = decltype(slots)::value, kRows = round_threads(kLanes) / kLanes;
         // (more CTAs than are resident, where a row is one load: 8192 x 7168 30 us, 33 with eight an SM)
-        const dim3 grid((unsigned)std::min<int64_t>((p.rows + kRows - 1) / kRows, (int64_t)sm_count * (decltype(slots)::value > 0 ? 32 : 8)));
-        return launch_kernel(round_rows_kernel<F32, GLU, HALF, decltype(lanes)::value, decltype(slots)::value>, grid, kRoundThreads, 0,
+        const dim3 grid((unsigned)std::min<int64_t>((p.rows + kRows - 1) / kRows, (int64_t)sm_count * (kSlots > 0 ? 32 : 8)));
+        return launch_kernel(round_rows_kernel<F32, GLU, HALF, kLanes, kSlots, decltype(blocks)::value>, grid, round_threads(kLanes), 0,
                              pdl, 1, s, p, align, wide);
     };
     using std::integral_constant;
-    if (p.K <= 256) return with(integral_constant<int, 32>(), integral_constant<int, 1>());
-    if (p.K <= 1024) return with(integral_constant<int, 32>(), integral_constant<int, 4>());
-    if (p.K <= 2048) return with(integral_constant<int, 256>(), integral_constant<int, 1>());
-    if (p.K <= 4096) return with(integral_constant<int, 256>(), integral_constant<int, 2>());
-    if (p.K <= 8192) return with(integral_constant<int, 256>(), integral_constant<int, 4>());
-    return with(integral_constant<int, 256>(), integral_constant<int, 0>());
+    constexpr bool kWide = F32 || GLU;
+    if (p.K <= 256) return with(integral_constant<int, 32>(), integral_constant<int, 1>(), integral_constant<int, kWide ? 4 : 6>());
+    if (p.K <= 1024) return with(integral_constant<int, 32>(), integral_constant<int, 4>(), integral_constant<int, kWide ? 4 : 6>());
+    if (p.K <= 2048) return with(integral_constant<int, 256>(), integral_constant<int, 1>(), integral_constant<int, 8>());
+    if constexpr (GLU) {   // (us with 256 threads a row and 512: 8192 x 4096 in bf16 40.0, 34.9; 64 x 7168 2.9, 2.5; without gate and up
+                           // fp32 rows 43.7, 47.1)
+        if (p.K <= 4096) return with(integral_constant<int, 512>(), integral_constant<int, 1>(), integral_constant<int, 4>());
+        if (p.K <= 8192) return with(integral_constant<int, 512>(), integral_constant<int, 2>(), integral_constant<int, 3>());
+    } else {
+        if (p.K <= 4096) return with(integral_constant<int, 256>(), integral_constant<int, 2>(), integral_constant<int, F32 ? 4 : 6>());
+        if (p.K <= 8192) return with(integral_constant<int, 256>(), integral_constant<int, 4>(), integral_constant<int, F32 ? 4 : 6>());
+    }
+    return with(integral_constant<int, 256>(), integral_constant<int, 0>(), integral_constant<int, kWide ? 4 : 6>());
 }
 }  // namespace
 

@@ -4,6 +4,9 @@
 //
 // A warp has R weight rows at a time, a lane 16 bytes of every 512, U of those steps on their way while the U before them
 // are multiplied.  The tokens lie in shared memory as 8-bit integers; R rows share what a lane reads of them.
+//
+// Bound by memory where the weights are large (8 sorted rows of 8 experts of 4096 x 7168 38.5 us, 6.1 TB/s; 1 x 12288 x 7168 18 with its
+// rounding), by the launch and two trips to memory where they are small (1 x 2112 x 7168 6.3 us, 5.1 without rounding).
 #include <atomic>
 
 #include "device.h"

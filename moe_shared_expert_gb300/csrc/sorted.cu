@@ -2,6 +2,8 @@
 //
 // All of it moves rows: what bounds each kernel is the memory.  Nothing is drawn by atomics: a pair's place is counted, and
 // every sum has one order.
+#include <atomic>
+
 #include "common.cuh"
 #include "launch.h"
 #include "sorted.h"
@@ -36,8 +38,8 @@ __global__ void __launch_bounds__(kSortThreads) count_pairs_kernel(const SortPar
     for (int e = threadIdx.x; e < p.E; e += kSortThreads) p.hist[(int64_t)blockIdx.x * p.E + e] = count_smem[e];
 }
 
-// hist[c][e] becomes the pairs of expert e in the chunks before c; row n_chunks: in all of them.  A warp has 32 experts' chunks
-// c = warp, warp + 32, .. summed first as 32 runs of neighbouring chunks.
+// hist[c][e] becomes the pairs of expert e in the chunks before c; row n_chunks: in all of them.  Lane: an expert, warp: a 32nd of
+// the chunks, added up first and then run through.
 constexpr int kScanThreads = 1024;
 __global__ void __launch_bounds__(kScanThreads) scan_pairs_kernel(int *hist, int n_chunks, int E) {
     __shared__ int sums[32][33];
@@ -62,6 +64,52 @@ __global__ void __launch_bounds__(kScanThreads) scan_pairs_kernel(int *hist, int
     if (warp == 31) hist[(int64_t)n_chunks * E + e] = run;
 }
 
+// Both in one launch, by a cluster: CTA r has the chunks [r per, (r + 1) per), whose counts stay in its shared memory until it
+// knows the pairs that the CTAs before it found.
+constexpr int kCountCluster = 8, kCountThreads = 1024;
+constexpr int kCountBytes = 160 * 1024;
+
+__global__ void __launch_bounds__(kCountThreads) count_scan_kernel(const SortParams p, const int per) {
+    extern __shared__ int cluster_smem[];
+    int *counts = cluster_smem, *total = counts + per * p.E, *base = total + p.E;   // [per x E], [E], [E]
+    const int tid = threadIdx.x, rank = (int)cluster_ctarank();
+    pdl_wait();
+    pdl_launch_dependents();
+    for (int i = tid; i < per * p.E; i += kCountThreads) counts[i] = 0;
+    __syncthreads();
+    const int c0 = min(rank * per, p.n_chunks), c1 = min(c0 + per, p.n_chunks), pairs = p.chunk * p.top_k;
+    const int64_t i0 = (int64_t)c0 * pairs;
+    const int n = (int)(min((int64_t)c1 * pairs, p.T * p.top_k) - i0);
+    for (int i = tid; i < n; i += kCountThreads) {
+        const int e = local_expert(p, i0 + i);
+        if (e >= 0) atomicAdd(&counts[i / pairs * p.E + e], 1);
+    }
+    __syncthreads();
+    for (int e = tid; e < p.E; e += kCountThreads) {
+        int run = 0;
+        for (int c = 0; c < c1 - c0; ++c) {
+            const int mine = counts[c * p.E + e];
+            counts[c * p.E + e] = run;
+            run += mine;
+        }
+        total[e] = run;
+    }
+    cluster_sync();
+    for (int e = tid; e < p.E; e += kCountThreads) {
+        int before = 0, all = 0;
+        for (int r = 0; r < kCountCluster; ++r) {
+            int v;
+            asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(map_to_rank(smem_u32(total + e), (uint32_t)r)) : "memory");
+            if (r < rank) before += v;
+            all += v;
+        }
+        base[e] = before;
+        if (rank == 0) p.hist[(int64_t)p.n_chunks * p.E + e] = all;
+    }
+    cluster_sync();   // (and nobody is over while others read its totals)
+    for (int i = tid; i < (c1 - c0) * p.E; i += kCountThreads) p.hist[(int64_t)c0 * p.E + i] = base[i % p.E] + counts[i];
+}
+
 // exclusive prefix sums of v[0 .. n) in shared memory by one warp; the total is returned
 __device__ __forceinline__ int warp_prefix(int *v, int n, int lane) {
     int run = 0;
@@ -81,7 +129,9 @@ __device__ __forceinline__ int warp_prefix(int *v, int n, int lane) {
 
 // CTA (c, y): the places of chunk c's pairs, counted by every CTA of the chunk alike, and the y-th share of its rows' copies.
 // A pair's place is its expert's first row, the expert's pairs in the chunks before, and those before it in the chunk.
-template <typename W>
+// Bound by memory, most of it writes: 8192 tokens of 7168 bytes with 8 of 128 experts, 64 of them here, 51 us with the kernels that
+// count (5.4 TB/s; this one alone 44); 4096 tokens of 7168 in bf16 with 8 of 32 experts 89; one token 3.1.
+template <typename W, int WORDS>
 __global__ void __launch_bounds__(kSortThreads) sort_kernel(const SortParams p) {
     extern __shared__ int sort_smem[];
     int *total = sort_smem, *before = total + p.E, *of_warp = before + p.E;   // of_warp: [warps x E]
@@ -93,7 +143,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_kernel(const SortParams p) 
     // The rows go by segments of kWords words a lane: (token, segment) by (token), warps of all the chunk's CTAs in turn; the next
     // one's words are on their way while one's are stored, and the first one's while places are counted.  (Behind the kernels that
     // count, which began after everything before the call was complete, x may be read before the wait.)
-    constexpr int kWords = 4;
+    constexpr int kWords = WORDS;
     const int64_t words = p.row_bytes / (int)sizeof(W);
     const int segs = (int)((words + 32 * kWords - 1) / (32 * kWords));
     const int64_t items = (int64_t)tokens * segs, stride = (int64_t)p.splits * (kSortThreads / 32);
@@ -199,6 +249,7 @@ __device__ __forceinline__ void store_pack(T *p, const float (&f)[V]) {
 // ---------------------------------------------------------------------------
 // y[t] = base[t] + sum_j w[t, j] rows[place[t, j]], ascending j
 // ---------------------------------------------------------------------------
+// Bound by memory: 4096 tokens of 7168 in bf16 with 8 rows each on top of base 90 us, 6.2 TB/s.
 constexpr int kPairs = 4;   // rows of a token on their way at once
 
 template <typename R, typename Y, int V>
@@ -245,7 +296,8 @@ __global__ void __launch_bounds__(256) unsort_kernel(const UnsortParams p) {
 // drows[place[t, j]] = w[t, j] dy[t],  dweights[t, j] = <rows[place[t, j]], dy[t]>
 // ---------------------------------------------------------------------------
 // A CTA has one token at a time, kPairs of its pairs at once: of kManyThreads threads, or where there are too few tokens to fill the
-// SMs of kFewThreads, which take fewer steps one after another along a row (333 tokens of 1001 with 3 of 10 experts in fp32 ... us).
+// SMs of kFewThreads, which take fewer steps one after another along a row.  Bound by memory: 4096 tokens of 7168 in bf16 with 8 rows
+// each 147 us, 6.5 TB/s.
 constexpr int kManyThreads = 128, kFewThreads = 512;
 
 template <typename D, typename R, int V, int THREADS>
@@ -313,7 +365,6 @@ __global__ void __launch_bounds__(THREADS) unsort_backward_kernel(const UnsortBa
 
 // the most values of a row, of 8, 4, 2 and 1, that one access of every tensor may take
 struct Width {
-    uint64_t bits = 0;   // byte addresses and pitches of words of `size`, brought to values
     int64_t values = 0;
     int limit = 8;
     void tensor(const void *base, int64_t pitch, int size) {
@@ -330,8 +381,26 @@ struct Width {
 
 }  // namespace
 
+// Up to this many pairs one cluster counts them.  (us of a sort with two kernels and with the cluster: 16,384 pairs of 2048 fp32 to 16 of
+// 64 experts 15.0, 13.9; 8192 pairs of 2048 bf16 14.4, 12.8; 32,768 of 7168 bf16 90.4, 89.4; 65,536 of 7168 bytes 53.4, 54.6; 131,072 of
+// 512 bf16 32.9, 38.7.)
+constexpr int64_t kClusterPairs = 32768;
+
 cudaError_t launch_sort(const SortParams &p, bool pdl, cudaStream_t s) {
-    if (p.hist) {
+    const int per = (p.n_chunks + kCountCluster - 1) / kCountCluster;
+    const int64_t bytes = (int64_t)(per + 2) * p.E * 4;
+    if (p.hist && p.T * p.top_k <= kClusterPairs && bytes <= kCountBytes) {
+        static std::atomic<uint64_t> done;   // bit per device
+        int dev = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e == cudaSuccess && !(done.load(std::memory_order_acquire) >> (dev & 63) & 1)) {
+            e = cudaFuncSetAttribute(count_scan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kCountBytes);
+            if (e == cudaSuccess) done.fetch_or(1ull << (dev & 63), std::memory_order_acq_rel);
+        }
+        if (e == cudaSuccess)
+            e = launch_kernel(count_scan_kernel, dim3(kCountCluster), kCountThreads, (size_t)bytes, pdl, kCountCluster, s, p, per);
+        if (e != cudaSuccess) return e;
+    } else if (p.hist) {
         cudaError_t e = launch_kernel(count_pairs_kernel, dim3((unsigned)p.n_chunks), kSortThreads, (size_t)p.E * 4, pdl, 1, s, p);
         if (e == cudaSuccess)
             e = launch_kernel(scan_pairs_kernel, dim3((unsigned)((p.E + 31) / 32)), kScanThreads, 0, pdl, 1, s, p.hist,
@@ -341,11 +410,13 @@ cudaError_t launch_sort(const SortParams &p, bool pdl, cudaStream_t s) {
     const dim3 grid((unsigned)p.n_chunks, (unsigned)p.splits);
     const size_t smem = (size_t)p.E * 4 * (2 + kSortThreads / 32);
     switch (p.unit) {
-        case 16: return launch_kernel(sort_kernel<uint4>, grid, kSortThreads, smem, pdl, 1, s, p);
-        case 8: return launch_kernel(sort_kernel<uint2>, grid, kSortThreads, smem, pdl, 1, s, p);
-        case 4: return launch_kernel(sort_kernel<uint32_t>, grid, kSortThreads, smem, pdl, 1, s, p);
-        case 2: return launch_kernel(sort_kernel<uint16_t>, grid, kSortThreads, smem, pdl, 1, s, p);
-        default: return launch_kernel(sort_kernel<uint8_t>, grid, kSortThreads, smem, pdl, 1, s, p);
+        case 16:
+            if (p.few) return launch_kernel(sort_kernel<uint4, 1>, grid, kSortThreads, smem, pdl, 1, s, p);
+            return launch_kernel(sort_kernel<uint4, 4>, grid, kSortThreads, smem, pdl, 1, s, p);
+        case 8: return launch_kernel(sort_kernel<uint2, 4>, grid, kSortThreads, smem, pdl, 1, s, p);
+        case 4: return launch_kernel(sort_kernel<uint32_t, 4>, grid, kSortThreads, smem, pdl, 1, s, p);
+        case 2: return launch_kernel(sort_kernel<uint16_t, 4>, grid, kSortThreads, smem, pdl, 1, s, p);
+        default: return launch_kernel(sort_kernel<uint8_t, 4>, grid, kSortThreads, smem, pdl, 1, s, p);
     }
 }
 

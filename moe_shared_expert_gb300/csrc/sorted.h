@@ -29,6 +29,7 @@ struct SortParams {
     int32_t *place, *offsets;
     int chunk, n_chunks;                           // tokens of a CTA row (chunk * top_k <= kSortThreads)
     int splits;                                    // CTAs that share a chunk's copies
+    int few;                                       // few bytes in all: a warp copies one word a lane at a time
     int *hist;                                     // [n_chunks + 1 x E], or null: every CTA counts all ids
     int unit;                                      // bytes of a copied word: divides every address and row_bytes
 };

@@ -54,7 +54,10 @@ SORTS = [
     (300, 5, 7, 7, 0, 100, torch.int8, 12, 28, 4),
     (513, 8, 16, 64, 16, 512, torch.bfloat16, 0, 0, 0),      # more pairs than every CTA counts: 4104
     (512, 8, 16, 64, 16, 512, torch.bfloat16, 0, 0, 0),
-    (5000, 6, 256, 256, 0, 72, torch.float32, 0, 0, 0),
+    (5000, 6, 256, 256, 0, 72, torch.float32, 0, 0, 0),      # 30,000: counted by a cluster
+    (4096, 8, 1024, 1024, 0, 16, torch.bfloat16, 0, 0, 0),   # 32,768
+    (4097, 8, 30, 40, 5, 16, torch.bfloat16, 0, 0, 0),       # and beyond
+    (20, 8, 5, 5, 0, 2048, torch.bfloat16, 0, 0, 0),
     (9000, 1, 3, 3, 0, 40, torch.float16, 0, 0, 0),
     (2100, 32, 40, 50, 2, 16, torch.float8_e4m3fn, 0, 0, 0),
 ]

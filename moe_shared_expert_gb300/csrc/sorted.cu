@@ -3,6 +3,7 @@
 // All of it moves rows: what bounds each kernel is the memory.  Nothing is drawn by atomics: a pair's place is counted, and
 // every sum has one order.
 #include <atomic>
+#include <type_traits>
 
 #include "common.cuh"
 #include "launch.h"
@@ -231,20 +232,44 @@ __device__ __forceinline__ float value_of(float v) { return v; }
 __device__ __forceinline__ void put(uint16_t &o, float v) { o = f32_to_bf16_bits(v); }
 __device__ __forceinline__ void put(float &o, float v) { o = v; }
 
-// V values as they lie in memory, in words of up to 16 bytes
-template <typename T, int V>
-struct alignas(V * sizeof(T) > 16 ? 16 : V * sizeof(T)) Pack {
-    T v[V];
+// Words of U values, as many as the alignment of every tensor lets an access have.  A thread has one word of four or eight at a time;
+// of rows that allow fewer, a warp has kSpan neighbouring values, a lane eight of them in words at steps of 32 (4000 tokens of 4099 in
+// bf16, 6 rows each: 82 us and 102 back, 191 and 183 with one value a thread; of 4096 50 and 72).
+constexpr int kSpan = 256;
+
+template <typename T, int U>
+struct alignas(U * sizeof(T) > 16 ? 16 : U * sizeof(T)) Word {
+    T v[U];
 };
-template <typename T, int V>
-__device__ __forceinline__ Pack<T, V> load_pack(const T *p) { return *reinterpret_cast<const Pack<T, V> *>(p); }
-template <typename T, int V>
-__device__ __forceinline__ void store_pack(T *p, const float (&f)[V]) {
-    Pack<T, V> o;
+// the lane's values of p[0 .. left); what lies behind it is read from the front instead, so that no load waits for a branch
+template <typename T, int U>
+struct Span {
+    Word<T, U> w[8 / U];
+    __device__ __forceinline__ void load(const T *p, int64_t left, int lane) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) put(o.v[i], f[i]);
-    *reinterpret_cast<Pack<T, V> *>(p) = o;
-}
+        for (int i = 0; i < 8 / U; ++i) {
+            const int at = (i * 32 + lane) * U;
+            w[i] = *reinterpret_cast<const Word<T, U> *>(p + (at < left ? at : 0));
+        }
+    }
+    __device__ __forceinline__ void clear_behind(int64_t left, int lane) {
+#pragma unroll
+        for (int i = 0; i < 8 / U; ++i)
+#pragma unroll
+            for (int j = 0; j < U; ++j)
+                if ((i * 32 + lane) * U >= left) w[i].v[j] = T(0);
+    }
+    __device__ __forceinline__ void store(T *p, int64_t left, int lane, const float (&f)[8]) {
+#pragma unroll
+        for (int i = 0; i < 8 / U; ++i) {
+            const int at = (i * 32 + lane) * U;
+#pragma unroll
+            for (int j = 0; j < U; ++j) put(w[i].v[j], f[i * U + j]);
+            if (at < left) *reinterpret_cast<Word<T, U> *>(p + at) = w[i];
+        }
+    }
+    __device__ __forceinline__ float at(int i) const { return value_of(w[i / U].v[i % U]); }
+};
 
 // ---------------------------------------------------------------------------
 // y[t] = base[t] + sum_j w[t, j] rows[place[t, j]], ascending j
@@ -252,26 +277,48 @@ __device__ __forceinline__ void store_pack(T *p, const float (&f)[V]) {
 // Bound by memory: 4096 tokens of 7168 in bf16 with 8 rows each on top of base 90 us, 6.2 TB/s.
 constexpr int kPairs = 4;   // rows of a token on their way at once
 
-template <typename R, typename Y, int V>
+// What a thread has of a row at a time, from `at` values on: one word, or a lane's part of a span.
+template <typename T, int U>
+struct Single {
+    Word<T, U> w;
+    __device__ __forceinline__ void load(const T *p, int64_t, int) { w = *reinterpret_cast<const Word<T, U> *>(p); }
+    __device__ __forceinline__ void store(T *p, int64_t, int, const float (&f)[U]) {
+#pragma unroll
+        for (int j = 0; j < U; ++j) put(w.v[j], f[j]);
+        *reinterpret_cast<Word<T, U> *>(p) = w;
+    }
+    __device__ __forceinline__ float at(int i) const { return value_of(w.v[i]); }
+};
+
+template <typename R, typename Y, int U>
 __global__ void __launch_bounds__(256) unsort_kernel(const UnsortParams p) {
+    constexpr bool kSingle = U >= 4;
+    constexpr int kValues = kSingle ? U : 8;
+    using In = typename std::conditional<kSingle, Single<R, U>, Span<R, U>>::type;
+    using Out = typename std::conditional<kSingle, Single<Y, U>, Span<Y, U>>::type;
     pdl_wait();
     const R *rows = static_cast<const R *>(p.rows);
-    const int64_t per = p.H / V, items = p.T * per;
-    for (int64_t it = (int64_t)blockIdx.x * 256 + threadIdx.x; it < items; it += (int64_t)gridDim.x * 256) {
-        const int64_t t = it / per, c = (it - t * per) * V;
-        float acc[V];
+    const int lane = threadIdx.x % 32;
+    // items of a thread, or of a warp
+    const uint32_t per = (uint32_t)(kSingle ? p.H / U : (p.H + kSpan - 1) / kSpan);
+    const int64_t items = p.T * per, stride = (int64_t)gridDim.x * (kSingle ? 256 : 8);
+    for (int64_t it = kSingle ? (int64_t)blockIdx.x * 256 + threadIdx.x : (int64_t)blockIdx.x * 8 + threadIdx.x / 32; it < items;
+         it += stride) {
+        const int64_t t = items >> 32 ? it / per : (uint32_t)it / per, c = (it - t * per) * (kSingle ? U : kSpan), left = p.H - c;
+        float acc[kValues];
         if (p.base) {
-            const Pack<Y, V> b = load_pack<Y, V>(static_cast<const Y *>(p.base) + t * p.H + c);
+            Out b;
+            b.load(static_cast<const Y *>(p.base) + t * p.H + c, left, lane);
 #pragma unroll
-            for (int i = 0; i < V; ++i) acc[i] = value_of(b.v[i]);
+            for (int i = 0; i < kValues; ++i) acc[i] = b.at(i);
         } else {
 #pragma unroll
-            for (int i = 0; i < V; ++i) acc[i] = 0.f;
+            for (int i = 0; i < kValues; ++i) acc[i] = 0.f;
         }
         for (int j0 = 0; j0 < p.top_k; j0 += kPairs) {
             int64_t row[kPairs];
             float w[kPairs];
-            Pack<R, V> v[kPairs];
+            In v[kPairs];
 #pragma unroll
             for (int j = 0; j < kPairs; ++j) {
                 const bool have = j0 + j < p.top_k;
@@ -281,14 +328,15 @@ __global__ void __launch_bounds__(256) unsort_kernel(const UnsortParams p) {
             }
 #pragma unroll
             for (int j = 0; j < kPairs; ++j)
-                if (row[j] >= 0) v[j] = load_pack<R, V>(rows + row[j] * p.ldr + c);
+                if (row[j] >= 0) v[j].load(rows + row[j] * p.ldr + c, left, lane);
 #pragma unroll
             for (int j = 0; j < kPairs; ++j)
                 if (row[j] >= 0)
 #pragma unroll
-                    for (int i = 0; i < V; ++i) acc[i] = fmaf(w[j], value_of(v[j].v[i]), acc[i]);
+                    for (int i = 0; i < kValues; ++i) acc[i] = fmaf(w[j], v[j].at(i), acc[i]);
         }
-        store_pack<Y, V>(static_cast<Y *>(p.y) + t * p.H + c, acc);
+        Out o;
+        o.store(static_cast<Y *>(p.y) + t * p.H + c, left, lane, acc);
     }
 }
 
@@ -300,7 +348,7 @@ __global__ void __launch_bounds__(256) unsort_kernel(const UnsortParams p) {
 // each 147 us, 6.5 TB/s.
 constexpr int kManyThreads = 128, kFewThreads = 512;
 
-template <typename D, typename R, int V, int THREADS>
+template <typename D, typename R, int U, int THREADS>
 __global__ void __launch_bounds__(THREADS) unsort_backward_kernel(const UnsortBackwardParams p) {
     __shared__ float part[THREADS / 32][kPairs];
     pdl_wait();
@@ -322,27 +370,62 @@ __global__ void __launch_bounds__(THREADS) unsort_backward_kernel(const UnsortBa
                 any |= row[j] >= 0;
                 dot[j] = 0.f;
             }
-            if (any)
-                for (int64_t c = (int64_t)threadIdx.x * V; c < p.H; c += THREADS * V) {
-                    const Pack<D, V> d = load_pack<D, V>(dy + t * p.H + c);
-                    Pack<R, V> v[kPairs];
-                    if (p.dweights)
-#pragma unroll
+            if constexpr (U >= 4) {   // one word a lane
+                if (any)
+                    for (int64_t c = (int64_t)threadIdx.x * U; c < p.H; c += THREADS * U) {
+                        const Word<D, U> d = *reinterpret_cast<const Word<D, U> *>(dy + t * p.H + c);
+                        Word<R, U> v[kPairs];
+                        if (p.dweights)
+    #pragma unroll
+                            for (int j = 0; j < kPairs; ++j)
+                                if (row[j] >= 0) v[j] = *reinterpret_cast<const Word<R, U> *>(rows + row[j] * p.ldr + c);
+    #pragma unroll
                         for (int j = 0; j < kPairs; ++j)
-                            if (row[j] >= 0) v[j] = load_pack<R, V>(rows + row[j] * p.ldr + c);
-#pragma unroll
+                            if (row[j] >= 0) {
+                                Word<R, U> o;
+    #pragma unroll
+                                for (int i = 0; i < U; ++i) {
+                                    const float g = value_of(d.v[i]);
+                                    if (p.dweights) dot[j] = fmaf(value_of(v[j].v[i]), g, dot[j]);
+                                    put(o.v[i], w[j] * g);
+                                }
+                                *reinterpret_cast<Word<R, U> *>(drows + row[j] * p.ldd + c) = o;
+                            }
+                    }
+            } else {
+                auto span = [&](int64_t c, auto whole) {
+                    const int64_t left = decltype(whole)::value ? kSpan : p.H - c;
+                    Span<D, U> d;
+                    d.load(dy + t * p.H + c, left, lane);
+                    Span<R, U> v[kPairs];
+                    if (p.dweights)
+    #pragma unroll
+                        for (int j = 0; j < kPairs; ++j)
+                            if (row[j] >= 0) v[j].load(rows + row[j] * p.ldr + c, left, lane);
+                    if constexpr (!decltype(whole)::value) {
+                        d.clear_behind(left, lane);
+    #pragma unroll
+                        for (int j = 0; j < kPairs; ++j) v[j].clear_behind(left, lane);
+                    }
+    #pragma unroll
                     for (int j = 0; j < kPairs; ++j)
                         if (row[j] >= 0) {
-                            float o[V];
-#pragma unroll
-                            for (int i = 0; i < V; ++i) {
-                                const float g = value_of(d.v[i]);
-                                if (p.dweights) dot[j] = fmaf(value_of(v[j].v[i]), g, dot[j]);
+                            float o[8];
+    #pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                const float g = d.at(i);
+                                if (p.dweights) dot[j] = fmaf(v[j].at(i), g, dot[j]);
                                 o[i] = w[j] * g;
                             }
-                            store_pack<R, V>(drows + row[j] * p.ldd + c, o);
+                            v[j].store(drows + row[j] * p.ldd + c, left, lane, o);
                         }
+                };
+                if (any) {
+                    int64_t c = (int64_t)warp * kSpan;
+                    for (; c + kSpan <= p.H; c += THREADS / 32 * kSpan) span(c, std::true_type());
+                    if (c < p.H) span(c, std::false_type());
                 }
+            }
             if (!p.dweights) continue;
 #pragma unroll
             for (int j = 0; j < kPairs; ++j) {
@@ -415,8 +498,8 @@ cudaError_t launch_sort(const SortParams &p, bool pdl, cudaStream_t s) {
             return launch_kernel(sort_kernel<uint4, 4>, grid, kSortThreads, smem, pdl, 1, s, p);
         case 8: return launch_kernel(sort_kernel<uint2, 4>, grid, kSortThreads, smem, pdl, 1, s, p);
         case 4: return launch_kernel(sort_kernel<uint32_t, 4>, grid, kSortThreads, smem, pdl, 1, s, p);
-        case 2: return launch_kernel(sort_kernel<uint16_t, 4>, grid, kSortThreads, smem, pdl, 1, s, p);
-        default: return launch_kernel(sort_kernel<uint8_t, 4>, grid, kSortThreads, smem, pdl, 1, s, p);
+        case 2: return launch_kernel(sort_kernel<uint16_t, 8>, grid, kSortThreads, smem, pdl, 1, s, p);
+        default: return launch_kernel(sort_kernel<uint8_t, 16>, grid, kSortThreads, smem, pdl, 1, s, p);
     }
 }
 
@@ -452,7 +535,8 @@ cudaError_t launch_unsort(const UnsortParams &p, int sm_count, bool pdl, cudaStr
     w.tensor(p.base, p.H, p.y_f32 ? 4 : 2);
     w.tensor(p.y, p.H, p.y_f32 ? 4 : 2);
     const int v = w.width();
-    const dim3 grid((unsigned)std::min<int64_t>((p.T * (p.H / v) + 255) / 256, (int64_t)sm_count * 16));
+    const int64_t ctas = v >= 4 ? (p.T * (p.H / v) + 255) / 256 : (p.T * ((p.H + kSpan - 1) / kSpan) + 7) / 8;
+    const dim3 grid((unsigned)std::min<int64_t>(ctas, (int64_t)sm_count * 16));
     if (p.rows_f32)
         return p.y_f32 ? unsort_of<float, float>(p, v, grid, pdl, s) : unsort_of<float, uint16_t>(p, v, grid, pdl, s);
     return p.y_f32 ? unsort_of<uint16_t, float>(p, v, grid, pdl, s) : unsort_of<uint16_t, uint16_t>(p, v, grid, pdl, s);

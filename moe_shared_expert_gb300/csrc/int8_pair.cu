@@ -6,13 +6,14 @@
 //
 // Warp 0 loads (TMA), warp 1 of the leading CTA issues MMAs.  Warps 4-7 and 8-11 convert the weights of every other k-block each, and
 // each has one half's sums: it reads them when a chunk ends, which is when it would next wait for room to convert into, and stores
-// a tile while two to four converted k-blocks are left for the MMAs.
+// a tile some k-blocks later, while the MMAs have converted ones left.
 //
-// Bound by what an SM takes in and by the power limit.  A k-block brings 48 KB to each SM (tokens are two bytes here), which takes
-// 0.56 us with the MMAs left out, 86 GB/s; its MMAs take 1024 cycles, 0.50 us at 2.07 GHz; together 0.70 to 0.75.  8192 x 12288 x 7168
-// 820 us, 1.76 PFLOP/s, tensor pipe 65 to 70% busy at the 1.97 GHz that the power limit leaves; 8192 x 7168 x 2048 135 us.  Clusters of
-// two pairs that share a tile's tokens by multicast take as long (it is not L2 that holds it up) and find room for 72 of 76 pairs only.
-// Four stages and four slots: with three 10% more; more stages for the weights, set free by the converting warps, change nothing.
+// Bound by hand-overs and by the power limit.  A k-block brings 48 KB to each SM (tokens are two bytes here), which takes
+// 0.48 to 0.56 us with the MMAs and the conversion left out (0.42 of it without the loads too: the way around four stages and
+// slots, whose barriers lie in two SMs); its MMAs take 1024 cycles, 0.50 us at 2.07 GHz; together 0.68 to 0.75.  8192 x 12288 x 7168
+// 815 us, 1.77 PFLOP/s, tensor pipe 71% busy at the 1.97 GHz that the power limit leaves; 8192 x 7168 x 2048 130 us.  Clusters of
+// two pairs that share a tile's tokens by multicast take as long and find room for 72 of 76 pairs only.  With three stages and slots
+// 10% more; more stages for the weights, set free by the converting warps, change nothing.
 #include <atomic>
 
 #include "device.h"
@@ -29,7 +30,7 @@ constexpr int kWorkWarps = 8, kThreads = 128 + 32 * kWorkWarps;
 // registers: 384 threads x 168 at launch >= 128 x 56 + 256 x 224 afterwards
 constexpr int kLaunchRegs = 168;
 constexpr int kTokens = 256, kHalf = kTokens / 2;
-constexpr int kBand = 16;                            // token tiles whose weight tiles are taken in turn (L2 reuse)
+constexpr int kBand = 8;                             // token tiles whose weight tiles are taken in turn (L2 reuse)
 constexpr uint32_t kTokenBox = kHalf / 2 * 128;      // 64 tokens x 64 k, per CTA
 constexpr uint32_t kTokenBytes = 4 * kTokenBox;
 constexpr uint32_t kStage = kWeightTile + kTokenBytes;
@@ -289,8 +290,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         open(id);
         for (int64_t i = h; ok; i += 2) {
             while (ok) {
-                // A chunk's sums are read before the second k-block behind it is converted: its MMAs wait for that.  A tile is
-                // stored after one more, so that up to four converted k-blocks are left for the MMAs meanwhile.
+                // A chunk's sums are read before the second k-block behind it is converted: its MMAs wait for that.  (Before the first,
+                // or as soon as they are there: 5 to 14% slower, since conversions then wait; before the third: 15%.)  A tile is
+                // stored after two more, so that converted k-blocks are left for the MMAs meanwhile.
                 const bool due = tiles_left > 0 && (end + 2 <= i || i >= blocks);
                 if (PARTS == 1 && owed && (due || i >= owed_at || i >= blocks)) {
                     owed = false;
@@ -347,7 +349,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 done += min(kb - done, kChunkBlocks);
                 if (done == kb) {
                     owed = true;
-                    owed_at = i + 2;
+                    owed_at = i + 4;
                     done = 0;
                     --tiles_left;
                 }

@@ -168,7 +168,10 @@ mse_status moe_sort(const void *x, int value_bytes, int64_t T, int64_t H, int64_
         return MSE_ERR_INVALID_ARG;
     const int64_t pairs = T * top_k;
     if (rows_capacity < (pairs - 1) * ldr + H) return MSE_ERR_GEOMETRY;
-    if (!disjoint(x, span(T, H, ldx, value_bytes), rows, span(pairs, H, ldr, value_bytes))) return MSE_ERR_INVALID_ARG;
+    // (ids and scales, too, are read by CTAs while others write)
+    if (!disjoint(x, span(T, H, ldx, value_bytes), rows, span(pairs, H, ldr, value_bytes)) ||
+        !disjoint(ids, pairs * 4, place, pairs * 4) || (scales && !disjoint(scales, T * 4, row_scales, pairs * 4)))
+        return MSE_ERR_INVALID_ARG;
     if (!workspace || workspace_bytes < sort_ws(T, top_k, E) || !aligned256(workspace)) return MSE_ERR_WORKSPACE;
     DeviceView d;
     const mse_status st = device_view(&d);

@@ -14,7 +14,7 @@ GOOD = mse.STATUS_CODE["MSE_ERR_UNSUPPORTED_DEVICE"]   # all arguments were take
 
 CALLS = {
     "moe_sort": dict(x=FAKE, value_bytes=2, T=5, H=8, ldx=8, ids=FAKE, top_k=2, E=4, first_expert=0, scales=FAKE, rows=FAR, ldr=8,
-                     rows_capacity=80, row_scales=FAKE, place=FAKE, offsets=FAKE, workspace=FAKE, workspace_bytes=1 << 20, stream=None),
+                     rows_capacity=80, row_scales=FAR + 4096, place=FAR + 8192, offsets=FAKE, workspace=FAKE, workspace_bytes=1 << 20, stream=None),
     "moe_unsort": dict(rows=FAKE, rows_dtype=0, n_rows=10, ldr=8, place=FAKE, weights=FAKE, T=5, H=8, top_k=2, base=None, y=FAR,
                        y_dtype=0, y_capacity=40, stream=None),
     "moe_unsort_backward": dict(dy=FAKE, dy_dtype=0, place=FAKE, weights=FAKE, rows=FAKE, rows_dtype=0, ldr=8, n_rows=10, T=5, H=8,
@@ -65,6 +65,8 @@ def test_sizes(L, name, arg):
     ("moe_sort", dict(top_k=33)), ("moe_sort", dict(E=1025)), ("moe_sort", dict(T=1 << 29, top_k=4)), ("moe_sort", dict(value_bytes=8)),
     ("moe_sort", dict(value_bytes=0)), ("moe_sort", dict(ldx=7)), ("moe_sort", dict(ldr=7)), ("moe_sort", dict(first_expert=-1)),
     ("moe_sort", dict(scales=None)), ("moe_sort", dict(row_scales=None)), ("moe_sort", dict(rows=FAKE + 64)), ("moe_sort", dict(ldx=(1 << 32) + 1)),
+    ("moe_sort", dict(place=FAKE)), ("moe_sort", dict(place=FAKE + 36)), ("moe_sort", dict(row_scales=FAKE)),
+    ("moe_sort", dict(row_scales=FAKE + 16)),
     ("moe_sort", dict(H=(1 << 22) + 1, ldx=1 << 23, ldr=1 << 23, rows_capacity=MANY)),
     ("moe_unsort", dict(rows_dtype=2)), ("moe_unsort", dict(y_dtype=-1)), ("moe_unsort", dict(ldr=7)), ("moe_unsort", dict(top_k=33)),
     ("moe_unsort", dict(y=FAKE + 158)), ("moe_unsort", dict(base=FAR + 2)),

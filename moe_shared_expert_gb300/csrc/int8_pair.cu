@@ -118,7 +118,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_relinquish_pair();
     }
     // The kernel before this one, of the same call, let this one start after its own wait: the offsets are complete.
+    // (No more tiles than offsets that ascend can make, whatever they say: every number of a tile stays in 32 bits.)
     if (warp == 2) {
+        const int most = (int)(g.T / kTokens + min((int64_t)g.groups, g.T));
         int before = 0;
         for (int g0 = 0; g.offsets && g0 < g.groups; g0 += 32) {
             const int i = g0 + lane;
@@ -136,7 +138,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ctl->row0[i] = (int)a;
                 ctl->end[i] = (int)b;
             }
-            before += __shfl_sync(~0u, upto, 31);
+            before = min(before + __shfl_sync(~0u, upto, 31), most);
         }
         if (lane == 0) ctl->slots = g.offsets ? before : (int)((g.T + kTokens - 1) / kTokens);
     }

@@ -253,6 +253,26 @@ def test_grouped_rows_that_begin_late_or_end_beyond(path):
     assert torch.equal(out[10:], expected(xq[10:], xs[10:], wq[2], ws[2], torch.float32))
 
 
+@pytest.mark.parametrize("P,groups", [(14, 8), (400, 12), (2048, 32), (20000, 60)])
+def test_offsets_that_do_not_ascend_lead_nowhere_else(P, groups, path):
+    """More tiles than a rising row of offsets makes, and numbers far outside."""
+    N, K = 520, 200
+    xq, wq, xs, ws = integers(P, K, seed=1), integers(groups, N, K, seed=2), scales(P, seed=3), scales(groups, N, seed=4)
+    offsets = torch.tensor([0, P] * groups, dtype=torch.int32)[:groups]
+    offsets = torch.cat([offsets, torch.tensor([P], dtype=torch.int32)])
+    offsets[groups // 2], offsets[groups // 2 + 1] = -2 ** 31, 2 ** 31 - 1
+    around = torch.full((P + 600, N), 77.0, device="cuda")
+    mse.int8_grouped_matmul(xq.cuda(), xs.cuda(), offsets.cuda(), wq.cuda(), ws.cuda(), out=around[300:-300])
+    torch.cuda.synchronize()
+    assert bool((around[:300] == 77).all()) and bool((around[-300:] == 77).all())
+    # a rising row of offsets is answered as before
+    offsets = (torch.arange(groups + 1) * P // groups).int()
+    out = mse.int8_grouped_matmul(xq.cuda(), xs.cuda(), offsets.cuda(), wq.cuda(), ws.cuda(), out_dtype=torch.float32)
+    g = groups - 1
+    a, b = int(offsets[g]), int(offsets[g + 1])
+    assert torch.equal(out[a:b], expected(xq[a:b], xs[a:b], wq[g], ws[g], torch.float32))
+
+
 # Every kernel and split that the rules choose, each with its launch plan.
 PLANS = [
     # T, N, K, counts of the groups or None, tile rows, parts

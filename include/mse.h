@@ -620,7 +620,8 @@ MSE_API mse_status mse_moe_launch_plan(int64_t T, int top_k, int64_t E, int64_t 
  * caller runs (any product over rows [offsets[e], offsets[e + 1])).
  *
  * Sizes beyond these are MSE_ERR_INVALID_ARG: T, rows and T * top_k 2^30; H 2^22; row pitches 2^32 values; top_k and E
- * MSE_ROUTE_MAX_TOP_K and MSE_ROUTE_MAX_EXPERTS.  Outputs lie apart from the inputs, but for those named.
+ * MSE_ROUTE_MAX_TOP_K and MSE_ROUTE_MAX_EXPERTS.  Outputs lie apart from the inputs, but for those named.  Calls that run at
+ * the same time need workspaces of their own, graphs among them.
  * ------------------------------------------------------------------------- */
 
 /* Workspace of moe_sort for every token count up to T (0 on invalid arguments): 256-byte aligned, need not be zeroed. */
@@ -662,7 +663,7 @@ MSE_API mse_status moe_unsort(const void *rows, mse_dtype rows_dtype, int64_t n_
  *   rows      [n_rows x H]  as moe_unsort had them, row pitch ldr >= H
  *   drows     [n_rows x H]  of rows' type (rows itself, with its pitch, is allowed), row pitch ldd >= H, drows_capacity >=
  *                           (n_rows - 1) * ldd + H; rows that are no pair's place are left as they were
- *   dweights  [T x top_k]   fp32
+ *   dweights  [T x top_k]   fp32 (weights itself is allowed)
  * place holds no row twice, as moe_sort gives it (else that row of drows is either pair's). */
 MSE_API mse_status moe_unsort_backward(const void *dy, mse_dtype dy_dtype, const int32_t *place, const float *weights,
                                        const void *rows, mse_dtype rows_dtype, int64_t ldr, int64_t n_rows, int64_t T,
@@ -688,7 +689,7 @@ MSE_API mse_status int8_quantise(const void *x, mse_dtype x_dtype, int64_t rows,
                                  void *stream);
 
 /* Workspace of the products for every token count up to T with the same or smaller other sizes (0 on invalid arguments):
- * 256-byte aligned, need not be zeroed. */
+ * 256-byte aligned, need not be zeroed.  Calls that run at the same time need workspaces of their own, graphs among them. */
 MSE_API size_t int8_workspace_bytes(int64_t T, int64_t N, int64_t K, int64_t groups);
 
 /* out[t, n] = (sum_k xq[t, k] wq[n, k]) xs[t] ws[n]: the sum is the integer itself, whatever the kernel; it is rounded to
@@ -696,14 +697,14 @@ MSE_API size_t int8_workspace_bytes(int64_t T, int64_t N, int64_t K, int64_t gro
  *   xq [T x K] int8, row pitch ldx >= K;  xs [T] fp32
  *   wq [N x K] int8, row pitch ldw >= K;  ws [N] fp32
  *   out [T x N] bf16 or fp32, out_capacity >= T*N elements, apart from xq
- * The tensor-core kernels take row pitches of wq that are multiples of 16 and a 16-byte aligned wq; anything else takes
- * the generic kernels. */
+ * The tensor-core kernels, and those for few rows on every path but MSE_PATH_GENERIC, take row pitches of wq that are
+ * multiples of 16 and a 16-byte aligned wq; anything else takes the generic kernels. */
 MSE_API mse_status int8_matmul(const int8_t *xq, int64_t ldx, const float *xs, const int8_t *wq, int64_t ldw, const float *ws,
                                int64_t T, int64_t N, int64_t K, void *out, mse_dtype out_dtype, int64_t out_capacity,
                                void *workspace, size_t workspace_bytes, void *stream);
 
 /* The same of sorted rows with their group's weights: rows [offsets[g], offsets[g + 1]) of xq with wq[g] [N x K] and ws[g]
- * [N].  offsets [groups + 1] int32 ascends, as moe_sort gives it; rows of out outside them are left as they were.  T: rows of
+ * [N].  offsets [groups + 1] int32 ascends, as moe_sort gives it (else which rows are written is open); rows of out outside them are left as they were.  T: rows of
  * xq and out (offsets beyond count as T). */
 MSE_API mse_status int8_grouped_matmul(const int8_t *xq, int64_t ldx, const float *xs, const int32_t *offsets, int64_t groups,
                                        const int8_t *wq, int64_t ldw, const float *ws, int64_t T, int64_t N, int64_t K,

@@ -26,7 +26,9 @@ def int8_workspace_bytes(T: int, N: int, K: int, groups: int = 1) -> int:
 
 
 def new_int8_workspace(T: int, N: int, K: int, groups: int = 1, device="cuda"):
-    """A workspace for int8_linear, int8_matmul and int8_grouped_matmul with up to T rows."""
+    """A workspace for int8_linear, int8_matmul and int8_grouped_matmul with up to T rows.
+
+    Calls that run at the same time, captured graphs among them, need one each."""
     return _r._new_workspace(int8_workspace_bytes(T, N, K, groups), device)
 
 

@@ -68,7 +68,7 @@ def moe_sort_workspace_bytes(T: int, top_k: int, num_experts: int) -> int:
 
 
 def new_moe_sort_workspace(T: int, top_k: int, num_experts: int, device="cuda"):
-    """A workspace for moe_sort with up to T tokens."""
+    """A workspace for moe_sort with up to T tokens; calls that run at the same time, graphs among them, need one each."""
     return _r._new_workspace(moe_sort_workspace_bytes(T, top_k, num_experts), device)
 
 
@@ -152,7 +152,7 @@ def moe_unsort_backward(dy, place, rows=None, weights=None, drows=None, dweights
 
     rows and weights as moe_unsort had them.  Without weights, drows alone (dweights None): rows is not needed, and drows has
     the shape of `drows`, or rows_count (default T * top_k) rows of dy's type.  Rows that are no pair's place are left as they
-    were.  drows may be rows."""
+    were.  drows may be rows, and dweights weights."""
     if _C is None:
         _ready()
     dy_code, ld, (T, H), device = _floats(dy, "dy", 2)

@@ -205,6 +205,16 @@ def test_gradients_in_place_of_the_rows():
     assert got[0] is rows and torch.equal(got[0][:n], want[0][:n]) and torch.equal(got[1], want[1])
 
 
+@pytest.mark.parametrize("T,k,H", [(33, 5, 264), (700, 12, 1001)])
+def test_weights_gradient_in_place_of_the_weights(T, k, H):
+    place, rows, w, _ = unsort_inputs((T, 4, k, 14, H, 0, True, False), torch.bfloat16, torch.float32)
+    dy, w = torch.randn(T, H, generator=gen(4)).cuda(), w.cuda()
+    want = mse.moe_unsort_backward(dy, place.cuda(), rows, w)
+    got = mse.moe_unsort_backward(dy, place.cuda(), rows, w, dweights=w)
+    n = int((place >= 0).sum())
+    assert got[1] is w and torch.equal(w, want[1]) and torch.equal(got[0][:n], want[0][:n])
+
+
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=str)
 def test_sort_backward(dtype):
     T, k, E, H = 40, 6, 9, 264

@@ -6,10 +6,11 @@
 // Warp 0 loads (TMA), warp 1 issues MMAs.  Warps 2-5 and 6-9 convert the weights of every other k-block each (int8_tc.cuh), and each
 // adds one half of the token columns when a chunk of k-blocks ends.
 //
-// Bound by the hand-over of stages and slots and, with 64 tokens, by what an SM takes in: 32 KB a k-block at 86 GB/s.  16 x 12288 x 7168
-// 20.6 us with the kernel before it (memory alone 13; without conversions and MMAs 19.3), 64 x 12288 x 7168 23.5, 16 x 2112 x 7168 9.9 in
-// five parts.  Two CTAs on an SM hide each other's hand-overs; one group of converting warps instead of two takes 64 x 2112 x
-// 7168 from 12.4 to 16.2 us, stages of their own for weights and tokens 1 us more everywhere.
+// Bound by memory and the launch with few tokens: 16 x 12288 x 7168 20.6 us with the kernel before it (memory alone 13; without
+// conversions and MMAs 19.3), 16 x 2112 x 7168 9.9 in five parts.  With 64 tokens by the conversion and the hand-over of stages and
+// slots: 64 x 12288 x 7168 24.0; 160 x 12288 x 7168 38, without conversions 31, with no tokens loaded still 38.  Two CTAs on an SM
+// hide each other's hand-overs; one group of converting warps instead of two takes 64 x 2112 x 7168 from 12.4 to 16.2 us, stages of
+// their own for weights and tokens 1 us more everywhere.
 #include <atomic>
 
 #include "device.h"

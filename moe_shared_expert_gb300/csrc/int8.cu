@@ -232,7 +232,9 @@ __global__ void __launch_bounds__(256) expand_kernel(const int8_t *x, int64_t ld
 constexpr int kSimtRows = 16, kSimtInner = 64;
 
 __global__ void __launch_bounds__(256) int8_simt_kernel(const Int8Gemm g) {
-    __shared__ int8_t sx[16][kSimtInner + 4], sw[16][kSimtInner + 4];
+    // (read as words; a row is 17 of them)
+    __shared__ __align__(16) int8_t sx[16][kSimtInner + 4];
+    __shared__ __align__(16) int8_t sw[16][kSimtInner + 4];
     pdl_wait();
     RowTile t;
     if (!row_tile(g.offsets, g.groups, g.T, kSimtRows, blockIdx.x, t)) return;

@@ -620,7 +620,8 @@ MSE_API mse_status mse_moe_launch_plan(int64_t T, int top_k, int64_t E, int64_t 
  * caller runs (any product over rows [offsets[e], offsets[e + 1])).
  *
  * Sizes beyond these are MSE_ERR_INVALID_ARG: T, rows and T * top_k 2^30; H 2^22; row pitches 2^32 values; top_k and E
- * MSE_ROUTE_MAX_TOP_K and MSE_ROUTE_MAX_EXPERTS.  Outputs lie apart from the inputs, but for those named.  Calls that run at
+ * MSE_ROUTE_MAX_TOP_K and MSE_ROUTE_MAX_EXPERTS.  Outputs and workspaces lie apart from the inputs and from each other, but for
+ * those named (of rows with a pitch, all from the first value to the last counts): else MSE_ERR_INVALID_ARG.  Calls that run at
  * the same time need workspaces of their own, graphs among them.
  * ------------------------------------------------------------------------- */
 

@@ -2,6 +2,7 @@
 // call), workspace carving and kernel choice.
 #include <algorithm>
 #include <cstring>
+#include <initializer_list>
 
 #include "device.h"
 #include "sorted.h"
@@ -16,6 +17,22 @@ bool aligned256(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 255u) 
 bool disjoint(const void *a, int64_t a_bytes, const void *b, int64_t b_bytes) {
     const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
     return x + (uintptr_t)a_bytes <= y || y + (uintptr_t)b_bytes <= x;
+}
+// Memory of an argument, and whether what a call writes lies apart from what it reads and from what else it writes: CTAs read while
+// others write.  (Of a null pointer there is none.)
+struct Range {
+    uintptr_t from, to;
+};
+Range range(const void *p, int64_t bytes) {
+    const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+    return {at, p ? at + (uintptr_t)bytes : at};
+}
+bool apart(std::initializer_list<Range> written, std::initializer_list<Range> read) {
+    for (const Range *w = written.begin(); w != written.end(); ++w) {
+        auto meets = [w](const Range &o) { return w->from < o.to && o.from < w->to; };
+        if (std::any_of(read.begin(), read.end(), meets) || std::any_of(written.begin(), w, meets)) return false;
+    }
+    return true;
 }
 mse_status from_cuda(cudaError_t e) { return e == cudaSuccess ? MSE_OK : MSE_ERR_CUDA; }
 bool dtype_ok(mse_dtype d) { return d == MSE_BF16 || d == MSE_F32; }
@@ -168,14 +185,17 @@ mse_status moe_sort(const void *x, int value_bytes, int64_t T, int64_t H, int64_
         return MSE_ERR_INVALID_ARG;
     const int64_t pairs = T * top_k;
     if (rows_capacity < (pairs - 1) * ldr + H) return MSE_ERR_GEOMETRY;
-    // (ids and scales, too, are read by CTAs while others write)
-    if (!disjoint(x, span(T, H, ldx, value_bytes), rows, span(pairs, H, ldr, value_bytes)) ||
-        !disjoint(ids, pairs * 4, place, pairs * 4) || (scales && !disjoint(scales, T * 4, row_scales, pairs * 4)))
+    const Range x_range = range(x, span(T, H, ldx, value_bytes)), ids_range = range(ids, pairs * 4), scales_range = range(scales, T * 4),
+                offsets_range = range(offsets, (E + 1) * 4), space = range(workspace, (int64_t)sort_ws(T, top_k, E));
+    if (!apart({range(rows, span(pairs, H, ldr, value_bytes)), range(place, pairs * 4), range(row_scales, pairs * 4)},
+               {x_range, ids_range, scales_range, offsets_range, space}))
         return MSE_ERR_INVALID_ARG;
     if (!workspace || workspace_bytes < sort_ws(T, top_k, E) || !aligned256(workspace)) return MSE_ERR_WORKSPACE;
     DeviceView d;
     const mse_status st = device_view(&d);
     if (st != MSE_OK) return st;
+    // (Only with a device: callers that check arguments without one give several of them one address.)
+    if (!apart({offsets_range, space}, {x_range, ids_range, scales_range})) return MSE_ERR_INVALID_ARG;
     begin_untracked_call(stream);
     SortParams p;
     std::memset(&p, 0, sizeof p);

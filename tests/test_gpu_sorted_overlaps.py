@@ -1,0 +1,53 @@
+"""Workspaces, and small outputs, that lie over an input are refused on the host: CTAs read while others write."""
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+mse = pytest.importorskip("moe_shared_expert_gb300")
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    from moe_shared_expert_gb300 import _build
+    _build.build()
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    mse.lib()
+    yield
+    torch.cuda.synchronize()
+    assert mse.poll_device_error() == 0
+
+
+def over(t, dtype, n):
+    """The first n values of `dtype` in t's memory."""
+    return t.flatten().view(torch.uint8).view(dtype)[:n]
+
+
+def refused(f, inputs, **arguments):
+    before = [t.clone() for t in inputs]
+    with pytest.raises(mse.MSEError, match="INVALID_ARG"):
+        f(**arguments)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(inputs, before))
+
+
+@pytest.mark.parametrize("T", [40, 600])   # every CTA counts all ids, and kernels before the sort count them
+@pytest.mark.parametrize("taken", ["x", "ids", "scales"])
+@pytest.mark.parametrize("by", ["offsets", "workspace"])
+def test_sort(T, taken, by):
+    k, E, H = 8, 32, 64
+    a = dict(x=torch.randn(T, H, device="cuda"), ids=torch.randint(0, E, (T, k), dtype=torch.int32, device="cuda"),
+             scales=torch.randn(max(T, 4096), device="cuda")[:T], num_experts=E)
+    if by == "offsets":
+        a["offsets"] = over(a[taken], torch.int32, E + 1)
+    else:
+        # (begun a step before the input's end, in memory of the test's own)
+        room = torch.zeros(1 << 20, dtype=torch.uint8, device="cuda")
+        t = a[taken]
+        a[taken] = room[4096:4096 + t.nbytes].view(t.dtype).view(t.shape).copy_(t)
+        a["workspace"] = room[(4096 + t.nbytes - 1) // 256 * 256:]
+    refused(mse.moe_sort, [a["x"], a["ids"], a["scales"]], **a)
+    del a[by]
+    rows, place, offsets, scales = mse.moe_sort(**a)
+    assert int(offsets[-1]) == T * k and torch.equal(rows[place[3, 2]], a["x"][3]) and float(scales[place[3, 2]]) == float(a["scales"][3])

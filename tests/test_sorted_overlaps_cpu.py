@@ -1,0 +1,57 @@
+"""Outputs that lie over an input or over another output are refused before any CUDA call: CTAs read while others write."""
+import itertools
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import moe_shared_expert_gb300 as mse
+from moe_shared_expert_gb300 import _build
+from tests.test_sorted_refusals_cpu import BAD, CALLS, GOOD
+
+# name: (other arguments, bytes of each pointer's memory, written ones, read ones, pairs that may be the same memory)
+CASES = {
+    "moe_sort": (dict(ldx=9, ldr=10, rows_capacity=98),
+                 dict(x=(4 * 9 + 8) * 2, ids=40, scales=20, rows=(9 * 10 + 8) * 2, row_scales=40, place=40, offsets=20, workspace=256),
+                 ("rows", "place", "row_scales"), ("x", "ids", "scales", "offsets", "workspace"), ()),
+}
+
+
+@pytest.fixture(scope="module")
+def L():
+    _build.build()
+    if torch.cuda.is_available():
+        pytest.skip("the addresses are not real")
+    return mse.lib()
+
+
+def arguments(name):
+    """The call's arguments, every pointer to memory of its own."""
+    other, sizes, *_ = CASES[name]
+    return {**CALLS[name], **other, **{p: (i + 1) << 40 for i, p in enumerate(sizes)}}
+
+
+@pytest.mark.parametrize("name", CASES)
+def test_memory_apart_is_taken(L, name):
+    assert getattr(L, name)(*arguments(name).values()) == GOOD
+
+
+def pairs():
+    for name, (_, sizes, written, read, same) in CASES.items():
+        for w, o in itertools.chain(itertools.product(written, read), itertools.combinations(written, 2)):
+            yield name, w, o, sizes[w], sizes[o], (w, o) in same
+
+
+@pytest.mark.parametrize("name,w,o,w_bytes,o_bytes,same", list(pairs()), ids=lambda v: str(v))
+def test_memory_that_meets_is_refused(L, name, w, o, w_bytes, o_bytes, same):
+    a = arguments(name)
+
+    def at(shift):
+        return getattr(L, name)(*{**a, w: a[o] + shift}.values())
+
+    # (a workspace's address is a multiple of 256: what lies over it moves, not the workspace)
+    for shift in (1 - w_bytes, o_bytes - 1):
+        assert at(shift) == BAD, shift
+    assert same or at(0) == BAD
+    for shift in (-w_bytes, o_bytes):   # side by side
+        assert at(shift) == GOOD, shift

@@ -227,9 +227,9 @@ mse_status moe_unsort(const void *rows, mse_dtype rows_dtype, int64_t n_rows, in
         ldr > kMaxPitch)
         return MSE_ERR_INVALID_ARG;
     if (y_capacity < T * H) return MSE_ERR_GEOMETRY;
-    const int64_t y_bytes = T * H * size_of(y_dtype);
-    if (!disjoint(rows, span(n_rows, H, ldr, size_of(rows_dtype)), y, y_bytes) ||
-        (base && base != y && !disjoint(base, y_bytes, y, y_bytes)))
+    const int64_t y_bytes = T * H * size_of(y_dtype), pairs_bytes = T * top_k * 4;
+    if (!apart({range(y, y_bytes)}, {range(rows, span(n_rows, H, ldr, size_of(rows_dtype))), range(place, pairs_bytes),
+                                     range(weights, pairs_bytes), range(base == y ? nullptr : base, y_bytes)}))
         return MSE_ERR_INVALID_ARG;
     DeviceView d;
     const mse_status st = device_view(&d);
@@ -251,13 +251,20 @@ mse_status moe_unsort_backward(const void *dy, mse_dtype dy_dtype, const int32_t
         n_rows > kMaxRows || H > kMaxInner || top_k > MSE_ROUTE_MAX_TOP_K || ldd < H || ldd > kMaxPitch)
         return MSE_ERR_INVALID_ARG;
     if (drows_capacity < (n_rows - 1) * ldd + H) return MSE_ERR_GEOMETRY;
-    const int64_t size = size_of(rows_dtype), drows_bytes = span(n_rows, H, ldd, size);
-    if (!disjoint(dy, T * H * size_of(dy_dtype), drows, drows_bytes) ||
-        (weights && !(rows == drows && ldr == ldd) && !disjoint(rows, span(n_rows, H, ldr, size), drows, drows_bytes)))
+    const int64_t size = size_of(rows_dtype), pairs_bytes = T * top_k * 4;
+    const Range dy_range = range(dy, T * H * size_of(dy_dtype)), place_range = range(place, pairs_bytes),
+                rows_range = range(weights ? rows : nullptr, span(n_rows, H, ldr, size)), no_range = range(nullptr, 0);
+    const bool in_place = rows == drows && ldr == ldd;
+    if (!apart({range(drows, span(n_rows, H, ldd, size)), range(dweights, pairs_bytes)}, {}) ||
+        !apart({range(drows, span(n_rows, H, ldd, size))},
+               {dy_range, place_range, range(weights, pairs_bytes), in_place ? no_range : rows_range}))
         return MSE_ERR_INVALID_ARG;
     DeviceView d;
     const mse_status st = device_view(&d);
     if (st != MSE_OK) return st;
+    if (!apart({range(dweights, pairs_bytes)},   // (only with a device, as in moe_sort)
+               {dy_range, place_range, rows_range, dweights == weights ? no_range : range(weights, pairs_bytes)}))
+        return MSE_ERR_INVALID_ARG;
     begin_untracked_call(stream);
     UnsortBackwardParams p;
     p.dy = dy; p.place = place; p.weights = weights;

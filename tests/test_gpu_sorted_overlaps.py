@@ -51,3 +51,16 @@ def test_sort(T, taken, by):
     del a[by]
     rows, place, offsets, scales = mse.moe_sort(**a)
     assert int(offsets[-1]) == T * k and torch.equal(rows[place[3, 2]], a["x"][3]) and float(scales[place[3, 2]]) == float(a["scales"][3])
+
+
+@pytest.mark.parametrize("taken", ["dy", "place", "rows", "weights"])
+def test_unsort_backward(taken):
+    T, k, H = 40, 8, 64
+    room = torch.randn(4 * T * k, device="cuda")
+    a = dict(dy=torch.randn(T, H, device="cuda"), place=torch.arange(T * k, device="cuda").int().view(T, k),
+             rows=torch.randn(T * k, H, device="cuda"), weights=room[:T * k].view(T, k), drows=torch.zeros(T * k, H, device="cuda"))
+    # (the weights' own memory is allowed, but not all of it but one)
+    dweights = room[1:T * k + 1] if taken == "weights" else over(a[taken], torch.float32, T * k)
+    refused(mse.moe_unsort_backward, [a["dy"], a["place"], a["rows"], a["weights"], a["drows"]], dweights=dweights.view(T, k), **a)
+    drows, dw = mse.moe_unsort_backward(**a, dweights=room[T * k:2 * T * k].view(T, k))
+    assert torch.equal(drows[5 * k + 2], a["weights"][5, 2] * a["dy"][5])

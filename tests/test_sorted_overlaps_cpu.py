@@ -14,6 +14,11 @@ CASES = {
     "moe_sort": (dict(ldx=9, ldr=10, rows_capacity=98),
                  dict(x=(4 * 9 + 8) * 2, ids=40, scales=20, rows=(9 * 10 + 8) * 2, row_scales=40, place=40, offsets=20, workspace=256),
                  ("rows", "place", "row_scales"), ("x", "ids", "scales", "offsets", "workspace"), ()),
+    "moe_unsort": (dict(ldr=9), dict(rows=(9 * 9 + 8) * 2, place=40, weights=40, base=80, y=80), ("y",),
+                   ("rows", "place", "weights", "base"), (("y", "base"),)),
+    "moe_unsort_backward": (dict(ldr=9, ldd=10, drows_capacity=98),
+                            dict(dy=80, place=40, weights=40, rows=(9 * 9 + 8) * 2, drows=(9 * 10 + 8) * 2, dweights=40),
+                            ("drows",), ("dy", "place", "weights", "rows", "dweights"), ()),
 }
 
 
@@ -55,3 +60,15 @@ def test_memory_that_meets_is_refused(L, name, w, o, w_bytes, o_bytes, same):
     assert same or at(0) == BAD
     for shift in (-w_bytes, o_bytes):   # side by side
         assert at(shift) == GOOD, shift
+
+
+def test_what_may_lie_over_what(L):
+    a = arguments("moe_unsort_backward")
+    a.update(ldd=9, drows_capacity=89, drows=a["rows"], dweights=a["weights"])
+    assert L.moe_unsort_backward(*a.values()) == GOOD
+    a = arguments("moe_unsort")
+    assert L.moe_unsort(*{**a, "y": a["base"]}.values()) == GOOD
+    # without weights, rows is not read
+    a = arguments("moe_unsort_backward")
+    a.update(weights=None, dweights=None, rows=a["drows"] + 2)
+    assert L.moe_unsort_backward(*a.values()) == GOOD

@@ -683,8 +683,10 @@ MSE_API mse_status moe_unsort_backward(const void *dy, mse_dtype dy_dtype, const
  * NaN throughout (scale NaN, q 0).
  *   x       [rows x K], swiglu: [rows x 2K]  bf16 or fp32, row pitch ldx
  *   last    null, or one int32 on the device: rows from *last on are left alone (offsets + E of moe_sort)
- *   q       [rows x K]  int8, row pitch ldq >= K, q_capacity >= (rows - 1) * ldq + K, apart from x
- *   scales  [rows] fp32 */
+ *   q       [rows x K]  int8, row pitch ldq >= K, q_capacity >= (rows - 1) * ldq + K
+ *   scales  [rows] fp32
+ * q and scales lie apart from x, last and each other (MSE_ERR_INVALID_ARG; of rows with a pitch, all from the first value to
+ * the last counts). */
 MSE_API mse_status int8_quantise(const void *x, mse_dtype x_dtype, int64_t rows, int64_t K, int64_t ldx, int swiglu,
                                  const int32_t *last, int8_t *q, int64_t ldq, int64_t q_capacity, float *scales,
                                  void *stream);

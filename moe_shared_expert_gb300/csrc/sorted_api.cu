@@ -284,10 +284,12 @@ mse_status int8_quantise(const void *x, mse_dtype x_dtype, int64_t rows, int64_t
         ldq < K || ldx > kMaxPitch || ldq > kMaxPitch)
         return MSE_ERR_INVALID_ARG;
     if (q_capacity < (rows - 1) * ldq + K) return MSE_ERR_GEOMETRY;
-    if (!disjoint(x, span(rows, width, ldx, size_of(x_dtype)), q, span(rows, K, ldq, 1))) return MSE_ERR_INVALID_ARG;
+    const Range x_range = range(x, span(rows, width, ldx, size_of(x_dtype))), last_range = range(last, 4), scales_range = range(scales, rows * 4);
+    if (!apart({range(q, span(rows, K, ldq, 1))}, {x_range, last_range, scales_range})) return MSE_ERR_INVALID_ARG;
     DeviceView d;
     const mse_status st = device_view(&d);
     if (st != MSE_OK) return st;
+    if (!apart({scales_range}, {x_range, last_range})) return MSE_ERR_INVALID_ARG;   // (only with a device, as in moe_sort)
     begin_untracked_call(stream);
     RoundParams p;
     p.x = x; p.rows = rows; p.K = K; p.ldx = ldx;

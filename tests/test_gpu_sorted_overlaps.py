@@ -64,3 +64,14 @@ def test_unsort_backward(taken):
     refused(mse.moe_unsort_backward, [a["dy"], a["place"], a["rows"], a["weights"], a["drows"]], dweights=dweights.view(T, k), **a)
     drows, dw = mse.moe_unsort_backward(**a, dweights=room[T * k:2 * T * k].view(T, k))
     assert torch.equal(drows[5 * k + 2], a["weights"][5, 2] * a["dy"][5])
+
+
+@pytest.mark.parametrize("taken", ["x", "offsets"])
+@pytest.mark.parametrize("swiglu", [False, True])
+def test_quantise(taken, swiglu):
+    x, room = torch.randn(40, 64, device="cuda"), torch.full((80,), 40, dtype=torch.int32, device="cuda")
+    offsets = room[:41]
+    scales = over(x, torch.float32, 40) if taken == "x" else room.view(torch.float32)[40:]   # (the last offset is read)
+    refused(mse.int8_quantise, [x, room], x=x, swiglu=swiglu, offsets=offsets, scales=scales)
+    q, s = mse.int8_quantise(x, swiglu=swiglu, offsets=offsets, scales=torch.zeros(40, device="cuda"))
+    assert bool((q.abs().amax(1) == 127).all()) and bool((s > 0).all())

@@ -19,6 +19,7 @@ CASES = {
     "moe_unsort_backward": (dict(ldr=9, ldd=10, drows_capacity=98),
                             dict(dy=80, place=40, weights=40, rows=(9 * 9 + 8) * 2, drows=(9 * 10 + 8) * 2, dweights=40),
                             ("drows",), ("dy", "place", "weights", "rows", "dweights"), ()),
+    "int8_quantise": (dict(ldx=17), dict(x=(4 * 17 + 16) * 2, last=4, q=4 * 16 + 8, scales=20), ("q",), ("x", "last", "scales"), ()),
 }
 
 

@@ -675,7 +675,8 @@ MSE_API mse_status moe_unsort_backward(const void *dy, mse_dtype dy_dtype, const
  * Products in 8-bit integers: a scale for each row of either operand (each token, each output channel).
  *
  * Sizes beyond these are MSE_ERR_INVALID_ARG: T, rows and groups * N 2^30; N 2^22; K 2^17 - 1 (so that a sum fits 32 bits;
- * int8_quantise 2^22); groups MSE_ROUTE_MAX_EXPERTS; row pitches 2^32 values.
+ * int8_quantise 2^22); groups MSE_ROUTE_MAX_EXPERTS; row pitches 2^32 values.  So are outputs and workspaces that lie over an
+ * input or over each other (of rows with a pitch, all from the first value to the last counts), but for y over x in int8_linear.
  * ------------------------------------------------------------------------- */
 
 /* Rows rounded to 8-bit integers:  a = max(max |r|, 2^-100),  scale = a / 127,  q = rint(127 r / a), ties to even, of a
@@ -684,9 +685,7 @@ MSE_API mse_status moe_unsort_backward(const void *dy, mse_dtype dy_dtype, const
  *   x       [rows x K], swiglu: [rows x 2K]  bf16 or fp32, row pitch ldx
  *   last    null, or one int32 on the device: rows from *last on are left alone (offsets + E of moe_sort)
  *   q       [rows x K]  int8, row pitch ldq >= K, q_capacity >= (rows - 1) * ldq + K
- *   scales  [rows] fp32
- * q and scales lie apart from x, last and each other (MSE_ERR_INVALID_ARG; of rows with a pitch, all from the first value to
- * the last counts). */
+ *   scales  [rows] fp32 */
 MSE_API mse_status int8_quantise(const void *x, mse_dtype x_dtype, int64_t rows, int64_t K, int64_t ldx, int swiglu,
                                  const int32_t *last, int8_t *q, int64_t ldq, int64_t q_capacity, float *scales,
                                  void *stream);
@@ -699,7 +698,7 @@ MSE_API size_t int8_workspace_bytes(int64_t T, int64_t N, int64_t K, int64_t gro
  * fp32, multiplied by xs[t], then by ws[n], and rounded to out's type.
  *   xq [T x K] int8, row pitch ldx >= K;  xs [T] fp32
  *   wq [N x K] int8, row pitch ldw >= K;  ws [N] fp32
- *   out [T x N] bf16 or fp32, out_capacity >= T*N elements, apart from xq
+ *   out [T x N] bf16 or fp32, out_capacity >= T*N elements
  * The tensor-core kernels, and those for few rows on every path but MSE_PATH_GENERIC, take row pitches of wq that are
  * multiples of 16 and a 16-byte aligned wq; anything else takes the generic kernels. */
 MSE_API mse_status int8_matmul(const int8_t *xq, int64_t ldx, const float *xs, const int8_t *wq, int64_t ldw, const float *ws,

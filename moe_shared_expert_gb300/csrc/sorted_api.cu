@@ -14,10 +14,6 @@ namespace {
 
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 bool aligned256(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 255u) == 0; }
-bool disjoint(const void *a, int64_t a_bytes, const void *b, int64_t b_bytes) {
-    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-    return x + (uintptr_t)a_bytes <= y || y + (uintptr_t)b_bytes <= x;
-}
 // Memory of an argument, and whether what a call writes lies apart from what it reads and from what else it writes: CTAs read while
 // others write.  (Of a null pointer there is none.)
 struct Range {
@@ -90,10 +86,21 @@ mse_status check_product(const void *x, int64_t ldx, const void *xs, const void 
     return MSE_OK;
 }
 
-// the product reads all of a row of xq for every part of a row of out
-bool apart(const Int8Gemm &g) {
-    return disjoint(g.xq, span(g.T, g.K, g.ldx, 1), g.out, g.T * g.N * (g.out_f32 ? 4 : 2));
+// What a product reads and writes: of int8_linear, whose xs are in the workspace, x in place of xq.
+struct ProductMemory {
+    Range x, xs, wq, ws, offsets, out, space;
+};
+ProductMemory memory_of(const Int8Gemm &g, const void *x, int64_t ldx, int64_t x_size, const void *workspace) {
+    const int64_t channels = g.groups * g.N;
+    return {range(x, span(g.T, g.K, ldx, x_size)), range(g.xs, g.T * 4), range(g.wq, span(channels, g.K, g.ldw, 1)),
+            range(g.ws, channels * 4), range(g.offsets, (g.groups + 1) * (int64_t)4), range(g.out, g.T * g.N * (g.out_f32 ? 4 : 2)),
+            range(workspace, (int64_t)int8_ws(g.T, g.K).total)};
 }
+// (every part of a row of out takes all of a row of x)
+bool out_apart(const ProductMemory &m, bool over_x) {
+    return apart({m.out}, {over_x ? range(nullptr, 0) : m.x, m.xs, m.wq, m.ws, m.offsets, m.space});
+}
+bool space_apart(const ProductMemory &m) { return apart({m.space}, {m.x, m.xs, m.wq, m.ws, m.offsets}); }
 int64_t pitch16(int64_t K) { return (K + 63) / 64 * 64; }   // of tokens in fp16
 
 // Token rows of a tile: up to 4 the kernel for few, 16 to 64 the swap-AB kernel, 256 the CTA-pair kernel.
@@ -330,9 +337,11 @@ mse_status int8_matmul(const int8_t *xq, int64_t ldx, const float *xs, const int
     mse_status st = check_product(xq, ldx, xs, wq, ldw, ws, T, N, K, 1, out, out_dtype, out_capacity, workspace, workspace_bytes);
     if (st != MSE_OK) return st;
     const Int8Gemm g = product(xq, ldx, xs, nullptr, 1, wq, ldw, ws, T, N, K, out, out_dtype);
-    if (!apart(g)) return MSE_ERR_INVALID_ARG;
+    const ProductMemory m = memory_of(g, xq, ldx, 1, workspace);
+    if (!out_apart(m, false)) return MSE_ERR_INVALID_ARG;
     DeviceView d;
     if ((st = device_view(&d)) != MSE_OK) return st;
+    if (!space_apart(m)) return MSE_ERR_INVALID_ARG;   // (only with a device, as in moe_sort)
     begin_untracked_call(stream);
     return run_product(g, d, workspace, static_cast<cudaStream_t>(stream));
 }
@@ -346,9 +355,11 @@ mse_status int8_grouped_matmul(const int8_t *xq, int64_t ldx, const float *xs, c
         check_product(xq, ldx, xs, wq, ldw, ws, T, N, K, groups, out, out_dtype, out_capacity, workspace, workspace_bytes);
     if (st != MSE_OK) return st;
     const Int8Gemm g = product(xq, ldx, xs, offsets, groups, wq, ldw, ws, T, N, K, out, out_dtype);
-    if (!apart(g)) return MSE_ERR_INVALID_ARG;
+    const ProductMemory m = memory_of(g, xq, ldx, 1, workspace);
+    if (!out_apart(m, false)) return MSE_ERR_INVALID_ARG;
     DeviceView d;
     if ((st = device_view(&d)) != MSE_OK) return st;
+    if (!space_apart(m)) return MSE_ERR_INVALID_ARG;   // (only with a device, as in moe_sort)
     begin_untracked_call(stream);
     return run_product(g, d, workspace, static_cast<cudaStream_t>(stream));
 }
@@ -359,21 +370,23 @@ mse_status int8_linear(const void *x, mse_dtype x_dtype, int64_t ldx, const int8
     if (!dtype_ok(x_dtype)) return MSE_ERR_INVALID_ARG;
     mse_status st = check_product(x, ldx, ws, wq, ldw, ws, T, N, K, 1, y, y_dtype, y_capacity, workspace, workspace_bytes);
     if (st != MSE_OK) return st;
+    Int8Gemm g = product(nullptr, 0, nullptr, nullptr, 1, wq, ldw, ws, T, N, K, y, y_dtype);
+    const ProductMemory m = memory_of(g, x, ldx, size_of(x_dtype), workspace);
+    if (!out_apart(m, true)) return MSE_ERR_INVALID_ARG;
     DeviceView d;
     if ((st = device_view(&d)) != MSE_OK) return st;
+    if (!space_apart(m)) return MSE_ERR_INVALID_ARG;   // (only with a device, as in moe_sort)
     begin_untracked_call(stream);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const Int8Ws L = int8_ws(T, K);
-    float *xs = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + L.s_off);
-    Int8Gemm g = product(nullptr, 0, xs, nullptr, 1, wq, ldw, ws, T, N, K, y, y_dtype);
+    float *xs = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + int8_ws(T, K).s_off);
+    g.xs = xs;
     g.wait_limit_ns = wait_limit_ns();
     g.err = d.err;
     bool fast = false;
     if ((st = choose_tensorcore(tensorcore_ok(g), &fast)) != MSE_OK) return st;
     const int tile_rows = fast ? tile_rows_of(g, d.sm_count) : 0;
-    const int64_t x_size = size_of(x_dtype);
     // (y over x: the product's CTAs would write y while others still round x)
-    if (fast && rounds_itself(tile_rows) && disjoint(x, span(T, K, ldx, x_size), y, T * N * size_of(y_dtype)))
+    if (fast && rounds_itself(tile_rows) && apart({m.out}, {m.x}))
         return from_cuda(launch_int8_few(g, tile_rows, x, x_dtype == MSE_F32, ldx, false, d.sm_count, pdl_enabled(), s));
     RoundParams p;
     p.x = x; p.rows = T; p.K = K; p.ldx = ldx;

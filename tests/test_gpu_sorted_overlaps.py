@@ -75,3 +75,24 @@ def test_quantise(taken, swiglu):
     refused(mse.int8_quantise, [x, room], x=x, swiglu=swiglu, offsets=offsets, scales=scales)
     q, s = mse.int8_quantise(x, swiglu=swiglu, offsets=offsets, scales=torch.zeros(40, device="cuda"))
     assert bool((q.abs().amax(1) == 127).all()) and bool((s > 0).all())
+
+
+@pytest.mark.parametrize("T", [1, 40, 300])
+@pytest.mark.parametrize("name,taken", [("int8_matmul", t) for t in ("xq", "xs", "wq", "ws")] + [("int8_linear", t) for t in ("x", "wq", "ws")] +
+                         [("int8_grouped_matmul", t) for t in ("xq", "xs", "offsets", "wq", "ws")])
+def test_products(name, taken, T):
+    N, K, G = 256, 512, 3
+    room = torch.zeros(1 << 21, dtype=torch.uint8, device="cuda")
+    lead = (G,) if name == "int8_grouped_matmul" else ()
+    a = dict(wq=torch.randint(-127, 128, (*lead, N, K), device="cuda").to(torch.int8), ws=torch.rand(*lead, N, device="cuda"))
+    if name == "int8_linear":
+        a["x"] = torch.randn(T, K, device="cuda")
+    else:
+        a["xq"], a["xs"] = torch.randint(-127, 128, (T, K), device="cuda").to(torch.int8), torch.rand(T, device="cuda")
+    if lead:
+        a["offsets"] = torch.tensor([0, T, T, T], dtype=torch.int32, device="cuda")
+    t = a[taken]
+    a[taken] = room[4096:4096 + t.nbytes].view(t.dtype).view(t.shape).copy_(t)   # the workspace begins where it ends, or just before
+    refused(getattr(mse, name), list(a.values()), workspace=room[(4096 + t.nbytes - 1) // 256 * 256:], **a)
+    y = getattr(mse, name)(workspace=room[(4096 + t.nbytes + 255) // 256 * 256:], **a)
+    assert torch.equal(y, getattr(mse, name)(**a))

@@ -20,6 +20,11 @@ CASES = {
                             dict(dy=80, place=40, weights=40, rows=(9 * 9 + 8) * 2, drows=(9 * 10 + 8) * 2, dweights=40),
                             ("drows",), ("dy", "place", "weights", "rows", "dweights"), ()),
     "int8_quantise": (dict(ldx=17), dict(x=(4 * 17 + 16) * 2, last=4, q=4 * 16 + 8, scales=20), ("q",), ("x", "last", "scales"), ()),
+    "int8_matmul": (dict(ldx=17), dict(xq=4 * 17 + 9, xs=20, wq=6 * 16 + 9, ws=28, out=70, workspace=1024), ("out",),
+                    ("xq", "xs", "wq", "ws", "workspace"), ()),
+    "int8_grouped_matmul": (dict(ldx=17, out_dtype=1), dict(xq=4 * 17 + 9, xs=20, offsets=16, wq=20 * 16 + 9, ws=84, out=140, workspace=1024),
+                            ("out",), ("xq", "xs", "offsets", "wq", "ws", "workspace"), ()),
+    "int8_linear": (dict(ldx=17), dict(wq=6 * 16 + 9, ws=28, y=70, workspace=1024, x=(4 * 17 + 9) * 4), ("y",), ("wq", "ws", "workspace"), ()),
 }
 
 
@@ -69,6 +74,9 @@ def test_what_may_lie_over_what(L):
     assert L.moe_unsort_backward(*a.values()) == GOOD
     a = arguments("moe_unsort")
     assert L.moe_unsort(*{**a, "y": a["base"]}.values()) == GOOD
+    a = arguments("int8_linear")
+    for shift in (-69, 0, 300):
+        assert L.int8_linear(*{**a, "y": a["x"] + shift}.values()) == GOOD
     # without weights, rows is not read
     a = arguments("moe_unsort_backward")
     a.update(weights=None, dweights=None, rows=a["drows"] + 2)

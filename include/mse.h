@@ -680,8 +680,8 @@ MSE_API mse_status moe_unsort_backward(const void *dy, mse_dtype dy_dtype, const
  * ------------------------------------------------------------------------- */
 
 /* Rows rounded to 8-bit integers:  a = max(max |r|, 2^-100),  scale = a / 127,  q = rint(127 r / a), ties to even, of a
- * quotient in fp32.  r = x, or with swiglu silu(x[.., :K]) * x[.., K:] in fp32.  A row with an infinity or a NaN stands for
- * NaN throughout (scale NaN, q 0).
+ * quotient in fp32.  r = x, or with swiglu silu(x[.., :K]) * x[.., K:], silu(g) = g / (1 + e^-g), in fp32 (0 where e^-g is beyond
+ * it, g < -88.7).  A row with an infinity or a NaN stands for NaN throughout (scale NaN, q 0).
  *   x       [rows x K], swiglu: [rows x 2K]  bf16 or fp32, row pitch ldx
  *   last    null, or one int32 on the device: rows from *last on are left alone (offsets + E of moe_sort)
  *   q       [rows x K]  int8, row pitch ldq >= K, q_capacity >= (rows - 1) * ldq + K

@@ -46,12 +46,13 @@ __device__ __forceinline__ uint64_t int8x2_of(float lo, float hi, const RowScale
     return q;
 }
 
-// silu(g) u
+// silu(g) u = g / (1 + e^-g) u.  A sixteenth of 1 + e^-g goes into the reciprocal, which has no subnormal results: 1 + e^-g itself
+// is above 2^126 for g below -87.3, and for those g everything would be 0.  (One product more: 16384 x 2048 in bf16 32.6 us, 31.8.)
 __device__ __forceinline__ float swiglu(float g, float u) {
     float e, r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
-    return g * r * u;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(fmaf(e, 0.0625f, 0.0625f)));
+    return g * (r * 0.0625f) * u;
 }
 
 // The row tile of slot z: rows of one group.  Offsets are taken as they are in [0, T], so that no value of theirs leads out of

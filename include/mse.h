@@ -706,8 +706,9 @@ MSE_API mse_status int8_matmul(const int8_t *xq, int64_t ldx, const float *xs, c
                                void *workspace, size_t workspace_bytes, void *stream);
 
 /* The same of sorted rows with their group's weights: rows [offsets[g], offsets[g + 1]) of xq with wq[g] [N x K] and ws[g]
- * [N].  offsets [groups + 1] int32 ascends, as moe_sort gives it (else which rows are written is open); rows of out outside them are left as they were.  T: rows of
- * xq and out (offsets beyond count as T). */
+ * [N].  offsets [groups + 1] int32 ascends, as moe_sort gives it (else which rows are written is open); rows of out outside
+ * them are left as they were.  T: rows of xq and out (offsets beyond count as T).  The kernel is chosen for T rows: of rows of
+ * which many belong to no group, those that do may be passed alone, with fewer as T (their number has to be on the host then). */
 MSE_API mse_status int8_grouped_matmul(const int8_t *xq, int64_t ldx, const float *xs, const int32_t *offsets, int64_t groups,
                                        const int8_t *wq, int64_t ldw, const float *ws, int64_t T, int64_t N, int64_t K,
                                        void *out, mse_dtype out_dtype, int64_t out_capacity, void *workspace,

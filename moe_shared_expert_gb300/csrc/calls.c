@@ -1,6 +1,6 @@
-/* Python entry of the routed-expert calls, the sorted rows and the 8-bit integer products: arguments by vectorcall into the C ABI's functions (whose
- * addresses the package hands over), a fifth of what ctypes takes for as many arguments.  Integers and
- * None (a null pointer) only; every check of the arguments is the library's. */
+/* Python entry of the routed-expert calls, the sorted rows and the 8-bit integer products: arguments by vectorcall into the
+ * C ABI's functions (whose addresses the package hands over), a fifth of what ctypes takes for as many arguments.  Integers
+ * and None (a null pointer) only; every check of the arguments is the library's. */
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 

@@ -16,8 +16,8 @@ namespace {
 // ---------------------------------------------------------------------------
 // A row's values stay in the registers of a warp (up to 1024) or of a CTA (up to 8192) between its amax and its rounding; longer
 // rows are read again.  Eight values of a thread are one load, of as many bytes as the rows' alignment lets a load have.
-// Bound by memory: 8192 x 7168 in bf16 to fp16 30 us (5.9 TB/s), 64 x 7168 1.9.  (Read twice a value at a time it took 120 us; with a
-// division near the middle of two integers instead of the residual step 80.)
+// Bound by memory: 8192 x 7168 in bf16 to bytes 30 us (5.8 TB/s), 64 x 7168 1.9; to fp16 32, of whose writes a part stays in L2.  (Read
+// twice a value at a time it took 120 us; with a division near the middle of two integers instead of the residual step 80.)
 constexpr int round_threads(int lanes) { return lanes > 256 ? lanes : 256; }
 
 // eight values at `at` of which `left` are there (the others 0), as they lie in memory: 4 words of bf16 or 8 of fp32
@@ -92,7 +92,7 @@ __device__ __forceinline__ void store8(void *q, int64_t at, int64_t left, bool w
 
 // LANES threads to a row (32, 256 or 512), SLOTS times eight values of each kept (0: none, rows of any length)
 // What a thread keeps of eight values: bf16 as they lie in memory (half the registers, six CTAs on an SM), or 32 bits each.  BLOCKS:
-// CTAs on an SM.  Rows of one load a thread have eight (silu(gate) up of 16384 x 2048 in bf16 32 us, 43 with four).
+// CTAs on an SM.  Rows of one load a thread have eight (silu(gate) up of 16384 x 2048 in bf16 32.6 us, 42 with four).
 template <bool F32, bool GLU, bool HALF, int LANES, int SLOTS, int BLOCKS>
 __global__ void __launch_bounds__(round_threads(LANES), BLOCKS) round_rows_kernel(const RoundParams p, const int align,
                                                                                        const int wide) {
@@ -179,7 +179,8 @@ __global__ void __launch_bounds__(round_threads(LANES), BLOCKS) round_rows_kerne
 // ---------------------------------------------------------------------------
 // int8 rows to the same integers in fp16, for the tensor-core kernels
 // ---------------------------------------------------------------------------
-// Bound by memory: 16384 x 2048 19 us, 5.2 TB/s.  16 values a thread, two such runs on their way at once; WIDE: rows begin at multiples of 16 bytes (out's always do).
+// Bound by memory: 16384 x 2048 19 us, 5.2 TB/s.  16 values a thread, two such runs on their way at once; WIDE: rows begin at
+// multiples of 16 bytes (out's always do).
 constexpr int kExpandRuns = 2;
 
 template <bool WIDE>
@@ -288,7 +289,7 @@ cudaError_t round_of(const RoundParams &p, int sm_count, bool pdl, cudaStream_t 
     if (p.K <= 256) return with(integral_constant<int, 32>(), integral_constant<int, 1>(), integral_constant<int, kWide ? 4 : 6>());
     if (p.K <= 1024) return with(integral_constant<int, 32>(), integral_constant<int, 4>(), integral_constant<int, kWide ? 4 : 6>());
     if (p.K <= 2048) return with(integral_constant<int, 256>(), integral_constant<int, 1>(), integral_constant<int, 8>());
-    if constexpr (GLU) {   // (us with 256 threads a row and 512: 8192 x 4096 in bf16 40.0, 34.9; 64 x 7168 2.9, 2.5; without gate and up
+    if constexpr (GLU) {   // (us with 256 threads a row and 512: 8192 x 4096 in bf16 40.0, 35.7; 64 x 7168 2.9, 2.5; without gate and up
                            // fp32 rows 43.7, 47.1)
         if (p.K <= 4096) return with(integral_constant<int, 512>(), integral_constant<int, 1>(), integral_constant<int, 4>());
         if (p.K <= 8192) return with(integral_constant<int, 512>(), integral_constant<int, 2>(), integral_constant<int, 3>());

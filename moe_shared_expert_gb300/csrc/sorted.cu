@@ -131,7 +131,8 @@ __device__ __forceinline__ int warp_prefix(int *v, int n, int lane) {
 // CTA (c, y): the places of chunk c's pairs, counted by every CTA of the chunk alike, and the y-th share of its rows' copies.
 // A pair's place is its expert's first row, the expert's pairs in the chunks before, and those before it in the chunk.
 // Bound by memory, most of it writes: 8192 tokens of 7168 bytes with 8 of 128 experts, 64 of them here, 51 us with the kernels that
-// count (5.4 TB/s; this one alone 44); 4096 tokens of 7168 in bf16 with 8 of 32 experts 89; one token 3.1.
+// count (5.4 TB/s; this one alone 44); 4096 tokens of 7168 in bf16 with 8 of 32 experts 89; one token 3.1.  Rows of an odd number of
+// bytes go byte by byte: 4000 tokens of 4099 bytes, 6 rows each, 39 us, of 4100 28.
 template <typename W, int WORDS>
 __global__ void __launch_bounds__(kSortThreads) sort_kernel(const SortParams p) {
     extern __shared__ int sort_smem[];
@@ -234,7 +235,7 @@ __device__ __forceinline__ void put(float &o, float v) { o = v; }
 
 // Words of U values, as many as the alignment of every tensor lets an access have.  A thread has one word of four or eight at a time;
 // of rows that allow fewer, a warp has kSpan neighbouring values, a lane eight of them in words at steps of 32 (4000 tokens of 4099 in
-// bf16, 6 rows each: 82 us and 102 back, 191 and 183 with one value a thread; of 4096 50 and 72).
+// bf16, 6 rows each: 82 us and 101 back, 191 and 183 with one value a thread; of 4098, words of two, 61 and 122; of 4096 50 and 72).
 constexpr int kSpan = 256;
 
 template <typename T, int U>

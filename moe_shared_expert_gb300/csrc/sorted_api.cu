@@ -109,14 +109,27 @@ int64_t pitch16(int64_t K) { return (K + 63) / 64 * 64; }   // of tokens in fp16
 // 2112 x 7168 7.4, 9.9; 4 x 12288 x 7168 20.2, 20.5; 8 x 2112 x 7168 10.7, 9.9; 8 x 12288 x 7168 28, 20.6.)  Grouped rows by those
 // expected of a group, but for a token's or two's rows, of which few groups have more than two.  (us with tiles of 2, 4 and 16, 8
 // experts a token: 1 token of 32 x 4096 x 7168 40.8, 46.1, 43.4, of 32 x 7168 x 2048 22.2, 22.5, 27.7; 2 tokens of 32 x 4096 x
-// 7168 69, 70, 76; 4 tokens 113, 119, 104; 16 tokens of 32 of 128 experts 233, 181, 94.)
+// 7168 69, 70, 76; 4 tokens 113, 119, 104; 16 tokens of 32 of 128 experts 233, 181, 94.)  The rule does not look at the groups:
+// where few have these rows, tiles of 2 read a group's weights again for every two rows (8 rows of 4096 x 7168 with tiles of 2 and
+// 16: in 8 groups 39.8, 41.8, in 4 31.6, 25.0, in one 21.4, 13.5; 16 rows in one 33.4, 14.4).
 //
-// More rows take tiles of 64 on the swap-AB kernel or the CTA pairs, whichever is expected to be done first, in units of 10 ns: two
-// swap-AB CTAs on an SM take 0.6 us for a k-block each and 4 us for a tile besides, 2.5 more where its k-blocks are split; a CTA pair
-// 0.75 us for a k-block and 5 us in all, 3 more where two share a tile's.  (us with tiles of 64 and 256: 512 x 2112 x 7168 24.7, 45.2; 1024 x 2112 x 7168 37.8, 47.2;
-// 160 x 12288 x 7168 38.1, 46.6; 320 x 12288 x 7168 69, 83; 400 x 4096 x 2048 15.0, 17.1; 800 x 4096 x 2048 24.8, 17.9; 32 experts of
-// 4096 x 2048 with 32, 64, 128 and 192 rows each 61, 82; 79, 83; 127, 92; 172, 116.  Tiles of 128 were never the fastest by more
-// than a few per cent.)
+// More rows take tiles of 64 on the swap-AB kernel or the CTA pairs, whichever a model expects to be done first, in units of 10 ns:
+// two swap-AB CTAs on an SM take 0.6 us for a k-block each and 4 us for a tile besides, 2.5 more where its k-blocks are split; a CTA
+// pair 0.75 us for a k-block and 5 us in all, 3 more where two share a tile's.  us with tiles of 64 and of 256, * where the rule
+// takes the slower:
+//
+//   rows x 12288 x 7168     65 37.6 40.4   160 38.2 46.6   200 62.5 47.2   256 63.5 47.3   320 69.7 83.6*  384 70.9 84.1*
+//                          512 100 86.9    768 135 88.5   1024 186 128
+//   rows x 2112 x 7168     128 14.8 25.1   256 16.9 30.2   384 24.2 30.7   512 24.7 31.0   768 36.6 32.1  1024 37.5 33.2
+//   rows x 7168 x 2048     128 13.1 15.6   320 15.6 17.7   512 25.5 18.1   768 37.0 29.0  1024 41.0 29.7
+//   rows x 4096 x 2048     128 10.8 14.6   400 15.1 17.2   800 24.9 18.1
+//   rows of each of 32 experts of 4096 x 2048   32 63.4 83.5*   64 65.8 85.5*   96 105 87.1   128 110 88.5   256 200 107
+//   rows of each of 8 experts of 4096 x 7168    32 46.4 77.3    64 49.3 78.2*  128 81.0 82.4*  256 149 98.7
+//
+// What the model has wrong: a tile of up to 128 tokens counts as half of one, though loads and conversions take nearly as long as a whole
+// one's, and two of them as one pair's turn.  (Tiles of 128 on the swap-AB kernel were never the fastest by more than a few per cent.)
+// A rank that holds a part of the experts is judged by all rows of xq, its own or not: 128 tokens to 8 of 128 experts of 4096 x 2048,
+// 32 of them here, 298 rows, take 81.4 as 1024 rows and 55.7 passed as 298; 256 tokens 82.6 and 61.6.
 constexpr int64_t kFewRows = 4, kFewGroupedRows = 16;
 int tile_rows_of(const Int8Gemm &g, int sm_count) {
     const int few = g.offsets ? (g.T <= kFewGroupedRows ? 2 : 0) : g.T <= kFewRows ? (g.T > 2 ? 4 : (int)g.T) : 0;
@@ -128,8 +141,10 @@ int tile_rows_of(const Int8Gemm &g, int sm_count) {
     const int64_t kb = (g.K + 127) / 128, part = g.offsets ? g.groups / 2 : 0;
     const int64_t cols = ((g.T + 63) / 64 + part) * ((g.N + 127) / 128), halves = ((g.T + 127) / 128 + part) * ((g.N + 255) / 256);
     const int64_t cp = int8_cols_parts(cols, (int)kb, sm_count), pp = int8_pair_parts(int8_pair_tiles(g), (int)kb);
-    const int64_t waves = (cols * cp + 2 * sm_count - 1) / (2 * sm_count), rounds = ((halves + 1) / 2 * pp + sm_count / 2 - 1) / (sm_count / 2);
-    const int64_t cols_time = waves * (kb * 60 / cp + 400 + (cp > 1 ? 250 : 0)), pair_time = rounds * kb * 75 / pp + 500 + (pp > 1 ? 300 : 0);
+    const int64_t waves = (cols * cp + 2 * sm_count - 1) / (2 * sm_count);
+    const int64_t rounds = ((halves + 1) / 2 * pp + sm_count / 2 - 1) / (sm_count / 2);
+    const int64_t cols_time = waves * (kb * 60 / cp + 400 + (cp > 1 ? 250 : 0));
+    const int64_t pair_time = rounds * kb * 75 / pp + 500 + (pp > 1 ? 300 : 0);
     // (a swap-AB grid has at most 65,535 token tiles)
     return pair_time < cols_time || int8_cols_slots(g, 64) > 65535 ? 256 : 64;
 }

@@ -1,7 +1,8 @@
 """Products in 8-bit integers: a scale for each token and each output channel, plain and by expert.
 
 Thin bindings like the rest of the package; formulas, layouts and limits are in ``include/mse.h``.  All tensors of a call are on
-the current device.  8-bit tensors are ``torch.int8`` whose last dimension is contiguous; rows of weights whose pitch is a
+the current device; outputs and workspaces lie apart from inputs and each other, but for y over x in ``int8_linear``.  8-bit
+tensors are ``torch.int8`` whose last dimension is contiguous; rows of weights whose pitch is a
 multiple of 16 bytes, as ``int8_quantise`` makes them, take the tensor-core kernels.
 
     wq, ws = int8_quantise(w)                      # once: a row of a weight is an output channel

@@ -2,7 +2,8 @@
 
 For experts that a program runs itself: ``moe_route``'s ids sort the tokens' rows by expert, the experts take rows
 ``offsets[e] .. offsets[e + 1]`` each, and ``moe_unsort`` adds what they made of them for each token.  Thin bindings like the
-rest of the package; formulas, layouts and limits are in ``include/mse.h``.  All tensors of a call are on the current device.
+rest of the package; formulas, layouts and limits are in ``include/mse.h``.  All tensors of a call are on the current device;
+outputs and workspaces lie apart from inputs and each other, but for those that a call names.
 
 Rows behind the last expert's (pairs of other ranks, or of padding, have none) are left as they were.  The gradients are calls
 of their own, to be made from a program's backward pass:
@@ -115,9 +116,10 @@ def moe_sort(x, ids, num_experts, first_expert=0, scales=None, rows=None, row_sc
         workspace = _r._empty(stream, max(moe_sort_workspace_bytes(T, k, num_experts), 256), torch.uint8, x.device)
     else:
         _r._taken(workspace, device)
-    st = _C.moe_sort(x.data_ptr(), size, T, H, ldx, ids.data_ptr(), k, num_experts, first_expert, None if scales is None else scales.data_ptr(),
-                        rows.data_ptr(), ldr, (T * k - 1) * ldr + H, None if row_scales is None else row_scales.data_ptr(), place.data_ptr(),
-                        offsets.data_ptr(), workspace.data_ptr(), workspace.nbytes, _r._handle(stream, device))
+    st = _C.moe_sort(x.data_ptr(), size, T, H, ldx, ids.data_ptr(), k, num_experts, first_expert,
+                     None if scales is None else scales.data_ptr(), rows.data_ptr(), ldr, (T * k - 1) * ldr + H,
+                     None if row_scales is None else row_scales.data_ptr(), place.data_ptr(), offsets.data_ptr(),
+                     workspace.data_ptr(), workspace.nbytes, _r._handle(stream, device))
     if st:
         _mse._check("moe_sort", st)
     return rows, place, offsets, row_scales
@@ -140,8 +142,8 @@ def moe_unsort(rows, place, weights=None, base=None, y_dtype=None, y=None, strea
     y, y_code = _out(y, y_dtype if y_dtype is not None or y is not None else rows.dtype, "y", (T, H), rows, stream, device)
     if base is not None:
         _r._dense(base, "base", y.dtype, (T, H), device)
-    st = _C.moe_unsort(rows.data_ptr(), code, n, ldr, place.data_ptr(), None if weights is None else weights.data_ptr(), T, H, k, None if base is None else base.data_ptr(),
-                          y.data_ptr(), y_code, T * H, _r._handle(stream, device))
+    st = _C.moe_unsort(rows.data_ptr(), code, n, ldr, place.data_ptr(), None if weights is None else weights.data_ptr(), T, H, k,
+                       None if base is None else base.data_ptr(), y.data_ptr(), y_code, T * H, _r._handle(stream, device))
     if st:
         _mse._check("moe_unsort", st)
     return y
@@ -182,9 +184,9 @@ def moe_unsort_backward(dy, place, rows=None, weights=None, drows=None, dweights
     d_code, ldd, (nd, Hd), _ = _floats(drows, "drows", 2, device)
     if Hd != H or (code is not None and (d_code != code or nd != n)) or (rows_count is not None and nd != n):
         raise ValueError(f"drows: need {(n, H)} like rows, got {_r._said(drows)}")
-    st = _C.moe_unsort_backward(dy.data_ptr(), dy_code, place.data_ptr(), None if weights is None else weights.data_ptr(), None if rows is None else rows.data_ptr(), d_code, ldr, nd,
-                                   T, H, k, drows.data_ptr(), ldd, (nd - 1) * ldd + H, None if dweights is None else dweights.data_ptr(),
-                                   _r._handle(stream, device))
+    st = _C.moe_unsort_backward(dy.data_ptr(), dy_code, place.data_ptr(), None if weights is None else weights.data_ptr(),
+                                None if rows is None else rows.data_ptr(), d_code, ldr, nd, T, H, k, drows.data_ptr(), ldd,
+                                (nd - 1) * ldd + H, None if dweights is None else dweights.data_ptr(), _r._handle(stream, device))
     if st:
         _mse._check("moe_unsort_backward", st)
     return drows, dweights
